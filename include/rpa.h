@@ -78,7 +78,9 @@ enum {
 /* Element types of q, k_pages, v_pages and out (all four share one). */
 enum { RPA_DTYPE_BF16 = 0, RPA_DTYPE_F32 = 1,
        RPA_DTYPE_FP8_E4M3 = 2 /* K/V pages only: OCP e4m3 bytes (bias 7, 3-bit
-                                 mantissa, max 448), a float scale per KV head */ };
+                                 mantissa, max 448), a float scale per KV head */,
+       RPA_DTYPE_FP4_E2M1 = 3 /* K/V pages only: 4-bit codes with a scale byte
+                                 per 16 dimensions (see rpa_write_kv4)         */ };
 
 /* Codes written into the workspace error word by the kernels. */
 enum {
@@ -87,9 +89,12 @@ enum {
   RPA_DEVERR_LENGTHS = 2,    /* device lengths disagree with the plan's copies  */
   RPA_DEVERR_PLAN = 3,       /* the work list in the workspace is not this plan */
   RPA_DEVERR_TIMEOUT = 4,    /* a bounded wait inside a kernel gave up          */
-  RPA_DEVERR_LAUNCH = 5      /* a kernel found its launch unusable (shared
+  RPA_DEVERR_LAUNCH = 5,     /* a kernel found its launch unusable (shared
                                 memory base not 1024-byte aligned) and did
                                 nothing                                        */
+  RPA_DEVERR_PAGES = 6       /* the stack of free pages is too short for a
+                                step's tokens, or too full for a release (see
+                                rpa_build_tables): nothing was changed         */
 };
 
 /* Kernel paths a plan may use. */
@@ -129,7 +134,14 @@ typedef struct rpa_plan_options {
   int32_t kv_dtype;         /* dtype of the K/V pages: 0 or `dtype` (the same),
                                or RPA_DTYPE_FP8_E4M3 with dtype BF16: decode
                                batches only (every q_len <= 1), head_dim 128 or
-                               256, run through rpa_forward_fp8kv               */
+                               256, run through rpa_forward_fp8kv; or
+                               RPA_DTYPE_FP4_E2M1 with dtype BF16, any q_len,
+                               page_size >= 16, num_q_heads / num_kv_heads <=
+                               128, run through rpa_forward_kv4 (of the other
+                               options it takes path AUTO or TC, q_block of one
+                               tile, num_sms, prefill_dynamic and
+                               prefill_grouping; the rest must be 0, else
+                               RPA_ERR_UNSUPPORTED)                             */
   int32_t prefill_split;    /* 0 or -1: whole prefill work items; n > 0: lay
                                the items' key tiles (128 keys each) end to end
                                and cut them into ranges of n tiles, one per
@@ -162,8 +174,10 @@ typedef struct rpa_plan_options {
 /* What a plan chose; filled by rpa_plan_get_info. */
 typedef struct rpa_plan_info {
   int32_t path;             /* RPA_PATH_SIMT or RPA_PATH_TC                     */
-  int32_t num_decode_seqs;  /* sequences with q_len == 1                        */
-  int32_t num_prefill_seqs; /* sequences with q_len > 1                         */
+  int32_t num_decode_seqs;  /* sequences with q_len == 1 (4-bit pages: those of
+                               few query rows, on the split-KV kernel)          */
+  int32_t num_prefill_seqs; /* sequences with q_len > 1 (4-bit pages: the
+                               others, on the tensor-core prefill)              */
   int32_t q_block;          /* prefill query block in tokens (query tokens of
                                one work item; on SM pairs, of both CTAs)     */
   int32_t kv_split;         /* decode split length in tokens                    */
@@ -404,6 +418,134 @@ rpa_status_t rpa_forward_kv(const void* q, const void* k_new, const void* v_new,
                             size_t workspace_bytes);
 
 /*
+ * The KV cache in 4 bits: rows of K and V written into 4-bit pages.
+ *
+ * Format.  A row of head_dim dimensions is blocks of 16.  Each dimension is an
+ * e2m1 code (bit 3 sign; magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 for the low three
+ * bits), two to a byte, the even dimension in the low half.  Each block has one
+ * scale byte without a sign: e = byte >> 3, m = byte & 7, scale = (1 + m / 8) *
+ * 2^(e - 15), or m * 2^-17 where e == 0; byte 255 is NaN.  A stored value is
+ * its code's magnitude times the scale.  Pages are arrays
+ *   k_pages,  v_pages  [num_pages, num_kv_heads, page_size, head_dim / 2] bytes
+ *   k_scales, v_scales [num_pages, num_kv_heads, page_size, head_dim / 16] bytes
+ * (a head's rows of a page are contiguous, unlike the 8- and 16-bit pools).
+ * 0.5625 bytes an element.
+ *
+ * Writing.  With a = the largest magnitude of a block, its scale is a / 6
+ * rounded to the nearest scale (ties to even) and at most 10240; each code is
+ * x / scale rounded to the nearest magnitude (ties to the even code, at most 6).
+ * A block of magnitudes below 6 * 2^-18 is stored as zeros; one that holds a NaN
+ * or an infinity reads back as NaN in all its 16 places.
+ *
+ * k_new, v_new [total_q, num_kv_heads, head_dim] of `dtype` (BF16 or F32), 16-B
+ * aligned; slot_map [total_q] int64: token t goes to slot slot_map[t] %
+ * page_size of page slot_map[t] / page_size (rpa_build_tables makes such a
+ * map); a negative entry leaves the token out.  The slots of a call are
+ * distinct (else the row that stays is one of them, block by block).
+ * k_pages, v_pages, k_scales and v_scales 16-B aligned.  head_dim 64, 128 or
+ * 256 and page_size a power of two in [16, 256], else RPA_ERR_UNSUPPORTED.
+ * `workspace` may be NULL; otherwise its error word records a slot outside the
+ * pool (that token is left out, never trapped).  Enqueues one kernel on
+ * `stream`; does not synchronise.
+ */
+rpa_status_t rpa_write_kv4(const void* k_new, const void* v_new, uint8_t* k_pages,
+                           uint8_t* v_pages, uint8_t* k_scales, uint8_t* v_scales,
+                           const int64_t* slot_map, int32_t total_q, int32_t num_kv_heads,
+                           int32_t head_dim, int32_t page_size, int32_t num_pages, int32_t dtype,
+                           void* workspace, rpa_stream_t stream);
+
+/*
+ * The reverse: rows taken back as values.  k_out, v_out [total_q, num_kv_heads,
+ * head_dim] of `dtype` (BF16 or F32; both hold every stored value exactly) get
+ * the rows of slots slot_map[t]; rows of negative entries, or of slots outside
+ * the pool, are left as they were.  Slots may repeat.  Otherwise as
+ * rpa_write_kv4.
+ */
+rpa_status_t rpa_read_kv4(const uint8_t* k_pages, const uint8_t* v_pages, const uint8_t* k_scales,
+                          const uint8_t* v_scales, const int64_t* slot_map, void* k_out,
+                          void* v_out, int32_t total_q, int32_t num_kv_heads, int32_t head_dim,
+                          int32_t page_size, int32_t num_pages, int32_t dtype, void* workspace,
+                          rpa_stream_t stream);
+
+/*
+ * Ragged paged attention over 4-bit pages: rpa_forward's definition with the
+ * keys and values the pages stand for (rpa_write_kv4), for any mix of single
+ * tokens, a few tokens and prompts.  The plan must have kv_dtype
+ * RPA_DTYPE_FP4_E2M1; q and out are bf16.  Sequences of few query rows (q_len
+ * times num_q_heads / num_kv_heads) run on a split-KV kernel that widens the
+ * codes in registers; the others' visible keys are first widened to bf16 in
+ * the workspace (whose size counts them: 4 * head_dim * num_kv_heads bytes a
+ * key).  Pages as rpa_write_kv4's; the other arguments, the error word, unused
+ * slots, threads and CUDA graphs as rpa_forward.
+ */
+rpa_status_t rpa_forward_kv4(const void* q, const uint8_t* k_pages, const uint8_t* v_pages,
+                             const uint8_t* k_scales, const uint8_t* v_scales,
+                             const int32_t* page_table, const int32_t* cu_q_lens,
+                             const int32_t* kv_lens, int32_t num_seqs, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                             const int32_t* window, float sm_scale, void* out,
+                             rpa_stream_t stream, const rpa_plan_t* plan, void* workspace,
+                             size_t workspace_bytes);
+
+/*
+ * A step's page table, slot map and lengths from its requests' lengths, on the
+ * GPU.  Works with every kind of page.
+ *
+ * The pages no request holds are a stack: free_pages[0 .. *free_count_prev),
+ * distinct ids, the last one taken first.  Request s has kv_lens_prev[s] tokens
+ * in the cache, its page-table row holds their ceil(kv_lens_prev[s] /
+ * page_size) pages, and it appends new_lens[s] >= 0 tokens.  The call takes the
+ * pages it still needs from the stack, requests in order (the k-th page of the
+ * step is free_pages[*free_count_prev - 1 - k]), and writes
+ *   page_table  those pages, behind the row's others (nothing else changes);
+ *   cu_q_lens   [num_seqs + 1] the prefix sums of new_lens;
+ *   kv_lens     [num_seqs] kv_lens_prev + new_lens;
+ *   slot_map    [max_tokens] of each new token, requests in order, its page
+ *               times page_size plus its place in the page; -1 behind the last;
+ *   free_count  [1] the pages left (free_pages itself is only read).
+ * kv_lens may be kv_lens_prev, and free_count free_count_prev: the step then
+ * advances them in place (a captured call does so at every replay).  Otherwise
+ * the outputs do not overlap the inputs (RPA_ERR_INVALID_ARG for those two).
+ *
+ * All or nothing: a negative length, a request longer than max_pages_per_seq
+ * pages or more than max_tokens new tokens sets RPA_DEVERR_LENGTHS, a stack too
+ * short RPA_DEVERR_PAGES; then the lengths and the stack's height stay as they
+ * were, cu_q_lens is all 0 and slot_map all -1.  A page id outside the pool, in
+ * the stack or in a row, sets RPA_DEVERR_PAGE_ID and becomes slot -1.
+ *
+ * Device pointers, contiguous, 4-byte (slot_map 8-byte) aligned; page_table
+ * [num_seqs, max_pages_per_seq], free_pages [num_pages].  page_size a power of
+ * two.  `workspace`: 256 bytes or more, 256-B aligned, zero-filled before its
+ * first use (any plan's workspace serves); calls that share one do not overlap
+ * on the GPU.  Enqueues one kernel on `stream`; does not synchronise.
+ */
+rpa_status_t rpa_build_tables(const int32_t* new_lens, const int32_t* kv_lens_prev,
+                              int32_t* page_table, const int32_t* free_pages,
+                              const int32_t* free_count_prev, int32_t* cu_q_lens,
+                              int32_t* kv_lens, int64_t* slot_map, int32_t* free_count,
+                              int32_t num_seqs, int32_t max_tokens, int32_t page_size,
+                              int32_t max_pages_per_seq, int32_t num_pages, void* workspace,
+                              rpa_stream_t stream);
+
+/*
+ * Finished requests' pages go back to the stack: for every s with finished[s]
+ * != 0, its ceil(kv_lens_prev[s] / page_size) pages are pushed in (request,
+ * slot) order, free_pages[*free_count_prev ...], and kv_lens[s] becomes 0
+ * (kv_lens_prev[s] for the others); free_count is the stack's new height.  The
+ * page table is only read.  In place, device pointers and workspace as
+ * rpa_build_tables.  All or nothing: a negative length or one beyond the table
+ * sets RPA_DEVERR_LENGTHS, more pages than the pool's RPA_DEVERR_PAGES; a page
+ * id outside the pool sets RPA_DEVERR_PAGE_ID and pushes -1 (which
+ * rpa_build_tables reports when it takes it).
+ */
+rpa_status_t rpa_release_tables(const int32_t* finished, const int32_t* kv_lens_prev,
+                                const int32_t* page_table, int32_t* free_pages,
+                                const int32_t* free_count_prev, int32_t* kv_lens,
+                                int32_t* free_count, int32_t num_seqs, int32_t page_size,
+                                int32_t max_pages_per_seq, int32_t num_pages, void* workspace,
+                                rpa_stream_t stream);
+
+/*
  * Read the device error word at the start of `workspace` after everything
  * enqueued on `stream` so far (this call synchronises `stream`), store it in
  * *err (an RPA_DEVERR_* code) and reset it to RPA_DEVERR_NONE.
@@ -477,7 +619,14 @@ enum {
   RPA_KERNEL_SIMT = 3,           /* CUDA-core (fp32) path             */
   RPA_KERNEL_KV_WRITE = 4,       /* KV-cache write of new tokens      */
   RPA_KERNEL_PROLOGUE = 5,       /* q/k/v norm + rotary + KV write    */
-  RPA_KERNEL_PREFILL_COMBINE = 6 /* combine of split prefill items    */
+  RPA_KERNEL_PREFILL_COMBINE = 6, /* combine of split prefill items   */
+  RPA_KERNEL_KV4_DECODE = 7,     /* split-KV attention, 4-bit pages   */
+  RPA_KERNEL_KV4_COMBINE = 8,    /* combine of its cut segments       */
+  RPA_KERNEL_KV4_EXPAND = 9,     /* 4-bit pages widened for prefill   */
+  RPA_KERNEL_KV4_WRITE = 10,     /* 4-bit cache write                 */
+  RPA_KERNEL_KV4_READ = 11,      /* 4-bit cache read                  */
+  RPA_KERNEL_BUILD_TABLES = 12,  /* page tables and slot maps built   */
+  RPA_KERNEL_RELEASE_TABLES = 13 /* finished requests' pages returned */
 };
 typedef struct rpa_trace_record {
   int32_t kernel; /* RPA_KERNEL_* */

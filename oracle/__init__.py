@@ -194,6 +194,26 @@ def dequantize_kv(codes, scale) -> np.ndarray:
     return (vals * np.asarray(scale, dtype=np.float32)[None, None, :, None]).astype(np.float32)
 
 
+def decode_kv4(codes, scales) -> np.ndarray:
+    """4-bit rows -> float32 values (exact): codes [..., D / 2] hold two e2m1
+    codes a byte (the even dimension low; sign, two exponent bits of bias 1, one
+    mantissa bit), scales [..., D / 16] a byte of five exponent bits (bias 15)
+    and three mantissa bits each, 255 NaN."""
+    codes, scales = np.asarray(codes), np.asarray(scales)
+    c = np.stack([codes & 15, codes >> 4], -1).reshape(codes.shape[:-1] + (2 * codes.shape[-1],)).astype(np.int64)
+    e, m = (c >> 1) & 3, c & 1
+    mag = np.where(e == 0, m * 0.5, (1 + m * 0.5) * 2.0 ** (e - 1))
+    se, sm = scales.astype(np.int64) >> 3, scales.astype(np.int64) & 7
+    s = np.where(se == 0, sm * 2.0 ** -17, (1 + sm / 8) * 2.0 ** (se - 15))
+    s = np.where(scales == 255, np.nan, s)
+    return (np.where(c >= 8, -mag, mag) * np.repeat(s, 16, -1)).astype(np.float32)
+
+
+def kv4_pool(codes, scales) -> np.ndarray:
+    """4-bit pages [num_pages, Hkv, P, ...] -> a float32 pool [num_pages, P, Hkv, D]."""
+    return np.ascontiguousarray(decode_kv4(codes, scales).transpose(0, 2, 1, 3))
+
+
 def bf16_bits_to_f32(bits) -> np.ndarray:
     """bf16 bit patterns (uint16) -> float32 (exact)."""
     return (np.asarray(bits, dtype=np.uint16).astype(np.uint32) << 16).view(np.float32)

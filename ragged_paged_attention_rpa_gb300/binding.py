@@ -28,12 +28,15 @@ RPA_ERR_PLAN_MISMATCH = -6
 RPA_DTYPE_BF16 = 0
 RPA_DTYPE_F32 = 1
 RPA_DTYPE_FP8_E4M3 = 2
+RPA_DTYPE_FP4_E2M1 = 3
 
 RPA_DEVERR_NONE = 0
 RPA_DEVERR_PAGE_ID = 1
 RPA_DEVERR_LENGTHS = 2
 RPA_DEVERR_PLAN = 3
 RPA_DEVERR_TIMEOUT = 4
+RPA_DEVERR_LAUNCH = 5
+RPA_DEVERR_PAGES = 6
 
 RPA_PATH_AUTO = 0
 RPA_PATH_SIMT = 1
@@ -43,10 +46,13 @@ EXPORTS = ["rpa_plan", "rpa_plan_destroy", "rpa_plan_get_info", "rpa_forward",
            "rpa_get_device_error", "rpa_clear_device_error", "rpa_trace_begin",
            "rpa_trace_end", "rpa_status_string", "rpa_forward_decode_noalloc",
            "rpa_write_kv", "rpa_forward_kv", "rpa_forward_fp8kv", "rpa_qkv_prologue",
-           "rpa_forward_qkv", "rpa_last_cuda_error"]
+           "rpa_forward_qkv", "rpa_last_cuda_error", "rpa_write_kv4", "rpa_read_kv4",
+           "rpa_forward_kv4", "rpa_build_tables", "rpa_release_tables"]
 
 RPA_KERNEL_NAMES = {0: "decode_split", 1: "decode_combine", 2: "prefill_tc", 3: "simt",
-                    4: "kv_write", 5: "prologue", 6: "prefill_combine"}
+                    4: "kv_write", 5: "prologue", 6: "prefill_combine", 7: "kv4_decode",
+                    8: "kv4_combine", 9: "kv4_expand", 10: "kv4_write", 11: "kv4_read",
+                    12: "build_tables", 13: "release_tables"}
 
 
 class QkvNorm(ctypes.Structure):
@@ -142,6 +148,16 @@ def lib() -> ctypes.CDLL:
                                       vp, i32, i32, i32, i32, i32, vp, ctypes.c_float, vp, vp,
                                       vp, vp, ctypes.c_size_t]
         L.rpa_forward_qkv.restype = i32
+        L.rpa_write_kv4.argtypes = [vp] * 7 + [i32] * 6 + [vp, vp]
+        L.rpa_write_kv4.restype = i32
+        L.rpa_read_kv4.argtypes = [vp] * 7 + [i32] * 6 + [vp, vp]
+        L.rpa_read_kv4.restype = i32
+        L.rpa_forward_kv4.argtypes = [vp] * 8 + [i32] * 5 + [vp, ctypes.c_float, vp, vp, vp, vp, sz]
+        L.rpa_forward_kv4.restype = i32
+        L.rpa_build_tables.argtypes = [vp] * 9 + [i32] * 5 + [vp, vp]
+        L.rpa_build_tables.restype = i32
+        L.rpa_release_tables.argtypes = [vp] * 7 + [i32] * 4 + [vp, vp]
+        L.rpa_release_tables.restype = i32
         L.rpa_get_device_error.argtypes = [vp, vp, ctypes.POINTER(i32)]
         L.rpa_get_device_error.restype = i32
         L.rpa_clear_device_error.argtypes = [vp, vp]
@@ -394,6 +410,141 @@ def rpa_forward_decode_noalloc(q, k_pages, v_pages, page_table, cu_q_lens, kv_le
         raise RpaError(st, "rpa_forward_decode_noalloc")
 
 
+def _kv4_pools(k_pages, v_pages, k_scales, v_scales):
+    """Pointers and (num_pages, Hkv, page_size, head_dim) of 4-bit pools."""
+    import torch
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be [num_pages, num_kv_heads, page_size, head_dim / 2]")
+    n, hkv, p, half = (int(x) for x in k_pages.shape)
+    for t, name, last in ((v_pages, "v_pages", half), (k_scales, "k_scales", half // 8),
+                          (v_scales, "v_scales", half // 8)):
+        if tuple(t.shape) != (n, hkv, p, last):
+            raise ValueError("%s must have shape %s, got %s" % (name, (n, hkv, p, last),
+                                                                tuple(t.shape)))
+    ptrs = [_dptr(t, name, torch.uint8) for t, name in
+            ((k_pages, "k_pages"), (v_pages, "v_pages"), (k_scales, "k_scales"),
+             (v_scales, "v_scales"))]
+    return ptrs, (n, hkv, p, 2 * half)
+
+
+def _kv4_rows(k, v, names, slot_map, shape):
+    import torch
+    _, hkv, _, d = shape
+    if k.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (names[0], k.dtype))
+    want = (int(slot_map.numel()), hkv, d)
+    for t, name in ((k, names[0]), (v, names[1])):
+        if tuple(t.shape) != want:
+            raise ValueError("%s must have shape %s, got %s" % (name, want, tuple(t.shape)))
+    return RPA_DTYPE_BF16 if k.dtype == torch.bfloat16 else RPA_DTYPE_F32
+
+
+def rpa_write_kv4(k_new, v_new, k_pages, v_pages, k_scales, v_scales, slot_map, workspace=None,
+                  stream=None) -> None:
+    """rpa_write_kv4 on torch CUDA tensors: rows [total_q, Hkv, D] (bf16 or
+    float32) into 4-bit pages (uint8: pages [N, Hkv, P, D/2], scales
+    [N, Hkv, P, D/16]) at the slots of slot_map ([total_q] int64, < 0: left out)."""
+    import torch
+    pools, shape = _kv4_pools(k_pages, v_pages, k_scales, v_scales)
+    dtype = _kv4_rows(k_new, v_new, ("k_new", "v_new"), slot_map, shape)
+    n, hkv, p, d = shape
+    st = lib().rpa_write_kv4(
+        _dptr(k_new, "k_new"), _dptr(v_new, "v_new", k_new.dtype), *pools,
+        _dptr(slot_map, "slot_map", torch.int64), int(slot_map.numel()), hkv, d, p, n, dtype,
+        _dptr(workspace, "workspace"), _stream_ptr(stream))
+    if st != RPA_OK:
+        raise RpaError(st, "rpa_write_kv4")
+
+
+def rpa_read_kv4(k_pages, v_pages, k_scales, v_scales, slot_map, k_out, v_out, workspace=None,
+                 stream=None) -> None:
+    """rpa_read_kv4 on torch CUDA tensors: the rows at slot_map's slots as
+    values, to k_out and v_out [total_q, Hkv, D] (bf16 or float32)."""
+    import torch
+    pools, shape = _kv4_pools(k_pages, v_pages, k_scales, v_scales)
+    dtype = _kv4_rows(k_out, v_out, ("k_out", "v_out"), slot_map, shape)
+    n, hkv, p, d = shape
+    st = lib().rpa_read_kv4(
+        *pools, _dptr(slot_map, "slot_map", torch.int64), _dptr(k_out, "k_out"),
+        _dptr(v_out, "v_out", k_out.dtype), int(slot_map.numel()), hkv, d, p, n, dtype,
+        _dptr(workspace, "workspace"), _stream_ptr(stream))
+    if st != RPA_OK:
+        raise RpaError(st, "rpa_read_kv4")
+
+
+def rpa_forward_kv4(q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv_lens,
+                    window, sm_scale: float, out, plan: Plan, workspace, stream=None) -> None:
+    """rpa_forward_kv4: attention over 4-bit pages (uint8 tensors; a plan with
+    kv_dtype=RPA_DTYPE_FP4_E2M1)."""
+    ForwardKv4Call(q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv_lens,
+                   window, sm_scale, out, plan, workspace, stream)()
+
+
+def _tables_args(page_table, kv_lens_prev, kv_lens, free_pages, free_count_prev, free_count):
+    import torch
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [num_seqs, max_pages_per_seq]")
+    n, width = (int(x) for x in page_table.shape)
+    for t, name in ((kv_lens_prev, "kv_lens_prev"), (kv_lens, "kv_lens")):
+        if tuple(t.shape) != (n,):
+            raise ValueError("%s must have num_seqs entries" % name)
+    for t, name in ((free_count_prev, "free_count_prev"), (free_count, "free_count")):
+        if t.numel() != 1:
+            raise ValueError("%s must have one entry" % name)
+    i32 = torch.int32
+    return (n, width, int(free_pages.numel()), _dptr(page_table, "page_table", i32),
+            _dptr(kv_lens_prev, "kv_lens_prev", i32), _dptr(kv_lens, "kv_lens", i32),
+            _dptr(free_pages, "free_pages", i32), _dptr(free_count_prev, "free_count_prev", i32),
+            _dptr(free_count, "free_count", i32))
+
+
+def rpa_build_tables(new_lens, kv_lens_prev, page_table, free_pages, free_count_prev, cu_q_lens,
+                     kv_lens, slot_map, free_count, page_size: int, workspace,
+                     stream=None) -> None:
+    """rpa_build_tables on torch CUDA tensors: the step's pages from the stack
+    free_pages ([num_pages] int32) into page_table, and cu_q_lens
+    ([num_seqs + 1]), kv_lens, slot_map ([max_tokens] int64) and free_count
+    ([1]); kv_lens may be kv_lens_prev and free_count free_count_prev."""
+    import torch
+    n, width, pool, table, prev, kv, free, c0, c1 = _tables_args(
+        page_table, kv_lens_prev, kv_lens, free_pages, free_count_prev, free_count)
+    if tuple(new_lens.shape) != (n,):
+        raise ValueError("new_lens must have num_seqs entries")
+    if tuple(cu_q_lens.shape) != (n + 1,):
+        raise ValueError("cu_q_lens must have num_seqs + 1 entries")
+    st = lib().rpa_build_tables(
+        _dptr(new_lens, "new_lens", torch.int32), prev, table, free, c0,
+        _dptr(cu_q_lens, "cu_q_lens", torch.int32), kv, _dptr(slot_map, "slot_map", torch.int64),
+        c1, n, int(slot_map.numel()), int(page_size), width, pool, _workspace_ptr(workspace),
+        _stream_ptr(stream))
+    if st != RPA_OK:
+        raise RpaError(st, "rpa_build_tables")
+
+
+def rpa_release_tables(finished, kv_lens_prev, page_table, free_pages, free_count_prev, kv_lens,
+                       free_count, page_size: int, workspace, stream=None) -> None:
+    """rpa_release_tables on torch CUDA tensors: the pages of every request
+    with finished != 0 ([num_seqs] int32) pushed on the stack free_pages, its
+    length to 0."""
+    import torch
+    n, width, pool, table, prev, kv, free, c0, c1 = _tables_args(
+        page_table, kv_lens_prev, kv_lens, free_pages, free_count_prev, free_count)
+    if tuple(finished.shape) != (n,):
+        raise ValueError("finished must have num_seqs entries")
+    st = lib().rpa_release_tables(
+        _dptr(finished, "finished", torch.int32), prev, table, free, c0, kv, c1, n,
+        int(page_size), width, pool, _workspace_ptr(workspace), _stream_ptr(stream))
+    if st != RPA_OK:
+        raise RpaError(st, "rpa_release_tables")
+
+
+def _workspace_ptr(workspace):
+    """The workspace's address; its header alone is 256 bytes."""
+    if workspace is not None and workspace.numel() * workspace.element_size() < 256:
+        raise ValueError("workspace must hold at least 256 bytes")
+    return _dptr(workspace, "workspace")
+
+
 def rpa_get_device_error(workspace, stream=None) -> int:
     """Read and clear the device error word (synchronises the stream)."""
     err = ctypes.c_int32(0)
@@ -599,3 +750,36 @@ class ForwardQkvCall(ForwardCall):
         st = self._fn(*self._args)
         if st != RPA_OK:
             raise RpaError(st, "rpa_forward_qkv")
+
+
+class ForwardKv4Call(ForwardCall):
+    """rpa_forward_kv4 (attention over 4-bit pages) with its arguments
+    marshalled once."""
+
+    def __init__(self, q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv_lens,
+                 window, sm_scale: float, out, plan: Plan, workspace, stream=None):
+        import torch
+        m = plan.meta
+        pools, shape = _kv4_pools(k_pages, v_pages, k_scales, v_scales)
+        if shape[1:] != (m["num_kv_heads"], m["page_size"], m["head_dim"]):
+            raise ValueError("the pools' shape differs from the plan's")
+        self._keep = (q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv_lens,
+                      window, out, plan, workspace)
+        self._args = (
+            _dptr(q, "q", torch.bfloat16), *pools,
+            _dptr(page_table, "page_table", torch.int32),
+            _dptr(cu_q_lens, "cu_q_lens", torch.int32),
+            _dptr(kv_lens, "kv_lens", torch.int32), m["num_seqs"], m["num_q_heads"],
+            m["num_kv_heads"], m["head_dim"], m["page_size"],
+            _dptr(window, "window", torch.int32), float(sm_scale),
+            _dptr(out, "out", torch.bfloat16), _stream_ptr(stream), plan.handle,
+            _dptr(workspace, "workspace"), workspace.numel() * workspace.element_size())
+        self._fn = lib().rpa_forward_kv4
+
+    def __call__(self, plan: Optional[Plan] = None):
+        args = self._args
+        if plan is not None:
+            args = args[:17] + (plan.handle,) + args[18:]
+        st = self._fn(*args)
+        if st != RPA_OK:
+            raise RpaError(st, "rpa_forward_kv4")

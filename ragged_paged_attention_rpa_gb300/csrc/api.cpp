@@ -93,7 +93,7 @@ rpa_status_t rpa_plan(rpa_plan_t** plan, const int32_t* cu_q_lens_host,
     std::memcpy(&o, opts, static_cast<size_t>(opts->struct_size));
   }
   if (o.q_block < 0 || o.kv_split < 0 || o.num_sms < 0 || o.prefill_pairs < 0 ||
-      o.prefill_pairs > 2 || o.kv_dtype < 0 || o.kv_dtype > RPA_DTYPE_FP8_E4M3 ||
+      o.prefill_pairs > 2 || o.kv_dtype < 0 || o.kv_dtype > RPA_DTYPE_FP4_E2M1 ||
       o.prefill_split < -1 || o.prefill_split > 65535 || o.decode_sms < -1 ||
       o.decode_kernel < 0 || o.decode_kernel > RPA_DECODE_KERNEL_TC || o.prefill_dynamic < -1 ||
       o.prefill_dynamic > 0 || o.prefill_grouping < -1 || o.prefill_grouping > 0)
@@ -148,7 +148,7 @@ rpa_status_t rpa_plan_get_info(const rpa_plan_t* plan, rpa_plan_info* info) {
   info->prefill_ctas = p.prefill_ctas;
   info->workspace_bytes = static_cast<int64_t>(p.ws_bytes);
   info->prefill_pairs = p.prefill_pairs ? 1 : 0;
-  info->kv_dtype = p.kv_fp8 ? RPA_DTYPE_FP8_E4M3 : p.dtype;
+  info->kv_dtype = p.kv_fp4 ? RPA_DTYPE_FP4_E2M1 : p.kv_fp8 ? RPA_DTYPE_FP8_E4M3 : p.dtype;
   info->prefill_split_items = static_cast<int32_t>(p.psplit.size());
   info->prefill_split_parts = p.n_split_items;
   info->prefill_max_tiles = p.prefill_max_tiles;
@@ -156,7 +156,7 @@ rpa_status_t rpa_plan_get_info(const rpa_plan_t* plan, rpa_plan_info* info) {
   info->prefill_sms = p.overlap ? p.prefill_sms : 0;
   info->prefill_dynamic = p.prefill_dynamic ? 1 : 0;
   info->prefill_groups = p.prefill_groups;
-  info->decode_kernel = (p.num_decode > 0 && !p.simt_decode)
+  info->decode_kernel = (p.num_decode > 0 && !p.simt_decode && !p.kv_fp4)
                             ? (p.decode_tc ? RPA_DECODE_KERNEL_TC : RPA_DECODE_KERNEL_MMA)
                             : 0;
   return RPA_OK;
@@ -269,7 +269,8 @@ rpa_status_t rpa_forward(const void* q, const void* k_pages, const void* v_pages
   if (plan == nullptr) return RPA_ERR_INVALID_ARG;
   const rpa::Plan& p = plan->p;
   if (num_seqs != p.num_seqs || num_q_heads != p.hq || num_kv_heads != p.hkv ||
-      head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp8)
+      head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp8 ||
+      p.kv_fp4)
     return RPA_ERR_PLAN_MISMATCH;
   if (workspace == nullptr || !aligned(workspace, 256)) return RPA_ERR_INVALID_ARG;
   if (workspace_bytes < p.ws_bytes) return RPA_ERR_WORKSPACE_TOO_SMALL;
@@ -327,7 +328,7 @@ rpa_status_t rpa_forward_kv(const void* q, const void* k_new, const void* v_new,
   if (plan == nullptr) return RPA_ERR_INVALID_ARG;
   const rpa::Plan& p = plan->p;
   if (num_seqs != p.num_seqs || num_q_heads != p.hq || num_kv_heads != p.hkv ||
-      head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window)
+      head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp4)
     return RPA_ERR_PLAN_MISMATCH;
   if (workspace == nullptr || !aligned(workspace, 256)) return RPA_ERR_INVALID_ARG;
   if (workspace_bytes < p.ws_bytes) return RPA_ERR_WORKSPACE_TOO_SMALL;
@@ -424,7 +425,8 @@ rpa_status_t rpa_forward_qkv(const void* q, const void* k, const void* v,
   if (plan == nullptr || norm == nullptr || !(norm->eps >= 0.f)) return RPA_ERR_INVALID_ARG;
   const rpa::Plan& p = plan->p;
   if (num_seqs != p.num_seqs || num_q_heads != p.hq || num_kv_heads != p.hkv ||
-      head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp8)
+      head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp8 ||
+      p.kv_fp4)
     return RPA_ERR_PLAN_MISMATCH;
   if (!rpa::prologue_supported(head_dim)) return RPA_ERR_UNSUPPORTED;
   if (workspace == nullptr || !aligned(workspace, 256)) return RPA_ERR_INVALID_ARG;
@@ -461,7 +463,8 @@ rpa_status_t rpa_forward_decode_noalloc(const void* q, const void* k_pages,
   if (plan == nullptr) return RPA_ERR_INVALID_ARG;
   const rpa::Plan& p = plan->p;
   if (num_seqs != p.num_seqs || num_q_heads != p.hq || num_kv_heads != p.hkv ||
-      head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp8)
+      head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp8 ||
+      p.kv_fp4)
     return RPA_ERR_PLAN_MISMATCH;
   if (p.num_prefill > 0 || p.simt_decode || p.dtype != RPA_DTYPE_BF16)
     return RPA_ERR_UNSUPPORTED;
@@ -483,6 +486,177 @@ rpa_status_t rpa_forward_decode_noalloc(const void* q, const void* k_pages,
               out, static_cast<unsigned char*>(scratch)};
   rpa::trace_start(stream);
   if (int err = rpa::launch_decode(p, a, stream)) return cuda_failed(err);
+  return RPA_OK;
+}
+
+namespace {
+
+// Whether [a, a + n) and [b, b + m) share a byte (0 bytes share none).
+bool overlap(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return n > 0 && m > 0 && x < y + m && y < x + n;
+}
+
+// Shapes both table calls share.
+bool table_shapes_ok(int32_t num_seqs, int32_t page_size, int32_t mpps, int32_t num_pages) {
+  return num_seqs >= 0 && page_size >= 1 && is_pow2(page_size) && mpps >= 1 && num_pages >= 1;
+}
+
+// In place or apart: the state a table call advances.
+bool state_ok(const int32_t* kv_prev, const int32_t* kv, int32_t num_seqs,
+              const int32_t* count_prev, const int32_t* count) {
+  const size_t n = static_cast<size_t>(num_seqs) * sizeof(int32_t);
+  return (kv == kv_prev || !overlap(kv, n, kv_prev, n)) &&
+         (count == count_prev || !overlap(count, sizeof(int32_t), count_prev, sizeof(int32_t)));
+}
+
+rpa_status_t kv4_cache(const void* k_rows, const void* v_rows, uint8_t* k_pages, uint8_t* v_pages,
+                       uint8_t* k_scales, uint8_t* v_scales, const int64_t* slot_map,
+                       int32_t total_q, int32_t num_kv_heads, int32_t head_dim,
+                       int32_t page_size, int32_t num_pages, int32_t dtype, void* workspace,
+                       rpa_stream_t stream, bool read) {
+  if (total_q < 0 || num_kv_heads < 1 || head_dim < 1 || page_size < 1 || !is_pow2(page_size) ||
+      num_pages < 1)
+    return RPA_ERR_INVALID_ARG;
+  if (dtype != RPA_DTYPE_BF16 && dtype != RPA_DTYPE_F32) return RPA_ERR_INVALID_ARG;
+  if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || page_size < 16 || page_size > 256)
+    return RPA_ERR_UNSUPPORTED;
+  if (total_q == 0) return RPA_OK;
+  if (k_rows == nullptr || v_rows == nullptr || k_pages == nullptr || v_pages == nullptr ||
+      k_scales == nullptr || v_scales == nullptr || slot_map == nullptr)
+    return RPA_ERR_INVALID_ARG;
+  if (!aligned(k_rows, 16) || !aligned(v_rows, 16) || !aligned(k_pages, 16) ||
+      !aligned(v_pages, 16) || !aligned(k_scales, 16) || !aligned(v_scales, 16) ||
+      !aligned(slot_map, 8) || (workspace != nullptr && !aligned(workspace, 256)))
+    return RPA_ERR_INVALID_ARG;
+  rpa::Kv4CacheArgs a{k_rows, v_rows, k_pages, v_pages, k_scales, v_scales, slot_map,
+                      static_cast<unsigned char*>(workspace), total_q, num_kv_heads, head_dim,
+                      dtype == RPA_DTYPE_F32 ? 4 : 2, page_size, num_pages, read};
+  rpa::trace_start(stream);
+  if (int err = rpa::launch_kv4_cache(a, stream)) return cuda_failed(err);
+  return RPA_OK;
+}
+
+}  // namespace
+
+rpa_status_t rpa_write_kv4(const void* k_new, const void* v_new, uint8_t* k_pages,
+                           uint8_t* v_pages, uint8_t* k_scales, uint8_t* v_scales,
+                           const int64_t* slot_map, int32_t total_q, int32_t num_kv_heads,
+                           int32_t head_dim, int32_t page_size, int32_t num_pages, int32_t dtype,
+                           void* workspace, rpa_stream_t stream) {
+  return kv4_cache(k_new, v_new, k_pages, v_pages, k_scales, v_scales, slot_map, total_q,
+                   num_kv_heads, head_dim, page_size, num_pages, dtype, workspace, stream, false);
+}
+
+rpa_status_t rpa_read_kv4(const uint8_t* k_pages, const uint8_t* v_pages, const uint8_t* k_scales,
+                          const uint8_t* v_scales, const int64_t* slot_map, void* k_out,
+                          void* v_out, int32_t total_q, int32_t num_kv_heads, int32_t head_dim,
+                          int32_t page_size, int32_t num_pages, int32_t dtype, void* workspace,
+                          rpa_stream_t stream) {
+  return kv4_cache(k_out, v_out, const_cast<uint8_t*>(k_pages), const_cast<uint8_t*>(v_pages),
+                   const_cast<uint8_t*>(k_scales), const_cast<uint8_t*>(v_scales), slot_map,
+                   total_q, num_kv_heads, head_dim, page_size, num_pages, dtype, workspace, stream,
+                   true);
+}
+
+rpa_status_t rpa_forward_kv4(const void* q, const uint8_t* k_pages, const uint8_t* v_pages,
+                             const uint8_t* k_scales, const uint8_t* v_scales,
+                             const int32_t* page_table, const int32_t* cu_q_lens,
+                             const int32_t* kv_lens, int32_t num_seqs, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                             const int32_t* window, float sm_scale, void* out,
+                             rpa_stream_t stream, const rpa_plan_t* plan, void* workspace,
+                             size_t workspace_bytes) {
+  if (plan == nullptr) return RPA_ERR_INVALID_ARG;
+  const rpa::Plan& p = plan->p;
+  if (num_seqs != p.num_seqs || num_q_heads != p.hq || num_kv_heads != p.hkv ||
+      head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || !p.kv_fp4)
+    return RPA_ERR_PLAN_MISMATCH;
+  if (workspace == nullptr || !aligned(workspace, 256)) return RPA_ERR_INVALID_ARG;
+  if (workspace_bytes < p.ws_bytes) return RPA_ERR_WORKSPACE_TOO_SMALL;
+  if (p.total_q == 0) return RPA_OK;
+  if (q == nullptr || k_pages == nullptr || v_pages == nullptr || k_scales == nullptr ||
+      v_scales == nullptr || page_table == nullptr || cu_q_lens == nullptr ||
+      kv_lens == nullptr || out == nullptr)
+    return RPA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
+      !aligned(k_scales, 16) || !aligned(v_scales, 16) || !aligned(page_table, 4) ||
+      !aligned(cu_q_lens, 4) || !aligned(kv_lens, 4) || !aligned(window, 4))
+    return RPA_ERR_INVALID_ARG;
+  rpa::Args a{q, k_pages, v_pages, page_table, cu_q_lens, kv_lens, window, sm_scale,
+              out, static_cast<unsigned char*>(workspace)};
+  a.k_block_scales = k_scales;
+  a.v_block_scales = v_scales;
+  rpa::trace_start(stream);
+  int err = 0;
+  if (!p.kv4_launches.empty() && (err = rpa::launch_kv4_decode(p, a, stream)) != 0)
+    return cuda_failed(err);
+  if (!p.items.empty()) {
+    if ((err = rpa::launch_kv4_expand(p, a, stream)) != 0) return cuda_failed(err);
+    rpa::Args b = a;
+    b.k_pages = a.workspace + p.off_kv4_k;
+    b.v_pages = a.workspace + p.off_kv4_v;
+    b.page_table = reinterpret_cast<const int32_t*>(a.workspace + p.off_kv4_table);
+    b.pool_pages = p.kv4_scratch_pages;
+    if ((err = rpa::launch_prefill_tc(p, b, stream)) != 0) return cuda_failed(err);
+  }
+  return RPA_OK;
+}
+
+rpa_status_t rpa_build_tables(const int32_t* new_lens, const int32_t* kv_lens_prev,
+                              int32_t* page_table, const int32_t* free_pages,
+                              const int32_t* free_count_prev, int32_t* cu_q_lens,
+                              int32_t* kv_lens, int64_t* slot_map, int32_t* free_count,
+                              int32_t num_seqs, int32_t max_tokens, int32_t page_size,
+                              int32_t max_pages_per_seq, int32_t num_pages, void* workspace,
+                              rpa_stream_t stream) {
+  if (!table_shapes_ok(num_seqs, page_size, max_pages_per_seq, num_pages) || max_tokens < 0)
+    return RPA_ERR_INVALID_ARG;
+  if (free_count_prev == nullptr || free_count == nullptr || cu_q_lens == nullptr ||
+      free_pages == nullptr || workspace == nullptr || (max_tokens > 0 && slot_map == nullptr) ||
+      (num_seqs > 0 && (new_lens == nullptr || kv_lens_prev == nullptr || kv_lens == nullptr ||
+                        page_table == nullptr)))
+    return RPA_ERR_INVALID_ARG;
+  if (!aligned(new_lens, 4) || !aligned(kv_lens_prev, 4) || !aligned(page_table, 4) ||
+      !aligned(free_pages, 4) || !aligned(free_count_prev, 4) || !aligned(cu_q_lens, 4) ||
+      !aligned(kv_lens, 4) || !aligned(slot_map, 8) || !aligned(free_count, 4) ||
+      !aligned(workspace, 256))
+    return RPA_ERR_INVALID_ARG;
+  if (!state_ok(kv_lens_prev, kv_lens, num_seqs, free_count_prev, free_count))
+    return RPA_ERR_INVALID_ARG;
+  rpa::TableArgs a{new_lens, kv_lens_prev, page_table, const_cast<int32_t*>(free_pages),
+                   free_count_prev, cu_q_lens, kv_lens, slot_map, free_count,
+                   static_cast<unsigned char*>(workspace), num_seqs, page_size,
+                   max_pages_per_seq, num_pages, max_tokens, false};
+  rpa::trace_start(stream);
+  if (int err = rpa::launch_tables(a, stream)) return cuda_failed(err);
+  return RPA_OK;
+}
+
+rpa_status_t rpa_release_tables(const int32_t* finished, const int32_t* kv_lens_prev,
+                                const int32_t* page_table, int32_t* free_pages,
+                                const int32_t* free_count_prev, int32_t* kv_lens,
+                                int32_t* free_count, int32_t num_seqs, int32_t page_size,
+                                int32_t max_pages_per_seq, int32_t num_pages, void* workspace,
+                                rpa_stream_t stream) {
+  if (!table_shapes_ok(num_seqs, page_size, max_pages_per_seq, num_pages)) return RPA_ERR_INVALID_ARG;
+  if (free_count_prev == nullptr || free_count == nullptr || free_pages == nullptr ||
+      workspace == nullptr ||
+      (num_seqs > 0 && (finished == nullptr || kv_lens_prev == nullptr || kv_lens == nullptr ||
+                        page_table == nullptr)))
+    return RPA_ERR_INVALID_ARG;
+  if (!aligned(finished, 4) || !aligned(kv_lens_prev, 4) || !aligned(page_table, 4) ||
+      !aligned(free_pages, 4) || !aligned(free_count_prev, 4) || !aligned(kv_lens, 4) ||
+      !aligned(free_count, 4) || !aligned(workspace, 256))
+    return RPA_ERR_INVALID_ARG;
+  if (!state_ok(kv_lens_prev, kv_lens, num_seqs, free_count_prev, free_count))
+    return RPA_ERR_INVALID_ARG;
+  rpa::TableArgs a{finished, kv_lens_prev, const_cast<int32_t*>(page_table), free_pages,
+                   free_count_prev, nullptr, kv_lens, nullptr, free_count,
+                   static_cast<unsigned char*>(workspace), num_seqs, page_size,
+                   max_pages_per_seq, num_pages, 0, true};
+  rpa::trace_start(stream);
+  if (int err = rpa::launch_tables(a, stream)) return cuda_failed(err);
   return RPA_OK;
 }
 

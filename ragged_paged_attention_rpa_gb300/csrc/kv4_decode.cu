@@ -1,0 +1,762 @@
+// Attention over 4-bit pages for sequences with few query rows (one decoded
+// token, or a handful of drafted ones): split-KV, codes widened in registers.
+//
+// Work.  The query rows of a sequence that share a KV head (token-major, G
+// heads a token) are cut into tiles of 8 or 16 rows; every (row tile, KV head)
+// is a segment of 16-key blocks over the keys any of its rows sees.  The
+// segments are laid end to end, each followed by a fixed charge for its merge,
+// and the line is cut into equal ranges, one per CTA, one wave.
+//
+// CTA.  The warps take a segment's blocks round-robin and never meet until its
+// end: each runs, per block of 16 keys,
+//     S^T[16 keys x rows] = K . Q^T        (mma.m16n8k16, f16 -> fp32)
+//     O^T[D x rows]     += V^T . P^T
+// with an online softmax whose reference grows only when a score passes it by
+// 2^8 (the probabilities stay below 256, exact in the sums' fp32).
+//
+// Layout.  A product's order of terms is free, so which dimension a fragment's
+// k index means is chosen such that a lane needs a contiguous run of bytes: of
+// K rows g and g + 8 its quarter of the row (Q is fetched with the same
+// permutation), of V its eighth of the rows of its four keys.  Each lane copies
+// exactly those bytes with cp.async into slots of its own in shared memory and
+// is the only one to read them: no bank conflicts, no barrier, and several
+// blocks in flight a warp.  Only the scales (2 D bytes a block) cross lanes.
+// Of V, two keys' codes are interleaved with two bit selects per eight codes
+// before they are widened, which gives the register pairs along the keys that
+// the second product wants without a transpose.
+//
+// Numbers.  Codes widen to f16 exactly, and times their scale they are still
+// exact.  Q is bf16 made f16 after a power of two for the row (its largest
+// element in [1, 2)): what rounds is below 2^-25 of the row's largest element.
+// P is rounded to f16 (half a step: 2^-12 of itself) for the second product.
+// Scores, maxima, sums and O are fp32.
+//
+// A key no row of the tile sees has its V scale set to zero (its bytes may be
+// anything, a NaN scale included) and its scores replaced by -inf.  A bad page
+// id sets the error word; its keys count as not seen.
+//
+// What bounds it: 0.5625 bytes an element come from HBM, and each element
+// costs about one issue slot in 32 (widen, scale, multiply): at the copy peak
+// the schedulers are ~70% busy, so either can be the limit.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kv4.cuh"
+#include "rpa_internal.h"
+
+namespace rpa {
+namespace {
+
+constexpr int kBlk = 16;
+
+struct Kv4Params {
+  const __nv_bfloat16* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  const uint8_t* ks;
+  const uint8_t* vs;
+  const int32_t* page_table;
+  __nv_bfloat16* out;
+  unsigned char* ws;
+  float* part_o;    // [2 * CTAs][rows][D]
+  float* part_lse;  // [2 * CTAs][rows]
+  int32_t hq, hkv, group, page_shift, mpps, num_pages;
+  float scale_log2;
+};
+
+// One launch's row tiles: tile e covers rows [r0, r0 + nrows) of sequence
+// seq, whose first query token is q0, at position pos0; its segments (one per
+// KV head) take [v0[e], v0[e + 1]) of the line.
+struct Kv4Tile {
+  int32_t seq, q0, r0, nrows, pos0, window;
+};
+template <int NSEG>
+struct Kv4Sched {
+  int32_t n, n_ctas;
+  int64_t v0[NSEG + 1];
+  Kv4Tile tile[NSEG];
+};
+
+// Start of CTA c's range of the line.
+template <int NSEG>
+__device__ __forceinline__ int64_t range_start(const Kv4Sched<NSEG>& sc, int c) {
+  return sc.v0[sc.n] * c / sc.n_ctas;
+}
+
+// A segment: tile e and KV head g, as CTA range [vb, ve) sees it.
+struct Seg {
+  int e, g;
+  int64_t v;       // its start on the line
+  int32_t cost;    // its length on the line (blocks + merge charge)
+  int32_t nb, fb;  // blocks; index of the first one
+  int32_t j0, j1;  // blocks in the range: [j0, j1)
+};
+
+__device__ __forceinline__ int32_t tile_lo(const Kv4Tile& t, int32_t group) {
+  return first_visible(t.pos0 + t.r0 / group, t.window);
+}
+__device__ __forceinline__ int32_t tile_hi(const Kv4Tile& t, int32_t group) {
+  return t.pos0 + (t.r0 + t.nrows - 1) / group;
+}
+
+template <int NSEG>
+__device__ __forceinline__ void seg_fill(const Kv4Sched<NSEG>& sc, const Kv4Params& p, Seg& s,
+                                         int64_t vb, int64_t ve) {
+  const Kv4Tile& t = sc.tile[s.e];
+  s.fb = tile_lo(t, p.group) / kBlk;
+  s.nb = tile_hi(t, p.group) / kBlk - s.fb + 1;
+  s.cost = s.nb + kKv4SegCost;
+  s.j0 = static_cast<int32_t>(max(static_cast<int64_t>(0), vb - s.v));
+  s.j1 = static_cast<int32_t>(min(static_cast<int64_t>(s.nb), ve - s.v));
+}
+
+// The segment that holds position x of the line.
+template <int NSEG>
+__device__ __forceinline__ Seg seg_at(const Kv4Sched<NSEG>& sc, const Kv4Params& p, int64_t x,
+                                      int64_t vb, int64_t ve) {
+  int lo = 0, hi = sc.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sc.v0[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  Seg s;
+  s.e = lo;
+  s.g = 0;
+  s.v = sc.v0[lo];
+  seg_fill(sc, p, s, vb, ve);
+  s.g = static_cast<int>((x - s.v) / s.cost);
+  s.v += static_cast<int64_t>(s.g) * s.cost;
+  seg_fill(sc, p, s, vb, ve);
+  return s;
+}
+
+template <int NSEG>
+__device__ __forceinline__ void seg_next(const Kv4Sched<NSEG>& sc, const Kv4Params& p, Seg& s,
+                                         int64_t vb, int64_t ve) {
+  s.v += s.cost;
+  if (++s.g == p.hkv) {
+    s.g = 0;
+    ++s.e;
+  }
+  if (s.v < ve) seg_fill(sc, p, s, vb, ve);
+}
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32_t src_bytes) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(src_bytes),
+                 "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int WORDS>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[WORDS]) {
+  if constexpr (WORDS == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+  else if constexpr (WORDS == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(addr));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// (a & m) | (b & ~m)
+__device__ __forceinline__ uint32_t bit_select(uint32_t m, uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xca;" : "=r"(r) : "r"(m), "r"(a), "r"(b));
+  return r;
+}
+
+// Shapes of an instance: D, NT tiles of 8 rows, W warps a CTA, S blocks in
+// flight a warp, CTAS CTAs a SM.  O and Q take (D / 4 + D / 8) NT registers of
+// a thread: up to 48 leaves 16 warps a SM (128 registers each), 96 leaves 12.
+template <int D_, int NT_>
+struct Kv4Shape {
+  static constexpr int D = D_, NT = NT_;
+  static constexpr bool kWide = D * NT >= 256;
+  static constexpr int W = kWide ? 4 : 8;
+  static constexpr int CTAS = kWide ? 3 : 2;
+  static constexpr int S = D == 256 ? 3 : D == 128 ? 4 : 6;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int KC = D == 256 ? 2 : 1;   // chunks of a K row a lane
+  static constexpr int KG = D / 8 / KC;         // bytes of such a chunk
+  static constexpr int KW = KG / 4;             // words
+  static constexpr int VG = D / 16;             // bytes of a V row a lane
+  static constexpr int VW = VG / 4;
+  static constexpr int MT = D / 16;             // 16-dimension tiles of O^T
+  // A stage: K, V, K scales, V scales of one block.
+  static constexpr int kVOff = 8 * D, kSOff = 16 * D, kStage = 18 * D;
+  static constexpr int kRing = W * S * kStage;
+  // Merge buffer: TPP accumulator tiles of every warp at a time.
+  static constexpr int TPP = MT * NT < 8 ? MT * NT : 8;
+  static constexpr int kMerge = W * TPP * 32 * 16;
+  static constexpr int kBytes = kRing + kMerge;
+  static_assert(CTAS * (kBytes + 2048) <= 227 * 1024, "shared memory of an SM");
+};
+
+template <typename Sh, int NSEG>
+__global__ void __launch_bounds__(Sh::W * 32, Sh::CTAS)
+kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
+  constexpr int D = Sh::D, NT = Sh::NT, W = Sh::W, S = Sh::S, MT = Sh::MT;
+  constexpr int KC = Sh::KC, KG = Sh::KG, KW = Sh::KW, VG = Sh::VG, VW = Sh::VW;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float wm[W][Sh::kRows], wl[W][Sh::kRows];
+  __shared__ int64_t s_row[Sh::kRows];  // offset in `out` of each row of the tile, or -1
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int64_t vb = range_start(sc, blockIdx.x), ve = range_start(sc, blockIdx.x + 1);
+  if (vb >= ve) return;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S * Sh::kStage;
+  float4* mbuf = reinterpret_cast<float4*>(smem + Sh::kRing);
+
+  // ---- The copies' side: the next block of this warp, its page read one
+  // step ahead of its copies.
+  Seg is = seg_at(sc, p, vb, vb, ve);
+  Seg cs = is;
+  int32_t ij = is.j0 + warp;
+  bool pend = true;
+  int32_t pkey = 0, ppage = 0, pg = 0, pseq = 0;
+  auto look_ahead = [&]() {
+    while (is.v < ve && ij >= is.j1) {
+      seg_next(sc, p, is, vb, ve);
+      ij = is.j0 + warp;
+    }
+    pend = is.v < ve;
+    if (!pend) return;
+    pkey = (is.fb + ij) * kBlk;
+    pg = is.g;
+    pseq = sc.tile[is.e].seq;
+    const int32_t slot = pkey >> p.page_shift;
+    ppage = slot < p.mpps ? __ldg(p.page_table + static_cast<int64_t>(pseq) * p.mpps + slot) : -1;
+    ij += W;
+  };
+  uint32_t bad_pages = 0;  // bit st: the block in stage st has no good page
+  auto issue = [&](int st) {
+    if (pend) {
+      const bool ok = ppage >= 0 && ppage < p.num_pages;
+      if (!ok && lane == 0)
+        report_error(p.ws, (pkey >> p.page_shift) < p.mpps ? RPA_DEVERR_PAGE_ID : RPA_DEVERR_LENGTHS,
+                     pseq);
+      bad_pages = (bad_pages & ~(1u << st)) | (ok ? 0u : 1u << st);
+      // The block's first row in the pool (rows of one head in a page are
+      // contiguous); a bad page's bytes arrive as zeros.
+      const int64_t row = ok ? ((static_cast<int64_t>(ppage) * p.hkv + pg) << p.page_shift) +
+                                   (pkey & ((1 << p.page_shift) - 1))
+                             : 0;
+      const uint32_t dst = ring + st * Sh::kStage;
+      const uint8_t* kp = p.k + row * (D / 2);
+      const uint8_t* vp = p.v + row * (D / 2);
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+          copy_async<KG>(dst + ((r * KC + j) * 32 + lane) * KG, kp + (g + 8 * r) * (D / 2) + (c + 4 * j) * KG,
+                         ok ? KG : 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        copy_async<VG>(dst + Sh::kVOff + (i * 32 + lane) * VG,
+                       vp + (2 * c + (i & 1) + 8 * (i >> 1)) * (D / 2) + g * VG, ok ? VG : 0);
+      if (lane < D / 8) {
+        constexpr int H = D / 16;  // 16-byte pieces of a block's K (or V) scales
+        const uint8_t* src = (lane < H ? p.ks : p.vs) + row * (D / 16) + (lane & (H - 1)) * 16;
+        copy_async<16>(dst + Sh::kSOff + lane * 16, src, ok ? 16 : 0);
+      }
+    }
+    copy_commit();
+  };
+  look_ahead();
+#pragma unroll
+  for (int st = 0; st < S; ++st) {
+    issue(st);
+    if (pend) look_ahead();
+  }
+
+  int st = 0;
+  for (; cs.v < ve; seg_next(sc, p, cs, vb, ve)) {
+    if (cs.j0 >= cs.j1) continue;  // only the segment's merge charge lies in this range
+    const Kv4Tile& tl = sc.tile[cs.e];
+    const int G = p.group;
+    // ---- The tile's queries as B fragments: lane (g, c) holds row g (+ 8 nt)
+    // and the dimensions of its chunks.
+    uint32_t qf[KC * KW][NT][4];
+    float sc0[NT], sc1[NT];   // logit scales of this lane's columns 2c, 2c + 1
+    int32_t lo0[NT], hi0[NT], lo1[NT], hi1[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int n = g + 8 * nt;
+      const int r = tl.r0 + n;
+      const bool has = n < tl.nrows;
+      const int64_t off = (static_cast<int64_t>(tl.q0 + r / G) * p.hq + cs.g * G + r % G) * D;
+      if (warp == 0 && c == 0) s_row[n] = has ? off : -1;
+      uint32_t top = 0;
+#pragma unroll
+      for (int w = 0; w < KC * KW; ++w) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (has)
+          u = __ldg(reinterpret_cast<const uint4*>(p.q + off + (c + 4 * (w / KW)) * (2 * KG) + 8 * (w % KW)));
+        qf[w][nt][0] = u.x;
+        qf[w][nt][1] = u.y;
+        qf[w][nt][2] = u.z;
+        qf[w][nt][3] = u.w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          top = max(top, qf[w][nt][i] & 0x7fffu);
+          top = max(top, (qf[w][nt][i] >> 16) & 0x7fffu);
+        }
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^ex: the power of two at or below the row's largest magnitude.
+      uint32_t ex = top >> 7;
+      if (ex == 0 || ex == 255) ex = 127;
+      ex = min(ex, 253u);
+      const float down = __uint_as_float((254u - ex) << 23), up = __uint_as_float(ex << 23);
+#pragma unroll
+      for (int w = 0; w < KC * KW; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t u = qf[w][nt][i];
+          qf[w][nt][i] = pack_f16x2(__uint_as_float(u << 16) * down, __uint_as_float(u & 0xffff0000u) * down);
+        }
+      sc0[nt] = p.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * c);
+      sc1[nt] = p.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * c + 4);
+      // Rows past the tile's last share its last row's keys; they are not written.
+      hi0[nt] = tl.pos0 + min(tl.r0 + 8 * nt + 2 * c, tl.r0 + tl.nrows - 1) / G;
+      hi1[nt] = tl.pos0 + min(tl.r0 + 8 * nt + 2 * c + 1, tl.r0 + tl.nrows - 1) / G;
+      lo0[nt] = first_visible(hi0[nt], tl.window);
+      lo1[nt] = first_visible(hi1[nt], tl.window);
+    }
+    const int32_t seg_lo = tile_lo(tl, G), seg_hi = tile_hi(tl, G);
+    // Keys every row sees.
+    const int32_t all_lo = first_visible(seg_hi, tl.window), all_hi = tl.pos0 + tl.r0 / G;
+
+    float o[MT][NT][4];
+    float m0[NT], m1[NT], l0[NT], l1[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m0[nt] = m1[nt] = -INFINITY;
+      l0[nt] = l1[nt] = 0.f;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.f;
+    }
+
+    for (int32_t j = cs.j0 + warp; j < cs.j1; j += W) {
+      const int32_t key0 = (cs.fb + j) * kBlk;
+      copy_wait<S - 1>();
+      __syncwarp();  // the scales are other lanes' copies
+      const uint32_t src = ring + st * Sh::kStage;
+      const bool bad = (bad_pages >> st) & 1u;
+      // ---- S^T = K Q^T
+      float x[NT][4];
+      {
+        float acc[2][NT][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) acc[i][nt][0] = acc[i][nt][1] = acc[i][nt][2] = acc[i][nt][3] = 0.f;
+#pragma unroll
+        for (int jc = 0; jc < KC; ++jc) {
+          uint32_t ka[KW], kb[KW];
+          lds<KW>(src + (jc * 32 + lane) * KG, ka);
+          lds<KW>(src + ((KC + jc) * 32 + lane) * KG, kb);
+          // Scale bytes of the chunk's 16-dimension blocks (two, or one of
+          // 64-dimension rows) in rows g and g + 8.
+          uint32_t sa, sb;
+          if constexpr (KW == 4) {
+            sa = lds_u16(src + Sh::kSOff + g * (D / 16) + (c + 4 * jc) * 2);
+            sb = lds_u16(src + Sh::kSOff + (g + 8) * (D / 16) + (c + 4 * jc) * 2);
+          } else {
+            sa = lds_u8(src + Sh::kSOff + g * (D / 16) + c);
+            sb = lds_u8(src + Sh::kSOff + (g + 8) * (D / 16) + c);
+          }
+#pragma unroll
+          for (int w = 0; w < KW; ++w) {
+            const uint32_t ha = kv4::scale_pair((sa >> (8 * (w >> 1))) & 255u, (sa >> (8 * (w >> 1))) & 255u);
+            const uint32_t hb = kv4::scale_pair((sb >> (8 * (w >> 1))) & 255u, (sb >> (8 * (w >> 1))) & 255u);
+            uint32_t a[4], b[4];
+            kv4::decode8(ka[w], a);
+            kv4::decode8(kb[w], b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[i] = kv4::hmul2(a[i], ha);
+              b[i] = kv4::hmul2(b[i], hb);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(acc[0][nt], a[0], b[0], a[1], b[1], qf[jc * KW + w][nt][0], qf[jc * KW + w][nt][1]);
+              mma_f16(acc[1][nt], a[2], b[2], a[3], b[3], qf[jc * KW + w][nt][2], qf[jc * KW + w][nt][3]);
+            }
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          x[nt][0] = (acc[0][nt][0] + acc[1][nt][0]) * sc0[nt];
+          x[nt][1] = (acc[0][nt][1] + acc[1][nt][1]) * sc1[nt];
+          x[nt][2] = (acc[0][nt][2] + acc[1][nt][2]) * sc0[nt];
+          x[nt][3] = (acc[0][nt][3] + acc[1][nt][3]) * sc1[nt];
+        }
+      }
+      // ---- Mask (blocks at a row's edges, or without a page)
+      const bool edge = bad || key0 < all_lo || key0 + kBlk - 1 > all_hi;
+      if (edge) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int32_t ka = key0 + g, kb = key0 + g + 8;
+          if (bad || ka < lo0[nt] || ka > hi0[nt]) x[nt][0] = -INFINITY;
+          if (bad || ka < lo1[nt] || ka > hi1[nt]) x[nt][1] = -INFINITY;
+          if (bad || kb < lo0[nt] || kb > hi0[nt]) x[nt][2] = -INFINITY;
+          if (bad || kb < lo1[nt] || kb > hi1[nt]) x[nt][3] = -INFINITY;
+        }
+      }
+      // ---- Online softmax
+      uint32_t pb[NT][2];
+      bool grow = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        grow |= fmaxf(x[nt][0], x[nt][2]) > m0[nt] + 8.f || fmaxf(x[nt][1], x[nt][3]) > m1[nt] + 8.f;
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float t0 = fmaxf(x[nt][0], x[nt][2]), t1 = fmaxf(x[nt][1], x[nt][3]);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
+            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
+          }
+          t0 = fmaxf(t0, m0[nt]);
+          t1 = fmaxf(t1, m1[nt]);
+          const float f0 = t0 == -INFINITY ? 1.f : fast_exp2(m0[nt] - t0);
+          const float f1 = t1 == -INFINITY ? 1.f : fast_exp2(m1[nt] - t1);
+          m0[nt] = t0;
+          m1[nt] = t1;
+          l0[nt] *= f0;
+          l1[nt] *= f1;
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            o[t][nt][0] *= f0;
+            o[t][nt][1] *= f1;
+            o[t][nt][2] *= f0;
+            o[t][nt][3] *= f1;
+          }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float r0 = m0[nt] == -INFINITY ? 0.f : m0[nt], r1 = m1[nt] == -INFINITY ? 0.f : m1[nt];
+        const float p0 = fast_exp2(x[nt][0] - r0), p1 = fast_exp2(x[nt][1] - r1);
+        const float p2 = fast_exp2(x[nt][2] - r0), p3 = fast_exp2(x[nt][3] - r1);
+        l0[nt] += p0 + p2;
+        l1[nt] += p1 + p3;
+        pb[nt][0] = transpose8x8(pack_f16x2(p0, p1));
+        pb[nt][1] = transpose8x8(pack_f16x2(p2, p3));
+      }
+      // ---- O^T += V^T P^T
+      {
+        uint32_t vw[4][VW];
+        uint32_t sv[4];  // scale bytes of this lane's dimensions in its four keys
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int kk = 2 * c + (i & 1) + 8 * (i >> 1);
+          lds<VW>(src + Sh::kVOff + (i * 32 + lane) * VG, vw[i]);
+          if constexpr (D == 256)
+            sv[i] = lds_u16(src + Sh::kSOff + D + kk * (D / 16) + 2 * g);
+          else
+            sv[i] = lds_u8(src + Sh::kSOff + D + kk * (D / 16) + (D == 128 ? g : g >> 1));
+          // Keys no row sees: whatever their bytes, their values are zeros.
+          if (edge && (bad || key0 + kk < seg_lo || key0 + kk > seg_hi)) sv[i] = 0;
+        }
+        uint32_t s01 = kv4::scale_pair(sv[0] & 255u, sv[1] & 255u);
+        uint32_t s23 = kv4::scale_pair(sv[2] & 255u, sv[3] & 255u);
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          if (D == 256 && w == 2) {
+            s01 = kv4::scale_pair(sv[0] >> 8, sv[1] >> 8);
+            s23 = kv4::scale_pair(sv[2] >> 8, sv[3] >> 8);
+          }
+          constexpr uint32_t kLow = 0x0f0f0f0fu;
+          uint32_t e01[4], d01[4], e23[4], d23[4];  // even and odd dimensions, key pairs
+          kv4::decode8(bit_select(kLow, vw[0][w], vw[1][w] << 4), e01);
+          kv4::decode8(bit_select(kLow, vw[0][w] >> 4, vw[1][w]), d01);
+          kv4::decode8(bit_select(kLow, vw[2][w], vw[3][w] << 4), e23);
+          kv4::decode8(bit_select(kLow, vw[2][w] >> 4, vw[3][w]), d23);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t a0 = kv4::hmul2(e01[t], s01), a1 = kv4::hmul2(d01[t], s01);
+            const uint32_t a2 = kv4::hmul2(e23[t], s23), a3 = kv4::hmul2(d23[t], s23);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(o[4 * w + t][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the scales: the stage may be refilled
+      issue(st);
+      if (pend) look_ahead();
+      if (++st == S) st = 0;
+    }
+
+    // ---- Merge the warps: each scales its state by its share of the
+    // normalised result, then the shares are added in warp order.
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        l0[nt] += __shfl_xor_sync(0xffffffffu, l0[nt], off);
+        l1[nt] += __shfl_xor_sync(0xffffffffu, l1[nt], off);
+      }
+      if (g == 0) {
+        wm[warp][8 * nt + 2 * c] = m0[nt];
+        wm[warp][8 * nt + 2 * c + 1] = m1[nt];
+        wl[warp][8 * nt + 2 * c] = l0[nt];
+        wl[warp][8 * nt + 2 * c + 1] = l1[nt];
+      }
+    }
+    __syncthreads();
+    const bool whole = cs.j0 == 0 && cs.j1 == cs.nb;
+    const int slot = 2 * blockIdx.x + (vb < cs.v ? 1 : 0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int n = 8 * nt + 2 * c + h;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, wm[w][n]);
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          L += wl[w][n] * (M == -INFINITY ? 1.f : fast_exp2(wm[w][n] - M));
+        const float mine = h ? m1[nt] : m0[nt];
+        f[h] = L == 0.f ? 0.f : (M == -INFINITY ? 1.f : fast_exp2(mine - M)) / L;
+        if (!whole && warp == 0 && g == 0)
+          p.part_lse[static_cast<int64_t>(slot) * Sh::kRows + n] = L == 0.f ? -INFINITY : M + __log2f(L);
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        o[t][nt][0] *= f[0];
+        o[t][nt][1] *= f[1];
+        o[t][nt][2] *= f[0];
+        o[t][nt][3] *= f[1];
+      }
+    }
+    constexpr int kPasses = MT * NT / Sh::TPP;
+#pragma unroll
+    for (int ps = 0; ps < kPasses; ++ps) {
+#pragma unroll
+      for (int i = 0; i < Sh::TPP; ++i) {
+        const int q = ps * Sh::TPP + i;
+        const float (&a)[4] = o[q / NT][q % NT];
+        mbuf[(warp * Sh::TPP + i) * 32 + lane] = make_float4(a[0], a[1], a[2], a[3]);
+      }
+      __syncthreads();
+      for (int i = tid; i < Sh::TPP * 32; i += W * 32) {
+        float4 a = mbuf[i];
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+          const float4 b = mbuf[w * Sh::TPP * 32 + i];
+          a.x += b.x;
+          a.y += b.y;
+          a.z += b.z;
+          a.w += b.w;
+        }
+        const int q = ps * Sh::TPP + (i >> 5);
+        const int mt = q / NT, nt = q % NT;
+        // Lane (g, c) holds columns 2c, 2c + 1 of dimensions d, d + 1.
+        const int d = g * (D / 8) + 2 * mt, n = 8 * nt + 2 * c;
+        if (whole) {
+          const int64_t r0 = s_row[n], r1 = s_row[n + 1];
+          if (r0 >= 0) *reinterpret_cast<uint32_t*>(p.out + r0 + d) = pack_bf16x2(a.x, a.z);
+          if (r1 >= 0) *reinterpret_cast<uint32_t*>(p.out + r1 + d) = pack_bf16x2(a.y, a.w);
+        } else {
+          float* dst = p.part_o + (static_cast<int64_t>(slot) * Sh::kRows + n) * D + d;
+          *reinterpret_cast<float2*>(dst) = make_float2(a.x, a.z);
+          *reinterpret_cast<float2*>(dst + D) = make_float2(a.y, a.w);
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// The segments cut across CTAs: out = sum_c 2^(lse_c - M) O_c / sum_c 2^(lse_c - M)
+// over the CTAs that hold a part.  One CTA per boundary between two ranges;
+// the first boundary inside a segment takes it, one warp per row.
+template <int D, int ROWS, int NSEG>
+__global__ void __launch_bounds__(256)
+kv4_combine_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
+  constexpr int E = D / 32;
+  const int b = blockIdx.x + 1;
+  const int64_t x = range_start(sc, b);
+  const Seg s = seg_at(sc, p, x, 0, sc.v0[sc.n]);
+  const int64_t end = s.v + s.nb;
+  // This boundary lies inside the segment, and the one before it does not.
+  const bool mine = x > s.v && x < end && range_start(sc, b - 1) <= s.v;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!mine) return;
+  int parts = 2;
+  while (range_start(sc, b - 1 + parts) < end) ++parts;
+  const Kv4Tile& tl = sc.tile[s.e];
+  const int lane = threadIdx.x & 31;
+  for (int n = threadIdx.x >> 5; n < tl.nrows; n += 8) {
+    auto slot = [&](int k) {
+      const int cta = b - 1 + k;
+      return static_cast<int64_t>(2 * cta + (k == 0 && range_start(sc, cta) < s.v ? 1 : 0)) * ROWS + n;
+    };
+    float M = -INFINITY;
+    for (int k = lane; k < parts; k += 32) M = fmaxf(M, p.part_lse[slot(k)]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float acc[E], wsum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+      const int nk = min(32, parts - k0);
+      float w_l = 0.f;
+      if (lane < nk) {
+        const float lse = p.part_lse[slot(k0 + lane)];
+        w_l = lse == -INFINITY ? 0.f : fast_exp2(lse - M);
+      }
+      for (int k = 0; k < nk; ++k) {
+        const float w = __shfl_sync(0xffffffffu, w_l, k);
+        wsum += w;
+        const float* src = p.part_o + slot(k0 + k) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = *reinterpret_cast<const float2*>(src + e);
+          acc[e] = fmaf(w, v.x, acc[e]);
+          acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
+        }
+      }
+    }
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+    const int r = tl.r0 + n;
+    __nv_bfloat16* dst = p.out +
+        (static_cast<int64_t>(tl.q0 + r / p.group) * p.hq + s.g * p.group + r % p.group) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
+template <int D, int NT, int NSEG>
+int launch_t(const Plan& plan, const Kv4Params& p, const Plan::Kv4Launch& l, cudaStream_t stream) {
+  using Sh = Kv4Shape<D, NT>;
+  auto* kernel = kv4_decode_kernel<Sh, NSEG>;
+  if (int e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), Sh::kBytes)) return e;
+  Kv4Sched<NSEG>& sc = thread_staging<Kv4Sched<NSEG>>();  // copied into the launch parameters
+  sc.n = l.end - l.begin;
+  sc.n_ctas = l.n_ctas;
+  sc.v0[0] = 0;
+  for (int i = 0; i < sc.n; ++i) {
+    const Plan::Kv4Tile& t = plan.kv4_tiles[l.begin + i];
+    sc.tile[i] = Kv4Tile{t.seq, t.q0, t.r0, t.nrows, t.pos0, t.window};
+    sc.v0[i + 1] = sc.v0[i] + static_cast<int64_t>(t.nb + kKv4SegCost) * plan.hkv;
+  }
+  kernel<<<l.n_ctas, Sh::W * 32, Sh::kBytes, stream>>>(p, sc);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return static_cast<int>(e);
+  trace_mark(RPA_KERNEL_KV4_DECODE, stream);
+  if (!l.cut) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(l.n_ctas - 1);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D, Sh::kRows, NSEG>, p, sc);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  trace_mark(RPA_KERNEL_KV4_COMBINE, stream);
+  return 0;
+}
+
+template <int D, int NT>
+int launch_n(const Plan& plan, const Kv4Params& p, const Plan::Kv4Launch& l, cudaStream_t stream) {
+  // Two sizes of launch parameters: 4 KB and 32 KB.
+  return l.end - l.begin <= kKv4TilesSmall ? launch_t<D, NT, kKv4TilesSmall>(plan, p, l, stream)
+                                           : launch_t<D, NT, kKv4TilesLarge>(plan, p, l, stream);
+}
+
+}  // namespace
+
+int kv4_ctas_per_sm(int32_t head_dim, int32_t nt) {
+  return head_dim * nt >= 256 ? Kv4Shape<256, 1>::CTAS : Kv4Shape<128, 1>::CTAS;
+}
+int kv4_warps(int32_t head_dim, int32_t nt) {
+  return head_dim * nt >= 256 ? Kv4Shape<256, 1>::W : Kv4Shape<128, 1>::W;
+}
+
+int launch_kv4_decode(const Plan& plan, const Args& a, void* stream) {
+  Kv4Params p;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.k = static_cast<const uint8_t*>(a.k_pages);
+  p.v = static_cast<const uint8_t*>(a.v_pages);
+  p.ks = a.k_block_scales;
+  p.vs = a.v_block_scales;
+  p.page_table = a.page_table;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.ws = a.workspace;
+  p.part_o = reinterpret_cast<float*>(a.workspace + plan.off_partial_o);
+  p.part_lse = reinterpret_cast<float*>(a.workspace + plan.off_partial_lse);
+  p.hq = plan.hq;
+  p.hkv = plan.hkv;
+  p.group = plan.hq / plan.hkv;
+  int shift = 0;
+  while ((1 << shift) < plan.p) ++shift;
+  p.page_shift = shift;
+  p.mpps = plan.mpps;
+  p.num_pages = plan.num_pages;
+  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  for (const Plan::Kv4Launch& l : plan.kv4_launches) {
+    int e = static_cast<int>(cudaErrorInvalidValue);
+    switch (plan.d) {
+      case 64: e = l.nt == 1 ? launch_n<64, 1>(plan, p, l, s) : launch_n<64, 2>(plan, p, l, s); break;
+      case 128: e = l.nt == 1 ? launch_n<128, 1>(plan, p, l, s) : launch_n<128, 2>(plan, p, l, s); break;
+      case 256: e = launch_n<256, 1>(plan, p, l, s); break;
+    }
+    if (e) return e;
+  }
+  return 0;
+}
+
+}  // namespace rpa

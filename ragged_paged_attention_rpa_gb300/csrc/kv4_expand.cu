@@ -1,0 +1,131 @@
+// 4-bit pages widened to bf16 for the tensor-core prefill.
+//
+// A prompt's keys are used by every query block: widening them in the prefill
+// kernel would convert each key once per block (128 x D codes per 128-key tile
+// against 128 x 128 exponentials: at D = 256 more work than the softmax).  So
+// the keys the sequences' queries see are widened once, to scratch pages in
+// the workspace ([page][slot][head][dim], the bf16 pool's layout) with a page
+// table of their own, and the prefill runs on those.  The values are exact in
+// bf16 (six significant bits).
+//
+// One thread per 16 dimensions of K and of V; HBM-bound: 0.5625 bytes an
+// element read, 2 written (and the prefill reads them back from L2 or HBM).
+#include <algorithm>
+
+#include "common.cuh"
+#include "kv4.cuh"
+#include "rpa_internal.h"
+
+namespace rpa {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct ExpandList {
+  int32_t n, page_end;  // sequences; one past the last scratch page
+  Plan::Kv4Expand s[kKv4ExpandSeqs];
+};
+
+struct ExpandParams {
+  const uint2* k;
+  const uint2* v;
+  const uint8_t* ks;
+  const uint8_t* vs;
+  uint4* k_out;
+  uint4* v_out;
+  const int32_t* page_table;
+  int32_t* table_out;
+  unsigned char* ws;
+  int32_t hkv, bpr_shift, page_shift, mpps, num_pages;
+};
+
+__device__ __forceinline__ void store_block(uint4* dst, uint2 codes, uint32_t byte) {
+  uint32_t h[8], w[8];
+  kv4::decode_block(codes, byte, h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = kv4::half2_floats(h[i]);
+    w[i] = pack_bf16x2(f.x, f.y);
+  }
+  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+__global__ void __launch_bounds__(kThreads)
+kv4_expand_kernel(const ExpandParams p, const __grid_constant__ ExpandList list) {
+  const int32_t first = list.s[0].page0;
+  const int64_t row_blocks = static_cast<int64_t>(p.hkv) << p.bpr_shift;  // of one key
+  const int64_t total = (static_cast<int64_t>(list.page_end - first) << p.page_shift) * row_blocks;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += step) {
+    const int64_t key_row = i / row_blocks;
+    const int32_t hb = static_cast<int32_t>(i - key_row * row_blocks);
+    const int32_t scratch = first + static_cast<int32_t>(key_row >> p.page_shift);
+    const int32_t in = static_cast<int32_t>(key_row) & ((1 << p.page_shift) - 1);
+    int lo = 0, hi = list.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (list.s[mid].page0 <= scratch) lo = mid; else hi = mid - 1;
+    }
+    const Plan::Kv4Expand& e = list.s[lo];
+    const int32_t slot = e.slot0 + (scratch - e.page0);
+    const int64_t at = static_cast<int64_t>(e.seq) * p.mpps + slot;
+    const int32_t page = __ldg(p.page_table + at);
+    const bool ok = page >= 0 && page < p.num_pages;
+    if (in == 0 && hb == 0) {
+      p.table_out[at] = ok ? scratch : -1;
+      if (!ok) report_error(p.ws, RPA_DEVERR_PAGE_ID, e.seq);
+    }
+    const int32_t key = (slot << p.page_shift) + in;
+    if (!ok || key < e.lo || key >= e.hi) continue;
+    const int32_t h = hb >> p.bpr_shift, b = hb & ((1 << p.bpr_shift) - 1);
+    const int64_t src = ((((static_cast<int64_t>(page) * p.hkv + h) << p.page_shift) + in) << p.bpr_shift) + b;
+    const int64_t dst = 2 * (static_cast<int64_t>(first) * (row_blocks << p.page_shift) + i);
+    const uint2 kc = __ldg(p.k + src), vc = __ldg(p.v + src);
+    const uint32_t ks = __ldg(p.ks + src), vs = __ldg(p.vs + src);
+    store_block(p.k_out + dst, kc, ks);
+    store_block(p.v_out + dst, vc, vs);
+  }
+}
+
+}  // namespace
+
+int launch_kv4_expand(const Plan& plan, const Args& a, void* stream) {
+  ExpandParams p;
+  p.k = static_cast<const uint2*>(a.k_pages);
+  p.v = static_cast<const uint2*>(a.v_pages);
+  p.ks = a.k_block_scales;
+  p.vs = a.v_block_scales;
+  p.k_out = reinterpret_cast<uint4*>(a.workspace + plan.off_kv4_k);
+  p.v_out = reinterpret_cast<uint4*>(a.workspace + plan.off_kv4_v);
+  p.page_table = a.page_table;
+  p.table_out = reinterpret_cast<int32_t*>(a.workspace + plan.off_kv4_table);
+  p.ws = a.workspace;
+  p.hkv = plan.hkv;
+  int shift = 0;
+  while ((16 << shift) < plan.d) ++shift;
+  p.bpr_shift = shift;
+  shift = 0;
+  while ((1 << shift) < plan.p) ++shift;
+  p.page_shift = shift;
+  p.mpps = plan.mpps;
+  p.num_pages = plan.num_pages;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ExpandList& list = thread_staging<ExpandList>();  // copied into the launch parameters
+  const size_t n = plan.kv4_expand.size();
+  for (size_t off = 0; off < n; off += kKv4ExpandSeqs) {
+    list.n = static_cast<int32_t>(std::min<size_t>(kKv4ExpandSeqs, n - off));
+    for (int i = 0; i < list.n; ++i) list.s[i] = plan.kv4_expand[off + i];
+    list.page_end = off + list.n < n ? plan.kv4_expand[off + list.n].page0 : plan.kv4_scratch_pages;
+    const int64_t blocks = (static_cast<int64_t>(list.page_end - list.s[0].page0) << p.page_shift) * p.hkv
+                           << p.bpr_shift;
+    const int grid = static_cast<int>(std::min<int64_t>((blocks + kThreads - 1) / kThreads, plan.num_sms * 64));
+    kv4_expand_kernel<<<grid, kThreads, 0, s>>>(p, list);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return static_cast<int>(e);
+    trace_mark(RPA_KERNEL_KV4_EXPAND, stream);
+  }
+  return 0;
+}
+
+}  // namespace rpa

@@ -283,7 +283,7 @@ void plan_prefill(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_
   std::vector<Cost> all;
   for (int32_t s = 0; s < plan.num_seqs; ++s) {
     const int32_t ql = cu[s + 1] - cu[s];
-    if (ql <= 1) continue;
+    if (ql < plan.prefill_min_q) continue;
     const int32_t L = kv[s];
     const int32_t w = win ? win[s] : 0;
     const int64_t span = plan.prefill_pairs ? 2 * qb : qb;   // query tokens per item
@@ -447,7 +447,7 @@ void plan_prefill(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_
       double total = 0;
       bool whole_prefix = true;
       for (int32_t sq = 0; sq < plan.num_seqs; ++sq) {
-        if (cu[sq + 1] - cu[sq] <= 1) continue;
+        if (cu[sq + 1] - cu[sq] < plan.prefill_min_q) continue;
         total += static_cast<double>(kv[sq]) * plan.d * 2.0 * 2.0 * plan.hkv;
         const int32_t w = win ? win[sq] : 0;
         if (w > 0 && w < kv[sq]) whole_prefix = false;
@@ -456,7 +456,7 @@ void plan_prefill(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_
       std::vector<int32_t> gid(static_cast<size_t>(plan.num_seqs) * plan.hkv, 0);
       double acc = 0;
       for (int32_t sq = 0; sq < plan.num_seqs; ++sq) {
-        if (cu[sq + 1] - cu[sq] <= 1) continue;
+        if (cu[sq + 1] - cu[sq] < plan.prefill_min_q) continue;
         for (int32_t h = 0; h < plan.hkv; ++h) {
           gid[static_cast<size_t>(sq) * plan.hkv + h] =
               std::min(ngroups - 1, static_cast<int32_t>(acc * ngroups / total));
@@ -513,7 +513,7 @@ TileStats prefill_tile_stats(const Plan& plan, const int32_t* cu, const int32_t*
   TileStats t;
   for (int32_t s = 0; s < plan.num_seqs; ++s) {
     const int32_t ql = cu[s + 1] - cu[s];
-    if (ql <= 1) continue;
+    if (ql < plan.prefill_min_q) continue;
     const int32_t L = kv[s];
     const int32_t w = win ? win[s] : 0;
     for (int64_t b = 0; b < ceil_div(ql, span); ++b) {
@@ -560,11 +560,126 @@ double prefill_cost_us(const TileStats& t, int32_t head_dim, int32_t sms) {
          kPrefillItemUs256 * f + kPrefillFixedUs;
 }
 
+// 4-bit pages.  A sequence whose q_len x G query rows per KV head number at
+// most kKv4MaxRows runs on the split-KV kernel; the others' visible pages are
+// widened to bf16 and run on the tensor-core prefill.
+constexpr int32_t kKv4MaxRows = 32;
+// Fewest key blocks (merge charges included) a warp of the split-KV kernel
+// gets before the batch is cut over more CTAs.
+constexpr int32_t kKv4BlocksPerWarp = 2;
+
+// Row tiles, launches and CTA counts of the split-KV part.
+void plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_t* win) {
+  const int32_t group = plan.hq / plan.hkv;
+  for (int32_t nt = 1; nt <= 2; ++nt) {
+    const int32_t first = static_cast<int32_t>(plan.kv4_tiles.size());
+    for (int32_t s = 0; s < plan.num_seqs; ++s) {
+      const int32_t ql = cu[s + 1] - cu[s];
+      if (ql < 1 || ql >= plan.prefill_min_q) continue;
+      const int32_t rows = ql * group;
+      // Tiles of 16 rows where a sequence has more than 8 and the kernel's
+      // registers hold them (head_dim below 256).
+      const int32_t want = rows > 8 && plan.d < 256 ? 2 : 1;
+      if (want != nt) continue;
+      ++plan.num_decode;
+      const int32_t w = win ? std::max(win[s], 0) : 0;
+      const int32_t pos0 = kv[s] - ql;
+      for (int32_t r0 = 0; r0 < rows; r0 += 8 * nt) {
+        const int32_t n = std::min(8 * nt, rows - r0);
+        const int32_t p0 = pos0 + r0 / group, p1 = pos0 + (r0 + n - 1) / group;
+        const int32_t lo = (w > 0 && p0 - (w - 1) > 0) ? p0 - (w - 1) : 0;
+        plan.kv4_tiles.push_back({s, cu[s], r0, n, pos0, w, p1 / 16 - lo / 16 + 1});
+      }
+    }
+    const int32_t last = static_cast<int32_t>(plan.kv4_tiles.size());
+    for (int32_t b = first; b < last; b += kKv4TilesLarge) {
+      const int32_t e = std::min(last, b + kKv4TilesLarge);
+      std::vector<int64_t> v0(1, 0);
+      for (int32_t i = b; i < e; ++i)
+        v0.push_back(v0.back() + static_cast<int64_t>(plan.kv4_tiles[i].nb + kKv4SegCost) * plan.hkv);
+      const int64_t total = v0.back();
+      const int64_t most = static_cast<int64_t>(plan.num_sms) * kv4_ctas_per_sm(plan.d, nt);
+      const int64_t n = std::max<int64_t>(1, std::min(most, total / (kKv4BlocksPerWarp * kv4_warps(plan.d, nt))));
+      Plan::Kv4Launch l{b, e, nt, static_cast<int32_t>(n), false};
+      // The boundaries between ranges that fall inside a segment cut it.
+      int64_t seg = -1, parts = 1;
+      for (int64_t c = 1; c < n; ++c) {
+        const int64_t x = total * c / n;
+        const size_t i = static_cast<size_t>(std::upper_bound(v0.begin(), v0.end(), x) - v0.begin()) - 1;
+        const int32_t nb = plan.kv4_tiles[b + static_cast<int32_t>(i)].nb;
+        const int64_t cost = nb + kKv4SegCost, off = (x - v0[i]) % cost;
+        if (off == 0 || off >= nb) continue;
+        l.cut = true;
+        const int64_t id = x - off;
+        parts = id == seg ? parts + 1 : 2;
+        seg = id;
+        plan.max_splits = std::max(plan.max_splits, static_cast<int32_t>(parts));
+      }
+      if (plan.kv_split == 0)
+        plan.kv_split = static_cast<int32_t>(std::min<int64_t>(ceil_div(total, n) * 16, 0x7fffffff));
+      plan.max_splits = std::max(plan.max_splits, 1);
+      plan.decode_ctas += n;
+      plan.kv4_part_rows = std::max(plan.kv4_part_rows, 2 * n * nt * 8);
+      plan.kv4_launches.push_back(l);
+    }
+  }
+}
+
+rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu, const int32_t* kv,
+                                const int32_t* win, const rpa_plan_options& opts) {
+  const int32_t group = plan.hq / plan.hkv;
+  if (plan.dtype != RPA_DTYPE_BF16 || opts.path == RPA_PATH_SIMT || plan.p < 16 ||
+      !prefill_tc_supported(plan.d, plan.p, group) || opts.kv_split != 0 ||
+      opts.prefill_pairs == 2 || opts.prefill_split > 0 || opts.decode_sms != 0 ||
+      opts.decode_kernel != 0 || opts.q_block > prefill_tokens_per_block(plan.d, group))
+    return RPA_ERR_UNSUPPORTED;
+  plan.kv_fp4 = true;
+  plan.path = RPA_PATH_TC;
+  plan.prefill_min_q = kKv4MaxRows / group + 1;
+  plan.num_decode = plan.num_prefill = 0;
+  plan_kv4_decode(plan, cu, kv, win);
+  size_t off = kHeaderBytes;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  if (plan.kv4_part_rows > 0) {
+    plan.off_partial_o = take(static_cast<size_t>(plan.kv4_part_rows) * plan.d * sizeof(float));
+    plan.off_partial_lse = take(static_cast<size_t>(plan.kv4_part_rows) * sizeof(float));
+  }
+  int64_t pages = 0;
+  for (int32_t s = 0; s < plan.num_seqs; ++s) {
+    const int32_t ql = cu[s + 1] - cu[s];
+    if (ql < plan.prefill_min_q) continue;
+    ++plan.num_prefill;
+    const int32_t w = win ? win[s] : 0;
+    const int32_t p0 = kv[s] - ql;
+    const int32_t lo = (w > 0 && p0 - (w - 1) > 0) ? p0 - (w - 1) : 0;
+    const int32_t slot0 = lo / plan.p;
+    plan.kv4_expand.push_back({s, slot0, static_cast<int32_t>(pages), lo, kv[s]});
+    pages += ceil_div(kv[s], plan.p) - slot0;
+    if (pages > 0x7fffffff) return RPA_ERR_UNSUPPORTED;
+  }
+  plan.kv4_scratch_pages = static_cast<int32_t>(pages);
+  if (plan.num_prefill > 0) {
+    plan_prefill(plan, cu, kv, win, opts.q_block, 0, opts.prefill_dynamic == 0,
+                 opts.prefill_grouping == 0);
+    const size_t bytes = static_cast<size_t>(pages) * plan.p * plan.hkv * plan.d * 2;
+    plan.off_kv4_k = take(bytes);
+    plan.off_kv4_v = take(bytes);
+    plan.off_kv4_table = take(static_cast<size_t>(plan.num_seqs) * plan.mpps * sizeof(int32_t));
+  }
+  plan.ws_bytes = off;
+  return RPA_OK;
+}
+
 }  // namespace
 
 rpa_status_t build_schedule(Plan& plan, const int32_t* cu, const int32_t* kv,
                             const int32_t* win, const rpa_plan_options& opts) {
   const int32_t group = plan.hq / plan.hkv;
+  if (opts.kv_dtype == RPA_DTYPE_FP4_E2M1) return build_kv4_schedule(plan, cu, kv, win, opts);
   plan.num_decode = plan.num_prefill = 0;
   for (int32_t s = 0; s < plan.num_seqs; ++s) {
     int32_t ql = cu[s + 1] - cu[s];

@@ -25,6 +25,9 @@ constexpr size_t kHeaderBytes = 256;
 // Offset in the header of the dynamic prefill item counter (two int32: items
 // taken, CTAs finished), zero between launches.
 constexpr size_t kPrefillCounterOff = 64;
+// Offset in the header of the table kernels' counter (one int32: CTAs
+// finished), zero between launches.
+constexpr size_t kTablesCounterOff = 128;
 
 // One prefill work item: query block `qb` (of plan.q_block tokens) of
 // sequence `seq`, for KV head `head`.  Ordered longest first in the plan.
@@ -86,11 +89,21 @@ constexpr int kMaxDecodeCtas = 1024;
 constexpr int kMaxDecodeGrid = 512;
 constexpr int kDecodeSegCost = 7;
 
+// Split-KV attention over 4-bit pages (kv4_decode.cu): row tiles one launch
+// carries in its parameters (two sizes), and the charge, in 16-key blocks, for
+// each segment (its merge and output).
+constexpr int kKv4TilesSmall = 120;
+constexpr int kKv4TilesLarge = 992;
+constexpr int kKv4SegCost = 8;
+// Sequences whose 4-bit pages one expansion launch lists.
+constexpr int kKv4ExpandSeqs = 1024;
+
 struct Plan {
   // Problem description (checked against every rpa_forward call).
   int32_t num_seqs = 0, hq = 0, hkv = 0, d = 0, p = 0, mpps = 0, num_pages = 0;
   int32_t dtype = RPA_DTYPE_BF16;
   bool kv_fp8 = false;               // K/V pages are e4m3 bytes (decode only)
+  bool kv_fp4 = false;               // K/V pages are 4-bit codes with block scales
   bool has_window = false;
   int64_t total_q = 0;
 
@@ -139,7 +152,33 @@ struct Plan {
   std::vector<DecodeCut> dcut;
   int32_t dec_slots = 0;              // partial slots over all launches
 
-  // Prefill (q_len > 1).
+  // 4-bit pages: sequences of few query rows run on the split-KV kernel of
+  // kv4_decode.cu as row tiles (rows [r0, r0 + nrows) of the sequence, nb key
+  // blocks); the others' visible pages are widened to bf16 in the workspace
+  // (kv4_expand.cu) and run as prefill work.
+  struct Kv4Tile {
+    int32_t seq, q0, r0, nrows, pos0, window, nb;
+  };
+  struct Kv4Launch {
+    int32_t begin, end;  // tiles [begin, end)
+    int32_t nt;          // rows a tile: 8 nt
+    int32_t n_ctas;
+    bool cut;            // some segment is cut across CTAs
+  };
+  // A sequence's pages from table slot `slot0` on, widened to scratch pages
+  // from `page0` on; keys [lo, hi) are converted.
+  struct Kv4Expand {
+    int32_t seq, slot0, page0, lo, hi;
+  };
+  std::vector<Kv4Tile> kv4_tiles;
+  std::vector<Kv4Launch> kv4_launches;
+  std::vector<Kv4Expand> kv4_expand;
+  int64_t kv4_part_rows = 0;      // rows of the split-KV partials (two tiles a CTA)
+  int32_t kv4_scratch_pages = 0;
+  size_t off_kv4_k = 0, off_kv4_v = 0, off_kv4_table = 0;
+
+  // Prefill (q_len >= prefill_min_q).
+  int32_t prefill_min_q = 2;
   int32_t num_prefill = 0;
   int32_t q_block = 0;
   bool prefill_pairs = false;      // items are pairs of query blocks (SM-pair kernel)
@@ -185,6 +224,9 @@ struct Args {
   unsigned char* workspace;
   const float* k_scale = nullptr;  // fp8 pages: per-KV-head scales of K and V
   const float* v_scale = nullptr;
+  const uint8_t* k_block_scales = nullptr;  // 4-bit pages: a scale byte per 16 dimensions
+  const uint8_t* v_block_scales = nullptr;
+  int32_t pool_pages = 0;                   // pages of k_pages / v_pages (0: the plan's)
 };
 
 // Kernel launchers; each returns cudaError_t as int (0 = success).
@@ -228,6 +270,47 @@ struct PrologueArgs {
 };
 bool prologue_supported(int32_t head_dim);
 int launch_prologue(const PrologueArgs& a, void* stream);
+
+// Attention over 4-bit pages: the split-KV kernel over the plan's row tiles
+// (kv4_decode.cu), its CTAs per SM and warps per CTA, and the widening of the
+// prefill sequences' visible pages into the workspace, with a page table of
+// their own (kv4_expand.cu).
+int launch_kv4_decode(const Plan& plan, const Args& a, void* stream);
+int kv4_ctas_per_sm(int32_t head_dim, int32_t nt);
+int kv4_warps(int32_t head_dim, int32_t nt);
+int launch_kv4_expand(const Plan& plan, const Args& a, void* stream);
+
+// The 4-bit cache's write and read (kv4_cache.cu).
+struct Kv4CacheArgs {
+  const void* k_rows;  // written by a read
+  const void* v_rows;
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  const int64_t* slot_map;
+  unsigned char* workspace;  // error word, or null
+  int32_t tokens, hkv, head_dim, elem_bytes, page_size, num_pages;
+  bool read;
+};
+int launch_kv4_cache(const Kv4CacheArgs& a, void* stream);
+
+// Page tables built and released on the GPU (tables.cu).
+struct TableArgs {
+  const int32_t* lens;  // build: new tokens; release: finished flags
+  const int32_t* kv_lens_prev;
+  int32_t* page_table;
+  int32_t* free_pages;
+  const int32_t* free_count_prev;
+  int32_t* cu_q_lens;   // build only, as slot_map and max_tokens
+  int32_t* kv_lens;
+  int64_t* slot_map;
+  int32_t* free_count;
+  unsigned char* workspace;
+  int32_t num_seqs, page_size, mpps, num_pages, max_tokens;
+  bool release;
+};
+int launch_tables(const TableArgs& a, void* stream);
 
 // Raise a kernel's dynamic shared-memory limit to `bytes` on the current
 // device, once per (kernel, device); thread-safe.  Returns a cudaError_t.

@@ -42,6 +42,12 @@ class Batch:
     v_fp8: Optional[np.ndarray] = None
     k_scale: Optional[np.ndarray] = None  # [Hkv] float32
     v_scale: Optional[np.ndarray] = None
+    # 4-bit copies of the pools (see with_kv4): codes [num_pages, Hkv, P, D / 2]
+    # and block scales [num_pages, Hkv, P, D / 16], uint8.
+    k_fp4: Optional[np.ndarray] = None
+    v_fp4: Optional[np.ndarray] = None
+    k_fp4_scale: Optional[np.ndarray] = None
+    v_fp4_scale: Optional[np.ndarray] = None
 
     @property
     def num_seqs(self) -> int:
@@ -266,3 +272,50 @@ def with_fp8_kv(b: Batch) -> Batch:
 
 
 WORKLOADS["decode_fp8"] = lambda seed=1, **kw: with_fp8_kv(decode_batch(seed=seed, **kw))
+
+
+# The 4-bit KV format: e2m1 magnitudes, and the block scales (five exponent
+# bits of bias 15, three mantissa bits, no sign) that are written, by byte.
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+KV4_SCALES = np.array([(b & 7) * 2.0 ** -17 if b < 8 else (1 + (b & 7) / 8) * 2.0 ** ((b >> 3) - 15)
+                       for b in range(0xE3)])
+
+
+def _nearest(a, points, unit):
+    """Index of the point nearest to a / unit (ties to the even index); the
+    midpoints times the unit are exact in float64."""
+    mid = (points[1:] + points[:-1]) / 2
+    lo = np.zeros(a.shape, dtype=np.int64)
+    for i, m in enumerate(mid):
+        # Past the midpoint, or on it with an even index above.
+        lo += (a > m * unit) | ((a == m * unit) & ((i + 1) % 2 == 0))
+    return lo
+
+
+def kv4_encode(x):
+    """Rows [..., D] (float) -> codes [..., D / 2] and block scales [..., D / 16]
+    (uint8) of the 4-bit KV format: scale = max|x| / 6 rounded to the nearest
+    scale (ties to even, at most 10240), code = x / scale rounded to the nearest
+    magnitude (ties to even, at most 6); a block with a NaN or an infinity gets
+    scale byte 255 and zero codes."""
+    x = np.asarray(x, dtype=np.float64)
+    b = x.reshape(x.shape[:-1] + (x.shape[-1] // 16, 16))
+    good = np.isfinite(b).all(-1)
+    a = np.where(good[..., None], np.abs(b), 0.0)
+    byte = _nearest(a.max(-1), KV4_SCALES, 6.0)
+    scale = KV4_SCALES[byte]
+    code = np.where(scale[..., None] > 0, _nearest(a, E2M1, scale[..., None]), 0)
+    code = np.where(good[..., None], code | np.where(np.signbit(b), 8, 0), 0)
+    code = code.reshape(x.shape).astype(np.uint8)
+    return code[..., 0::2] | (code[..., 1::2] << 4), np.where(good, byte, 255).astype(np.uint8)
+
+
+def with_kv4(b: Batch) -> Batch:
+    """The batch with 4-bit copies of its K/V pools."""
+    def quant(pool):
+        vals = (pool.astype(np.uint32) << 16).view(np.float32) if pool.dtype == np.uint16 else pool
+        return kv4_encode(np.ascontiguousarray(vals.transpose(0, 2, 1, 3)))
+    kf, ks = quant(b.k_pages)
+    vf, vs = quant(b.v_pages)
+    return dataclasses.replace(b, name=b.name + "_kv4", k_fp4=kf, v_fp4=vf, k_fp4_scale=ks,
+                               v_fp4_scale=vs)
