@@ -47,8 +47,6 @@
 namespace rpa {
 namespace {
 
-constexpr int kBlk = 16;
-
 struct Kv4Params {
   const __nv_bfloat16* q;
   const uint8_t* k;
@@ -64,81 +62,39 @@ struct Kv4Params {
   float scale_log2;
 };
 
-// One launch's row tiles: tile e covers rows [r0, r0 + nrows) of sequence
-// seq, whose first query token is q0, at position pos0; its segments (one per
-// KV head) take [v0[e], v0[e + 1]) of the line.
+// One launch's row tiles: tile e covers rows [r0, r0 + nrows) of sequence seq,
+// whose first query token is q0, at position pos0.  Its segments (one per KV
+// head) have nb blocks from block fb on.  The CTAs' ranges of the line, by
+// where they start: block j of segment (tile, head), and their length
+// (blocks and merge charges); computed by the plan, since a search for it
+// would cost a CTA several misses of the constant cache before its first copy.
 struct Kv4Tile {
-  int32_t seq, q0, r0, nrows, pos0, window;
+  int32_t seq, q0, r0, nrows, pos0, window, fb, nb;
+};
+struct Kv4Start {
+  int32_t tile, head, j, len;
 };
 template <int NSEG>
 struct Kv4Sched {
-  int32_t n, n_ctas;
-  int64_t v0[NSEG + 1];
+  Kv4Start cta[kKv4MaxCtas];
   Kv4Tile tile[NSEG];
 };
 
-// Start of CTA c's range of the line.
-template <int NSEG>
-__device__ __forceinline__ int64_t range_start(const Kv4Sched<NSEG>& sc, int c) {
-  return sc.v0[sc.n] * c / sc.n_ctas;
-}
-
-// A segment: tile e and KV head g, as CTA range [vb, ve) sees it.
-struct Seg {
-  int e, g;
-  int64_t v;       // its start on the line
-  int32_t cost;    // its length on the line (blocks + merge charge)
-  int32_t nb, fb;  // blocks; index of the first one
-  int32_t j0, j1;  // blocks in the range: [j0, j1)
+// A place on the line: segment (e, g) entered at block j, rem units of the
+// range left from there.
+struct Place {
+  int32_t e, g, j, rem;
+  int32_t nb;
 };
-
-__device__ __forceinline__ int32_t tile_lo(const Kv4Tile& t, int32_t group) {
-  return first_visible(t.pos0 + t.r0 / group, t.window);
-}
-__device__ __forceinline__ int32_t tile_hi(const Kv4Tile& t, int32_t group) {
-  return t.pos0 + (t.r0 + t.nrows - 1) / group;
-}
-
 template <int NSEG>
-__device__ __forceinline__ void seg_fill(const Kv4Sched<NSEG>& sc, const Kv4Params& p, Seg& s,
-                                         int64_t vb, int64_t ve) {
-  const Kv4Tile& t = sc.tile[s.e];
-  s.fb = tile_lo(t, p.group) / kBlk;
-  s.nb = tile_hi(t, p.group) / kBlk - s.fb + 1;
-  s.cost = s.nb + kKv4SegCost;
-  s.j0 = static_cast<int32_t>(max(static_cast<int64_t>(0), vb - s.v));
-  s.j1 = static_cast<int32_t>(min(static_cast<int64_t>(s.nb), ve - s.v));
-}
-
-// The segment that holds position x of the line.
-template <int NSEG>
-__device__ __forceinline__ Seg seg_at(const Kv4Sched<NSEG>& sc, const Kv4Params& p, int64_t x,
-                                      int64_t vb, int64_t ve) {
-  int lo = 0, hi = sc.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (sc.v0[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  Seg s;
-  s.e = lo;
-  s.g = 0;
-  s.v = sc.v0[lo];
-  seg_fill(sc, p, s, vb, ve);
-  s.g = static_cast<int>((x - s.v) / s.cost);
-  s.v += static_cast<int64_t>(s.g) * s.cost;
-  seg_fill(sc, p, s, vb, ve);
-  return s;
-}
-
-template <int NSEG>
-__device__ __forceinline__ void seg_next(const Kv4Sched<NSEG>& sc, const Kv4Params& p, Seg& s,
-                                         int64_t vb, int64_t ve) {
-  s.v += s.cost;
+__device__ __forceinline__ void place_next(const Kv4Sched<NSEG>& sc, const Kv4Params& p, Place& s) {
+  s.rem -= s.nb + kKv4SegCost - s.j;
+  s.j = 0;
   if (++s.g == p.hkv) {
     s.g = 0;
     ++s.e;
   }
-  if (s.v < ve) seg_fill(sc, p, s, vb, ve);
+  if (s.rem > 0) s.nb = sc.tile[s.e].nb;
 }
 
 template <int BYTES>
@@ -203,16 +159,33 @@ __device__ __forceinline__ uint32_t bit_select(uint32_t m, uint32_t a, uint32_t 
   return r;
 }
 
-// Shapes of an instance: D, NT tiles of 8 rows, W warps a CTA, S blocks in
-// flight a warp, CTAS CTAs a SM.  O and Q take (D / 4 + D / 8) NT registers of
-// a thread: up to 48 leaves 16 warps a SM (128 registers each), 96 leaves 12.
+// The column reference before any score: below every scaled score that is not
+// -inf itself, and small enough that a score minus it is still finite.
+constexpr float kNoScore = -1e38f;
+
+// Scale byte `i` (0 or 1) of s, whose upper half is zero, as f16 in both
+// halves; and of two such words, in the low and the high half.
+__device__ __forceinline__ uint32_t scale_dup(uint32_t s, int i) {
+  return __byte_perm(s, 0, i == 0 ? 0x3030 : 0x3131) << 7;
+}
+__device__ __forceinline__ uint32_t scale_pair_of(uint32_t lo, uint32_t hi, int i) {
+  return __byte_perm(lo, hi, i == 0 ? 0x3430 : 0x3531) << 7;
+}
+
+// Shapes of an instance: D, NT tiles of 8 rows, W warps a CTA, CTAS CTAs a SM,
+// SUB 16-key parts a block, S blocks in flight a warp.  O and Q take (D / 4 +
+// D / 8) NT registers of a thread: up to 48 leaves 16 warps a SM (128 registers
+// each) and blocks of 32 keys, which halve the cost of the loop around the
+// products; 96 leaves 12 warps and blocks of 16.
 template <int D_, int NT_>
 struct Kv4Shape {
   static constexpr int D = D_, NT = NT_;
   static constexpr bool kWide = D * NT >= 256;
   static constexpr int W = kWide ? 4 : 8;
   static constexpr int CTAS = kWide ? 3 : 2;
-  static constexpr int S = D == 256 ? 3 : D == 128 ? 4 : 6;
+  static constexpr int SUB = kWide ? 1 : 2;
+  static constexpr int S = D == 256 ? 3 : kWide ? 5 : D == 128 ? 2 : 3;
+  static constexpr int kBlk = 16 * SUB;
   static constexpr int kRows = 8 * NT;
   static constexpr int KC = D == 256 ? 2 : 1;   // chunks of a K row a lane
   static constexpr int KG = D / 8 / KC;         // bytes of such a chunk
@@ -220,8 +193,9 @@ struct Kv4Shape {
   static constexpr int VG = D / 16;             // bytes of a V row a lane
   static constexpr int VW = VG / 4;
   static constexpr int MT = D / 16;             // 16-dimension tiles of O^T
-  // A stage: K, V, K scales, V scales of one block.
-  static constexpr int kVOff = 8 * D, kSOff = 16 * D, kStage = 18 * D;
+  // A part of a stage: K, V, K scales, V scales of 16 keys.
+  static constexpr int kVOff = 8 * D, kSOff = 16 * D, kPart = 18 * D;
+  static constexpr int kStage = SUB * kPart;
   static constexpr int kRing = W * S * kStage;
   // Merge buffer: TPP accumulator tiles of every warp at a time.
   static constexpr int TPP = MT * NT < 8 ? MT * NT : 8;
@@ -233,91 +207,132 @@ struct Kv4Shape {
 template <typename Sh, int NSEG>
 __global__ void __launch_bounds__(Sh::W * 32, Sh::CTAS)
 kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
-  constexpr int D = Sh::D, NT = Sh::NT, W = Sh::W, S = Sh::S, MT = Sh::MT;
+  constexpr int D = Sh::D, NT = Sh::NT, W = Sh::W, S = Sh::S, MT = Sh::MT, SUB = Sh::SUB;
   constexpr int KC = Sh::KC, KG = Sh::KG, KW = Sh::KW, VG = Sh::VG, VW = Sh::VW;
+  constexpr int kBlk = Sh::kBlk;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float wm[W][Sh::kRows], wl[W][Sh::kRows];
   __shared__ int64_t s_row[Sh::kRows];  // offset in `out` of each row of the tile, or -1
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = lane >> 2, c = lane & 3;
-  const int64_t vb = range_start(sc, blockIdx.x), ve = range_start(sc, blockIdx.x + 1);
-  if (vb >= ve) return;
+  const Kv4Start start = sc.cta[blockIdx.x];
+  if (start.len <= 0) return;
+  Place cs{start.tile, start.head, start.j, start.len, sc.tile[start.tile].nb};
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S * Sh::kStage;
   float4* mbuf = reinterpret_cast<float4*>(smem + Sh::kRing);
 
-  // ---- The copies' side: the next block of this warp, its page read one
-  // step ahead of its copies.
-  Seg is = seg_at(sc, p, vb, vb, ve);
-  Seg cs = is;
-  int32_t ij = is.j0 + warp;
-  bool pend = true;
-  int32_t pkey = 0, ppage = 0, pg = 0, pseq = 0;
-  auto look_ahead = [&]() {
-    while (is.v < ve && ij >= is.j1) {
-      seg_next(sc, p, is, vb, ve);
-      ij = is.j0 + warp;
-    }
-    pend = is.v < ve;
-    if (!pend) return;
-    pkey = (is.fb + ij) * kBlk;
-    pg = is.g;
-    pseq = sc.tile[is.e].seq;
-    const int32_t slot = pkey >> p.page_shift;
-    ppage = slot < p.mpps ? __ldg(p.page_table + static_cast<int64_t>(pseq) * p.mpps + slot) : -1;
-    ij += W;
+  // ---- The copies' side.  This warp's blocks of the range, in order, come in
+  // batches of up to 32 of one segment: lane i holds the page ids of the
+  // batch's block i, read a batch ahead of their use.
+  struct Batch {
+    int32_t n, blk;        // blocks; the first one (the others are W apart)
+    int32_t g, seq, lo, hi;  // KV head, sequence, keys the tile sees
+    int32_t page[2];       // (lane) page of the block's first and, where pages are 16 keys, second part
   };
-  uint32_t bad_pages = 0;  // bit st: the block in stage st has no good page
+  Place bs = cs;          // where the next batch comes from
+  int32_t bj = bs.j + warp;
+  auto next_batch = [&](Batch& b) {
+    int32_t j1 = 0;
+    for (;; place_next(sc, p, bs), bj = bs.j + warp) {
+      if (bs.rem <= 0) {
+        b.n = 0;
+        return;
+      }
+      j1 = min(bs.nb, bs.j + bs.rem);
+      if (bj < j1) break;
+    }
+    const Kv4Tile& t = sc.tile[bs.e];
+    b.n = min(32, (j1 - bj + W - 1) / W);
+    b.blk = t.fb + bj;
+    b.g = bs.g;
+    b.seq = t.seq;
+    b.lo = first_visible(t.pos0 + t.r0 / p.group, t.window);
+    b.hi = t.pos0 + (t.r0 + t.nrows - 1) / p.group;
+    b.page[0] = b.page[1] = -1;
+    if (lane < b.n) {
+      const int32_t key = (b.blk + lane * W) * kBlk;
+      const int32_t* row = p.page_table + static_cast<int64_t>(t.seq) * p.mpps;
+      // Parts no row of the tile sees are not looked up (-2).
+#pragma unroll
+      for (int h = 0; h < SUB; ++h) {
+        const int32_t k0 = key + 16 * h;
+        if (h > 0 && p.page_shift > 4) {
+          b.page[h] = b.page[0];
+        } else if (k0 > b.hi || (p.page_shift == 4 && k0 + 15 < b.lo)) {
+          b.page[h] = -2;
+        } else {
+          const int32_t slot = k0 >> p.page_shift;
+          b.page[h] = slot < p.mpps ? __ldg(row + slot) : p.num_pages;
+        }
+      }
+    }
+    bj += 32 * W;
+  };
+  Batch cur, nxt;
+  next_batch(cur);
+  next_batch(nxt);
+  int32_t bi = 0;          // next block of `cur`
+  uint32_t bad_parts = 0;  // bit st * SUB + h: that part has no good page
+  const uint8_t* const k_lane = p.k + g * (D / 2) + c * KG;
+  const uint8_t* const v_lane = p.v + 2 * c * (D / 2) + g * VG;
+  constexpr int H = D / 16;  // 16-byte pieces of 16 keys' K (or V) scales
+  const uint8_t* const s_lane = (lane < H ? p.ks : p.vs) + (lane & (H - 1)) * 16;
   auto issue = [&](int st) {
-    if (pend) {
-      const bool ok = ppage >= 0 && ppage < p.num_pages;
-      if (!ok && lane == 0)
-        report_error(p.ws, (pkey >> p.page_shift) < p.mpps ? RPA_DEVERR_PAGE_ID : RPA_DEVERR_LENGTHS,
-                     pseq);
-      bad_pages = (bad_pages & ~(1u << st)) | (ok ? 0u : 1u << st);
-      // The block's first row in the pool (rows of one head in a page are
-      // contiguous); a bad page's bytes arrive as zeros.
-      const int64_t row = ok ? ((static_cast<int64_t>(ppage) * p.hkv + pg) << p.page_shift) +
-                                   (pkey & ((1 << p.page_shift) - 1))
-                             : 0;
+    if (bi < cur.n) {
+      const int32_t key = (cur.blk + bi * W) * kBlk;
       const uint32_t dst = ring + st * Sh::kStage;
-      const uint8_t* kp = p.k + row * (D / 2);
-      const uint8_t* vp = p.v + row * (D / 2);
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int h = 0; h < SUB; ++h) {
+        const int32_t page = __shfl_sync(0xffffffffu, cur.page[h], bi);
+        const bool ok = page >= 0 && page < p.num_pages;
+        const uint32_t bit = 1u << (st * SUB + h);
+        bad_parts = ok ? bad_parts & ~bit : bad_parts | bit;
+        if (!ok && page != -2 && lane == 0)
+          report_error(p.ws, ((key + 16 * h) >> p.page_shift) < p.mpps ? RPA_DEVERR_PAGE_ID : RPA_DEVERR_LENGTHS,
+                       cur.seq);
+        // The part's first row in the pool (rows of one head in a page are
+        // contiguous); without a page the bytes arrive as zeros.
+        const int64_t row = ok ? ((static_cast<int64_t>(page) * p.hkv + cur.g) << p.page_shift) +
+                                     ((key + 16 * h) & ((1 << p.page_shift) - 1))
+                               : 0;
+        const uint32_t d = dst + h * Sh::kPart;
+        const uint8_t* kp = k_lane + row * (D / 2);
+        const uint8_t* vp = v_lane + row * (D / 2);
 #pragma unroll
-        for (int j = 0; j < KC; ++j)
-          copy_async<KG>(dst + ((r * KC + j) * 32 + lane) * KG, kp + (g + 8 * r) * (D / 2) + (c + 4 * j) * KG,
-                         ok ? KG : 0);
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        copy_async<VG>(dst + Sh::kVOff + (i * 32 + lane) * VG,
-                       vp + (2 * c + (i & 1) + 8 * (i >> 1)) * (D / 2) + g * VG, ok ? VG : 0);
-      if (lane < D / 8) {
-        constexpr int H = D / 16;  // 16-byte pieces of a block's K (or V) scales
-        const uint8_t* src = (lane < H ? p.ks : p.vs) + row * (D / 16) + (lane & (H - 1)) * 16;
-        copy_async<16>(dst + Sh::kSOff + lane * 16, src, ok ? 16 : 0);
+          for (int j = 0; j < KC; ++j)
+            copy_async<KG>(d + ((r * KC + j) * 32 + lane) * KG, kp + r * 8 * (D / 2) + j * 4 * KG, ok ? KG : 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          copy_async<VG>(d + Sh::kVOff + (i * 32 + lane) * VG, vp + ((i & 1) + 8 * (i >> 1)) * (D / 2),
+                         ok ? VG : 0);
+        if (lane < 2 * H) copy_async<16>(d + Sh::kSOff + lane * 16, s_lane + row * (D / 16), ok ? 16 : 0);
+      }
+      if (++bi == cur.n) {
+        cur = nxt;
+        bi = 0;
+        if (cur.n > 0) next_batch(nxt);
       }
     }
     copy_commit();
   };
-  look_ahead();
 #pragma unroll
-  for (int st = 0; st < S; ++st) {
-    issue(st);
-    if (pend) look_ahead();
-  }
+  for (int st = 0; st < S; ++st) issue(st);
 
   int st = 0;
-  for (; cs.v < ve; seg_next(sc, p, cs, vb, ve)) {
-    if (cs.j0 >= cs.j1) continue;  // only the segment's merge charge lies in this range
+  bool first = true;
+  for (; cs.rem > 0; place_next(sc, p, cs), first = false) {
+    const int32_t j1 = min(cs.nb, cs.j + cs.rem);
+    if (cs.j >= j1) continue;  // only the segment's merge charge lies in this range
     const Kv4Tile& tl = sc.tile[cs.e];
     const int G = p.group;
     // ---- The tile's queries as B fragments: lane (g, c) holds row g (+ 8 nt)
     // and the dimensions of its chunks.
     uint32_t qf[KC * KW][NT][4];
     float sc0[NT], sc1[NT];   // logit scales of this lane's columns 2c, 2c + 1
-    int32_t lo0[NT], hi0[NT], lo1[NT], hi1[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int n = g + 8 * nt;
@@ -357,59 +372,61 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
         }
       sc0[nt] = p.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * c);
       sc1[nt] = p.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * c + 4);
-      // Rows past the tile's last share its last row's keys; they are not written.
-      hi0[nt] = tl.pos0 + min(tl.r0 + 8 * nt + 2 * c, tl.r0 + tl.nrows - 1) / G;
-      hi1[nt] = tl.pos0 + min(tl.r0 + 8 * nt + 2 * c + 1, tl.r0 + tl.nrows - 1) / G;
-      lo0[nt] = first_visible(hi0[nt], tl.window);
-      lo1[nt] = first_visible(hi1[nt], tl.window);
     }
-    const int32_t seg_lo = tile_lo(tl, G), seg_hi = tile_hi(tl, G);
+    const int32_t seg_hi = tl.pos0 + (tl.r0 + tl.nrows - 1) / G;
     // Keys every row sees.
     const int32_t all_lo = first_visible(seg_hi, tl.window), all_hi = tl.pos0 + tl.r0 / G;
 
     float o[MT][NT][4];
+    // Columns' reference (a finite stand-in for -inf until the first score)
+    // and this lane's sums.
     float m0[NT], m1[NT], l0[NT], l1[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m0[nt] = m1[nt] = -INFINITY;
+      m0[nt] = m1[nt] = kNoScore;
       l0[nt] = l1[nt] = 0.f;
 #pragma unroll
       for (int t = 0; t < MT; ++t) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.f;
     }
 
-    for (int32_t j = cs.j0 + warp; j < cs.j1; j += W) {
-      const int32_t key0 = (cs.fb + j) * kBlk;
+    for (int32_t j = cs.j + warp; j < j1; j += W) {
       copy_wait<S - 1>();
       __syncwarp();  // the scales are other lanes' copies
       const uint32_t src = ring + st * Sh::kStage;
-      const bool bad = (bad_pages >> st) & 1u;
+      const int32_t key0 = (tl.fb + j) * kBlk;
+      const uint32_t bad = (bad_parts >> (st * SUB)) & ((1u << SUB) - 1);
+      const bool edge = bad != 0 || key0 < all_lo || key0 + kBlk - 1 > all_hi;
       // ---- S^T = K Q^T
-      float x[NT][4];
-      {
-        float acc[2][NT][4];
+      float x[SUB][NT][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+      for (int h = 0; h < SUB; ++h) {
+        const uint32_t part = src + h * Sh::kPart;
+        // One chain of products per part; a block of one part takes two, so
+        // that the products need not wait for one another.
+        constexpr int CH = SUB == 1 ? 2 : 1;
+        float acc[CH][NT][4];
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) acc[i][nt][0] = acc[i][nt][1] = acc[i][nt][2] = acc[i][nt][3] = 0.f;
 #pragma unroll
         for (int jc = 0; jc < KC; ++jc) {
           uint32_t ka[KW], kb[KW];
-          lds<KW>(src + (jc * 32 + lane) * KG, ka);
-          lds<KW>(src + ((KC + jc) * 32 + lane) * KG, kb);
+          lds<KW>(part + (jc * 32 + lane) * KG, ka);
+          lds<KW>(part + ((KC + jc) * 32 + lane) * KG, kb);
           // Scale bytes of the chunk's 16-dimension blocks (two, or one of
           // 64-dimension rows) in rows g and g + 8.
           uint32_t sa, sb;
           if constexpr (KW == 4) {
-            sa = lds_u16(src + Sh::kSOff + g * (D / 16) + (c + 4 * jc) * 2);
-            sb = lds_u16(src + Sh::kSOff + (g + 8) * (D / 16) + (c + 4 * jc) * 2);
+            sa = lds_u16(part + Sh::kSOff + g * (D / 16) + (c + 4 * jc) * 2);
+            sb = lds_u16(part + Sh::kSOff + (g + 8) * (D / 16) + (c + 4 * jc) * 2);
           } else {
-            sa = lds_u8(src + Sh::kSOff + g * (D / 16) + c);
-            sb = lds_u8(src + Sh::kSOff + (g + 8) * (D / 16) + c);
+            sa = lds_u8(part + Sh::kSOff + g * (D / 16) + c);
+            sb = lds_u8(part + Sh::kSOff + (g + 8) * (D / 16) + c);
           }
 #pragma unroll
           for (int w = 0; w < KW; ++w) {
-            const uint32_t ha = kv4::scale_pair((sa >> (8 * (w >> 1))) & 255u, (sa >> (8 * (w >> 1))) & 255u);
-            const uint32_t hb = kv4::scale_pair((sb >> (8 * (w >> 1))) & 255u, (sb >> (8 * (w >> 1))) & 255u);
+            const uint32_t ha = scale_dup(sa, w >> 1), hb = scale_dup(sb, w >> 1);
             uint32_t a[4], b[4];
             kv4::decode8(ka[w], a);
             kv4::decode8(kb[w], b);
@@ -421,51 +438,97 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma_f16(acc[0][nt], a[0], b[0], a[1], b[1], qf[jc * KW + w][nt][0], qf[jc * KW + w][nt][1]);
-              mma_f16(acc[1][nt], a[2], b[2], a[3], b[3], qf[jc * KW + w][nt][2], qf[jc * KW + w][nt][3]);
+              mma_f16(acc[CH - 1][nt], a[2], b[2], a[3], b[3], qf[jc * KW + w][nt][2], qf[jc * KW + w][nt][3]);
             }
           }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          x[nt][0] = (acc[0][nt][0] + acc[1][nt][0]) * sc0[nt];
-          x[nt][1] = (acc[0][nt][1] + acc[1][nt][1]) * sc1[nt];
-          x[nt][2] = (acc[0][nt][2] + acc[1][nt][2]) * sc0[nt];
-          x[nt][3] = (acc[0][nt][3] + acc[1][nt][3]) * sc1[nt];
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[h][nt][i] = CH == 2 ? acc[0][nt][i] + acc[CH - 1][nt][i] : acc[0][nt][i];
       }
-      // ---- Mask (blocks at a row's edges, or without a page)
-      const bool edge = bad || key0 < all_lo || key0 + kBlk - 1 > all_hi;
-      if (edge) {
+      // ---- Online softmax: exponents against the columns' references; where
+      // one passes 8, the references are raised first.
+      float y[SUB][NT][4];
+      auto exponents = [&]() {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int32_t ka = key0 + g, kb = key0 + g + 8;
-          if (bad || ka < lo0[nt] || ka > hi0[nt]) x[nt][0] = -INFINITY;
-          if (bad || ka < lo1[nt] || ka > hi1[nt]) x[nt][1] = -INFINITY;
-          if (bad || kb < lo0[nt] || kb > hi0[nt]) x[nt][2] = -INFINITY;
-          if (bad || kb < lo1[nt] || kb > hi1[nt]) x[nt][3] = -INFINITY;
+        for (int h = 0; h < SUB; ++h)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            y[h][nt][0] = fmaf(x[h][nt][0], sc0[nt], -m0[nt]);
+            y[h][nt][1] = fmaf(x[h][nt][1], sc1[nt], -m1[nt]);
+            y[h][nt][2] = fmaf(x[h][nt][2], sc0[nt], -m0[nt]);
+            y[h][nt][3] = fmaf(x[h][nt][3], sc1[nt], -m1[nt]);
+          }
+        if (edge) {
+          // Blocks at a row's edges, or without a page.  Rows past the tile's
+          // last take its last row's keys; they are not written.
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int32_t last = tl.r0 + tl.nrows - 1, n = tl.r0 + 8 * nt + 2 * c;
+            const int32_t hi0 = tl.pos0 + min(n, last) / G, hi1 = tl.pos0 + min(n + 1, last) / G;
+            const int32_t lo0 = first_visible(hi0, tl.window), lo1 = first_visible(hi1, tl.window);
+#pragma unroll
+            for (int h = 0; h < SUB; ++h) {
+              const int32_t ka = key0 + 16 * h + g, kb = ka + 8;
+              const bool no = (bad >> h) & 1u;
+              if (no || ka < lo0 || ka > hi0) y[h][nt][0] = -INFINITY;
+              if (no || ka < lo1 || ka > hi1) y[h][nt][1] = -INFINITY;
+              if (no || kb < lo0 || kb > hi0) y[h][nt][2] = -INFINITY;
+              if (no || kb < lo1 || kb > hi1) y[h][nt][3] = -INFINITY;
+            }
+          }
         }
-      }
-      // ---- Online softmax
-      uint32_t pb[NT][2];
-      bool grow = false;
+      };
+      exponents();
+      float top = -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        grow |= fmaxf(x[nt][0], x[nt][2]) > m0[nt] + 8.f || fmaxf(x[nt][1], x[nt][3]) > m1[nt] + 8.f;
-      if (__any_sync(0xffffffffu, grow)) {
+      for (int h = 0; h < SUB; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          top = fmaxf(fmaxf(top, fmaxf(y[h][nt][0], y[h][nt][1])), fmaxf(y[h][nt][2], y[h][nt][3]));
+      if (__any_sync(0xffffffffu, top > 8.f)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float t0 = fmaxf(x[nt][0], x[nt][2]), t1 = fmaxf(x[nt][1], x[nt][3]);
+          // The columns' largest exponents, relative to the references.
+          float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < SUB; ++h) {
+            t0 = fmaxf(t0, fmaxf(y[h][nt][0], y[h][nt][2]));
+            t1 = fmaxf(t1, fmaxf(y[h][nt][1], y[h][nt][3]));
+          }
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) {
             t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
             t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
           }
-          t0 = fmaxf(t0, m0[nt]);
-          t1 = fmaxf(t1, m1[nt]);
-          const float f0 = t0 == -INFINITY ? 1.f : fast_exp2(m0[nt] - t0);
-          const float f1 = t1 == -INFINITY ? 1.f : fast_exp2(m1[nt] - t1);
-          m0[nt] = t0;
-          m1[nt] = t1;
+          // Raised from the stand-in, the reference is the score itself (the
+          // difference to the stand-in has lost its low bits).
+          const bool new0 = m0[nt] == kNoScore, new1 = m1[nt] == kNoScore;
+          t0 = fmaxf(t0, 0.f);
+          t1 = fmaxf(t1, 0.f);
+          float n0 = m0[nt] + t0, n1 = m1[nt] + t1;
+          if (new0 || new1) {
+            float s0 = -INFINITY, s1 = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < SUB; ++h) {
+              if (y[h][nt][0] > -INFINITY) s0 = fmaxf(s0, x[h][nt][0] * sc0[nt]);
+              if (y[h][nt][2] > -INFINITY) s0 = fmaxf(s0, x[h][nt][2] * sc0[nt]);
+              if (y[h][nt][1] > -INFINITY) s1 = fmaxf(s1, x[h][nt][1] * sc1[nt]);
+              if (y[h][nt][3] > -INFINITY) s1 = fmaxf(s1, x[h][nt][3] * sc1[nt]);
+            }
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+              s0 = fmaxf(s0, __shfl_xor_sync(0xffffffffu, s0, off));
+              s1 = fmaxf(s1, __shfl_xor_sync(0xffffffffu, s1, off));
+            }
+            if (new0) n0 = s0 == -INFINITY ? kNoScore : s0;
+            if (new1) n1 = s1 == -INFINITY ? kNoScore : s1;
+          }
+          const float f0 = new0 ? 1.f : fast_exp2(m0[nt] - n0), f1 = new1 ? 1.f : fast_exp2(m1[nt] - n1);
+          m0[nt] = n0;
+          m1[nt] = n1;
           l0[nt] *= f0;
           l1[nt] *= f1;
 #pragma unroll
@@ -476,40 +539,48 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
             o[t][nt][3] *= f1;
           }
         }
+        exponents();
       }
+      uint32_t pb[SUB][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float r0 = m0[nt] == -INFINITY ? 0.f : m0[nt], r1 = m1[nt] == -INFINITY ? 0.f : m1[nt];
-        const float p0 = fast_exp2(x[nt][0] - r0), p1 = fast_exp2(x[nt][1] - r1);
-        const float p2 = fast_exp2(x[nt][2] - r0), p3 = fast_exp2(x[nt][3] - r1);
-        l0[nt] += p0 + p2;
-        l1[nt] += p1 + p3;
-        pb[nt][0] = transpose8x8(pack_f16x2(p0, p1));
-        pb[nt][1] = transpose8x8(pack_f16x2(p2, p3));
-      }
+      for (int h = 0; h < SUB; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float p0 = fast_exp2(y[h][nt][0]), p1 = fast_exp2(y[h][nt][1]);
+          const float p2 = fast_exp2(y[h][nt][2]), p3 = fast_exp2(y[h][nt][3]);
+          l0[nt] += p0 + p2;
+          l1[nt] += p1 + p3;
+          pb[h][nt][0] = transpose8x8(pack_f16x2(p0, p1));
+          pb[h][nt][1] = transpose8x8(pack_f16x2(p2, p3));
+        }
       // ---- O^T += V^T P^T
-      {
+#pragma unroll
+      for (int h = 0; h < SUB; ++h) {
+        const uint32_t part = src + h * Sh::kPart;
         uint32_t vw[4][VW];
         uint32_t sv[4];  // scale bytes of this lane's dimensions in its four keys
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int kk = 2 * c + (i & 1) + 8 * (i >> 1);
-          lds<VW>(src + Sh::kVOff + (i * 32 + lane) * VG, vw[i]);
+          lds<VW>(part + Sh::kVOff + (i * 32 + lane) * VG, vw[i]);
           if constexpr (D == 256)
-            sv[i] = lds_u16(src + Sh::kSOff + D + kk * (D / 16) + 2 * g);
+            sv[i] = lds_u16(part + Sh::kSOff + D + kk * (D / 16) + 2 * g);
           else
-            sv[i] = lds_u8(src + Sh::kSOff + D + kk * (D / 16) + (D == 128 ? g : g >> 1));
-          // Keys no row sees: whatever their bytes, their values are zeros.
-          if (edge && (bad || key0 + kk < seg_lo || key0 + kk > seg_hi)) sv[i] = 0;
+            sv[i] = lds_u8(part + Sh::kSOff + D + kk * (D / 16) + (D == 128 ? g : g >> 1));
         }
-        uint32_t s01 = kv4::scale_pair(sv[0] & 255u, sv[1] & 255u);
-        uint32_t s23 = kv4::scale_pair(sv[2] & 255u, sv[3] & 255u);
+        if (edge) {
+          // Keys no row sees: whatever their bytes, their values are zeros.
+          const int32_t seg_lo = first_visible(all_hi, tl.window);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int32_t key = key0 + 16 * h + 2 * c + (i & 1) + 8 * (i >> 1);
+            if (((bad >> h) & 1u) || key < seg_lo || key > seg_hi) sv[i] = 0;
+          }
+        }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
-          if (D == 256 && w == 2) {
-            s01 = kv4::scale_pair(sv[0] >> 8, sv[1] >> 8);
-            s23 = kv4::scale_pair(sv[2] >> 8, sv[3] >> 8);
-          }
+          const uint32_t s01 = scale_pair_of(sv[0], sv[1], D == 256 ? w >> 1 : 0);
+          const uint32_t s23 = scale_pair_of(sv[2], sv[3], D == 256 ? w >> 1 : 0);
           constexpr uint32_t kLow = 0x0f0f0f0fu;
           uint32_t e01[4], d01[4], e23[4], d23[4];  // even and odd dimensions, key pairs
           kv4::decode8(bit_select(kLow, vw[0][w], vw[1][w] << 4), e01);
@@ -522,13 +593,12 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
             const uint32_t a2 = kv4::hmul2(e23[t], s23), a3 = kv4::hmul2(d23[t], s23);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_f16(o[4 * w + t][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+              mma_f16(o[4 * w + t][nt], a0, a1, a2, a3, pb[h][nt][0], pb[h][nt][1]);
           }
         }
       }
       __syncwarp();  // every lane has read the scales: the stage may be refilled
       issue(st);
-      if (pend) look_ahead();
       if (++st == S) st = 0;
     }
 
@@ -549,22 +619,21 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
       }
     }
     __syncthreads();
-    const bool whole = cs.j0 == 0 && cs.j1 == cs.nb;
-    const int slot = 2 * blockIdx.x + (vb < cs.v ? 1 : 0);
+    const bool whole = cs.j == 0 && j1 == cs.nb;
+    const int slot = 2 * blockIdx.x + (first ? 0 : 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float f[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int n = 8 * nt + 2 * c + h;
-        float M = -INFINITY, L = 0.f;
+        float M = kNoScore, L = 0.f;
 #pragma unroll
         for (int w = 0; w < W; ++w) M = fmaxf(M, wm[w][n]);
+        // (A warp without a score has l = 0, or NaN, which stays.)
 #pragma unroll
-        for (int w = 0; w < W; ++w)
-          L += wl[w][n] * (M == -INFINITY ? 1.f : fast_exp2(wm[w][n] - M));
-        const float mine = h ? m1[nt] : m0[nt];
-        f[h] = L == 0.f ? 0.f : (M == -INFINITY ? 1.f : fast_exp2(mine - M)) / L;
+        for (int w = 0; w < W; ++w) L += wl[w][n] * fast_exp2(wm[w][n] - M);
+        f[h] = L == 0.f ? 0.f : fast_exp2((h ? m1[nt] : m0[nt]) - M) / L;
         if (!whole && warp == 0 && g == 0)
           p.part_lse[static_cast<int64_t>(slot) * Sh::kRows + n] = L == 0.f ? -INFINITY : M + __log2f(L);
       }
@@ -623,21 +692,22 @@ __global__ void __launch_bounds__(256)
 kv4_combine_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
   constexpr int E = D / 32;
   const int b = blockIdx.x + 1;
-  const int64_t x = range_start(sc, b);
-  const Seg s = seg_at(sc, p, x, 0, sc.v0[sc.n]);
-  const int64_t end = s.v + s.nb;
-  // This boundary lies inside the segment, and the one before it does not.
-  const bool mine = x > s.v && x < end && range_start(sc, b - 1) <= s.v;
+  const Kv4Start s = sc.cta[b], before = sc.cta[b - 1];
+  const Kv4Tile& tl = sc.tile[s.tile];
+  const bool same = before.tile == s.tile && before.head == s.head;
+  const bool mine = s.j > 0 && s.j < tl.nb && !(same && before.j > 0);
+  int parts = 2;
+  if (mine)
+    while (b - 1 + parts <= static_cast<int>(gridDim.x) && sc.cta[b - 1 + parts].tile == s.tile &&
+           sc.cta[b - 1 + parts].head == s.head && sc.cta[b - 1 + parts].j < tl.nb)
+      ++parts;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!mine) return;
-  int parts = 2;
-  while (range_start(sc, b - 1 + parts) < end) ++parts;
-  const Kv4Tile& tl = sc.tile[s.e];
   const int lane = threadIdx.x & 31;
   for (int n = threadIdx.x >> 5; n < tl.nrows; n += 8) {
+    // The first part is its CTA's first segment only if the range starts with it.
     auto slot = [&](int k) {
-      const int cta = b - 1 + k;
-      return static_cast<int64_t>(2 * cta + (k == 0 && range_start(sc, cta) < s.v ? 1 : 0)) * ROWS + n;
+      return static_cast<int64_t>(2 * (b - 1 + k) + (k == 0 && !same ? 1 : 0)) * ROWS + n;
     };
     float M = -INFINITY;
     for (int k = lane; k < parts; k += 32) M = fmaxf(M, p.part_lse[slot(k)]);
@@ -668,7 +738,7 @@ kv4_combine_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc)
     const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
     const int r = tl.r0 + n;
     __nv_bfloat16* dst = p.out +
-        (static_cast<int64_t>(tl.q0 + r / p.group) * p.hq + s.g * p.group + r % p.group) * D + lane * E;
+        (static_cast<int64_t>(tl.q0 + r / p.group) * p.hq + s.head * p.group + r % p.group) * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
       *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
@@ -681,13 +751,13 @@ int launch_t(const Plan& plan, const Kv4Params& p, const Plan::Kv4Launch& l, cud
   auto* kernel = kv4_decode_kernel<Sh, NSEG>;
   if (int e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), Sh::kBytes)) return e;
   Kv4Sched<NSEG>& sc = thread_staging<Kv4Sched<NSEG>>();  // copied into the launch parameters
-  sc.n = l.end - l.begin;
-  sc.n_ctas = l.n_ctas;
-  sc.v0[0] = 0;
-  for (int i = 0; i < sc.n; ++i) {
-    const Plan::Kv4Tile& t = plan.kv4_tiles[l.begin + i];
-    sc.tile[i] = Kv4Tile{t.seq, t.q0, t.r0, t.nrows, t.pos0, t.window};
-    sc.v0[i + 1] = sc.v0[i] + static_cast<int64_t>(t.nb + kKv4SegCost) * plan.hkv;
+  for (int i = l.begin; i < l.end; ++i) {
+    const Plan::Kv4Tile& t = plan.kv4_tiles[i];
+    sc.tile[i - l.begin] = Kv4Tile{t.seq, t.q0, t.r0, t.nrows, t.pos0, t.window, t.fb, t.nb};
+  }
+  for (int i = 0; i < l.n_ctas; ++i) {
+    const Plan::Kv4Start& c = plan.kv4_starts[l.cta_begin + i];
+    sc.cta[i] = Kv4Start{c.tile, c.head, c.j, c.len};
   }
   kernel<<<l.n_ctas, Sh::W * 32, Sh::kBytes, stream>>>(p, sc);
   cudaError_t e = cudaGetLastError();
@@ -718,11 +788,11 @@ int launch_n(const Plan& plan, const Kv4Params& p, const Plan::Kv4Launch& l, cud
 
 }  // namespace
 
-int kv4_ctas_per_sm(int32_t head_dim, int32_t nt) {
-  return head_dim * nt >= 256 ? Kv4Shape<256, 1>::CTAS : Kv4Shape<128, 1>::CTAS;
-}
-int kv4_warps(int32_t head_dim, int32_t nt) {
-  return head_dim * nt >= 256 ? Kv4Shape<256, 1>::W : Kv4Shape<128, 1>::W;
+Kv4Grain kv4_grain(int32_t head_dim, int32_t nt) {
+  using Narrow = Kv4Shape<128, 1>;
+  using Wide = Kv4Shape<256, 1>;
+  return head_dim * nt >= 256 ? Kv4Grain{Wide::CTAS, Wide::W, Wide::kBlk}
+                              : Kv4Grain{Narrow::CTAS, Narrow::W, Narrow::kBlk};
 }
 
 int launch_kv4_decode(const Plan& plan, const Args& a, void* stream) {

@@ -569,9 +569,10 @@ constexpr int32_t kKv4MaxRows = 32;
 constexpr int32_t kKv4BlocksPerWarp = 2;
 
 // Row tiles, launches and CTA counts of the split-KV part.
-void plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_t* win) {
+rpa_status_t plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_t* win) {
   const int32_t group = plan.hq / plan.hkv;
   for (int32_t nt = 1; nt <= 2; ++nt) {
+    const Kv4Grain grain = kv4_grain(plan.d, nt);
     const int32_t first = static_cast<int32_t>(plan.kv4_tiles.size());
     for (int32_t s = 0; s < plan.num_seqs; ++s) {
       const int32_t ql = cu[s + 1] - cu[s];
@@ -588,7 +589,8 @@ void plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, const int
         const int32_t n = std::min(8 * nt, rows - r0);
         const int32_t p0 = pos0 + r0 / group, p1 = pos0 + (r0 + n - 1) / group;
         const int32_t lo = (w > 0 && p0 - (w - 1) > 0) ? p0 - (w - 1) : 0;
-        plan.kv4_tiles.push_back({s, cu[s], r0, n, pos0, w, p1 / 16 - lo / 16 + 1});
+        const int32_t fb = lo / grain.block_keys;
+        plan.kv4_tiles.push_back({s, cu[s], r0, n, pos0, w, fb, p1 / grain.block_keys - fb + 1});
       }
     }
     const int32_t last = static_cast<int32_t>(plan.kv4_tiles.size());
@@ -598,31 +600,36 @@ void plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, const int
       for (int32_t i = b; i < e; ++i)
         v0.push_back(v0.back() + static_cast<int64_t>(plan.kv4_tiles[i].nb + kKv4SegCost) * plan.hkv);
       const int64_t total = v0.back();
-      const int64_t most = static_cast<int64_t>(plan.num_sms) * kv4_ctas_per_sm(plan.d, nt);
-      const int64_t n = std::max<int64_t>(1, std::min(most, total / (kKv4BlocksPerWarp * kv4_warps(plan.d, nt))));
-      Plan::Kv4Launch l{b, e, nt, static_cast<int32_t>(n), false};
-      // The boundaries between ranges that fall inside a segment cut it.
+      const int64_t most = std::min<int64_t>(static_cast<int64_t>(plan.num_sms) * grain.ctas_per_sm, kKv4MaxCtas);
+      const int64_t n = std::max<int64_t>(
+          std::max<int64_t>(1, std::min(most, total / (kKv4BlocksPerWarp * grain.warps))),
+          std::min(most, ceil_div(total, 0x3fffffff)));
+      if (ceil_div(total, n) > 0x7fffffff) return RPA_ERR_UNSUPPORTED;
+      Plan::Kv4Launch l{b, e, nt, static_cast<int32_t>(plan.kv4_starts.size()), static_cast<int32_t>(n), false};
+      // Equal ranges of the line; the boundaries that fall inside a segment cut it.
       int64_t seg = -1, parts = 1;
-      for (int64_t c = 1; c < n; ++c) {
-        const int64_t x = total * c / n;
+      for (int64_t c = 0; c < n; ++c) {
+        const int64_t x = total * c / n, end = total * (c + 1) / n;
         const size_t i = static_cast<size_t>(std::upper_bound(v0.begin(), v0.end(), x) - v0.begin()) - 1;
         const int32_t nb = plan.kv4_tiles[b + static_cast<int32_t>(i)].nb;
         const int64_t cost = nb + kKv4SegCost, off = (x - v0[i]) % cost;
+        plan.kv4_starts.push_back({static_cast<int32_t>(i), static_cast<int32_t>((x - v0[i]) / cost),
+                                   static_cast<int32_t>(off), static_cast<int32_t>(end - x)});
         if (off == 0 || off >= nb) continue;
         l.cut = true;
-        const int64_t id = x - off;
-        parts = id == seg ? parts + 1 : 2;
-        seg = id;
+        parts = x - off == seg ? parts + 1 : 2;
+        seg = x - off;
         plan.max_splits = std::max(plan.max_splits, static_cast<int32_t>(parts));
       }
       if (plan.kv_split == 0)
-        plan.kv_split = static_cast<int32_t>(std::min<int64_t>(ceil_div(total, n) * 16, 0x7fffffff));
+        plan.kv_split = static_cast<int32_t>(std::min<int64_t>(ceil_div(total, n) * grain.block_keys, 0x7fffffff));
       plan.max_splits = std::max(plan.max_splits, 1);
       plan.decode_ctas += n;
       plan.kv4_part_rows = std::max(plan.kv4_part_rows, 2 * n * nt * 8);
       plan.kv4_launches.push_back(l);
     }
   }
+  return RPA_OK;
 }
 
 rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu, const int32_t* kv,
@@ -637,7 +644,7 @@ rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu, const int32_t* kv
   plan.path = RPA_PATH_TC;
   plan.prefill_min_q = kKv4MaxRows / group + 1;
   plan.num_decode = plan.num_prefill = 0;
-  plan_kv4_decode(plan, cu, kv, win);
+  if (rpa_status_t st = plan_kv4_decode(plan, cu, kv, win)) return st;
   size_t off = kHeaderBytes;
   auto take = [&](size_t bytes) {
     const size_t at = off;

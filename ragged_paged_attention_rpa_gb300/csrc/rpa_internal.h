@@ -90,10 +90,12 @@ constexpr int kMaxDecodeGrid = 512;
 constexpr int kDecodeSegCost = 7;
 
 // Split-KV attention over 4-bit pages (kv4_decode.cu): row tiles one launch
-// carries in its parameters (two sizes), and the charge, in 16-key blocks, for
-// each segment (its merge and output).
-constexpr int kKv4TilesSmall = 120;
-constexpr int kKv4TilesLarge = 992;
+// carries in its parameters (two sizes), CTAs of its grid (whose starts travel
+// there too), and the charge, in key blocks, for each segment (its merge and
+// output).
+constexpr int kKv4TilesSmall = 160;
+constexpr int kKv4TilesLarge = 736;
+constexpr int kKv4MaxCtas = 512;
 constexpr int kKv4SegCost = 8;
 // Sequences whose 4-bit pages one expansion launch lists.
 constexpr int kKv4ExpandSeqs = 1024;
@@ -157,12 +159,17 @@ struct Plan {
   // blocks); the others' visible pages are widened to bf16 in the workspace
   // (kv4_expand.cu) and run as prefill work.
   struct Kv4Tile {
-    int32_t seq, q0, r0, nrows, pos0, window, nb;
+    int32_t seq, q0, r0, nrows, pos0, window, fb, nb;
+  };
+  // A CTA's range of the line of segments: from block j of (tile, head) on,
+  // len blocks and merge charges.  Tiles relative to the launch.
+  struct Kv4Start {
+    int32_t tile, head, j, len;
   };
   struct Kv4Launch {
     int32_t begin, end;  // tiles [begin, end)
     int32_t nt;          // rows a tile: 8 nt
-    int32_t n_ctas;
+    int32_t cta_begin, n_ctas;  // kv4_starts[cta_begin ...]
     bool cut;            // some segment is cut across CTAs
   };
   // A sequence's pages from table slot `slot0` on, widened to scratch pages
@@ -171,6 +178,7 @@ struct Plan {
     int32_t seq, slot0, page0, lo, hi;
   };
   std::vector<Kv4Tile> kv4_tiles;
+  std::vector<Kv4Start> kv4_starts;
   std::vector<Kv4Launch> kv4_launches;
   std::vector<Kv4Expand> kv4_expand;
   int64_t kv4_part_rows = 0;      // rows of the split-KV partials (two tiles a CTA)
@@ -272,12 +280,14 @@ bool prologue_supported(int32_t head_dim);
 int launch_prologue(const PrologueArgs& a, void* stream);
 
 // Attention over 4-bit pages: the split-KV kernel over the plan's row tiles
-// (kv4_decode.cu), its CTAs per SM and warps per CTA, and the widening of the
+// (kv4_decode.cu), its grain for row tiles of 8 nt rows, and the widening of the
 // prefill sequences' visible pages into the workspace, with a page table of
 // their own (kv4_expand.cu).
 int launch_kv4_decode(const Plan& plan, const Args& a, void* stream);
-int kv4_ctas_per_sm(int32_t head_dim, int32_t nt);
-int kv4_warps(int32_t head_dim, int32_t nt);
+struct Kv4Grain {
+  int32_t ctas_per_sm, warps, block_keys;
+};
+Kv4Grain kv4_grain(int32_t head_dim, int32_t nt);
 int launch_kv4_expand(const Plan& plan, const Args& a, void* stream);
 
 // The 4-bit cache's write and read (kv4_cache.cu).
