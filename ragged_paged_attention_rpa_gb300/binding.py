@@ -410,33 +410,72 @@ def rpa_forward_decode_noalloc(q, k_pages, v_pages, page_table, cu_q_lens, kv_le
         raise RpaError(st, "rpa_forward_decode_noalloc")
 
 
-def _kv4_pools(k_pages, v_pages, k_scales, v_scales):
-    """Pointers and (num_pages, Hkv, page_size, head_dim) of 4-bit pools."""
+def _current(stream):
+    """The current device's index and the stream's handle (None: its current
+    stream)."""
     import torch
-    if k_pages.dim() != 4:
+    dev = torch._C._cuda_getDevice()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, stream.cuda_stream
+
+
+def _addr(t, name, dtype, dev):
+    """The address of a contiguous tensor of `dtype` on device `dev` (four
+    attribute reads; what is wrong is found out only where something is)."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dptr(t, name, dtype)
+    if t is None:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    raise ValueError("%s is on device %s, the current one is %d" % (name, t.device, dev))
+
+
+def _workspace(workspace, dev, least=256):
+    """Address and size in bytes of a workspace tensor of any dtype."""
+    n = workspace.nbytes
+    if n < least:
+        raise ValueError("workspace must hold at least %d bytes" % least)
+    return _addr(workspace, "workspace", workspace.dtype, dev), n
+
+
+def _kv4_pools(k_pages, v_pages, k_scales, v_scales, dev):
+    """Addresses and (num_pages, Hkv, page_size, head_dim) of 4-bit pools."""
+    import torch
+    u8 = torch.uint8
+    shape = k_pages.shape
+    if len(shape) != 4:
         raise ValueError("k_pages must be [num_pages, num_kv_heads, page_size, head_dim / 2]")
-    n, hkv, p, half = (int(x) for x in k_pages.shape)
-    for t, name, last in ((v_pages, "v_pages", half), (k_scales, "k_scales", half // 8),
-                          (v_scales, "v_scales", half // 8)):
-        if tuple(t.shape) != (n, hkv, p, last):
-            raise ValueError("%s must have shape %s, got %s" % (name, (n, hkv, p, last),
-                                                                tuple(t.shape)))
-    ptrs = [_dptr(t, name, torch.uint8) for t, name in
-            ((k_pages, "k_pages"), (v_pages, "v_pages"), (k_scales, "k_scales"),
-             (v_scales, "v_scales"))]
-    return ptrs, (n, hkv, p, 2 * half)
+    n, hkv, p, half = shape
+    want = (n, hkv, p, half // 8)
+    if v_pages.shape != shape or k_scales.shape != want or v_scales.shape != want:
+        for t, name, w in ((v_pages, "v_pages", tuple(shape)), (k_scales, "k_scales", want),
+                           (v_scales, "v_scales", want)):
+            if tuple(t.shape) != w:
+                raise ValueError("%s must have shape %s, got %s" % (name, w, tuple(t.shape)))
+    return (_addr(k_pages, "k_pages", u8, dev), _addr(v_pages, "v_pages", u8, dev),
+            _addr(k_scales, "k_scales", u8, dev), _addr(v_scales, "v_scales", u8, dev),
+            n, hkv, p, 2 * half)
 
 
-def _kv4_rows(k, v, names, slot_map, shape):
+def _kv4_rows(k, v, k_name, v_name, tokens, hkv, d, dev):
+    """Addresses and dtype code of the rows a cache call reads or writes."""
     import torch
-    _, hkv, _, d = shape
-    if k.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError("%s must be bfloat16 or float32, got %s" % (names[0], k.dtype))
-    want = (int(slot_map.numel()), hkv, d)
-    for t, name in ((k, names[0]), (v, names[1])):
-        if tuple(t.shape) != want:
-            raise ValueError("%s must have shape %s, got %s" % (name, want, tuple(t.shape)))
-    return RPA_DTYPE_BF16 if k.dtype == torch.bfloat16 else RPA_DTYPE_F32
+    dt = k.dtype
+    if dt is torch.bfloat16:
+        code = RPA_DTYPE_BF16
+    elif dt is torch.float32:
+        code = RPA_DTYPE_F32
+    else:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (k_name, dt))
+    want = (tokens, hkv, d)
+    if k.shape != want or v.shape != want:
+        raise ValueError("%s and %s must have shape %s, got %s and %s"
+                         % (k_name, v_name, want, tuple(k.shape), tuple(v.shape)))
+    return _addr(k, k_name, dt, dev), _addr(v, v_name, dt, dev), code
 
 
 def rpa_write_kv4(k_new, v_new, k_pages, v_pages, k_scales, v_scales, slot_map, workspace=None,
@@ -445,15 +484,15 @@ def rpa_write_kv4(k_new, v_new, k_pages, v_pages, k_scales, v_scales, slot_map, 
     float32) into 4-bit pages (uint8: pages [N, Hkv, P, D/2], scales
     [N, Hkv, P, D/16]) at the slots of slot_map ([total_q] int64, < 0: left out)."""
     import torch
-    pools, shape = _kv4_pools(k_pages, v_pages, k_scales, v_scales)
-    dtype = _kv4_rows(k_new, v_new, ("k_new", "v_new"), slot_map, shape)
-    n, hkv, p, d = shape
-    st = lib().rpa_write_kv4(
-        _dptr(k_new, "k_new"), _dptr(v_new, "v_new", k_new.dtype), *pools,
-        _dptr(slot_map, "slot_map", torch.int64), int(slot_map.numel()), hkv, d, p, n, dtype,
-        _dptr(workspace, "workspace"), _stream_ptr(stream))
-    if st != RPA_OK:
-        raise RpaError(st, "rpa_write_kv4")
+    dev, st = _current(stream)
+    kp, vp, ks, vs, n, hkv, p, d = _kv4_pools(k_pages, v_pages, k_scales, v_scales, dev)
+    t = slot_map.numel()
+    k, v, dtype = _kv4_rows(k_new, v_new, "k_new", "v_new", t, hkv, d, dev)
+    rc = lib().rpa_write_kv4(k, v, kp, vp, ks, vs, _addr(slot_map, "slot_map", torch.int64, dev),
+                             t, hkv, d, p, n, dtype,
+                             None if workspace is None else _workspace(workspace, dev)[0], st)
+    if rc != RPA_OK:
+        raise RpaError(rc, "rpa_write_kv4")
 
 
 def rpa_read_kv4(k_pages, v_pages, k_scales, v_scales, slot_map, k_out, v_out, workspace=None,
@@ -461,41 +500,57 @@ def rpa_read_kv4(k_pages, v_pages, k_scales, v_scales, slot_map, k_out, v_out, w
     """rpa_read_kv4 on torch CUDA tensors: the rows at slot_map's slots as
     values, to k_out and v_out [total_q, Hkv, D] (bf16 or float32)."""
     import torch
-    pools, shape = _kv4_pools(k_pages, v_pages, k_scales, v_scales)
-    dtype = _kv4_rows(k_out, v_out, ("k_out", "v_out"), slot_map, shape)
-    n, hkv, p, d = shape
-    st = lib().rpa_read_kv4(
-        *pools, _dptr(slot_map, "slot_map", torch.int64), _dptr(k_out, "k_out"),
-        _dptr(v_out, "v_out", k_out.dtype), int(slot_map.numel()), hkv, d, p, n, dtype,
-        _dptr(workspace, "workspace"), _stream_ptr(stream))
-    if st != RPA_OK:
-        raise RpaError(st, "rpa_read_kv4")
+    dev, st = _current(stream)
+    kp, vp, ks, vs, n, hkv, p, d = _kv4_pools(k_pages, v_pages, k_scales, v_scales, dev)
+    t = slot_map.numel()
+    k, v, dtype = _kv4_rows(k_out, v_out, "k_out", "v_out", t, hkv, d, dev)
+    rc = lib().rpa_read_kv4(kp, vp, ks, vs, _addr(slot_map, "slot_map", torch.int64, dev), k, v,
+                            t, hkv, d, p, n, dtype,
+                            None if workspace is None else _workspace(workspace, dev)[0], st)
+    if rc != RPA_OK:
+        raise RpaError(rc, "rpa_read_kv4")
+
+
+def _kv4_args(q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv_lens, window,
+              sm_scale, out, plan, workspace, stream):
+    """The marshalled arguments of rpa_forward_kv4."""
+    import torch
+    m = plan.meta
+    dev, st = _current(stream)
+    i32, bf16 = torch.int32, torch.bfloat16
+    kp, vp, ks, vs, _, hkv, p, d = _kv4_pools(k_pages, v_pages, k_scales, v_scales, dev)
+    s, hq = m["num_seqs"], m["num_q_heads"]
+    if hkv != m["num_kv_heads"] or p != m["page_size"] or d != m["head_dim"]:
+        raise ValueError("the pools' shape differs from the plan's")
+    ws, n = _workspace(workspace, dev)
+    return (_addr(q, "q", bf16, dev), kp, vp, ks, vs, _addr(page_table, "page_table", i32, dev),
+            _addr(cu_q_lens, "cu_q_lens", i32, dev), _addr(kv_lens, "kv_lens", i32, dev),
+            s, hq, hkv, d, p, None if window is None else _addr(window, "window", i32, dev),
+            float(sm_scale), _addr(out, "out", bf16, dev), st, plan.handle, ws, n)
 
 
 def rpa_forward_kv4(q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv_lens,
                     window, sm_scale: float, out, plan: Plan, workspace, stream=None) -> None:
     """rpa_forward_kv4: attention over 4-bit pages (uint8 tensors; a plan with
     kv_dtype=RPA_DTYPE_FP4_E2M1)."""
-    ForwardKv4Call(q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv_lens,
-                   window, sm_scale, out, plan, workspace, stream)()
+    rc = lib().rpa_forward_kv4(*_kv4_args(q, k_pages, v_pages, k_scales, v_scales, page_table,
+                                          cu_q_lens, kv_lens, window, sm_scale, out, plan,
+                                          workspace, stream))
+    if rc != RPA_OK:
+        raise RpaError(rc, "rpa_forward_kv4")
 
 
-def _tables_args(page_table, kv_lens_prev, kv_lens, free_pages, free_count_prev, free_count):
-    import torch
-    if page_table.dim() != 2:
+def _tables_state(page_table, lens, kv_lens_prev, kv_lens, free_count_prev, free_count):
+    """num_seqs and max_pages_per_seq of a table call's tensors."""
+    shape = page_table.shape
+    if len(shape) != 2:
         raise ValueError("page_table must be [num_seqs, max_pages_per_seq]")
-    n, width = (int(x) for x in page_table.shape)
-    for t, name in ((kv_lens_prev, "kv_lens_prev"), (kv_lens, "kv_lens")):
-        if tuple(t.shape) != (n,):
-            raise ValueError("%s must have num_seqs entries" % name)
-    for t, name in ((free_count_prev, "free_count_prev"), (free_count, "free_count")):
-        if t.numel() != 1:
-            raise ValueError("%s must have one entry" % name)
-    i32 = torch.int32
-    return (n, width, int(free_pages.numel()), _dptr(page_table, "page_table", i32),
-            _dptr(kv_lens_prev, "kv_lens_prev", i32), _dptr(kv_lens, "kv_lens", i32),
-            _dptr(free_pages, "free_pages", i32), _dptr(free_count_prev, "free_count_prev", i32),
-            _dptr(free_count, "free_count", i32))
+    n, width = shape
+    if lens.numel() != n or kv_lens_prev.numel() != n or kv_lens.numel() != n:
+        raise ValueError("the requests' lengths must have num_seqs = %d entries" % n)
+    if free_count_prev.numel() != 1 or free_count.numel() != 1:
+        raise ValueError("free_count_prev and free_count must have one entry")
+    return n, width
 
 
 def rpa_build_tables(new_lens, kv_lens_prev, page_table, free_pages, free_count_prev, cu_q_lens,
@@ -506,19 +561,20 @@ def rpa_build_tables(new_lens, kv_lens_prev, page_table, free_pages, free_count_
     ([num_seqs + 1]), kv_lens, slot_map ([max_tokens] int64) and free_count
     ([1]); kv_lens may be kv_lens_prev and free_count free_count_prev."""
     import torch
-    n, width, pool, table, prev, kv, free, c0, c1 = _tables_args(
-        page_table, kv_lens_prev, kv_lens, free_pages, free_count_prev, free_count)
-    if tuple(new_lens.shape) != (n,):
-        raise ValueError("new_lens must have num_seqs entries")
-    if tuple(cu_q_lens.shape) != (n + 1,):
+    i32 = torch.int32
+    dev, st = _current(stream)
+    n, width = _tables_state(page_table, new_lens, kv_lens_prev, kv_lens, free_count_prev, free_count)
+    if cu_q_lens.numel() != n + 1:
         raise ValueError("cu_q_lens must have num_seqs + 1 entries")
-    st = lib().rpa_build_tables(
-        _dptr(new_lens, "new_lens", torch.int32), prev, table, free, c0,
-        _dptr(cu_q_lens, "cu_q_lens", torch.int32), kv, _dptr(slot_map, "slot_map", torch.int64),
-        c1, n, int(slot_map.numel()), int(page_size), width, pool, _workspace_ptr(workspace),
-        _stream_ptr(stream))
-    if st != RPA_OK:
-        raise RpaError(st, "rpa_build_tables")
+    rc = lib().rpa_build_tables(
+        _addr(new_lens, "new_lens", i32, dev), _addr(kv_lens_prev, "kv_lens_prev", i32, dev),
+        _addr(page_table, "page_table", i32, dev), _addr(free_pages, "free_pages", i32, dev),
+        _addr(free_count_prev, "free_count_prev", i32, dev), _addr(cu_q_lens, "cu_q_lens", i32, dev),
+        _addr(kv_lens, "kv_lens", i32, dev), _addr(slot_map, "slot_map", torch.int64, dev),
+        _addr(free_count, "free_count", i32, dev), n, slot_map.numel(), page_size, width,
+        free_pages.numel(), _workspace(workspace, dev)[0], st)
+    if rc != RPA_OK:
+        raise RpaError(rc, "rpa_build_tables")
 
 
 def rpa_release_tables(finished, kv_lens_prev, page_table, free_pages, free_count_prev, kv_lens,
@@ -527,22 +583,17 @@ def rpa_release_tables(finished, kv_lens_prev, page_table, free_pages, free_coun
     with finished != 0 ([num_seqs] int32) pushed on the stack free_pages, its
     length to 0."""
     import torch
-    n, width, pool, table, prev, kv, free, c0, c1 = _tables_args(
-        page_table, kv_lens_prev, kv_lens, free_pages, free_count_prev, free_count)
-    if tuple(finished.shape) != (n,):
-        raise ValueError("finished must have num_seqs entries")
-    st = lib().rpa_release_tables(
-        _dptr(finished, "finished", torch.int32), prev, table, free, c0, kv, c1, n,
-        int(page_size), width, pool, _workspace_ptr(workspace), _stream_ptr(stream))
-    if st != RPA_OK:
-        raise RpaError(st, "rpa_release_tables")
-
-
-def _workspace_ptr(workspace):
-    """The workspace's address; its header alone is 256 bytes."""
-    if workspace is not None and workspace.numel() * workspace.element_size() < 256:
-        raise ValueError("workspace must hold at least 256 bytes")
-    return _dptr(workspace, "workspace")
+    i32 = torch.int32
+    dev, st = _current(stream)
+    n, width = _tables_state(page_table, finished, kv_lens_prev, kv_lens, free_count_prev, free_count)
+    rc = lib().rpa_release_tables(
+        _addr(finished, "finished", i32, dev), _addr(kv_lens_prev, "kv_lens_prev", i32, dev),
+        _addr(page_table, "page_table", i32, dev), _addr(free_pages, "free_pages", i32, dev),
+        _addr(free_count_prev, "free_count_prev", i32, dev), _addr(kv_lens, "kv_lens", i32, dev),
+        _addr(free_count, "free_count", i32, dev), n, page_size, width, free_pages.numel(),
+        _workspace(workspace, dev)[0], st)
+    if rc != RPA_OK:
+        raise RpaError(rc, "rpa_release_tables")
 
 
 def rpa_get_device_error(workspace, stream=None) -> int:
@@ -758,22 +809,10 @@ class ForwardKv4Call(ForwardCall):
 
     def __init__(self, q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv_lens,
                  window, sm_scale: float, out, plan: Plan, workspace, stream=None):
-        import torch
-        m = plan.meta
-        pools, shape = _kv4_pools(k_pages, v_pages, k_scales, v_scales)
-        if shape[1:] != (m["num_kv_heads"], m["page_size"], m["head_dim"]):
-            raise ValueError("the pools' shape differs from the plan's")
         self._keep = (q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv_lens,
                       window, out, plan, workspace)
-        self._args = (
-            _dptr(q, "q", torch.bfloat16), *pools,
-            _dptr(page_table, "page_table", torch.int32),
-            _dptr(cu_q_lens, "cu_q_lens", torch.int32),
-            _dptr(kv_lens, "kv_lens", torch.int32), m["num_seqs"], m["num_q_heads"],
-            m["num_kv_heads"], m["head_dim"], m["page_size"],
-            _dptr(window, "window", torch.int32), float(sm_scale),
-            _dptr(out, "out", torch.bfloat16), _stream_ptr(stream), plan.handle,
-            _dptr(workspace, "workspace"), workspace.numel() * workspace.element_size())
+        self._args = _kv4_args(q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens,
+                               kv_lens, window, sm_scale, out, plan, workspace, stream)
         self._fn = lib().rpa_forward_kv4
 
     def __call__(self, plan: Optional[Plan] = None):
