@@ -443,7 +443,8 @@ rpa_status_t rpa_forward_kv(const void* q, const void* k_new, const void* v_new,
  * map); a negative entry leaves the token out.  The slots of a call are
  * distinct (else the row that stays is one of them, block by block).
  * k_pages, v_pages, k_scales and v_scales 16-B aligned.  head_dim 64, 128 or
- * 256 and page_size a power of two in [16, 256], else RPA_ERR_UNSUPPORTED.
+ * 256, page_size a power of two in [16, 256] and total_q * num_kv_heads below
+ * 2^31, else RPA_ERR_UNSUPPORTED.
  * `workspace` may be NULL; otherwise its error word records a slot outside the
  * pool (that token is left out, never trapped).  Enqueues one kernel on
  * `stream`; does not synchronise.

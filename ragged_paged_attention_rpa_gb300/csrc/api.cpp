@@ -522,6 +522,7 @@ rpa_status_t kv4_cache(const void* k_rows, const void* v_rows, uint8_t* k_pages,
   if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || page_size < 16 || page_size > 256)
     return RPA_ERR_UNSUPPORTED;
   if (total_q == 0) return RPA_OK;
+  if (static_cast<int64_t>(total_q) * num_kv_heads > 0x7fffffff) return RPA_ERR_UNSUPPORTED;
   if (k_rows == nullptr || v_rows == nullptr || k_pages == nullptr || v_pages == nullptr ||
       k_scales == nullptr || v_scales == nullptr || slot_map == nullptr)
     return RPA_ERR_INVALID_ARG;

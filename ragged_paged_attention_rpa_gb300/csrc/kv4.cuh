@@ -20,13 +20,36 @@ namespace kv4 {
 
 constexpr float kMaxScale = 10240.f;
 
+// Division of row indices below 2^31 by a head count: one wide product and a
+// shift (a 64-bit division by a variable costs some 50 instructions, a tenth of
+// what a thread of the cache's kernels runs).
+struct HeadDiv {
+  uint32_t magic, shift;
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return (__umulhi(n, magic) + n) >> shift;
+  }
+};
+inline HeadDiv head_div(int32_t heads) {
+  uint32_t shift = 0;
+  while ((1ll << shift) < heads) ++shift;
+  return {static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - heads)) / heads + 1), shift};
+}
+
+// x / d from r ~ 1 / d by one correction with the exact remainder: the quotient
+// itself where it is representable, and otherwise within little more than half
+// a step of it.
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, d, x), r, q);
+}
+
 // The scale byte for a block whose largest magnitude is `amax` (finite): the
-// nearest scale to amax / 6, ties to even.  The division is correctly rounded,
-// and no float next to a midpoint of two scales divides onto it (the midpoint
-// times 6 has at most 7 significant bits), so this equals rounding the exact
-// quotient.
+// nearest scale to amax / 6, ties to even.  A midpoint of two scales times 6
+// has at most 7 significant bits, so it divides back onto the midpoint, and the
+// floats next to it are more than half a step away: this equals rounding the
+// exact quotient.
 __device__ __forceinline__ uint32_t scale_byte(float amax) {
-  const float t = fminf(__fdiv_rn(amax, 6.f), kMaxScale);
+  const float t = fminf(quotient(amax, 6.f, 1.f / 6.f), kMaxScale);
   if (t < 6.103515625e-5f)  // below 2^-14: steps of 2^-17
     return static_cast<uint32_t>(__float2int_rn(t * 131072.f));
   const uint32_t b = __float_as_uint(t);
@@ -37,40 +60,46 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
 }
 
-// Two codes (low half first) of two floats: round to nearest even, at most 6.
-__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+// Eight codes (lowest four bits first) of eight floats: round to nearest even,
+// at most 6.
+__device__ __forceinline__ uint32_t encode8(const float* x) {
   uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n mov.b32 %0, {t, 0, 0, 0};\n}\n"
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
       : "=r"(r)
-      : "f"(lo), "f"(hi));
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+
+// Largest magnitude of three floats, NaN if one is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
   return r;
 }
 
 // A block of 16 floats -> codes (element 0 in the lowest four bits) and the
-// scale byte.  x / s is computed as x r with r ~ 1 / s and one correction by
-// the exact remainder, which gives the quotient itself wherever it is
-// representable (the ties between codes are), so a tie goes to the even code.
+// scale byte.  x / s by `quotient`: one that is a midpoint of two magnitudes is
+// representable and stays one, so the conversion's tie goes to the even code,
+// and no other lands on it (as for the scale).
 __device__ __forceinline__ uint32_t encode_block(const float (&x)[16], uint2& codes) {
-  uint32_t top = 0;  // largest magnitude as bits: NaN > infinity > finite
+  float t[5];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  for (int i = 0; i < 5; ++i) t[i] = max_abs3(x[3 * i], x[3 * i + 1], x[3 * i + 2]);
+  const float top = max_abs3(max_abs3(t[0], t[1], t[2]), max_abs3(t[3], t[4], x[15]), 0.f);
   codes = make_uint2(0u, 0u);
-  if (top >= 0x7f800000u) return 255u;
-  const uint32_t byte = scale_byte(__uint_as_float(top));
+  if (!(top < INFINITY)) return 255u;
+  const uint32_t byte = scale_byte(top);
   const float s = scale_value(byte);
-  const float r = byte ? __frcp_rn(s) : 0.f;
-  uint32_t w[2] = {0u, 0u};
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  if (byte == 0) r = 0.f;
+  float v[16];
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    float v[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float q = x[i + k] * r;
-      v[k] = fmaf(fmaf(-q, s, x[i + k]), r, q);
-    }
-    w[i >> 3] |= encode2(v[0], v[1]) << (4 * (i & 7));
-  }
-  codes = make_uint2(w[0], w[1]);
+  for (int i = 0; i < 16; ++i) v[i] = quotient(x[i], s, r);
+  codes = make_uint2(encode8(v), encode8(v + 8));
   return byte;
 }
 
@@ -109,6 +138,45 @@ __device__ __forceinline__ void decode_block(uint2 codes, uint32_t byte, uint32_
 
 __device__ __forceinline__ float2 half2_floats(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// 32 bytes from or to global memory: one access where they are 32-byte aligned
+// (two 16-byte ones, 32 bytes apart between lanes, touch every sector twice:
+// the read of 8192 rows of 16 heads of 256 took 37.5 us with them, 28.0 us so).
+__device__ __forceinline__ void load32(const void* src, bool whole, uint32_t (&w)[8]) {
+  if (whole) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+        : "l"(src));
+  } else {
+    const uint4* p = static_cast<const uint4*>(src);
+    const uint4 a = __ldg(p), b = __ldg(p + 1);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store32(void* dst, bool whole, const uint32_t (&w)[8]) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    uint4* p = static_cast<uint4*>(dst);
+    p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// A block's values as 16 bf16 (exact: six significant bits).
+__device__ __forceinline__ void decode_block_bf16(uint2 codes, uint32_t byte, uint32_t (&w)[8]) {
+  uint32_t h[8];
+  decode_block(codes, byte, h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = half2_floats(h[i]);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
 }
 
 }  // namespace kv4

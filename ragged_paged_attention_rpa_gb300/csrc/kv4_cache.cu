@@ -34,56 +34,57 @@ struct Kv4CacheParams {
   int64_t blocks;     // tokens * heads * blocks a row
   int64_t pool_slots;
   int32_t heads, bpr_shift, page_shift;  // blocks a row = 1 << bpr_shift
+  kv4::HeadDiv by_heads;
+  bool whole;         // k_rows and v_rows are 32-byte aligned
 };
 
-// 16 consecutive elements (32- or 64-byte aligned within a 16-byte aligned
-// array) as floats.
-__device__ __forceinline__ void load16(const __nv_bfloat16* src, float (&x)[16]) {
-  const uint4* p = reinterpret_cast<const uint4*>(src);
-  const uint4 a = __ldg(p), b = __ldg(p + 1);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void load16(const float* src, float (&x)[16]) {
-  const float4* p = reinterpret_cast<const float4*>(src);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 a = __ldg(p + i);
-    x[4 * i] = a.x;
-    x[4 * i + 1] = a.y;
-    x[4 * i + 2] = a.z;
-    x[4 * i + 3] = a.w;
-  }
-}
-__device__ __forceinline__ void store16(__nv_bfloat16* dst, const uint32_t (&h)[8]) {
+// Block i of an array of rows, as floats and back.
+__device__ __forceinline__ void load16(const __nv_bfloat16* rows, int64_t i, bool whole, float (&x)[16]) {
   uint32_t w[8];
+  kv4::load32(rows + i * 16, whole, w);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = kv4::half2_floats(h[i]);
-    w[i] = pack_bf16x2(f.x, f.y);  // exact: six significant bits
+  for (int j = 0; j < 8; ++j) {
+    x[2 * j] = __uint_as_float(w[j] << 16);
+    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
   }
-  reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
-__device__ __forceinline__ void store16(float* dst, const uint32_t (&h)[8]) {
+__device__ __forceinline__ void load16(const float* rows, int64_t i, bool whole, float (&x)[16]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = kv4::half2_floats(h[2 * i]), b = kv4::half2_floats(h[2 * i + 1]);
-    reinterpret_cast<float4*>(dst)[i] = make_float4(a.x, a.y, b.x, b.y);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+    kv4::load32(rows + i * 16 + 8 * h, whole, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[8 * h + j] = __uint_as_float(w[j]);
+  }
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* rows, int64_t i, bool whole, uint2 codes, uint32_t byte) {
+  uint32_t w[8];
+  kv4::decode_block_bf16(codes, byte, w);
+  kv4::store32(rows + i * 16, whole, w);
+}
+__device__ __forceinline__ void store16(float* rows, int64_t i, bool whole, uint2 codes, uint32_t byte) {
+  uint32_t h[8];
+  kv4::decode_block(codes, byte, h);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = kv4::half2_floats(h[4 * q + j]);
+      w[2 * j] = __float_as_uint(f.x);
+      w[2 * j + 1] = __float_as_uint(f.y);
+    }
+    kv4::store32(rows + i * 16 + 8 * q, whole, w);
   }
 }
 
 // Block index in the pool of block `b` of head h of token t, or -1 (padding,
 // or a slot outside the pool, which sets the error word).
 __device__ __forceinline__ int64_t pool_block(const Kv4CacheParams& p, int64_t i) {
-  const int64_t row = i >> p.bpr_shift;
+  const uint32_t row = static_cast<uint32_t>(i >> p.bpr_shift);  // below 2^31
   const int32_t b = static_cast<int32_t>(i) & ((1 << p.bpr_shift) - 1);
-  const int64_t t = row / p.heads;
-  const int32_t h = static_cast<int32_t>(row - t * p.heads);
+  const uint32_t t = p.by_heads(row);
+  const uint32_t h = row - t * p.heads;
   const int64_t slot = __ldg(p.slot_map + t);
   if (slot < 0) return -1;
   if (slot >= p.pool_slots) {
@@ -100,8 +101,8 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4CacheParam
   const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < p.blocks; i += step) {
     float k[16], v[16];
-    load16(static_cast<const T*>(p.k_rows) + i * 16, k);
-    load16(static_cast<const T*>(p.v_rows) + i * 16, v);
+    load16(static_cast<const T*>(p.k_rows), i, p.whole, k);
+    load16(static_cast<const T*>(p.v_rows), i, p.whole, v);
     const int64_t dst = pool_block(p, i);
     if (dst < 0) continue;
     uint2 kc, vc;
@@ -122,11 +123,8 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4CacheParams
     const uint2 kc = reinterpret_cast<const uint2*>(p.k_pages)[src];
     const uint2 vc = reinterpret_cast<const uint2*>(p.v_pages)[src];
     const uint32_t ks = p.k_scales[src], vs = p.v_scales[src];
-    uint32_t h[8];
-    kv4::decode_block(kc, ks, h);
-    store16(static_cast<T*>(const_cast<void*>(p.k_rows)) + i * 16, h);
-    kv4::decode_block(vc, vs, h);
-    store16(static_cast<T*>(const_cast<void*>(p.v_rows)) + i * 16, h);
+    store16(static_cast<T*>(const_cast<void*>(p.k_rows)), i, p.whole, kc, ks);
+    store16(static_cast<T*>(const_cast<void*>(p.v_rows)), i, p.whole, vc, vs);
   }
 }
 
@@ -140,6 +138,7 @@ int launch_kv4_cache(const Kv4CacheArgs& a, void* stream) {
   p.v_pages = a.v_pages;
   p.k_scales = a.k_scales;
   p.v_scales = a.v_scales;
+  p.whole = ((reinterpret_cast<uintptr_t>(a.k_rows) | reinterpret_cast<uintptr_t>(a.v_rows)) & 31) == 0;
   p.slot_map = a.slot_map;
   p.ws = a.workspace;
   p.heads = a.hkv;
@@ -148,6 +147,7 @@ int launch_kv4_cache(const Kv4CacheArgs& a, void* stream) {
   p.bpr_shift = shift;
   p.blocks = (static_cast<int64_t>(a.tokens) * a.hkv) << shift;
   if (p.blocks == 0) return 0;
+  p.by_heads = kv4::head_div(a.hkv);
   shift = 0;
   while ((1 << shift) < a.page_size) ++shift;
   p.page_shift = shift;

@@ -37,29 +37,22 @@ struct ExpandParams {
   int32_t* table_out;
   unsigned char* ws;
   int32_t hkv, bpr_shift, page_shift, mpps, num_pages;
+  kv4::HeadDiv by_heads;
 };
-
-__device__ __forceinline__ void store_block(uint4* dst, uint2 codes, uint32_t byte) {
-  uint32_t h[8], w[8];
-  kv4::decode_block(codes, byte, h);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = kv4::half2_floats(h[i]);
-    w[i] = pack_bf16x2(f.x, f.y);
-  }
-  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-}
 
 __global__ void __launch_bounds__(kThreads)
 kv4_expand_kernel(const ExpandParams p, const __grid_constant__ ExpandList list) {
   const int32_t first = list.s[0].page0;
-  const int64_t row_blocks = static_cast<int64_t>(p.hkv) << p.bpr_shift;  // of one key
-  const int64_t total = (static_cast<int64_t>(list.page_end - first) << p.page_shift) * row_blocks;
+  // Rows (key, head) of the scratch pages: below 2^31, since 2^31 of them would
+  // be 512 GB of bf16 K and V.
+  const int64_t rows = (static_cast<int64_t>(list.page_end - first) << p.page_shift) * p.hkv;
+  const int64_t row0 = (static_cast<int64_t>(first) << p.page_shift) * p.hkv;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += step) {
-    const int64_t key_row = i / row_blocks;
-    const int32_t hb = static_cast<int32_t>(i - key_row * row_blocks);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < rows << p.bpr_shift; i += step) {
+    const uint32_t row = static_cast<uint32_t>(i >> p.bpr_shift);
+    const int32_t b = static_cast<int32_t>(i) & ((1 << p.bpr_shift) - 1);
+    const uint32_t key_row = p.by_heads(row);
+    const int32_t h = static_cast<int32_t>(row - key_row * p.hkv);
     const int32_t scratch = first + static_cast<int32_t>(key_row >> p.page_shift);
     const int32_t in = static_cast<int32_t>(key_row) & ((1 << p.page_shift) - 1);
     int lo = 0, hi = list.n - 1;
@@ -72,19 +65,21 @@ kv4_expand_kernel(const ExpandParams p, const __grid_constant__ ExpandList list)
     const int64_t at = static_cast<int64_t>(e.seq) * p.mpps + slot;
     const int32_t page = __ldg(p.page_table + at);
     const bool ok = page >= 0 && page < p.num_pages;
-    if (in == 0 && hb == 0) {
+    if (in == 0 && h == 0 && b == 0) {
       p.table_out[at] = ok ? scratch : -1;
       if (!ok) report_error(p.ws, RPA_DEVERR_PAGE_ID, e.seq);
     }
     const int32_t key = (slot << p.page_shift) + in;
     if (!ok || key < e.lo || key >= e.hi) continue;
-    const int32_t h = hb >> p.bpr_shift, b = hb & ((1 << p.bpr_shift) - 1);
     const int64_t src = ((((static_cast<int64_t>(page) * p.hkv + h) << p.page_shift) + in) << p.bpr_shift) + b;
-    const int64_t dst = 2 * (static_cast<int64_t>(first) * (row_blocks << p.page_shift) + i);
+    const int64_t dst = 2 * ((row0 << p.bpr_shift) + i);
     const uint2 kc = __ldg(p.k + src), vc = __ldg(p.v + src);
     const uint32_t ks = __ldg(p.ks + src), vs = __ldg(p.vs + src);
-    store_block(p.k_out + dst, kc, ks);
-    store_block(p.v_out + dst, vc, vs);
+    uint32_t w[8];  // the workspace's arrays are 256-byte aligned
+    kv4::decode_block_bf16(kc, ks, w);
+    kv4::store32(p.k_out + dst, true, w);
+    kv4::decode_block_bf16(vc, vs, w);
+    kv4::store32(p.v_out + dst, true, w);
   }
 }
 
@@ -102,6 +97,7 @@ int launch_kv4_expand(const Plan& plan, const Args& a, void* stream) {
   p.table_out = reinterpret_cast<int32_t*>(a.workspace + plan.off_kv4_table);
   p.ws = a.workspace;
   p.hkv = plan.hkv;
+  p.by_heads = kv4::head_div(plan.hkv);
   int shift = 0;
   while ((16 << shift) < plan.d) ++shift;
   p.bpr_shift = shift;

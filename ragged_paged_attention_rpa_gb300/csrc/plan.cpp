@@ -666,7 +666,8 @@ rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu, const int32_t* kv
     const int32_t slot0 = lo / plan.p;
     plan.kv4_expand.push_back({s, slot0, static_cast<int32_t>(pages), lo, kv[s]});
     pages += ceil_div(kv[s], plan.p) - slot0;
-    if (pages > 0x7fffffff) return RPA_ERR_UNSUPPORTED;
+    // (The expansion counts the scratch rows of all heads in 31 bits.)
+    if (pages * plan.p * plan.hkv > 0x7fffffff) return RPA_ERR_UNSUPPORTED;
   }
   plan.kv4_scratch_pages = static_cast<int32_t>(pages);
   if (plan.num_prefill > 0) {
