@@ -58,6 +58,7 @@ struct Kv4Params {
   unsigned char* ws;
   float* part_o;    // [2 * CTAs][rows][D]
   float* part_lse;  // [2 * CTAs][rows]
+  float4* piece_o;  // [CTAs * warps][accumulator tiles][32 lanes]
   int32_t hq, hkv, group, page_shift, mpps, num_pages;
   float scale_log2;
 };
@@ -96,6 +97,22 @@ __device__ __forceinline__ void place_next(const Kv4Sched<NSEG>& sc, const Kv4Pa
   }
   if (s.rem > 0) s.nb = sc.tile[s.e].nb;
 }
+// The place `off` units further on (0 <= off <= rem).
+template <int NSEG>
+__device__ __forceinline__ void place_skip(const Kv4Sched<NSEG>& sc, const Kv4Params& p, Place& s, int32_t off) {
+  while (off > 0 && off >= s.nb + kKv4SegCost - s.j) {
+    off -= s.nb + kKv4SegCost - s.j;
+    place_next(sc, p, s);
+  }
+  s.j += off;
+  s.rem -= off;
+}
+
+// What a warp holds of a segment it shares: blocks [j0, j1) of segment (e, g);
+// e < 0: nothing.
+struct Piece {
+  int32_t e, g, j0, j1;
+};
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32_t src_bytes) {
@@ -172,19 +189,21 @@ __device__ __forceinline__ uint32_t scale_pair_of(uint32_t lo, uint32_t hi, int 
   return __byte_perm(lo, hi, i == 0 ? 0x3430 : 0x3531) << 7;
 }
 
-// Shapes of an instance: D, NT tiles of 8 rows, W warps a CTA, CTAS CTAs a SM,
-// SUB 16-key parts a block, S blocks in flight a warp.  O and Q take (D / 4 +
-// D / 8) NT registers of a thread: up to 48 leaves 16 warps a SM (128 registers
-// each) and blocks of 32 keys, which halve the cost of the loop around the
-// products; 96 leaves 12 warps and blocks of 16.
+// Shapes of an instance: D, NT tiles of 8 rows, W warps a CTA, SUB 16-key parts
+// a block, S blocks in flight a warp.  One CTA a SM: of two or three, the SM
+// serves the oldest first (with equal shares of the 32 long contexts the first
+// CTAs of the SMs ended after 112 us, the second after 130 us), while the warps
+// of one CTA end together.  O takes D NT / 4 registers of a thread and Q D NT / 8:
+// up to 48 together leaves 16 warps (128 registers each) and blocks of 32 keys,
+// which halve the cost of the loop around the products; 96 (kWide) leaves 12
+// warps and blocks of 16.
 template <int D_, int NT_>
 struct Kv4Shape {
   static constexpr int D = D_, NT = NT_;
   static constexpr bool kWide = D * NT >= 256;
-  static constexpr int W = kWide ? 4 : 8;
-  static constexpr int CTAS = kWide ? 3 : 2;
+  static constexpr int W = kWide ? 12 : 16;
   static constexpr int SUB = kWide ? 1 : 2;
-  static constexpr int S = D == 256 ? 3 : kWide ? 5 : D == 128 ? 2 : 3;
+  static constexpr int S = D == 256 ? 4 : kWide ? 8 : D == 128 ? 3 : 6;
   static constexpr int kBlk = 16 * SUB;
   static constexpr int kRows = 8 * NT;
   static constexpr int KC = D == 256 ? 2 : 1;   // chunks of a K row a lane
@@ -197,22 +216,26 @@ struct Kv4Shape {
   static constexpr int kVOff = 8 * D, kSOff = 16 * D, kPart = 18 * D;
   static constexpr int kStage = SUB * kPart;
   static constexpr int kRing = W * S * kStage;
-  // Merge buffer: TPP accumulator tiles of every warp at a time.
-  static constexpr int TPP = MT * NT < 8 ? MT * NT : 8;
-  static constexpr int kMerge = W * TPP * 32 * 16;
-  static constexpr int kBytes = kRing + kMerge;
-  static_assert(CTAS * (kBytes + 2048) <= 227 * 1024, "shared memory of an SM");
+  static constexpr int kBytes = kRing;
+  static_assert(W * MT * NT * 512 <= kRing, "the merge meets in the ring");
+  static_assert(kBytes + 2 * W * (16 * kRows + 16) + 1024 <= 228 * 1024, "shared memory of an SM");
+  static_assert(kRows <= 16 && 2 * W <= 32 && SUB * S <= 32, "merge and flags");
 };
 
 template <typename Sh, int NSEG>
-__global__ void __launch_bounds__(Sh::W * 32, Sh::CTAS)
+__global__ void __launch_bounds__(Sh::W * 32, 1)
 kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
   constexpr int D = Sh::D, NT = Sh::NT, W = Sh::W, S = Sh::S, MT = Sh::MT, SUB = Sh::SUB;
   constexpr int KC = Sh::KC, KG = Sh::KG, KW = Sh::KW, VG = Sh::VG, VW = Sh::VW;
   constexpr int kBlk = Sh::kBlk;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float wm[W][Sh::kRows], wl[W][Sh::kRows];
-  __shared__ int64_t s_row[Sh::kRows];  // offset in `out` of each row of the tile, or -1
+  // Per warp up to two pieces of segments it shares with others: one that ends
+  // in its range (its state goes to the workspace) and the one it ends in
+  // (kept in registers); their references and sums per row.
+  __shared__ Piece s_piece[2 * W];
+  __shared__ float wm[2 * W][Sh::kRows], wl[2 * W][Sh::kRows];
+  __shared__ __align__(8) float s_share[2 * W][Sh::kRows];
+  __shared__ float s_lse[2 * W][Sh::kRows];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -220,22 +243,30 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
   const Kv4Start start = sc.cta[blockIdx.x];
   if (start.len <= 0) return;
   Place cs{start.tile, start.head, start.j, start.len, sc.tile[start.tile].nb};
+  {
+    // This warp's share: an equal, contiguous part of the CTA's range.
+    const int32_t w0 = static_cast<int32_t>(static_cast<int64_t>(start.len) * warp / W);
+    const int32_t w1 = static_cast<int32_t>(static_cast<int64_t>(start.len) * (warp + 1) / W);
+    place_skip(sc, p, cs, w0);
+    cs.rem = w1 - w0;
+    if (lane < 2) s_piece[2 * warp + lane].e = -1;
+  }
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S * Sh::kStage;
-  float4* mbuf = reinterpret_cast<float4*>(smem + Sh::kRing);
+  float4* mbuf = reinterpret_cast<float4*>(smem);
 
   // ---- The copies' side.  This warp's blocks of the range, in order, come in
   // batches of up to 32 of one segment: lane i holds the page ids of the
   // batch's block i, read a batch ahead of their use.
   struct Batch {
-    int32_t n, blk;        // blocks; the first one (the others are W apart)
+    int32_t n, blk;        // blocks; the first one
     int32_t g, seq, lo, hi;  // KV head, sequence, keys the tile sees
     int32_t page[2];       // (lane) page of the block's first and, where pages are 16 keys, second part
   };
   Place bs = cs;          // where the next batch comes from
-  int32_t bj = bs.j + warp;
+  int32_t bj = bs.j;
   auto next_batch = [&](Batch& b) {
     int32_t j1 = 0;
-    for (;; place_next(sc, p, bs), bj = bs.j + warp) {
+    for (;; place_next(sc, p, bs), bj = bs.j) {
       if (bs.rem <= 0) {
         b.n = 0;
         return;
@@ -244,7 +275,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
       if (bj < j1) break;
     }
     const Kv4Tile& t = sc.tile[bs.e];
-    b.n = min(32, (j1 - bj + W - 1) / W);
+    b.n = min(32, j1 - bj);
     b.blk = t.fb + bj;
     b.g = bs.g;
     b.seq = t.seq;
@@ -252,7 +283,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
     b.hi = t.pos0 + (t.r0 + t.nrows - 1) / p.group;
     b.page[0] = b.page[1] = -1;
     if (lane < b.n) {
-      const int32_t key = (b.blk + lane * W) * kBlk;
+      const int32_t key = (b.blk + lane) * kBlk;
       const int32_t* row = p.page_table + static_cast<int64_t>(t.seq) * p.mpps;
       // Parts no row of the tile sees are not looked up (-2).
 #pragma unroll
@@ -268,7 +299,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
         }
       }
     }
-    bj += 32 * W;
+    bj += 32;
   };
   Batch cur, nxt;
   next_batch(cur);
@@ -281,7 +312,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
   const uint8_t* const s_lane = (lane < H ? p.ks : p.vs) + (lane & (H - 1)) * 16;
   auto issue = [&](int st) {
     if (bi < cur.n) {
-      const int32_t key = (cur.blk + bi * W) * kBlk;
+      const int32_t key = (cur.blk + bi) * kBlk;
       const uint32_t dst = ring + st * Sh::kStage;
 #pragma unroll
       for (int h = 0; h < SUB; ++h) {
@@ -323,10 +354,14 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
   for (int st = 0; st < S; ++st) issue(st);
 
   int st = 0;
-  bool first = true;
-  for (; cs.rem > 0; place_next(sc, p, cs), first = false) {
+  float o[MT][NT][4];
+  // Columns' reference (a finite stand-in for -inf until the first score) and
+  // this lane's sums.
+  float m0[NT], m1[NT], l0[NT], l1[NT];
+  bool held = false;  // o, m and l are the piece kept for the merge
+  for (; cs.rem > 0; place_next(sc, p, cs)) {
     const int32_t j1 = min(cs.nb, cs.j + cs.rem);
-    if (cs.j >= j1) continue;  // only the segment's merge charge lies in this range
+    if (cs.j >= j1) continue;  // only the segment's charge lies in this range
     const Kv4Tile& tl = sc.tile[cs.e];
     const int G = p.group;
     // ---- The tile's queries as B fragments: lane (g, c) holds row g (+ 8 nt)
@@ -339,7 +374,6 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
       const int r = tl.r0 + n;
       const bool has = n < tl.nrows;
       const int64_t off = (static_cast<int64_t>(tl.q0 + r / G) * p.hq + cs.g * G + r % G) * D;
-      if (warp == 0 && c == 0) s_row[n] = has ? off : -1;
       uint32_t top = 0;
 #pragma unroll
       for (int w = 0; w < KC * KW; ++w) {
@@ -377,10 +411,6 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
     // Keys every row sees.
     const int32_t all_lo = first_visible(seg_hi, tl.window), all_hi = tl.pos0 + tl.r0 / G;
 
-    float o[MT][NT][4];
-    // Columns' reference (a finite stand-in for -inf until the first score)
-    // and this lane's sums.
-    float m0[NT], m1[NT], l0[NT], l1[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m0[nt] = m1[nt] = kNoScore;
@@ -389,7 +419,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
       for (int t = 0; t < MT; ++t) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.f;
     }
 
-    for (int32_t j = cs.j + warp; j < j1; j += W) {
+    for (int32_t j = cs.j; j < j1; ++j) {
       copy_wait<S - 1>();
       __syncwarp();  // the scales are other lanes' copies
       const uint32_t src = ring + st * Sh::kStage;
@@ -602,84 +632,138 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
       if (++st == S) st = 0;
     }
 
-    // ---- Merge the warps: each scales its state by its share of the
-    // normalised result, then the shares are added in warp order.
+    // ---- The segment's end in this warp's range.
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         l0[nt] += __shfl_xor_sync(0xffffffffu, l0[nt], off);
         l1[nt] += __shfl_xor_sync(0xffffffffu, l1[nt], off);
       }
-      if (g == 0) {
-        wm[warp][8 * nt + 2 * c] = m0[nt];
-        wm[warp][8 * nt + 2 * c + 1] = m1[nt];
-        wl[warp][8 * nt + 2 * c] = l0[nt];
-        wl[warp][8 * nt + 2 * c + 1] = l1[nt];
+    if (cs.j == 0 && j1 == cs.nb) {
+      // All of it: normalise and store, 16 bytes (8 dimensions) at a time.
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float l = h ? l1[nt] : l0[nt];
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int n = 8 * nt + 2 * c + h, r = tl.r0 + n;
+          if (n < tl.nrows) {
+            __nv_bfloat16* dst =
+                p.out + (static_cast<int64_t>(tl.q0 + r / G) * p.hq + cs.g * G + r % G) * D + g * (D / 8);
+#pragma unroll
+            for (int w = 0; w < MT / 4; ++w) {
+              uint32_t v[4];
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                v[t] = pack_bf16x2(o[4 * w + t][nt][h] * inv, o[4 * w + t][nt][2 + h] * inv);
+              reinterpret_cast<uint4*>(dst)[w] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          }
+        }
+      continue;
+    }
+    held = cs.rem <= cs.nb + kKv4SegCost - cs.j;  // nothing follows in this range
+    const int piece = 2 * warp + (held ? 1 : 0);
+    if (lane == 0) s_piece[piece] = Piece{cs.e, cs.g, cs.j, j1};
+    if (g == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        wm[piece][8 * nt + 2 * c] = m0[nt];
+        wm[piece][8 * nt + 2 * c + 1] = m1[nt];
+        wl[piece][8 * nt + 2 * c] = l0[nt];
+        wl[piece][8 * nt + 2 * c + 1] = l1[nt];
       }
     }
-    __syncthreads();
-    const bool whole = cs.j == 0 && j1 == cs.nb;
-    const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+    if (held) break;
+    float4* dst = p.piece_o + (static_cast<int64_t>(blockIdx.x) * W + warp) * (MT * NT * 32) + lane;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float f[2];
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int n = 8 * nt + 2 * c + h;
-        float M = kNoScore, L = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+        dst[(t * NT + nt) * 32] = make_float4(o[t][nt][0], o[t][nt][1], o[t][nt][2], o[t][nt][3]);
+  }
+  // ---- Merge the CTA's pieces, once.  Those of one segment follow one another:
+  // the kept ones of warps in order (one without blocks has a zero share), then
+  // (of the warp it ends in) one from the workspace.  Their sum, each times its
+  // share of the normalised result, is taken in that order.  The states meet in the ring, which
+  // is free by now.  (Rolled loops: this code runs once a launch, and fetching
+  // it, fully unrolled, took longer than running it.)
+  copy_wait<0>();
+  __syncthreads();
 #pragma unroll
-        for (int w = 0; w < W; ++w) M = fmaxf(M, wm[w][n]);
-        // (A warp without a score has l = 0, or NaN, which stays.)
+  for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int w = 0; w < W; ++w) L += wl[w][n] * fast_exp2(wm[w][n] - M);
-        f[h] = L == 0.f ? 0.f : fast_exp2((h ? m1[nt] : m0[nt]) - M) / L;
-        if (!whole && warp == 0 && g == 0)
-          p.part_lse[static_cast<int64_t>(slot) * Sh::kRows + n] = L == 0.f ? -INFINITY : M + __log2f(L);
-      }
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        o[t][nt][0] *= f[0];
-        o[t][nt][1] *= f[1];
-        o[t][nt][2] *= f[0];
-        o[t][nt][3] *= f[1];
-      }
+    for (int nt = 0; nt < NT; ++nt)
+      mbuf[(warp * MT * NT + t * NT + nt) * 32 + lane] =
+          held ? make_float4(o[t][nt][0], o[t][nt][1], o[t][nt][2], o[t][nt][3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+  // Lane k looks at piece k: which others are its segment's.
+  const int my_e = lane < 2 * W ? s_piece[lane].e : -1;
+  const uint32_t my_members =
+      __match_any_sync(0xffffffffu, my_e < 0 ? -1ll : (static_cast<int64_t>(my_e) << 32) + s_piece[lane].g);
+  const uint32_t heads = __ballot_sync(0xffffffffu, my_e >= 0 && __ffs(my_members) - 1 == lane);
+  // Thread (i, n): piece i's share of row n, 2^(m_i - M) / sum_k 2^(m_k - M) l_k.
+  static_assert(32 % Sh::kRows == 0, "whole rows a warp");
+  const int pi = min(tid / Sh::kRows, 31), pn = tid % Sh::kRows;
+  uint32_t members = __shfl_sync(0xffffffffu, my_members, pi);
+  if (pi >= 2 * W || __shfl_sync(0xffffffffu, my_e, pi) < 0) members = 0;
+  if (tid < 2 * W * Sh::kRows) {
+    float M = kNoScore, L = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < 2 * W; ++k) {
+      const float m = wm[k][pn];
+      M = fmaxf(M, (members >> k) & 1u ? m : kNoScore);
     }
-    constexpr int kPasses = MT * NT / Sh::TPP;
-#pragma unroll
-    for (int ps = 0; ps < kPasses; ++ps) {
-#pragma unroll
-      for (int i = 0; i < Sh::TPP; ++i) {
-        const int q = ps * Sh::TPP + i;
-        const float (&a)[4] = o[q / NT][q % NT];
-        mbuf[(warp * Sh::TPP + i) * 32 + lane] = make_float4(a[0], a[1], a[2], a[3]);
-      }
-      __syncthreads();
-      for (int i = tid; i < Sh::TPP * 32; i += W * 32) {
-        float4 a = mbuf[i];
-#pragma unroll
-        for (int w = 1; w < W; ++w) {
-          const float4 b = mbuf[w * Sh::TPP * 32 + i];
-          a.x += b.x;
-          a.y += b.y;
-          a.z += b.z;
-          a.w += b.w;
-        }
-        const int q = ps * Sh::TPP + (i >> 5);
-        const int mt = q / NT, nt = q % NT;
-        // Lane (g, c) holds columns 2c, 2c + 1 of dimensions d, d + 1.
-        const int d = g * (D / 8) + 2 * mt, n = 8 * nt + 2 * c;
-        if (whole) {
-          const int64_t r0 = s_row[n], r1 = s_row[n + 1];
-          if (r0 >= 0) *reinterpret_cast<uint32_t*>(p.out + r0 + d) = pack_bf16x2(a.x, a.z);
-          if (r1 >= 0) *reinterpret_cast<uint32_t*>(p.out + r1 + d) = pack_bf16x2(a.y, a.w);
-        } else {
-          float* dst = p.part_o + (static_cast<int64_t>(slot) * Sh::kRows + n) * D + d;
-          *reinterpret_cast<float2*>(dst) = make_float2(a.x, a.z);
-          *reinterpret_cast<float2*>(dst + D) = make_float2(a.y, a.w);
-        }
-      }
-      __syncthreads();
+#pragma unroll 8
+    for (int k = 0; k < 2 * W; ++k) {
+      const float f = fast_exp2(wm[k][pn] - M) * wl[k][pn];
+      L += (members >> k) & 1u ? f : 0.f;
+    }
+    // (A segment without a score has L = 0; a NaN stays.)
+    s_share[pi][pn] = members == 0 || L == 0.f ? 0.f : fast_exp2(wm[pi][pn] - M) / L;
+    s_lse[pi][pn] = L == 0.f ? -INFINITY : M + __log2f(L);
+  }
+  __syncthreads();
+  constexpr int kItems = MT * NT * 32;  // float4 of a state: a multiple of the warp
+  const int total = __popc(heads) * kItems;
+#pragma unroll 1
+  for (int idx = tid; idx < total; idx += W * 32) {
+    const int k0 = __fns(heads, 0, idx / kItems + 1);  // (the same for the whole warp)
+    const int k1 = 31 - __clz(__shfl_sync(0xffffffffu, my_members, k0));
+    const int i = idx % kItems;
+    const int mt = (i >> 5) / NT, nt = (i >> 5) % NT;
+    // Lane (g, c) holds columns 2c, 2c + 1 of dimensions d, d + 1.
+    const int d = g * (D / 8) + 2 * mt, n = 8 * nt + 2 * c;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int k, const float4& b) {
+      const float2 f = *reinterpret_cast<const float2*>(&s_share[k][n]);
+      a.x = fmaf(b.x, f.x, a.x);
+      a.y = fmaf(b.y, f.y, a.y);
+      a.z = fmaf(b.z, f.x, a.z);
+      a.w = fmaf(b.w, f.y, a.w);
+    };
+#pragma unroll 4
+    for (int k = k0 | 1; k <= k1; k += 2) add(k, mbuf[(k >> 1) * kItems + i]);
+    if ((k1 & 1) == 0) add(k1, p.piece_o[(static_cast<int64_t>(blockIdx.x) * W + (k1 >> 1)) * kItems + i]);
+    const Piece head = s_piece[k0];
+    const Kv4Tile& tl = sc.tile[head.e];
+    if (head.j0 == 0 && s_piece[k1].j1 == tl.nb) {
+      const int r = tl.r0 + n;
+      __nv_bfloat16* const col = p.out + static_cast<int64_t>(head.g * p.group) * D + d;
+      auto row = [&](int r) {
+        return (static_cast<int64_t>(tl.q0 + r / p.group) * p.hq + r % p.group) * D;
+      };
+      if (n < tl.nrows) *reinterpret_cast<uint32_t*>(col + row(r)) = pack_bf16x2(a.x, a.z);
+      if (n + 1 < tl.nrows) *reinterpret_cast<uint32_t*>(col + row(r + 1)) = pack_bf16x2(a.y, a.w);
+    } else {
+      // Cut across CTAs: the normalised part goes out with its log2-sum-exp.
+      const int64_t slot = 2 * blockIdx.x + (head.e == start.tile && head.g == start.head ? 0 : 1);
+      float* const dst = p.part_o + (slot * Sh::kRows + n) * D + d;
+      *reinterpret_cast<float2*>(dst) = make_float2(a.x, a.z);
+      *reinterpret_cast<float2*>(dst + D) = make_float2(a.y, a.w);
+      if (mt == 0 && g == 0)
+        *reinterpret_cast<float2*>(&p.part_lse[slot * Sh::kRows + n]) = make_float2(s_lse[k0][n], s_lse[k0][n + 1]);
     }
   }
 }
@@ -791,8 +875,7 @@ int launch_n(const Plan& plan, const Kv4Params& p, const Plan::Kv4Launch& l, cud
 Kv4Grain kv4_grain(int32_t head_dim, int32_t nt) {
   using Narrow = Kv4Shape<128, 1>;
   using Wide = Kv4Shape<256, 1>;
-  return head_dim * nt >= 256 ? Kv4Grain{Wide::CTAS, Wide::W, Wide::kBlk}
-                              : Kv4Grain{Narrow::CTAS, Narrow::W, Narrow::kBlk};
+  return head_dim * nt >= 256 ? Kv4Grain{Wide::W, Wide::kBlk} : Kv4Grain{Narrow::W, Narrow::kBlk};
 }
 
 int launch_kv4_decode(const Plan& plan, const Args& a, void* stream) {
@@ -807,6 +890,7 @@ int launch_kv4_decode(const Plan& plan, const Args& a, void* stream) {
   p.ws = a.workspace;
   p.part_o = reinterpret_cast<float*>(a.workspace + plan.off_partial_o);
   p.part_lse = reinterpret_cast<float*>(a.workspace + plan.off_partial_lse);
+  p.piece_o = reinterpret_cast<float4*>(a.workspace + plan.off_kv4_pieces);
   p.hq = plan.hq;
   p.hkv = plan.hkv;
   p.group = plan.hq / plan.hkv;

@@ -600,7 +600,7 @@ rpa_status_t plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, c
       for (int32_t i = b; i < e; ++i)
         v0.push_back(v0.back() + static_cast<int64_t>(plan.kv4_tiles[i].nb + kKv4SegCost) * plan.hkv);
       const int64_t total = v0.back();
-      const int64_t most = std::min<int64_t>(static_cast<int64_t>(plan.num_sms) * grain.ctas_per_sm, kKv4MaxCtas);
+      const int64_t most = std::min<int64_t>(plan.num_sms, kKv4MaxCtas);
       const int64_t n = std::max<int64_t>(
           std::max<int64_t>(1, std::min(most, total / (kKv4BlocksPerWarp * grain.warps))),
           std::min(most, ceil_div(total, 0x3fffffff)));
@@ -626,6 +626,7 @@ rpa_status_t plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, c
       plan.max_splits = std::max(plan.max_splits, 1);
       plan.decode_ctas += n;
       plan.kv4_part_rows = std::max(plan.kv4_part_rows, 2 * n * nt * 8);
+      plan.kv4_piece_rows = std::max(plan.kv4_piece_rows, grain.warps * n * nt * 8);
       plan.kv4_launches.push_back(l);
     }
   }
@@ -654,6 +655,7 @@ rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu, const int32_t* kv
   if (plan.kv4_part_rows > 0) {
     plan.off_partial_o = take(static_cast<size_t>(plan.kv4_part_rows) * plan.d * sizeof(float));
     plan.off_partial_lse = take(static_cast<size_t>(plan.kv4_part_rows) * sizeof(float));
+    plan.off_kv4_pieces = take(static_cast<size_t>(plan.kv4_piece_rows) * plan.d * sizeof(float));
   }
   int64_t pages = 0;
   for (int32_t s = 0; s < plan.num_seqs; ++s) {

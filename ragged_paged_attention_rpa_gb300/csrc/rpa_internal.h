@@ -94,9 +94,9 @@ constexpr int kDecodeSegCost = 7;
 // there too), and the charge, in key blocks, for each segment (its merge and
 // output).
 constexpr int kKv4TilesSmall = 160;
-constexpr int kKv4TilesLarge = 736;
-constexpr int kKv4MaxCtas = 512;
-constexpr int kKv4SegCost = 8;
+constexpr int kKv4TilesLarge = 864;
+constexpr int kKv4MaxCtas = 256;
+constexpr int kKv4SegCost = 3;
 // Sequences whose 4-bit pages one expansion launch lists.
 constexpr int kKv4ExpandSeqs = 1024;
 
@@ -182,7 +182,9 @@ struct Plan {
   std::vector<Kv4Launch> kv4_launches;
   std::vector<Kv4Expand> kv4_expand;
   int64_t kv4_part_rows = 0;      // rows of the split-KV partials (two tiles a CTA)
+  int64_t kv4_piece_rows = 0;     // rows of its warps' pieces (one tile a warp)
   int32_t kv4_scratch_pages = 0;
+  size_t off_kv4_pieces = 0;
   size_t off_kv4_k = 0, off_kv4_v = 0, off_kv4_table = 0;
 
   // Prefill (q_len >= prefill_min_q).
@@ -285,7 +287,7 @@ int launch_prologue(const PrologueArgs& a, void* stream);
 // their own (kv4_expand.cu).
 int launch_kv4_decode(const Plan& plan, const Args& a, void* stream);
 struct Kv4Grain {
-  int32_t ctas_per_sm, warps, block_keys;
+  int32_t warps, block_keys;  // of a CTA (one a SM); keys of a block
 };
 Kv4Grain kv4_grain(int32_t head_dim, int32_t nt);
 int launch_kv4_expand(const Plan& plan, const Args& a, void* stream);
