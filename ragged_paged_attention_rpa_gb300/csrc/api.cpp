@@ -6,6 +6,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <functional>
 #include <mutex>
 #include <new>
 #include <set>
@@ -207,6 +208,33 @@ int side_stream(SideStream** out) {
   return 0;
 }
 
+// `here` on the caller's stream and `there` on the side stream, forked after
+// everything enqueued so far; the caller's stream then waits for `there`.
+// Their grids share the SMs between them and fill them once.
+using Launch = std::function<int(rpa_stream_t)>;  // enqueues on a stream; a cudaError_t
+rpa_status_t side_by_side(rpa_stream_t stream, const Launch& here, const Launch& there) {
+  SideStream* side = nullptr;
+  int err = side_stream(&side);
+  if (err) return cuda_failed(err);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaEventRecord(side->fork, s);
+  if (e == cudaSuccess) e = cudaStreamWaitEvent(side->stream, side->fork, 0);
+  if (e != cudaSuccess) return cuda_failed(static_cast<int>(e));
+  rpa_stream_t ss = reinterpret_cast<rpa_stream_t>(side->stream);
+  rpa::trace_start(ss);
+  err = there(ss);
+  if (err) return cuda_failed(err);
+  if ((e = cudaEventRecord(side->join, side->stream)) != cudaSuccess)
+    return cuda_failed(static_cast<int>(e));
+  err = here(stream);
+  // Join even when that launch failed, so that a capture in progress is left
+  // with every forked stream joined.
+  e = cudaStreamWaitEvent(s, side->join, 0);
+  if (err) return cuda_failed(err);
+  if (e != cudaSuccess) return cuda_failed(static_cast<int>(e));
+  return RPA_OK;
+}
+
 rpa_status_t forward_launch(const rpa::Plan& p, const rpa::Args& a,
                             const rpa::KvWriteArgs* kvw, rpa_stream_t stream,
                             const rpa::PrologueArgs* pro = nullptr) {
@@ -218,27 +246,11 @@ rpa_status_t forward_launch(const rpa::Plan& p, const rpa::Args& a,
   const bool prefill = !p.items.empty();
   if (decode && prefill && p.overlap) {
     // Side by side: the prefill grid (prefill_sms CTAs) on the side stream,
-    // forked after everything enqueued so far, the decode grid (decode_sms
-    // CTAs) on the caller's stream; the caller's stream then waits for the
-    // prefill.  Together the grids fill the SMs once.
-    SideStream* side = nullptr;
-    if ((err = side_stream(&side)) != 0) return cuda_failed(err);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaEventRecord(side->fork, s);
-    if (e == cudaSuccess) e = cudaStreamWaitEvent(side->stream, side->fork, 0);
-    if (e != cudaSuccess) return cuda_failed(static_cast<int>(e));
-    rpa_stream_t ss = reinterpret_cast<rpa_stream_t>(side->stream);
-    rpa::trace_start(ss);
-    err = rpa::launch_prefill_tc(p, a, ss);
-    if (err) return cuda_failed(err);
-    if ((e = cudaEventRecord(side->join, side->stream)) != cudaSuccess)
-      return cuda_failed(static_cast<int>(e));
-    err = rpa::launch_decode(p, a, stream);
-    // Join even when the decode launch failed, so that a capture in progress
-    // is left with every forked stream joined.
-    e = cudaStreamWaitEvent(s, side->join, 0);
-    if (err) return cuda_failed(err);
-    if (e != cudaSuccess) return cuda_failed(static_cast<int>(e));
+    // the decode grid (decode_sms CTAs) on the caller's stream.
+    rpa_status_t st = side_by_side(
+        stream, [&](rpa_stream_t s) { return rpa::launch_decode(p, a, s); },
+        [&](rpa_stream_t s) { return rpa::launch_prefill_tc(p, a, s); });
+    if (st != RPA_OK) return st;
   } else {
     if (decode) {
       err = rpa::launch_decode(p, a, stream);
@@ -589,18 +601,20 @@ rpa_status_t rpa_forward_kv4(const void* q, const uint8_t* k_pages, const uint8_
   a.k_block_scales = k_scales;
   a.v_block_scales = v_scales;
   rpa::trace_start(stream);
-  int err = 0;
-  if (!p.kv4_launches.empty() && (err = rpa::launch_kv4_decode(p, a, stream)) != 0)
-    return cuda_failed(err);
-  if (!p.items.empty()) {
-    if ((err = rpa::launch_kv4_expand(p, a, stream)) != 0) return cuda_failed(err);
+  auto decode = [&](rpa_stream_t s) { return rpa::launch_kv4_decode(p, a, s); };
+  auto prefill = [&](rpa_stream_t s) {
+    if (int e = rpa::launch_kv4_expand(p, a, s)) return e;
     rpa::Args b = a;
     b.k_pages = a.workspace + p.off_kv4_k;
     b.v_pages = a.workspace + p.off_kv4_v;
     b.page_table = reinterpret_cast<const int32_t*>(a.workspace + p.off_kv4_table);
     b.pool_pages = p.kv4_scratch_pages;
-    if ((err = rpa::launch_prefill_tc(p, b, stream)) != 0) return cuda_failed(err);
-  }
+    return rpa::launch_prefill_tc(p, b, s);
+  };
+  if (p.overlap) return side_by_side(stream, decode, prefill);
+  int err = 0;
+  if (!p.kv4_launches.empty() && (err = decode(stream)) != 0) return cuda_failed(err);
+  if (!p.items.empty() && (err = prefill(stream)) != 0) return cuda_failed(err);
   return RPA_OK;
 }
 

@@ -17,10 +17,8 @@
 // Layout.  A product's order of terms is free, so which dimension a fragment's
 // k index means is chosen such that a lane needs a contiguous run of bytes: of
 // K rows g and g + 8 its quarter of the row (Q is fetched with the same
-// permutation), of V its eighth of the rows of its four keys.  Each lane copies
-// exactly those bytes with cp.async into slots of its own in shared memory and
-// is the only one to read them: no bank conflicts, no barrier, and several
-// blocks in flight a warp.  Only the scales (2 D bytes a block) cross lanes.
+// permutation), of V its eighth of the rows of its four keys.  Every warp copies
+// its own blocks with cp.async, a few ahead, into a ring of its own.
 // Of V, two keys' codes are interleaved with two bit selects per eight codes
 // before they are widened, which gives the register pairs along the keys that
 // the second product wants without a transpose.
@@ -114,15 +112,9 @@ struct Piece {
   int32_t e, g, j0, j1;
 };
 
-template <int BYTES>
+// 16 bytes from global to shared memory; zeros where src_bytes is 0.
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32_t src_bytes) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(src_bytes),
-                 "n"(BYTES)
-                 : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -189,6 +181,31 @@ __device__ __forceinline__ uint32_t scale_pair_of(uint32_t lo, uint32_t hi, int 
   return __byte_perm(lo, hi, i == 0 ? 0x3430 : 0x3531) << 7;
 }
 
+// Where 16 keys' rows of D / 2 bytes sit in shared memory: in order, as lines of
+// 128 bytes, the eight 16-byte chunks of line n permuted by XOR with swz(n).  A
+// copy instruction then fills four whole lines from 512 contiguous bytes, and
+// the reads below meet every bank once.  (Each lane copying just what it reads
+// itself costs a wavefront a lane instead of one for eight: 263 of them a
+// 256-wide block of 16 keys, as long as all the rest of the block.)
+template <int D>
+struct RowLayout {
+  static __device__ __forceinline__ uint32_t swz(uint32_t line) {
+    return D == 256 ? line & 7 : D == 128 ? 2 * (line & 3) : 2 * (line & 1);
+  }
+  // Byte of the lane's chunk in the first copy instruction, and in the i-th.
+  static __device__ __forceinline__ uint32_t copy_at(uint32_t lane) {
+    return (lane >> 3) * 128 + ((lane & 7) ^ swz(lane >> 3)) * 16;
+  }
+  static __device__ __forceinline__ uint32_t copy_step(uint32_t at, int i) {
+    return i * 512 + (D == 256 && (i & 1) ? at ^ 64 : at);  // lines 4 on: swz of 256-wide rows + 4
+  }
+  // Byte `at` (a multiple of what is read) of row r.
+  static __device__ __forceinline__ uint32_t byte(uint32_t r, uint32_t at) {
+    const uint32_t b = r * (D / 2) + at, line = b >> 7;
+    return line * 128 + (((b >> 4 & 7) ^ swz(line)) * 16) + (b & 15);
+  }
+};
+
 // Shapes of an instance: D, NT tiles of 8 rows, W warps a CTA, SUB 16-key parts
 // a block, S blocks in flight a warp.  One CTA a SM: of two or three, the SM
 // serves the oldest first (with equal shares of the 32 long contexts the first
@@ -203,7 +220,7 @@ struct Kv4Shape {
   static constexpr bool kWide = D * NT >= 256;
   static constexpr int W = kWide ? 12 : 16;
   static constexpr int SUB = kWide ? 1 : 2;
-  static constexpr int S = D == 256 ? 4 : kWide ? 8 : D == 128 ? 3 : 6;
+  static constexpr int S = D == 256 ? 2 : kWide ? 4 : D == 128 ? 2 : 4;
   static constexpr int kBlk = 16 * SUB;
   static constexpr int kRows = 8 * NT;
   static constexpr int KC = D == 256 ? 2 : 1;   // chunks of a K row a lane
@@ -216,8 +233,8 @@ struct Kv4Shape {
   static constexpr int kVOff = 8 * D, kSOff = 16 * D, kPart = 18 * D;
   static constexpr int kStage = SUB * kPart;
   static constexpr int kRing = W * S * kStage;
-  static constexpr int kBytes = kRing;
-  static_assert(W * MT * NT * 512 <= kRing, "the merge meets in the ring");
+  static constexpr int kBytes = kRing > W * MT * NT * 512 ? kRing : W * MT * NT * 512;  // (the merge meets in the ring)
+
   static_assert(kBytes + 2 * W * (16 * kRows + 16) + 1024 <= 228 * 1024, "shared memory of an SM");
   static_assert(kRows <= 16 && 2 * W <= 32 && SUB * S <= 32, "merge and flags");
 };
@@ -227,6 +244,7 @@ __global__ void __launch_bounds__(Sh::W * 32, 1)
 kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
   constexpr int D = Sh::D, NT = Sh::NT, W = Sh::W, S = Sh::S, MT = Sh::MT, SUB = Sh::SUB;
   constexpr int KC = Sh::KC, KG = Sh::KG, KW = Sh::KW, VG = Sh::VG, VW = Sh::VW;
+  using Lay = RowLayout<D>;
   constexpr int kBlk = Sh::kBlk;
   extern __shared__ __align__(128) uint8_t smem[];
   // Per warp up to two pieces of segments it shares with others: one that ends
@@ -306,8 +324,9 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
   next_batch(nxt);
   int32_t bi = 0;          // next block of `cur`
   uint32_t bad_parts = 0;  // bit st * SUB + h: that part has no good page
-  const uint8_t* const k_lane = p.k + g * (D / 2) + c * KG;
-  const uint8_t* const v_lane = p.v + 2 * c * (D / 2) + g * VG;
+  const uint8_t* const k_lane = p.k + lane * 16;
+  const uint8_t* const v_lane = p.v + lane * 16;
+  const uint32_t copy_at = Lay::copy_at(lane);
   constexpr int H = D / 16;  // 16-byte pieces of 16 keys' K (or V) scales
   const uint8_t* const s_lane = (lane < H ? p.ks : p.vs) + (lane & (H - 1)) * 16;
   auto issue = [&](int st) {
@@ -332,15 +351,11 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
         const uint8_t* kp = k_lane + row * (D / 2);
         const uint8_t* vp = v_lane + row * (D / 2);
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int j = 0; j < KC; ++j)
-            copy_async<KG>(d + ((r * KC + j) * 32 + lane) * KG, kp + r * 8 * (D / 2) + j * 4 * KG, ok ? KG : 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          copy_async<VG>(d + Sh::kVOff + (i * 32 + lane) * VG, vp + ((i & 1) + 8 * (i >> 1)) * (D / 2),
-                         ok ? VG : 0);
-        if (lane < 2 * H) copy_async<16>(d + Sh::kSOff + lane * 16, s_lane + row * (D / 16), ok ? 16 : 0);
+        for (int i = 0; i < D / 64; ++i) {  // 512 bytes of K and of V each
+          copy_async(d + Lay::copy_step(copy_at, i), kp + i * 512, ok ? 16 : 0);
+          copy_async(d + Sh::kVOff + Lay::copy_step(copy_at, i), vp + i * 512, ok ? 16 : 0);
+        }
+        if (lane < 2 * H) copy_async(d + Sh::kSOff + lane * 16, s_lane + row * (D / 16), ok ? 16 : 0);
       }
       if (++bi == cur.n) {
         cur = nxt;
@@ -352,6 +367,14 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
   };
 #pragma unroll
   for (int st = 0; st < S; ++st) issue(st);
+
+  // What this lane reads: of K rows g and g + 8 its quarter (KC chunks), of V
+  // its eighth of keys 2c, 2c + 1 and those eight on.
+  uint32_t k_at[KC], v_at[2];
+#pragma unroll
+  for (int j = 0; j < KC; ++j) k_at[j] = Lay::byte(g, (KC * c + j) * KG);
+#pragma unroll
+  for (int b = 0; b < 2; ++b) v_at[b] = Lay::byte(2 * c + b, g * VG);
 
   int st = 0;
   float o[MT][NT][4];
@@ -379,7 +402,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
       for (int w = 0; w < KC * KW; ++w) {
         uint4 u = make_uint4(0, 0, 0, 0);
         if (has)
-          u = __ldg(reinterpret_cast<const uint4*>(p.q + off + (c + 4 * (w / KW)) * (2 * KG) + 8 * (w % KW)));
+          u = __ldg(reinterpret_cast<const uint4*>(p.q + off + (KC * c) * (2 * KG) + 8 * w));
         qf[w][nt][0] = u.x;
         qf[w][nt][1] = u.y;
         qf[w][nt][2] = u.z;
@@ -442,14 +465,14 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
 #pragma unroll
         for (int jc = 0; jc < KC; ++jc) {
           uint32_t ka[KW], kb[KW];
-          lds<KW>(part + (jc * 32 + lane) * KG, ka);
-          lds<KW>(part + ((KC + jc) * 32 + lane) * KG, kb);
+          lds<KW>(part + k_at[jc], ka);
+          lds<KW>(part + k_at[jc] + 4 * D, kb);  // eight rows on
           // Scale bytes of the chunk's 16-dimension blocks (two, or one of
           // 64-dimension rows) in rows g and g + 8.
           uint32_t sa, sb;
           if constexpr (KW == 4) {
-            sa = lds_u16(part + Sh::kSOff + g * (D / 16) + (c + 4 * jc) * 2);
-            sb = lds_u16(part + Sh::kSOff + (g + 8) * (D / 16) + (c + 4 * jc) * 2);
+            sa = lds_u16(part + Sh::kSOff + g * (D / 16) + (KC * c + jc) * 2);
+            sb = lds_u16(part + Sh::kSOff + (g + 8) * (D / 16) + (KC * c + jc) * 2);
           } else {
             sa = lds_u8(part + Sh::kSOff + g * (D / 16) + c);
             sb = lds_u8(part + Sh::kSOff + (g + 8) * (D / 16) + c);
@@ -592,7 +615,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int kk = 2 * c + (i & 1) + 8 * (i >> 1);
-          lds<VW>(part + Sh::kVOff + (i * 32 + lane) * VG, vw[i]);
+          lds<VW>(part + Sh::kVOff + v_at[i & 1] + (i >> 1) * 4 * D, vw[i]);
           if constexpr (D == 256)
             sv[i] = lds_u16(part + Sh::kSOff + D + kk * (D / 16) + 2 * g);
           else

@@ -568,6 +568,12 @@ constexpr int32_t kKv4MaxRows = 32;
 // gets before the batch is cut over more CTAs.
 constexpr int32_t kKv4BlocksPerWarp = 2;
 
+// Cost model of the split-KV part beside a prefill (per row tile of 8): GB/s an
+// SM, GB/s of them all, and its start, merge and combine.
+constexpr double kKv4SmGBs = 60.0;
+constexpr double kKv4HbmGBs = 5000.0;
+constexpr double kKv4FixedUs = 10.0;
+
 // Row tiles, launches and CTA counts of the split-KV part.
 rpa_status_t plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_t* win) {
   const int32_t group = plan.hq / plan.hkv;
@@ -600,7 +606,7 @@ rpa_status_t plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, c
       for (int32_t i = b; i < e; ++i)
         v0.push_back(v0.back() + static_cast<int64_t>(plan.kv4_tiles[i].nb + kKv4SegCost) * plan.hkv);
       const int64_t total = v0.back();
-      const int64_t most = std::min<int64_t>(plan.num_sms, kKv4MaxCtas);
+      const int64_t most = std::min<int64_t>(plan.decode_sms > 0 ? plan.decode_sms : plan.num_sms, kKv4MaxCtas);
       const int64_t n = std::max<int64_t>(
           std::max<int64_t>(1, std::min(most, total / (kKv4BlocksPerWarp * grain.warps))),
           std::min(most, ceil_div(total, 0x3fffffff)));
@@ -633,18 +639,71 @@ rpa_status_t plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, c
   return RPA_OK;
 }
 
+// A mixed batch's two parts side by side, as for 16-bit pages: the split of the
+// SMs that evens their modelled times, where that beats one after the other.
+void split_sms_kv4(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_t* win,
+                   const rpa_plan_options& opts) {
+  const int32_t group = plan.hq / plan.hkv;
+  double dec_bytes = 0, exp_bytes = 0;
+  bool dec = false, pre = false;
+  for (int32_t s = 0; s < plan.num_seqs; ++s) {
+    const int32_t ql = cu[s + 1] - cu[s];
+    if (ql < 1) continue;
+    const int32_t w = win ? win[s] : 0;
+    const int32_t p0 = kv[s] - ql;
+    const int32_t lo = (w > 0 && p0 - (w - 1) > 0) ? p0 - (w - 1) : 0;
+    const double elems = 2.0 * (kv[s] - lo) * plan.hkv * plan.d;
+    if (ql < plan.prefill_min_q) {
+      dec = true;
+      dec_bytes += 0.5625 * elems * static_cast<double>(ceil_div(ql * group, 8));
+    } else {
+      pre = true;
+      exp_bytes += 2.5625 * elems;
+    }
+  }
+  plan.overlap = false;
+  plan.decode_sms = plan.prefill_sms = 0;
+  if (!dec || !pre || opts.decode_sms < 0 || plan.num_sms < 2) return;
+  const int32_t n = plan.num_sms;
+  const TileStats ts = prefill_tile_stats(plan, cu, kv, win,
+                                          opts.q_block > 0 ? opts.q_block : prefill_tokens_per_block(plan.d, group));
+  auto decode_us = [&](int32_t x) {
+    return dec_bytes / std::min(x * kKv4SmGBs, kKv4HbmGBs) * 1e-3 + kKv4FixedUs;
+  };
+  auto prefill_us = [&](int32_t x) {
+    return prefill_cost_us(ts, plan.d, x) + exp_bytes / kDecodeHbmGBs * 1e-3;
+  };
+  int32_t best = 0;
+  double best_t = decode_us(n) + prefill_us(n);
+  for (int32_t x = 1; x < n && opts.decode_sms == 0; ++x) {
+    const double t = std::max(decode_us(x), prefill_us(n - x));
+    if (t < best_t) {
+      best_t = t;
+      best = x;
+    }
+  }
+  if (opts.decode_sms > 0) best = std::min(opts.decode_sms, n - 1);
+  if (best == 0) return;
+  plan.overlap = true;
+  plan.decode_sms = best;
+  plan.prefill_sms = n - best;
+  plan.est_decode_us = static_cast<float>(decode_us(best));
+  plan.est_prefill_us = static_cast<float>(prefill_us(n - best));
+}
+
 rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu, const int32_t* kv,
                                 const int32_t* win, const rpa_plan_options& opts) {
   const int32_t group = plan.hq / plan.hkv;
   if (plan.dtype != RPA_DTYPE_BF16 || opts.path == RPA_PATH_SIMT || plan.p < 16 ||
       !prefill_tc_supported(plan.d, plan.p, group) || opts.kv_split != 0 ||
-      opts.prefill_pairs == 2 || opts.prefill_split > 0 || opts.decode_sms != 0 ||
+      opts.prefill_pairs == 2 || opts.prefill_split > 0 ||
       opts.decode_kernel != 0 || opts.q_block > prefill_tokens_per_block(plan.d, group))
     return RPA_ERR_UNSUPPORTED;
   plan.kv_fp4 = true;
   plan.path = RPA_PATH_TC;
   plan.prefill_min_q = kKv4MaxRows / group + 1;
   plan.num_decode = plan.num_prefill = 0;
+  split_sms_kv4(plan, cu, kv, win, opts);
   if (rpa_status_t st = plan_kv4_decode(plan, cu, kv, win)) return st;
   size_t off = kHeaderBytes;
   auto take = [&](size_t bytes) {

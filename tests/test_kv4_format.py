@@ -92,7 +92,7 @@ def test_plan_reports_its_pages():
 
 def test_plan_refuses_what_4_bit_pages_do_not_take():
     for kw in ({"dtype": binding.RPA_DTYPE_F32}, {"path": binding.RPA_PATH_SIMT}, {"p": 8, "mpps": 13},
-               {"kv_split": 64}, {"decode_sms": 4}, {"decode_sms": -1}, {"decode_kernel": 1},
+               {"kv_split": 64}, {"decode_kernel": 1},
                {"prefill_pairs": 2}, {"prefill_split": 2}, {"q_block": 32},
                {"hq": 256, "hkv": 1}):
         with pytest.raises(RpaError) as e:
