@@ -210,17 +210,20 @@ struct RowLayout {
 // a block, S blocks in flight a warp.  One CTA a SM: of two or three, the SM
 // serves the oldest first (with equal shares of the 32 long contexts the first
 // CTAs of the SMs ended after 112 us, the second after 130 us), while the warps
-// of one CTA end together.  O takes D NT / 4 registers of a thread and Q D NT / 8:
-// up to 48 together leaves 16 warps (128 registers each) and blocks of 32 keys,
+// of one CTA end together.  O takes D NT / 4 registers of a thread and Q D NT / 8.
+// Up to 48 together leaves 16 warps (128 registers each) and blocks of 32 keys,
 // which halve the cost of the loop around the products; 96 (kWide) leaves 12
-// warps and blocks of 16.
+// warps and blocks of 16.  (192 would leave 8: 16 rows of 256 a tile, measured,
+// took as long as two tiles of 8.)
+// Two blocks in flight a warp are enough: more only make the first ones wait
+// (the 32 long contexts took 132.4 us with three, 129.7 us with two).
 template <int D_, int NT_>
 struct Kv4Shape {
   static constexpr int D = D_, NT = NT_;
   static constexpr bool kWide = D * NT >= 256;
   static constexpr int W = kWide ? 12 : 16;
   static constexpr int SUB = kWide ? 1 : 2;
-  static constexpr int S = D == 256 ? 2 : kWide ? 4 : D == 128 ? 2 : 4;
+  static constexpr int S = D == 64 ? 4 : 2;
   static constexpr int kBlk = 16 * SUB;
   static constexpr int kRows = 8 * NT;
   static constexpr int KC = D == 256 ? 2 : 1;   // chunks of a K row a lane
@@ -233,10 +236,10 @@ struct Kv4Shape {
   static constexpr int kVOff = 8 * D, kSOff = 16 * D, kPart = 18 * D;
   static constexpr int kStage = SUB * kPart;
   static constexpr int kRing = W * S * kStage;
-  static constexpr int kBytes = kRing > W * MT * NT * 512 ? kRing : W * MT * NT * 512;  // (the merge meets in the ring)
-
+  static constexpr int kMerge = W * MT * NT * 512;  // the merge meets in the ring
+  static constexpr int kBytes = kRing > kMerge ? kRing : kMerge;
   static_assert(kBytes + 2 * W * (16 * kRows + 16) + 1024 <= 228 * 1024, "shared memory of an SM");
-  static_assert(kRows <= 16 && 2 * W <= 32 && SUB * S <= 32, "merge and flags");
+  static_assert((2 * W * kRows) % 32 == 0 && 2 * W <= 32 && SUB * S <= 32, "merge and flags");
 };
 
 template <typename Sh, int NSEG>
@@ -254,7 +257,6 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
   __shared__ float wm[2 * W][Sh::kRows], wl[2 * W][Sh::kRows];
   __shared__ __align__(8) float s_share[2 * W][Sh::kRows];
   __shared__ float s_lse[2 * W][Sh::kRows];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = lane >> 2, c = lane & 3;
@@ -388,8 +390,9 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
     const Kv4Tile& tl = sc.tile[cs.e];
     const int G = p.group;
     // ---- The tile's queries as B fragments: lane (g, c) holds row g (+ 8 nt)
-    // and the dimensions of its chunks.
-    uint32_t qf[KC * KW][NT][4];
+    // and the dimensions of its chunks, word by word.
+    constexpr int QW = KC * KW;
+    uint32_t qf[QW][NT][4];
     float sc0[NT], sc1[NT];   // logit scales of this lane's columns 2c, 2c + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -397,36 +400,38 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
       const int r = tl.r0 + n;
       const bool has = n < tl.nrows;
       const int64_t off = (static_cast<int64_t>(tl.q0 + r / G) * p.hq + cs.g * G + r % G) * D;
-      uint32_t top = 0;
+      uint4 u[QW];
+      uint32_t top = 0;  // the row's largest magnitude, as bf16 bits
 #pragma unroll
-      for (int w = 0; w < KC * KW; ++w) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (has)
-          u = __ldg(reinterpret_cast<const uint4*>(p.q + off + (KC * c) * (2 * KG) + 8 * w));
-        qf[w][nt][0] = u.x;
-        qf[w][nt][1] = u.y;
-        qf[w][nt][2] = u.z;
-        qf[w][nt][3] = u.w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          top = max(top, qf[w][nt][i] & 0x7fffu);
-          top = max(top, (qf[w][nt][i] >> 16) & 0x7fffu);
-        }
+      for (int w = 0; w < QW; ++w) {
+        u[w] = make_uint4(0, 0, 0, 0);
+        if (has) u[w] = __ldg(reinterpret_cast<const uint4*>(p.q + off + (KC * c) * (2 * KG) + 8 * w));
       }
+#pragma unroll
+      for (int w = 0; w < QW; ++w) {
+        top = __vmaxu2(top, u[w].x & 0x7fff7fffu);
+        top = __vmaxu2(top, u[w].y & 0x7fff7fffu);
+        top = __vmaxu2(top, u[w].z & 0x7fff7fffu);
+        top = __vmaxu2(top, u[w].w & 0x7fff7fffu);
+      }
+      top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^ex: the power of two at or below the row's largest magnitude.
+      // 2^ex: the power of two at or below it.
       uint32_t ex = top >> 7;
       if (ex == 0 || ex == 255) ex = 127;
       ex = min(ex, 253u);
       const float down = __uint_as_float((254u - ex) << 23), up = __uint_as_float(ex << 23);
+      auto half = [&](uint32_t v) {
+        return pack_f16x2(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down);
+      };
 #pragma unroll
-      for (int w = 0; w < KC * KW; ++w)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t u = qf[w][nt][i];
-          qf[w][nt][i] = pack_f16x2(__uint_as_float(u << 16) * down, __uint_as_float(u & 0xffff0000u) * down);
-        }
+      for (int w = 0; w < QW; ++w) {
+        qf[w][nt][0] = half(u[w].x);
+        qf[w][nt][1] = half(u[w].y);
+        qf[w][nt][2] = half(u[w].z);
+        qf[w][nt][3] = half(u[w].w);
+      }
       sc0[nt] = p.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * c);
       sc1[nt] = p.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * c + 4);
     }
@@ -454,9 +459,9 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
 #pragma unroll
       for (int h = 0; h < SUB; ++h) {
         const uint32_t part = src + h * Sh::kPart;
-        // One chain of products per part; a block of one part takes two, so
-        // that the products need not wait for one another.
-        constexpr int CH = SUB == 1 ? 2 : 1;
+        // One chain of products per part and row tile; a block of one part and
+        // one tile takes two, so that the products need not wait for one another.
+        constexpr int CH = SUB * NT == 1 ? 2 : 1;
         float acc[CH][NT][4];
 #pragma unroll
         for (int i = 0; i < CH; ++i)
@@ -490,8 +495,9 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_f16(acc[0][nt], a[0], b[0], a[1], b[1], qf[jc * KW + w][nt][0], qf[jc * KW + w][nt][1]);
-              mma_f16(acc[CH - 1][nt], a[2], b[2], a[3], b[3], qf[jc * KW + w][nt][2], qf[jc * KW + w][nt][3]);
+              const uint32_t (&q)[4] = qf[jc * KW + w][nt];
+              mma_f16(acc[0][nt], a[0], b[0], a[1], b[1], q[0], q[1]);
+              mma_f16(acc[CH - 1][nt], a[2], b[2], a[3], b[3], q[2], q[3]);
             }
           }
         }
@@ -714,6 +720,10 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
   // is free by now.  (Rolled loops: this code runs once a launch, and fetching
   // it, fully unrolled, took longer than running it.)
   copy_wait<0>();
+  // The combine may be scheduled now (it waits for this grid's end).  From the
+  // start on, its waiting CTAs would keep registers that a prefill grid beside
+  // this one needs.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < MT; ++t)
@@ -727,11 +737,11 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
       __match_any_sync(0xffffffffu, my_e < 0 ? -1ll : (static_cast<int64_t>(my_e) << 32) + s_piece[lane].g);
   const uint32_t heads = __ballot_sync(0xffffffffu, my_e >= 0 && __ffs(my_members) - 1 == lane);
   // Thread (i, n): piece i's share of row n, 2^(m_i - M) / sum_k 2^(m_k - M) l_k.
-  static_assert(32 % Sh::kRows == 0, "whole rows a warp");
-  const int pi = min(tid / Sh::kRows, 31), pn = tid % Sh::kRows;
-  uint32_t members = __shfl_sync(0xffffffffu, my_members, pi);
-  if (pi >= 2 * W || __shfl_sync(0xffffffffu, my_e, pi) < 0) members = 0;
-  if (tid < 2 * W * Sh::kRows) {
+#pragma unroll 1
+  for (int it = tid; it < 2 * W * Sh::kRows; it += W * 32) {
+    const int pi = it / Sh::kRows, pn = it % Sh::kRows;
+    const uint32_t members =
+        __shfl_sync(0xffffffffu, my_members, pi) & (__shfl_sync(0xffffffffu, my_e, pi) < 0 ? 0u : ~0u);
     float M = kNoScore, L = 0.f;
 #pragma unroll 8
     for (int k = 0; k < 2 * W; ++k) {
@@ -926,10 +936,12 @@ int launch_kv4_decode(const Plan& plan, const Args& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (const Plan::Kv4Launch& l : plan.kv4_launches) {
     int e = static_cast<int>(cudaErrorInvalidValue);
-    switch (plan.d) {
-      case 64: e = l.nt == 1 ? launch_n<64, 1>(plan, p, l, s) : launch_n<64, 2>(plan, p, l, s); break;
-      case 128: e = l.nt == 1 ? launch_n<128, 1>(plan, p, l, s) : launch_n<128, 2>(plan, p, l, s); break;
-      case 256: e = launch_n<256, 1>(plan, p, l, s); break;
+    switch (plan.d * 8 + l.nt) {
+      case 64 * 8 + 1: e = launch_n<64, 1>(plan, p, l, s); break;
+      case 64 * 8 + 2: e = launch_n<64, 2>(plan, p, l, s); break;
+      case 128 * 8 + 1: e = launch_n<128, 1>(plan, p, l, s); break;
+      case 128 * 8 + 2: e = launch_n<128, 2>(plan, p, l, s); break;
+      case 256 * 8 + 1: e = launch_n<256, 1>(plan, p, l, s); break;
     }
     if (e) return e;
   }

@@ -560,19 +560,117 @@ double prefill_cost_us(const TileStats& t, int32_t head_dim, int32_t sms) {
          kPrefillItemUs256 * f + kPrefillFixedUs;
 }
 
-// 4-bit pages.  A sequence whose q_len x G query rows per KV head number at
-// most kKv4MaxRows runs on the split-KV kernel; the others' visible pages are
-// widened to bf16 and run on the tensor-core prefill.
-constexpr int32_t kKv4MaxRows = 32;
+// 4-bit pages.  Sequences of up to some number of query rows per KV head (q_len
+// x G) run on the split-KV kernel, in tiles of 8 or 16 rows that each widen the
+// keys anew; the others' visible keys are widened to bf16 once and run on the
+// tensor-core prefill, which does not split a sequence's keys over CTAs.  Which
+// is faster depends on the batch (128 sequences of 64 rows over 128-2048 keys of
+// 256: 89 us against 72; 8 of them over 16k-30k keys: 76 us against 459; one of
+// 128 rows over 2016 keys: 15 us against 35), so the number is the one of
+// kKv4RowLimits with the smallest modelled time.
+constexpr int32_t kKv4RowLimits[] = {16, 32, 64, 128};
 // Fewest key blocks (merge charges included) a warp of the split-KV kernel
 // gets before the batch is cut over more CTAs.
 constexpr int32_t kKv4BlocksPerWarp = 2;
 
-// Cost model of the split-KV part beside a prefill (per row tile of 8): GB/s an
-// SM, GB/s of them all, and its start, merge and combine.
-constexpr double kKv4SmGBs = 60.0;
-constexpr double kKv4HbmGBs = 5000.0;
-constexpr double kKv4FixedUs = 10.0;
+// The split-KV kernel's model, fitted to GB300 timings on 12-152 SMs: 4-bit
+// bytes it widens a second on an SM (single tiles of 8 rows, several of them or
+// tiles of 16), bytes from HBM, and its start, merge and combine; and the
+// bandwidth of the widening to bf16.
+constexpr double kKv4OneTileGBs = 39.0;
+constexpr double kKv4TilesGBs = 30.0;
+constexpr double kKv4Tile16GBs = 26.0;
+constexpr double kKv4HbmGBs = 5700.0;
+constexpr double kKv4FixedUs = 18.0;
+constexpr double kKv4ExpandGBs = 5000.0;
+
+// Rows of a split-KV tile: 16 where a sequence has more than 8 and the kernel's
+// registers hold them (head_dim below 256).
+int32_t kv4_tile_rows(const Plan& plan, int32_t rows) { return rows > 8 && plan.d < 256 ? 16 : 8; }
+
+// Modelled work of the two parts for the current prefill_min_q.
+struct Kv4Work {
+  double sm_us = 0;      // split-KV part: microseconds on one SM
+  double hbm_us = 0;     // and of HBM time
+  double expand_us = 0;  // widening for the prefill part
+  bool dec = false, pre = false;
+  TileStats tiles;
+  double decode_us(int32_t sms) const {
+    return dec ? std::max(sm_us / sms, hbm_us) + kKv4FixedUs : 0.0;
+  }
+  double prefill_us(int32_t head_dim, int32_t sms) const {
+    return pre ? prefill_cost_us(tiles, head_dim, sms) + expand_us : 0.0;
+  }
+};
+Kv4Work kv4_work(const Plan& plan, const int32_t* cu, const int32_t* kv, const int32_t* win,
+                 int32_t q_block) {
+  const int32_t group = plan.hq / plan.hkv;
+  Kv4Work k;
+  for (int32_t s = 0; s < plan.num_seqs; ++s) {
+    const int32_t ql = cu[s + 1] - cu[s];
+    if (ql < 1) continue;
+    const int32_t w = win ? win[s] : 0;
+    const int32_t p0 = kv[s] - ql;
+    const int32_t lo = (w > 0 && p0 - (w - 1) > 0) ? p0 - (w - 1) : 0;
+    const double elems = 2.0 * (kv[s] - lo) * plan.hkv * plan.d, bytes = 0.5625 * elems;
+    if (ql < plan.prefill_min_q) {
+      const int32_t rows = ql * group, tile = kv4_tile_rows(plan, rows);
+      const double gbs = tile == 16 ? kKv4Tile16GBs : rows > 8 ? kKv4TilesGBs : kKv4OneTileGBs;
+      k.dec = true;
+      k.sm_us += bytes * static_cast<double>(ceil_div(rows, tile)) / gbs * 1e-3;
+      k.hbm_us += bytes / kKv4HbmGBs * 1e-3;
+    } else {
+      k.pre = true;
+      k.expand_us += (bytes + 2.0 * elems) / kKv4ExpandGBs * 1e-3;
+    }
+  }
+  if (k.pre) k.tiles = prefill_tile_stats(plan, cu, kv, win, q_block);
+  return k;
+}
+
+// The row limit, and a mixed batch's split of the SMs between the two parts, as
+// for 16-bit pages: side by side where the split that evens their modelled
+// times beats one after the other.
+void split_kv4(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_t* win,
+               const rpa_plan_options& opts) {
+  const int32_t group = plan.hq / plan.hkv, n = plan.num_sms;
+  const int32_t q_block = opts.q_block > 0 ? opts.q_block : prefill_tokens_per_block(plan.d, group);
+  Kv4Work best;
+  double best_t = 0;
+  int32_t best_q = 0;
+  for (const int32_t limit : kKv4RowLimits) {
+    plan.prefill_min_q = limit / group + 1;
+    if (plan.prefill_min_q == best_q) continue;
+    const Kv4Work k = kv4_work(plan, cu, kv, win, q_block);
+    const double t = k.decode_us(n) + k.prefill_us(plan.d, n);
+    if (best_q != 0 && t >= best_t) continue;
+    best = k;
+    best_t = t;
+    best_q = plan.prefill_min_q;
+  }
+  plan.prefill_min_q = best_q;
+  plan.overlap = false;
+  plan.decode_sms = plan.prefill_sms = 0;
+  if (!best.dec || !best.pre || opts.decode_sms < 0 || n < 2) return;
+  int32_t x = 0;
+  if (opts.decode_sms > 0) {
+    x = std::min(opts.decode_sms, n - 1);
+  } else {
+    for (int32_t i = 1; i < n; ++i) {
+      const double t = std::max(best.decode_us(i), best.prefill_us(plan.d, n - i));
+      if (t < best_t) {
+        best_t = t;
+        x = i;
+      }
+    }
+  }
+  if (x == 0) return;
+  plan.overlap = true;
+  plan.decode_sms = x;
+  plan.prefill_sms = n - x;
+  plan.est_decode_us = static_cast<float>(best.decode_us(x));
+  plan.est_prefill_us = static_cast<float>(best.prefill_us(plan.d, n - x));
+}
 
 // Row tiles, launches and CTA counts of the split-KV part.
 rpa_status_t plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_t* win) {
@@ -584,10 +682,7 @@ rpa_status_t plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, c
       const int32_t ql = cu[s + 1] - cu[s];
       if (ql < 1 || ql >= plan.prefill_min_q) continue;
       const int32_t rows = ql * group;
-      // Tiles of 16 rows where a sequence has more than 8 and the kernel's
-      // registers hold them (head_dim below 256).
-      const int32_t want = rows > 8 && plan.d < 256 ? 2 : 1;
-      if (want != nt) continue;
+      if (kv4_tile_rows(plan, rows) != 8 * nt) continue;
       ++plan.num_decode;
       const int32_t w = win ? std::max(win[s], 0) : 0;
       const int32_t pos0 = kv[s] - ql;
@@ -639,58 +734,6 @@ rpa_status_t plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, c
   return RPA_OK;
 }
 
-// A mixed batch's two parts side by side, as for 16-bit pages: the split of the
-// SMs that evens their modelled times, where that beats one after the other.
-void split_sms_kv4(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_t* win,
-                   const rpa_plan_options& opts) {
-  const int32_t group = plan.hq / plan.hkv;
-  double dec_bytes = 0, exp_bytes = 0;
-  bool dec = false, pre = false;
-  for (int32_t s = 0; s < plan.num_seqs; ++s) {
-    const int32_t ql = cu[s + 1] - cu[s];
-    if (ql < 1) continue;
-    const int32_t w = win ? win[s] : 0;
-    const int32_t p0 = kv[s] - ql;
-    const int32_t lo = (w > 0 && p0 - (w - 1) > 0) ? p0 - (w - 1) : 0;
-    const double elems = 2.0 * (kv[s] - lo) * plan.hkv * plan.d;
-    if (ql < plan.prefill_min_q) {
-      dec = true;
-      dec_bytes += 0.5625 * elems * static_cast<double>(ceil_div(ql * group, 8));
-    } else {
-      pre = true;
-      exp_bytes += 2.5625 * elems;
-    }
-  }
-  plan.overlap = false;
-  plan.decode_sms = plan.prefill_sms = 0;
-  if (!dec || !pre || opts.decode_sms < 0 || plan.num_sms < 2) return;
-  const int32_t n = plan.num_sms;
-  const TileStats ts = prefill_tile_stats(plan, cu, kv, win,
-                                          opts.q_block > 0 ? opts.q_block : prefill_tokens_per_block(plan.d, group));
-  auto decode_us = [&](int32_t x) {
-    return dec_bytes / std::min(x * kKv4SmGBs, kKv4HbmGBs) * 1e-3 + kKv4FixedUs;
-  };
-  auto prefill_us = [&](int32_t x) {
-    return prefill_cost_us(ts, plan.d, x) + exp_bytes / kDecodeHbmGBs * 1e-3;
-  };
-  int32_t best = 0;
-  double best_t = decode_us(n) + prefill_us(n);
-  for (int32_t x = 1; x < n && opts.decode_sms == 0; ++x) {
-    const double t = std::max(decode_us(x), prefill_us(n - x));
-    if (t < best_t) {
-      best_t = t;
-      best = x;
-    }
-  }
-  if (opts.decode_sms > 0) best = std::min(opts.decode_sms, n - 1);
-  if (best == 0) return;
-  plan.overlap = true;
-  plan.decode_sms = best;
-  plan.prefill_sms = n - best;
-  plan.est_decode_us = static_cast<float>(decode_us(best));
-  plan.est_prefill_us = static_cast<float>(prefill_us(n - best));
-}
-
 rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu, const int32_t* kv,
                                 const int32_t* win, const rpa_plan_options& opts) {
   const int32_t group = plan.hq / plan.hkv;
@@ -701,9 +744,8 @@ rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu, const int32_t* kv
     return RPA_ERR_UNSUPPORTED;
   plan.kv_fp4 = true;
   plan.path = RPA_PATH_TC;
-  plan.prefill_min_q = kKv4MaxRows / group + 1;
   plan.num_decode = plan.num_prefill = 0;
-  split_sms_kv4(plan, cu, kv, win, opts);
+  split_kv4(plan, cu, kv, win, opts);
   if (rpa_status_t st = plan_kv4_decode(plan, cu, kv, win)) return st;
   size_t off = kHeaderBytes;
   auto take = [&](size_t bytes) {
