@@ -762,9 +762,16 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
   const int total = __popc(heads) * kItems;
 #pragma unroll 1
   for (int idx = tid; idx < total; idx += W * 32) {
-    const int k0 = __fns(heads, 0, idx / kItems + 1);  // (the same for the whole warp)
+    uint32_t head_bits = heads;  // (the same for the whole warp)
+    for (int q = idx / kItems; q > 0; --q) head_bits &= head_bits - 1;
+    const int k0 = __ffs(head_bits) - 1;
     const int k1 = 31 - __clz(__shfl_sync(0xffffffffu, my_members, k0));
     const int i = idx % kItems;
+    // Loads from far first.
+    float4 far = make_float4(0.f, 0.f, 0.f, 0.f);
+    if ((k1 & 1) == 0) far = p.piece_o[(static_cast<int64_t>(blockIdx.x) * W + (k1 >> 1)) * kItems + i];
+    const Piece head = s_piece[k0];
+    const Kv4Tile tl = sc.tile[head.e];
     const int mt = (i >> 5) / NT, nt = (i >> 5) % NT;
     // Lane (g, c) holds columns 2c, 2c + 1 of dimensions d, d + 1.
     const int d = g * (D / 8) + 2 * mt, n = 8 * nt + 2 * c;
@@ -778,9 +785,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
     };
 #pragma unroll 4
     for (int k = k0 | 1; k <= k1; k += 2) add(k, mbuf[(k >> 1) * kItems + i]);
-    if ((k1 & 1) == 0) add(k1, p.piece_o[(static_cast<int64_t>(blockIdx.x) * W + (k1 >> 1)) * kItems + i]);
-    const Piece head = s_piece[k0];
-    const Kv4Tile& tl = sc.tile[head.e];
+    if ((k1 & 1) == 0) add(k1, far);
     if (head.j0 == 0 && s_piece[k1].j1 == tl.nb) {
       const int r = tl.r0 + n;
       __nv_bfloat16* const col = p.out + static_cast<int64_t>(head.g * p.group) * D + d;
@@ -826,8 +831,18 @@ kv4_combine_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc)
     auto slot = [&](int k) {
       return static_cast<int64_t>(2 * (b - 1 + k) + (k == 0 && !same ? 1 : 0)) * ROWS + n;
     };
-    float M = -INFINITY;
-    for (int k = lane; k < parts; k += 32) M = fmaxf(M, p.part_lse[slot(k)]);
+    // The first parts' rows are on their way while the log-sum-exps come.
+    constexpr int kAhead = 4;
+    float2 first[kAhead][E / 2];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        first[k][e / 2] = k < parts ? *reinterpret_cast<const float2*>(p.part_o + slot(k) * D + lane * E + e)
+                                    : make_float2(0.f, 0.f);
+    const float lse0 = lane < parts ? p.part_lse[slot(lane)] : -INFINITY;
+    float M = lse0;
+    for (int k = lane + 32; k < parts; k += 32) M = fmaxf(M, p.part_lse[slot(k)]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float acc[E], wsum = 0.f;
@@ -835,21 +850,28 @@ kv4_combine_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc)
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     for (int k0 = 0; k0 < parts; k0 += 32) {
       const int nk = min(32, parts - k0);
-      float w_l = 0.f;
-      if (lane < nk) {
-        const float lse = p.part_lse[slot(k0 + lane)];
-        w_l = lse == -INFINITY ? 0.f : fast_exp2(lse - M);
-      }
-      for (int k = 0; k < nk; ++k) {
+      const float lse = k0 == 0 ? lse0 : lane < nk ? p.part_lse[slot(k0 + lane)] : -INFINITY;
+      const float w_l = lse == -INFINITY ? 0.f : fast_exp2(lse - M);
+      auto add = [&](int k, const float2* row) {
         const float w = __shfl_sync(0xffffffffu, w_l, k);
         wsum += w;
-        const float* src = p.part_o + slot(k0 + k) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
-          const float2 v = *reinterpret_cast<const float2*>(src + e);
-          acc[e] = fmaf(w, v.x, acc[e]);
-          acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
+          acc[e] = fmaf(w, row[e / 2].x, acc[e]);
+          acc[e + 1] = fmaf(w, row[e / 2].y, acc[e + 1]);
         }
+      };
+      if (k0 == 0) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (k < nk) add(k, first[k]);
+      }
+      for (int k = k0 == 0 ? kAhead : 0; k < nk; ++k) {
+        float2 row[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+          row[e / 2] = *reinterpret_cast<const float2*>(p.part_o + slot(k0 + k) * D + lane * E + e);
+        add(k, row);
       }
     }
     const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
