@@ -210,19 +210,21 @@ struct RowLayout {
 // a block, S blocks in flight a warp.  One CTA a SM: of two or three, the SM
 // serves the oldest first (with equal shares of the 32 long contexts the first
 // CTAs of the SMs ended after 112 us, the second after 130 us), while the warps
-// of one CTA end together.  O takes D NT / 4 registers of a thread and Q D NT / 8.
-// Up to 48 together leaves 16 warps (128 registers each) and blocks of 32 keys,
-// which halve the cost of the loop around the products; 96 (kWide) leaves 12
-// warps and blocks of 16.  (192 would leave 8: 16 rows of 256 a tile, measured,
-// took as long as two tiles of 8.)
+// of one CTA end together.  O takes D NT / 4 registers of a thread and Q D NT / 8;
+// blocks of 32 keys halve the cost of the loop around the products and give a
+// warp two independent chains of them.  Measured (warps x keys a block, each
+// with the registers it leaves): 256 dimensions 8 x 32 6.35 TB/s of 4-bit pages
+// over 152 contexts of 16k, 12 x 16 6.02, 16 x 16 6.16 with spills, 12 x 32
+// spills; 128 dimensions 12 x 32 5.80 over 32 long contexts, 16 x 32 5.75,
+// 16 x 16 5.29; 10 or 14 warps, which the four schedulers cannot share evenly,
+// 5 to 11% below their neighbours.
 // Two blocks in flight a warp are enough: more only make the first ones wait
 // (the 32 long contexts took 132.4 us with three, 129.7 us with two).
 template <int D_, int NT_>
 struct Kv4Shape {
   static constexpr int D = D_, NT = NT_;
-  static constexpr bool kWide = D * NT >= 256;
-  static constexpr int W = kWide ? 12 : 16;
-  static constexpr int SUB = kWide ? 1 : 2;
+  static constexpr int W = D == 256 ? 8 : D == 128 ? 12 : 16;
+  static constexpr int SUB = D * NT == 256 && NT > 1 ? 1 : 2;
   static constexpr int S = D == 64 ? 4 : 2;
   static constexpr int kBlk = 16 * SUB;
   static constexpr int kRows = 8 * NT;
@@ -928,9 +930,13 @@ int launch_n(const Plan& plan, const Kv4Params& p, const Plan::Kv4Launch& l, cud
 }  // namespace
 
 Kv4Grain kv4_grain(int32_t head_dim, int32_t nt) {
-  using Narrow = Kv4Shape<128, 1>;
-  using Wide = Kv4Shape<256, 1>;
-  return head_dim * nt >= 256 ? Kv4Grain{Wide::W, Wide::kBlk} : Kv4Grain{Narrow::W, Narrow::kBlk};
+  switch (head_dim * 8 + nt) {
+    case 64 * 8 + 1: return {Kv4Shape<64, 1>::W, Kv4Shape<64, 1>::kBlk};
+    case 64 * 8 + 2: return {Kv4Shape<64, 2>::W, Kv4Shape<64, 2>::kBlk};
+    case 128 * 8 + 1: return {Kv4Shape<128, 1>::W, Kv4Shape<128, 1>::kBlk};
+    case 128 * 8 + 2: return {Kv4Shape<128, 2>::W, Kv4Shape<128, 2>::kBlk};
+    default: return {Kv4Shape<256, 1>::W, Kv4Shape<256, 1>::kBlk};
+  }
 }
 
 int launch_kv4_decode(const Plan& plan, const Args& a, void* stream) {

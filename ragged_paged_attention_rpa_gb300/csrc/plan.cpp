@@ -577,7 +577,7 @@ constexpr int32_t kKv4BlocksPerWarp = 2;
 // bytes it widens a second on an SM (single tiles of 8 rows, several of them or
 // tiles of 16), bytes from HBM, and its start, merge and combine; and the
 // bandwidth of the widening to bf16.
-constexpr double kKv4OneTileGBs = 39.0;
+constexpr double kKv4OneTileGBs = 34.0;
 constexpr double kKv4TilesGBs = 30.0;
 constexpr double kKv4Tile16GBs = 26.0;
 constexpr double kKv4HbmGBs = 5700.0;
