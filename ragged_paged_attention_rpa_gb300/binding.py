@@ -436,6 +436,8 @@ def _addr(t, name, dtype, dev):
 
 def _workspace(workspace, dev, least=256):
     """Address and size in bytes of a workspace tensor of any dtype."""
+    if workspace is None:
+        raise TypeError("workspace must be a CUDA tensor")
     n = workspace.nbytes
     if n < least:
         raise ValueError("workspace must hold at least %d bytes" % least)

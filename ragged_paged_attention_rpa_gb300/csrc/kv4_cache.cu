@@ -20,7 +20,7 @@
 namespace rpa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct Kv4CacheParams {
   const void* k_rows;  // the read's are written

@@ -216,7 +216,8 @@ struct RowLayout {
 // with the registers it leaves): 256 dimensions 8 x 32 6.35 TB/s of 4-bit pages
 // over 152 contexts of 16k, 12 x 16 6.02, 16 x 16 6.16 with spills, 12 x 32
 // spills; 128 dimensions 12 x 32 5.80 over 32 long contexts, 16 x 32 5.75,
-// 16 x 16 5.29; 10 or 14 warps, which the four schedulers cannot share evenly,
+// 16 x 16 5.29; 64 dimensions 16 x 64 4.60 over 64 long contexts, 16 x 32 4.22;
+// 10 or 14 warps, which the four schedulers cannot share evenly,
 // 5 to 11% below their neighbours.
 // Two blocks in flight a warp are enough: more only make the first ones wait
 // (the 32 long contexts took 132.4 us with three, 129.7 us with two).
@@ -224,8 +225,8 @@ template <int D_, int NT_>
 struct Kv4Shape {
   static constexpr int D = D_, NT = NT_;
   static constexpr int W = D == 256 ? 8 : D == 128 ? 12 : 16;
-  static constexpr int SUB = D * NT == 256 && NT > 1 ? 1 : 2;
-  static constexpr int S = D == 64 ? 4 : 2;
+  static constexpr int SUB = D * NT == 64 ? 4 : D == 128 && NT == 2 ? 1 : 2;
+  static constexpr int S = 2;
   static constexpr int kBlk = 16 * SUB;
   static constexpr int kRows = 8 * NT;
   static constexpr int KC = D == 256 ? 2 : 1;   // chunks of a K row a lane
@@ -282,7 +283,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
   struct Batch {
     int32_t n, blk;        // blocks; the first one
     int32_t g, seq, lo, hi;  // KV head, sequence, keys the tile sees
-    int32_t page[2];       // (lane) page of the block's first and, where pages are 16 keys, second part
+    int32_t page[SUB];     // (lane) pages of the block's parts
   };
   Place bs = cs;          // where the next batch comes from
   int32_t bj = bs.j;
@@ -303,17 +304,18 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
     b.seq = t.seq;
     b.lo = first_visible(t.pos0 + t.r0 / p.group, t.window);
     b.hi = t.pos0 + (t.r0 + t.nrows - 1) / p.group;
-    b.page[0] = b.page[1] = -1;
     if (lane < b.n) {
       const int32_t key = (b.blk + lane) * kBlk;
       const int32_t* row = p.page_table + static_cast<int64_t>(t.seq) * p.mpps;
-      // Parts no row of the tile sees are not looked up (-2).
+      // One page holds the block, or each part is looked up for itself; then
+      // those that no row of the tile sees are not (-2).
 #pragma unroll
       for (int h = 0; h < SUB; ++h) {
         const int32_t k0 = key + 16 * h;
-        if (h > 0 && p.page_shift > 4) {
+        const bool one_page = (1 << p.page_shift) >= kBlk;
+        if (h > 0 && one_page) {
           b.page[h] = b.page[0];
-        } else if (k0 > b.hi || (p.page_shift == 4 && k0 + 15 < b.lo)) {
+        } else if (!one_page && (k0 > b.hi || k0 + 15 < b.lo)) {
           b.page[h] = -2;
         } else {
           const int32_t slot = k0 >> p.page_shift;

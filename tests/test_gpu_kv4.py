@@ -136,6 +136,110 @@ def test_slots_outside_the_pool_set_the_error_word():
     assert bool((out[0] == 66 / 64).all()) and bool((out[1:] == 0).all())
 
 
+def test_rows_on_16_byte_boundaries():
+    """Rows that start 16 but not 32 bytes into a line, written and read."""
+    t, hkv, d, p = 9, 3, 64, 16
+    for bf16 in (True, False):
+        k, v = rows((t, hkv, d), 31, bf16), rows((t, hkv, d), 32, bf16)
+        skip = 8 if bf16 else 4
+        def off(x):
+            flat = torch.zeros(x.numel() + skip, dtype=x.dtype, device="cuda")
+            y = flat[skip:].view(x.shape)
+            y.copy_(x)
+            assert y.data_ptr() % 32 == 16
+            return y
+        pool = pools(2, hkv, p, d)
+        slots = cuda(np.arange(t, dtype=np.int64) * 3)
+        binding.rpa_write_kv4(off(k), off(v), *pool, slots)
+        ko, vo = off(torch.zeros_like(k)), off(torch.zeros_like(v))
+        binding.rpa_read_kv4(*pool, slots, ko, vo)
+        for x, y in ((k, ko), (v, vo)):
+            want = oracle.decode_kv4(*workloads.kv4_encode(x.float().numpy()))
+            assert np.array_equal(y.float().cpu().numpy(), want)
+
+
+def test_a_pool_beyond_four_gigabytes():
+    """Slots whose byte offsets pass 2^32 (codes) and 2^31 (scales): written,
+    read back and attended, by the split-KV kernel and through the prefill."""
+    hkv, d, p, n = 2, 256, 256, 70000                 # 4.6 GB of codes each, 0.6 GB of scales
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    pool = [torch.empty((n, hkv, p, last), dtype=torch.uint8, device="cuda") for last in (128, 128, 16, 16)]
+    t = 300
+    k, v, q = (torch.from_numpy(np.random.default_rng(i).standard_normal((t, h, d)).astype(np.float32)).to(torch.bfloat16)
+               for i, h in ((1, hkv), (2, hkv), (3, 4)))
+    table = np.array([[n - 1, n - 3]], np.int32)
+    pos = np.arange(t)
+    slots = cuda(table[0, pos // p].astype(np.int64) * p + pos % p)
+    binding.rpa_write_kv4(k.cuda(), v.cuda(), *pool, slots)
+    ko, vo = torch.empty_like(k, device="cuda"), torch.empty_like(v, device="cuda")
+    binding.rpa_read_kv4(*pool, slots, ko, vo)
+    held = [oracle.decode_kv4(*workloads.kv4_encode(x.float().numpy())).astype(np.float64) for x in (k, v)]
+    assert np.array_equal(ko.float().cpu().numpy(), held[0]) and np.array_equal(vo.float().cpu().numpy(), held[1])
+    for new in (1, t):
+        cu = np.array([0, new], np.int32)
+        plan = binding.rpa_plan(cu, np.array([t], np.int32), None, 4, hkv, d, p, 2, n, kv_dtype=binding.RPA_DTYPE_FP4_E2M1)
+        ws = binding.alloc_workspace(plan)
+        out = torch.empty((new, 4, d), dtype=torch.bfloat16, device="cuda")
+        binding.rpa_forward_kv4(q[t - new:].cuda(), *pool, cuda(table), cuda(cu), cuda(np.array([t], np.int32)), None,
+                                d ** -0.5, out, plan, ws)
+        assert binding.rpa_get_device_error(ws) == 0
+        got = out.float().cpu().numpy()
+        for i in range(0, new, 37):
+            m = t - new + i + 1
+            for h in range(4):
+                x = held[0][:m, h // 2] @ q[t - new + i, h].double().numpy() * d ** -0.5
+                w = np.exp(x - x.max())
+                w /= w.sum()
+                ref, mag = w @ held[1][:m, h // 2], w @ np.abs(held[1][:m, h // 2])
+                assert (np.abs(got[i, h] - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7.9 * mag).all()
+
+
+def test_refusals_of_the_binding():
+    pool = pools(4, 2, 16, 64)
+    k = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device="cuda")
+    slots = cuda(np.arange(3, dtype=np.int64))
+    write = binding.rpa_write_kv4
+    with pytest.raises(TypeError):
+        write(k.half(), k.half(), *pool, slots)
+    with pytest.raises(TypeError):
+        write(k, k.float(), *pool, slots)
+    with pytest.raises(TypeError):
+        write(k, k, *pool, slots.int())
+    with pytest.raises(TypeError):
+        write(k.cpu(), k, *pool, slots)
+    with pytest.raises(TypeError):
+        write(k, k, pool[0].char(), *pool[1:], slots)
+    with pytest.raises(ValueError):
+        write(k[:2], k, *pool, slots)
+    with pytest.raises(ValueError):
+        write(k, k, pool[0], pool[1][:3], *pool[2:], slots)
+    with pytest.raises(ValueError):
+        write(k, k, *pool[:2], pool[2][..., :2], pool[3], slots)
+    with pytest.raises(ValueError):
+        write(k.transpose(0, 1).contiguous().transpose(0, 1), k, *pool, slots)
+    with pytest.raises(ValueError):
+        write(k, k, *pool, slots, torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    b = batch([1], [40], 4, 2, 64, 16, seed=3)
+    r = Kv4Batch(b)
+    with pytest.raises(TypeError):
+        r.ws = None
+        r.call()
+    r = Kv4Batch(b)
+    r.pool = pools(4, 1, 16, 64)
+    with pytest.raises(ValueError):
+        r.call()
+
+
+def test_trace_names_the_kernels():
+    b = batch([1] * 4 + [200], [3000, 40, 50, 60, 300], 8, 2, 128, 16, seed=4)
+    r = Kv4Batch(b, decode_sms=-1)
+    binding.rpa_trace_begin(16)
+    r.call()
+    names = [n for n, _ in binding.rpa_trace_end()]
+    assert names == ["kv4_decode", "kv4_combine", "kv4_expand", "prefill_tc"]
+
+
 # ---------------------------------------------------------------- attention
 
 def batch(ql, kv, hq, hkv, d, p, win=None, seed=0, **kw):
@@ -320,6 +424,31 @@ def test_bad_pages_and_lengths(ql):
     ok = r.call()
     assert binding.rpa_get_device_error(r.ws) == 0
     check(b, ok)
+
+
+@pytest.mark.parametrize("sms", [-1, 20])
+def test_mixed_batches_side_by_side_and_after_another(sms):
+    """The two parts on disjoint SMs or one after the other, and a workspace whose
+    scratch holds NaN bytes: the same bound, and the same bits twice."""
+    b = batch([1] * 30 + [300, 150], [40 + 97 * i % 1500 for i in range(30)] + [700, 151], 8, 2, 128, 16,
+              [0, 200] * 16, seed=61)
+    r = Kv4Batch(b, decode_sms=sms)
+    assert r.plan.info()["decode_sms"] == max(0, sms)
+    r.ws[256:] = 0xFF
+    out = r.call().clone()
+    assert binding.rpa_get_device_error(r.ws) == 0
+    check(b, out)
+    assert torch.equal(r.call(), out)
+
+
+def test_a_launch_holds_so_many_tiles():
+    """More row tiles than one launch's parameters carry (864): several launches."""
+    kv = [1 + 13 * i % 90 for i in range(1000)]
+    b = batch([1] * 1000, kv, 4, 2, 64, 16, seed=62)
+    r = Kv4Batch(b)
+    out = r.call()
+    assert binding.rpa_get_device_error(r.ws) == 0
+    check(b, out, prefill=False)
 
 
 def test_rows_behind_the_last_sequence_stay():
