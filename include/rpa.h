@@ -139,7 +139,7 @@ typedef struct rpa_plan_options {
                                page_size >= 16, num_q_heads / num_kv_heads <=
                                128, run through rpa_forward_kv4 (of the other
                                options it takes path AUTO or TC, q_block of one
-                               tile, num_sms, prefill_dynamic and
+                               tile, num_sms, decode_sms, prefill_dynamic and
                                prefill_grouping; the rest must be 0, else
                                RPA_ERR_UNSUPPORTED)                             */
   int32_t prefill_split;    /* 0 or -1: whole prefill work items; n > 0: lay

@@ -6,6 +6,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <functional>
 #include <mutex>
 #include <new>
@@ -33,7 +34,9 @@ bool log_plans() {
 }
 
 void log_plan(const rpa::Plan& p) {
+  const rpa::Plan& f = p.kv4_prefill ? *p.kv4_prefill : p;  // the prefill's plan
   int64_t cuts = static_cast<int64_t>(p.dcut.size());
+  for (const rpa::Plan::Kv4Launch& l : p.kv4_launches) cuts += l.cut ? l.n_ctas - 1 : 0;
   std::fprintf(stderr,
                "librpa plan: %d seqs (%d decode, %d prefill), %s path; decode: %d launch(es), "
                "%lld CTAs, longest range %d tokens, %lld cut sequences; prefill: %zu items on "
@@ -41,9 +44,10 @@ void log_plan(const rpa::Plan& p) {
                "bytes\n",
                p.num_seqs, p.num_decode, p.num_prefill,
                p.path == RPA_PATH_TC ? "tensor-core" : "CUDA-core",
-               static_cast<int>(p.dlaunch.size()), static_cast<long long>(p.decode_ctas),
-               p.kv_split, static_cast<long long>(cuts), p.items.size(), p.prefill_ctas,
-               p.q_block, p.prefill_max_tiles, p.n_split_items, p.ws_bytes);
+               static_cast<int>(p.dlaunch.size() + p.kv4_launches.size()),
+               static_cast<long long>(p.decode_ctas), p.kv_split, static_cast<long long>(cuts),
+               f.items.size(), f.prefill_ctas, f.q_block, f.prefill_max_tiles, f.n_split_items,
+               p.ws_bytes);
 }
 
 bool aligned(const void* ptr, uintptr_t a) {
@@ -119,7 +123,13 @@ rpa_status_t rpa_plan(rpa_plan_t** plan, const int32_t* cu_q_lens_host,
   int32_t sms = o.num_sms;
   if (sms == 0) sms = device_sm_count();
   p.num_sms = sms > 0 ? sms : 152;
-  st = rpa::build_schedule(p, cu_q_lens_host, kv_lens_host, window_host, o);
+  try {
+    st = o.kv_dtype == RPA_DTYPE_FP4_E2M1
+             ? rpa::build_kv4_schedule(p, cu_q_lens_host, kv_lens_host, window_host, o)
+             : rpa::build_schedule(p, cu_q_lens_host, kv_lens_host, window_host, o);
+  } catch (const std::exception&) {  // out of host memory
+    st = RPA_ERR_INVALID_ARG;
+  }
   if (st != RPA_OK) {
     delete pl;
     return st;
@@ -141,22 +151,23 @@ rpa_status_t rpa_plan_get_info(const rpa_plan_t* plan, rpa_plan_info* info) {
   info->path = p.path;
   info->num_decode_seqs = p.num_decode;
   info->num_prefill_seqs = p.num_prefill;
+  const rpa::Plan& f = p.kv4_prefill ? *p.kv4_prefill : p;  // the prefill's plan
   // Query tokens per work item: on SM pairs each CTA holds half of them.
-  info->q_block = p.prefill_pairs ? 2 * p.q_block : p.q_block;
+  info->q_block = f.prefill_pairs ? 2 * f.q_block : f.q_block;
   info->kv_split = p.kv_split;
   info->max_splits = p.max_splits;
-  info->num_prefill_items = static_cast<int32_t>(p.items.size());
-  info->prefill_ctas = p.prefill_ctas;
+  info->num_prefill_items = static_cast<int32_t>(f.items.size());
+  info->prefill_ctas = f.prefill_ctas;
   info->workspace_bytes = static_cast<int64_t>(p.ws_bytes);
   info->prefill_pairs = p.prefill_pairs ? 1 : 0;
   info->kv_dtype = p.kv_fp4 ? RPA_DTYPE_FP4_E2M1 : p.kv_fp8 ? RPA_DTYPE_FP8_E4M3 : p.dtype;
   info->prefill_split_items = static_cast<int32_t>(p.psplit.size());
   info->prefill_split_parts = p.n_split_items;
-  info->prefill_max_tiles = p.prefill_max_tiles;
+  info->prefill_max_tiles = f.prefill_max_tiles;
   info->decode_sms = p.overlap ? p.decode_sms : 0;
   info->prefill_sms = p.overlap ? p.prefill_sms : 0;
-  info->prefill_dynamic = p.prefill_dynamic ? 1 : 0;
-  info->prefill_groups = p.prefill_groups;
+  info->prefill_dynamic = f.prefill_dynamic ? 1 : 0;
+  info->prefill_groups = f.prefill_groups;
   info->decode_kernel = (p.num_decode > 0 && !p.simt_decode && !p.kv_fp4)
                             ? (p.decode_tc ? RPA_DECODE_KERNEL_TC : RPA_DECODE_KERNEL_MMA)
                             : 0;
@@ -608,13 +619,12 @@ rpa_status_t rpa_forward_kv4(const void* q, const uint8_t* k_pages, const uint8_
     b.k_pages = a.workspace + p.off_kv4_k;
     b.v_pages = a.workspace + p.off_kv4_v;
     b.page_table = reinterpret_cast<const int32_t*>(a.workspace + p.off_kv4_table);
-    b.pool_pages = p.kv4_scratch_pages;
-    return rpa::launch_prefill_tc(p, b, s);
+    return rpa::launch_prefill_tc(*p.kv4_prefill, b, s);
   };
   if (p.overlap) return side_by_side(stream, decode, prefill);
   int err = 0;
   if (!p.kv4_launches.empty() && (err = decode(stream)) != 0) return cuda_failed(err);
-  if (!p.items.empty() && (err = prefill(stream)) != 0) return cuda_failed(err);
+  if (p.kv4_prefill && (err = prefill(stream)) != 0) return cuda_failed(err);
   return RPA_OK;
 }
 

@@ -283,7 +283,7 @@ void plan_prefill(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_
   std::vector<Cost> all;
   for (int32_t s = 0; s < plan.num_seqs; ++s) {
     const int32_t ql = cu[s + 1] - cu[s];
-    if (ql < plan.prefill_min_q) continue;
+    if (ql <= 1) continue;
     const int32_t L = kv[s];
     const int32_t w = win ? win[s] : 0;
     const int64_t span = plan.prefill_pairs ? 2 * qb : qb;   // query tokens per item
@@ -447,7 +447,7 @@ void plan_prefill(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_
       double total = 0;
       bool whole_prefix = true;
       for (int32_t sq = 0; sq < plan.num_seqs; ++sq) {
-        if (cu[sq + 1] - cu[sq] < plan.prefill_min_q) continue;
+        if (cu[sq + 1] - cu[sq] <= 1) continue;
         total += static_cast<double>(kv[sq]) * plan.d * 2.0 * 2.0 * plan.hkv;
         const int32_t w = win ? win[sq] : 0;
         if (w > 0 && w < kv[sq]) whole_prefix = false;
@@ -456,7 +456,7 @@ void plan_prefill(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_
       std::vector<int32_t> gid(static_cast<size_t>(plan.num_seqs) * plan.hkv, 0);
       double acc = 0;
       for (int32_t sq = 0; sq < plan.num_seqs; ++sq) {
-        if (cu[sq + 1] - cu[sq] < plan.prefill_min_q) continue;
+        if (cu[sq + 1] - cu[sq] <= 1) continue;
         for (int32_t h = 0; h < plan.hkv; ++h) {
           gid[static_cast<size_t>(sq) * plan.hkv + h] =
               std::min(ngroups - 1, static_cast<int32_t>(acc * ngroups / total));
@@ -513,7 +513,7 @@ TileStats prefill_tile_stats(const Plan& plan, const int32_t* cu, const int32_t*
   TileStats t;
   for (int32_t s = 0; s < plan.num_seqs; ++s) {
     const int32_t ql = cu[s + 1] - cu[s];
-    if (ql < plan.prefill_min_q) continue;
+    if (ql <= 1) continue;
     const int32_t L = kv[s];
     const int32_t w = win ? win[s] : 0;
     for (int64_t b = 0; b < ceil_div(ql, span); ++b) {
@@ -560,237 +560,11 @@ double prefill_cost_us(const TileStats& t, int32_t head_dim, int32_t sms) {
          kPrefillItemUs256 * f + kPrefillFixedUs;
 }
 
-// 4-bit pages.  Sequences of up to some number of query rows per KV head (q_len
-// x G) run on the split-KV kernel, in tiles of 8 or 16 rows that each widen the
-// keys anew; the others' visible keys are widened to bf16 once and run on the
-// tensor-core prefill, which does not split a sequence's keys over CTAs.  Which
-// is faster depends on the batch (128 sequences of 64 rows over 128-2048 keys of
-// 256: 89 us against 72; 8 of them over 16k-30k keys: 76 us against 459; one of
-// 128 rows over 2016 keys: 15 us against 35), so the number is the one of
-// kKv4RowLimits with the smallest modelled time.
-constexpr int32_t kKv4RowLimits[] = {16, 32, 64, 128};
-// Fewest key blocks (merge charges included) a warp of the split-KV kernel
-// gets before the batch is cut over more CTAs.
-constexpr int32_t kKv4BlocksPerWarp = 2;
-
-// The split-KV kernel's model, fitted to GB300 timings on 12-152 SMs: 4-bit
-// bytes it widens a second on an SM (single tiles of 8 rows, several of them or
-// tiles of 16), bytes from HBM, and its start, merge and combine; and the
-// bandwidth of the widening to bf16.
-constexpr double kKv4OneTileGBs = 34.0;
-constexpr double kKv4TilesGBs = 30.0;
-constexpr double kKv4Tile16GBs = 26.0;
-constexpr double kKv4HbmGBs = 5700.0;
-constexpr double kKv4FixedUs = 18.0;
-constexpr double kKv4ExpandGBs = 5000.0;
-
-// Rows of a split-KV tile: 16 where a sequence has more than 8 and the kernel's
-// registers hold them (head_dim below 256).
-int32_t kv4_tile_rows(const Plan& plan, int32_t rows) { return rows > 8 && plan.d < 256 ? 16 : 8; }
-
-// Modelled work of the two parts for the current prefill_min_q.
-struct Kv4Work {
-  double sm_us = 0;      // split-KV part: microseconds on one SM
-  double hbm_us = 0;     // and of HBM time
-  double expand_us = 0;  // widening for the prefill part
-  bool dec = false, pre = false;
-  TileStats tiles;
-  double decode_us(int32_t sms) const {
-    return dec ? std::max(sm_us / sms, hbm_us) + kKv4FixedUs : 0.0;
-  }
-  double prefill_us(int32_t head_dim, int32_t sms) const {
-    return pre ? prefill_cost_us(tiles, head_dim, sms) + expand_us : 0.0;
-  }
-};
-Kv4Work kv4_work(const Plan& plan, const int32_t* cu, const int32_t* kv, const int32_t* win,
-                 int32_t q_block) {
-  const int32_t group = plan.hq / plan.hkv;
-  Kv4Work k;
-  for (int32_t s = 0; s < plan.num_seqs; ++s) {
-    const int32_t ql = cu[s + 1] - cu[s];
-    if (ql < 1) continue;
-    const int32_t w = win ? win[s] : 0;
-    const int32_t p0 = kv[s] - ql;
-    const int32_t lo = (w > 0 && p0 - (w - 1) > 0) ? p0 - (w - 1) : 0;
-    const double elems = 2.0 * (kv[s] - lo) * plan.hkv * plan.d, bytes = 0.5625 * elems;
-    if (ql < plan.prefill_min_q) {
-      const int32_t rows = ql * group, tile = kv4_tile_rows(plan, rows);
-      const double gbs = tile == 16 ? kKv4Tile16GBs : rows > 8 ? kKv4TilesGBs : kKv4OneTileGBs;
-      k.dec = true;
-      k.sm_us += bytes * static_cast<double>(ceil_div(rows, tile)) / gbs * 1e-3;
-      k.hbm_us += bytes / kKv4HbmGBs * 1e-3;
-    } else {
-      k.pre = true;
-      k.expand_us += (bytes + 2.0 * elems) / kKv4ExpandGBs * 1e-3;
-    }
-  }
-  if (k.pre) k.tiles = prefill_tile_stats(plan, cu, kv, win, q_block);
-  return k;
-}
-
-// The row limit, and a mixed batch's split of the SMs between the two parts, as
-// for 16-bit pages: side by side where the split that evens their modelled
-// times beats one after the other.
-void split_kv4(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_t* win,
-               const rpa_plan_options& opts) {
-  const int32_t group = plan.hq / plan.hkv, n = plan.num_sms;
-  const int32_t q_block = opts.q_block > 0 ? opts.q_block : prefill_tokens_per_block(plan.d, group);
-  Kv4Work best;
-  double best_t = 0;
-  int32_t best_q = 0;
-  for (const int32_t limit : kKv4RowLimits) {
-    plan.prefill_min_q = limit / group + 1;
-    if (plan.prefill_min_q == best_q) continue;
-    const Kv4Work k = kv4_work(plan, cu, kv, win, q_block);
-    const double t = k.decode_us(n) + k.prefill_us(plan.d, n);
-    if (best_q != 0 && t >= best_t) continue;
-    best = k;
-    best_t = t;
-    best_q = plan.prefill_min_q;
-  }
-  plan.prefill_min_q = best_q;
-  plan.overlap = false;
-  plan.decode_sms = plan.prefill_sms = 0;
-  if (!best.dec || !best.pre || opts.decode_sms < 0 || n < 2) return;
-  int32_t x = 0;
-  if (opts.decode_sms > 0) {
-    x = std::min(opts.decode_sms, n - 1);
-  } else {
-    for (int32_t i = 1; i < n; ++i) {
-      const double t = std::max(best.decode_us(i), best.prefill_us(plan.d, n - i));
-      if (t < best_t) {
-        best_t = t;
-        x = i;
-      }
-    }
-  }
-  if (x == 0) return;
-  plan.overlap = true;
-  plan.decode_sms = x;
-  plan.prefill_sms = n - x;
-  plan.est_decode_us = static_cast<float>(best.decode_us(x));
-  plan.est_prefill_us = static_cast<float>(best.prefill_us(plan.d, n - x));
-}
-
-// Row tiles, launches and CTA counts of the split-KV part.
-rpa_status_t plan_kv4_decode(Plan& plan, const int32_t* cu, const int32_t* kv, const int32_t* win) {
-  const int32_t group = plan.hq / plan.hkv;
-  for (int32_t nt = 1; nt <= 2; ++nt) {
-    const Kv4Grain grain = kv4_grain(plan.d, nt);
-    const int32_t first = static_cast<int32_t>(plan.kv4_tiles.size());
-    for (int32_t s = 0; s < plan.num_seqs; ++s) {
-      const int32_t ql = cu[s + 1] - cu[s];
-      if (ql < 1 || ql >= plan.prefill_min_q) continue;
-      const int32_t rows = ql * group;
-      if (kv4_tile_rows(plan, rows) != 8 * nt) continue;
-      ++plan.num_decode;
-      const int32_t w = win ? std::max(win[s], 0) : 0;
-      const int32_t pos0 = kv[s] - ql;
-      for (int32_t r0 = 0; r0 < rows; r0 += 8 * nt) {
-        const int32_t n = std::min(8 * nt, rows - r0);
-        const int32_t p0 = pos0 + r0 / group, p1 = pos0 + (r0 + n - 1) / group;
-        const int32_t lo = (w > 0 && p0 - (w - 1) > 0) ? p0 - (w - 1) : 0;
-        const int32_t fb = lo / grain.block_keys;
-        plan.kv4_tiles.push_back({s, cu[s], r0, n, pos0, w, fb, p1 / grain.block_keys - fb + 1});
-      }
-    }
-    const int32_t last = static_cast<int32_t>(plan.kv4_tiles.size());
-    for (int32_t b = first; b < last; b += kKv4TilesLarge) {
-      const int32_t e = std::min(last, b + kKv4TilesLarge);
-      std::vector<int64_t> v0(1, 0);
-      for (int32_t i = b; i < e; ++i)
-        v0.push_back(v0.back() + static_cast<int64_t>(plan.kv4_tiles[i].nb + kKv4SegCost) * plan.hkv);
-      const int64_t total = v0.back();
-      const int64_t most = std::min<int64_t>(plan.decode_sms > 0 ? plan.decode_sms : plan.num_sms, kKv4MaxCtas);
-      const int64_t n = std::max<int64_t>(
-          std::max<int64_t>(1, std::min(most, total / (kKv4BlocksPerWarp * grain.warps))),
-          std::min(most, ceil_div(total, 0x3fffffff)));
-      if (ceil_div(total, n) > 0x7fffffff) return RPA_ERR_UNSUPPORTED;
-      Plan::Kv4Launch l{b, e, nt, static_cast<int32_t>(plan.kv4_starts.size()), static_cast<int32_t>(n), false};
-      // Equal ranges of the line; the boundaries that fall inside a segment cut it.
-      int64_t seg = -1, parts = 1;
-      for (int64_t c = 0; c < n; ++c) {
-        const int64_t x = total * c / n, end = total * (c + 1) / n;
-        const size_t i = static_cast<size_t>(std::upper_bound(v0.begin(), v0.end(), x) - v0.begin()) - 1;
-        const int32_t nb = plan.kv4_tiles[b + static_cast<int32_t>(i)].nb;
-        const int64_t cost = nb + kKv4SegCost, off = (x - v0[i]) % cost;
-        plan.kv4_starts.push_back({static_cast<int32_t>(i), static_cast<int32_t>((x - v0[i]) / cost),
-                                   static_cast<int32_t>(off), static_cast<int32_t>(end - x)});
-        if (off == 0 || off >= nb) continue;
-        l.cut = true;
-        parts = x - off == seg ? parts + 1 : 2;
-        seg = x - off;
-        plan.max_splits = std::max(plan.max_splits, static_cast<int32_t>(parts));
-      }
-      if (plan.kv_split == 0)
-        plan.kv_split = static_cast<int32_t>(std::min<int64_t>(ceil_div(total, n) * grain.block_keys, 0x7fffffff));
-      plan.max_splits = std::max(plan.max_splits, 1);
-      plan.decode_ctas += n;
-      plan.kv4_part_rows = std::max(plan.kv4_part_rows, 2 * n * nt * 8);
-      plan.kv4_piece_rows = std::max(plan.kv4_piece_rows, grain.warps * n * nt * 8);
-      plan.kv4_launches.push_back(l);
-    }
-  }
-  return RPA_OK;
-}
-
-rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu, const int32_t* kv,
-                                const int32_t* win, const rpa_plan_options& opts) {
-  const int32_t group = plan.hq / plan.hkv;
-  if (plan.dtype != RPA_DTYPE_BF16 || opts.path == RPA_PATH_SIMT || plan.p < 16 ||
-      !prefill_tc_supported(plan.d, plan.p, group) || opts.kv_split != 0 ||
-      opts.prefill_pairs == 2 || opts.prefill_split > 0 ||
-      opts.decode_kernel != 0 || opts.q_block > prefill_tokens_per_block(plan.d, group))
-    return RPA_ERR_UNSUPPORTED;
-  plan.kv_fp4 = true;
-  plan.path = RPA_PATH_TC;
-  plan.num_decode = plan.num_prefill = 0;
-  split_kv4(plan, cu, kv, win, opts);
-  if (rpa_status_t st = plan_kv4_decode(plan, cu, kv, win)) return st;
-  size_t off = kHeaderBytes;
-  auto take = [&](size_t bytes) {
-    const size_t at = off;
-    off += (bytes + 255) / 256 * 256;
-    return at;
-  };
-  if (plan.kv4_part_rows > 0) {
-    plan.off_partial_o = take(static_cast<size_t>(plan.kv4_part_rows) * plan.d * sizeof(float));
-    plan.off_partial_lse = take(static_cast<size_t>(plan.kv4_part_rows) * sizeof(float));
-    plan.off_kv4_pieces = take(static_cast<size_t>(plan.kv4_piece_rows) * plan.d * sizeof(float));
-  }
-  int64_t pages = 0;
-  for (int32_t s = 0; s < plan.num_seqs; ++s) {
-    const int32_t ql = cu[s + 1] - cu[s];
-    if (ql < plan.prefill_min_q) continue;
-    ++plan.num_prefill;
-    const int32_t w = win ? win[s] : 0;
-    const int32_t p0 = kv[s] - ql;
-    const int32_t lo = (w > 0 && p0 - (w - 1) > 0) ? p0 - (w - 1) : 0;
-    const int32_t slot0 = lo / plan.p;
-    plan.kv4_expand.push_back({s, slot0, static_cast<int32_t>(pages), lo, kv[s]});
-    pages += ceil_div(kv[s], plan.p) - slot0;
-    // (The expansion counts the scratch rows of all heads in 31 bits.)
-    if (pages * plan.p * plan.hkv > 0x7fffffff) return RPA_ERR_UNSUPPORTED;
-  }
-  plan.kv4_scratch_pages = static_cast<int32_t>(pages);
-  if (plan.num_prefill > 0) {
-    plan_prefill(plan, cu, kv, win, opts.q_block, 0, opts.prefill_dynamic == 0,
-                 opts.prefill_grouping == 0);
-    const size_t bytes = static_cast<size_t>(pages) * plan.p * plan.hkv * plan.d * 2;
-    plan.off_kv4_k = take(bytes);
-    plan.off_kv4_v = take(bytes);
-    plan.off_kv4_table = take(static_cast<size_t>(plan.num_seqs) * plan.mpps * sizeof(int32_t));
-  }
-  plan.ws_bytes = off;
-  return RPA_OK;
-}
-
 }  // namespace
 
 rpa_status_t build_schedule(Plan& plan, const int32_t* cu, const int32_t* kv,
                             const int32_t* win, const rpa_plan_options& opts) {
   const int32_t group = plan.hq / plan.hkv;
-  if (opts.kv_dtype == RPA_DTYPE_FP4_E2M1) return build_kv4_schedule(plan, cu, kv, win, opts);
   plan.num_decode = plan.num_prefill = 0;
   for (int32_t s = 0; s < plan.num_seqs; ++s) {
     int32_t ql = cu[s + 1] - cu[s];

@@ -1044,8 +1044,7 @@ int launch_prefill_t(const Plan& plan, const Args& a, cudaStream_t stream) {
   // A V stage that is one box high (its kVKeys keys in one page) takes all
   // its 64-dimension chunks in one 4-D box ([chunk][key][128 B], the stage's
   // layout); otherwise one 3-D box per chunk and per page.
-  const int32_t pool_pages = a.pool_pages > 0 ? a.pool_pages : plan.num_pages;
-  const uint64_t pool_rows = static_cast<uint64_t>(pool_pages) * plan.p;
+  const uint64_t pool_rows = static_cast<uint64_t>(plan.num_pages) * plan.p;
   const bool v_4d = Lay::kChunks > 1 && box_rows_v == Lay::kVKeys;
   if (!make_tmap_3d(&tq, a.q, D, plan.hq, static_cast<uint64_t>(plan.total_q), G, qb) ||
       !make_tmap_3d(&tk, a.k_pages, D, plan.hkv, pool_rows, 1, box_rows_k) ||
@@ -1070,7 +1069,7 @@ int launch_prefill_t(const Plan& plan, const Args& a, cudaStream_t stream) {
   p.box_rows_v = box_rows_v;
   p.v_4d = v_4d ? 1 : 0;
   p.mpps = plan.mpps;
-  p.num_pages = pool_pages;
+  p.num_pages = plan.num_pages;
   p.scale_log2 = a.sm_scale * 1.4426950408889634f;
   p.out_v8 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 ? 1 : 0;
   p.ppart_o = reinterpret_cast<float*>(a.workspace + plan.off_ppart_o);

@@ -187,8 +187,9 @@ struct Plan {
   size_t off_kv4_pieces = 0;
   size_t off_kv4_k = 0, off_kv4_v = 0, off_kv4_table = 0;
 
-  // Prefill (q_len >= prefill_min_q).
-  int32_t prefill_min_q = 2;
+  std::unique_ptr<Plan> kv4_prefill;  // the prefill part's plan, over the widened pages
+
+  // Prefill (q_len > 1).
   int32_t num_prefill = 0;
   int32_t q_block = 0;
   bool prefill_pairs = false;      // items are pairs of query blocks (SM-pair kernel)
@@ -215,6 +216,10 @@ struct Plan {
 rpa_status_t build_schedule(Plan& plan, const int32_t* cu_q_lens, const int32_t* kv_lens,
                             const int32_t* window, const rpa_plan_options& opts);
 
+// The scheduler for 4-bit pages (plan_kv4.cpp), for a plan as build_schedule's.
+rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu_q_lens, const int32_t* kv_lens,
+                                const int32_t* window, const rpa_plan_options& opts);
+
 // Host-side checks of the metadata (plan.cpp).
 rpa_status_t validate_metadata(const int32_t* cu_q_lens, const int32_t* kv_lens,
                                int32_t num_seqs, int32_t page_size,
@@ -236,7 +241,6 @@ struct Args {
   const float* v_scale = nullptr;
   const uint8_t* k_block_scales = nullptr;  // 4-bit pages: a scale byte per 16 dimensions
   const uint8_t* v_block_scales = nullptr;
-  int32_t pool_pages = 0;                   // pages of k_pages / v_pages (0: the plan's)
 };
 
 // Kernel launchers; each returns cudaError_t as int (0 = success).
