@@ -37,6 +37,7 @@
 // costs about one issue slot in 32 (widen, scale, multiply): at the copy peak
 // the schedulers are ~70% busy, so either can be the limit.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kv4.cuh"
@@ -335,33 +336,43 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
   const uint32_t copy_at = Lay::copy_at(lane);
   constexpr int H = D / 16;  // 16-byte pieces of 16 keys' K (or V) scales
   const uint8_t* const s_lane = (lane < H ? p.ks : p.vs) + (lane & (H - 1)) * 16;
+  // Parts [h0, h0 + N) of the block into stage st, from page `page` on.
+  auto copy_parts = [&](int st, int32_t key, int32_t page, int h0, auto parts) {
+    constexpr int N = decltype(parts)::value;
+    const bool ok = page >= 0 && page < p.num_pages;
+    const uint32_t bits = ((1u << N) - 1u) << (st * SUB + h0);
+    bad_parts = ok ? bad_parts & ~bits : bad_parts | bits;
+    if (!ok && page != -2 && lane == 0)
+      report_error(p.ws, (key >> p.page_shift) < p.mpps ? RPA_DEVERR_PAGE_ID : RPA_DEVERR_LENGTHS, cur.seq);
+    // The first row in the pool (rows of one head in a page are contiguous);
+    // without a page the bytes arrive as zeros.
+    const int64_t row = ok ? ((static_cast<int64_t>(page) * p.hkv + cur.g) << p.page_shift) +
+                                 (key & ((1 << p.page_shift) - 1))
+                           : 0;
+    const uint32_t bytes = ok ? 16 : 0;
+    const uint32_t d = ring + st * Sh::kStage + h0 * Sh::kPart;
+    const uint8_t* kp = k_lane + row * (D / 2);
+    const uint8_t* vp = v_lane + row * (D / 2);
+    const uint8_t* sp = s_lane + row * (D / 16);
+#pragma unroll
+    for (int h = 0; h < N; ++h) {
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {  // 512 bytes of K and of V each
+        copy_async(d + h * Sh::kPart + Lay::copy_step(copy_at, i), kp + (h * 8 * D + i * 512), bytes);
+        copy_async(d + h * Sh::kPart + Sh::kVOff + Lay::copy_step(copy_at, i), vp + (h * 8 * D + i * 512), bytes);
+      }
+      if (lane < 2 * H) copy_async(d + h * Sh::kPart + Sh::kSOff + lane * 16, sp + h * D, bytes);
+    }
+  };
   auto issue = [&](int st) {
     if (bi < cur.n) {
       const int32_t key = (cur.blk + bi) * kBlk;
-      const uint32_t dst = ring + st * Sh::kStage;
+      if ((1 << p.page_shift) >= kBlk) {
+        copy_parts(st, key, __shfl_sync(0xffffffffu, cur.page[0], bi), 0, std::integral_constant<int, SUB>());
+      } else {
 #pragma unroll
-      for (int h = 0; h < SUB; ++h) {
-        const int32_t page = __shfl_sync(0xffffffffu, cur.page[h], bi);
-        const bool ok = page >= 0 && page < p.num_pages;
-        const uint32_t bit = 1u << (st * SUB + h);
-        bad_parts = ok ? bad_parts & ~bit : bad_parts | bit;
-        if (!ok && page != -2 && lane == 0)
-          report_error(p.ws, ((key + 16 * h) >> p.page_shift) < p.mpps ? RPA_DEVERR_PAGE_ID : RPA_DEVERR_LENGTHS,
-                       cur.seq);
-        // The part's first row in the pool (rows of one head in a page are
-        // contiguous); without a page the bytes arrive as zeros.
-        const int64_t row = ok ? ((static_cast<int64_t>(page) * p.hkv + cur.g) << p.page_shift) +
-                                     ((key + 16 * h) & ((1 << p.page_shift) - 1))
-                               : 0;
-        const uint32_t d = dst + h * Sh::kPart;
-        const uint8_t* kp = k_lane + row * (D / 2);
-        const uint8_t* vp = v_lane + row * (D / 2);
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {  // 512 bytes of K and of V each
-          copy_async(d + Lay::copy_step(copy_at, i), kp + i * 512, ok ? 16 : 0);
-          copy_async(d + Sh::kVOff + Lay::copy_step(copy_at, i), vp + i * 512, ok ? 16 : 0);
-        }
-        if (lane < 2 * H) copy_async(d + Sh::kSOff + lane * 16, s_lane + row * (D / 16), ok ? 16 : 0);
+        for (int h = 0; h < SUB; ++h)
+          copy_parts(st, key + 16 * h, __shfl_sync(0xffffffffu, cur.page[h], bi), h, std::integral_constant<int, 1>());
       }
       if (++bi == cur.n) {
         cur = nxt;
