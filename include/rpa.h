@@ -516,7 +516,8 @@ rpa_status_t rpa_forward_kv4(const void* q, const uint8_t* k_pages, const uint8_
  *
  * Device pointers, contiguous, 4-byte (slot_map 8-byte) aligned; page_table
  * [num_seqs, max_pages_per_seq], free_pages [num_pages].  page_size a power of
- * two.  `workspace`: 256 bytes or more, 256-B aligned, zero-filled before its
+ * two; num_seqs, num_pages and max_tokens at most 2^30, else
+ * RPA_ERR_UNSUPPORTED.  `workspace`: 256 bytes or more, 256-B aligned, zero-filled before its
  * first use (any plan's workspace serves); calls that share one do not overlap
  * on the GPU.  Enqueues one kernel on `stream`; does not synchronise.
  */

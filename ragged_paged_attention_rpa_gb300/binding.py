@@ -250,7 +250,8 @@ def rpa_plan(cu_q_lens_host, kv_lens_host, window_host, num_q_heads: int,
         raise RpaError(st, "rpa_plan")
     meta = dict(num_seqs=num_seqs, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads,
                 head_dim=head_dim, page_size=page_size, has_window=win is not None,
-                dtype=dtype, total_q=int(cu[-1]))
+                dtype=dtype, total_q=int(cu[-1]), num_pages=num_pages,
+                max_pages_per_seq=max_pages_per_seq)
     return Plan(handle.value, ws.value, meta)
 
 
@@ -520,10 +521,16 @@ def _kv4_args(q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv
     m = plan.meta
     dev, st = _current(stream)
     i32, bf16 = torch.int32, torch.bfloat16
-    kp, vp, ks, vs, _, hkv, p, d = _kv4_pools(k_pages, v_pages, k_scales, v_scales, dev)
+    kp, vp, ks, vs, pages, hkv, p, d = _kv4_pools(k_pages, v_pages, k_scales, v_scales, dev)
     s, hq = m["num_seqs"], m["num_q_heads"]
-    if hkv != m["num_kv_heads"] or p != m["page_size"] or d != m["head_dim"]:
+    if (hkv != m["num_kv_heads"] or p != m["page_size"] or d != m["head_dim"]
+            or pages < m["num_pages"]):
         raise ValueError("the pools' shape differs from the plan's")
+    least = m["total_q"] * hq * d
+    if q.numel() < least or out.numel() < least:
+        raise ValueError("q and out must hold the plan's %d rows of %d x %d" % (m["total_q"], hq, d))
+    if page_table.numel() < s * m["max_pages_per_seq"]:
+        raise ValueError("page_table must be [%d, %d]" % (s, m["max_pages_per_seq"]))
     ws, n = _workspace(workspace, dev)
     return (_addr(q, "q", bf16, dev), kp, vp, ks, vs, _addr(page_table, "page_table", i32, dev),
             _addr(cu_q_lens, "cu_q_lens", i32, dev), _addr(kv_lens, "kv_lens", i32, dev),

@@ -2,6 +2,7 @@
 // launch sequence of rpa_forward.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -649,6 +650,7 @@ rpa_status_t rpa_build_tables(const int32_t* new_lens, const int32_t* kv_lens_pr
     return RPA_ERR_INVALID_ARG;
   if (!state_ok(kv_lens_prev, kv_lens, num_seqs, free_count_prev, free_count))
     return RPA_ERR_INVALID_ARG;
+  if (std::max(std::max(num_seqs, num_pages), max_tokens) > rpa::kTablesMost) return RPA_ERR_UNSUPPORTED;
   rpa::TableArgs a{new_lens, kv_lens_prev, page_table, const_cast<int32_t*>(free_pages),
                    free_count_prev, cu_q_lens, kv_lens, slot_map, free_count,
                    static_cast<unsigned char*>(workspace), num_seqs, page_size,
@@ -676,6 +678,7 @@ rpa_status_t rpa_release_tables(const int32_t* finished, const int32_t* kv_lens_
     return RPA_ERR_INVALID_ARG;
   if (!state_ok(kv_lens_prev, kv_lens, num_seqs, free_count_prev, free_count))
     return RPA_ERR_INVALID_ARG;
+  if (std::max(num_seqs, num_pages) > rpa::kTablesMost) return RPA_ERR_UNSUPPORTED;
   rpa::TableArgs a{finished, kv_lens_prev, const_cast<int32_t*>(page_table), free_pages,
                    free_count_prev, nullptr, kv_lens, nullptr, free_count,
                    static_cast<unsigned char*>(workspace), num_seqs, page_size,

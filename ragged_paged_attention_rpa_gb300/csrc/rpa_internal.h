@@ -28,6 +28,9 @@ constexpr size_t kPrefillCounterOff = 64;
 // Offset in the header of the table kernels' counter (one int32: CTAs
 // finished), zero between launches.
 constexpr size_t kTablesCounterOff = 128;
+// Most requests, pages and tokens of a table call (its loop indices add a grid's
+// threads to them in 31 bits).
+constexpr int32_t kTablesMost = 1 << 30;
 
 // One prefill work item: query block `qb` (of plan.q_block tokens) of
 // sequence `seq`, for KV head `head`.  Ordered longest first in the plan.

@@ -229,6 +229,16 @@ def test_refusals_of_the_binding():
     r.pool = pools(4, 1, 16, 64)
     with pytest.raises(ValueError):
         r.call()
+    r = Kv4Batch(b)
+    args = (r.db.page_table, r.db.cu_q_lens, r.db.kv_lens, None, b.sm_scale)
+    with pytest.raises(ValueError):     # a pool of fewer pages than the plan's
+        binding.rpa_forward_kv4(r.db.q, *pools(1, 2, 16, 64), *args, r.out, r.plan, r.ws)
+    with pytest.raises(ValueError):     # too few rows of q, of out, of the table
+        binding.rpa_forward_kv4(r.db.q[:0], *r.pool, *args, r.out, r.plan, r.ws)
+    with pytest.raises(ValueError):
+        binding.rpa_forward_kv4(r.db.q, *r.pool, *args, r.out[:, :2].contiguous(), r.plan, r.ws)
+    with pytest.raises(ValueError):
+        binding.rpa_forward_kv4(r.db.q, *r.pool, r.db.page_table[:, :1].contiguous(), *args[1:], r.out, r.plan, r.ws)
 
 
 def test_trace_names_the_kernels():

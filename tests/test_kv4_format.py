@@ -179,6 +179,12 @@ def test_table_calls_check_before_any_launch():
         ws = len(ok) - 2
         assert f(*changed(ok, **{"_%d" % ws: None})) == RPA_ERR_INVALID_ARG
         assert f(*changed(ok, **{"_%d" % ws: addr((1 << 21) + 128)})) == RPA_ERR_INVALID_ARG
+    # Sizes whose loop indices would leave 31 bits.
+    most = (1 << 30) + 1
+    for f, ok, sizes in ((L.rpa_build_tables, build_ok, (9, 10, 13)), (L.rpa_release_tables, release_ok, (7, 10))):
+        kv = {"_5" if f is L.rpa_release_tables else "_6": addr(1 << 40)}  # apart from kv_lens_prev
+        for i in sizes:
+            assert f(*changed(ok, **kv, **{"_%d" % i: most})) == RPA_ERR_UNSUPPORTED, i
     # Lengths or the stack's height that overlap their inputs without being them.
     assert L.rpa_build_tables(*changed(build_ok, _6=addr(a[1].value + 4))) == RPA_ERR_INVALID_ARG
     assert L.rpa_release_tables(*changed(release_ok, _5=addr(a[1].value + 12))) == RPA_ERR_INVALID_ARG
