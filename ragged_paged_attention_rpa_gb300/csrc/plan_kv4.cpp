@@ -39,6 +39,7 @@ constexpr int32_t kBlocksPerWarp = 2;
 constexpr double kOneTileGBs = 43.0;
 constexpr double kTilesGBs = 30.0;
 constexpr double kTile16GBs = 26.0;
+constexpr double kRows64GBs = 10.0;
 constexpr double kHbmGBs = 5700.0;
 constexpr double kFixedUs = 18.0;
 constexpr double kExpandGBs = 5000.0;
@@ -72,7 +73,10 @@ struct Problem {
 
 // Rows of a split-KV tile: 16 where a sequence has more than 8 and the kernel's
 // registers hold them (head_dim below 256).
-int32_t tile_rows(int32_t head_dim, int32_t rows) { return rows > 8 && head_dim < 256 ? 16 : 8; }
+int32_t tile_rows(int32_t head_dim, int32_t rows) {
+  if (rows > (head_dim == 256 ? 16 : 32)) return 8 * kKv4RowsTile;
+  return rows > 8 && head_dim < 256 ? 16 : 8;
+}
 
 // Modelled work of the two parts where sequences of q_len >= min_q are prefill.
 struct Work {
@@ -101,7 +105,7 @@ Work work_of(const Problem& b, int32_t min_q) {
       const int32_t rows = ql * b.group, tile = tile_rows(p.d, rows);
       k.dec = true;
       k.sm_us += bytes * static_cast<double>(ceil_div(rows, tile)) * 1e-3 /
-                 (tile == 16 ? kTile16GBs : rows > 8 ? kTilesGBs : kOneTileGBs);
+                 (tile > 16 ? kRows64GBs : tile == 16 ? kTile16GBs : rows > 8 ? kTilesGBs : kOneTileGBs);
       k.hbm_us += bytes * 1e-3 / kHbmGBs;
       continue;
     }
@@ -120,7 +124,7 @@ Work work_of(const Problem& b, int32_t min_q) {
 
 // Row tiles, launches and CTA ranges of the split-KV part.
 rpa_status_t plan_split(Plan& plan, const Problem& b, int32_t min_q) {
-  for (int32_t nt = 1; nt <= 2; ++nt) {
+  for (const int32_t nt : {1, 2, kKv4RowsTile}) {
     const Kv4Grain grain = kv4_grain(plan.d, nt);
     const int32_t first = static_cast<int32_t>(plan.kv4_tiles.size());
     for (int32_t s = 0; s < plan.num_seqs; ++s) {
@@ -170,7 +174,7 @@ rpa_status_t plan_split(Plan& plan, const Problem& b, int32_t min_q) {
       plan.max_splits = std::max(plan.max_splits, 1);
       plan.decode_ctas += n;
       plan.kv4_part_rows = std::max(plan.kv4_part_rows, 2 * n * nt * 8);
-      plan.kv4_piece_rows = std::max(plan.kv4_piece_rows, grain.warps * n * nt * 8);
+      if (nt != kKv4RowsTile) plan.kv4_piece_rows = std::max(plan.kv4_piece_rows, grain.warps * n * nt * 8);
       plan.kv4_launches.push_back(l);
     }
   }

@@ -100,6 +100,7 @@ constexpr int kKv4TilesSmall = 160;
 constexpr int kKv4TilesLarge = 864;
 constexpr int kKv4MaxCtas = 256;
 constexpr int kKv4SegCost = 3;
+constexpr int kKv4RowsTile = 8;  // the tiles of kv4_rows.cu, in rows of 8
 // Sequences whose 4-bit pages one expansion launch lists.
 constexpr int kKv4ExpandSeqs = 1024;
 
@@ -297,6 +298,8 @@ struct Kv4Grain {
   int32_t warps, block_keys;  // of a CTA (one a SM); keys of a block
 };
 Kv4Grain kv4_grain(int32_t head_dim, int32_t nt);
+Kv4Grain kv4_rows_grain(int32_t head_dim);
+int launch_kv4_rows(const Plan& plan, const Args& a, const Plan::Kv4Launch& l, void* stream);
 int launch_kv4_expand(const Plan& plan, const Args& a, void* stream);
 
 // The 4-bit cache's write and read (kv4_cache.cu).
