@@ -9,7 +9,7 @@
 //
 // CTA.  8 warps, blocks of 8192 / D keys.  Per block a warp
 //   - widens an eighth of it, 2048 elements of K or of V, which it copied itself
-//     (cp.async, three blocks ahead; the codes need no barrier);
+//     (cp.async, four blocks in flight; the codes need no barrier);
 //   - after one barrier (the f16 blocks are double-buffered) takes 16 rows of
 //     the tile and half of the block's keys: S = Q K^T, an online softmax, and
 //     O += P V (mma.m16n8k16, f16 -> fp32).
@@ -20,8 +20,16 @@
 // a lane) and the eight rows of an ldmatrix meet every bank once.
 //
 // Numbers, unseen keys and bad pages: as in kv4_decode.cu.
-#include <algorithm>
-
+//
+// What bounds it: instructions.  A warp runs some 500 a block (64 products, 32
+// ldmatrix, the widening, the softmax, the next copies) at about four cycles
+// each, two warps a scheduler: O and Q of 16 rows take 192 registers at 256
+// dimensions.  128 sequences of 64 rows over 128-2048 keys of 256 dimensions take
+// 59.1 us (47 MB from HBM; widening to bf16 pages and the prefill kernel 72.7 us,
+// tiles of 8 rows 77 us); 32 rows of each 46 us.  Tried: the next block's widening
+// between this one's products 61 us; 16 warps of 128 registers, each with a
+// quarter of the keys for S and of the dimensions for O, 69 us (the copies' and
+// the softmax's instructions then run in twice as many warps).
 #include "kv4_split.cuh"
 
 namespace rpa {
@@ -38,7 +46,8 @@ struct RowsShape {
   static constexpr int KT = D / 16;       // 16-dimension steps
   static constexpr int kStage = 8 * 1024 + 8 * 128;
   static constexpr int kHalf = 16384;     // f16 K (or V) of a block
-  static constexpr int kBytes = 4 * kHalf + S * kStage;
+  static constexpr int kMerge = D * 256;  // O of half the keys
+  static constexpr int kBytes = 4 * kHalf + S * kStage + kMerge;
 };
 
 __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, uint32_t src_bytes) {
@@ -67,7 +76,11 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = lane >> 2, c = lane & 3;
-  const int rg = warp & 3, ks = warp >> 2;    // this warp's 16 rows and half of the keys
+  // This warp's 16 rows and half of the keys (a tile of 32 rows is the work of
+  // warps 0-3, one on each scheduler); the quarter of K or V that it widens.
+  const int rg = warp >> 1, ks = warp & 1;
+  const int quarter = warp & 3;
+  const bool is_k = warp < 4;
   const Kv4Start start = sc.cta[blockIdx.x];
   if (start.len <= 0) return;
   const uint32_t half0 = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
@@ -83,70 +96,119 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
   // ---- The copies' side: warps 0-3 copy the block's quarters of K, 4-7 of V.
   Place cp = cs;
   int32_t page[NP];        // of the next block to copy
-  uint32_t good = 0;       // bit st * NP + i: the stage's 16-key group i has a page
-  const uint8_t* const codes = (ks == 0 ? p.k : p.v) + lane * 16;
-  const uint8_t* const scales = (ks == 0 ? p.ks : p.vs) + (NP == 2 ? lane & 15 : lane) * 4;
-  auto find_pages = [&]() {
+  // By stage: whether this lane's key is one that a row sees, and whether the 16
+  // keys around it have a page.
+  uint32_t seen = 0, paged = 0;
+  const uint8_t* const codes = (is_k ? p.k : p.v) + lane * 16;
+  const uint8_t* const scales = (is_k ? p.ks : p.vs) + (NP == 2 ? lane & 15 : lane) * 4;
+  const int wkey = quarter * Sh::kWarpKeys + lane / (D / 64), wline = lane & (D / 64 - 1);  // of a block
+  // Its first key, the keys that its tile's rows see, and their row of the page
+  // table (worked out once a segment: of the divisions alone, a block would run
+  // a hundred instructions).
+  int32_t c_key = 0, c_lo = 0, c_hi = 0;
+  const int32_t* c_row = nullptr;
+  auto enter = [&]() {
+    to_block(cp);
     if (cp.rem <= 0) return;
     const Kv4Tile& t = sc.tile[cp.e];
-    const int32_t lo = first_visible(t.pos0 + t.r0 / p.group, t.window);
-    const int32_t hi = t.pos0 + (t.r0 + t.nrows - 1) / p.group;
+    c_key = (t.fb + cp.j) * kBlk;
+    c_lo = first_visible(t.pos0 + t.r0 / p.group, t.window);
+    c_hi = t.pos0 + (t.r0 + t.nrows - 1) / p.group;
+    c_row = p.page_table + static_cast<int64_t>(t.seq) * p.mpps;
+  };
+  auto find_pages = [&]() {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int32_t k0 = ((t.fb + cp.j) * kBlk + rg * Sh::kWarpKeys + 16 * i) & ~15, slot = k0 >> p.page_shift;
-      if (k0 > hi || k0 + 15 < lo)
+      const int32_t k0 = (c_key + quarter * Sh::kWarpKeys + 16 * i) & ~15, slot = k0 >> p.page_shift;
+      if (k0 > c_hi || k0 + 15 < c_lo)
         page[i] = -2;      // no row of the tile sees these 16
       else
-        page[i] = slot < p.mpps ? __ldg(p.page_table + static_cast<int64_t>(t.seq) * p.mpps + slot) : p.num_pages;
+        page[i] = slot < p.mpps ? __ldg(c_row + slot) : p.num_pages;
     }
   };
   auto issue = [&](int st) {
     if (cp.rem > 0) {
-      const Kv4Tile& t = sc.tile[cp.e];
       const uint32_t dst = ring + st * Sh::kStage;
+      const int32_t key = c_key + wkey;
       int64_t row[NP];
+      bool ok[NP];
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const int32_t k0 = (t.fb + cp.j) * kBlk + rg * Sh::kWarpKeys + 16 * i;
-        const bool ok = page[i] >= 0 && page[i] < p.num_pages;
-        const uint32_t bit = 1u << (st * NP + i);
-        good = ok ? good | bit : good & ~bit;
-        if (!ok && page[i] != -2 && lane == 0)
-          report_error(p.ws, (k0 >> p.page_shift) < p.mpps ? RPA_DEVERR_PAGE_ID : RPA_DEVERR_LENGTHS, t.seq);
-        row[i] = ok ? ((static_cast<int64_t>(page[i]) * p.hkv + cp.g) << p.page_shift) +
-                          (k0 & ((1 << p.page_shift) - 1))
-                    : 0;
+        const int32_t k0 = c_key + quarter * Sh::kWarpKeys + 16 * i;
+        ok[i] = page[i] >= 0 && page[i] < p.num_pages;
+        if (!ok[i] && page[i] != -2 && lane == 0)
+          report_error(p.ws, (k0 >> p.page_shift) < p.mpps ? RPA_DEVERR_PAGE_ID : RPA_DEVERR_LENGTHS,
+                       sc.tile[cp.e].seq);
+        row[i] = ok[i] ? ((static_cast<int64_t>(page[i]) * p.hkv + cp.g) << p.page_shift) +
+                             (k0 & ((1 << p.page_shift) - 1))
+                       : 0;
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int q = NP == 2 ? i : 0;  // (two groups of 16 keys are 512 bytes each)
-        copy_async(dst + warp * 1024 + i * 512 + lane * 16, codes + row[q] * (D / 2) + (NP == 2 ? 0 : i * 512),
-                   (good >> (st * NP + q)) & 1u ? 16 : 0);
+        copy_async(dst + warp * 1024 + i * 512 + (lane ^ (lane >> 3 & 1)) * 16, codes + row[q] * (D / 2) + (NP == 2 ? 0 : i * 512),
+                   ok[q] ? 16 : 0);
       }
-      const int q = NP == 2 ? lane >> 4 : 0;
-      copy_async4(dst + 8192 + warp * 128 + lane * 4, scales + (q ? row[NP - 1] : row[0]) * (D / 16),
-                  (good >> (st * NP + q)) & 1u ? 4 : 0);
+      const bool upper = NP == 2 && lane >= 16, mine = upper ? ok[NP - 1] : ok[0];
+      copy_async4(dst + 8192 + warp * 128 + lane * 4, scales + (upper ? row[NP - 1] : row[0]) * (D / 16),
+                  mine ? 4 : 0);
+      const bool visible = mine && key >= c_lo && key <= c_hi;
+      seen = (seen & ~(1u << st)) | (static_cast<uint32_t>(visible) << st);
+      paged = (paged & ~(1u << st)) | (static_cast<uint32_t>(mine) << st);
       ++cp.j;
       --cp.rem;
-      to_block(cp);
-      find_pages();
+      c_key += kBlk;
+      if (cp.rem <= 0 || cp.j >= cp.nb) enter();
+      if (cp.rem > 0) find_pages();
     }
     copy_commit();
   };
-  find_pages();
+  enter();
+  if (cp.rem > 0) find_pages();
 #pragma unroll
   for (int st = 0; st < S; ++st) issue(st);
 
-  // What this lane widens: 64 dimensions of one key; and where it reads f16 rows.
-  const int wkey = rg * Sh::kWarpKeys + lane / (D / 64), wline = lane & (D / 64 - 1);
-  const uint32_t wdst = ks * Sh::kHalf + wkey * 2 * D + wline * 128;
+  // ---- Widening: 64 dimensions of one key a lane, in four pieces of 16.
+  const uint32_t wdst = half0 + (is_k ? 0 : Sh::kHalf) + wkey * 2 * D + wline * 128;
   const uint32_t wswz = ((wkey & 7) ^ (wline << kLineSwz)) << 4;
-  const int krow = (lane & 7) + ((lane >> 4) << 3), vrow = lane & 15;
-  const uint32_t kat = (ks * (kBlk / 2) + krow) * 2 * D, kx = ((lane & 7) ^ ((lane >> 3) & 1)) << 4;
-  const uint32_t vat = Sh::kHalf + (ks * (kBlk / 2) + vrow) * 2 * D, vx = ((lane & 7) ^ (lane >> 4)) << 4;
+  int st = 0, par = 0;     // the next block's stage; its half of the f16 buffer
+  uint32_t wscale = 0;
+  auto widen_begin = [&](int to) {
+    copy_wait<S - 1>();
+    __syncwarp();  // the codes are other lanes' copies
+    uint32_t w[1];
+    lds<1>(ring + st * Sh::kStage + 8192 + warp * 128 + lane * 4, w);
+    wscale = (seen >> st) & 1u ? w[0] : 0u;  // keys no row sees: whatever their bytes, zeros
+    if (is_k && (lane & 15) == 0) s_bad[to][wkey >> 4] = !((paged >> st) & 1u);
+  };
+  auto widen = [&](int to, int b) {
+    uint32_t w[2], h[8];
+    // (Every other four lanes' codes lie with their 16-byte halves swapped.)
+    lds<2>(ring + st * Sh::kStage + warp * 1024 + lane * 32 + (((b >> 1) ^ (lane >> 2 & 1)) * 16 + (b & 1) * 8), w);
+    kv4::decode_block(make_uint2(w[0], w[1]), (wscale >> (8 * b)) & 0xffu, h);
+    const uint32_t dst = wdst + to * 2 * Sh::kHalf;
+    sts128(dst + (((2 * b) << 4) ^ wswz), h[0], h[1], h[2], h[3]);
+    sts128(dst + (((2 * b + 1) << 4) ^ wswz), h[4], h[5], h[6], h[7]);
+  };
+  auto widen_end = [&]() {
+    __syncwarp();  // every lane has read the codes: the stage may be refilled
+    issue(st);
+    if (++st == S) st = 0;
+  };
 
-  int st = 0, par = 0;
-  float4* const mbuf = reinterpret_cast<float4*>(smem) + rg * (D / 8) * 32 + lane;
+  // (A quarter of a line has its two chunks at one of four places: quarter q of
+  // line u at at[q ^ u], of two lines at at[q ^ 2 u].)
+  uint32_t at[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    at[q] = half0 + (ks * (kBlk / 2) + (lane & 15)) * 2 * D + (((2 * q) ^ (lane & 7) ^ (lane >> 4)) << 4);
+
+  auto at_flip = [&]() {  // to the other f16 block
+    const uint32_t by = par ? 2 * Sh::kHalf : 0u - 2 * Sh::kHalf;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) at[q] += by;
+  };
+  float4* const mbuf = reinterpret_cast<float4*>(smem + 4 * Sh::kHalf + S * Sh::kStage) + rg * (D / 8) * 32 + lane;
   while (cs.rem > 0) {
     const Kv4Tile& tl = sc.tile[cs.e];
     const int G = p.group;
@@ -156,11 +218,11 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
     const int ra = tl.r0 + rg * 16 + g, rb = ra + 8;  // this lane's rows
     auto row_at = [&](int r) { return (static_cast<int64_t>(tl.q0 + r / G) * p.hq + cs.g * G + r % G) * D; };
     // Keys each row sees (rows past the tile's last take its last row's; they
-    // are not written), any row does, and every row does.
+    // are not written), and every row does.
     const int32_t hi_a = tl.pos0 + min(ra, last) / G, hi_b = tl.pos0 + min(rb, last) / G;
     const int32_t lo_a = first_visible(hi_a, tl.window), lo_b = first_visible(hi_b, tl.window);
-    const int32_t all_hi = tl.pos0 + tl.r0 / G, seg_hi = tl.pos0 + last / G;
-    const int32_t seg_lo = first_visible(all_hi, tl.window), all_lo = first_visible(seg_hi, tl.window);
+    const int32_t all_hi = tl.pos0 + tl.r0 / G;
+    const int32_t all_lo = first_visible(tl.pos0 + last / G, tl.window);
     // ---- Q: f16 after a power of two for the row, as A fragments.
     uint32_t qf[KT][4];
     float sca = 0.f, scb = 0.f;
@@ -211,34 +273,25 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
 
     for (int32_t j = cs.j; j < j1; ++j) {
       const int32_t key0 = (tl.fb + j) * kBlk;
-      const uint32_t buf = half0 + par * 2 * Sh::kHalf;
-      // ---- Widen this warp's part.
-      copy_wait<S - 1>();
-      __syncwarp();  // the codes are other lanes' copies
-      {
-        const uint32_t src = ring + st * Sh::kStage;
-        uint32_t w[2][4], s[1];
-        lds<4>(src + warp * 1024 + lane * 32, w[0]);
-        lds<4>(src + warp * 1024 + lane * 32 + 16, w[1]);
-        lds<1>(src + 8192 + warp * 128 + lane * 4, s);
-        // Keys no row sees: whatever their bytes, zeros.
-        const int32_t key = key0 + wkey;
-        const uint32_t ok = (good >> (st * NP + (NP == 2 ? lane >> 4 : 0))) & 1u;
-        if (!ok || key < seg_lo || key > seg_hi) s[0] = 0;
-        if (ks == 0 && (lane & 15) == 0) s_bad[par][wkey >> 4] = !ok;
+      widen_begin(par);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t h[8];
-          kv4::decode_block(make_uint2(w[b >> 1][2 * (b & 1)], w[b >> 1][2 * (b & 1) + 1]), (s[0] >> (8 * b)) & 0xffu, h);
-          sts128(buf + wdst + (((2 * b) << 4) ^ wswz), h[0], h[1], h[2], h[3]);
-          sts128(buf + wdst + (((2 * b + 1) << 4) ^ wswz), h[4], h[5], h[6], h[7]);
-        }
-      }
-      __syncwarp();  // every lane has read the codes: the stage may be refilled
-      issue(st);
-      if (++st == S) st = 0;
-      __syncthreads();
+      for (int b = 0; b < 4; ++b) widen(par, b);
+      widen_end();
+      __syncthreads();  // the block is widened, and every warp done with the one before
       if (active) {
+        // The products' B fragments in order, K's steps and then V's, each read
+        // two steps before its use.
+        constexpr int kSteps = SUB * KT, kAhead = 2;
+        uint32_t b[kAhead + 1][4];
+        auto fetch = [&](int i) {
+          uint32_t(&r)[4] = b[i % (kAhead + 1)];
+          const int t = i % KT, h = i % kSteps / KT, u = t >> 2;
+          const uint32_t from = at[(t & 3) ^ (D == 256 ? u : 2 * u)] + h * 32 * D + u * 128;
+          if (i < kSteps) ldmatrix4(from, r);
+          else ldmatrix4_trans(from + Sh::kHalf, r);
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(i);
         // ---- S = Q K^T
         float x[SUB][2][4];
 #pragma unroll
@@ -251,11 +304,11 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
             for (int n = 0; n < 2; ++n) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
 #pragma unroll
           for (int k = 0; k < KT; ++k) {
-            uint32_t b[4];
-            ldmatrix4(buf + kat + h * 32 * D + (k >> 2) * 128 +
-                          (((2 * (k & 3)) ^ ((k >> 2) << kLineSwz)) << 4 ^ kx), b);
-            mma_f16(acc[k % CH][0], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[0], b[1]);
-            mma_f16(acc[k % CH][1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[2], b[3]);
+            const int i = h * KT + k;
+            fetch(i + kAhead);
+            const uint32_t(&r)[4] = b[i % (kAhead + 1)];  // keys 0-7, 8-15 of dimensions 0-7; of 8-15
+            mma_f16(acc[k % CH][0], qf[k][0], qf[k][1], qf[k][2], qf[k][3], r[0], r[2]);
+            mma_f16(acc[k % CH][1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], r[1], r[3]);
           }
 #pragma unroll
           for (int n = 0; n < 2; ++n)
@@ -354,14 +407,15 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
         for (int h = 0; h < SUB; ++h)
 #pragma unroll
           for (int t = 0; t < KT; ++t) {
-            uint32_t b[4];
-            ldmatrix4_trans(buf + vat + h * 32 * D + (t >> 2) * 128 +
-                                (((2 * (t & 3)) ^ ((t >> 2) << kLineSwz)) << 4 ^ vx), b);
-            mma_f16(o[2 * t], pa[h][0], pa[h][1], pa[h][2], pa[h][3], b[0], b[1]);
-            mma_f16(o[2 * t + 1], pa[h][0], pa[h][1], pa[h][2], pa[h][3], b[2], b[3]);
+            const int i = kSteps + h * KT + t;
+            if (i + kAhead < 2 * kSteps) fetch(i + kAhead);
+            const uint32_t(&r)[4] = b[i % (kAhead + 1)];
+            mma_f16(o[2 * t], pa[h][0], pa[h][1], pa[h][2], pa[h][3], r[0], r[1]);
+            mma_f16(o[2 * t + 1], pa[h][0], pa[h][1], pa[h][2], pa[h][3], r[2], r[3]);
           }
       }
       par ^= 1;
+      at_flip();
     }
 
     // ---- The segment's end in this range: the halves of the keys meet.
@@ -377,7 +431,6 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
       l_a += __shfl_xor_sync(0xffffffffu, l_a, off);
       l_b += __shfl_xor_sync(0xffffffffu, l_b, off);
     }
-    __syncthreads();  // the f16 blocks are no longer read
     if (ks == 1 && active) {
 #pragma unroll
       for (int t = 0; t < D / 8; ++t) mbuf[t * 32] = make_float4(o[t][0], o[t][1], o[t][2], o[t][3]);
@@ -425,8 +478,8 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
         if (has_b) p.part_lse[static_cast<int64_t>(slot) * Sh::kRows + nb] = Lb == 0.f ? -INFINITY : Mb + __log2f(Lb);
       }
     }
-    __syncthreads();  // the merge's values are read: the buffers may be filled again
   }
+  copy_wait<0>();
 }
 
 template <int D, int NSEG>

@@ -151,7 +151,7 @@ kv4_combine_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!mine) return;
   const int lane = threadIdx.x & 31;
-  for (int n = threadIdx.x >> 5; n < tl.nrows; n += 8) {
+  for (int n = blockIdx.y * 8 + (threadIdx.x >> 5); n < tl.nrows; n += 8 * gridDim.y) {
     // The first part is its CTA's first segment only if the range starts with it.
     auto slot = [&](int k) {
       return static_cast<int64_t>(2 * (b - 1 + k) + (k == 0 && !same ? 1 : 0)) * ROWS + n;
@@ -254,7 +254,7 @@ int launch_split(const Plan& plan, const Kv4Params& p, const Plan::Kv4Launch& l,
   trace_mark(RPA_KERNEL_KV4_DECODE, stream);
   if (!l.cut) return 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(l.n_ctas - 1);
+  cfg.gridDim = dim3(l.n_ctas - 1, ROWS > 16 ? ROWS / 8 : 1);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

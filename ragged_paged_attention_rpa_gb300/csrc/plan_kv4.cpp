@@ -1,8 +1,8 @@
 // The scheduler for 4-bit pages (RPA_DTYPE_FP4_E2M1).  Host only.
 //
 // Sequences of few query rows per KV head (q_len x G; single tokens always) run
-// on the split-KV kernel of kv4_decode.cu, in tiles of 8 or 16 rows that each
-// widen the keys anew; the others' visible keys are widened to bf16 once
+// on the split-KV kernels, in tiles of 8 or 16 rows (kv4_decode.cu) or of 64
+// (kv4_rows.cu) that each widen the keys anew; the others' visible keys are widened to bf16 once
 // (kv4_expand.cu) and run on the tensor-core prefill, as a plan of its own
 // (Plan::kv4_prefill) over the widened pages.
 #include <algorithm>
@@ -22,10 +22,10 @@ namespace {
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Which part is faster for a sequence of several rows depends on the batch: the
-// prefill does not split a sequence's keys over CTAs, the split-KV kernel widens
+// prefill does not split a sequence's keys over CTAs, the split-KV kernels widen
 // them once a tile (128 sequences of 64 rows over 128-2048 keys of 256: 72 us on
-// the prefill, 77 split; 8 of them over 16k-30k keys: 459 against 71; one of 128
-// rows over 2016 keys: 35 against 12).  So the row limit is the one of these
+// the prefill, 59 split; 64 of 128 rows over as many: 51 against 61; 8 of 64 rows
+// over 16k-30k keys: 459 against 69).  So the row limit is the one of these
 // with the smallest modelled time.
 constexpr int32_t kRowLimits[] = {16, 32, 64, 128};
 // Fewest key blocks (segment charges included) a warp of the split-KV kernel
@@ -34,12 +34,12 @@ constexpr int32_t kBlocksPerWarp = 2;
 
 // The split-KV kernel's model, fitted to GB300 timings on 12-152 SMs: 4-bit
 // bytes it widens a second on an SM (a single tile of 8 rows, several of them,
-// tiles of 16), bytes from HBM, and its start, merge and combine; and the
+// tiles of 16, tiles of 64), bytes from HBM, and its start, merge and combine; and the
 // bandwidth of the widening to bf16.
 constexpr double kOneTileGBs = 43.0;
 constexpr double kTilesGBs = 30.0;
 constexpr double kTile16GBs = 26.0;
-constexpr double kRows64GBs = 10.0;
+constexpr double kRows64GBs = 5.8;
 constexpr double kHbmGBs = 5700.0;
 constexpr double kFixedUs = 18.0;
 constexpr double kExpandGBs = 5000.0;
@@ -71,8 +71,11 @@ struct Problem {
   }
 };
 
-// Rows of a split-KV tile: 16 where a sequence has more than 8 and the kernel's
-// registers hold them (head_dim below 256).
+// Rows of a split-KV tile.  Up to two tiles of kv4_decode.cu: 8 rows, or 16 where
+// a sequence has more than 8 and the kernel's registers hold them (head_dim below
+// 256).  Beyond, tiles of 64 (32 sequences of 32 rows of 128 dimensions, 8 heads,
+// over 120-4000 keys: 62 us in tiles of 16, 73 in one of 64; 128 sequences of 32
+// rows of 256: 73 us on the prefill, 46 in one of 64).
 int32_t tile_rows(int32_t head_dim, int32_t rows) {
   if (rows > (head_dim == 256 ? 16 : 32)) return 8 * kKv4RowsTile;
   return rows > 8 && head_dim < 256 ? 16 : 8;

@@ -548,3 +548,43 @@ def test_a_step_written_then_attended():
                     val = held_v[s][:n, h // 4].astype(np.float64)
                     ref, mag = w @ val, w @ np.abs(val)
                     assert (np.abs(got[starts[s] + i, h] - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7.9 * mag).all()
+
+
+ROWS = [
+    # (q_lens, kv_lens, Hq, Hkv, D, P, windows): 17 to 128 query rows a sequence
+    ([8, 3, 5, 1], [700, 8, 33, 500], 8, 1, 256, 16, None),
+    ([8, 8], [2047, 1300], 8, 1, 256, 256, [100, 0]),
+    ([5, 13, 1], [65, 130, 3], 8, 2, 128, 16, [0, 7, 0]),
+    ([16, 9], [4000, 3001], 4, 1, 128, 32, [0, 1000]),                           # cut over CTAs
+    ([4, 6, 16], [127, 600, 1029], 8, 1, 64, 16, [0, 0, 50]),
+    ([1, 1, 1], [900, 1, 128], 64, 1, 64, 32, [0, 0, 33]),                       # single tokens, G = 64
+    ([1, 1], [513, 31], 128, 1, 256, 64, None),                                  # G = 128: two tiles
+    ([2, 1], [300, 20], 57, 1, 128, 64, None),                                   # G = 57: 114 rows
+]
+
+
+@pytest.mark.parametrize("case", range(len(ROWS)))
+def test_tens_of_rows(case):
+    """Tiles of 64 rows: blocks widened once for all of them.  With NaN bytes in
+    every unseen slot the bits are the same, and a bad page is reported and
+    counts as unseen."""
+    ql, kv, hq, hkv, d, p, win = ROWS[case]
+    b = batch(ql, kv, hq, hkv, d, p, win, seed=700 + case)
+    r = Kv4Batch(b)
+    assert r.plan.info()["num_prefill_seqs"] == 0
+    out = r.call().clone()
+    assert binding.rpa_get_device_error(r.ws) == 0
+    check(b, out)
+    unseen = unseen_slots(b)
+    for name in ("k_fp4_scale", "v_fp4_scale"):
+        x = getattr(b, name).copy()
+        x.transpose(0, 2, 1, 3)[unseen] = 255
+        setattr(b, name, x)
+    r2 = Kv4Batch(b)
+    assert torch.equal(r2.call(), out)
+    table = b.page_table.copy()
+    table[0, 0] = b.num_pages
+    bad = r2.call(page_table=cuda(table))
+    seen = not (win and win[0] > 0 and kv[0] - ql[0] - (win[0] - 1) >= p)
+    assert binding.rpa_get_device_error(r2.ws) == (binding.RPA_DEVERR_PAGE_ID if seen else 0)
+    assert bool(torch.isfinite(bad).all())
