@@ -10,9 +10,9 @@
 // CTA.  8 warps, blocks of 8192 / D keys.  Per block a warp
 //   - widens an eighth of it, 2048 elements of K or of V, which it copied itself
 //     (cp.async, four blocks in flight; the codes need no barrier);
-//   - after one barrier (the f16 blocks are double-buffered) takes 16 rows of
-//     the tile and half of the block's keys: S = Q K^T, an online softmax, and
-//     O += P V (mma.m16n8k16, f16 -> fp32).
+//   - after a barrier of the four warps that share its half of the block's keys
+//     (the f16 blocks are double-buffered) takes 16 rows of the tile: S = Q K^T,
+//     an online softmax, and O += P V (mma.m16n8k16, f16 -> fp32).
 // The two halves of the keys meet at the segment's end.
 //
 // Layout.  A row of f16 is lines of 128 bytes whose 16-byte chunks are permuted
@@ -26,8 +26,10 @@
 // each, two warps a scheduler: O and Q of 16 rows take 192 registers at 256
 // dimensions.  128 sequences of 64 rows over 128-2048 keys of 256 dimensions take
 // 59.1 us (47 MB from HBM; widening to bf16 pages and the prefill kernel 72.7 us,
-// tiles of 8 rows 77 us); 32 rows of each 46 us.  Tried: the next block's widening
-// between this one's products 61 us; 16 warps of 128 registers, each with a
+// tiles of 8 rows 77 us); 32 rows of each 46 us.  Tried: one barrier for both
+// halves (as fast; at 128 dimensions 32 sequences of 64 rows over 120-4000 keys
+// of 8 heads 96 us, 92 so); the next block's widening between this one's products
+// 61 us; 16 warps of 128 registers, each with a
 // quarter of the keys for S and of the dimensions for O, 69 us (the copies' and
 // the softmax's instructions then run in twice as many warps).
 #include "kv4_split.cuh"
@@ -65,10 +67,13 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
+// A barrier of the four warps of a half.
+__device__ __forceinline__ void half_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
 template <typename Sh, int NSEG>
 __global__ void __launch_bounds__(Sh::W * 32, 1)
 kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
-  constexpr int D = Sh::D, W = Sh::W, S = Sh::S, SUB = Sh::SUB, NP = Sh::NP, KT = Sh::KT, kBlk = Sh::kBlk;
+  constexpr int D = Sh::D, S = Sh::S, SUB = Sh::SUB, NP = Sh::NP, KT = Sh::KT, kBlk = Sh::kBlk;
   constexpr int kLineSwz = D == 256 ? 1 : 2;  // line u of a row: chunks XORed with u << this
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint8_t s_bad[2][2 * SUB];       // (block parity) 16-key parts without a good page
@@ -76,11 +81,13 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = lane >> 2, c = lane & 3;
-  // This warp's 16 rows and half of the keys (a tile of 32 rows is the work of
-  // warps 0-3, one on each scheduler); the quarter of K or V that it widens.
-  const int rg = warp >> 1, ks = warp & 1;
-  const int quarter = warp & 3;
-  const bool is_k = warp < 4;
+  // Warps 0-3 and 4-7 take a half of each block's keys each, and widen just
+  // that: they need not keep in step, so that one half's products run beside
+  // the other's widening.  A scheduler has a warp of either; of a tile of 32 rows
+  // it has one that multiplies.
+  const int ks = warp >> 2, rg = (warp & 3) ^ (2 * ks);  // half of the keys; 16 rows
+  const int quarter = 2 * ks + (warp & 1);               // of K or V, that the warp widens
+  const bool is_k = (warp & 3) < 2;
   const Kv4Start start = sc.cta[blockIdx.x];
   if (start.len <= 0) return;
   const uint32_t half0 = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
@@ -93,7 +100,7 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
   Place cs{start.tile, start.head, start.j, start.len, sc.tile[start.tile].nb};
   to_block(cs);
 
-  // ---- The copies' side: warps 0-3 copy the block's quarters of K, 4-7 of V.
+  // ---- The copies' side: a warp copies what it widens.
   Place cp = cs;
   int32_t page[NP];        // of the next block to copy
   // By stage: whether this lane's key is one that a row sees, and whether the 16
@@ -277,7 +284,7 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) widen(par, b);
       widen_end();
-      __syncthreads();  // the block is widened, and every warp done with the one before
+      half_sync(1 + ks);  // the half is widened, and its warps done with the one before
       if (active) {
         // The products' B fragments in order, K's steps and then V's, each read
         // two steps before its use.
@@ -478,6 +485,7 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
         if (has_b) p.part_lse[static_cast<int64_t>(slot) * Sh::kRows + nb] = Lb == 0.f ? -INFINITY : Mb + __log2f(Lb);
       }
     }
+    __syncthreads();  // read: the next segment's may come
   }
   copy_wait<0>();
 }
