@@ -218,12 +218,12 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
   float4* const mbuf = reinterpret_cast<float4*>(smem + 4 * Sh::kHalf + S * Sh::kStage) + rg * (D / 8) * 32 + lane;
   while (cs.rem > 0) {
     const Kv4Tile& tl = sc.tile[cs.e];
-    const int G = p.group;
+    const int G = p.group, head = cs.g;  // (`cs` moves on before the output is written)
     const int32_t j1 = min(cs.nb, cs.j + cs.rem);
     const bool active = rg * 16 < tl.nrows;
     const int last = tl.r0 + tl.nrows - 1;
     const int ra = tl.r0 + rg * 16 + g, rb = ra + 8;  // this lane's rows
-    auto row_at = [&](int r) { return (static_cast<int64_t>(tl.q0 + r / G) * p.hq + cs.g * G + r % G) * D; };
+    auto row_at = [&](int r) { return (static_cast<int64_t>(tl.q0 + r / G) * p.hq + head * G + r % G) * D; };
     // Keys each row sees (rows past the tile's last take its last row's; they
     // are not written), and every row does.
     const int32_t hi_a = tl.pos0 + min(ra, last) / G, hi_b = tl.pos0 + min(rb, last) / G;

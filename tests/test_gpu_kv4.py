@@ -560,6 +560,8 @@ ROWS = [
     ([1, 1, 1], [900, 1, 128], 64, 1, 64, 32, [0, 0, 33]),                       # single tokens, G = 64
     ([1, 1], [513, 31], 128, 1, 256, 64, None),                                  # G = 128: two tiles
     ([2, 1], [300, 20], 57, 1, 128, 64, None),                                   # G = 57: 114 rows
+    ([4, 8, 3], [8, 19, 33], 24, 3, 256, 16, None),                              # whole segments of three heads
+    ([8, 8], [19, 40], 24, 3, 128, 32, [0, 3]),
 ]
 
 
