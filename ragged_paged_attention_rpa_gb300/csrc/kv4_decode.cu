@@ -460,7 +460,9 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
           t0 = fmaxf(t0, 0.f);
           t1 = fmaxf(t1, 0.f);
           float n0 = m0[nt] + t0, n1 = m1[nt] + t1;
-          if (new0 || new1) {
+          // (For the whole warp: with a window, columns get their first score in
+          // different blocks, and the shuffles take every lane.)
+          if (__any_sync(0xffffffffu, new0 || new1)) {
             float s0 = -INFINITY, s1 = -INFINITY;
 #pragma unroll
             for (int h = 0; h < SUB; ++h) {

@@ -590,3 +590,17 @@ def test_tens_of_rows(case):
     seen = not (win and win[0] > 0 and kv[0] - ql[0] - (win[0] - 1) >= p)
     assert binding.rpa_get_device_error(r2.ws) == (binding.RPA_DEVERR_PAGE_ID if seen else 0)
     assert bool(torch.isfinite(bad).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("tokens", [3, 7, 14])
+def test_rows_that_see_their_first_key_in_different_blocks(d, tokens):
+    """Small windows over many positions: the rows of a tile begin in different
+    blocks, wherever a block's border lies."""
+    kv = [tokens + 20 + 5 * i for i in range(24)] + [1312]
+    b = batch([tokens] * 25, kv, 1, 1, d, 16, [17, 2, 5, 33, 9] * 5, seed=800 + tokens)
+    for kw in ({}, {"num_sms": 1}):
+        r = Kv4Batch(b, **kw)
+        out = r.call()
+        assert binding.rpa_get_device_error(r.ws) == 0
+        check(b, out)
