@@ -142,7 +142,7 @@ __device__ __forceinline__ float2 half2_floats(uint32_t h) {
 
 // 32 bytes from or to global memory: one access where they are 32-byte aligned
 // (two 16-byte ones, 32 bytes apart between lanes, touch every sector twice:
-// the read of 8192 rows of 16 heads of 256 took 37.5 us with them, 28.0 us so).
+// the read of 8192 rows of 16 heads of 256 took 37.5 us with them, 25.7 us so).
 __device__ __forceinline__ void load32(const void* src, bool whole, uint32_t (&w)[8]) {
   if (whole) {
     asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"

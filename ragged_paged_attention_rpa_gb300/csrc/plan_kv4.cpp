@@ -257,8 +257,8 @@ rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu, const int32_t* kv
   }
   // A mixed batch's split of the SMs between the two parts, as for 16-bit
   // pages: side by side where the split that evens their modelled times beats
-  // one after the other (512 single tokens and 4 chunks of 2048: 185 us at 41 /
-  // 111 SMs, 211 us one after the other).
+  // one after the other (512 single tokens and 4 chunks of 2048: 187 us at 39 /
+  // 113 SMs, 208 us one after the other).
   if (best.dec && best.pre && opts.decode_sms >= 0 && n >= 2) {
     int32_t x = opts.decode_sms > 0 ? std::min(opts.decode_sms, n - 1) : 0;
     best_t *= kBesideGain;

@@ -604,3 +604,21 @@ def test_rows_that_see_their_first_key_in_different_blocks(d, tokens):
         out = r.call()
         assert binding.rpa_get_device_error(r.ws) == 0
         check(b, out)
+
+
+@pytest.mark.parametrize("d,tokens", [(64, 5), (64, 12), (128, 5), (128, 12), (128, 40), (256, 6), (256, 30)])
+def test_a_nan_query_reaches_its_row_only(d, tokens):
+    b = batch([tokens, tokens], [300, 90], 1, 1, d, 16, seed=900 + tokens)
+    ref = reference(b)
+    rows = [1, tokens + 2]
+    b.q[rows, 0, 3] = 0x7FC0
+    r = Kv4Batch(b)
+    out = r.call().clone()
+    assert r.plan.info()["num_prefill_seqs"] == 0
+    assert bool(torch.isnan(out[rows]).all())
+    keep = np.ones(2 * tokens, bool)
+    keep[rows] = False
+    got = out.float().cpu().numpy().reshape(-1, d).astype(np.float64)
+    got[rows] = ref[0][rows]
+    assert np.isfinite(got[keep]).all()
+    check(b, torch.from_numpy(got), ref=ref)
