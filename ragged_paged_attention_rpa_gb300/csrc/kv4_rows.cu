@@ -153,7 +153,8 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int q = NP == 2 ? i : 0;  // (two groups of 16 keys are 512 bytes each)
-        copy_async(dst + warp * 1024 + i * 512 + (lane ^ (lane >> 3 & 1)) * 16, codes + row[q] * (D / 2) + (NP == 2 ? 0 : i * 512),
+        copy_async(dst + warp * 1024 + i * 512 + (lane ^ (lane >> 3 & 1)) * 16,
+                   codes + row[q] * (D / 2) + (NP == 2 ? 0 : i * 512),
                    ok[q] ? 16 : 0);
       }
       const bool upper = NP == 2 && lane >= 16, mine = upper ? ok[NP - 1] : ok[0];
