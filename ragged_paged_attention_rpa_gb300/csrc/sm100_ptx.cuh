@@ -314,19 +314,24 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 
+// The larger one, NaN if either is.
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // 2^x for a pair of arguments on the FMA pipe (no MUFU): Cody-Waite style
 // range reduction x = n + f with n = round(x) (the 1.5 * 2^23 shifter) and
 // f in [-0.5, 0.5], a degree-3 polynomial for 2^f whose coefficients are a
 // relative-error minimax fit computed for this library (max relative error
 // 7.5e-5, ample for P that is rounded to bf16), and 2^n added into the
 // exponent field.  Arguments below -125 (including -inf, a masked score)
-// give exactly 0.
+// give exactly 0, NaN gives NaN: for both the polynomial's bits mean nothing
+// and max(x, 0), which keeps NaN, is taken instead.
 __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
   float a0, b0;
   f2_unpack(x2, a0, b0);
-  const float a = fmaxf(a0, -125.f);
-  const float b = fmaxf(b0, -125.f);
-  x2 = f2_pack(a, b);
   const uint64_t shifter = f2_pack(12582912.f, 12582912.f);
   const uint64_t t2 = f2_add(x2, shifter);
   const uint64_t n2 = f2_add(t2, f2_pack(-12582912.f, -12582912.f));
@@ -337,8 +342,8 @@ __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
   float pa, pb, ta, tb;
   f2_unpack(p, pa, pb);
   f2_unpack(t2, ta, tb);
-  pa = a0 < -125.f ? 0.f : __int_as_float(__float_as_int(pa) + (__float_as_int(ta) << 23));
-  pb = b0 < -125.f ? 0.f : __int_as_float(__float_as_int(pb) + (__float_as_int(tb) << 23));
+  pa = a0 >= -125.f ? __int_as_float(__float_as_int(pa) + (__float_as_int(ta) << 23)) : fmax_nan(a0, 0.f);
+  pb = b0 >= -125.f ? __int_as_float(__float_as_int(pb) + (__float_as_int(tb) << 23)) : fmax_nan(b0, 0.f);
   return f2_pack(pa, pb);
 }
 
