@@ -30,8 +30,9 @@
 // Scores, maxima, sums and O are fp32.
 //
 // A key no row of the tile sees has its V scale set to zero (its bytes may be
-// anything, a NaN scale included) and its scores replaced by -inf.  A bad page
-// id sets the error word; its keys count as not seen.
+// anything, a NaN scale included) and its scores replaced by -inf; a NaN at a key
+// that only some rows see reaches those alone (kv4_split.cuh).  A bad page id
+// sets the error word; its keys count as not seen.
 //
 // What bounds it: 0.5625 bytes an element come from HBM, and each element
 // costs about one issue slot in 32 (widen, scale, multiply).  Long contexts run
@@ -337,6 +338,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
     const int32_t seg_hi = tl.pos0 + (tl.r0 + tl.nrows - 1) / G;
     // Keys every row sees.
     const int32_t all_lo = first_visible(seg_hi, tl.window), all_hi = tl.pos0 + tl.r0 / G;
+    uint32_t nan_seen = 0;  // scales of NaN taken out (kv4_split.cuh)
 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -529,12 +531,16 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
             sv[i] = lds_u8(part + Sh::kSOff + D + kk * (D / 16) + (D == 128 ? g : g >> 1));
         }
         if (edge) {
-          // Keys no row sees: whatever their bytes, their values are zeros.
+          // Keys no row sees: whatever their bytes, their values are zeros.  A NaN
+          // of a key that some do not see is put into the others' rows at the end.
           const int32_t seg_lo = first_visible(all_hi, tl.window);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int32_t key = key0 + 16 * h + 2 * c + (i & 1) + 8 * (i >> 1);
             if (((bad >> h) & 1u) || key < seg_lo || key > seg_hi) sv[i] = 0;
+            const uint32_t nan = key < all_lo || key > all_hi ? nan_bytes(sv[i]) : 0u;
+            sv[i] = without_nan(sv[i], nan);
+            nan_seen |= nan;
           }
         }
 #pragma unroll
@@ -563,6 +569,28 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
     }
 
     // ---- The segment's end in this warp's range.
+    if (__any_sync(0xffffffffu, nan_seen != 0)) {
+      uint32_t hit[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) hit[nt][0] = hit[nt][1] = 0;
+      each_uneven_nan<D>(p, tl.seq, cs.g, max((tl.fb + cs.j) * kBlk, first_visible(all_hi, tl.window)),
+                         min((tl.fb + j1) * kBlk - 1, seg_hi), all_lo, all_hi, [&](int32_t key, uint32_t blocks) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int32_t hi = tl.pos0 + min(tl.r0 + 8 * nt + 2 * c + i, tl.r0 + tl.nrows - 1) / G;
+            if (key <= hi && key >= first_visible(hi, tl.window)) hit[nt][i] |= blocks;
+          }
+      });
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)  // dimensions g (D / 8) + 2 t and the next
+            if (hit[nt][i] >> ((g * (D / 8) + 2 * t) / 16) & 1u) o[t][nt][i] = o[t][nt][2 + i] = quiet_nan();
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

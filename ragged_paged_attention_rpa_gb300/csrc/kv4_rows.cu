@@ -78,6 +78,7 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint8_t s_bad[2][2 * SUB];       // (block parity) 16-key parts without a good page
   __shared__ float s_m[Sh::kRows], s_l[Sh::kRows];
+  __shared__ int32_t s_nan;                   // last segment with a NaN taken out of V (kv4_split.cuh)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = lane >> 2, c = lane & 3;
@@ -90,6 +91,8 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
   const bool is_k = (warp & 3) < 2;
   const Kv4Start start = sc.cta[blockIdx.x];
   if (start.len <= 0) return;
+  if (tid == 0) s_nan = -1;
+  __syncthreads();
   const uint32_t half0 = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
   const uint32_t ring = half0 + 4 * Sh::kHalf;
 
@@ -219,6 +222,7 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
   float4* const mbuf = reinterpret_cast<float4*>(smem + 4 * Sh::kHalf + S * Sh::kStage) + rg * (D / 8) * 32 + lane;
   while (cs.rem > 0) {
     const Kv4Tile& tl = sc.tile[cs.e];
+    const int32_t seg = cs.e * p.hkv + cs.g;
     const int G = p.group, head = cs.g;  // (`cs` moves on before the output is written)
     const int32_t j1 = min(cs.nb, cs.j + cs.rem);
     const bool active = rg * 16 < tl.nrows;
@@ -281,9 +285,19 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
 
     for (int32_t j = cs.j; j < j1; ++j) {
       const int32_t key0 = (tl.fb + j) * kBlk;
+      bool edge = key0 < all_lo || key0 + kBlk - 1 > all_hi;
       widen_begin(par);
 #pragma unroll
       for (int b = 0; b < 4; ++b) widen(par, b);
+      if (edge && !is_k && (key0 + wkey < all_lo || key0 + wkey > all_hi)) {
+        // A NaN of V at a key that not every row sees: once more without it.
+        if (const uint32_t nan = nan_bytes(wscale)) {
+          wscale = without_nan(wscale, nan);
+          s_nan = seg;
+#pragma unroll 1
+          for (int b = 0; b < 4; ++b) widen(par, b);
+        }
+      }
       widen_end();
       half_sync(1 + ks);  // the half is widened, and its warps done with the one before
       if (active) {
@@ -325,7 +339,6 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
         }
         // ---- Online softmax, the references raised where a score passes them by 2^8.
         const int32_t mykey0 = key0 + ks * (kBlk / 2);
-        bool edge = key0 < all_lo || key0 + kBlk - 1 > all_hi;
         uint32_t bad = 0;
 #pragma unroll
         for (int h = 0; h < SUB; ++h) bad |= static_cast<uint32_t>(s_bad[par][ks * SUB + h]) << h;
@@ -428,6 +441,7 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
 
     // ---- The segment's end in this range: the halves of the keys meet.
     const bool whole = cs.j == 0 && j1 == cs.nb;
+    const int32_t key_from = (tl.fb + cs.j) * kBlk, key_to = (tl.fb + j1) * kBlk - 1;
     const int32_t slot = 2 * blockIdx.x + (cs.e == start.tile && cs.g == start.head ? 0 : 1);
     cs.rem -= j1 - cs.j;
     cs.j = j1;
@@ -451,6 +465,16 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
     }
     __syncthreads();
     if (ks == 0 && active) {
+      if (s_nan == seg)
+        each_uneven_nan<D>(p, tl.seq, head, max(key_from, first_visible(all_hi, tl.window)),
+                           min(key_to, tl.pos0 + last / G), all_lo, all_hi, [&](int32_t key, uint32_t blocks) {
+          const uint32_t in_a = key >= lo_a && key <= hi_a ? blocks : 0u, in_b = key >= lo_b && key <= hi_b ? blocks : 0u;
+#pragma unroll
+          for (int t = 0; t < D / 8; ++t) {
+            if (in_a >> (t >> 1) & 1u) o[t][0] = o[t][1] = quiet_nan();
+            if (in_b >> (t >> 1) & 1u) o[t][2] = o[t][3] = quiet_nan();
+          }
+        });
       const float ma2 = s_m[rg * 16 + g], mb2 = s_m[rg * 16 + g + 8];
       const float Ma = fmaxf(m_a, ma2), Mb = fmaxf(m_b, mb2);
       float fa = fast_exp2(m_a - Ma), fa2 = fast_exp2(ma2 - Ma);

@@ -127,6 +127,53 @@ __device__ __forceinline__ uint32_t bit_select(uint32_t m, uint32_t a, uint32_t 
   return r;
 }
 
+// NaN in V at keys that some rows of a tile see and others do not.  In the
+// product it would reach every row (0 times NaN), so such scales are zeroed as
+// the block is widened, and a segment that had one looks its uneven keys'
+// scales up again at its end and puts the NaN into the rows that see them.
+
+// The top bits of the bytes of w that are 255 (scales that read as NaN); and w
+// without those bytes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & w & 0x80808080u;
+}
+__device__ __forceinline__ uint32_t without_nan(uint32_t w, uint32_t nan) { return w & ~((nan >> 7) * 255u); }
+
+// The 16-dimension blocks of `key`'s row of V that read as NaN, a bit each.
+template <int D>
+__device__ __forceinline__ uint32_t nan_blocks(const Kv4Params& p, int32_t seq, int32_t head, int32_t key) {
+  const int32_t slot = key >> p.page_shift;
+  if (slot >= p.mpps) return 0;
+  const int32_t page = __ldg(p.page_table + static_cast<int64_t>(seq) * p.mpps + slot);
+  if (page < 0 || page >= p.num_pages) return 0;
+  const int64_t row = ((static_cast<int64_t>(page) * p.hkv + head) << p.page_shift) +
+                      (key & ((1 << p.page_shift) - 1));
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(p.vs + row * (D / 16));
+  uint32_t blocks = 0;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const uint32_t nan = nan_bytes(__ldg(w + i));
+    blocks |= ((nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) | (nan >> 28 & 8u)) << (4 * i);
+  }
+  return blocks;
+}
+
+// Calls f(key, blocks) for the keys in [first, last] with such blocks that not
+// every row sees (every row sees [all_lo, all_hi]).
+template <int D, typename F>
+__device__ __forceinline__ void each_uneven_nan(const Kv4Params& p, int32_t seq, int32_t head, int32_t first,
+                                                int32_t last, int32_t all_lo, int32_t all_hi, F&& f) {
+#pragma unroll 1
+  for (int32_t key = first; key <= last; ++key) {
+    if (key >= all_lo && key <= all_hi) {
+      key = all_hi;
+      continue;
+    }
+    if (const uint32_t blocks = nan_blocks<D>(p, seq, head, key)) f(key, blocks);
+  }
+}
+__device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7fffffffu); }
+
 // The column reference before any score: below every scaled score that is not
 // -inf itself, and small enough that a score minus it is still finite.
 constexpr float kNoScore = -1e38f;

@@ -84,3 +84,68 @@ def test_a_nan_key_of_16_bit_pages_reaches_the_prompt_rows_that_see_it(d, pairs,
     got = db.forward(plan, ws).float().cpu().numpy()
     assert binding.rpa_get_device_error(ws) == 0
     assert np.array_equal(np.isnan(got), want)
+
+
+# ---------------------------------------------------------------- NaN values
+
+VALUES = [
+    # (q_lens, kv_lens, Hq, Hkv, D, P, windows, num_sms): what holds the rows
+    ([3, 2], [300, 40], 2, 2, 64, 16, None, 0),                       # tiles of 8
+    ([4, 16], [70, 500], 3, 1, 64, 32, [0, 9], 0),                    # of 16, of 64
+    ([12, 7, 1], [513, 100, 30], 1, 1, 128, 16, [0, 5, 0], 0),        # of 16, of 8
+    ([6, 4], [4000, 130], 4, 2, 128, 64, None, 0),                    # of 16, cut over CTAs
+    ([8, 5], [700, 90], 1, 1, 256, 128, [0, 3], 0),                   # of 8
+    ([5, 16], [90, 3000], 3, 1, 256, 16, None, 0),                    # two of 8; of 64
+    ([40, 33], [2000, 33], 1, 1, 128, 64, [0, 6], 0),                 # of 64
+    ([20, 30], [300, 65], 2, 2, 256, 16, [0, 9], 0),
+    ([16, 9], [5000, 70], 4, 1, 64, 16, [700, 0], 0),
+    ([3] * 30, [50 + 9 * i for i in range(30)], 2, 1, 128, 16, None, 1),  # whole segments, one CTA
+    ([5] * 30, [50 + 9 * i for i in range(30)], 8, 2, 64, 16, None, 1),
+]
+
+
+def nan_values(ql, kv, hq, hkv, d, p, win, sms, seed):
+    """A block of V that reads as NaN makes NaN its 16 dimensions of the rows
+    that see its key, and nothing else: not the rows for which the key lies in
+    the future or before the window."""
+    b = batch(ql, kv, hq, hkv, d, p, win, seed=seed)
+    ref = reference(b)
+    want = np.zeros((b.q.shape[0], hq, d), bool)
+    group = hq // hkv
+    rng = np.random.default_rng(seed)
+    for s in range(len(ql)):
+        if s % 3 == 2:
+            continue
+        first = kv[s] - ql[s]
+        keys = {kv[s] - 1, first + ql[s] // 2, min(kv[s] - 1, first + 1), max(0, first - 3), int(rng.integers(0, kv[s]))}
+        see = sees(b, s)
+        for key in sorted(keys):
+            g, blk = int(rng.integers(0, hkv)), int(rng.integers(0, d // 16))
+            page, at = slot(b, s, key)
+            b.v_fp4_scale[page, g, at, blk] = 255
+            rows = b.cu_q_lens[s] + np.nonzero(see[:, key])[0]
+            want[rows, g * group:(g + 1) * group, 16 * blk:16 * blk + 16] = True
+    assert want.any() and not want.all()
+    r = Kv4Batch(b, num_sms=sms)
+    prefill = r.plan.info()["num_prefill_seqs"] > 0
+    assert prefill == (max(ql) * group > 128)
+    out = r.call().clone()
+    assert binding.rpa_get_device_error(r.ws) == 0
+    check_nan(b, out, want, ref, prefill)
+    # Without them, on the same workspace, nothing of it is left.
+    good = batch(ql, kv, hq, hkv, d, p, win, seed=seed)
+    r.pool[3].copy_(cuda(good.v_fp4_scale))
+    check(good, r.call(), prefill=prefill, ref=ref)
+    # In a captured call, with and without.
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r.call()
+    for scales, expect in ((b, want), (good, np.zeros_like(want)), (b, want)):
+        r.pool[3].copy_(cuda(scales.v_fp4_scale))
+        graph.replay()
+        check_nan(b, r.out, expect, ref, prefill)
+
+
+@pytest.mark.parametrize("case", range(len(VALUES)))
+def test_a_nan_value_reaches_the_rows_that_see_it(case):
+    nan_values(*VALUES[case], seed=1000 + case)
