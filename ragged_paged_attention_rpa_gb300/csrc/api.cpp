@@ -620,6 +620,8 @@ rpa_status_t rpa_forward_kv4(const void* q, const uint8_t* k_pages, const uint8_
     b.k_pages = a.workspace + p.off_kv4_k;
     b.v_pages = a.workspace + p.off_kv4_v;
     b.page_table = reinterpret_cast<const int32_t*>(a.workspace + p.off_kv4_table);
+    b.kv4_page_table = a.page_table;
+    b.kv4_num_pages = p.num_pages;
     return rpa::launch_prefill_tc(*p.kv4_prefill, b, s);
   };
   if (p.overlap) return side_by_side(stream, decode, prefill);

@@ -60,6 +60,26 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
 }
 
+// The top bits of the bytes of w that are 255 (scales that read as NaN); and w
+// without those bytes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & w & 0x80808080u;
+}
+__device__ __forceinline__ uint32_t without_nan(uint32_t w, uint32_t nan) { return w & ~((nan >> 7) * 255u); }
+
+// The blocks of a row of D dimensions that read as NaN, a bit each, from its
+// scale bytes.
+template <int D>
+__device__ __forceinline__ uint32_t nan_blocks(const uint8_t* scales) {
+  uint32_t blocks = 0;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const uint32_t nan = nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(scales) + i));
+    blocks |= ((nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) | (nan >> 28 & 8u)) << (4 * i);
+  }
+  return blocks;
+}
+
 // Eight codes (lowest four bits first) of eight floats: round to nearest even,
 // at most 6.
 __device__ __forceinline__ uint32_t encode8(const float* x) {

@@ -538,8 +538,8 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
           for (int i = 0; i < 4; ++i) {
             const int32_t key = key0 + 16 * h + 2 * c + (i & 1) + 8 * (i >> 1);
             if (((bad >> h) & 1u) || key < seg_lo || key > seg_hi) sv[i] = 0;
-            const uint32_t nan = key < all_lo || key > all_hi ? nan_bytes(sv[i]) : 0u;
-            sv[i] = without_nan(sv[i], nan);
+            const uint32_t nan = key < all_lo || key > all_hi ? kv4::nan_bytes(sv[i]) : 0u;
+            sv[i] = kv4::without_nan(sv[i], nan);
             nan_seen |= nan;
           }
         }

@@ -6,7 +6,10 @@
 // the keys the sequences' queries see are widened once, to scratch pages in
 // the workspace ([page][slot][head][dim], the bf16 pool's layout) with a page
 // table of their own, and the prefill runs on those.  The values are exact in
-// bf16 (six significant bits).
+// bf16 (six significant bits).  A block of V that reads as NaN becomes zeros (in
+// the product it would reach the rows that do not see its key, 0 times NaN) and
+// sets a word of the header, on which the prefill's epilogue looks the scales up
+// for each row.
 //
 // One thread per 16 dimensions of K and of V; HBM-bound: 0.5625 bytes an
 // element read, 2 written (and the prefill reads them back from L2 or HBM).  A
@@ -49,6 +52,7 @@ kv4_expand_kernel(const ExpandParams p, const __grid_constant__ ExpandList list)
   const int64_t rows = (static_cast<int64_t>(list.page_end - first) << p.page_shift) * p.hkv;
   const int64_t row0 = (static_cast<int64_t>(first) << p.page_shift) * p.hkv;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+  bool v_nan = false;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < rows << p.bpr_shift; i += step) {
     const uint32_t row = static_cast<uint32_t>(i >> p.bpr_shift);
     const int32_t b = static_cast<int32_t>(i) & ((1 << p.bpr_shift) - 1);
@@ -76,12 +80,14 @@ kv4_expand_kernel(const ExpandParams p, const __grid_constant__ ExpandList list)
     const int64_t dst = 2 * ((row0 << p.bpr_shift) + i);
     const uint2 kc = __ldg(p.k + src), vc = __ldg(p.v + src);
     const uint32_t ks = __ldg(p.ks + src), vs = __ldg(p.vs + src);
+    v_nan |= vs == 255u;
     uint32_t w[8];  // the workspace's arrays are 256-byte aligned
     kv4::decode_block_bf16(kc, ks, w);
     kv4::store32(p.k_out + dst, true, w);
-    kv4::decode_block_bf16(vc, vs, w);
+    kv4::decode_block_bf16(vc, vs == 255u ? 0u : vs, w);
     kv4::store32(p.v_out + dst, true, w);
   }
+  if (v_nan) *reinterpret_cast<int32_t*>(p.ws + kKv4NanOff) = 1;
 }
 
 }  // namespace

@@ -291,8 +291,8 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
       for (int b = 0; b < 4; ++b) widen(par, b);
       if (edge && !is_k && (key0 + wkey < all_lo || key0 + wkey > all_hi)) {
         // A NaN of V at a key that not every row sees: once more without it.
-        if (const uint32_t nan = nan_bytes(wscale)) {
-          wscale = without_nan(wscale, nan);
+        if (const uint32_t nan = kv4::nan_bytes(wscale)) {
+          wscale = kv4::without_nan(wscale, nan);
           s_nan = seg;
 #pragma unroll 1
           for (int b = 0; b < 4; ++b) widen(par, b);

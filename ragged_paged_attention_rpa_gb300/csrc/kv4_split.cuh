@@ -132,13 +132,6 @@ __device__ __forceinline__ uint32_t bit_select(uint32_t m, uint32_t a, uint32_t 
 // the block is widened, and a segment that had one looks its uneven keys'
 // scales up again at its end and puts the NaN into the rows that see them.
 
-// The top bits of the bytes of w that are 255 (scales that read as NaN); and w
-// without those bytes.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  return ((w & 0x7f7f7f7fu) + 0x01010101u) & w & 0x80808080u;
-}
-__device__ __forceinline__ uint32_t without_nan(uint32_t w, uint32_t nan) { return w & ~((nan >> 7) * 255u); }
-
 // The 16-dimension blocks of `key`'s row of V that read as NaN, a bit each.
 template <int D>
 __device__ __forceinline__ uint32_t nan_blocks(const Kv4Params& p, int32_t seq, int32_t head, int32_t key) {
@@ -148,14 +141,7 @@ __device__ __forceinline__ uint32_t nan_blocks(const Kv4Params& p, int32_t seq, 
   if (page < 0 || page >= p.num_pages) return 0;
   const int64_t row = ((static_cast<int64_t>(page) * p.hkv + head) << p.page_shift) +
                       (key & ((1 << p.page_shift) - 1));
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(p.vs + row * (D / 16));
-  uint32_t blocks = 0;
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const uint32_t nan = nan_bytes(__ldg(w + i));
-    blocks |= ((nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) | (nan >> 28 & 8u)) << (4 * i);
-  }
-  return blocks;
+  return kv4::nan_blocks<D>(p.vs + row * (D / 16));
 }
 
 // Calls f(key, blocks) for the keys in [first, last] with such blocks that not

@@ -57,6 +57,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "kv4.cuh"
 #include "rpa_internal.h"
 #include "sm100_ptx.cuh"
 
@@ -123,6 +124,21 @@ struct PrefillParams {
   float* ppart_lse;    // [slot][kBM]
   int32_t out_v8;      // `out` is 32-byte aligned: the epilogue stores 32 bytes at once
   int32_t v_4d;        // tm_v is 4-D (chunks outermost): one box per V stage
+};
+
+// What the kernel has beside (last of its parameters, so that the others lie
+// where they did): nothing, or over widened 4-bit pages (kv4_expand.cu) the
+// 4-bit pages' V scales, table and number, by which the epilogue finds the rows
+// that see a NaN in V.
+struct Pages16 {
+  static constexpr bool kKv4 = false;
+};
+struct Pages4 {
+  static constexpr bool kKv4 = true;
+  const uint8_t* v_scales;
+  const int32_t* page_table;
+  int32_t num_pages;
+  int32_t last_launch;  // no launch of this call follows
 };
 
 // One 32-byte store (eight 32-bit words) to a 32-byte aligned address.
@@ -284,6 +300,40 @@ __device__ __forceinline__ void leave_item_counter(unsigned char* ws) {
     atomicExch(&ctr[1], 0);
   }
 }
+// The same over widened 4-bit pages, with the word that the widening sets, which
+// the last CTA of the call's last launch (a dynamic list has one) sets back.
+__device__ __forceinline__ void leave_kv4(unsigned char* ws, bool dyn, bool last_launch) {
+  int32_t* ctr = reinterpret_cast<int32_t*>(ws + kPrefillCounterOff);
+  int32_t* nan = reinterpret_cast<int32_t*>(ws + kKv4NanOff);
+  if (!dyn && !last_launch) return;
+  __threadfence();
+  if (atomicAdd(dyn ? &ctr[1] : &nan[1], 1) == static_cast<int32_t>(gridDim.x) - 1) {
+    if (dyn) atomicExch(&ctr[0], 0);
+    atomicExch(dyn ? &ctr[1] : &nan[1], 0);
+    atomicExch(&nan[0], 0);
+  }
+}
+
+// The 16-dimension blocks in which keys [lo, pos] of the item's sequence and
+// head hold a NaN in V, from the 4-bit pages' scales.  (Run only where the
+// widening met one.)
+template <int D>
+__device__ __noinline__ uint32_t kv4_nan_blocks(const uint8_t* v_scales, const int32_t* table_row, int32_t num_pages,
+                                                int32_t page_shift, int32_t hkv, int32_t head, int32_t lo,
+                                                int32_t pos) {
+  uint32_t blocks = 0;
+  for (int32_t key = lo; key <= pos;) {
+    const int32_t page = __ldg(table_row + (key >> page_shift));
+    const int32_t in = key & ((1 << page_shift) - 1), n = min((1 << page_shift) - in, pos - key + 1);
+    if (page >= 0 && page < num_pages) {
+      const uint8_t* row = v_scales + (((static_cast<int64_t>(page) * hkv + head) << page_shift) + in) * (D / 16);
+#pragma unroll 4
+      for (int32_t i = 0; i < n; ++i) blocks |= kv4::nan_blocks<D>(row + i * (D / 16));
+    }
+    key += n;
+  }
+  return blocks;
+}
 
 // Zero rows [0, a) and [b, kVKeys) of a V stage ([chunk][kVKeys rows][128 B]),
 // then order the stores before the tensor core's reads (whole warp).  Out of
@@ -319,11 +369,12 @@ __device__ __forceinline__ bool take_item(Barriers& B, uint32_t& R, ItemSlot& e,
   return true;
 }
 
-template <int D>
+template <int D, typename Pages>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const PrefillParams p,
-                  const __grid_constant__ ItemList items) {
+                  const __grid_constant__ ItemList items, const __grid_constant__ Pages x) {
+  constexpr bool kKv4 = Pages::kKv4;
   using Lay = Layout<D>;
   // The 128-byte swizzle needs 1024-byte aligned tiles; the layout fills
   // the shared memory with no slack, so a misaligned base ends the launch.
@@ -331,7 +382,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   if (smem_addr(smem_raw) & 1023u) {
     if (threadIdx.x == 0) {
       report_error(p.ws, RPA_DEVERR_LAUNCH, blockIdx.x);
-      if (items.dyn) leave_item_counter(p.ws);
+      if constexpr (kKv4)
+        leave_kv4(p.ws, items.dyn, x.last_launch);
+      else if (items.dyn)
+        leave_item_counter(p.ws);
     }
     return;
   }
@@ -851,6 +905,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     const int tok = r / G, head = r % G;
     const float* l_s = reinterpret_cast<const float*>(smem + Lay::kLOff);
+    bool look_for_nan = false;   // the widening of 4-bit pages met one in V
+    if constexpr (kKv4) look_for_nan = *reinterpret_cast<const volatile int32_t*>(p.ws + kKv4NanOff) != 0;
     uint32_t T = 0, L = 0;                              // tiles, items taken over
     bool alive = true;
     uint32_t R = 0;
@@ -898,6 +954,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
         }
       } else {
+        uint32_t nan = 0;  // blocks of 16 dimensions that hold a NaN for this row
+        if constexpr (kKv4) {
+          if (look_for_nan && valid) {
+            const int32_t pos = gm.pos_first + tok;
+            nan = kv4_nan_blocks<D>(x.v_scales, x.page_table + static_cast<int64_t>(gm.seq) * p.mpps, x.num_pages,
+                                    p.page_shift, p.hq / G, gm.g, first_visible(pos, gm.W), pos);
+          }
+        }
         __nv_bfloat16* orow =
             p.out + (static_cast<int64_t>(gm.t0 + tok) * p.hq + gm.g * G + head) * D;
         // Each thread writes 32 bytes of its own row per 16 columns (one
@@ -909,6 +973,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             w[q] = pack_bf16x2(__uint_as_float(o[2 * q]) * inv, __uint_as_float(o[2 * q + 1]) * inv);
+          if constexpr (kKv4)
+            if (nan >> (col >> 4) & 1u) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) w[q] = 0x7fff7fffu;
+            }
           if (p.out_v8) {
             st_global_v8(orow + col, w);
           } else {
@@ -943,7 +1012,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     tc_fence_after();
     tmem_dealloc(tmem, Lay::kCols);
   }
-  if (threadIdx.x == 0 && items.dyn) leave_item_counter(p.ws);
+  if constexpr (kKv4) {
+    if (threadIdx.x == 0) leave_kv4(p.ws, items.dyn, x.last_launch);
+  } else {
+    if (threadIdx.x == 0 && items.dyn) leave_item_counter(p.ws);
+  }
 }
 
 struct SplitList {
@@ -1031,10 +1104,10 @@ int launch_prefill_combine(const Plan& plan, const PrefillParams& p, cudaStream_
   return 0;
 }
 
-template <int D>
+template <int D, typename Pages>
 int launch_prefill_t(const Plan& plan, const Args& a, cudaStream_t stream) {
   using Lay = Layout<D>;
-  if (int e = ensure_dynamic_smem(reinterpret_cast<const void*>(prefill_tc_kernel<D>), Lay::kBytes))
+  if (int e = ensure_dynamic_smem(reinterpret_cast<const void*>(prefill_tc_kernel<D, Pages>), Lay::kBytes))
     return e;
   const int G = plan.hq / plan.hkv;
   const int qb = plan.q_block;
@@ -1094,13 +1167,20 @@ int launch_prefill_t(const Plan& plan, const Args& a, cudaStream_t stream) {
       list.n_ctas = grid;
       for (int c = 0; c <= grid; ++c) list.cta0[c] = plan.pcta0[c];
     }
-    prefill_tc_kernel<D><<<grid, kThreads, Lay::kBytes, stream>>>(tq, tk, tv, p, list);
+    Pages x;
+    if constexpr (Pages::kKv4) x = Pages{a.v_block_scales, a.kv4_page_table, a.kv4_num_pages, off + cnt == n};
+    prefill_tc_kernel<D, Pages><<<grid, kThreads, Lay::kBytes, stream>>>(tq, tk, tv, p, list, x);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return static_cast<int>(e);
     trace_mark(RPA_KERNEL_PREFILL_TC, stream);
   }
   if (!plan.psplit.empty()) return launch_prefill_combine<D>(plan, p, stream);
   return 0;
+}
+
+template <int D>
+int launch_prefill_d(const Plan& plan, const Args& a, cudaStream_t stream) {
+  return a.kv4_page_table ? launch_prefill_t<D, Pages4>(plan, a, stream) : launch_prefill_t<D, Pages16>(plan, a, stream);
 }
 
 }  // namespace
@@ -1117,9 +1197,9 @@ int prefill_tokens_per_block(int32_t, int32_t group) { return group >= kBM ? 1 :
 int launch_prefill_tc(const Plan& plan, const Args& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (plan.d) {
-    case 64: return launch_prefill_t<64>(plan, a, s);
-    case 128: return launch_prefill_t<128>(plan, a, s);
-    case 256: return launch_prefill_t<256>(plan, a, s);
+    case 64: return launch_prefill_d<64>(plan, a, s);
+    case 128: return launch_prefill_d<128>(plan, a, s);
+    case 256: return launch_prefill_d<256>(plan, a, s);
     default: return static_cast<int>(cudaErrorInvalidValue);
   }
 }

@@ -28,6 +28,9 @@ constexpr size_t kPrefillCounterOff = 64;
 // Offset in the header of the table kernels' counter (one int32: CTAs
 // finished), zero between launches.
 constexpr size_t kTablesCounterOff = 128;
+// Offset in the header of the 4-bit prompts' words (two int32: whether the
+// widening met a NaN in V, CTAs finished), zero between calls.
+constexpr size_t kKv4NanOff = 192;
 // Most requests, pages and tokens of a table call (its loop indices add a grid's
 // threads to them in 31 bits).
 constexpr int32_t kTablesMost = 1 << 30;
@@ -245,6 +248,9 @@ struct Args {
   const float* v_scale = nullptr;
   const uint8_t* k_block_scales = nullptr;  // 4-bit pages: a scale byte per 16 dimensions
   const uint8_t* v_block_scales = nullptr;
+  // The prefill over widened 4-bit pages: the 4-bit pages' table and number.
+  const int32_t* kv4_page_table = nullptr;
+  int32_t kv4_num_pages = 0;
 };
 
 // Kernel launchers; each returns cudaError_t as int (0 = success).

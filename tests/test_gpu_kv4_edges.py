@@ -104,7 +104,7 @@ VALUES = [
 ]
 
 
-def nan_values(ql, kv, hq, hkv, d, p, win, sms, seed):
+def nan_values(ql, kv, hq, hkv, d, p, win, sms, seed, **plan_kw):
     """A block of V that reads as NaN makes NaN its 16 dimensions of the rows
     that see its key, and nothing else: not the rows for which the key lies in
     the future or before the window."""
@@ -126,12 +126,13 @@ def nan_values(ql, kv, hq, hkv, d, p, win, sms, seed):
             rows = b.cu_q_lens[s] + np.nonzero(see[:, key])[0]
             want[rows, g * group:(g + 1) * group, 16 * blk:16 * blk + 16] = True
     assert want.any() and not want.all()
-    r = Kv4Batch(b, num_sms=sms)
+    r = Kv4Batch(b, num_sms=sms, **plan_kw)
     prefill = r.plan.info()["num_prefill_seqs"] > 0
     assert prefill == (max(ql) * group > 128)
     out = r.call().clone()
     assert binding.rpa_get_device_error(r.ws) == 0
     check_nan(b, out, want, ref, prefill)
+    assert bool((r.ws[:256] == 0).all())             # words of the header back at zero
     # Without them, on the same workspace, nothing of it is left.
     good = batch(ql, kv, hq, hkv, d, p, win, seed=seed)
     r.pool[3].copy_(cuda(good.v_fp4_scale))
@@ -149,3 +150,19 @@ def nan_values(ql, kv, hq, hkv, d, p, win, sms, seed):
 @pytest.mark.parametrize("case", range(len(VALUES)))
 def test_a_nan_value_reaches_the_rows_that_see_it(case):
     nan_values(*VALUES[case], seed=1000 + case)
+
+
+# ---------------------------------------------------------------- NaN values of prompts
+
+PROMPT_VALUES = [
+    ([200, 1], [333, 50], 2, 2, 128, 16, None, 0),                    # prompts
+    ([150, 140], [150, 400], 8, 1, 256, 128, [0, 33], 0),
+    ([300, 129], [300, 700], 4, 2, 64, 16, [7, 0], 0),
+    ([260], [260], 128, 1, 64, 32, [100], 0),                         # G = 128
+]
+
+
+@pytest.mark.parametrize("dynamic", [0, -1])
+@pytest.mark.parametrize("case", range(len(PROMPT_VALUES)))
+def test_a_nan_value_reaches_the_prompt_rows_that_see_it(case, dynamic):
+    nan_values(*PROMPT_VALUES[case], seed=1050 + case, prefill_dynamic=dynamic)
