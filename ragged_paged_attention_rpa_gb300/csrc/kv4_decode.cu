@@ -11,8 +11,9 @@
 // end: each runs, per block of 16 keys,
 //     S^T[16 keys x rows] = K . Q^T        (mma.m16n8k16, f16 -> fp32)
 //     O^T[D x rows]     += V^T . P^T
-// with an online softmax whose reference grows only when a score passes it by
-// 2^8 (the probabilities stay below 256, exact in the sums' fp32).
+// with an online softmax whose reference is 10 below the largest score when it
+// is raised, which is when a score passes it by 15 (kv4_split.cuh: the
+// probabilities stay at or below 2^15).
 //
 // Layout.  A product's order of terms is free, so which dimension a fragment's
 // k index means is chosen such that a lane needs a contiguous run of bytes: of
@@ -26,7 +27,8 @@
 // Numbers.  Codes widen to f16 exactly, and times their scale they are still
 // exact.  Q is bf16 made f16 after a power of two for the row (its largest
 // element in [1, 2)): what rounds is below 2^-25 of the row's largest element.
-// P is rounded to f16 (half a step: 2^-12 of itself) for the second product.
+// P is rounded to f16 for the second product: at most 2^-11 of itself down to
+// 2^-24 of the score that the reference was raised for, 2^-35 of that below.
 // Scores, maxima, sums and O are fp32.
 //
 // A key no row of the tile sees has its V scale set to zero (its bytes may be
@@ -409,7 +411,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
             x[h][nt][i] = CH == 2 ? acc[0][nt][i] + acc[CH - 1][nt][i] : acc[0][nt][i];
       }
       // ---- Online softmax: exponents against the columns' references; where
-      // one passes 8, the references are raised first.
+      // one passes kRaiseAt, the references are raised first.
       float y[SUB][NT][4];
       auto exponents = [&]() {
 #pragma unroll
@@ -448,7 +450,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
           top = fmaxf(fmaxf(top, fmaxf(y[h][nt][0], y[h][nt][1])), fmaxf(y[h][nt][2], y[h][nt][3]));
-      if (__any_sync(0xffffffffu, top > 8.f)) {
+      if (__any_sync(0xffffffffu, top > kRaiseAt)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           // The columns' largest exponents, relative to the references.
@@ -463,11 +465,11 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
             t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
             t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
           }
-          // Raised from the stand-in, the reference is the score itself (the
-          // difference to the stand-in has lost its low bits).
+          // Raised from the stand-in, the reference comes from the score itself
+          // (the difference to the stand-in has lost its low bits).
           const bool new0 = m0[nt] == kNoScore, new1 = m1[nt] == kNoScore;
-          t0 = fmaxf(t0, 0.f);
-          t1 = fmaxf(t1, 0.f);
+          t0 = fmaxf(t0 - kBelowTop, 0.f);
+          t1 = fmaxf(t1 - kBelowTop, 0.f);
           float n0 = m0[nt] + t0, n1 = m1[nt] + t1;
           // (For the whole warp: with a window, columns get their first score in
           // different blocks, and the shuffles take every lane.)
@@ -485,8 +487,8 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
               s0 = fmaxf(s0, __shfl_xor_sync(0xffffffffu, s0, off));
               s1 = fmaxf(s1, __shfl_xor_sync(0xffffffffu, s1, off));
             }
-            if (new0) n0 = s0 == -INFINITY ? kNoScore : s0;
-            if (new1) n1 = s1 == -INFINITY ? kNoScore : s1;
+            if (new0) n0 = s0 == -INFINITY ? kNoScore : s0 - kBelowTop;
+            if (new1) n1 = s1 == -INFINITY ? kNoScore : s1 - kBelowTop;
           }
           const float f0 = new0 ? 1.f : fast_exp2(m0[nt] - n0), f1 = new1 ? 1.f : fast_exp2(m1[nt] - n1);
           m0[nt] = n0;
@@ -502,6 +504,12 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
           }
         }
         exponents();
+#pragma unroll
+        for (int h = 0; h < SUB; ++h)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[h][nt][i] = raised(y[h][nt][i]);
       }
       uint32_t pb[SUB][NT][2];
 #pragma unroll

@@ -337,7 +337,7 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[h][n][i] = CH == 2 ? acc[0][n][i] + acc[CH - 1][n][i] : acc[0][n][i];
         }
-        // ---- Online softmax, the references raised where a score passes them by 2^8.
+        // ---- Online softmax, the references raised where a score passes them by kRaiseAt.
         const int32_t mykey0 = key0 + ks * (kBlk / 2);
         uint32_t bad = 0;
 #pragma unroll
@@ -377,9 +377,8 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
             ta = fmaxf(ta, fmaxf(y[h][n][0], y[h][n][1]));
             tb = fmaxf(tb, fmaxf(y[h][n][2], y[h][n][3]));
           }
-        if (__any_sync(0xffffffffu, fmaxf(ta, tb) > 8.f)) {
-          // Raised from the stand-in, a reference is the score itself (the
-          // difference to the stand-in has lost its low bits).
+        if (__any_sync(0xffffffffu, fmaxf(ta, tb) > kRaiseAt)) {
+          // (From the scores: a difference to the stand-in has lost its low bits.)
           float sa = -INFINITY, sb = -INFINITY;
 #pragma unroll
           for (int h = 0; h < SUB; ++h)
@@ -395,7 +394,7 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
             sa = fmaxf(sa, __shfl_xor_sync(0xffffffffu, sa, off));
             sb = fmaxf(sb, __shfl_xor_sync(0xffffffffu, sb, off));
           }
-          const float na = fmaxf(m_a, sa), nb = fmaxf(m_b, sb);
+          const float na = fmaxf(m_a, sa - kBelowTop), nb = fmaxf(m_b, sb - kBelowTop);
           const float fa = fast_exp2(m_a - na), fb = fast_exp2(m_b - nb);
           m_a = na;
           m_b = nb;
@@ -409,6 +408,12 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
             o[t][3] *= fb;
           }
           exponents();
+#pragma unroll
+          for (int h = 0; h < SUB; ++h)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) y[h][n][i] = raised(y[h][n][i]);
         }
         uint32_t pa[SUB][4];
 #pragma unroll

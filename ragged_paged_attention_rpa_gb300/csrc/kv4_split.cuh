@@ -163,6 +163,19 @@ __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7fffffff
 // The column reference before any score: below every scaled score that is not
 // -inf itself, and small enough that a score minus it is still finite.
 constexpr float kNoScore = -1e38f;
+// A column's reference is this much below its largest score when it is raised,
+// which is where a score passes it by kRaiseAt: probabilities up to 2^15 fit f16,
+// and those down to 2^-24 of the score that raised it keep all their bits (with
+// the reference at the score itself down to 2^-14: what 200 keys of 2^-20.4 of the
+// largest add up to came out 4% off).
+constexpr float kBelowTop = 10.f, kRaiseAt = 15.f;
+// An exponent against a raised reference: of scores beyond 2^26, whose steps are
+// 8 and more, the difference may round past what f16 holds.
+__device__ __forceinline__ float raised(float y) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(y), "f"(kRaiseAt));
+  return r;
+}
 
 // The segments cut across CTAs: out = sum_c 2^(lse_c - M) O_c / sum_c 2^(lse_c - M)
 // over the CTAs that hold a part.  One CTA per boundary between two ranges;

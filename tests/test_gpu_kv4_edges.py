@@ -166,3 +166,62 @@ PROMPT_VALUES = [
 @pytest.mark.parametrize("case", range(len(PROMPT_VALUES)))
 def test_a_nan_value_reaches_the_prompt_rows_that_see_it(case, dynamic):
     nan_values(*PROMPT_VALUES[case], seed=1050 + case, prefill_dynamic=dynamic)
+
+
+# ---------------------------------------------------------------- small probabilities
+
+@pytest.mark.parametrize("hq,tokens,d", [(1, 1, 64), (12, 1, 64), (12, 1, 128), (8, 1, 128), (8, 1, 256), (64, 1, 64),
+                                         (64, 1, 128), (32, 1, 256)])
+def test_probabilities_far_below_the_largest(hq, tokens, d):
+    """One key takes nearly all of each row and has a value of zero; the output
+    is what the others, 2^-20.4 of it each, add up to.  Their probabilities lie
+    midway between two multiples of 2^-24 of the largest."""
+    n, kv = 64, 200
+    b = batch([tokens] * n, [kv] * n, hq, 1, d, 16, seed=5)
+    gap = 24 - np.log2(12.5)
+    k = np.zeros(b.k_fp4.shape[:3] + (d,))
+    v = np.ones_like(k)
+    k[..., 0] = -6.0
+    for s in range(n):
+        page, at = slot(b, s, 0)
+        k[page, 0, at, 0] = 6.0
+        v[page, 0, at] = 0.0
+    q = np.zeros(b.q.shape, np.float32)
+    q[..., 0] = 1.0
+    b.q = oracle.round_bf16(q)
+    b.k_fp4, b.k_fp4_scale = workloads.kv4_encode(k)
+    b.v_fp4, b.v_fp4_scale = workloads.kv4_encode(v)
+    b.sm_scale = float(np.float32(gap * np.log(2) / 12))
+    r = Kv4Batch(b, num_sms=1)                       # whole segments
+    assert r.plan.info()["num_prefill_seqs"] == 0
+    out = r.call()
+    assert binding.rpa_get_device_error(r.ws) == 0
+    check(b, out, prefill=False)
+
+
+@pytest.mark.parametrize("hq,tokens,d", [(1, 1, 64), (12, 1, 64), (8, 1, 128), (8, 1, 256), (64, 1, 64), (64, 1, 128), (32, 1, 256)])
+@pytest.mark.parametrize("top", [2.0 ** 20, 2.0 ** 26 * 1.1, 2.0 ** 28 * 1.3, 2.0 ** 33])
+def test_scores_whose_steps_pass_f16(hq, tokens, d, top):
+    """Logits so large that fp32 holds them in steps of many: the largest key
+    takes the row."""
+    n, kv = 5, 300
+    b = batch([tokens] * n, [kv] * n, hq, 1, d, 16, seed=6)
+    k = np.zeros(b.k_fp4.shape[:3] + (d,))
+    for s in range(n):
+        for key in range(kv):                        # a third below the largest, or more
+            page, at = slot(b, s, key)
+            k[page, 0, at, 0] = [0.5, 1, 1.5, 2, 3, 4][key * 7 % 6]
+            k[page, 0, at, 1] = 6.0                  # the block's scale is one
+        page, at = slot(b, s, 37 * s + 5)
+        k[page, 0, at, 0] = 6.0
+    q = np.zeros(b.q.shape, np.float32)
+    q[..., 0] = 1.0
+    b.q = oracle.round_bf16(q)
+    b.k_fp4, b.k_fp4_scale = workloads.kv4_encode(k)
+    b.sm_scale = top / 6
+    out = Kv4Batch(b).call().float().cpu().numpy()
+    v = oracle.kv4_pool(b.v_fp4, b.v_fp4_scale)
+    for s in range(n):
+        page, at = slot(b, s, 37 * s + 5)
+        want = np.broadcast_to(v[page, at, 0], out[s].shape)
+        assert (np.abs(out[s] - want) <= 2.0 ** -8 * np.abs(want)).all()
