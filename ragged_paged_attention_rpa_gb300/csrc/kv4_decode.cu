@@ -271,6 +271,9 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
   };
 #pragma unroll
   for (int st = 0; st < S; ++st) issue(st);
+  if (const int t = blockIdx.x + gridDim.x * tid; t < sc.n_tiles)
+    check_lengths(sc.tile, t, sc.n_tiles, p.cu_q_lens, p.kv_lens, p.num_seqs, p.total_q, p.ws);
+
 
   // What this lane reads: of K rows g and g + 8 its quarter (KC chunks), of V
   // its eighth of keys 2c, 2c + 1 and those eight on.

@@ -38,6 +38,8 @@ struct ExpandParams {
   uint4* k_out;
   uint4* v_out;
   const int32_t* page_table;
+  const int32_t* cu_q_lens;
+  const int32_t* kv_lens;
   int32_t* table_out;
   unsigned char* ws;
   int32_t hkv, bpr_shift, page_shift, mpps, num_pages;
@@ -73,6 +75,11 @@ kv4_expand_kernel(const ExpandParams p, const __grid_constant__ ExpandList list)
     if (in == 0 && h == 0 && b == 0) {
       p.table_out[at] = ok ? scratch : -1;
       if (!ok) report_error(p.ws, RPA_DEVERR_PAGE_ID, e.seq);
+      // (What is widened goes by the plan's lengths, the prefill by the device's.)
+      if (scratch == e.page0) {
+        const int32_t q0 = p.cu_q_lens[e.seq], q1 = p.cu_q_lens[e.seq + 1];
+        if (q0 != e.q0 || q1 - q0 != e.q_len || p.kv_lens[e.seq] != e.hi) report_error(p.ws, RPA_DEVERR_LENGTHS, e.seq);
+      }
     }
     const int32_t key = (slot << p.page_shift) + in;
     if (!ok || key < e.lo || key >= e.hi) continue;
@@ -101,6 +108,8 @@ int launch_kv4_expand(const Plan& plan, const Args& a, void* stream) {
   p.k_out = reinterpret_cast<uint4*>(a.workspace + plan.off_kv4_k);
   p.v_out = reinterpret_cast<uint4*>(a.workspace + plan.off_kv4_v);
   p.page_table = a.page_table;
+  p.cu_q_lens = a.cu_q_lens;
+  p.kv_lens = a.kv_lens;
   p.table_out = reinterpret_cast<int32_t*>(a.workspace + plan.off_kv4_table);
   p.ws = a.workspace;
   p.hkv = plan.hkv;

@@ -178,6 +178,9 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
   if (cp.rem > 0) find_pages();
 #pragma unroll
   for (int st = 0; st < S; ++st) issue(st);
+  if (const int t = blockIdx.x + gridDim.x * tid; t < sc.n_tiles)
+    check_lengths(sc.tile, t, sc.n_tiles, p.cu_q_lens, p.kv_lens, p.num_seqs, p.total_q, p.ws);
+
 
   // ---- Widening: 64 dimensions of one key a lane, in four pieces of 16.
   const uint32_t wdst = half0 + (is_k ? 0 : Sh::kHalf) + wkey * 2 * D + wline * 128;

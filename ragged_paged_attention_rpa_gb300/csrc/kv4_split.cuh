@@ -17,6 +17,8 @@ struct Kv4Params {
   const uint8_t* ks;
   const uint8_t* vs;
   const int32_t* page_table;
+  const int32_t* cu_q_lens;
+  const int32_t* kv_lens;
   __nv_bfloat16* out;
   unsigned char* ws;
   float* part_o;    // [2 * CTAs][rows][D]
@@ -24,6 +26,7 @@ struct Kv4Params {
   float4* piece_o;  // [CTAs * warps][accumulator tiles][32 lanes]
   int32_t hq, hkv, group, page_shift, mpps, num_pages;
   float scale_log2;
+  int32_t num_seqs, total_q;
 };
 
 // One launch's row tiles: tile e covers rows [r0, r0 + nrows) of sequence seq,
@@ -42,7 +45,22 @@ template <int NSEG>
 struct Kv4Sched {
   Kv4Start cta[kKv4MaxCtas];
   Kv4Tile tile[NSEG];
+  int32_t n_tiles;
 };
+
+// Whether the device's lengths are the plan's, by which the tiles were cut: each
+// CTA looks at its share of the tiles, while its first copies are on their way.
+// (Out of line: inlined, it took up to 27 registers from the kernels' loops.)
+__device__ __noinline__ void check_lengths(const Kv4Tile* tiles, int t, int n_tiles, const int32_t* cu_q_lens,
+                                           const int32_t* kv_lens, int32_t num_seqs, int32_t total_q,
+                                           unsigned char* ws) {
+  for (; t < n_tiles; t += gridDim.x * blockDim.x) {
+    const Kv4Tile& tl = tiles[t];
+    const int32_t* cu = cu_q_lens + tl.seq;
+    const int32_t q0 = __ldg(cu), q1 = __ldg(cu + 1), kv = __ldg(kv_lens + tl.seq), total = __ldg(cu_q_lens + num_seqs);
+    if (q0 != tl.q0 || kv - (q1 - q0) != tl.pos0 || total != total_q) report_error(ws, RPA_DEVERR_LENGTHS, tl.seq);
+  }
+}
 
 // A place on the line: segment (e, g) entered at block j, rem units of the
 // range left from there.
@@ -263,6 +281,8 @@ inline Kv4Params kv4_params(const Plan& plan, const Args& a) {
   p.ks = a.k_block_scales;
   p.vs = a.v_block_scales;
   p.page_table = a.page_table;
+  p.cu_q_lens = a.cu_q_lens;
+  p.kv_lens = a.kv_lens;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.ws = a.workspace;
   p.part_o = reinterpret_cast<float*>(a.workspace + plan.off_partial_o);
@@ -277,6 +297,8 @@ inline Kv4Params kv4_params(const Plan& plan, const Args& a) {
   p.mpps = plan.mpps;
   p.num_pages = plan.num_pages;
   p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  p.num_seqs = plan.num_seqs;
+  p.total_q = static_cast<int32_t>(plan.total_q);
   return p;
 }
 
@@ -290,6 +312,7 @@ int launch_split(const Plan& plan, const Kv4Params& p, const Plan::Kv4Launch& l,
     const Plan::Kv4Tile& t = plan.kv4_tiles[i];
     sc.tile[i - l.begin] = Kv4Tile{t.seq, t.q0, t.r0, t.nrows, t.pos0, t.window, t.fb, t.nb};
   }
+  sc.n_tiles = l.end - l.begin;
   for (int i = 0; i < l.n_ctas; ++i) {
     const Plan::Kv4Start& c = plan.kv4_starts[l.cta_begin + i];
     sc.cta[i] = Kv4Start{c.tile, c.head, c.j, c.len};

@@ -196,7 +196,7 @@ rpa_status_t plan_widened(Plan& plan, const Problem& b, int32_t min_q, const rpa
     ++plan.num_prefill;
     cu[s + 1] += ql;
     const int32_t lo = b.first_key(s, b.kv[s] - ql), slot0 = lo / plan.p;
-    plan.kv4_expand.push_back({s, slot0, static_cast<int32_t>(pages), lo, b.kv[s]});
+    plan.kv4_expand.push_back({s, slot0, static_cast<int32_t>(pages), lo, b.kv[s], b.cu[s], ql});
     pages += ceil_div(b.kv[s], plan.p) - slot0;
     // (The widening counts the rows of all heads in 31 bits.)
     if (pages * plan.p * plan.hkv > 0x7fffffff) return RPA_ERR_UNSUPPORTED;

@@ -180,9 +180,10 @@ struct Plan {
     bool cut;            // some segment is cut across CTAs
   };
   // A sequence's pages from table slot `slot0` on, widened to scratch pages
-  // from `page0` on; keys [lo, hi) are converted.
+  // from `page0` on; keys [lo, hi) are converted, hi is its length; its query
+  // tokens.
   struct Kv4Expand {
-    int32_t seq, slot0, page0, lo, hi;
+    int32_t seq, slot0, page0, lo, hi, q0, q_len;
   };
   std::vector<Kv4Tile> kv4_tiles;
   std::vector<Kv4Start> kv4_starts;

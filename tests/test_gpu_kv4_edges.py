@@ -225,3 +225,44 @@ def test_scores_whose_steps_pass_f16(hq, tokens, d, top):
         page, at = slot(b, s, 37 * s + 5)
         want = np.broadcast_to(v[page, at, 0], out[s].shape)
         assert (np.abs(out[s] - want) <= 2.0 ** -8 * np.abs(want)).all()
+
+
+# ---------------------------------------------------------------- lengths
+
+@pytest.mark.parametrize("ql,kv", [([1, 1], [100, 50]), ([3, 1], [700, 60]), ([30, 17], [200, 90]), ([200], [300]),
+                                   ([1, 200], [90, 300])])
+def test_lengths_that_disagree_with_the_plan(ql, kv):
+    """Device lengths other than the plan's set the error word, on whichever
+    kernel: a step that the table build refused (no new token, the lengths as
+    before), keys more or fewer, tokens fewer."""
+    b = batch(ql, kv, 4, 2, 128, 16, seed=7, max_pages_per_seq=max(kv) // 16 + 2)
+    r = Kv4Batch(b)
+    db = r.db
+    good = r.call().clone()
+    assert binding.rpa_get_device_error(r.ws) == 0
+    cu, lens = b.cu_q_lens.copy(), b.kv_lens.copy()
+    last = np.zeros_like(lens)
+    last[-1] = 1
+    for new_cu, new_lens in ((0 * cu, lens - np.diff(cu)), (cu, lens + last), (cu, lens - last),
+                             (np.concatenate([cu[:-1], cu[-1:] - 1]), lens - last),
+                             (np.concatenate([cu[:-1], cu[-1:] - 1]), lens)):
+        db.cu_q_lens.copy_(cuda(new_cu.astype(np.int32)))
+        db.kv_lens.copy_(cuda(new_lens.astype(np.int32)))
+        r.call()
+        assert binding.rpa_get_device_error(r.ws) == binding.RPA_DEVERR_LENGTHS, (new_cu, new_lens)
+    db.cu_q_lens.copy_(cuda(cu))
+    db.kv_lens.copy_(cuda(lens))
+    assert torch.equal(r.call(), good) and binding.rpa_get_device_error(r.ws) == 0
+
+
+def test_many_tiles_are_all_looked_at():
+    """Every sequence's lengths, whichever CTA works on it."""
+    b = batch([1] * 900, [20 + i % 40 for i in range(900)], 2, 2, 64, 16, seed=8)
+    r = Kv4Batch(b)
+    r.call()
+    assert binding.rpa_get_device_error(r.ws) == 0
+    for s in (0, 151, 152, 500, 863, 864, 899):
+        r.db.kv_lens[s] += 1
+        r.call()
+        assert binding.rpa_get_device_error(r.ws) == binding.RPA_DEVERR_LENGTHS, s
+        r.db.kv_lens[s] -= 1
