@@ -15,6 +15,7 @@
 #include <utility>
 
 #include "rpa.h"
+#include "fork_join.h"
 #include "rpa_internal.h"
 
 struct rpa_plan {
@@ -229,22 +230,21 @@ rpa_status_t side_by_side(rpa_stream_t stream, const Launch& here, const Launch&
   int err = side_stream(&side);
   if (err) return cuda_failed(err);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaEventRecord(side->fork, s);
-  if (e == cudaSuccess) e = cudaStreamWaitEvent(side->stream, side->fork, 0);
-  if (e != cudaSuccess) return cuda_failed(static_cast<int>(e));
-  rpa_stream_t ss = reinterpret_cast<rpa_stream_t>(side->stream);
-  rpa::trace_start(ss);
-  err = there(ss);
-  if (err) return cuda_failed(err);
-  if ((e = cudaEventRecord(side->join, side->stream)) != cudaSuccess)
-    return cuda_failed(static_cast<int>(e));
-  err = here(stream);
-  // Join even when that launch failed, so that a capture in progress is left
-  // with every forked stream joined.
-  e = cudaStreamWaitEvent(s, side->join, 0);
-  if (err) return cuda_failed(err);
-  if (e != cudaSuccess) return cuda_failed(static_cast<int>(e));
-  return RPA_OK;
+  err = rpa::fork_join(
+      [&] {
+        cudaError_t e = cudaEventRecord(side->fork, s);
+        if (e == cudaSuccess) e = cudaStreamWaitEvent(side->stream, side->fork, 0);
+        return static_cast<int>(e);
+      },
+      [&] {
+        rpa_stream_t ss = reinterpret_cast<rpa_stream_t>(side->stream);
+        rpa::trace_start(ss);
+        return there(ss);
+      },
+      [&] { return static_cast<int>(cudaEventRecord(side->join, side->stream)); },
+      [&] { return here(stream); },
+      [&] { return static_cast<int>(cudaStreamWaitEvent(s, side->join, 0)); });
+  return err ? cuda_failed(err) : RPA_OK;
 }
 
 rpa_status_t forward_launch(const rpa::Plan& p, const rpa::Args& a,
