@@ -526,11 +526,15 @@ def _kv4_args(q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv
     if (hkv != m["num_kv_heads"] or p != m["page_size"] or d != m["head_dim"]
             or pages < m["num_pages"]):
         raise ValueError("the pools' shape differs from the plan's")
-    least = m["total_q"] * hq * d
-    if q.numel() < least or out.numel() < least:
-        raise ValueError("q and out must hold the plan's %d rows of %d x %d" % (m["total_q"], hq, d))
-    if page_table.numel() < s * m["max_pages_per_seq"]:
-        raise ValueError("page_table must be [%d, %d]" % (s, m["max_pages_per_seq"]))
+    least, rows = m["total_q"] * hq * d, (hq, d)
+    for t in (q, out):
+        if t.numel() < least or (t.dim() == 3 and t.shape[1:] != rows):
+            raise ValueError("q and out must hold the plan's %d rows of %d x %d" % (m["total_q"], hq, d))
+    width = m["max_pages_per_seq"]
+    if page_table.numel() < s * width or (page_table.dim() == 2 and page_table.shape[1] != width):
+        raise ValueError("page_table must be [%d, %d], got %s" % (s, width, tuple(page_table.shape)))
+    if cu_q_lens.numel() <= s or kv_lens.numel() < s or (window is not None and window.numel() < s):
+        raise ValueError("cu_q_lens must have %d entries, kv_lens and window %d" % (s + 1, s))
     ws, n = _workspace(workspace, dev)
     return (_addr(q, "q", bf16, dev), kp, vp, ks, vs, _addr(page_table, "page_table", i32, dev),
             _addr(cu_q_lens, "cu_q_lens", i32, dev), _addr(kv_lens, "kv_lens", i32, dev),
@@ -827,6 +831,10 @@ class ForwardKv4Call(ForwardCall):
     def __call__(self, plan: Optional[Plan] = None):
         args = self._args
         if plan is not None:
+            m, mine = plan.meta, self._keep[10].meta
+            if (m["total_q"] > mine["total_q"] or m["num_pages"] > mine["num_pages"]
+                    or m["max_pages_per_seq"] != mine["max_pages_per_seq"]):
+                raise ValueError("the tensors of this call are too small for that plan")
             args = args[:17] + (plan.handle,) + args[18:]
         st = self._fn(*args)
         if st != RPA_OK:

@@ -266,3 +266,56 @@ def test_many_tiles_are_all_looked_at():
         r.call()
         assert binding.rpa_get_device_error(r.ws) == binding.RPA_DEVERR_LENGTHS, s
         r.db.kv_lens[s] -= 1
+
+
+# ---------------------------------------------------------------- the binding
+
+def test_refusals_of_tensors_too_small_for_the_plan():
+    """Each tensor that the kernels index by sequence or by row."""
+    b = batch([1, 200, 3], [40, 300, 70], 4, 2, 64, 16, [0, 9, 0], seed=3)
+    r = Kv4Batch(b)
+    db = r.db
+    good = dict(q=db.q, page_table=db.page_table, cu_q_lens=db.cu_q_lens, kv_lens=db.kv_lens, window=db.window, out=r.out)
+
+    def call(**changed):
+        a = {**good, **changed}
+        binding.rpa_forward_kv4(a["q"], *r.pool, a["page_table"], a["cu_q_lens"], a["kv_lens"], a["window"], b.sm_scale,
+                                a["out"], r.plan, r.ws)
+    call()
+    wide = torch.cat([db.page_table, db.page_table], 1)        # rows of another length
+    for changed in (dict(cu_q_lens=db.cu_q_lens[:3]), dict(kv_lens=db.kv_lens[:2]), dict(window=db.window[:2]),
+                    dict(page_table=wide), dict(page_table=db.page_table[:2]), dict(page_table=db.page_table.view(-1)[:-1]),
+                    dict(q=db.q[:203]), dict(out=r.out[:203]), dict(q=db.q.view(-1, 2, 128)),
+                    dict(out=r.out.view(-1, 8, 32))):
+        with pytest.raises(ValueError):
+            call(**changed)
+    # More than the plan has is no matter, nor are rows laid out flat.
+    call(q=db.q.view(204, -1), out=r.out.view(-1), page_table=db.page_table.view(-1))
+    call(cu_q_lens=torch.cat([db.cu_q_lens, db.cu_q_lens]), kv_lens=torch.cat([db.kv_lens, db.kv_lens]),
+         page_table=torch.cat([db.page_table, db.page_table]))
+    assert binding.rpa_get_device_error(r.ws) == 0
+    check(b, r.out)
+
+
+def test_a_prepared_call():
+    """ForwardKv4Call: marshalled once, run again, under another plan of the
+    same tensors; plans that they are too small for are refused."""
+    b = batch([1, 5, 200], [400, 30, 300], 4, 2, 128, 16, seed=4)
+    r = Kv4Batch(b)
+    want = r.call().clone()
+    db = r.db
+    one = binding.rpa_plan(b.cu_q_lens, b.kv_lens, None, 4, 2, 128, 16, b.max_pages_per_seq, b.num_pages, num_sms=3,
+                           kv_dtype=binding.RPA_DTYPE_FP4_E2M1)
+    ws = torch.zeros(max(r.plan.workspace_bytes, one.workspace_bytes), dtype=torch.uint8, device="cuda")
+    call = binding.ForwardKv4Call(db.q, *r.pool, db.page_table, db.cu_q_lens, db.kv_lens, None, b.sm_scale, r.out, r.plan, ws)
+    for plan in (None, one, r.plan):
+        r.out.fill_(float("nan"))
+        call() if plan is None else call(plan)
+        check(b, r.out)
+    assert torch.equal(r.out, want) and binding.rpa_get_device_error(ws) == 0
+    big = np.array([0, 1, 6, 206 + 1], np.int32)
+    for cu, width, pages in ((big, b.max_pages_per_seq, b.num_pages), (b.cu_q_lens, b.max_pages_per_seq + 1, b.num_pages),
+                             (b.cu_q_lens, b.max_pages_per_seq, b.num_pages + 1)):
+        plan = binding.rpa_plan(cu, b.kv_lens, None, 4, 2, 128, 16, width, pages, kv_dtype=binding.RPA_DTYPE_FP4_E2M1)
+        with pytest.raises(ValueError):
+            call(plan)
