@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -617,6 +619,9 @@ rpa_status_t rpa_forward_kv4(const void* q, const uint8_t* k_pages, const uint8_
   auto prefill = [&](rpa_stream_t s) {
     if (int e = rpa::launch_kv4_expand(p, a, s)) return e;
     rpa::Args b = a;
+    // (Positive for the prefill, see launch_kv4_expand; the smallest one for zero,
+    // under which no logit differs from zero and a masked one is still -inf.)
+    b.sm_scale = std::fabs(a.sm_scale) < FLT_MIN ? FLT_MIN : std::fabs(a.sm_scale);
     b.k_pages = a.workspace + p.off_kv4_k;
     b.v_pages = a.workspace + p.off_kv4_v;
     b.page_table = reinterpret_cast<const int32_t*>(a.workspace + p.off_kv4_table);

@@ -9,7 +9,8 @@
 // bf16 (six significant bits).  A block of V that reads as NaN becomes zeros (in
 // the product it would reach the rows that do not see its key, 0 times NaN) and
 // sets a word of the header, on which the prefill's epilogue looks the scales up
-// for each row.
+// for each row.  The prefill takes maxima of the products before it scales them,
+// which wants a positive logit scale: for a negative one K's signs are turned.
 //
 // One thread per 16 dimensions of K and of V; HBM-bound: 0.5625 bytes an
 // element read, 2 written (and the prefill reads them back from L2 or HBM).  A
@@ -42,6 +43,7 @@ struct ExpandParams {
   const int32_t* kv_lens;
   int32_t* table_out;
   unsigned char* ws;
+  uint32_t k_signs;  // turned in K's codes
   int32_t hkv, bpr_shift, page_shift, mpps, num_pages;
   kv4::HeadDiv by_heads;
 };
@@ -89,7 +91,7 @@ kv4_expand_kernel(const ExpandParams p, const __grid_constant__ ExpandList list)
     const uint32_t ks = __ldg(p.ks + src), vs = __ldg(p.vs + src);
     v_nan |= vs == 255u;
     uint32_t w[8];  // the workspace's arrays are 256-byte aligned
-    kv4::decode_block_bf16(kc, ks, w);
+    kv4::decode_block_bf16(make_uint2(kc.x ^ p.k_signs, kc.y ^ p.k_signs), ks, w);
     kv4::store32(p.k_out + dst, true, w);
     kv4::decode_block_bf16(vc, vs == 255u ? 0u : vs, w);
     kv4::store32(p.v_out + dst, true, w);
@@ -112,6 +114,7 @@ int launch_kv4_expand(const Plan& plan, const Args& a, void* stream) {
   p.kv_lens = a.kv_lens;
   p.table_out = reinterpret_cast<int32_t*>(a.workspace + plan.off_kv4_table);
   p.ws = a.workspace;
+  p.k_signs = a.sm_scale < 0.f ? 0x88888888u : 0u;
   p.hkv = plan.hkv;
   p.by_heads = kv4::head_div(plan.hkv);
   int shift = 0;

@@ -268,6 +268,37 @@ def test_many_tiles_are_all_looked_at():
         r.db.kv_lens[s] -= 1
 
 
+# ---------------------------------------------------------------- logit scales
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, -0.125, -40.0])
+def test_scales_of_zero_and_below(scale):
+    """sm_scale is any number: the same on every kernel."""
+    b = batch([1, 6, 33, 200], [90, 300, 100, 260], 2, 1, 128, 16, [0, 4, 0, 50], seed=9)
+    b.sm_scale = scale
+    k, v = oracle.kv4_pool(b.k_fp4, b.k_fp4_scale), oracle.kv4_pool(b.v_fp4, b.v_fp4_scale)
+    q = oracle.bf16_bits_to_f32(b.q)
+    meta = (b.page_table, b.cu_q_lens, b.kv_lens, b.window, b.sm_scale)
+    ref = oracle.attention(q, k, v, *meta, precision=64)
+    mag = oracle.attention(q, k, np.abs(v), *meta, precision=64)
+    kmax = np.sqrt((k.astype(np.float64) ** 2).sum(-1).max())
+    qn = np.sqrt((q.reshape(-1, 128).astype(np.float64) ** 2).sum(-1))[:, None]
+    # The module's terms; the exponential's and the logit scale's rounding grow
+    # with the scores, which |q| |k| |scale| bounds.
+    ds = (128 + 2) * 2.0 ** -23 * abs(scale) * qn * kmax + 2.0 ** -21 * abs(scale) * qn * kmax
+    r = Kv4Batch(b)
+    info = r.plan.info()
+    assert info["num_decode_seqs"] > 0 and info["num_prefill_seqs"] > 0
+    got = r.call().float().cpu().numpy().reshape(-1, 128).astype(np.float64)
+    assert binding.rpa_get_device_error(r.ws) == 0
+    # A probability p of the largest that f16 holds as a subnormal is off by half
+    # its step, 2^-25 over the largest's 2^10: 2^-35 of the largest, of at most 300
+    # keys.  (At -40 a row's second key can have 2^-200 of the first, which is zero
+    # in fp32 already; where the first key's value is zero the relative terms alone
+    # would ask for it.)
+    bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * ds + 2.0 ** -16) * mag + 300 * 2.0 ** -35 * np.abs(v).max()
+    assert (np.abs(got - ref) <= bound).all()
+
+
 # ---------------------------------------------------------------- the binding
 
 def test_refusals_of_tensors_too_small_for_the_plan():
