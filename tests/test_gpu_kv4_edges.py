@@ -15,7 +15,7 @@ import torch
 import oracle
 from ragged_paged_attention_rpa_gb300 import binding, build, workloads
 
-from .test_gpu_kv4 import Kv4Batch, batch, check, cuda, reference
+from .test_gpu_kv4 import FEW, ROWS, Kv4Batch, batch, check, cuda, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -166,6 +166,36 @@ PROMPT_VALUES = [
 @pytest.mark.parametrize("case", range(len(PROMPT_VALUES)))
 def test_a_nan_value_reaches_the_prompt_rows_that_see_it(case, dynamic):
     nan_values(*PROMPT_VALUES[case], seed=1050 + case, prefill_dynamic=dynamic)
+
+
+# ---------------------------------------------------------------- NaN anywhere
+
+@pytest.mark.parametrize("seed", range(40))
+def test_nan_blocks_anywhere(seed):
+    """Random batches with NaN blocks of K (all of the rows that see the key) and
+    of V (their 16 dimensions), wherever they lie."""
+    rng = np.random.default_rng(7000 + seed)
+    pick = lambda *a: a[int(rng.integers(len(a)))]
+    d, p, hkv, group = pick(64, 128, 256), pick(16, 32, 128), pick(1, 2, 3), pick(1, 2, 3, 8, 16)
+    ql = [pick(1, 2, 4, 8, int(rng.integers(9, 40)), int(rng.integers(40, 260))) for _ in range(int(rng.integers(1, 8)))]
+    kv = [q + pick(0, int(rng.integers(0, 40)), int(rng.integers(0, 900))) for q in ql]
+    win = pick(None, [pick(0, 1, 7, 60) for _ in ql])
+    b = batch(ql, kv, hkv * group, hkv, d, p, win, seed=seed)
+    ref = reference(b)
+    want = np.zeros((b.q.shape[0], hkv * group, d), bool)
+    for _ in range(int(rng.integers(1, 12))):
+        s = int(rng.integers(len(ql)))
+        key, g, blk = int(rng.integers(max(0, kv[s] - 300), kv[s])), int(rng.integers(hkv)), int(rng.integers(d // 16))
+        page, at = slot(b, s, key)
+        rows = b.cu_q_lens[s] + np.nonzero(sees(b, s)[:, key])[0]
+        of_k = rng.random() < 0.2
+        (b.k_fp4_scale if of_k else b.v_fp4_scale)[page, g, at, blk] = 255
+        want[rows, g * group:(g + 1) * group, slice(None) if of_k else slice(16 * blk, 16 * blk + 16)] = True
+    r = Kv4Batch(b, num_sms=pick(0, 0, 1, 9))
+    out = r.call().clone()
+    assert binding.rpa_get_device_error(r.ws) == 0
+    check_nan(b, out, want, ref, r.plan.info()["num_prefill_seqs"] > 0)
+    assert torch.equal(r.call().view(torch.int16), out.view(torch.int16))
 
 
 # ---------------------------------------------------------------- small probabilities
@@ -350,3 +380,55 @@ def test_a_prepared_call():
         plan = binding.rpa_plan(cu, b.kv_lens, None, 4, 2, 128, 16, width, pages, kv_dtype=binding.RPA_DTYPE_FP4_E2M1)
         with pytest.raises(ValueError):
             call(plan)
+
+
+# ---------------------------------------------------------------- each kernel's own bound
+
+def run_and_check(b, **plan_kw):
+    """The bound of the kernels that ran, and the same bits twice."""
+    r = Kv4Batch(b, **plan_kw)
+    out = r.call().clone()
+    assert binding.rpa_get_device_error(r.ws) == 0
+    check(b, out, prefill=r.plan.info()["num_prefill_seqs"] > 0)
+    assert torch.equal(r.call(), out)
+
+
+@pytest.mark.parametrize("case", range(len(FEW)))
+def test_few_tokens_within_the_split_kernels_bound(case):
+    ql, kv, hq, hkv, d, p, win = FEW[case]
+    run_and_check(batch(ql, kv, hq, hkv, d, p, win, seed=340 + case))
+
+
+@pytest.mark.parametrize("case", range(len(ROWS)))
+def test_tens_of_rows_within_the_split_kernels_bound(case):
+    ql, kv, hq, hkv, d, p, win = ROWS[case]
+    run_and_check(batch(ql, kv, hq, hkv, d, p, win, seed=700 + case))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("tokens", [3, 7, 14, 30])
+def test_small_windows_within_the_split_kernels_bound(d, tokens):
+    kv = [tokens + 20 + 5 * i for i in range(24)] + [1312]
+    b = batch([tokens] * 25, kv, 1, 1, d, 16, [17, 2, 5, 33, 9] * 5, seed=800 + tokens)
+    for kw in ({}, {"num_sms": 1}):
+        run_and_check(b, **kw)
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_batches(seed):
+    """Heads, dimensions, pages, windows, lengths, SMs and their split drawn."""
+    rng = np.random.default_rng(5000 + seed)
+    pick = lambda *a: a[int(rng.integers(len(a)))]
+    d, p, hkv = pick(64, 128, 256), pick(16, 32, 64, 128, 256), pick(1, 1, 2, 3, 8)
+    group = pick(1, 2, 3, 4, 7, 8, 16, 40)
+    n = int(rng.integers(1, 25))
+    ql, kv = [], []
+    for _ in range(n):
+        q = pick(0, 1, 1, 1, 2, int(rng.integers(2, 17)), int(rng.integers(17, 200)))
+        ql.append(q)
+        kv.append(q + pick(0, int(rng.integers(0, 40)), int(rng.integers(0, 700)), int(rng.integers(0, 3000))))
+    if not any(ql):
+        ql[0], kv[0] = 1, kv[0] + 1
+    win = pick(None, [int(rng.integers(0, 90)) for _ in range(n)], [pick(0, 1, 500) for _ in range(n)])
+    run_and_check(batch(ql, kv, hkv * group, hkv, d, p, win, seed=seed), num_sms=pick(0, 0, 1, 7, 40),
+                  decode_sms=pick(0, 0, -1))
