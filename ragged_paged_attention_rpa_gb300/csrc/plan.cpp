@@ -576,7 +576,8 @@ rpa_status_t build_schedule(Plan& plan, const int32_t* cu, const int32_t* kv,
   const bool f32 = plan.dtype == RPA_DTYPE_F32;
   if (want == RPA_PATH_TC && f32) return RPA_ERR_UNSUPPORTED;
   bool tc_decode = false, tc_prefill = false;
-  if (want != RPA_PATH_SIMT && !f32) {
+  // (The tensor-core work lists hold a KV head in eight bits.)
+  if (want != RPA_PATH_SIMT && !f32 && plan.hkv <= kPlanMaxKvHeads) {
     tc_decode = decode_supported(plan.d, group, plan.p);
     tc_prefill = prefill_tc_supported(plan.d, plan.p, group);
   }

@@ -203,6 +203,7 @@ rpa_status_t plan_widened(Plan& plan, const Problem& b, int32_t min_q, const rpa
   }
   plan.kv4_scratch_pages = static_cast<int32_t>(pages);
   if (plan.num_prefill == 0) return RPA_OK;
+  if (plan.hkv > kPlanMaxKvHeads) return RPA_ERR_UNSUPPORTED;
   plan.kv4_prefill.reset(new (std::nothrow) Plan());
   if (!plan.kv4_prefill) return RPA_ERR_INVALID_ARG;
   Plan& f = *plan.kv4_prefill;

@@ -35,6 +35,10 @@ constexpr size_t kKv4NanOff = 192;
 // threads to them in 31 bits).
 constexpr int32_t kTablesMost = 1 << 30;
 
+// Most KV heads of a plan's tensor-core work (its items and segments hold a head
+// in eight bits).
+constexpr int32_t kPlanMaxKvHeads = 256;
+
 // One prefill work item: query block `qb` (of plan.q_block tokens) of
 // sequence `seq`, for KV head `head`.  Ordered longest first in the plan.
 struct PrefillItem {
