@@ -354,7 +354,8 @@ rpa_status_t rpa_forward_kv(const void* q, const void* k_new, const void* v_new,
   if (plan == nullptr) return RPA_ERR_INVALID_ARG;
   const rpa::Plan& p = plan->p;
   if (num_seqs != p.num_seqs || num_q_heads != p.hq || num_kv_heads != p.hkv ||
-      head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp4)
+      head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp8 ||
+      p.kv_fp4)
     return RPA_ERR_PLAN_MISMATCH;
   if (workspace == nullptr || !aligned(workspace, 256)) return RPA_ERR_INVALID_ARG;
   if (workspace_bytes < p.ws_bytes) return RPA_ERR_WORKSPACE_TOO_SMALL;
