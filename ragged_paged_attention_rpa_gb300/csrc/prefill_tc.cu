@@ -139,6 +139,7 @@ struct Pages4 {
   const int32_t* page_table;
   int32_t num_pages;
   int32_t last_launch;  // no launch of this call follows
+  int32_t total_q;      // rows of q and out
 };
 
 // One 32-byte store (eight 32-bit words) to a 32-byte aligned address.
@@ -482,6 +483,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
             gm = item_geom(p, items.items[it]);
             split = items.items[it].split;
+            // (Lengths built on the device may pass the plan's.)
+            if constexpr (kKv4) gm.ok = gm.ok && gm.t0 >= 0 && gm.t0 + gm.ntok <= x.total_q;
             if (gm.ok) break;
             if (items.items[it].seq >= 0) report_error(p.ws, RPA_DEVERR_LENGTHS, gm.seq);
             it = next_item(it);
@@ -1168,7 +1171,8 @@ int launch_prefill_t(const Plan& plan, const Args& a, cudaStream_t stream) {
       for (int c = 0; c <= grid; ++c) list.cta0[c] = plan.pcta0[c];
     }
     Pages x;
-    if constexpr (Pages::kKv4) x = Pages{a.v_block_scales, a.kv4_page_table, a.kv4_num_pages, off + cnt == n};
+    if constexpr (Pages::kKv4) x = Pages{a.v_block_scales, a.kv4_page_table, a.kv4_num_pages, off + cnt == n,
+                                            static_cast<int32_t>(plan.total_q)};
     prefill_tc_kernel<D, Pages><<<grid, kThreads, Lay::kBytes, stream>>>(tq, tk, tv, p, list, x);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return static_cast<int>(e);

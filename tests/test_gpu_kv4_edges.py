@@ -285,6 +285,24 @@ def test_lengths_that_disagree_with_the_plan(ql, kv):
     assert torch.equal(r.call(), good) and binding.rpa_get_device_error(r.ws) == 0
 
 
+@pytest.mark.parametrize("ql,kv", [([200], [300]), ([1, 200], [90, 300]), ([5, 3], [90, 40])])
+def test_device_lengths_past_the_plans_rows(ql, kv):
+    """Device lengths that name rows behind the plan's, or before them: reported,
+    and nothing is written there."""
+    b = batch(ql, kv, 4, 2, 128, 16, seed=7, max_pages_per_seq=max(kv) // 16 + 2)
+    r = Kv4Batch(b)
+    q = torch.cat([r.db.q, r.db.q])
+    out = torch.full_like(q, 3.0)
+    cu, n = b.cu_q_lens, int(b.cu_q_lens[-1])
+    last = np.zeros_like(cu)
+    last[-1] = 1
+    for moved in (cu + last, cu + 1, cu - 300):
+        binding.rpa_forward_kv4(q, *r.pool, r.db.page_table, cuda(moved), cuda(b.kv_lens + last[1:]), None, b.sm_scale,
+                                out, r.plan, r.ws)
+        assert binding.rpa_get_device_error(r.ws) == binding.RPA_DEVERR_LENGTHS
+        assert bool((out[n:] == 3.0).all())
+
+
 def test_many_tiles_are_all_looked_at():
     """Every sequence's lengths, whichever CTA works on it."""
     b = batch([1] * 900, [20 + i % 40 for i in range(900)], 2, 2, 64, 16, seed=8)
