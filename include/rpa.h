@@ -137,7 +137,9 @@ typedef struct rpa_plan_options {
                                256, run through rpa_forward_fp8kv; or
                                RPA_DTYPE_FP4_E2M1 with dtype BF16, any q_len,
                                page_size >= 16, num_q_heads / num_kv_heads <=
-                               128, run through rpa_forward_kv4 (of the other
+                               128 (and at most 256 KV heads where a sequence
+                               runs on the prefill), run through
+                               rpa_forward_kv4 (of the other
                                options it takes path AUTO or TC, q_block of one
                                tile, num_sms, decode_sms, prefill_dynamic and
                                prefill_grouping; the rest must be 0, else
@@ -218,8 +220,9 @@ typedef struct rpa_plan rpa_plan_t;
  *       (cu_q_lens_host[0] == 0, non-decreasing; q_len <= kv_len).
  *   window_host: host int32 [num_seqs] (<= 0: full causal), or NULL (all
  *       full causal).  It must match what is later passed to rpa_forward.
- *   num_q_heads % num_kv_heads == 0.  head_dim in {64, 128, 256}; page_size
- *       a power of two in [1, 256] (the tensor-core prefill needs >= 16);
+ *   num_q_heads % num_kv_heads == 0 (the tensor-core paths take at most 256
+ *       KV heads; more run on the CUDA-core one).  head_dim in {64, 128, 256};
+ *       page_size a power of two in [1, 256] (the tensor-core prefill needs >= 16);
  *       dtype RPA_DTYPE_BF16 or RPA_DTYPE_F32 (F32 always takes the SIMT path,
  *       the fp32 debug build).
  *   max_pages_per_seq: row length of the page table; every sequence needs
@@ -271,8 +274,13 @@ rpa_status_t rpa_plan_get_info(const rpa_plan_t* plan, rpa_plan_info* info);
  *            owns) may hold anything, NaN and infinities included.  The
  *            kernels load some of them along with the visible keys (whole
  *            boxes of a page) but zero them before any product uses them.
+ *            A NaN in K makes NaN the rows that see its key; a NaN or an
+ *            infinity in V those, and in a prefill it may also reach rows of the
+ *            same sequence that do not see the key (0 times NaN).
  * The scalar arguments must equal the plan's, else RPA_ERR_PLAN_MISMATCH.
- * sm_scale multiplies q.k before the softmax (1/sqrt(head_dim) is usual).
+ * sm_scale multiplies q.k before the softmax (1/sqrt(head_dim) is usual); with
+ * sequences on the tensor-core prefill, which scales after its maxima, it must
+ * be positive.
  * Enqueues on `stream` the split-KV decode kernel and, where a sequence is
  * cut across its CTAs, the log-sum-exp combine kernel (a programmatic
  * dependent launch), then the tensor-core prefill and the CUDA-core path, as
@@ -424,8 +432,12 @@ rpa_status_t rpa_forward_kv(const void* q, const void* k_new, const void* v_new,
  * e2m1 code (bit 3 sign; magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 for the low three
  * bits), two to a byte, the even dimension in the low half.  Each block has one
  * scale byte without a sign: e = byte >> 3, m = byte & 7, scale = (1 + m / 8) *
- * 2^(e - 15), or m * 2^-17 where e == 0; byte 255 is NaN.  A stored value is
- * its code's magnitude times the scale.  Pages are arrays
+ * 2^(e - 15), or m * 2^-17 where e == 0, up to byte 226 (10240); byte 255 is NaN;
+ * 227 to 254 are not valid in a visible slot (the kernels read a scale as the
+ * f16 of its bits, where some of them overflow).  A stored value is its code's
+ * magnitude times the scale.  The format is this library's: its scales are
+ * neither the signed e4m3 ones with a second scale per tensor nor the powers of
+ * two per 32 elements that other 4-bit formats have.  Pages are arrays
  *   k_pages,  v_pages  [num_pages, num_kv_heads, page_size, head_dim / 2] bytes
  *   k_scales, v_scales [num_pages, num_kv_heads, page_size, head_dim / 16] bytes
  * (a head's rows of a page are contiguous, unlike the 8- and 16-bit pools).
@@ -441,7 +453,8 @@ rpa_status_t rpa_forward_kv(const void* q, const void* k_new, const void* v_new,
  * aligned; slot_map [total_q] int64: token t goes to slot slot_map[t] %
  * page_size of page slot_map[t] / page_size (rpa_build_tables makes such a
  * map); a negative entry leaves the token out.  The slots of a call are
- * distinct (else the row that stays is one of them, block by block).
+ * distinct: where two tokens name one, what it holds afterwards may be one's
+ * codes under the other's scales.
  * k_pages, v_pages, k_scales and v_scales 16-B aligned.  head_dim 64, 128 or
  * 256, page_size a power of two in [16, 256] and total_q * num_kv_heads below
  * 2^31, else RPA_ERR_UNSUPPORTED.
@@ -474,10 +487,20 @@ rpa_status_t rpa_read_kv4(const uint8_t* k_pages, const uint8_t* v_pages, const 
  * tokens, a few tokens and prompts.  The plan must have kv_dtype
  * RPA_DTYPE_FP4_E2M1; q and out are bf16.  Sequences of few query rows (q_len
  * times num_q_heads / num_kv_heads) run on a split-KV kernel that widens the
- * codes in registers; the others' visible keys are first widened to bf16 in
- * the workspace (whose size counts them: 4 * head_dim * num_kv_heads bytes a
- * key).  Pages as rpa_write_kv4's; the other arguments, the error word, unused
- * slots, threads and CUDA graphs as rpa_forward.
+ * codes in registers (or, for tens of rows, in shared memory); the others'
+ * visible keys are first widened to bf16 in the workspace: 4 * head_dim *
+ * num_kv_heads bytes a key (3.6 times the pages' own), for the whole visible
+ * prefix of each such sequence and anew at every call, so a chunk of a prompt
+ * after 128k keys of 8 heads of 128 takes 537 MB.  A plan whose widened keys
+ * times heads pass 2^31 is refused with RPA_ERR_UNSUPPORTED.
+ * A block of K that reads as NaN makes NaN the rows that see its key, a block of
+ * V its 16 dimensions of them; no other row, on whichever kernel.  sm_scale may
+ * be any number.  Device lengths that differ from the plan's (those of a step that
+ * rpa_build_tables refused, for one) set RPA_DEVERR_LENGTHS; the rows of such a
+ * sequence are then not to be used.  Let the calls of a step share a workspace:
+ * one read of its error word then tells of all of them.
+ * Pages as rpa_write_kv4's; the other arguments, the error word, unused slots,
+ * threads and CUDA graphs as rpa_forward.
  */
 rpa_status_t rpa_forward_kv4(const void* q, const uint8_t* k_pages, const uint8_t* v_pages,
                              const uint8_t* k_scales, const uint8_t* v_scales,

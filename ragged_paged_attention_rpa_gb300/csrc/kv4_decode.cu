@@ -3,12 +3,12 @@
 //
 // Work.  The query rows of a sequence that share a KV head (token-major, G
 // heads a token) are cut into tiles of 8 or 16 rows; every (row tile, KV head)
-// is a segment of 16-key blocks over the keys any of its rows sees.  The
+// is a segment of blocks of 16 to 64 keys over the keys any of its rows sees.  The
 // segments are laid end to end, each followed by a fixed charge for its merge,
 // and the line is cut into equal ranges, one per CTA, one wave.
 //
-// CTA.  The warps take a segment's blocks round-robin and never meet until its
-// end: each runs, per block of 16 keys,
+// CTA.  A warp takes a contiguous share of the CTA's range and meets the others
+// once, at the range's end.  Per 16 keys it runs
 //     S^T[16 keys x rows] = K . Q^T        (mma.m16n8k16, f16 -> fp32)
 //     O^T[D x rows]     += V^T . P^T
 // with an online softmax whose reference is 10 below the largest score when it
@@ -272,7 +272,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
 #pragma unroll
   for (int st = 0; st < S; ++st) issue(st);
   if (const int t = blockIdx.x + gridDim.x * tid; t < sc.n_tiles)
-    check_lengths(sc.tile, t, sc.n_tiles, p.cu_q_lens, p.kv_lens, p.num_seqs, p.total_q, p.ws);
+    check_lengths(sc.tile, t, sc.n_tiles, sc.cu_q_lens, sc.kv_lens, sc.num_seqs, sc.total_q, p.ws);
 
 
   // What this lane reads: of K rows g and g + 8 its quarter (KC chunks), of V
@@ -289,6 +289,22 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
   // this lane's sums.
   float m0[NT], m1[NT], l0[NT], l1[NT];
   bool held = false;  // o, m and l are the piece kept for the merge
+  // By column (16 bits each): the blocks of dimensions into which a NaN of V at
+  // an uneven key goes, once the segment's O is in memory, where the loop need not
+  // be unrolled.
+  uint32_t nan_hit[NT];
+  auto nan_to_state = [&](float4* state) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      if (nan_hit[nt] != 0)
+#pragma unroll 1
+        for (int t = 0; t < MT; ++t) {
+          float* const f = reinterpret_cast<float*>(state + (t * NT + nt) * 32);
+          const uint32_t hit = nan_hit[nt] >> ((g * (D / 8) + 2 * t) / 16);  // dimensions g (D / 8) + 2 t, + 1
+          if (hit & 1u) f[0] = f[2] = quiet_nan();
+          if (hit & 0x10000u) f[1] = f[3] = quiet_nan();
+        }
+  };
   for (; cs.rem > 0; place_next(sc, p, cs)) {
     const int32_t j1 = min(cs.nb, cs.j + cs.rem);
     if (cs.j >= j1) continue;  // only the segment's charge lies in this range
@@ -580,10 +596,9 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
     }
 
     // ---- The segment's end in this warp's range.
-    if (__any_sync(0xffffffffu, nan_seen != 0)) {
-      uint32_t hit[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) hit[nt][0] = hit[nt][1] = 0;
+    for (int nt = 0; nt < NT; ++nt) nan_hit[nt] = 0;
+    if (__any_sync(0xffffffffu, nan_seen != 0)) {
       each_uneven_nan<D>(p, tl.seq, cs.g, max((tl.fb + cs.j) * kBlk, first_visible(all_hi, tl.window)),
                          min((tl.fb + j1) * kBlk - 1, seg_hi), all_lo, all_hi, [&](int32_t key, uint32_t blocks) {
 #pragma unroll
@@ -591,16 +606,9 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int32_t hi = tl.pos0 + min(tl.r0 + 8 * nt + 2 * c + i, tl.r0 + tl.nrows - 1) / G;
-            if (key <= hi && key >= first_visible(hi, tl.window)) hit[nt][i] |= blocks;
+            if (key <= hi && key >= first_visible(hi, tl.window)) nan_hit[nt] |= blocks << (16 * i);
           }
       });
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)  // dimensions g (D / 8) + 2 t and the next
-            if (hit[nt][i] >> ((g * (D / 8) + 2 * t) / 16) & 1u) o[t][nt][i] = o[t][nt][2 + i] = quiet_nan();
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -629,6 +637,10 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
                 v[t] = pack_bf16x2(o[4 * w + t][nt][h] * inv, o[4 * w + t][nt][2 + h] * inv);
               reinterpret_cast<uint4*>(dst)[w] = make_uint4(v[0], v[1], v[2], v[3]);
             }
+            if (const uint32_t blocks = nan_hit[nt] >> (16 * h) & 0xffffu)
+#pragma unroll 1
+              for (int t = 0; t < MT; ++t)
+                if (blocks >> ((g * (D / 8) + 2 * t) / 16) & 1u) reinterpret_cast<uint32_t*>(dst)[t] = 0x7fff7fffu;
           }
         }
       continue;
@@ -652,6 +664,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         dst[(t * NT + nt) * 32] = make_float4(o[t][nt][0], o[t][nt][1], o[t][nt][2], o[t][nt][3]);
+    nan_to_state(dst);
   }
   // ---- Merge the CTA's pieces, once.  Those of one segment follow one another:
   // the kept ones of warps in order (one without blocks has a zero share), then
@@ -671,6 +684,7 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
     for (int nt = 0; nt < NT; ++nt)
       mbuf[(warp * MT * NT + t * NT + nt) * 32 + lane] =
           held ? make_float4(o[t][nt][0], o[t][nt][1], o[t][nt][2], o[t][nt][3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+  if (held) nan_to_state(mbuf + warp * MT * NT * 32 + lane);
   // Lane k looks at piece k: which others are its segment's.
   const int my_e = lane < 2 * W ? s_piece[lane].e : -1;
   const uint32_t my_members =
@@ -747,16 +761,16 @@ kv4_decode_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) 
 }
 
 template <int D, int NT, int NSEG>
-int launch_t(const Plan& plan, const Kv4Params& p, const Plan::Kv4Launch& l, cudaStream_t stream) {
+int launch_t(const Plan& plan, const Args& a, const Kv4Params& p, const Plan::Kv4Launch& l, cudaStream_t stream) {
   using Sh = Kv4Shape<D, NT>;
-  return launch_split<D, Sh::kRows, NSEG>(plan, p, l, Sh::W * 32, Sh::kBytes, kv4_decode_kernel<Sh, NSEG>, stream);
+  return launch_split<D, Sh::kRows, NSEG>(plan, a, p, l, Sh::W * 32, Sh::kBytes, kv4_decode_kernel<Sh, NSEG>, stream);
 }
 
 template <int D, int NT>
-int launch_n(const Plan& plan, const Kv4Params& p, const Plan::Kv4Launch& l, cudaStream_t stream) {
-  // Two sizes of launch parameters: 4 KB and 32 KB.
-  return l.end - l.begin <= kKv4TilesSmall ? launch_t<D, NT, kKv4TilesSmall>(plan, p, l, stream)
-                                           : launch_t<D, NT, kKv4TilesLarge>(plan, p, l, stream);
+int launch_n(const Plan& plan, const Args& a, const Kv4Params& p, const Plan::Kv4Launch& l, cudaStream_t stream) {
+  // Two sizes of launch parameters: 9 KB and 32 KB.
+  return l.end - l.begin <= kKv4TilesSmall ? launch_t<D, NT, kKv4TilesSmall>(plan, a, p, l, stream)
+                                           : launch_t<D, NT, kKv4TilesLarge>(plan, a, p, l, stream);
 }
 
 }  // namespace
@@ -782,11 +796,11 @@ int launch_kv4_decode(const Plan& plan, const Args& a, void* stream) {
       continue;
     }
     switch (plan.d * 8 + l.nt) {
-      case 64 * 8 + 1: e = launch_n<64, 1>(plan, p, l, s); break;
-      case 64 * 8 + 2: e = launch_n<64, 2>(plan, p, l, s); break;
-      case 128 * 8 + 1: e = launch_n<128, 1>(plan, p, l, s); break;
-      case 128 * 8 + 2: e = launch_n<128, 2>(plan, p, l, s); break;
-      case 256 * 8 + 1: e = launch_n<256, 1>(plan, p, l, s); break;
+      case 64 * 8 + 1: e = launch_n<64, 1>(plan, a, p, l, s); break;
+      case 64 * 8 + 2: e = launch_n<64, 2>(plan, a, p, l, s); break;
+      case 128 * 8 + 1: e = launch_n<128, 1>(plan, a, p, l, s); break;
+      case 128 * 8 + 2: e = launch_n<128, 2>(plan, a, p, l, s); break;
+      case 256 * 8 + 1: e = launch_n<256, 1>(plan, a, p, l, s); break;
     }
     if (e) return e;
   }

@@ -179,7 +179,7 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
 #pragma unroll
   for (int st = 0; st < S; ++st) issue(st);
   if (const int t = blockIdx.x + gridDim.x * tid; t < sc.n_tiles)
-    check_lengths(sc.tile, t, sc.n_tiles, p.cu_q_lens, p.kv_lens, p.num_seqs, p.total_q, p.ws);
+    check_lengths(sc.tile, t, sc.n_tiles, sc.cu_q_lens, sc.kv_lens, sc.num_seqs, sc.total_q, p.ws);
 
 
   // ---- Widening: 64 dimensions of one key a lane, in four pieces of 16.
@@ -524,14 +524,14 @@ kv4_rows_kernel(const Kv4Params p, const __grid_constant__ Kv4Sched<NSEG> sc) {
 }
 
 template <int D, int NSEG>
-int launch_rows_t(const Plan& plan, const Kv4Params& p, const Plan::Kv4Launch& l, cudaStream_t stream) {
+int launch_rows_t(const Plan& plan, const Args& a, const Kv4Params& p, const Plan::Kv4Launch& l, cudaStream_t stream) {
   using Sh = RowsShape<D>;
-  return launch_split<D, Sh::kRows, NSEG>(plan, p, l, Sh::W * 32, Sh::kBytes, kv4_rows_kernel<Sh, NSEG>, stream);
+  return launch_split<D, Sh::kRows, NSEG>(plan, a, p, l, Sh::W * 32, Sh::kBytes, kv4_rows_kernel<Sh, NSEG>, stream);
 }
 template <int D>
-int launch_rows_n(const Plan& plan, const Kv4Params& p, const Plan::Kv4Launch& l, cudaStream_t stream) {
-  return l.end - l.begin <= kKv4TilesSmall ? launch_rows_t<D, kKv4TilesSmall>(plan, p, l, stream)
-                                           : launch_rows_t<D, kKv4TilesLarge>(plan, p, l, stream);
+int launch_rows_n(const Plan& plan, const Args& a, const Kv4Params& p, const Plan::Kv4Launch& l, cudaStream_t stream) {
+  return l.end - l.begin <= kKv4TilesSmall ? launch_rows_t<D, kKv4TilesSmall>(plan, a, p, l, stream)
+                                           : launch_rows_t<D, kKv4TilesLarge>(plan, a, p, l, stream);
 }
 
 }  // namespace
@@ -542,9 +542,9 @@ int launch_kv4_rows(const Plan& plan, const Args& a, const Plan::Kv4Launch& l, v
   const Kv4Params p = kv4_params(plan, a);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (plan.d) {
-    case 64: return launch_rows_n<64>(plan, p, l, s);
-    case 128: return launch_rows_n<128>(plan, p, l, s);
-    default: return launch_rows_n<256>(plan, p, l, s);
+    case 64: return launch_rows_n<64>(plan, a, p, l, s);
+    case 128: return launch_rows_n<128>(plan, a, p, l, s);
+    default: return launch_rows_n<256>(plan, a, p, l, s);
   }
 }
 

@@ -957,14 +957,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
         }
       } else {
-        uint32_t nan = 0;  // blocks of 16 dimensions that hold a NaN for this row
-        if constexpr (kKv4) {
-          if (look_for_nan && valid) {
-            const int32_t pos = gm.pos_first + tok;
-            nan = kv4_nan_blocks<D>(x.v_scales, x.page_table + static_cast<int64_t>(gm.seq) * p.mpps, x.num_pages,
-                                    p.page_shift, p.hq / G, gm.g, first_visible(pos, gm.W), pos);
-          }
-        }
         __nv_bfloat16* orow =
             p.out + (static_cast<int64_t>(gm.t0 + tok) * p.hq + gm.g * G + head) * D;
         // Each thread writes 32 bytes of its own row per 16 columns (one
@@ -976,11 +968,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             w[q] = pack_bf16x2(__uint_as_float(o[2 * q]) * inv, __uint_as_float(o[2 * q + 1]) * inv);
-          if constexpr (kKv4)
-            if (nan >> (col >> 4) & 1u) {
-#pragma unroll
-              for (int q = 0; q < 8; ++q) w[q] = 0x7fff7fffu;
-            }
           if (p.out_v8) {
             st_global_v8(orow + col, w);
           } else {
@@ -1001,6 +988,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           store16(ob, c0 + 16);
           tmem_wait_ld();
         }
+        if constexpr (kKv4)
+          if (look_for_nan && valid) {
+            // NaN over the 16-dimension blocks in which a key of the row has one.
+            const int32_t pos = gm.pos_first + tok;
+            const uint32_t nan =
+                kv4_nan_blocks<D>(x.v_scales, x.page_table + static_cast<int64_t>(gm.seq) * p.mpps, x.num_pages,
+                                  p.page_shift, p.hq / G, gm.g, first_visible(pos, gm.W), pos);
+#pragma unroll 1
+            for (int w = 0; w < D / 8; ++w)
+              if (nan >> (w >> 1) & 1u) reinterpret_cast<uint4*>(orow)[w] = make_uint4(~0u, ~0u, ~0u, ~0u);
+          }
       }
       tc_fence_before();
       mbar_arrive(&B.o_free);
