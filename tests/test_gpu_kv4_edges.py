@@ -159,6 +159,7 @@ PROMPT_VALUES = [
     ([150, 140], [150, 400], 8, 1, 256, 128, [0, 33], 0),
     ([300, 129], [300, 700], 4, 2, 64, 16, [7, 0], 0),
     ([260], [260], 128, 1, 64, 32, [100], 0),                         # G = 128
+    ([129] * 5, [129, 140, 150, 333, 129], 256, 256, 64, 16, None, 0),  # more items than a launch takes
 ]
 
 
