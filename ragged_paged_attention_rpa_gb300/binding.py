@@ -251,7 +251,8 @@ def rpa_plan(cu_q_lens_host, kv_lens_host, window_host, num_q_heads: int,
     meta = dict(num_seqs=num_seqs, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads,
                 head_dim=head_dim, page_size=page_size, has_window=win is not None,
                 dtype=dtype, total_q=int(cu[-1]), num_pages=num_pages,
-                max_pages_per_seq=max_pages_per_seq)
+                max_pages_per_seq=max_pages_per_seq, q_shape=(int(cu[-1]), num_q_heads, head_dim),
+                table_shape=(num_seqs, max_pages_per_seq))
     return Plan(handle.value, ws.value, meta)
 
 
@@ -514,6 +515,20 @@ def rpa_read_kv4(k_pages, v_pages, k_scales, v_scales, slot_map, k_out, v_out, w
         raise RpaError(rc, "rpa_read_kv4")
 
 
+def _kv4_check_sizes(m, q, out, page_table, cu_q_lens, kv_lens, window):
+    """Sizes other than the plan's own: larger ones, and rows laid out flat, will
+    do."""
+    s, rows, width = m["num_seqs"], m["q_shape"][1:], m["max_pages_per_seq"]
+    least = m["total_q"] * rows[0] * rows[1]
+    for t in (q, out):
+        if t.numel() < least or (t.dim() == 3 and t.shape[1:] != rows):
+            raise ValueError("q and out must hold the plan's %d rows of %d x %d" % (m["total_q"], *rows))
+    if page_table.numel() < s * width or (page_table.dim() == 2 and page_table.shape[1] != width):
+        raise ValueError("page_table must be [%d, %d], got %s" % (s, width, tuple(page_table.shape)))
+    if cu_q_lens.numel() <= s or kv_lens.numel() < s or (window is not None and window.numel() < s):
+        raise ValueError("cu_q_lens must have %d entries, kv_lens and window %d" % (s + 1, s))
+
+
 def _kv4_args(q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv_lens, window,
               sm_scale, out, plan, workspace, stream):
     """The marshalled arguments of rpa_forward_kv4."""
@@ -526,15 +541,9 @@ def _kv4_args(q, k_pages, v_pages, k_scales, v_scales, page_table, cu_q_lens, kv
     if (hkv != m["num_kv_heads"] or p != m["page_size"] or d != m["head_dim"]
             or pages < m["num_pages"]):
         raise ValueError("the pools' shape differs from the plan's")
-    least, rows = m["total_q"] * hq * d, (hq, d)
-    for t in (q, out):
-        if t.numel() < least or (t.dim() == 3 and t.shape[1:] != rows):
-            raise ValueError("q and out must hold the plan's %d rows of %d x %d" % (m["total_q"], hq, d))
-    width = m["max_pages_per_seq"]
-    if page_table.numel() < s * width or (page_table.dim() == 2 and page_table.shape[1] != width):
-        raise ValueError("page_table must be [%d, %d], got %s" % (s, width, tuple(page_table.shape)))
-    if cu_q_lens.numel() <= s or kv_lens.numel() < s or (window is not None and window.numel() < s):
-        raise ValueError("cu_q_lens must have %d entries, kv_lens and window %d" % (s + 1, s))
+    if not (q.shape == m["q_shape"] and out.shape == m["q_shape"] and page_table.shape == m["table_shape"]
+            and cu_q_lens.numel() == s + 1 and kv_lens.numel() == s and (window is None or window.numel() == s)):
+        _kv4_check_sizes(m, q, out, page_table, cu_q_lens, kv_lens, window)
     ws, n = _workspace(workspace, dev)
     return (_addr(q, "q", bf16, dev), kp, vp, ks, vs, _addr(page_table, "page_table", i32, dev),
             _addr(cu_q_lens, "cu_q_lens", i32, dev), _addr(kv_lens, "kv_lens", i32, dev),
