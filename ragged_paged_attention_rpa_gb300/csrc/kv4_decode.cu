@@ -39,13 +39,14 @@
 // What bounds it: 0.5625 bytes an element come from HBM, and each element
 // costs about one issue slot in 32 (widen, scale, multiply).  Long contexts run
 // at HBM's rate: 32 tokens over 4096-32768 keys of 8 heads of 128 (727 MB)
-// 122.0 us, 6.0 TB/s, with the schedulers 65% busy and no pipe above 50%; 152
-// contexts of 16k keys of 256 dimensions 112.6 us, 6.4 TB/s; at 64 dimensions,
+// 125.6 us, 5.8 TB/s, with the schedulers 65% busy and no pipe above 50%; 152
+// contexts of 16k keys of 256 dimensions 113.4 us, 6.3 TB/s; at 64 dimensions,
 // where a row's scale and address work is shared by fewer elements, issue is the
-// limit: 64 contexts of 8 heads 71.0 us, 5.1 TB/s.  Short ones are latency: 128
-// tokens over 128-2048 keys of 256 (37.6 MB) take 17.3 us, of which 6 until the
-// first data, 5-7 for the range, 4-6 for the merge and the combine; one token
-// over 700 keys of 64 takes 6.6 us.
+// limit: 32 contexts of 8 heads 71.0 us, 5.1 TB/s.  Short ones are latency: 128
+// tokens over 128-2048 keys of 256 (37.6 MB) take 20.2 us, of which 6 until the
+// first data, 5-7 for the range, 4-6 for the merge and the combine (17.8 us where
+// the pages are in L2); one token over 700 keys of 64 takes 7.0 us.  (Calls
+// replayed from a graph, the inputs rotated past L2.)
 #include <algorithm>
 #include <type_traits>
 
@@ -104,7 +105,7 @@ struct RowLayout {
 // with the registers it leaves): 256 dimensions 8 x 32 6.35 TB/s of 4-bit pages
 // over 152 contexts of 16k, 12 x 16 6.02, 16 x 16 6.16 with spills, 12 x 32
 // spills; 128 dimensions 12 x 32 5.80 over 32 long contexts, 16 x 32 5.75,
-// 16 x 16 5.29; 64 dimensions 16 x 64 4.60 over 64 long contexts, 16 x 32 4.22;
+// 16 x 16 5.29; 64 dimensions 16 x 64 4.60 over 32 long contexts, 16 x 32 4.22;
 // 10 or 14 warps, which the four schedulers cannot share evenly,
 // 5 to 11% below their neighbours.
 // Two blocks in flight a warp are enough: more only make the first ones wait

@@ -25,13 +25,14 @@
 // ldmatrix, the widening, the softmax, the next copies) at about four cycles
 // each, two warps a scheduler: O and Q of 16 rows take 192 registers at 256
 // dimensions.  128 sequences of 64 rows over 128-2048 keys of 256 dimensions take
-// 59.1 us (47 MB from HBM; widening to bf16 pages and the prefill kernel 72.7 us,
-// tiles of 8 rows 77 us); 32 rows of each 46 us.  Tried: one barrier for both
-// halves (as fast; at 128 dimensions 32 sequences of 64 rows over 120-4000 keys
-// of 8 heads 96 us, 92 so); the next block's widening between this one's products
-// 61 us; 16 warps of 128 registers, each with a
-// quarter of the keys for S and of the dimensions for O, 69 us (the copies' and
-// the softmax's instructions then run in twice as many warps).
+// 63.6 us (61.6 with the 47 MB of pages in L2); 32 rows of each 48.5 us.  While it
+// took 59 of those 61.6 (the looks for NaN in V and at the lengths are the rest):
+// widening to bf16 pages and the prefill kernel 72.7 us, tiles of 8 rows 77 us; one
+// barrier for both halves as fast (at 128 dimensions 32 sequences of 64 rows over
+// 120-4000 keys of 8 heads 96 us, 92 so); the next block's widening between this
+// one's products 61 us; 16 warps of 128 registers, each with a quarter of the keys
+// for S and of the dimensions for O, 69 us (the copies' and the softmax's
+// instructions then run in twice as many warps).
 #include "kv4_split.cuh"
 
 namespace rpa {

@@ -24,8 +24,8 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Which part is faster for a sequence of several rows depends on the batch: the
 // prefill does not split a sequence's keys over CTAs, the split-KV kernels widen
 // them once a tile (128 sequences of 64 rows over 128-2048 keys of 256: 72 us on
-// the prefill, 59 split; 64 of 128 rows over as many: 51 against 61; 8 of 64 rows
-// over 16k-30k keys: 459 against 69).  So the row limit is the one of these
+// the prefill, 62 split; 64 of 128 rows over as many: 51 against 61; 8 of 64 rows
+// over 16k-30k keys: 459 against 71).  So the row limit is the one of these
 // with the smallest modelled time.
 constexpr int32_t kRowLimits[] = {16, 32, 64, 128};
 // Fewest key blocks (segment charges included) a warp of the split-KV kernel
@@ -75,7 +75,7 @@ struct Problem {
 // a sequence has more than 8 and the kernel's registers hold them (head_dim below
 // 256).  Beyond, tiles of 64 (32 sequences of 32 rows of 128 dimensions, 8 heads,
 // over 120-4000 keys: 62 us in tiles of 16, 73 in one of 64; 128 sequences of 32
-// rows of 256: 73 us on the prefill, 46 in one of 64).
+// rows of 256: 73 us on the prefill, 48 in one of 64).
 int32_t tile_rows(int32_t head_dim, int32_t rows) {
   if (rows > (head_dim == 256 ? 16 : 32)) return 8 * kKv4RowsTile;
   return rows > 8 && head_dim < 256 ? 16 : 8;
@@ -258,7 +258,7 @@ rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu, const int32_t* kv
   }
   // A mixed batch's split of the SMs between the two parts, as for 16-bit
   // pages: side by side where the split that evens their modelled times beats
-  // one after the other (512 single tokens and 4 chunks of 2048: 187 us at 39 /
+  // one after the other (512 single tokens and 4 chunks of 2048: 189 us at 39 /
   // 113 SMs, 208 us one after the other).
   if (best.dec && best.pre && opts.decode_sms >= 0 && n >= 2) {
     int32_t x = opts.decode_sms > 0 ? std::min(opts.decode_sms, n - 1) : 0;
