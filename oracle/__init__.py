@@ -198,7 +198,7 @@ def decode_kv4(codes, scales) -> np.ndarray:
     """4-bit rows -> float32 values (exact): codes [..., D / 2] hold two e2m1
     codes a byte (the even dimension low; sign, two exponent bits of bias 1, one
     mantissa bit), scales [..., D / 16] a byte of five exponent bits (bias 15)
-    and three mantissa bits each, 255 NaN."""
+    and three mantissa bits each, 255 NaN (227 to 254 are in no valid pool)."""
     codes, scales = np.asarray(codes), np.asarray(scales)
     c = np.stack([codes & 15, codes >> 4], -1).reshape(codes.shape[:-1] + (2 * codes.shape[-1],)).astype(np.int64)
     e, m = (c >> 1) & 3, c & 1

@@ -8,6 +8,8 @@ Bounds are those of test_gpu_kv4.py, with the probabilities' own rounding: f16
 
 from __future__ import annotations
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -451,3 +453,57 @@ def test_random_batches(seed):
     win = pick(None, [int(rng.integers(0, 90)) for _ in range(n)], [pick(0, 1, 500) for _ in range(n)])
     run_and_check(batch(ql, kv, hkv * group, hkv, d, p, win, seed=seed), num_sms=pick(0, 0, 1, 7, 40),
                   decode_sms=pick(0, 0, -1))
+
+
+# ---------------------------------------------------------------- at once
+
+def test_calls_at_once():
+    """Mixed batches from several host threads, and from one thread on two
+    streams in turn, each with a workspace of its own: the bits of calls made
+    one at a time.  One of them holds NaN, the others' headers do not hear of it."""
+    runs = []
+    for i in range(4):
+        n = 30 + 7 * i
+        kv = [40 + 61 * j % 900 for j in range(n)]
+        ql = [1] * (n - 3) + [7, 150 + i, 20]
+        kv[-3:] = [400, 500, 300]
+        b = batch(ql, kv, 8, 2, 128, 16, [0] * n if i % 2 else [j % 3 * 50 for j in range(n)], seed=60 + i)
+        if i == 2:
+            for s in (3, n - 2):
+                page, at = slot(b, s, kv[s] - 1)
+                b.v_fp4_scale[page, 0, at, 2] = 255
+        runs.append(Kv4Batch(b, decode_sms=20 if i != 1 else -1))
+    want = [r.call().clone() for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    errors = []
+
+    def work(i):
+        try:
+            torch.cuda.set_device(0)
+            for _ in range(20):
+                runs[i].call(stream=streams[i])
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    def same():
+        torch.cuda.synchronize()
+        assert not errors, errors
+        for i, r in enumerate(runs):
+            assert binding.rpa_get_device_error(r.ws) == 0 and bool((r.ws[:256] == 0).all())
+            assert torch.equal(r.out.view(torch.int16), want[i].view(torch.int16)), i
+            r.out.zero_()
+        torch.cuda.synchronize()
+    for r in runs:
+        r.out.zero_()
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    same()
+    for _ in range(10):
+        for i in range(4):
+            runs[i].call(stream=streams[i])
+    same()
