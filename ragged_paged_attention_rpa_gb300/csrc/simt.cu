@@ -51,11 +51,20 @@ simt_attention_kernel(Args a, SimtParams p) {
     const int32_t s = find_seq(a.cu_q_lens, p.num_seqs, t);
     const int32_t q0 = __ldg(a.cu_q_lens + s);
     const int32_t q1 = __ldg(a.cu_q_lens + s + 1);
-    const int32_t seg_end = min(t_end, q1);
+    const int32_t L = __ldg(a.kv_lens + s);
     const int32_t ql = q1 - q0;
+    // Lengths that hold no token t (those of a step that the table build refused:
+    // all of them 0), or fewer keys than queries, are not the plan's.  Either way
+    // the loop goes on behind t.
+    const bool bad = q0 > t || q1 <= t || L < ql;
+    const int32_t seg_end = q1 > t ? min(t_end, q1) : t_end;
+    if (bad) {
+      if (threadIdx.x == 0) report_error(a.workspace, RPA_DEVERR_LENGTHS, s);
+      t = seg_end;
+      continue;
+    }
     const bool take = (ql == 1) ? p.do_decode : p.do_prefill;
     if (take) {
-      const int32_t L = __ldg(a.kv_lens + s);
       const int32_t W = a.window ? __ldg(a.window + s) : 0;
       const int32_t n_rows = (seg_end - t) * G;
       const int32_t pos_first = L - ql + (t - q0);
