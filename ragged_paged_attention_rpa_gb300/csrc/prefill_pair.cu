@@ -112,8 +112,9 @@ struct Geom {
   bool ok;
 };
 
-__device__ __forceinline__ Geom pair_geom(const PairParams& p, const PrefillItem& it,
-                                          uint32_t rank) {
+// total_q: rows of q and out, which device lengths may pass.
+__device__ __forceinline__ Geom pair_geom(const PairParams& p, const PrefillItem& it, uint32_t rank,
+                                          int32_t total_q) {
   Geom r;
   r.seq = it.seq;
   r.g = it.qb_head & 255;
@@ -132,7 +133,7 @@ __device__ __forceinline__ Geom pair_geom(const PairParams& p, const PrefillItem
   r.t0 = q0 + qb * qbt;
   r.ntok = rank == 0 ? n0 : n1;
   r.pos_first = L - ql + qb * qbt;
-  r.ok = n0 > 0 && first0 >= 0 && r.pos_last < L && (r.pos_last >> p.page_shift) < p.mpps;
+  r.ok = q0 >= 0 && q0 + b0 * qbt + n0 + n1 <= total_q && n0 > 0 && first0 >= 0 && r.pos_last < L && (r.pos_last >> p.page_shift) < p.mpps;
   r.lo = first_visible(first0, r.W);
   r.key_first = r.lo / kTileAlign * kTileAlign;
   r.ntiles = r.ok ? (r.pos_last - r.key_first) / kBN + 1 : 0;
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const PairParams p,
-                    const __grid_constant__ ItemList items) {
+                    const __grid_constant__ ItemList items, int32_t total_q) {
   using Lay = Layout<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // Both CTAs of the pair take the same branch here (same launch, same
@@ -252,7 +253,7 @@ prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_q,
     uint32_t C = 0, I = 0, issued_q = 0;
     bool alive = true;
     for (int it = pair_id; it < items.n && alive; it += n_pairs) {
-      const Geom gm = pair_geom(p, items.items[it], rank);
+      const Geom gm = pair_geom(p, items.items[it], rank, total_q);
       if (!gm.ok) {
         if (lane == 0 && is_k) report_error(p.ws, RPA_DEVERR_LENGTHS, gm.seq);
         continue;
@@ -414,7 +415,7 @@ prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_q,
         return true;
       };
       for (int it = pair_id; it < items.n && alive; it += n_pairs) {
-        const Geom gm = pair_geom(p, items.items[it], 0);
+        const Geom gm = pair_geom(p, items.items[it], 0, total_q);
         if (!gm.ok) continue;
         alive = wait(&B.q_full, I & 1);
         if (!alive) break;
@@ -477,7 +478,7 @@ prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_q,
       return o;
     };
     for (int it = pair_id; it < items.n && alive; it += n_pairs) {
-      const Geom gm = pair_geom(p, items.items[it], rank);
+      const Geom gm = pair_geom(p, items.items[it], rank, total_q);
       if (!gm.ok) continue;
       const bool valid = tok < gm.ntok && r < G * p.qb_tokens;
       const int32_t pos = gm.pos_first + tok;
@@ -693,7 +694,8 @@ int launch_pair_t(const Plan& plan, const Args& a, cudaStream_t stream) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_pair_kernel<D>, tq, tk, tv, p, list);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_pair_kernel<D>, tq, tk, tv, p, list,
+                                       static_cast<int32_t>(plan.total_q));
     if (e != cudaSuccess) return static_cast<int>(e);
     trace_mark(RPA_KERNEL_PREFILL_TC, stream);
   }

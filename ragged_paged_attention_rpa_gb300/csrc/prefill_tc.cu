@@ -127,11 +127,12 @@ struct PrefillParams {
 };
 
 // What the kernel has beside (last of its parameters, so that the others lie
-// where they did): nothing, or over widened 4-bit pages (kv4_expand.cu) the
-// 4-bit pages' V scales, table and number, by which the epilogue finds the rows
-// that see a NaN in V.
+// where they did): the rows of q and out, and over widened 4-bit pages
+// (kv4_expand.cu) the 4-bit pages' V scales, table and number, by which the
+// epilogue finds the rows that see a NaN in V.
 struct Pages16 {
   static constexpr bool kKv4 = false;
+  int32_t total_q;
 };
 struct Pages4 {
   static constexpr bool kKv4 = true;
@@ -139,7 +140,7 @@ struct Pages4 {
   const int32_t* page_table;
   int32_t num_pages;
   int32_t last_launch;  // no launch of this call follows
-  int32_t total_q;      // rows of q and out
+  int32_t total_q;
 };
 
 // One 32-byte store (eight 32-bit words) to a 32-byte aligned address.
@@ -483,8 +484,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
             gm = item_geom(p, items.items[it]);
             split = items.items[it].split;
-            // (Lengths built on the device may pass the plan's.)
-            if constexpr (kKv4) gm.ok = gm.ok && gm.t0 >= 0 && gm.t0 + gm.ntok <= x.total_q;
+            // (Device lengths may name rows that q and out have not.)
+            gm.ok = gm.ok && gm.t0 >= 0 && gm.t0 + gm.ntok <= x.total_q;
             if (gm.ok) break;
             if (items.items[it].seq >= 0) report_error(p.ws, RPA_DEVERR_LENGTHS, gm.seq);
             it = next_item(it);
@@ -1032,7 +1033,7 @@ struct SplitList {
 // loads are issued before they are summed.
 template <int D>
 __global__ void __launch_bounds__(256)
-prefill_combine_kernel(const PrefillParams p, const __grid_constant__ SplitList gl) {
+prefill_combine_kernel(const PrefillParams p, const __grid_constant__ SplitList gl, int32_t total_q) {
   constexpr int E = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (static_cast<int>(blockIdx.x) >= gl.n) return;
@@ -1044,7 +1045,7 @@ prefill_combine_kernel(const PrefillParams p, const __grid_constant__ SplitList 
   const int32_t ntok = min(p.qb_tokens, ql - qb * p.qb_tokens);
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (r >= ntok * G) return;
+  if (r >= ntok * G || q0 < 0 || q0 + qb * p.qb_tokens + ntok > total_q) return;
   // Largest log2-sum-exp over the parts (lane k reads parts k, k + 32, ...).
   float M = -INFINITY;
   for (int k = lane; k < g.nparts; k += 32)
@@ -1098,7 +1099,7 @@ int launch_prefill_combine(const Plan& plan, const PrefillParams& p, cudaStream_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_combine_kernel<D>, p, gl);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_combine_kernel<D>, p, gl, static_cast<int32_t>(plan.total_q));
     if (e != cudaSuccess) return static_cast<int>(e);
     trace_mark(RPA_KERNEL_PREFILL_COMBINE, stream);
   }
@@ -1169,8 +1170,9 @@ int launch_prefill_t(const Plan& plan, const Args& a, cudaStream_t stream) {
       for (int c = 0; c <= grid; ++c) list.cta0[c] = plan.pcta0[c];
     }
     Pages x;
-    if constexpr (Pages::kKv4) x = Pages{a.v_block_scales, a.kv4_page_table, a.kv4_num_pages, off + cnt == n,
-                                            static_cast<int32_t>(plan.total_q)};
+    if constexpr (Pages::kKv4)
+      x = Pages{a.v_block_scales, a.kv4_page_table, a.kv4_num_pages, off + cnt == n, 0};
+    x.total_q = static_cast<int32_t>(plan.total_q);
     prefill_tc_kernel<D, Pages><<<grid, kThreads, Lay::kBytes, stream>>>(tq, tk, tv, p, list, x);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return static_cast<int>(e);

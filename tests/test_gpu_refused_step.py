@@ -69,3 +69,32 @@ def test_the_cuda_core_path_ends(case):
     forward(b, db.cu_q_lens + last, db.kv_lens + last[1:])
     err, out = forward(b, db.cu_q_lens, db.kv_lens)
     assert err == 0 and bool(torch.isfinite(out).all()) and not bool((out == 3.0).all())
+
+
+PREFILL = [
+    # (q_lens, kv_lens, Hq, Hkv, D, P, plan options): the single-SM kernel, its
+    # static lists and split items, SM pairs, beside decode
+    ([200], [300], 4, 2, 64, 16, {}),
+    ([200, 70], [300, 90], 8, 1, 256, 16, dict(prefill_dynamic=-1)),
+    ([200], [1500], 4, 2, 128, 16, dict(prefill_split=2)),
+    ([300, 33], [300, 33], 4, 1, 128, 16, dict(prefill_pairs=2)),
+    ([1] * 5 + [150], [40 + 16 * i for i in range(5)] + [170], 8, 2, 128, 32, {}),
+]
+
+
+@pytest.mark.parametrize("case", range(len(PREFILL)))
+def test_the_tensor_core_prefill_stays_inside(case):
+    ql, kv, hq, hkv, d, p, kw = PREFILL[case]
+    b = workloads.make_batch(ql, kv, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, page_size=p, seed=10 + case,
+                             max_pages_per_seq=max(kv) // p + 2)
+    err, good = forward(b, *(lambda db: (db.cu_q_lens, db.kv_lens))(binding.Batch(b)), **kw)
+    assert err == 0 and bool(torch.isfinite(good).all())
+    new = np.diff(b.cu_q_lens)
+    if any(-(-k // p) > -(-(k - n) // p) for k, n in zip(kv, new)):
+        assert forward(b, *refused(b), **kw)[0] == binding.RPA_DEVERR_LENGTHS
+    db = binding.Batch(b)
+    last = torch.zeros_like(db.cu_q_lens)
+    last[-1] = 1
+    for cu, lens in ((db.cu_q_lens + last, db.kv_lens + last[1:]), (db.cu_q_lens + 1, db.kv_lens),
+                     (db.cu_q_lens - 300, db.kv_lens)):
+        assert forward(b, cu, lens, **kw)[0] == binding.RPA_DEVERR_LENGTHS
