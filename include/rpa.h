@@ -171,6 +171,12 @@ typedef struct rpa_plan_options {
                                (DRAM reads near the algorithmic bytes, ~1%
                                longer on the causal 8k prefill), -1 longest
                                first over the whole batch                      */
+  int32_t tree_words;       /* 0: none of the below.  1..16: a plan for
+                               rpa_forward_tree, whose masks have that many
+                               64-bit words a row (every q_len at most 64 times
+                               as many); of the other options it takes path and
+                               num_sms, the rest must be 0, else
+                               RPA_ERR_UNSUPPORTED                              */
 } rpa_plan_options;
 
 /* What a plan chose; filled by rpa_plan_get_info. */
@@ -571,6 +577,163 @@ rpa_status_t rpa_release_tables(const int32_t* finished, const int32_t* kv_lens_
                                 rpa_stream_t stream);
 
 /*
+ * The steps below are a speculative one whose drafted tokens form a tree: request
+ * s verifies its q_len new tokens (nodes) at once, node i following node
+ * parents[i] (or the cached context), so that several nodes may hold the same
+ * position.  A step is rpa_build_tables (pages and slots for the nodes),
+ * rpa_build_tree (masks and positions), for each layer rpa_append_rope and
+ * rpa_forward_tree, then the caller's choice of a path, for each layer
+ * rpa_commit_tree and at last rpa_trim_tables.  C = kv_lens[s] - q_len is a
+ * request's context; node i's row lies at place C + i of its cache until the path
+ * is committed.
+ */
+
+/*
+ * Masks and positions of the nodes from their parents, on the GPU.
+ *
+ * parents [total_q] int32: for node i of its request an earlier node j of the same
+ * request (0 <= j < i), or -1 where it follows the context.  depth(i) is 0 there
+ * and depth(j) + 1 otherwise.  Writes
+ *   tree_mask [total_q, mask_words] 64-bit words: bit j % 64 of word j / 64 of row
+ *             cu_q_lens[s] + i is set iff node j is node i or one of its ancestors
+ *             (and, where window[s] > 0, depth(i) - depth(j) < window[s]);
+ *   positions [total_q] int32: kv_lens[s] - q_len + depth(i).
+ * window [num_seqs] int32 (<= 0: none) or NULL.  Rows behind the last request are
+ * left as they were.
+ *
+ * A parent outside [-1, i) sets RPA_DEVERR_LENGTHS and counts as -1.  A request
+ * whose lengths cannot be used (decreasing, more than 64 * mask_words nodes, more
+ * nodes than keys, rows behind total_q) sets it too, and its rows are left as they
+ * were.  mask_words 1..16.  Device pointers 4-byte (tree_mask 8-byte) aligned;
+ * `workspace` may be NULL, otherwise its error word records these.  Enqueues one
+ * kernel on `stream`; does not synchronise.
+ */
+rpa_status_t rpa_build_tree(const int32_t* parents, const int32_t* cu_q_lens,
+                            const int32_t* kv_lens, const int32_t* window, uint64_t* tree_mask,
+                            int32_t* positions, int32_t num_seqs, int32_t total_q,
+                            int32_t mask_words, void* workspace, rpa_stream_t stream);
+
+/*
+ * Rows of q and k rotated by given positions, and the rows of k and v written into
+ * their pages.  (rpa_qkv_prologue derives consecutive positions and slots from the
+ * lengths; here both are given, as a tree of tokens needs them.)
+ *
+ * With a = positions[t] * inv_freq[i] for i < rotary_dim / 2, dimensions x and y
+ * of every q and k row become x cos a - y sin a and y cos a + x sin a, where (x, y)
+ * are (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when `interleaved` is nonzero;
+ * dimensions from rotary_dim on, and v, stay as they are.  fp32 arithmetic; the
+ * angle is reduced in fixed point, its error at most 2^-47 |a| + 2^-23.  Any int32
+ * is a position.
+ */
+typedef struct rpa_rope {
+  const float* inv_freq; /* device, [rotary_dim / 2]; NULL with rotary_dim 0   */
+  int32_t rotary_dim;    /* a multiple of 16 in [0, head_dim]; 0: no rotation  */
+  int32_t interleaved;   /* 0: the two halves turn together; else neighbours   */
+} rpa_rope;
+
+/*
+ * q [total_q, num_q_heads, head_dim], k, v [total_q, num_kv_heads, head_dim] of
+ * `dtype` (BF16 or F32), a token's heads contiguous and tokens q_stride, k_stride
+ * and v_stride elements apart (slices of one projection's output, for instance;
+ * strides at least a token's heads and a multiple of 16 bytes).  q_out [total_q,
+ * num_q_heads, head_dim] contiguous; it may be q.  With num_q_heads 0, q and q_out
+ * are not used (NULL).  slot_map [total_q] int64: token t goes to slot slot_map[t]
+ * of the pool (slot_map[t] / page_size is its page); of a token with a negative
+ * entry only q is written.  The slots of a call are distinct.
+ *
+ * kv_dtype is `dtype`, or RPA_DTYPE_FP8_E4M3: k_pages, v_pages [num_pages,
+ * page_size, num_kv_heads, head_dim] of it.  e4m3 pages hold row / k_scale[head]
+ * (v_scale for v; device float32 [num_kv_heads], positive) rounded to the nearest
+ * (ties to even) and at most 448, NaN as NaN: what rpa_forward_fp8kv reads.
+ * Otherwise k_scale and v_scale are NULL.
+ *
+ * head_dim 64, 128 or 256 and a page_size that is a power of two, else
+ * RPA_ERR_UNSUPPORTED.  Pointers to rows and pages 16-byte aligned.  `workspace` may
+ * be NULL; otherwise its error word records a slot outside the pool
+ * (RPA_DEVERR_PAGE_ID; of that token, too, only q is written).  Enqueues one
+ * kernel on `stream`; does not synchronise.
+ */
+rpa_status_t rpa_append_rope(const void* q, const void* k, const void* v, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                             const int64_t* slot_map, const rpa_rope* rope, void* q_out,
+                             void* k_pages, void* v_pages, const float* k_scale,
+                             const float* v_scale, int32_t total_q, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                             int32_t num_pages, int32_t dtype, int32_t kv_dtype, void* workspace,
+                             rpa_stream_t stream);
+
+/*
+ * Attention of the nodes over their context and their tree: rpa_forward with
+ * another mask.  Node i of request s, at row t = cu_q_lens[s] + i, sees
+ *   key j < C          iff window[s] <= 0 or positions[t] - j < window[s];
+ *   key C + j, j < q_len, iff bit j % 64 of tree_mask[t][j / 64] is set.
+ * Any mask will do (a node need not see itself, and may see a later one).  A row
+ * that sees no key, or whose visible scores are all -infinity, is written as zeros.
+ * `sm_scale` is any number.
+ *
+ * The plan must have tree_words > 0; tree_mask [total_q, tree_words] 64-bit words,
+ * 8-byte aligned.  positions [total_q] int32 are read where there is a window (with
+ * NULL window they may be NULL): those of rpa_build_tree, or any in [C, kv_lens[s]);
+ * one outside sets RPA_DEVERR_LENGTHS and counts as the nearest of these.  kv_lens
+ * includes the nodes, whose rows are in their pages already.
+ *
+ * bf16 q, pages and out run on tensor cores (page_size at least 16 and num_q_heads
+ * / num_kv_heads at most 128), fp32 and the rest on CUDA cores.  A NaN or an
+ * infinity in K or V reaches the rows that see its key, and no other.  Device
+ * lengths that differ from the plan's set RPA_DEVERR_LENGTHS; the call goes by the
+ * plan's.  The other arguments, the error word, unused slots, threads and CUDA
+ * graphs as rpa_forward.
+ */
+rpa_status_t rpa_forward_tree(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* page_table, const int32_t* cu_q_lens,
+                              const int32_t* kv_lens, const uint64_t* tree_mask,
+                              const int32_t* positions, int32_t num_seqs, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                              const int32_t* window, float sm_scale, void* out,
+                              rpa_stream_t stream, const rpa_plan_t* plan, void* workspace,
+                              size_t workspace_bytes);
+
+/*
+ * The accepted path's rows moved together: for every request s and k with
+ * path[s][k] >= 0 the rows of K and V of node path[s][k] are copied to node k's
+ * slot, as if all were read before any is written.
+ *
+ * path [num_seqs, max_path] int32: increasing nodes of the request, then -1.
+ * slot_map [total_q] int64 as for rpa_append_rope (node i of request s has entry
+ * cu_q_lens[s] + i), its slots distinct.  Nothing else in the pool changes.
+ * k_pages, v_pages [num_pages, page_size, num_kv_heads, head_dim] of `dtype` (BF16,
+ * F32 or FP8_E4M3), 16-byte aligned; head_dim times the element size a multiple
+ * of 16 bytes, max_path at most 1024, else RPA_ERR_UNSUPPORTED.
+ *
+ * A path that does not increase, has a node behind its request's, or one after a
+ * -1 sets RPA_DEVERR_LENGTHS (as do lengths that cannot be used), a slot outside
+ * the pool RPA_DEVERR_PAGE_ID; that request's rows then stay as they were.
+ * `workspace` may be NULL.  Enqueues one kernel on `stream`; does not synchronise.
+ */
+rpa_status_t rpa_commit_tree(void* k_pages, void* v_pages, const int64_t* slot_map,
+                             const int32_t* cu_q_lens, const int32_t* path, int32_t num_seqs,
+                             int32_t total_q, int32_t max_path, int32_t num_kv_heads,
+                             int32_t head_dim, int32_t page_size, int32_t num_pages,
+                             int32_t dtype, void* workspace, rpa_stream_t stream);
+
+/*
+ * Requests cut short: drop_lens[s] >= 0 tokens leave the end of request s, whose
+ * pages behind its new length go back to the stack: kv_lens[s] = kv_lens_prev[s] -
+ * drop_lens[s], and the pages at slots ceil(kv_lens[s] / page_size) up to
+ * ceil(kv_lens_prev[s] / page_size) of its row are pushed in (request, slot) order,
+ * free_pages[*free_count_prev ...]; free_count is the stack's new height.  The
+ * page table is only read.  In place, device pointers and workspace as
+ * rpa_build_tables, all or nothing and its errors as rpa_release_tables (a request
+ * that drops more than it has sets RPA_DEVERR_LENGTHS).
+ */
+rpa_status_t rpa_trim_tables(const int32_t* drop_lens, const int32_t* kv_lens_prev,
+                             const int32_t* page_table, int32_t* free_pages,
+                             const int32_t* free_count_prev, int32_t* kv_lens,
+                             int32_t* free_count, int32_t num_seqs, int32_t page_size,
+                             int32_t max_pages_per_seq, int32_t num_pages, void* workspace,
+                             rpa_stream_t stream);
+
+/*
  * Read the device error word at the start of `workspace` after everything
  * enqueued on `stream` so far (this call synchronises `stream`), store it in
  * *err (an RPA_DEVERR_* code) and reset it to RPA_DEVERR_NONE.
@@ -651,7 +814,13 @@ enum {
   RPA_KERNEL_KV4_WRITE = 10,     /* 4-bit cache write                 */
   RPA_KERNEL_KV4_READ = 11,      /* 4-bit cache read                  */
   RPA_KERNEL_BUILD_TABLES = 12,  /* page tables and slot maps built   */
-  RPA_KERNEL_RELEASE_TABLES = 13 /* finished requests' pages returned */
+  RPA_KERNEL_RELEASE_TABLES = 13, /* finished requests' pages returned */
+  RPA_KERNEL_BUILD_TREE = 14,    /* masks and positions of drafted trees */
+  RPA_KERNEL_APPEND_ROPE = 15,   /* rotation and cache write          */
+  RPA_KERNEL_TREE_ATTN = 16,     /* attention of drafted trees        */
+  RPA_KERNEL_TREE_COMBINE = 17,  /* combine of its cut segments       */
+  RPA_KERNEL_COMMIT_TREE = 18,   /* an accepted path's rows moved     */
+  RPA_KERNEL_TRIM_TABLES = 19    /* requests cut short                */
 };
 typedef struct rpa_trace_record {
   int32_t kernel; /* RPA_KERNEL_* */

@@ -13,4 +13,5 @@ from .binding import (  # noqa: F401
     RPA_DEVERR_NONE, RPA_DEVERR_PAGE_ID, RPA_DEVERR_LENGTHS, RPA_DEVERR_PLAN,
     RPA_DEVERR_TIMEOUT, RPA_DEVERR_LAUNCH, RPA_DEVERR_PAGES, Batch, ForwardCall, Plan, RpaError, alloc_workspace, rpa_clear_device_error,
     rpa_build_tables, rpa_forward, rpa_forward_kv4, rpa_get_device_error, rpa_plan, rpa_read_kv4,
-    rpa_release_tables, rpa_status_string, rpa_trace_begin, rpa_trace_end, rpa_write_kv4)
+    rpa_release_tables, rpa_status_string, rpa_trace_begin, rpa_trace_end, rpa_write_kv4,
+    rpa_append_rope, rpa_build_tree, rpa_commit_tree, rpa_forward_tree, rpa_trim_tables)

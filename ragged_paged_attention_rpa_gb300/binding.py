@@ -47,12 +47,15 @@ EXPORTS = ["rpa_plan", "rpa_plan_destroy", "rpa_plan_get_info", "rpa_forward",
            "rpa_trace_end", "rpa_status_string", "rpa_forward_decode_noalloc",
            "rpa_write_kv", "rpa_forward_kv", "rpa_forward_fp8kv", "rpa_qkv_prologue",
            "rpa_forward_qkv", "rpa_last_cuda_error", "rpa_write_kv4", "rpa_read_kv4",
-           "rpa_forward_kv4", "rpa_build_tables", "rpa_release_tables"]
+           "rpa_forward_kv4", "rpa_build_tables", "rpa_release_tables", "rpa_build_tree",
+           "rpa_append_rope", "rpa_forward_tree", "rpa_commit_tree", "rpa_trim_tables"]
 
 RPA_KERNEL_NAMES = {0: "decode_split", 1: "decode_combine", 2: "prefill_tc", 3: "simt",
                     4: "kv_write", 5: "prologue", 6: "prefill_combine", 7: "kv4_decode",
                     8: "kv4_combine", 9: "kv4_expand", 10: "kv4_write", 11: "kv4_read",
-                    12: "build_tables", 13: "release_tables"}
+                    12: "build_tables", 13: "release_tables", 14: "build_tree",
+                    15: "append_rope", 16: "tree_attn", 17: "tree_combine", 18: "commit_tree",
+                    19: "trim_tables"}
 
 
 class QkvNorm(ctypes.Structure):
@@ -61,6 +64,13 @@ class QkvNorm(ctypes.Structure):
     _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
                 ("v_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
                 ("rope_theta", ctypes.c_float)]
+
+
+class Rope(ctypes.Structure):
+    """rpa_rope: device float32 frequencies [rotary_dim / 2], the dimensions
+    they turn and whether neighbours (else the two halves) turn together."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 class RpaError(RuntimeError):
@@ -83,7 +93,8 @@ class _Options(ctypes.Structure):
                 ("num_sms", ctypes.c_int32), ("prefill_pairs", ctypes.c_int32),
                 ("kv_dtype", ctypes.c_int32), ("prefill_split", ctypes.c_int32),
                 ("decode_sms", ctypes.c_int32), ("decode_kernel", ctypes.c_int32),
-                ("prefill_dynamic", ctypes.c_int32), ("prefill_grouping", ctypes.c_int32)]
+                ("prefill_dynamic", ctypes.c_int32), ("prefill_grouping", ctypes.c_int32),
+                ("tree_words", ctypes.c_int32)]
 
 
 class PlanInfo(ctypes.Structure):
@@ -158,6 +169,18 @@ def lib() -> ctypes.CDLL:
         L.rpa_build_tables.restype = i32
         L.rpa_release_tables.argtypes = [vp] * 7 + [i32] * 4 + [vp, vp]
         L.rpa_release_tables.restype = i32
+        i64 = ctypes.c_int64
+        L.rpa_build_tree.argtypes = [vp] * 6 + [i32] * 3 + [vp, vp]
+        L.rpa_build_tree.restype = i32
+        L.rpa_append_rope.argtypes = ([vp] * 3 + [i64] * 3 + [vp, vp, ctypes.POINTER(Rope)] + [vp] * 5
+                                      + [i32] * 8 + [vp, vp])
+        L.rpa_append_rope.restype = i32
+        L.rpa_forward_tree.argtypes = [vp] * 8 + [i32] * 5 + [vp, ctypes.c_float, vp, vp, vp, vp, sz]
+        L.rpa_forward_tree.restype = i32
+        L.rpa_commit_tree.argtypes = [vp] * 5 + [i32] * 8 + [vp, vp]
+        L.rpa_commit_tree.restype = i32
+        L.rpa_trim_tables.argtypes = [vp] * 7 + [i32] * 4 + [vp, vp]
+        L.rpa_trim_tables.restype = i32
         L.rpa_get_device_error.argtypes = [vp, vp, ctypes.POINTER(i32)]
         L.rpa_get_device_error.restype = i32
         L.rpa_clear_device_error.argtypes = [vp, vp]
@@ -227,7 +250,7 @@ def rpa_plan(cu_q_lens_host, kv_lens_host, window_host, num_q_heads: int,
              q_block: int = 0, kv_split: int = 0, num_sms: int = 0,
              prefill_pairs: int = 0, kv_dtype: int = 0, prefill_split: int = 0,
              decode_sms: int = 0, decode_kernel: int = 0,
-             prefill_dynamic: int = 0, prefill_grouping: int = 0) -> Plan:
+             prefill_dynamic: int = 0, prefill_grouping: int = 0, tree_words: int = 0) -> Plan:
     """rpa_plan from host (numpy) metadata; returns a Plan."""
     cu = _np_i32(cu_q_lens_host)
     kv = _np_i32(kv_lens_host)
@@ -239,7 +262,7 @@ def rpa_plan(cu_q_lens_host, kv_lens_host, window_host, num_q_heads: int,
         raise ValueError("window must have num_seqs entries")
     opts = _Options(ctypes.sizeof(_Options), path, q_block, kv_split, num_sms, prefill_pairs,
                     kv_dtype, prefill_split, decode_sms, decode_kernel, prefill_dynamic,
-                    prefill_grouping)
+                    prefill_grouping, tree_words)
     handle = ctypes.c_void_p()
     ws = ctypes.c_size_t()
     st = lib().rpa_plan(ctypes.byref(handle), _np_ptr(cu), _np_ptr(kv), _np_ptr(win),
@@ -252,7 +275,7 @@ def rpa_plan(cu_q_lens_host, kv_lens_host, window_host, num_q_heads: int,
                 head_dim=head_dim, page_size=page_size, has_window=win is not None,
                 dtype=dtype, total_q=int(cu[-1]), num_pages=num_pages,
                 max_pages_per_seq=max_pages_per_seq, q_shape=(int(cu[-1]), num_q_heads, head_dim),
-                table_shape=(num_seqs, max_pages_per_seq))
+                table_shape=(num_seqs, max_pages_per_seq), tree_words=tree_words)
     return Plan(handle.value, ws.value, meta)
 
 
@@ -599,23 +622,202 @@ def rpa_build_tables(new_lens, kv_lens_prev, page_table, free_pages, free_count_
         raise RpaError(rc, "rpa_build_tables")
 
 
+def _return_pages(fn, where, lens, lens_name, kv_lens_prev, page_table, free_pages, free_count_prev,
+                  kv_lens, free_count, page_size, workspace, stream):
+    """rpa_release_tables or rpa_trim_tables."""
+    import torch
+    i32 = torch.int32
+    dev, st = _current(stream)
+    n, width = _tables_state(page_table, lens, kv_lens_prev, kv_lens, free_count_prev, free_count)
+    rc = fn(_addr(lens, lens_name, i32, dev), _addr(kv_lens_prev, "kv_lens_prev", i32, dev),
+            _addr(page_table, "page_table", i32, dev), _addr(free_pages, "free_pages", i32, dev),
+            _addr(free_count_prev, "free_count_prev", i32, dev), _addr(kv_lens, "kv_lens", i32, dev),
+            _addr(free_count, "free_count", i32, dev), n, page_size, width, free_pages.numel(),
+            _workspace(workspace, dev)[0], st)
+    if rc != RPA_OK:
+        raise RpaError(rc, where)
+
+
 def rpa_release_tables(finished, kv_lens_prev, page_table, free_pages, free_count_prev, kv_lens,
                        free_count, page_size: int, workspace, stream=None) -> None:
     """rpa_release_tables on torch CUDA tensors: the pages of every request
     with finished != 0 ([num_seqs] int32) pushed on the stack free_pages, its
     length to 0."""
+    _return_pages(lib().rpa_release_tables, "rpa_release_tables", finished, "finished", kv_lens_prev,
+                  page_table, free_pages, free_count_prev, kv_lens, free_count, page_size, workspace,
+                  stream)
+
+
+def rpa_trim_tables(drop_lens, kv_lens_prev, page_table, free_pages, free_count_prev, kv_lens,
+                    free_count, page_size: int, workspace, stream=None) -> None:
+    """rpa_trim_tables on torch CUDA tensors: drop_lens ([num_seqs] int32)
+    tokens leave the end of every request, the pages behind its new length go
+    back to the stack free_pages."""
+    _return_pages(lib().rpa_trim_tables, "rpa_trim_tables", drop_lens, "drop_lens", kv_lens_prev,
+                  page_table, free_pages, free_count_prev, kv_lens, free_count, page_size, workspace,
+                  stream)
+
+
+def _optional_workspace(workspace, dev):
+    return None if workspace is None else _workspace(workspace, dev)[0]
+
+
+def rpa_build_tree(parents, cu_q_lens, kv_lens, window, tree_mask, positions, workspace=None,
+                   stream=None) -> None:
+    """rpa_build_tree on torch CUDA tensors: masks ([total_q, mask_words] int64)
+    and positions ([total_q] int32) of drafted nodes from their parents
+    ([total_q] int32, -1: behind the context)."""
     import torch
     i32 = torch.int32
     dev, st = _current(stream)
-    n, width = _tables_state(page_table, finished, kv_lens_prev, kv_lens, free_count_prev, free_count)
-    rc = lib().rpa_release_tables(
-        _addr(finished, "finished", i32, dev), _addr(kv_lens_prev, "kv_lens_prev", i32, dev),
-        _addr(page_table, "page_table", i32, dev), _addr(free_pages, "free_pages", i32, dev),
-        _addr(free_count_prev, "free_count_prev", i32, dev), _addr(kv_lens, "kv_lens", i32, dev),
-        _addr(free_count, "free_count", i32, dev), n, page_size, width, free_pages.numel(),
-        _workspace(workspace, dev)[0], st)
+    n, total = kv_lens.numel(), parents.numel()
+    if cu_q_lens.numel() != n + 1 or (window is not None and window.numel() != n):
+        raise ValueError("cu_q_lens must have num_seqs + 1 entries, kv_lens and window num_seqs")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != total or positions.numel() != total:
+        raise ValueError("tree_mask must be [%d, mask_words], positions [%d]" % (total, total))
+    rc = lib().rpa_build_tree(
+        _addr(parents, "parents", i32, dev), _addr(cu_q_lens, "cu_q_lens", i32, dev),
+        _addr(kv_lens, "kv_lens", i32, dev), None if window is None else _addr(window, "window", i32, dev),
+        _addr(tree_mask, "tree_mask", torch.int64, dev), _addr(positions, "positions", i32, dev), n, total,
+        tree_mask.shape[1], _optional_workspace(workspace, dev), st)
     if rc != RPA_OK:
-        raise RpaError(rc, "rpa_release_tables")
+        raise RpaError(rc, "rpa_build_tree")
+
+
+def _strided_rows(t, name, shape, dtype, dev):
+    """Address and token stride of rows [total_q, heads, head_dim] whose heads
+    and dimensions are contiguous."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _dptr(t.contiguous(), name, dtype)
+        raise ValueError("%s is on device %s, the current one is %d" % (name, t.device, dev))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    n, heads, d = shape
+    st = t.stride()
+    if (d > 1 and st[2] != 1) or (heads > 1 and st[1] != d):
+        raise ValueError("%s: a token's heads must be contiguous" % name)
+    return t.data_ptr(), st[0] if n > 1 else heads * d
+
+
+def rpa_append_rope(q, k, v, positions, slot_map, inv_freq, q_out, k_pages, v_pages, k_scale=None,
+                    v_scale=None, interleaved: bool = False, workspace=None, stream=None) -> None:
+    """rpa_append_rope on torch CUDA tensors: q and k rows ([total_q, heads, D],
+    tokens any stride apart) turned by positions ([total_q] int32) times
+    inv_freq ([rotary_dim / 2] float32, None: not at all), q to q_out (both None:
+    only the cache), k and v to the slots of slot_map ([total_q] int64, < 0:
+    left out) of the pages [N, P, Hkv, D]: of the rows' dtype, or uint8 (e4m3)
+    with float32 scales per KV head."""
+    import torch
+    dev, st = _current(stream)
+    dt = k.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise TypeError("k must be bfloat16 or float32, got %s" % dt)
+    code = RPA_DTYPE_BF16 if dt is torch.bfloat16 else RPA_DTYPE_F32
+    if len(k.shape) != 3 or len(k_pages.shape) != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k must be [total_q, Hkv, D], k_pages and v_pages [num_pages, page_size, Hkv, D]")
+    n, p, hkv, d = k_pages.shape
+    t = k.shape[0]
+    if slot_map.numel() != t or (positions is not None and positions.numel() != t):
+        raise ValueError("slot_map and positions must have %d entries" % t)
+    kp, ks = _strided_rows(k, "k", (t, hkv, d), dt, dev)
+    vp, vs = _strided_rows(v, "v", (t, hkv, d), dt, dev)
+    hq = qp = qs = op = 0
+    if q is not None:
+        hq = q.shape[1]
+        qp, qs = _strided_rows(q, "q", (t, hq, d), dt, dev)
+        op = _addr(q_out, "q_out", dt, dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    kv_dt, kv_code, kss, vss = dt, code, None, None
+    if k_pages.dtype is torch.uint8:
+        kv_dt, kv_code = torch.uint8, RPA_DTYPE_FP8_E4M3
+        if k_scale is None or v_scale is None or k_scale.numel() != hkv or v_scale.numel() != hkv:
+            raise ValueError("e4m3 pages need k_scale and v_scale of %d entries" % hkv)
+        kss, vss = _addr(k_scale, "k_scale", torch.float32, dev), _addr(v_scale, "v_scale", torch.float32, dev)
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale and v_scale are for e4m3 pages")
+    rope = Rope(None, 0, 0)
+    if inv_freq is not None:
+        rope = Rope(_addr(inv_freq, "inv_freq", torch.float32, dev), 2 * inv_freq.numel(), int(interleaved))
+    rc = lib().rpa_append_rope(
+        qp, kp, vp, qs, ks, vs, None if positions is None else _addr(positions, "positions", torch.int32, dev),
+        _addr(slot_map, "slot_map", torch.int64, dev), ctypes.byref(rope), op, _addr(k_pages, "k_pages", kv_dt, dev),
+        _addr(v_pages, "v_pages", kv_dt, dev), kss, vss, t, hq, hkv, d, p, n, code, kv_code,
+        _optional_workspace(workspace, dev), st)
+    if rc != RPA_OK:
+        raise RpaError(rc, "rpa_append_rope")
+
+
+def _tree_args(q, k_pages, v_pages, page_table, cu_q_lens, kv_lens, tree_mask, positions, window, sm_scale,
+               out, plan, workspace, stream):
+    """The marshalled arguments of rpa_forward_tree."""
+    import torch
+    m = plan.meta
+    dev, st = _current(stream)
+    i32 = torch.int32
+    dt = torch.bfloat16 if m["dtype"] == RPA_DTYPE_BF16 else torch.float32
+    s, total, words = m["num_seqs"], m["total_q"], m["tree_words"]
+    pool = (m["page_size"], m["num_kv_heads"], m["head_dim"])
+    if (len(k_pages.shape) != 4 or k_pages.shape[1:] != pool or v_pages.shape != k_pages.shape
+            or k_pages.shape[0] < m["num_pages"]):
+        raise ValueError("the pools' shape differs from the plan's")
+    rows = m["q_shape"][1:]
+    if (q.dim() != 3 or out.dim() != 3 or q.shape[1:] != rows or out.shape[1:] != rows
+            or q.shape[0] < total or out.shape[0] < total):
+        raise ValueError("q and out must be [>= %d, %d, %d]" % m["q_shape"])
+    if (page_table.shape != m["table_shape"] or cu_q_lens.numel() != s + 1 or kv_lens.numel() != s
+            or (window is not None and window.numel() != s)):
+        raise ValueError("page_table must be [%d, %d], cu_q_lens, kv_lens and window of %d requests"
+                         % (*m["table_shape"], s))
+    if (tree_mask.dim() != 2 or tree_mask.shape[0] < total or tree_mask.shape[1] != words
+            or (positions is not None and positions.numel() < total)):
+        raise ValueError("tree_mask must be [>= %d, %d], positions [>= %d]" % (total, words, total))
+    ws, n = _workspace(workspace, dev)
+    return (_addr(q, "q", dt, dev), _addr(k_pages, "k_pages", dt, dev), _addr(v_pages, "v_pages", dt, dev),
+            _addr(page_table, "page_table", i32, dev), _addr(cu_q_lens, "cu_q_lens", i32, dev),
+            _addr(kv_lens, "kv_lens", i32, dev), _addr(tree_mask, "tree_mask", torch.int64, dev),
+            None if positions is None else _addr(positions, "positions", i32, dev), s, m["num_q_heads"],
+            m["num_kv_heads"], m["head_dim"], m["page_size"],
+            None if window is None else _addr(window, "window", i32, dev), float(sm_scale),
+            _addr(out, "out", dt, dev), st, plan.handle, ws, n)
+
+
+def rpa_forward_tree(q, k_pages, v_pages, page_table, cu_q_lens, kv_lens, tree_mask, positions, window,
+                     sm_scale: float, out, plan: Plan, workspace, stream=None) -> None:
+    """rpa_forward_tree on torch CUDA tensors: attention of drafted nodes over
+    their context and their tree (tree_mask [total_q, tree_words] int64; a plan
+    with tree_words)."""
+    rc = lib().rpa_forward_tree(*_tree_args(q, k_pages, v_pages, page_table, cu_q_lens, kv_lens, tree_mask,
+                                            positions, window, sm_scale, out, plan, workspace, stream))
+    if rc != RPA_OK:
+        raise RpaError(rc, "rpa_forward_tree")
+
+
+def rpa_commit_tree(k_pages, v_pages, slot_map, cu_q_lens, path, workspace=None, stream=None) -> None:
+    """rpa_commit_tree on torch CUDA tensors: the K and V rows of the accepted
+    nodes path ([num_seqs, max_path] int32, increasing, then -1) moved to the
+    slots of nodes 0, 1, ... of their request (slot_map [total_q] int64)."""
+    import torch
+    dev, st = _current(stream)
+    dt = k_pages.dtype
+    codes = {torch.bfloat16: RPA_DTYPE_BF16, torch.float32: RPA_DTYPE_F32, torch.uint8: RPA_DTYPE_FP8_E4M3}
+    if dt not in codes:
+        raise TypeError("k_pages must be bfloat16, float32 or uint8 (e4m3), got %s" % dt)
+    if len(k_pages.shape) != 4 or v_pages.shape != k_pages.shape or path.dim() != 2:
+        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, D], path [num_seqs, max_path]")
+    n, p, hkv, d = k_pages.shape
+    s, most = path.shape
+    if cu_q_lens.numel() != s + 1:
+        raise ValueError("cu_q_lens must have num_seqs + 1 entries")
+    rc = lib().rpa_commit_tree(
+        _addr(k_pages, "k_pages", dt, dev), _addr(v_pages, "v_pages", dt, dev),
+        _addr(slot_map, "slot_map", torch.int64, dev), _addr(cu_q_lens, "cu_q_lens", torch.int32, dev),
+        _addr(path, "path", torch.int32, dev), s, slot_map.numel(), most, hkv, d, p, n, codes[dt],
+        _optional_workspace(workspace, dev), st)
+    if rc != RPA_OK:
+        raise RpaError(rc, "rpa_commit_tree")
 
 
 def rpa_get_device_error(workspace, stream=None) -> int:
@@ -848,3 +1050,21 @@ class ForwardKv4Call(ForwardCall):
         st = self._fn(*args)
         if st != RPA_OK:
             raise RpaError(st, "rpa_forward_kv4")
+
+
+class ForwardTreeCall(ForwardCall):
+    """rpa_forward_tree (attention of drafted trees) with its arguments
+    marshalled once."""
+
+    def __init__(self, q, k_pages, v_pages, page_table, cu_q_lens, kv_lens, tree_mask, positions, window,
+                 sm_scale: float, out, plan: Plan, workspace, stream=None):
+        self._keep = (q, k_pages, v_pages, page_table, cu_q_lens, kv_lens, tree_mask, positions, window, out,
+                      plan, workspace)
+        self._args = _tree_args(q, k_pages, v_pages, page_table, cu_q_lens, kv_lens, tree_mask, positions,
+                                window, sm_scale, out, plan, workspace, stream)
+        self._fn = lib().rpa_forward_tree
+
+    def __call__(self):
+        st = self._fn(*self._args)
+        if st != RPA_OK:
+            raise RpaError(st, "rpa_forward_tree")

@@ -41,6 +41,7 @@ void log_plan(const rpa::Plan& p) {
   const rpa::Plan& f = p.kv4_prefill ? *p.kv4_prefill : p;  // the prefill's plan
   int64_t cuts = static_cast<int64_t>(p.dcut.size());
   for (const rpa::Plan::Kv4Launch& l : p.kv4_launches) cuts += l.cut ? l.n_ctas - 1 : 0;
+  cuts += static_cast<int64_t>(p.tree_cuts.size());
   std::fprintf(stderr,
                "librpa plan: %d seqs (%d decode, %d prefill), %s path; decode: %d launch(es), "
                "%lld CTAs, longest range %d tokens, %lld cut sequences; prefill: %zu items on "
@@ -48,7 +49,7 @@ void log_plan(const rpa::Plan& p) {
                "bytes\n",
                p.num_seqs, p.num_decode, p.num_prefill,
                p.path == RPA_PATH_TC ? "tensor-core" : "CUDA-core",
-               static_cast<int>(p.dlaunch.size() + p.kv4_launches.size()),
+               static_cast<int>(p.dlaunch.size() + p.kv4_launches.size() + p.tree_launches.size()),
                static_cast<long long>(p.decode_ctas), p.kv_split, static_cast<long long>(cuts),
                f.items.size(), f.prefill_ctas, f.q_block, f.prefill_max_tiles, f.n_split_items,
                p.ws_bytes);
@@ -105,7 +106,8 @@ rpa_status_t rpa_plan(rpa_plan_t** plan, const int32_t* cu_q_lens_host,
       o.prefill_pairs > 2 || o.kv_dtype < 0 || o.kv_dtype > RPA_DTYPE_FP4_E2M1 ||
       o.prefill_split < -1 || o.prefill_split > 65535 || o.decode_sms < -1 ||
       o.decode_kernel < 0 || o.decode_kernel > RPA_DECODE_KERNEL_TC || o.prefill_dynamic < -1 ||
-      o.prefill_dynamic > 0 || o.prefill_grouping < -1 || o.prefill_grouping > 0)
+      o.prefill_dynamic > 0 || o.prefill_grouping < -1 || o.prefill_grouping > 0 ||
+      o.tree_words < 0 || o.tree_words > rpa::kTreeMaxWords)
     return RPA_ERR_INVALID_ARG;
   rpa_status_t st = rpa::validate_metadata(cu_q_lens_host, kv_lens_host, num_seqs,
                                            page_size, max_pages_per_seq);
@@ -128,7 +130,9 @@ rpa_status_t rpa_plan(rpa_plan_t** plan, const int32_t* cu_q_lens_host,
   if (sms == 0) sms = device_sm_count();
   p.num_sms = sms > 0 ? sms : 152;
   try {
-    st = o.kv_dtype == RPA_DTYPE_FP4_E2M1
+    st = o.tree_words > 0
+             ? rpa::build_tree_schedule(p, cu_q_lens_host, kv_lens_host, window_host, o)
+         : o.kv_dtype == RPA_DTYPE_FP4_E2M1
              ? rpa::build_kv4_schedule(p, cu_q_lens_host, kv_lens_host, window_host, o)
              : rpa::build_schedule(p, cu_q_lens_host, kv_lens_host, window_host, o);
   } catch (const std::exception&) {  // out of host memory
@@ -172,7 +176,7 @@ rpa_status_t rpa_plan_get_info(const rpa_plan_t* plan, rpa_plan_info* info) {
   info->prefill_sms = p.overlap ? p.prefill_sms : 0;
   info->prefill_dynamic = f.prefill_dynamic ? 1 : 0;
   info->prefill_groups = f.prefill_groups;
-  info->decode_kernel = (p.num_decode > 0 && !p.simt_decode && !p.kv_fp4)
+  info->decode_kernel = (p.num_decode > 0 && !p.simt_decode && !p.kv_fp4 && p.tree_words == 0)
                             ? (p.decode_tc ? RPA_DECODE_KERNEL_TC : RPA_DECODE_KERNEL_MMA)
                             : 0;
   return RPA_OK;
@@ -296,7 +300,7 @@ rpa_status_t rpa_forward(const void* q, const void* k_pages, const void* v_pages
   const rpa::Plan& p = plan->p;
   if (num_seqs != p.num_seqs || num_q_heads != p.hq || num_kv_heads != p.hkv ||
       head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp8 ||
-      p.kv_fp4)
+      p.kv_fp4 || p.tree_words > 0)
     return RPA_ERR_PLAN_MISMATCH;
   if (workspace == nullptr || !aligned(workspace, 256)) return RPA_ERR_INVALID_ARG;
   if (workspace_bytes < p.ws_bytes) return RPA_ERR_WORKSPACE_TOO_SMALL;
@@ -355,7 +359,7 @@ rpa_status_t rpa_forward_kv(const void* q, const void* k_new, const void* v_new,
   const rpa::Plan& p = plan->p;
   if (num_seqs != p.num_seqs || num_q_heads != p.hq || num_kv_heads != p.hkv ||
       head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp8 ||
-      p.kv_fp4)
+      p.kv_fp4 || p.tree_words > 0)
     return RPA_ERR_PLAN_MISMATCH;
   if (workspace == nullptr || !aligned(workspace, 256)) return RPA_ERR_INVALID_ARG;
   if (workspace_bytes < p.ws_bytes) return RPA_ERR_WORKSPACE_TOO_SMALL;
@@ -453,7 +457,7 @@ rpa_status_t rpa_forward_qkv(const void* q, const void* k, const void* v,
   const rpa::Plan& p = plan->p;
   if (num_seqs != p.num_seqs || num_q_heads != p.hq || num_kv_heads != p.hkv ||
       head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp8 ||
-      p.kv_fp4)
+      p.kv_fp4 || p.tree_words > 0)
     return RPA_ERR_PLAN_MISMATCH;
   if (!rpa::prologue_supported(head_dim)) return RPA_ERR_UNSUPPORTED;
   if (workspace == nullptr || !aligned(workspace, 256)) return RPA_ERR_INVALID_ARG;
@@ -491,7 +495,7 @@ rpa_status_t rpa_forward_decode_noalloc(const void* q, const void* k_pages,
   const rpa::Plan& p = plan->p;
   if (num_seqs != p.num_seqs || num_q_heads != p.hq || num_kv_heads != p.hkv ||
       head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window || p.kv_fp8 ||
-      p.kv_fp4)
+      p.kv_fp4 || p.tree_words > 0)
     return RPA_ERR_PLAN_MISMATCH;
   if (p.num_prefill > 0 || p.simt_decode || p.dtype != RPA_DTYPE_BF16)
     return RPA_ERR_UNSUPPORTED;
@@ -662,11 +666,45 @@ rpa_status_t rpa_build_tables(const int32_t* new_lens, const int32_t* kv_lens_pr
   rpa::TableArgs a{new_lens, kv_lens_prev, page_table, const_cast<int32_t*>(free_pages),
                    free_count_prev, cu_q_lens, kv_lens, slot_map, free_count,
                    static_cast<unsigned char*>(workspace), num_seqs, page_size,
-                   max_pages_per_seq, num_pages, max_tokens, false};
+                   max_pages_per_seq, num_pages, max_tokens, rpa::TableArgs::kBuild};
   rpa::trace_start(stream);
   if (int err = rpa::launch_tables(a, stream)) return cuda_failed(err);
   return RPA_OK;
 }
+
+namespace {
+
+// Pages pushed back to the stack: a release (`lens` the finished flags) or a trim
+// (`lens` the tokens that leave).
+rpa_status_t return_pages(const int32_t* lens, const int32_t* kv_lens_prev,
+                          const int32_t* page_table, int32_t* free_pages,
+                          const int32_t* free_count_prev, int32_t* kv_lens, int32_t* free_count,
+                          int32_t num_seqs, int32_t page_size, int32_t max_pages_per_seq,
+                          int32_t num_pages, void* workspace, rpa_stream_t stream,
+                          rpa::TableArgs::Kind kind) {
+  if (!table_shapes_ok(num_seqs, page_size, max_pages_per_seq, num_pages)) return RPA_ERR_INVALID_ARG;
+  if (free_count_prev == nullptr || free_count == nullptr || free_pages == nullptr ||
+      workspace == nullptr ||
+      (num_seqs > 0 && (lens == nullptr || kv_lens_prev == nullptr || kv_lens == nullptr ||
+                        page_table == nullptr)))
+    return RPA_ERR_INVALID_ARG;
+  if (!aligned(lens, 4) || !aligned(kv_lens_prev, 4) || !aligned(page_table, 4) ||
+      !aligned(free_pages, 4) || !aligned(free_count_prev, 4) || !aligned(kv_lens, 4) ||
+      !aligned(free_count, 4) || !aligned(workspace, 256))
+    return RPA_ERR_INVALID_ARG;
+  if (!state_ok(kv_lens_prev, kv_lens, num_seqs, free_count_prev, free_count))
+    return RPA_ERR_INVALID_ARG;
+  if (std::max(num_seqs, num_pages) > rpa::kTablesMost) return RPA_ERR_UNSUPPORTED;
+  rpa::TableArgs a{lens, kv_lens_prev, const_cast<int32_t*>(page_table), free_pages,
+                   free_count_prev, nullptr, kv_lens, nullptr, free_count,
+                   static_cast<unsigned char*>(workspace), num_seqs, page_size,
+                   max_pages_per_seq, num_pages, 0, kind};
+  rpa::trace_start(stream);
+  if (int err = rpa::launch_tables(a, stream)) return cuda_failed(err);
+  return RPA_OK;
+}
+
+}  // namespace
 
 rpa_status_t rpa_release_tables(const int32_t* finished, const int32_t* kv_lens_prev,
                                 const int32_t* page_table, int32_t* free_pages,
@@ -674,25 +712,163 @@ rpa_status_t rpa_release_tables(const int32_t* finished, const int32_t* kv_lens_
                                 int32_t* free_count, int32_t num_seqs, int32_t page_size,
                                 int32_t max_pages_per_seq, int32_t num_pages, void* workspace,
                                 rpa_stream_t stream) {
-  if (!table_shapes_ok(num_seqs, page_size, max_pages_per_seq, num_pages)) return RPA_ERR_INVALID_ARG;
-  if (free_count_prev == nullptr || free_count == nullptr || free_pages == nullptr ||
-      workspace == nullptr ||
-      (num_seqs > 0 && (finished == nullptr || kv_lens_prev == nullptr || kv_lens == nullptr ||
-                        page_table == nullptr)))
+  return return_pages(finished, kv_lens_prev, page_table, free_pages, free_count_prev, kv_lens,
+                      free_count, num_seqs, page_size, max_pages_per_seq, num_pages, workspace,
+                      stream, rpa::TableArgs::kRelease);
+}
+
+rpa_status_t rpa_trim_tables(const int32_t* drop_lens, const int32_t* kv_lens_prev,
+                             const int32_t* page_table, int32_t* free_pages,
+                             const int32_t* free_count_prev, int32_t* kv_lens,
+                             int32_t* free_count, int32_t num_seqs, int32_t page_size,
+                             int32_t max_pages_per_seq, int32_t num_pages, void* workspace,
+                             rpa_stream_t stream) {
+  return return_pages(drop_lens, kv_lens_prev, page_table, free_pages, free_count_prev, kv_lens,
+                      free_count, num_seqs, page_size, max_pages_per_seq, num_pages, workspace,
+                      stream, rpa::TableArgs::kTrim);
+}
+
+rpa_status_t rpa_build_tree(const int32_t* parents, const int32_t* cu_q_lens,
+                            const int32_t* kv_lens, const int32_t* window, uint64_t* tree_mask,
+                            int32_t* positions, int32_t num_seqs, int32_t total_q,
+                            int32_t mask_words, void* workspace, rpa_stream_t stream) {
+  if (num_seqs < 0 || total_q < 0 || mask_words < 1 || mask_words > rpa::kTreeMaxWords)
     return RPA_ERR_INVALID_ARG;
-  if (!aligned(finished, 4) || !aligned(kv_lens_prev, 4) || !aligned(page_table, 4) ||
-      !aligned(free_pages, 4) || !aligned(free_count_prev, 4) || !aligned(kv_lens, 4) ||
-      !aligned(free_count, 4) || !aligned(workspace, 256))
+  if (num_seqs == 0 || total_q == 0) return RPA_OK;
+  if (parents == nullptr || cu_q_lens == nullptr || kv_lens == nullptr || tree_mask == nullptr ||
+      positions == nullptr)
     return RPA_ERR_INVALID_ARG;
-  if (!state_ok(kv_lens_prev, kv_lens, num_seqs, free_count_prev, free_count))
+  if (!aligned(parents, 4) || !aligned(cu_q_lens, 4) || !aligned(kv_lens, 4) ||
+      !aligned(window, 4) || !aligned(tree_mask, 8) || !aligned(positions, 4) ||
+      (workspace != nullptr && !aligned(workspace, 256)))
     return RPA_ERR_INVALID_ARG;
-  if (std::max(num_seqs, num_pages) > rpa::kTablesMost) return RPA_ERR_UNSUPPORTED;
-  rpa::TableArgs a{finished, kv_lens_prev, const_cast<int32_t*>(page_table), free_pages,
-                   free_count_prev, nullptr, kv_lens, nullptr, free_count,
-                   static_cast<unsigned char*>(workspace), num_seqs, page_size,
-                   max_pages_per_seq, num_pages, 0, true};
+  rpa::BuildTreeArgs a{parents, cu_q_lens, kv_lens, window, tree_mask, positions,
+                       static_cast<unsigned char*>(workspace), num_seqs, total_q, mask_words};
   rpa::trace_start(stream);
-  if (int err = rpa::launch_tables(a, stream)) return cuda_failed(err);
+  if (int err = rpa::launch_build_tree(a, stream)) return cuda_failed(err);
+  return RPA_OK;
+}
+
+rpa_status_t rpa_append_rope(const void* q, const void* k, const void* v, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                             const int64_t* slot_map, const rpa_rope* rope, void* q_out,
+                             void* k_pages, void* v_pages, const float* k_scale,
+                             const float* v_scale, int32_t total_q, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                             int32_t num_pages, int32_t dtype, int32_t kv_dtype, void* workspace,
+                             rpa_stream_t stream) {
+  if (rope == nullptr || total_q < 0 || num_q_heads < 0 || num_kv_heads < 1 || head_dim < 1 ||
+      page_size < 1 || num_pages < 1 || rope->rotary_dim < 0 || rope->rotary_dim > head_dim)
+    return RPA_ERR_INVALID_ARG;
+  if (dtype != RPA_DTYPE_BF16 && dtype != RPA_DTYPE_F32) return RPA_ERR_INVALID_ARG;
+  const bool fp8 = kv_dtype == RPA_DTYPE_FP8_E4M3;
+  if (!fp8 && kv_dtype != dtype) return RPA_ERR_UNSUPPORTED;
+  if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || !is_pow2(page_size) ||
+      rope->rotary_dim % 16 != 0)
+    return RPA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_q_heads) + 2 * static_cast<int64_t>(num_kv_heads) > (1 << 20))
+    return RPA_ERR_UNSUPPORTED;
+  if (total_q == 0) return RPA_OK;
+  const bool has_q = num_q_heads > 0;
+  if (k == nullptr || v == nullptr || slot_map == nullptr || k_pages == nullptr ||
+      v_pages == nullptr || (has_q && (q == nullptr || q_out == nullptr)) ||
+      (rope->rotary_dim > 0 && (rope->inv_freq == nullptr || positions == nullptr)) ||
+      (k_scale != nullptr) != fp8 || (v_scale != nullptr) != fp8)
+    return RPA_ERR_INVALID_ARG;
+  const int64_t esz = dtype == RPA_DTYPE_F32 ? 4 : 2;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * head_dim;
+  const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if ((has_q && q_stride < q_row) || k_stride < kv_row || v_stride < kv_row ||
+      (has_q && q_stride * esz % 16 != 0) || k_stride * esz % 16 != 0 || v_stride * esz % 16 != 0)
+    return RPA_ERR_INVALID_ARG;
+  if ((has_q && (!aligned(q, 16) || !aligned(q_out, 16))) || !aligned(k, 16) || !aligned(v, 16) ||
+      !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(positions, 4) ||
+      !aligned(slot_map, 8) || !aligned(rope->inv_freq, 4) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4) || (workspace != nullptr && !aligned(workspace, 256)))
+    return RPA_ERR_INVALID_ARG;
+  // q rotated in place, or apart from everything that is read.
+  const size_t out_bytes = static_cast<size_t>(total_q * q_row * esz);
+  auto span = [&](int64_t stride, int64_t row) {
+    return static_cast<size_t>(((total_q - 1) * stride + row) * esz);
+  };
+  if (has_q && ((!(q_out == q && q_stride == q_row) &&
+                 overlap(q_out, out_bytes, q, span(q_stride, q_row))) ||
+                overlap(q_out, out_bytes, k, span(k_stride, kv_row)) ||
+                overlap(q_out, out_bytes, v, span(v_stride, kv_row))))
+    return RPA_ERR_INVALID_ARG;
+  rpa::AppendArgs a{q, k, v, q_stride, k_stride, v_stride, positions, slot_map, rope->inv_freq,
+                    rope->rotary_dim, rope->interleaved != 0, q_out, k_pages, v_pages, k_scale,
+                    v_scale, static_cast<unsigned char*>(workspace), total_q, num_q_heads,
+                    num_kv_heads, head_dim, static_cast<int64_t>(num_pages) * page_size,
+                    dtype == RPA_DTYPE_F32};
+  rpa::trace_start(stream);
+  if (int err = rpa::launch_append_rope(a, stream)) return cuda_failed(err);
+  return RPA_OK;
+}
+
+rpa_status_t rpa_forward_tree(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* page_table, const int32_t* cu_q_lens,
+                              const int32_t* kv_lens, const uint64_t* tree_mask,
+                              const int32_t* positions, int32_t num_seqs, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                              const int32_t* window, float sm_scale, void* out,
+                              rpa_stream_t stream, const rpa_plan_t* plan, void* workspace,
+                              size_t workspace_bytes) {
+  if (plan == nullptr) return RPA_ERR_INVALID_ARG;
+  const rpa::Plan& p = plan->p;
+  if (num_seqs != p.num_seqs || num_q_heads != p.hq || num_kv_heads != p.hkv ||
+      head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window ||
+      p.tree_words == 0)
+    return RPA_ERR_PLAN_MISMATCH;
+  if (workspace == nullptr || !aligned(workspace, 256)) return RPA_ERR_INVALID_ARG;
+  if (workspace_bytes < p.ws_bytes) return RPA_ERR_WORKSPACE_TOO_SMALL;
+  if (p.total_q == 0) return RPA_OK;
+  if (q == nullptr || k_pages == nullptr || v_pages == nullptr || page_table == nullptr ||
+      cu_q_lens == nullptr || kv_lens == nullptr || tree_mask == nullptr || out == nullptr ||
+      (window != nullptr && positions == nullptr))
+    return RPA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_pages, 128) ||
+      !aligned(v_pages, 128) || !aligned(page_table, 4) || !aligned(cu_q_lens, 4) ||
+      !aligned(kv_lens, 4) || !aligned(window, 4) || !aligned(tree_mask, 8) ||
+      !aligned(positions, 4))
+    return RPA_ERR_INVALID_ARG;
+  rpa::Args a{q, k_pages, v_pages, page_table, cu_q_lens, kv_lens, window, sm_scale,
+              out, static_cast<unsigned char*>(workspace)};
+  a.tree_mask = tree_mask;
+  a.positions = positions;
+  rpa::trace_start(stream);
+  const int err = p.path == RPA_PATH_TC ? rpa::launch_tree_attn(p, a, stream)
+                                        : rpa::launch_tree_simt(p, a, stream);
+  return err ? cuda_failed(err) : RPA_OK;
+}
+
+rpa_status_t rpa_commit_tree(void* k_pages, void* v_pages, const int64_t* slot_map,
+                             const int32_t* cu_q_lens, const int32_t* path, int32_t num_seqs,
+                             int32_t total_q, int32_t max_path, int32_t num_kv_heads,
+                             int32_t head_dim, int32_t page_size, int32_t num_pages,
+                             int32_t dtype, void* workspace, rpa_stream_t stream) {
+  if (num_seqs < 0 || total_q < 0 || max_path < 0 || num_kv_heads < 1 || head_dim < 1 ||
+      !is_pow2(page_size) || num_pages < 1)
+    return RPA_ERR_INVALID_ARG;
+  if (dtype != RPA_DTYPE_BF16 && dtype != RPA_DTYPE_F32 && dtype != RPA_DTYPE_FP8_E4M3)
+    return RPA_ERR_INVALID_ARG;
+  const int64_t head_bytes =
+      static_cast<int64_t>(head_dim) * (dtype == RPA_DTYPE_F32 ? 4 : dtype == RPA_DTYPE_BF16 ? 2 : 1);
+  if (head_bytes % 16 != 0 || max_path > 1024 || num_kv_heads * head_bytes > (1 << 24))
+    return RPA_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || total_q == 0 || max_path == 0) return RPA_OK;
+  if (k_pages == nullptr || v_pages == nullptr || slot_map == nullptr || cu_q_lens == nullptr ||
+      path == nullptr)
+    return RPA_ERR_INVALID_ARG;
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(slot_map, 8) ||
+      !aligned(cu_q_lens, 4) || !aligned(path, 4) ||
+      (workspace != nullptr && !aligned(workspace, 256)))
+    return RPA_ERR_INVALID_ARG;
+  rpa::CommitTreeArgs a{k_pages, v_pages, slot_map, cu_q_lens, path,
+                        static_cast<unsigned char*>(workspace), num_seqs, total_q, max_path,
+                        static_cast<int64_t>(num_pages) * page_size, num_kv_heads * head_bytes};
+  rpa::trace_start(stream);
+  if (int err = rpa::launch_commit_tree(a, stream)) return cuda_failed(err);
   return RPA_OK;
 }
 

@@ -111,6 +111,40 @@ constexpr int kKv4RowsTile = 8;  // the tiles of kv4_rows.cu, in rows of 8
 // Sequences whose 4-bit pages one expansion launch lists.
 constexpr int kKv4ExpandSeqs = 1024;
 
+// Attention of drafted trees (tree_attn.cu, tree_simt.cu).  A request: its row of
+// the page table, first node, nodes, keys (nodes included) and window.
+struct TreeSeq {
+  int32_t seq, q0, nodes, len, window;
+};
+// Row tiles of the tensor-core kernel: 128 rows are 128 / G nodes of G heads; a
+// segment is (request, KV head, row_tiles(D) such tiles), its keys in tiles of 128.
+// The segments' key tiles lie end to end and every CTA takes a contiguous range:
+// `tiles` of them from tile j of (request i, head, segment st) on.
+struct TreeStart {
+  int32_t i, head, st, j, tiles;
+};
+// A segment cut across CTAs cta .. cta + nparts - 1: the first holds its partial in
+// slot 2 cta + first, each later CTA c in slot 2 c.
+struct TreeCut {
+  int32_t i, head, st, cta, first, nparts;
+};
+struct TreeLaunch {
+  int32_t seq_begin, seq_end, start_begin, n_ctas, cut_begin, n_cut;
+};
+constexpr int kTreeMaxWords = 16;
+constexpr int kTreeRows = 128;
+constexpr int kTreeKeys = 128;
+constexpr int kTreeSeqsSmall = 128;   // requests a launch carries in its parameters
+constexpr int kTreeSeqsLarge = 1024;
+constexpr int kTreeMaxCtas = 256;
+RPA_HD constexpr int32_t tree_row_tiles(int32_t head_dim) { return head_dim == 256 ? 1 : 2; }
+// First of the 128-key tiles that a request's nodes can see (a node's position is
+// at least that of the first behind the context).
+RPA_HD constexpr int32_t tree_first_tile(const TreeSeq& s) {
+  const int32_t ctx = s.len - s.nodes;
+  return s.window > 0 && ctx - s.window + 1 > 0 ? (ctx - s.window + 1) / kTreeKeys : 0;
+}
+
 struct Plan {
   // Problem description (checked against every rpa_forward call).
   int32_t num_seqs = 0, hq = 0, hkv = 0, d = 0, p = 0, mpps = 0, num_pages = 0;
@@ -201,6 +235,14 @@ struct Plan {
 
   std::unique_ptr<Plan> kv4_prefill;  // the prefill part's plan, over the widened pages
 
+  // Trees of drafted tokens (plan_tree.cpp).
+  int32_t tree_words = 0;             // 64-bit words of a mask row (0: not such a plan)
+  std::vector<TreeSeq> tree_seqs;     // requests with nodes
+  std::vector<TreeLaunch> tree_launches;
+  std::vector<TreeStart> tree_starts;
+  std::vector<TreeCut> tree_cuts;
+  int32_t tree_slots = 0;             // partial slots of the largest launch
+
   // Prefill (q_len > 1).
   int32_t num_prefill = 0;
   int32_t q_block = 0;
@@ -232,6 +274,10 @@ rpa_status_t build_schedule(Plan& plan, const int32_t* cu_q_lens, const int32_t*
 rpa_status_t build_kv4_schedule(Plan& plan, const int32_t* cu_q_lens, const int32_t* kv_lens,
                                 const int32_t* window, const rpa_plan_options& opts);
 
+// The scheduler for drafted trees (plan_tree.cpp), likewise.
+rpa_status_t build_tree_schedule(Plan& plan, const int32_t* cu_q_lens, const int32_t* kv_lens,
+                                 const int32_t* window, const rpa_plan_options& opts);
+
 // Host-side checks of the metadata (plan.cpp).
 rpa_status_t validate_metadata(const int32_t* cu_q_lens, const int32_t* kv_lens,
                                int32_t num_seqs, int32_t page_size,
@@ -256,6 +302,8 @@ struct Args {
   // The prefill over widened 4-bit pages: the 4-bit pages' table and number.
   const int32_t* kv4_page_table = nullptr;
   int32_t kv4_num_pages = 0;
+  const uint64_t* tree_mask = nullptr;  // drafted trees
+  const int32_t* positions = nullptr;
 };
 
 // Kernel launchers; each returns cudaError_t as int (0 = success).
@@ -341,9 +389,63 @@ struct TableArgs {
   int32_t* free_count;
   unsigned char* workspace;
   int32_t num_seqs, page_size, mpps, num_pages, max_tokens;
-  bool release;
+  enum Kind { kBuild, kRelease, kTrim } kind;
 };
 int launch_tables(const TableArgs& a, void* stream);
+
+// Attention of drafted trees: on tensor cores (tree_attn.cu) or CUDA cores
+// (tree_simt.cu).
+bool tree_tc_supported(int32_t head_dim, int32_t page_size, int32_t group);
+int launch_tree_attn(const Plan& plan, const Args& a, void* stream);
+int launch_tree_simt(const Plan& plan, const Args& a, void* stream);
+
+// Masks and positions of drafted trees, and the rows of an accepted path moved
+// (tree.cu).
+struct BuildTreeArgs {
+  const int32_t* parents;
+  const int32_t* cu_q_lens;
+  const int32_t* kv_lens;
+  const int32_t* window;
+  uint64_t* mask;
+  int32_t* positions;
+  unsigned char* workspace;  // error word, or null
+  int32_t num_seqs, total_q, words;
+};
+int launch_build_tree(const BuildTreeArgs& a, void* stream);
+struct CommitTreeArgs {
+  void* k_pages;
+  void* v_pages;
+  const int64_t* slot_map;
+  const int32_t* cu_q_lens;
+  const int32_t* path;
+  unsigned char* workspace;  // error word, or null
+  int32_t num_seqs, total_q, max_path;
+  int64_t pool_slots, row_bytes;
+};
+int launch_commit_tree(const CommitTreeArgs& a, void* stream);
+
+// Rotation and cache write at given positions and slots (rope_append.cu).
+struct AppendArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  const int32_t* positions;
+  const int64_t* slot_map;
+  const float* inv_freq;
+  int32_t rotary_dim;
+  bool interleaved;
+  void* q_out;
+  void* k_pages;
+  void* v_pages;
+  const float* k_scale;  // e4m3 pages, else null
+  const float* v_scale;
+  unsigned char* workspace;  // error word, or null
+  int32_t tokens, hq, hkv, head_dim;
+  int64_t pool_slots;
+  bool f32;
+};
+int launch_append_rope(const AppendArgs& a, void* stream);
 
 // Raise a kernel's dynamic shared-memory limit to `bytes` on the current
 // device, once per (kernel, device); thread-safe.  Returns a cudaError_t.

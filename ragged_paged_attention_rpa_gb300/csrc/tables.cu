@@ -7,8 +7,9 @@
 // pages for it; the k-th page of the step, counted over the requests in order,
 // is free_pages[count - 1 - k].  A token's slot is its page times P plus its
 // position in the page.  Releasing requests pushes their pages back in
-// (request, slot) order.  Both are all or nothing: a step that the stack or
-// the slot map cannot hold changes nothing and sets the error word.
+// (request, slot) order, and cutting requests short pushes the pages behind their
+// new lengths.  All or nothing: a step that the stack or the slot map cannot hold
+// changes nothing and sets the error word.
 //
 // Integer work on a few kilobytes: what bounds it is latency, so every CTA
 // scans all the requests' lengths for itself (L2 reads, two block scans) and
@@ -33,7 +34,7 @@ constexpr int kChunk = kThreads * kPer;      // requests scanned at once
 constexpr int kWarps = kThreads / 32;
 
 struct TableParams {
-  const int32_t* lens;       // build: new_lens; release: the finished flags
+  const int32_t* lens;       // build: new_lens; release: the finished flags; trim: drop_lens
   const int32_t* kv_prev;
   int32_t* table;
   int32_t* free_pages;
@@ -46,6 +47,8 @@ struct TableParams {
   int32_t num_seqs, mpps, num_pages, page_size, page_shift, max_tokens;
 };
 
+using Kind = TableArgs::Kind;
+
 struct Totals {
   int64_t tokens, pages;
   int32_t bad;
@@ -55,7 +58,7 @@ struct Totals {
 struct Chunk {
   int32_t cu[kChunk + 1];    // tokens before each request (build)
   int32_t base[kChunk + 1];  // pages before each request
-  int32_t prev[kChunk];
+  int32_t prev[kChunk];      // tokens held (trim: tokens left)
   uint32_t warp_sum[2][kWarps];
   long long tot[2];
   int32_t bad;
@@ -66,16 +69,22 @@ __device__ __forceinline__ int32_t pages_of(const TableParams& p, int32_t n) {
 }
 
 // Tokens and pages of request s, and whether its lengths are unusable.
-template <bool kRelease>
+template <Kind kKind>
 __device__ __forceinline__ void request(const TableParams& p, int32_t s, int32_t& prev,
                                         int32_t& tok, int32_t& pg, bool& bad) {
   prev = p.kv_prev[s];
   const int32_t n = p.lens[s];
   tok = pg = 0;
-  if constexpr (kRelease) {
+  if constexpr (kKind == Kind::kRelease) {
     if (n == 0) return;
     bad = prev < 0 || pages_of(p, prev) > p.mpps;
     if (!bad) pg = pages_of(p, prev);
+  } else if constexpr (kKind == Kind::kTrim) {
+    bad = n < 0 || n > prev || pages_of(p, prev) > p.mpps;
+    if (!bad) {
+      pg = pages_of(p, prev) - pages_of(p, prev - n);
+      prev -= n;
+    }
   } else {
     const int64_t sum = static_cast<int64_t>(prev) + n;
     bad = prev < 0 || n < 0 || sum > 0x7fffffff - p.page_size ||
@@ -90,7 +99,7 @@ __device__ __forceinline__ void request(const TableParams& p, int32_t s, int32_t
 // Exclusive prefix sums of the chunk of requests from c0 on into shared
 // memory, continuing from (tok0, pg0); the chunk's sums are added to the
 // totals.  Every thread of the CTA takes part; ends with a barrier.
-template <bool kRelease>
+template <Kind kKind>
 __device__ __forceinline__ void scan_chunk(const TableParams& p, Chunk& ch, int32_t c0, uint32_t tok0,
                            uint32_t pg0) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -101,7 +110,7 @@ __device__ __forceinline__ void scan_chunk(const TableParams& p, Chunk& ch, int3
     const int32_t l = tid * kPer + i, s = c0 + l;
     int32_t prev = 0, tok = 0, pg = 0;
     bool bad = false;
-    if (s < p.num_seqs) request<kRelease>(p, s, prev, tok, pg, bad);
+    if (s < p.num_seqs) request<kKind>(p, s, prev, tok, pg, bad);
     ch.prev[l] = prev;
     t[i] = st;
     g[i] = sg;
@@ -143,7 +152,7 @@ __device__ __forceinline__ void scan_chunk(const TableParams& p, Chunk& ch, int3
 }
 
 // The step's totals, in 64 bits (every thread of the CTA returns them).
-template <bool kRelease>
+template <Kind kKind>
 __device__ __forceinline__ Totals totals(const TableParams& p, Chunk& ch) {
   if (threadIdx.x == 0) {
     ch.tot[0] = ch.tot[1] = 0;
@@ -155,7 +164,7 @@ __device__ __forceinline__ Totals totals(const TableParams& p, Chunk& ch) {
   for (int32_t s = threadIdx.x; s < p.num_seqs; s += kThreads) {
     int32_t prev, tok, pg;
     bool bad = false;
-    request<kRelease>(p, s, prev, tok, pg, bad);
+    request<kKind>(p, s, prev, tok, pg, bad);
     tok_sum += tok;
     pg_sum += pg;
     any_bad |= bad;
@@ -214,13 +223,18 @@ __device__ __forceinline__ bool last_cta(unsigned char* ws) {
 
 // New lengths and stack height.  In place (kv == kv_prev, count == count_prev)
 // the last CTA writes them, else the CTAs between them as they go.
-template <bool kRelease>
+template <Kind kKind>
 __device__ __forceinline__ void write_state(const TableParams& p, bool ok, int32_t count_new) {
   const bool kv_in_place = p.kv == p.kv_prev, count_in_place = p.count == p.count_prev;
   auto lengths = [&](int32_t first, int32_t step) {
     for (int32_t s = first; s < p.num_seqs; s += step) {
       const int32_t prev = p.kv_prev[s], n = p.lens[s];
-      p.kv[s] = !ok ? prev : (kRelease ? (n != 0 ? 0 : prev) : prev + n);
+      if (!ok)
+        p.kv[s] = prev;
+      else if (kKind == Kind::kRelease)
+        p.kv[s] = n != 0 ? 0 : prev;
+      else
+        p.kv[s] = kKind == Kind::kTrim ? prev - n : prev + n;
     }
   };
   if (!kv_in_place) lengths(blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
@@ -236,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const TableParam
   __shared__ Chunk ch;
   const int32_t gtid = blockIdx.x * kThreads + threadIdx.x, gstep = gridDim.x * kThreads;
   const int32_t count = *p.count_prev;
-  const Totals tot = totals<false>(p, ch);
+  const Totals tot = totals<Kind::kBuild>(p, ch);
   const bool ok = !tot.bad && tot.tokens <= p.max_tokens && count >= 0 && count <= p.num_pages &&
                   tot.pages <= count;
   if (!ok && gtid == 0)
@@ -246,12 +260,12 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const TableParam
   for (int32_t t = total + gtid; t < p.max_tokens; t += gstep) p.slots[t] = -1;
   if (!ok) {
     for (int32_t s = gtid; s <= p.num_seqs; s += gstep) p.cu[s] = 0;
-    write_state<false>(p, false, count);
+    write_state<Kind::kBuild>(p, false, count);
     return;
   }
   uint32_t tok0 = 0, pg0 = 0;
   for (int32_t c0 = 0; c0 < p.num_seqs; c0 += kChunk) {
-    scan_chunk<false>(p, ch, c0, tok0, pg0);
+    scan_chunk<Kind::kBuild>(p, ch, c0, tok0, pg0);
     const int32_t tok1 = ch.cu[kChunk], pg1 = ch.base[kChunk];
     const int32_t n = min(kChunk, p.num_seqs - c0);
     for (int32_t l = gtid; l < n; l += gstep) p.cu[c0 + l] = ch.cu[l];
@@ -284,27 +298,31 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const TableParam
     __syncthreads();  // the next chunk overwrites this one
   }
   if (gtid == 0) p.cu[p.num_seqs] = total;
-  write_state<false>(p, true, count - static_cast<int32_t>(tot.pages));
+  write_state<Kind::kBuild>(p, true, count - static_cast<int32_t>(tot.pages));
 }
 
+// Pages pushed back: those of finished requests (kRelease), or those behind the new
+// lengths (kTrim).
+template <Kind kKind>
 __global__ void __launch_bounds__(kThreads) release_tables_kernel(const TableParams p) {
   __shared__ Chunk ch;
   const int32_t gtid = blockIdx.x * kThreads + threadIdx.x, gstep = gridDim.x * kThreads;
   const int32_t count = *p.count_prev;
-  const Totals tot = totals<true>(p, ch);
+  const Totals tot = totals<kKind>(p, ch);
   const bool ok = !tot.bad && count >= 0 && count + tot.pages <= p.num_pages;
   if (!ok) {
     if (gtid == 0) report_error(p.ws, tot.bad ? RPA_DEVERR_LENGTHS : RPA_DEVERR_PAGES, 0);
-    write_state<true>(p, false, count);
+    write_state<kKind>(p, false, count);
     return;
   }
   uint32_t pg0 = 0;
   for (int32_t c0 = 0; c0 < p.num_seqs; c0 += kChunk) {
-    scan_chunk<true>(p, ch, c0, 0, pg0);
+    scan_chunk<kKind>(p, ch, c0, 0, pg0);
     const int32_t pg1 = ch.base[kChunk];
     for (int32_t k = static_cast<int32_t>(pg0) + gtid; k < pg1; k += gstep) {
       const int l = owner(ch.base, k);
-      int32_t page = __ldg(p.table + static_cast<int64_t>(c0 + l) * p.mpps + (k - ch.base[l]));
+      const int32_t first = kKind == Kind::kTrim ? pages_of(p, ch.prev[l]) : 0;
+      int32_t page = __ldg(p.table + static_cast<int64_t>(c0 + l) * p.mpps + first + (k - ch.base[l]));
       if (page < 0 || page >= p.num_pages) {
         report_error(p.ws, RPA_DEVERR_PAGE_ID, c0 + l);
         page = -1;
@@ -314,7 +332,7 @@ __global__ void __launch_bounds__(kThreads) release_tables_kernel(const TablePar
     pg0 = static_cast<uint32_t>(pg1);
     __syncthreads();
   }
-  write_state<true>(p, true, count + static_cast<int32_t>(tot.pages));
+  write_state<kKind>(p, true, count + static_cast<int32_t>(tot.pages));
 }
 
 }  // namespace
@@ -339,20 +357,27 @@ int launch_tables(const TableArgs& a, void* stream) {
   while ((1 << shift) < a.page_size) ++shift;
   p.page_shift = shift;
   p.max_tokens = a.max_tokens;
-  // One CTA per 512 tokens (build) or pages (release: at most the pool's) of
+  // One CTA per 512 tokens (build) or pages (release, trim: at most the pool's) of
   // the step, one wave at most.
-  const int64_t items = a.release ? std::min<int64_t>(static_cast<int64_t>(a.num_seqs) * a.mpps, a.num_pages)
-                                  : a.max_tokens;
+  const int64_t items = a.kind == Kind::kBuild
+                            ? a.max_tokens
+                            : std::min<int64_t>(static_cast<int64_t>(a.num_seqs) * a.mpps, a.num_pages);
   const int64_t most = std::max<int64_t>(items, a.num_seqs);
   const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((most + kThreads - 1) / kThreads, 152)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a.release)
-    release_tables_kernel<<<grid, kThreads, 0, s>>>(p);
-  else
+  int mark = RPA_KERNEL_BUILD_TABLES;
+  if (a.kind == Kind::kBuild) {
     build_tables_kernel<<<grid, kThreads, 0, s>>>(p);
+  } else if (a.kind == Kind::kRelease) {
+    release_tables_kernel<Kind::kRelease><<<grid, kThreads, 0, s>>>(p);
+    mark = RPA_KERNEL_RELEASE_TABLES;
+  } else {
+    release_tables_kernel<Kind::kTrim><<<grid, kThreads, 0, s>>>(p);
+    mark = RPA_KERNEL_TRIM_TABLES;
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return static_cast<int>(e);
-  trace_mark(a.release ? RPA_KERNEL_RELEASE_TABLES : RPA_KERNEL_BUILD_TABLES, stream);
+  trace_mark(mark, stream);
   return 0;
 }
 
