@@ -100,7 +100,9 @@ rpa_status_t build_tree_schedule(Plan& plan, const int32_t* cu, const int32_t* k
       opts.prefill_pairs != 0 || opts.prefill_split != 0 || opts.decode_sms != 0 || opts.decode_kernel != 0 ||
       opts.prefill_dynamic != 0 || opts.prefill_grouping != 0)
     return RPA_ERR_UNSUPPORTED;
-  const bool tc = plan.dtype == RPA_DTYPE_BF16 && tree_tc_supported(plan.d, plan.p, group);
+  // (A row of the pool is a 31-bit coordinate of its tensor map.)
+  const bool tc = plan.dtype == RPA_DTYPE_BF16 && tree_tc_supported(plan.d, plan.p, group) &&
+                  static_cast<int64_t>(plan.num_pages) * plan.p <= 0x7fffffff;
   if (opts.path == RPA_PATH_TC && !tc) return RPA_ERR_UNSUPPORTED;
   if (plan.hq > 65535) return RPA_ERR_UNSUPPORTED;  // (the CUDA-core grid's second side)
   plan.tree_words = opts.tree_words;

@@ -1,10 +1,930 @@
-// Attention of drafted trees on tensor cores: not there yet, every plan takes the
-// CUDA-core kernel (tree_simt.cu).
-#include "rpa_internal.h"
+// Attention of drafted trees on tensor cores (tcgen05 + TMA), split over the keys.
+//
+// A node sees its request's whole context (within its window) and, of the tree, the
+// nodes of its mask.  The 128 rows of an MMA are 128 / G nodes by the G query heads
+// of one KV head; a segment is (request, KV head, one such row tile, or two where
+// head_dim leaves tensor memory for two outputs), its keys come in tiles of 128.
+// plan_tree.cpp lays the segments' tiles end to end and cuts the line into equal
+// ranges, one per CTA, one CTA per SM: few rows over long contexts are bound by HBM,
+// and only all SMs together reach it.  A CTA's range is a list of parts of segments;
+// a part that is not its whole segment leaves fp32 O / l and log2-sum-exps, which
+// tree_combine_kernel joins.
+//
+// Within a part the score tile S = Q K^T (SMEM x SMEM -> TMEM) runs one ahead of
+// O += P V (P from TMEM, written over half of its S; V MN-major from SMEM).  With two
+// streams (head_dim 64 and 128) two softmax warpgroups take the score tiles by turns, each with
+// an S buffer and an O of its own:
+//   two row tiles: a stream per row tile, both fed from the same K and V stages;
+//   one row tile: the streams take the key tiles by turns and merge at the part's
+//   end (by the maxima and sums that they swap through shared memory).
+// At head_dim 256 one O fills half of tensor memory: one stream, two S buffers.
+//
+// Warps: 0 copies Q and K, 1 copies V (TMA boxes through the page table, 16 KB
+// stages), 2 issues the MMAs, 3 makes V safe (below), 4 on are the softmax
+// warpgroups, a thread per row; each writes its rows at the part's end while the
+// copies run on into the ring.
+//
+// Masks are looked up where a tile holds nodes or a window's edge; 128 bits a row.
+// A product gives 0 * NaN to the rows that do not see a key, so in those tiles warp
+// 3 goes over V before the MMA reads it: rows of keys that no node sees become zero,
+// and of the others each NaN or infinity, which the rows that see it then get back
+// from memory after they are written (add_unseen).
+//
+// Rounding: P to bf16 (2^-8 of itself; the sums take it unrounded), O / l to bf16.
+// Every wait is bounded; see prefill_tc.cu for what follows when one gives up.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "sm100_ptx.cuh"
+#include "tree.cuh"
 
 namespace rpa {
+namespace {
 
-bool tree_tc_supported(int32_t, int32_t, int32_t) { return false; }
-int launch_tree_attn(const Plan& plan, const Args& a, void* stream) { return launch_tree_simt(plan, a, stream); }
+using namespace sm100;
+
+constexpr int kStage = 16384;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kDrainNs = 200000000ull;
+
+template <int N>
+struct TreeWork {
+  TreeSeqs<N> seqs;
+  TreeStart start[kTreeMaxCtas];
+};
+
+struct TreeParams {
+  const int32_t* page_table;
+  const int32_t* cu_q_lens;
+  const int32_t* kv_lens;
+  const uint64_t* mask;
+  const int32_t* positions;
+  const __nv_bfloat16* v_pages;
+  __nv_bfloat16* out;
+  float* part_o;    // [slot][row][D]
+  float* part_lse;  // [slot][row]
+  unsigned char* ws;
+  int32_t hq, hkv, group, per_tile;  // nodes a row tile
+  int32_t page_size, page_shift, mpps, num_pages, words;
+  int32_t box_rows_k, box_rows_v, v_4d, out_v8;
+  float scale_log2;  // |sm_scale| log2(e)
+  uint32_t sign;     // flips the scores of a negative scale
+};
+
+template <int D>
+struct Layout {
+  static constexpr int kStreams = tree_row_tiles(D);
+  static constexpr int kThreads = 128 + 128 * kStreams;
+  static constexpr int kChunks = D / 64;         // 128-byte pieces of a row; stages of a tile, of K and of V
+  static constexpr int kVKeys = 8192 / D;        // keys of a V stage
+  static constexpr int kDepth = D == 64 ? 6 : 5; // stages of each ring
+  static constexpr int kQTile = kTreeRows * D * 2;
+  static constexpr int kKOff = kStreams * kQTile;
+  static constexpr int kVOff = kKOff + kDepth * kStage;
+  static constexpr int kBarOff = kVOff + kDepth * kStage;
+  static constexpr int kXchOff = kBarOff + 512;  // [stream][row] (maximum, sum)
+  static constexpr int kUsed = kXchOff + (kStreams == 2 ? 2 * kTreeRows * 8 : 0);
+  static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;  // one CTA per SM
+  static_assert(kUsed <= 227 * 1024, "more shared memory than one CTA may have");
+  // Tensor memory: the streams' O, then two S buffers of 128 columns.
+  static constexpr int kSCol = kStreams * D;
+  static constexpr int kCols = 512;
+  static_assert(kSCol + 256 <= kCols, "tensor memory");
+};
+
+struct Barriers {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t o_free;          // every row of the part's O has been read
+  uint64_t xch;             // the streams' maxima and sums are posted
+  uint64_t v_ask, v_safe;   // a masked tile's V has landed / may be read
+  uint64_t fin;
+  uint32_t tmem_base;
+  int abort;
+  int32_t poison[2];        // 1 + the part of this parity in which warp 3 took something out
+};
+static_assert(sizeof(Barriers) <= 512, "barrier block");
+
+// A part of a segment.
+struct Part {
+  TreeSeq s;
+  int32_t head, node0, n0, n1;  // first node, nodes of the first and the second row tile
+  int32_t key0, n;              // first key, key tiles
+  int32_t lo;                   // first key that any node can see
+  int32_t masked_below, masked_from;  // tiles that begin below or end behind these are masked
+  bool whole;
+  __device__ __forceinline__ bool masked(int32_t key) const { return key < masked_below || key + kTreeKeys > masked_from; }
+};
+
+// A CTA's parts, in order.
+template <int D, int N>
+struct Walk {
+  int32_t i, head, st, j, left;
+  __device__ __forceinline__ explicit Walk(const TreeWork<N>& w) {
+    const TreeStart& s = w.start[blockIdx.x];
+    i = s.i;
+    head = s.head;
+    st = s.st;
+    j = s.j;
+    left = s.tiles;
+  }
+  __device__ __forceinline__ bool next(const TreeWork<N>& w, const TreeParams& p, Part& a) {
+    if (left <= 0) return false;
+    a.s = w.seqs.s[i];
+    const int32_t per = p.per_tile * Layout<D>::kStreams, first = tree_first_tile(a.s);
+    const int32_t nb = (a.s.len - 1) / kTreeKeys + 1 - first;
+    a.head = head;
+    a.node0 = st * per;
+    a.n0 = min(p.per_tile, a.s.nodes - a.node0);
+    a.n1 = Layout<D>::kStreams == 2 ? max(0, min(p.per_tile, a.s.nodes - a.node0 - p.per_tile)) : 0;
+    a.n = min(left, nb - j);
+    a.key0 = (first + j) * kTreeKeys;
+    a.whole = a.n == nb;
+    const int32_t ctx = a.s.len - a.s.nodes, w0 = a.s.window;
+    a.lo = w0 > 0 ? max(0, ctx - w0 + 1) : 0;
+    a.masked_below = w0 > 0 ? min(ctx, a.s.len - w0) : 0;
+    a.masked_from = ctx;
+    left -= a.n;
+    j += a.n;
+    if (j == nb) {
+      j = 0;
+      if (a.node0 + per >= a.s.nodes) {
+        st = 0;
+        if (++head == p.hkv) {
+          head = 0;
+          ++i;
+        }
+      } else {
+        ++st;
+      }
+    }
+    return true;
+  }
+};
+
+// TMA source row of the box of `rows` keys from `key` on (in one page); -rows, which
+// is filled with zeros, where no node sees any of them or the page is not one.
+__device__ __forceinline__ int32_t box_row(const TreeParams& p, const Part& a, int32_t key, int32_t rows) {
+  if (key >= a.s.len || key + rows <= a.lo) return -rows;
+  const int32_t page = __ldg(p.page_table + static_cast<int64_t>(a.s.seq) * p.mpps + (key >> p.page_shift));
+  if (page < 0 || page >= p.num_pages) {
+    report_error(p.ws, RPA_DEVERR_PAGE_ID, a.s.seq);
+    return -rows;
+  }
+  return page * p.page_size + (key & (p.page_size - 1));
+}
+
+// Whether one of two bf16 is NaN or infinite, and the two without such ones.
+__device__ __forceinline__ bool not_finite2(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+  return w;
+}
+
+// A V stage ([chunk][key][128 B]) of keys from `key` on made safe (whole warp);
+// true where a NaN or an infinity of a visible key was taken out.
+template <int D>
+__device__ __noinline__ bool make_safe(uint8_t* stage, int32_t key, int32_t lo, int32_t len, int lane) {
+  constexpr int kVKeys = Layout<D>::kVKeys;
+  bool found = false;
+#pragma unroll 8
+  for (int u = lane; u < kStage / 16; u += 32) {
+    const int32_t k = key + ((u >> 3) & (kVKeys - 1));
+    uint4* at = reinterpret_cast<uint4*>(stage) + u;
+    if (k < lo || k >= len) {
+      *at = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    const uint4 v = *at;
+    if (not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) || not_finite2(v.w)) {
+      *at = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+      found = true;
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  return __any_sync(0xffffffffu, found);
+}
+
+// What make_safe took out of the part's tiles and this row sees, added to what was
+// stored of columns [c0, c1) (T: bf16 outputs or fp32 partials, the row's start).
+template <typename T>
+__device__ __noinline__ void add_unseen(const TreeParams& p, const Part& a, const uint64_t* mask_row, int32_t first,
+                                        int32_t d, int32_t c0, int32_t c1, T* row) {
+  for (int32_t k0 = a.key0; k0 < a.key0 + a.n * kTreeKeys; k0 += kTreeKeys) {
+    if (!a.masked(k0)) continue;
+    for (int32_t k = k0; k < min(k0 + kTreeKeys, a.s.len); k += 32) {
+      for (uint32_t bits = tree_sees32(a.s, mask_row, first, k); bits; bits &= bits - 1) {
+        const int32_t key = k + __ffs(bits) - 1;
+        if (key >= a.s.len) break;
+        const int32_t from = box_row(p, a, key, 1);
+        if (from < 0) continue;
+        const __nv_bfloat16* v = p.v_pages + (static_cast<int64_t>(from) * p.hkv + a.head) * d;
+        for (int32_t c = c0; c < c1; ++c) {
+          const float x = to_float(v[c]);
+          if (!(fabsf(x) < INFINITY)) row[c] = from_float<T>(to_float(row[c]) + x);
+        }
+      }
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ float max_tree(const uint32_t* v) {
+  if constexpr (N == 1) {
+    return __uint_as_float(v[0]);
+  } else if constexpr (N == 2) {
+    return fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+  } else {
+    constexpr int M = (N + 2) / 3;
+    uint32_t t[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const float a = __uint_as_float(v[3 * i]);
+      float m = a;
+      if (3 * i + 2 < N)
+        m = fmax3(a, __uint_as_float(v[3 * i + 1]), __uint_as_float(v[3 * i + 2]));
+      else if (3 * i + 1 < N)
+        m = fmaxf(a, __uint_as_float(v[3 * i + 1]));
+      t[i] = __float_as_uint(m);
+    }
+    return max_tree<M>(t);
+  }
+}
+
+// One 32-byte store, or two 16-byte ones.
+__device__ __forceinline__ void store32(void* dst, bool whole, const uint32_t (&w)[8]) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(Layout<D>::kThreads, 1)
+tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p,
+                 const __grid_constant__ TreeWork<N> work) {
+  using Lay = Layout<D>;
+  constexpr int kDepth = Lay::kDepth, kChunks = Lay::kChunks, kStreams = Lay::kStreams;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_addr(smem) & 1023u) {
+    if (threadIdx.x == 0) report_error(p.ws, RPA_DEVERR_LAUNCH, blockIdx.x);
+    return;
+  }
+  // The combine may be scheduled now; it waits for this grid.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Barriers& B = *reinterpret_cast<Barriers*>(smem + Lay::kBarOff);
+  volatile int* abort = &B.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&B.q_full, 1);
+    mbar_init(&B.q_empty, 1);
+    for (int i = 0; i < kDepth; ++i) {
+      mbar_init(&B.k_full[i], 1);
+      mbar_init(&B.k_empty[i], 1);
+      mbar_init(&B.v_full[i], 1);
+      mbar_init(&B.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B.s_full[i], 1);
+      mbar_init(&B.p_full[i], 128);
+      mbar_init(&B.o_done[i], 1);
+      B.poison[i] = 0;
+    }
+    mbar_init(&B.o_free, 128 * kStreams);
+    mbar_init(&B.xch, 256);
+    mbar_init(&B.v_ask, 1);
+    mbar_init(&B.v_safe, 1);
+    mbar_init(&B.fin, 1);
+    B.abort = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == 2) {
+    tmem_alloc(&B.tmem_base, Lay::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B.tmem_base;
+  Walk<D, N> walk(work);
+  Part a;
+  if (warp <= 1) {
+    // ------------------------------------------------------------ copies
+    const bool is_k = warp == 0;
+    uint64_t* full = is_k ? B.k_full : B.v_full;
+    uint64_t* empty = is_k ? B.k_empty : B.v_empty;
+    uint8_t* ring = smem + (is_k ? Lay::kKOff : Lay::kVOff);
+    const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+    const int rows = is_k ? p.box_rows_k : p.box_rows_v;
+    const int nbox = (is_k ? kTreeKeys : Lay::kVKeys) / rows;  // boxes of a stage
+    const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.per_tile) * 128u * kChunks;
+    uint32_t C = 0, parts = 0, issued_q = 0;
+    bool alive = true;
+    for (; alive && walk.next(work, p, a); ++parts) {
+      if (is_k && lane == 0) {
+        // (The device's lengths, once a request.)
+        if (a.head == 0 && a.node0 == 0 && a.key0 + a.n * kTreeKeys >= a.s.len)
+          tree_check_lengths(a.s, p.cu_q_lens, p.kv_lens, p.ws);
+        alive = mbar_wait(&B.q_empty, (parts & 1) ^ 1, abort, kWaitNs);
+        if (alive) {
+          mbar_arrive_expect_tx(&B.q_full, q_bytes * (a.n1 > 0 ? 2u : 1u));
+          for (int t = 0; t < (a.n1 > 0 ? 2 : 1); ++t)
+            for (int c = 0; c < kChunks; ++c)
+              tma_load_3d(smem + t * Lay::kQTile + c * (kTreeRows * 128), &tm_q, &B.q_full, c * 64,
+                          a.head * p.group, a.s.q0 + a.node0 + t * p.per_tile);
+          ++issued_q;
+        }
+      }
+      alive = __shfl_sync(0xffffffffu, alive, 0);
+      // A tile's source rows are looked up a tile ahead (lane < nbox: one box a stage).
+      auto tile_rows = [&](int j, int32_t (&rw)[kChunks]) {
+        const int32_t k0 = a.key0 + j * kTreeKeys;
+        if (is_k) {
+          const int32_t r = lane < nbox ? box_row(p, a, k0 + lane * rows, rows) : 0;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) rw[c] = r;
+        } else {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            rw[c] = lane < nbox ? box_row(p, a, k0 + c * Lay::kVKeys + lane * rows, rows) : 0;
+        }
+      };
+      int32_t rcur[kChunks], rnext[kChunks];
+      tile_rows(0, rcur);
+      for (int j = 0; j < a.n && alive; ++j) {
+        if (j + 1 < a.n) tile_rows(j + 1, rnext);
+#pragma unroll 1
+        for (int c = 0; c < kChunks; ++c, ++C) {
+          const int sl = C % kDepth;
+          if (lane == 0) alive = mbar_wait(&empty[sl], ((C / kDepth) & 1) ^ 1, abort, kWaitNs);
+          alive = __shfl_sync(0xffffffffu, alive, 0);
+          if (!alive) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[sl], kStage);
+          __syncwarp();
+          int32_t row = rcur[0];
+#pragma unroll
+          for (int x = 1; x < kChunks; ++x)
+            if (x == c) row = rcur[x];
+          if (lane < nbox) {
+            uint8_t* dst = ring + sl * kStage + lane * rows * 128;
+            if (is_k) {
+              tma_load_3d(dst, tm, &full[sl], c * 64, a.head, row);
+            } else if (p.v_4d) {
+              tma_load_4d(dst, tm, &full[sl], 0, a.head, row, 0);
+            } else {
+              for (int x = 0; x < kChunks; ++x)
+                tma_load_3d(dst + x * Lay::kVKeys * 128, tm, &full[sl], x * 64, a.head, row);
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) rcur[c] = rnext[c];
+      }
+    }
+    if (!alive && lane == 0) {
+      // Every copy lands before its shared memory goes.
+      report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
+      int none = 0;
+      for (uint32_t t = C > kDepth ? C - kDepth : 0; t < C; ++t)
+        mbar_wait(&full[t % kDepth], (t / kDepth) & 1, &none, kDrainNs);
+      if (issued_q > 0) mbar_wait(&B.q_full, (issued_q - 1) & 1, &none, kDrainNs);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ MMAs
+    constexpr uint32_t kIdS = idesc_bf16(kTreeKeys, 0), kIdPV = idesc_bf16(D, 1);
+    // Operands differ from these in the start address alone (see prefill_tc.cu).
+    const uint64_t q_d0 = smem_desc(smem_addr(smem), 16, 1024);
+    const uint64_t k_d0 = smem_desc(smem_addr(smem + Lay::kKOff), 16, 1024);
+    const uint64_t v_d0 = smem_desc(smem_addr(smem + Lay::kVOff), Lay::kVKeys * 128, 1024);
+    uint32_t parts = 0, asked = 0, pv[2] = {0, 0};
+    int ks = 0, vs = 0;
+    uint32_t kph = 0, vph = 0;
+    bool alive = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, kWaitNs));
+    };
+    auto step = [&](int& sl, uint32_t& ph) {
+      if (++sl == kDepth) {
+        sl = 0;
+        ph ^= 1;
+      }
+    };
+    // S of operation `op` (row tile `t` of Q) from the next K tile, which is given back
+    // after its last use.
+    auto issue_s = [&](int op, int t, bool last) -> bool {
+      const uint32_t sc = tmem + Lay::kSCol + (op & 1) * kTreeKeys;
+      int sl = ks;
+      uint32_t ph = kph;
+#pragma unroll 1
+      for (int c = 0; c < kChunks; ++c) {
+        if (!wait(&B.k_full[sl], ph)) return false;
+        tc_fence_after();
+        const uint64_t kd = k_d0 + static_cast<uint64_t>(sl * (kStage >> 4));
+        const uint64_t qd = q_d0 + static_cast<uint64_t>((t * Lay::kQTile + c * (kTreeRows * 128)) >> 4);
+        if (last)
+          mma_ss4_commit(sc, qd, qd + 2, qd + 4, qd + 6, kd, kd + 2, kd + 4, kd + 6, kIdS, c > 0 ? 1u : 0u,
+                         &B.k_empty[sl]);
+        else
+          mma_ss4(sc, qd, qd + 2, qd + 4, qd + 6, kd, kd + 2, kd + 4, kd + 6, kIdS, c > 0 ? 1u : 0u);
+        step(sl, ph);
+      }
+      if (last) {
+        ks = sl;
+        kph = ph;
+      }
+      mma_commit(&B.s_full[op & 1]);
+      return true;
+    };
+    // O += P V of operation `op`; `fresh`: its stream's first in the part; `ask`: the
+    // tile's V has to be made safe first.
+    auto issue_pv = [&](int op, bool last, bool fresh, bool first_use, bool masked) -> bool {
+      const int b = op & 1;
+      if (masked && first_use) {
+        int sl = vs;
+        uint32_t ph = vph;
+        for (int c = 0; c < kChunks; ++c) {
+          if (!wait(&B.v_full[sl], ph)) return false;
+          step(sl, ph);
+        }
+        if (lane == 0) mbar_arrive(&B.v_ask);
+      }
+      if (!wait(&B.p_full[b], pv[b] & 1)) return false;
+      ++pv[b];
+      if (op == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
+      if (masked && first_use) {
+        if (!wait(&B.v_safe, asked & 1)) return false;
+        ++asked;
+      }
+      const uint32_t p_col = tmem + Lay::kSCol + b * kTreeKeys + 64;
+      const uint32_t o_col = tmem + (kStreams == 2 ? b * D : 0);
+      int sl = vs;
+      uint32_t ph = vph;
+#pragma unroll 1
+      for (int c = 0; c < kChunks; ++c) {
+        if (!wait(&B.v_full[sl], ph)) return false;
+        tc_fence_after();
+        const uint64_t vd = v_d0 + static_cast<uint64_t>(sl * (kStage >> 4));
+        // kVKeys / 16 MMAs of 16 keys (P: 8 columns, V: 2048 B apart), in pairs.
+        constexpr int kPairs = Lay::kVKeys / 32;
+        const uint32_t pc = p_col + c * (Lay::kVKeys / 2);
+#pragma unroll
+        for (int q = 0; q < kPairs; ++q) {
+          const uint32_t acc = !fresh || c > 0 || q > 0 ? 1u : 0u;
+          if (q == kPairs - 1 && last)
+            mma_ts2_commit(o_col, pc + 16 * q, pc + 16 * q + 8, vd + 256 * q, vd + 256 * q + 128, kIdPV, acc,
+                           &B.v_empty[sl]);
+          else
+            mma_ts2(o_col, pc + 16 * q, pc + 16 * q + 8, vd + 256 * q, vd + 256 * q + 128, kIdPV, acc);
+        }
+        step(sl, ph);
+      }
+      if (last) {
+        vs = sl;
+        vph = ph;
+      }
+      mma_commit(&B.o_done[b]);
+      return true;
+    };
+    for (; alive && walk.next(work, p, a); ++parts) {
+      alive = wait(&B.q_full, parts & 1);
+      const bool two = a.n1 > 0;
+      const int ops = two ? 2 * a.n : a.n;
+      auto s_of = [&](int op) { return issue_s(op, two ? op & 1 : 0, !two || (op & 1)); };
+      if (alive) alive = s_of(0);
+      if (ops == 1) mma_commit(&B.q_empty);
+      for (int op = 0; op < ops && alive; ++op) {
+        if (op + 1 < ops) {
+          if (!(alive = s_of(op + 1))) break;
+          if (op + 2 == ops) mma_commit(&B.q_empty);
+        }
+        const int tile = two ? op >> 1 : op;
+        alive = issue_pv(op, !two || (op & 1), op < kStreams, !two || !(op & 1),
+                         a.masked(a.key0 + tile * kTreeKeys));
+      }
+    }
+    // Every MMA issued finishes before tensor memory is released.
+    mma_commit(&B.fin);
+    int none = 0;
+    mbar_wait(&B.fin, 0, &none, kDrainNs);
+    __syncwarp();
+    if (!alive && lane == 0) report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ V made safe
+    uint32_t C = 0, asked = 0, parts = 0;
+    bool alive = true;
+    for (; alive && walk.next(work, p, a); ++parts) {
+      for (int j = 0; j < a.n; ++j, C += kChunks) {
+        const int32_t k0 = a.key0 + j * kTreeKeys;
+        if (!a.masked(k0)) continue;
+        alive = __all_sync(0xffffffffu, mbar_wait(&B.v_ask, asked & 1, abort, kWaitNs));
+        if (!alive) break;
+        ++asked;
+        bool found = false;
+        for (int c = 0; c < kChunks; ++c)
+          found |= make_safe<D>(smem + Lay::kVOff + (C + c) % kDepth * kStage, k0 + c * Lay::kVKeys, a.lo, a.s.len,
+                                lane);
+        __syncwarp();
+        if (lane == 0) {
+          if (found) *reinterpret_cast<volatile int32_t*>(&B.poison[parts & 1]) = static_cast<int32_t>(parts) + 1;
+          mbar_arrive(&B.v_safe);
+        }
+      }
+    }
+    if (!alive && lane == 0) report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    const int w = kStreams == 2 ? (warp - 4) >> 2 : 0;  // stream
+    const int q4 = warp & 3, r = 32 * q4 + lane;        // lane quarter, row
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16);
+    const int G = p.group, tok = r / G, hd = r - tok * G;
+    const float c = p.scale_log2;
+    uint32_t used[2] = {0, 0};  // operations seen of each S buffer
+    uint32_t parts = 0, merges = 0;
+    bool alive = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, kWaitNs));
+    };
+    for (; alive && walk.next(work, p, a); ++parts) {
+      const bool two = a.n1 > 0;
+      const int tile_w = two ? w : 0;                     // row tile of this warp
+      const int nodes = tile_w ? a.n1 : a.n0;
+      const bool valid = tok < nodes && tok < p.per_tile;
+      const int32_t node = a.s.q0 + a.node0 + tile_w * p.per_tile + tok;
+      const uint64_t* mask_row = p.mask + static_cast<int64_t>(valid ? node : a.s.q0) * p.words;
+      const int32_t first = valid ? tree_first_key(a.s, p.positions, node, p.ws) : 0;
+      const bool some = __any_sync(0xffffffffu, valid);
+      // This stream's operations: all, or every second one.
+      const int ops = two ? 2 * a.n : a.n, step = kStreams;
+      float m_ref = -INFINITY, l = 0.f;
+      int mine = 0, last_b = 0;
+      for (int op = w; op < ops; op += step, ++mine) {
+        const int b = op & 1;
+        if (!(alive = wait(&B.s_full[b], used[b] & 1))) break;
+        const int prev_b = last_b;
+        last_b = b;
+        ++used[b];
+        tc_fence_after();
+        if (!some) {  // no row of this warp is one: its P may be anything
+          tc_fence_before();
+          mbar_arrive(&B.p_full[b]);
+          continue;
+        }
+        const int32_t key = a.key0 + (two ? op >> 1 : op) * kTreeKeys;
+        const uint32_t s_col = lane_addr + Lay::kSCol + b * kTreeKeys;
+        const bool masked = a.masked(key);
+        uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bits[i] = valid ? tree_sees32(a.s, mask_row, first, key + 32 * i) : 0u;
+        }
+        // A quarter of the row's scores, read twice (for the maximum, then for the
+        // weights; the last two quarters stay): 128 of them would not leave room.
+        uint32_t sa[32], sb[32];
+        auto flip = [&](uint32_t (&x)[32]) {
+          if (p.sign) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] ^= p.sign;
+          }
+        };
+        auto most = [&](uint32_t (&x)[32], uint32_t seen) -> float {
+          flip(x);
+          if (!masked) return max_tree<32>(x);
+          uint32_t y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = seen >> i & 1u ? x[i] : 0xff800000u;  // -inf
+          return max_tree<32>(y);
+        };
+        tmem_ld32(s_col, sa);
+        tmem_ld32(s_col + 32, sb);
+        tmem_wait_ld();
+        tmem_loaded(sa);
+        tmem_loaded(sb);
+        float mx = fmaxf(most(sa, bits[0]), most(sb, bits[1]));
+        tmem_ld32(s_col + 64, sa);
+        tmem_ld32(s_col + 96, sb);
+        tmem_wait_ld();
+        tmem_loaded(sa);
+        tmem_loaded(sb);
+        mx = fmax3(mx, most(sa, bits[2]), most(sb, bits[3]));
+        mx = mx == -INFINITY ? -INFINITY : mx * c;
+        const float m_new = fmaxf(m_ref, mx);
+        const bool grow = m_new > m_ref + 8.f;  // also for the first visible key
+        const bool rescale = grow && m_ref != -INFINITY;
+        if (__any_sync(0xffffffffu, rescale)) {
+          // O holds earlier tiles: after the last of their products.
+          if (!(alive = wait(&B.o_done[prev_b], (used[prev_b] - (prev_b == b ? 2 : 1)) & 1))) break;
+          tc_fence_after();
+          const float f = rescale ? fast_exp2(m_ref - m_new) : 1.f;
+          const uint32_t o_col = lane_addr + (kStreams == 2 ? w * D : 0);
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_col + c0, o);
+            tmem_wait_ld();
+            tmem_loaded(o);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+            tmem_st16(o_col + c0, o);
+          }
+          tmem_wait_st();
+        }
+        if (grow) {
+          if (l > 0.f) l *= fast_exp2(m_ref - m_new);
+          m_ref = m_new;
+        }
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_use, -m_use);
+        uint64_t acc = f2_pack(0.f, 0.f);
+        // P of a quarter, into columns 64 + 16 i of the buffer: over scores that are in
+        // registers by then.
+        auto weights = [&](const uint32_t (&x)[32], int i, uint32_t seen) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint64_t x2 =
+                f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, nm2);
+            float x0, x1;
+            f2_unpack(x2, x0, x1);
+            float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+            // (-inf times a scale of zero is NaN: the mask is applied to the weights.)
+            if (masked) {
+              p0 = seen >> (2 * k) & 1u ? p0 : 0.f;
+              p1 = seen >> (2 * k + 1) & 1u ? p1 : 0.f;
+            }
+            acc = f2_add(acc, f2_pack(p0, p1));
+            pk[k] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16(s_col + 64 + 16 * i, pk);
+        };
+        weights(sa, 2, bits[2]);
+        tmem_ld32(s_col, sa);
+        weights(sb, 3, bits[3]);
+        tmem_wait_ld();
+        tmem_loaded(sa);
+        tmem_ld32(s_col + 32, sb);
+        flip(sa);
+        weights(sa, 0, bits[0]);
+        tmem_wait_ld();
+        tmem_loaded(sb);
+        flip(sb);
+        weights(sb, 1, bits[1]);
+        float a0, a1;
+        f2_unpack(acc, a0, a1);
+        l += a0 + a1;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&B.p_full[b]);
+      }
+      if (!alive) break;
+      // The part's rows: this stream's, or half the columns of both streams' sum.
+      if (mine > 0 && !(alive = wait(&B.o_done[last_b], (used[last_b] - 1) & 1))) break;
+      tc_fence_after();
+      const bool merge = kStreams == 2 && !two;
+      float f0 = 1.f, f1 = 0.f, m = m_ref, sum = l;  // O = f0 O_0 + f1 O_1
+      if (merge) {
+        // (Products of this part have been waited for, so the last part's values have
+        // been read; a stream without one leaves them.)
+        float2* x = reinterpret_cast<float2*>(smem + Lay::kXchOff);
+        if (mine > 0) x[w * kTreeRows + r] = make_float2(m_ref, l);
+        tc_fence_before();
+        mbar_arrive(&B.xch);
+        if (!(alive = wait(&B.xch, merges & 1))) break;
+        ++merges;
+        tc_fence_after();
+        const float2 e0 = x[r], e1 = ops > 1 ? x[kTreeRows + r] : make_float2(-INFINITY, 0.f);
+        m = fmaxf(e0.x, e1.x);
+        f0 = e0.y == 0.f ? 0.f : e0.x == m ? 1.f : fast_exp2(e0.x - m);
+        f1 = e1.y == 0.f ? 0.f : e1.x == m ? 1.f : fast_exp2(e1.x - m);
+        sum = f0 * e0.y + f1 * e1.y;
+      }
+      if (some) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        f0 *= inv;
+        f1 *= inv;
+        const int c0 = merge ? w * (D / 2) : 0, c1 = merge ? c0 + D / 2 : D;
+        const bool both = merge && ops > 1;  // (else the second O holds nothing of this part)
+        const uint32_t o_col = lane_addr + (kStreams == 2 && !merge ? w * D : 0);
+        __nv_bfloat16* out = p.out + (static_cast<int64_t>(node) * p.hq + a.head * G + hd) * D;
+        const int64_t row = (2ll * blockIdx.x + (parts > 0 ? 1 : 0)) * (kTreeRows * kStreams) + tile_w * kTreeRows + r;
+        float* part = p.part_o + row * D;
+#pragma unroll 1
+        for (int col = c0; col < c1; col += 16) {
+          uint32_t o[16];
+          tmem_ld16(o_col + col, o);
+          if (both) {
+            uint32_t o1[16];
+            tmem_ld16(o_col + D + col, o1);
+            tmem_wait_ld();
+            tmem_loaded(o);
+            tmem_loaded(o1);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), f0, __uint_as_float(o1[i]) * f1));
+          } else {
+            tmem_wait_ld();
+            tmem_loaded(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+          }
+          if (!valid) continue;
+          uint32_t t[8];
+          if (a.whole) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+            store32(out + col, p.out_v8, t);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) t[x] = o[8 * i + x];
+              store32(part + col + 8 * i, true, t);
+            }
+          }
+        }
+        if (valid && !a.whole && (!merge || w == 0))
+          p.part_lse[row] = sum == 0.f ? -INFINITY : m + __log2f(sum);
+        if (valid && *reinterpret_cast<volatile int32_t*>(&B.poison[parts & 1]) == static_cast<int32_t>(parts) + 1) {
+          if (a.whole)
+            add_unseen(p, a, mask_row, first, D, c0, c1, out);
+          else
+            add_unseen(p, a, mask_row, first, D, c0, c1, part);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      mbar_arrive(&B.o_free);
+    }
+    if (!alive && lane == 0) report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
+  }
+  // Every MMA is finished before tensor memory is released.
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Lay::kCols);
+  }
+}
+
+template <int N>
+struct CutList {
+  TreeCut cut[kTreeMaxCtas];
+  TreeSeqs<N> seqs;
+};
+
+// The parts of each cut segment joined: out = sum_k 2^(lse_k - M) O_k / sum_k
+// 2^(lse_k - M), M the largest lse_k.  A warp per row.
+template <int D, int N>
+__global__ void __launch_bounds__(256)
+tree_combine_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CutList<N> list) {
+  constexpr int E = D / 32, kRows = kTreeRows * tree_row_tiles(D);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const TreeCut& g = list.cut[blockIdx.x];
+  const TreeSeq& s = list.seqs.s[g.i];
+  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int tile = row / kTreeRows, r = row % kTreeRows, tok = r / p.group, hd = r - tok * p.group;
+  const int32_t node = (g.st * tree_row_tiles(D) + tile) * p.per_tile + tok;
+  if (tok >= p.per_tile || node >= s.nodes) return;
+  auto slot = [&](int k) -> int64_t { return (2ll * (g.cta + k) + (k == 0 ? g.first : 0)) * kRows + row; };
+  float M = -INFINITY;
+  for (int k = lane; k < g.nparts; k += 32) M = fmaxf(M, p.part_lse[slot(k)]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float acc[E], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int k0 = 0; k0 < g.nparts; k0 += 32) {
+    const int n = min(32, g.nparts - k0);
+    const float lse = lane < n ? p.part_lse[slot(k0 + lane)] : -INFINITY;
+    const float mine = lse == -INFINITY ? 0.f : lse == M ? 1.f : fast_exp2(lse - M);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float w = __shfl_sync(0xffffffffu, mine, k);
+      const float* src = p.part_o + slot(k0 + k) * D + lane * E;
+      sum += w;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(src + e);
+        acc[e] = fmaf(w, v.x, acc[e]);
+        acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat16* dst =
+      p.out + (static_cast<int64_t>(s.q0 + node) * p.hq + g.head * p.group + hd) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+}
+
+template <int D, int N>
+int launch_one(const Plan& plan, const TreeLaunch& l, const CUtensorMap& tq, const CUtensorMap& tk,
+               const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
+  using Lay = Layout<D>;
+  if (int e = ensure_dynamic_smem(reinterpret_cast<const void*>(tree_attn_kernel<D, N>), Lay::kBytes)) return e;
+  TreeWork<N>& w = thread_staging<TreeWork<N>>();
+  w.seqs.n = l.seq_end - l.seq_begin;
+  std::copy(plan.tree_seqs.begin() + l.seq_begin, plan.tree_seqs.begin() + l.seq_end, w.seqs.s);
+  std::copy_n(plan.tree_starts.begin() + l.start_begin, l.n_ctas, w.start);
+  tree_attn_kernel<D, N><<<l.n_ctas, Lay::kThreads, Lay::kBytes, stream>>>(tq, tk, tv, p, w);
+  if (cudaError_t e = cudaGetLastError()) return static_cast<int>(e);
+  trace_mark(RPA_KERNEL_TREE_ATTN, stream);
+  if (l.n_cut == 0) return 0;
+  CutList<N>& c = thread_staging<CutList<N>>();
+  std::copy_n(plan.tree_cuts.begin() + l.cut_begin, l.n_cut, c.cut);
+  std::copy_n(w.seqs.s, w.seqs.n, c.seqs.s);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(l.n_cut, kTreeRows * Lay::kStreams / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, N>, p, c)) return static_cast<int>(e);
+  trace_mark(RPA_KERNEL_TREE_COMBINE, stream);
+  return 0;
+}
+
+template <int D>
+int launch_d(const Plan& plan, const Args& a, cudaStream_t stream) {
+  using Lay = Layout<D>;
+  const int G = plan.hq / plan.hkv;
+  TreeParams p;
+  p.page_table = a.page_table;
+  p.cu_q_lens = a.cu_q_lens;
+  p.kv_lens = a.kv_lens;
+  p.mask = a.tree_mask;
+  p.positions = a.positions;
+  p.v_pages = static_cast<const __nv_bfloat16*>(a.v_pages);
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.part_o = reinterpret_cast<float*>(a.workspace + plan.off_partial_o);
+  p.part_lse = reinterpret_cast<float*>(a.workspace + plan.off_partial_lse);
+  p.ws = a.workspace;
+  p.hq = plan.hq;
+  p.hkv = plan.hkv;
+  p.group = G;
+  p.per_tile = kTreeRows / G;
+  p.page_size = plan.p;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < plan.p) ++p.page_shift;
+  p.mpps = plan.mpps;
+  p.num_pages = plan.num_pages;
+  p.words = plan.tree_words;
+  // Boxes never cross a page.
+  p.box_rows_k = std::min(plan.p, kTreeKeys);
+  p.box_rows_v = std::min(plan.p, Lay::kVKeys);
+  // A V stage in one page takes all its 64-dimension chunks in one box.
+  p.v_4d = Lay::kChunks > 1 && p.box_rows_v == Lay::kVKeys ? 1 : 0;
+  p.out_v8 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 ? 1 : 0;
+  p.scale_log2 = std::fabs(a.sm_scale) * 1.4426950408889634f;
+  p.sign = std::signbit(a.sm_scale) ? 0x80000000u : 0u;
+  CUtensorMap tq, tk, tv;
+  const uint64_t pool_rows = static_cast<uint64_t>(plan.num_pages) * plan.p;
+  if (!make_tmap_3d(&tq, a.q, D, plan.hq, static_cast<uint64_t>(plan.total_q), G, p.per_tile) ||
+      !make_tmap_3d(&tk, a.k_pages, D, plan.hkv, pool_rows, 1, p.box_rows_k) ||
+      !(p.v_4d ? make_tmap_4d_chunks(&tv, a.v_pages, D, plan.hkv, pool_rows, 1, p.box_rows_v, false)
+               : make_tmap_3d(&tv, a.v_pages, D, plan.hkv, pool_rows, 1, p.box_rows_v)))
+    return static_cast<int>(cudaErrorInvalidValue);
+  for (const TreeLaunch& l : plan.tree_launches) {
+    const int e = l.seq_end - l.seq_begin <= kTreeSeqsSmall
+                      ? launch_one<D, kTreeSeqsSmall>(plan, l, tq, tk, tv, p, stream)
+                      : launch_one<D, kTreeSeqsLarge>(plan, l, tq, tk, tv, p, stream);
+    if (e) return e;
+  }
+  return 0;
+}
+
+}  // namespace
+
+bool tree_tc_supported(int32_t head_dim, int32_t page_size, int32_t group) {
+  return (head_dim == 64 || head_dim == 128 || head_dim == 256) && page_size >= 16 && group >= 1 &&
+         group <= kTreeRows;
+}
+
+int launch_tree_attn(const Plan& plan, const Args& a, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (plan.d) {
+    case 64: return launch_d<64>(plan, a, s);
+    case 128: return launch_d<128>(plan, a, s);
+    case 256: return launch_d<256>(plan, a, s);
+    default: return static_cast<int>(cudaErrorInvalidValue);
+  }
+}
 
 }  // namespace rpa

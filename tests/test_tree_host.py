@@ -4,6 +4,8 @@ return before anything is enqueued."""
 from __future__ import annotations
 
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -35,7 +37,7 @@ def refused(status, fn, *args):
 
 def test_plans():
     info = plan().info()
-    assert info["num_decode_seqs"] == 2 and info["num_prefill_seqs"] == 0 and info["decode_kernel"] == 0
+    assert info["path"] == binding.RPA_PATH_TC and info["num_decode_seqs"] == 2 and info["num_prefill_seqs"] == 0 and info["decode_kernel"] == 0
     assert plan(nodes=(0, 0)).workspace_bytes == 256
     assert plan(nodes=(), ctx=()).workspace_bytes == 256
     assert plan(dtype=binding.RPA_DTYPE_F32).info()["path"] == binding.RPA_PATH_SIMT
@@ -173,3 +175,15 @@ def test_trim_tables_refusals():
     args[7] = (1 << 30) + 1
     args[5] = args[1]
     assert L.rpa_trim_tables(*args) == UNSUPPORTED
+
+
+def test_schedules_cover_every_tile_once(tmp_path):
+    """Random batches through the scheduler alone (tests/csrc/tree_plan_check.cpp)."""
+    exe = str(tmp_path / "tree_plan_check")
+    here = os.path.dirname(os.path.abspath(__file__))
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc()))), "include")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-I" + build.INCLUDE, "-I" + build.CSRC, "-I" + cuda,
+                    os.path.join(here, "csrc", "tree_plan_check.cpp"), os.path.join(build.CSRC, "plan_tree.cpp"),
+                    "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout
