@@ -192,20 +192,6 @@ __device__ __forceinline__ void mma_ss4_commit(uint32_t d_tmem, uint64_t a0, uin
       : "memory");
 }
 
-// The same without the commit (operands that are used again).
-__device__ __forceinline__ void mma_ss4(uint32_t d_tmem, uint64_t a0, uint64_t a1, uint64_t a2, uint64_t a3,
-                                        uint64_t b0, uint64_t b1, uint64_t b2, uint64_t b3, uint32_t idesc,
-                                        uint32_t acc0) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %10, 0;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %9, p;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, 1;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, 1;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, 1;\n}\n" ::"r"(d_tmem),
-      "l"(a0), "l"(a1), "l"(a2), "l"(a3), "l"(b0), "l"(b1), "l"(b2), "l"(b3), "r"(idesc), "r"(acc0)
-      : "memory");
-}
-
 // Two D (+)= A_i[tmem] * B_i (B in shared memory) from one elected lane; the
 // first accumulates when `acc0` is nonzero.  With `bar`, a commit follows.
 __device__ __forceinline__ void mma_ts2(uint32_t d_tmem, uint32_t a0, uint32_t a1, uint64_t b0,
@@ -227,6 +213,67 @@ __device__ __forceinline__ void mma_ts2_commit(uint32_t d_tmem, uint32_t a0, uin
       " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n}\n" ::"r"(
           d_tmem),
       "r"(a0), "r"(a1), "l"(b0), "l"(b1), "r"(idesc), "r"(acc0), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Groups of one elected lane whose descriptors step inside: D (+)= A_i * B_i, A and B in
+// shared memory, i over 64 dimensions (32 bytes a step) of one 64-dimension chunk, or
+// of two chunks 16 KB apart.
+__device__ __forceinline__ void mma_ss_chunk(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t acc0) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n setp.ne.b32 p, %4, 0;\n"
+      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc0)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss_2chunks(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred e;\n .reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n"
+      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n add.s64 a4, %1, 1024;\n"
+      " add.s64 a5, %1, 1026;\n add.s64 a6, %1, 1028;\n add.s64 a7, %1, 1030;\n"
+      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n add.s64 b4, %2, 1024;\n"
+      " add.s64 b5, %2, 1026;\n add.s64 b6, %2, 1028;\n add.s64 b7, %2, 1030;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, 1;\n}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc)
+      : "memory");
+}
+// D (+)= A_i[tmem] * B_i over 128 keys, 16 a step (8 columns of A, 2048 bytes of B);
+// the last 64 keys' B begins kHalf descriptor units behind the first's.
+template <int kHalf>
+__device__ __forceinline__ void mma_ts_128keys(uint32_t d_tmem, uint32_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t acc0) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b64 b1, b2, b3, b4, b5, b6, b7;\n"
+      " .reg .b32 a1, a2, a3, a4, a5, a6, a7;\n setp.ne.b32 p, %4, 0;\n"
+      " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n add.s64 b4, %2, %5;\n"
+      " add.s64 b5, b4, 128;\n add.s64 b6, b4, 256;\n add.s64 b7, b4, 384;\n"
+      " add.s32 a1, %1, 8;\n add.s32 a2, %1, 16;\n add.s32 a3, %1, 24;\n add.s32 a4, %1, 32;\n"
+      " add.s32 a5, %1, 40;\n add.s32 a6, %1, 48;\n add.s32 a7, %1, 56;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, 1;\n}\n" ::"r"(d_tmem),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc0), "n"(kHalf)
       : "memory");
 }
 

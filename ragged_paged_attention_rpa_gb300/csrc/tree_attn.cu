@@ -35,7 +35,7 @@
 #include <cuda.h>
 
 #include <algorithm>
-#include <cmath>
+#include <type_traits>
 
 #include "sm100_ptx.cuh"
 #include "tree.cuh"
@@ -45,9 +45,21 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kStage = 16384;
+constexpr int kSub = 16384;  // a 64-dimension chunk of 128 keys of K, or 8192 / D keys of V
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
+
+// A wait (mbar_wait) of a converged warp, which agrees on the answer; what follows a phase that
+// is not complete yet stays out of the way of the caller's code.
+__device__ __noinline__ bool warp_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                            uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns));
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          uint64_t limit_ns) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait_slow(bar, parity, abort, limit_ns);
+}
 
 template <int N>
 struct TreeWork {
@@ -69,21 +81,23 @@ struct TreeParams {
   int32_t hq, hkv, group, per_tile;  // nodes a row tile
   int32_t page_size, page_shift, mpps, num_pages, words;
   int32_t box_rows_k, box_rows_v, v_4d, out_v8;
-  float scale_log2;  // |sm_scale| log2(e)
-  uint32_t sign;     // flips the scores of a negative scale
+  float scale_log2;  // sm_scale log2(e)
 };
 
 template <int D>
 struct Layout {
   static constexpr int kStreams = tree_row_tiles(D);
   static constexpr int kThreads = 128 + 128 * kStreams;
-  static constexpr int kChunks = D / 64;         // 128-byte pieces of a row; stages of a tile, of K and of V
-  static constexpr int kVKeys = 8192 / D;        // keys of a V stage
-  static constexpr int kDepth = D == 64 ? 6 : 5; // stages of each ring
+  static constexpr int kChunks = D / 64;         // 128-byte pieces of a row; 16 KB pieces of a tile, of K and of V
+  static constexpr int kVKeys = 8192 / D;        // keys of such a piece of V
+  // Ring slots: a tile of 64 or 128 dimensions, a quarter of one of 256 (whose MMAs
+  // start before all of it has landed); their number for K and V.
+  static constexpr int kSubs = D == 128 ? 2 : 1, kSlots = kChunks / kSubs, kSlot = kSubs * kSub;
+  static constexpr int kKDepth = D == 64 ? 6 : D == 128 ? 2 : 5, kVDepth = D == 64 ? 6 : D == 128 ? 3 : 5;
   static constexpr int kQTile = kTreeRows * D * 2;
   static constexpr int kKOff = kStreams * kQTile;
-  static constexpr int kVOff = kKOff + kDepth * kStage;
-  static constexpr int kBarOff = kVOff + kDepth * kStage;
+  static constexpr int kVOff = kKOff + kKDepth * kSlot;
+  static constexpr int kBarOff = kVOff + kVDepth * kSlot;
   static constexpr int kXchOff = kBarOff + 512;  // [stream][row] (maximum, sum)
   static constexpr int kUsed = kXchOff + (kStreams == 2 ? 2 * kTreeRows * 8 : 0);
   static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;  // one CTA per SM
@@ -187,27 +201,42 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
   return w;
 }
 
-// A V stage ([chunk][key][128 B]) of keys from `key` on made safe (whole warp);
-// true where a NaN or an infinity of a visible key was taken out.
+// 16 KB of V ([chunk][key][128 B]) of keys from `key` on made safe (whole warp); true
+// where a NaN or an infinity of a visible key was taken out.  Mostly there is none: a
+// first pass takes the largest magnitude (its bits are in order) of everything.
 template <int D>
-__device__ __noinline__ bool make_safe(uint8_t* stage, int32_t key, int32_t lo, int32_t len, int lane) {
-  constexpr int kVKeys = Layout<D>::kVKeys;
-  bool found = false;
-#pragma unroll 8
-  for (int u = lane; u < kStage / 16; u += 32) {
-    const int32_t k = key + ((u >> 3) & (kVKeys - 1));
-    uint4* at = reinterpret_cast<uint4*>(stage) + u;
-    if (k < lo || k >= len) {
-      *at = make_uint4(0u, 0u, 0u, 0u);
-      continue;
-    }
-    const uint4 v = *at;
-    if (not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) || not_finite2(v.w)) {
-      *at = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
-      found = true;
-    }
+__device__ __noinline__ bool make_safe(uint8_t* piece, int32_t key, int32_t lo, int32_t len, int lane) {
+  constexpr int kVKeys = Layout<D>::kVKeys, kUnits = kSub / 16;
+  uint4* at = reinterpret_cast<uint4*>(piece);
+  auto row_of = [&](int u) { return (u >> 3) & (kVKeys - 1); };
+  const int32_t a = max(0, min(kVKeys, lo - key)), b = max(0, min(kVKeys, len - key));  // rows [a, b) are visible
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int u0 = 0; u0 < kUnits; u0 += 32 * 8) {
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = at[u0 + 32 * i + lane];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      top = __vmaxu2(__vmaxu2(__vmaxu2(top, v[i].x & 0x7fff7fffu), v[i].y & 0x7fff7fffu),
+                     __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
   }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  const bool any = __any_sync(0xffffffffu, not_finite2(top));
+  bool found = false;
+  if (any) {
+    for (int u = lane; u < kUnits; u += 32) {
+      if (row_of(u) < a || row_of(u) >= b) continue;
+      const uint4 v = at[u];
+      if (not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) || not_finite2(v.w)) {
+        at[u] = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+        found = true;
+      }
+    }
+    // Rows that nobody sees.
+    for (int u = lane; u < kUnits; u += 32)
+      if (row_of(u) < a || row_of(u) >= b) at[u] = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
   return __any_sync(0xffffffffu, found);
 }
 
@@ -234,12 +263,19 @@ __device__ __noinline__ void add_unseen(const TreeParams& p, const Part& a, cons
   }
 }
 
-template <int N>
-__device__ __forceinline__ float max_tree(const uint32_t* v) {
+// The largest (or smallest) of N floats, as a tree of three-input operations.
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <int N, bool kMax>
+__device__ __forceinline__ float extremum(const uint32_t* v) {
   if constexpr (N == 1) {
     return __uint_as_float(v[0]);
   } else if constexpr (N == 2) {
-    return fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+    return kMax ? fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]))
+                : fminf(__uint_as_float(v[0]), __uint_as_float(v[1]));
   } else {
     constexpr int M = (N + 2) / 3;
     uint32_t t[M];
@@ -247,13 +283,15 @@ __device__ __forceinline__ float max_tree(const uint32_t* v) {
     for (int i = 0; i < M; ++i) {
       const float a = __uint_as_float(v[3 * i]);
       float m = a;
-      if (3 * i + 2 < N)
-        m = fmax3(a, __uint_as_float(v[3 * i + 1]), __uint_as_float(v[3 * i + 2]));
-      else if (3 * i + 1 < N)
-        m = fmaxf(a, __uint_as_float(v[3 * i + 1]));
+      if (3 * i + 2 < N) {
+        const float b = __uint_as_float(v[3 * i + 1]), c = __uint_as_float(v[3 * i + 2]);
+        m = kMax ? fmax3(a, b, c) : fmin3(a, b, c);
+      } else if (3 * i + 1 < N) {
+        m = kMax ? fmaxf(a, __uint_as_float(v[3 * i + 1])) : fminf(a, __uint_as_float(v[3 * i + 1]));
+      }
       t[i] = __float_as_uint(m);
     }
-    return max_tree<M>(t);
+    return extremum<M, kMax>(t);
   }
 }
 
@@ -275,7 +313,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p,
                  const __grid_constant__ TreeWork<N> work) {
   using Lay = Layout<D>;
-  constexpr int kDepth = Lay::kDepth, kChunks = Lay::kChunks, kStreams = Lay::kStreams;
+  constexpr int kChunks = Lay::kChunks, kStreams = Lay::kStreams, kSubs = Lay::kSubs, kSlots = Lay::kSlots;
+  constexpr int kKDepth = Lay::kKDepth, kVDepth = Lay::kVDepth;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_addr(smem) & 1023u) {
     if (threadIdx.x == 0) report_error(p.ws, RPA_DEVERR_LAUNCH, blockIdx.x);
@@ -289,7 +328,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (threadIdx.x == 0) {
     mbar_init(&B.q_full, 1);
     mbar_init(&B.q_empty, 1);
-    for (int i = 0; i < kDepth; ++i) {
+    for (int i = 0; i < 6; ++i) {
       mbar_init(&B.k_full[i], 1);
       mbar_init(&B.k_empty[i], 1);
       mbar_init(&B.v_full[i], 1);
@@ -330,8 +369,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     uint8_t* ring = smem + (is_k ? Lay::kKOff : Lay::kVOff);
     const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
     const int rows = is_k ? p.box_rows_k : p.box_rows_v;
-    const int nbox = (is_k ? kTreeKeys : Lay::kVKeys) / rows;  // boxes of a stage
+    const int nbox = (is_k ? kTreeKeys : Lay::kVKeys) / rows;  // boxes of 16 KB
+    const int depth = is_k ? kKDepth : kVDepth;
     const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.per_tile) * 128u * kChunks;
+    int sl = 0;       // next slot
+    uint32_t ph = 0;  // and its phase
     uint32_t C = 0, parts = 0, issued_q = 0;
     bool alive = true;
     for (; alive && walk.next(work, p, a); ++parts) {
@@ -367,28 +409,30 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       tile_rows(0, rcur);
       for (int j = 0; j < a.n && alive; ++j) {
         if (j + 1 < a.n) tile_rows(j + 1, rnext);
-#pragma unroll 1
-        for (int c = 0; c < kChunks; ++c, ++C) {
-          const int sl = C % kDepth;
-          if (lane == 0) alive = mbar_wait(&empty[sl], ((C / kDepth) & 1) ^ 1, abort, kWaitNs);
-          alive = __shfl_sync(0xffffffffu, alive, 0);
-          if (!alive) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full[sl], kStage);
-          __syncwarp();
-          int32_t row = rcur[0];
 #pragma unroll
-          for (int x = 1; x < kChunks; ++x)
-            if (x == c) row = rcur[x];
+        for (int c = 0; c < kChunks; ++c) {
+          if (c % kSubs == 0) {
+            if (lane == 0) alive = mbar_wait(&empty[sl], ph ^ 1, abort, kWaitNs);
+            alive = __shfl_sync(0xffffffffu, alive, 0);
+            if (!alive) break;
+            if (lane == 0) mbar_arrive_expect_tx(&full[sl], Lay::kSlot);
+            ++C;
+            __syncwarp();
+          }
           if (lane < nbox) {
-            uint8_t* dst = ring + sl * kStage + lane * rows * 128;
+            uint8_t* dst = ring + sl * Lay::kSlot + (c % kSubs) * kSub + lane * rows * 128;
             if (is_k) {
-              tma_load_3d(dst, tm, &full[sl], c * 64, a.head, row);
+              tma_load_3d(dst, tm, &full[sl], c * 64, a.head, rcur[c]);
             } else if (p.v_4d) {
-              tma_load_4d(dst, tm, &full[sl], 0, a.head, row, 0);
+              tma_load_4d(dst, tm, &full[sl], 0, a.head, rcur[c], 0);
             } else {
               for (int x = 0; x < kChunks; ++x)
-                tma_load_3d(dst + x * Lay::kVKeys * 128, tm, &full[sl], x * 64, a.head, row);
+                tma_load_3d(dst + x * Lay::kVKeys * 128, tm, &full[sl], x * 64, a.head, rcur[c]);
             }
+          }
+          if (c % kSubs == kSubs - 1 && ++sl == depth) {
+            sl = 0;
+            ph ^= 1;
           }
         }
 #pragma unroll
@@ -399,8 +443,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // Every copy lands before its shared memory goes.
       report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
       int none = 0;
-      for (uint32_t t = C > kDepth ? C - kDepth : 0; t < C; ++t)
-        mbar_wait(&full[t % kDepth], (t / kDepth) & 1, &none, kDrainNs);
+      for (uint32_t t = C > static_cast<uint32_t>(depth) ? C - depth : 0; t < C; ++t)
+        mbar_wait(&full[t % depth], (t / depth) & 1, &none, kDrainNs);
       if (issued_q > 0) mbar_wait(&B.q_full, (issued_q - 1) & 1, &none, kDrainNs);
     }
   } else if (warp == 2) {
@@ -414,87 +458,87 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     int ks = 0, vs = 0;
     uint32_t kph = 0, vph = 0;
     bool alive = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, kWaitNs));
-    };
-    auto step = [&](int& sl, uint32_t& ph) {
-      if (++sl == kDepth) {
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, abort, kWaitNs); };
+    auto step = [&](int& sl, uint32_t& ph, int depth) {
+      if (++sl == depth) {
         sl = 0;
         ph ^= 1;
       }
     };
-    // S of operation `op` (row tile `t` of Q) from the next K tile, which is given back
-    // after its last use.
-    auto issue_s = [&](int op, int t, bool last) -> bool {
+    // S of operation `op` (row tile `t` of Q) from the next K tile; `first`, `last`: of
+    // its uses, after which it is given back.
+    auto issue_s = [&](int op, int t, bool first, bool last) -> bool {
       const uint32_t sc = tmem + Lay::kSCol + (op & 1) * kTreeKeys;
-      int sl = ks;
-      uint32_t ph = kph;
-#pragma unroll 1
-      for (int c = 0; c < kChunks; ++c) {
-        if (!wait(&B.k_full[sl], ph)) return false;
+      const uint64_t qd = q_d0 + static_cast<uint64_t>(t * (Lay::kQTile >> 4));
+      if constexpr (kSlots == 1) {
+        if (first && !wait(&B.k_full[ks], kph)) return false;
         tc_fence_after();
-        const uint64_t kd = k_d0 + static_cast<uint64_t>(sl * (kStage >> 4));
-        const uint64_t qd = q_d0 + static_cast<uint64_t>((t * Lay::kQTile + c * (kTreeRows * 128)) >> 4);
-        if (last)
-          mma_ss4_commit(sc, qd, qd + 2, qd + 4, qd + 6, kd, kd + 2, kd + 4, kd + 6, kIdS, c > 0 ? 1u : 0u,
-                         &B.k_empty[sl]);
+        const uint64_t kd = k_d0 + static_cast<uint64_t>(ks * (Lay::kSlot >> 4));
+        if constexpr (kSubs == 2)
+          mma_ss_2chunks(sc, qd, kd, kIdS);
         else
-          mma_ss4(sc, qd, qd + 2, qd + 4, qd + 6, kd, kd + 2, kd + 4, kd + 6, kIdS, c > 0 ? 1u : 0u);
-        step(sl, ph);
-      }
-      if (last) {
-        ks = sl;
-        kph = ph;
+          mma_ss_chunk(sc, qd, kd, kIdS, 0);
+        if (last) {
+          mma_commit(&B.k_empty[ks]);
+          step(ks, kph, kKDepth);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < kSlots; ++c) {
+          if (!wait(&B.k_full[ks], kph)) return false;
+          tc_fence_after();
+          mma_ss_chunk(sc, qd + static_cast<uint64_t>(c * (kSub >> 4)),
+                       k_d0 + static_cast<uint64_t>(ks * (Lay::kSlot >> 4)), kIdS, c > 0 ? 1u : 0u);
+          mma_commit(&B.k_empty[ks]);
+          step(ks, kph, kKDepth);
+        }
       }
       mma_commit(&B.s_full[op & 1]);
       return true;
     };
-    // O += P V of operation `op`; `fresh`: its stream's first in the part; `ask`: the
-    // tile's V has to be made safe first.
-    auto issue_pv = [&](int op, bool last, bool fresh, bool first_use, bool masked) -> bool {
+    // O += P V of operation `op`; `fresh`: its stream's first in the part; `first`,
+    // `last`: the V tile's uses; `masked`: it has to be made safe before the first.
+    auto issue_pv = [&](int op, bool fresh, bool first, bool last, bool masked) -> bool {
       const int b = op & 1;
-      if (masked && first_use) {
+      if (masked && first) {
         int sl = vs;
         uint32_t ph = vph;
-        for (int c = 0; c < kChunks; ++c) {
+        for (int c = 0; c < kSlots; ++c) {
           if (!wait(&B.v_full[sl], ph)) return false;
-          step(sl, ph);
+          step(sl, ph, kVDepth);
         }
         if (lane == 0) mbar_arrive(&B.v_ask);
       }
       if (!wait(&B.p_full[b], pv[b] & 1)) return false;
       ++pv[b];
       if (op == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
-      if (masked && first_use) {
+      if (masked && first) {
         if (!wait(&B.v_safe, asked & 1)) return false;
         ++asked;
       }
       const uint32_t p_col = tmem + Lay::kSCol + b * kTreeKeys + 64;
       const uint32_t o_col = tmem + (kStreams == 2 ? b * D : 0);
-      int sl = vs;
-      uint32_t ph = vph;
-#pragma unroll 1
-      for (int c = 0; c < kChunks; ++c) {
-        if (!wait(&B.v_full[sl], ph)) return false;
+      if constexpr (kSlots == 1) {
+        if (first && !wait(&B.v_full[vs], vph)) return false;
         tc_fence_after();
-        const uint64_t vd = v_d0 + static_cast<uint64_t>(sl * (kStage >> 4));
-        // kVKeys / 16 MMAs of 16 keys (P: 8 columns, V: 2048 B apart), in pairs.
-        constexpr int kPairs = Lay::kVKeys / 32;
-        const uint32_t pc = p_col + c * (Lay::kVKeys / 2);
-#pragma unroll
-        for (int q = 0; q < kPairs; ++q) {
-          const uint32_t acc = !fresh || c > 0 || q > 0 ? 1u : 0u;
-          if (q == kPairs - 1 && last)
-            mma_ts2_commit(o_col, pc + 16 * q, pc + 16 * q + 8, vd + 256 * q, vd + 256 * q + 128, kIdPV, acc,
-                           &B.v_empty[sl]);
-          else
-            mma_ts2(o_col, pc + 16 * q, pc + 16 * q + 8, vd + 256 * q, vd + 256 * q + 128, kIdPV, acc);
+        mma_ts_128keys<kSubs == 2 ? kSub / 16 : 512>(o_col, p_col, v_d0 + static_cast<uint64_t>(vs * (Lay::kSlot >> 4)),
+                                                     kIdPV, fresh ? 0u : 1u);
+        if (last) {
+          mma_commit(&B.v_empty[vs]);
+          step(vs, vph, kVDepth);
         }
-        step(sl, ph);
-      }
-      if (last) {
-        vs = sl;
-        vph = ph;
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < kSlots; ++c) {
+          if (!wait(&B.v_full[vs], vph)) return false;
+          tc_fence_after();
+          // Two MMAs of 16 keys (P: 8 columns, V: 2048 B apart).
+          static_assert(kSlots == 1 || Lay::kVKeys == 32, "");
+          const uint64_t vd = v_d0 + static_cast<uint64_t>(vs * (Lay::kSlot >> 4));
+          const uint32_t pc = p_col + c * 16;
+          mma_ts2_commit(o_col, pc, pc + 8, vd, vd + 128, kIdPV, !fresh || c > 0 ? 1u : 0u, &B.v_empty[vs]);
+          step(vs, vph, kVDepth);
+        }
       }
       mma_commit(&B.o_done[b]);
       return true;
@@ -503,7 +547,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       alive = wait(&B.q_full, parts & 1);
       const bool two = a.n1 > 0;
       const int ops = two ? 2 * a.n : a.n;
-      auto s_of = [&](int op) { return issue_s(op, two ? op & 1 : 0, !two || (op & 1)); };
+      auto s_of = [&](int op) { return issue_s(op, two ? op & 1 : 0, !two || !(op & 1), !two || (op & 1)); };
       if (alive) alive = s_of(0);
       if (ops == 1) mma_commit(&B.q_empty);
       for (int op = 0; op < ops && alive; ++op) {
@@ -512,7 +556,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           if (op + 2 == ops) mma_commit(&B.q_empty);
         }
         const int tile = two ? op >> 1 : op;
-        alive = issue_pv(op, !two || (op & 1), op < kStreams, !two || !(op & 1),
+        alive = issue_pv(op, op < kStreams, !two || !(op & 1), !two || (op & 1),
                          a.masked(a.key0 + tile * kTreeKeys));
       }
     }
@@ -524,19 +568,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (!alive && lane == 0) report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
   } else if (warp == 3) {
     // ------------------------------------------------------------ V made safe
-    uint32_t C = 0, asked = 0, parts = 0;
+    uint32_t asked = 0, parts = 0;
+    int sl = 0;  // slot of the next tile's V
     bool alive = true;
     for (; alive && walk.next(work, p, a); ++parts) {
-      for (int j = 0; j < a.n; ++j, C += kChunks) {
+      for (int j = 0; j < a.n; ++j) {
         const int32_t k0 = a.key0 + j * kTreeKeys;
-        if (!a.masked(k0)) continue;
-        alive = __all_sync(0xffffffffu, mbar_wait(&B.v_ask, asked & 1, abort, kWaitNs));
-        if (!alive) break;
+        if (!a.masked(k0)) {
+          if ((sl += kSlots) >= kVDepth) sl -= kVDepth;
+          continue;
+        }
+        if (!(alive = warp_wait(&B.v_ask, asked & 1, abort, kWaitNs))) break;
         ++asked;
         bool found = false;
-        for (int c = 0; c < kChunks; ++c)
-          found |= make_safe<D>(smem + Lay::kVOff + (C + c) % kDepth * kStage, k0 + c * Lay::kVKeys, a.lo, a.s.len,
-                                lane);
+        for (int c = 0; c < kChunks; ++c) {
+          found |= make_safe<D>(smem + Lay::kVOff + sl * Lay::kSlot + (c % kSubs) * kSub, k0 + c * Lay::kVKeys, a.lo,
+                                a.s.len, lane);
+          if (c % kSubs == kSubs - 1 && ++sl == kVDepth) sl = 0;
+        }
         __syncwarp();
         if (lane == 0) {
           if (found) *reinterpret_cast<volatile int32_t*>(&B.poison[parts & 1]) = static_cast<int32_t>(parts) + 1;
@@ -551,13 +600,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int q4 = warp & 3, r = 32 * q4 + lane;        // lane quarter, row
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     const int G = p.group, tok = r / G, hd = r - tok * G;
-    const float c = p.scale_log2;
+    const float c = p.scale_log2, none = c < 0.f ? INFINITY : -INFINITY;
     uint32_t used[2] = {0, 0};  // operations seen of each S buffer
     uint32_t parts = 0, merges = 0;
     bool alive = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, kWaitNs));
-    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, abort, kWaitNs); };
     for (; alive && walk.next(work, p, a); ++parts) {
       const bool two = a.n1 > 0;
       const int tile_w = two ? w : 0;                     // row tile of this warp
@@ -573,6 +620,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       int mine = 0, last_b = 0;
       for (int op = w; op < ops; op += step, ++mine) {
         const int b = op & 1;
+        // (The mask's words come while the scores are awaited.)
+        const int32_t key = a.key0 + (two ? op >> 1 : op) * kTreeKeys;
+        const bool masked = a.masked(key);
+        uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bits[i] = valid ? tree_sees32(a.s, mask_row, first, key + 32 * i) : 0u;
+        }
         if (!(alive = wait(&B.s_full[b], used[b] & 1))) break;
         const int prev_b = last_b;
         last_b = b;
@@ -583,44 +638,35 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           mbar_arrive(&B.p_full[b]);
           continue;
         }
-        const int32_t key = a.key0 + (two ? op >> 1 : op) * kTreeKeys;
         const uint32_t s_col = lane_addr + Lay::kSCol + b * kTreeKeys;
-        const bool masked = a.masked(key);
-        uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) bits[i] = valid ? tree_sees32(a.s, mask_row, first, key + 32 * i) : 0u;
-        }
-        // A quarter of the row's scores, read twice (for the maximum, then for the
+        // A quarter of the row's scores, read twice (for the extremum, then for the
         // weights; the last two quarters stay): 128 of them would not leave room.
+        // The largest score under a negative scale is the smallest product.
         uint32_t sa[32], sb[32];
-        auto flip = [&](uint32_t (&x)[32]) {
-          if (p.sign) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] ^= p.sign;
-          }
-        };
-        auto most = [&](uint32_t (&x)[32], uint32_t seen) -> float {
-          flip(x);
-          if (!masked) return max_tree<32>(x);
+        auto most = [&](const uint32_t (&x)[32], uint32_t seen) -> float {
+          if (!masked) return c < 0.f ? extremum<32, false>(x) : extremum<32, true>(x);
           uint32_t y[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = seen >> i & 1u ? x[i] : 0xff800000u;  // -inf
-          return max_tree<32>(y);
+          for (int i = 0; i < 32; ++i) y[i] = seen & 1u << i ? x[i] : __float_as_uint(none);
+          return c < 0.f ? extremum<32, false>(y) : extremum<32, true>(y);
         };
         tmem_ld32(s_col, sa);
         tmem_ld32(s_col + 32, sb);
         tmem_wait_ld();
         tmem_loaded(sa);
         tmem_loaded(sb);
-        float mx = fmaxf(most(sa, bits[0]), most(sb, bits[1]));
+        float mx = most(sa, bits[0]), mx1 = most(sb, bits[1]);
+        mx = c < 0.f ? fminf(mx, mx1) : fmaxf(mx, mx1);
         tmem_ld32(s_col + 64, sa);
         tmem_ld32(s_col + 96, sb);
         tmem_wait_ld();
         tmem_loaded(sa);
         tmem_loaded(sb);
-        mx = fmax3(mx, most(sa, bits[2]), most(sb, bits[3]));
-        mx = mx == -INFINITY ? -INFINITY : mx * c;
+        mx1 = most(sa, bits[2]);
+        mx = c < 0.f ? fminf(mx, mx1) : fmaxf(mx, mx1);
+        mx1 = most(sb, bits[3]);
+        mx = c < 0.f ? fminf(mx, mx1) : fmaxf(mx, mx1);
+        mx = mx == none ? -INFINITY : mx * c;
         const float m_new = fmaxf(m_ref, mx);
         const bool grow = m_new > m_ref + 8.f;  // also for the first visible key
         const bool rescale = grow && m_ref != -INFINITY;
@@ -651,7 +697,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         uint64_t acc = f2_pack(0.f, 0.f);
         // P of a quarter, into columns 64 + 16 i of the buffer: over scores that are in
         // registers by then.
-        auto weights = [&](const uint32_t (&x)[32], int i, uint32_t seen) {
+        auto weights = [&](auto with_mask, const uint32_t (&x)[32], int i, uint32_t seen) {
           uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -661,27 +707,31 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             f2_unpack(x2, x0, x1);
             float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
             // (-inf times a scale of zero is NaN: the mask is applied to the weights.)
-            if (masked) {
-              p0 = seen >> (2 * k) & 1u ? p0 : 0.f;
-              p1 = seen >> (2 * k + 1) & 1u ? p1 : 0.f;
+            if constexpr (with_mask) {
+              p0 = seen & 1u << 2 * k ? p0 : 0.f;
+              p1 = seen & 2u << 2 * k ? p1 : 0.f;
             }
             acc = f2_add(acc, f2_pack(p0, p1));
             pk[k] = pack_bf16x2(p0, p1);
           }
           tmem_st16(s_col + 64 + 16 * i, pk);
         };
-        weights(sa, 2, bits[2]);
-        tmem_ld32(s_col, sa);
-        weights(sb, 3, bits[3]);
-        tmem_wait_ld();
-        tmem_loaded(sa);
-        tmem_ld32(s_col + 32, sb);
-        flip(sa);
-        weights(sa, 0, bits[0]);
-        tmem_wait_ld();
-        tmem_loaded(sb);
-        flip(sb);
-        weights(sb, 1, bits[1]);
+        auto all_weights = [&](auto with_mask) {
+          weights(with_mask, sa, 2, bits[2]);
+          tmem_ld32(s_col, sa);
+          weights(with_mask, sb, 3, bits[3]);
+          tmem_wait_ld();
+          tmem_loaded(sa);
+          tmem_ld32(s_col + 32, sb);
+          weights(with_mask, sa, 0, bits[0]);
+          tmem_wait_ld();
+          tmem_loaded(sb);
+          weights(with_mask, sb, 1, bits[1]);
+        };
+        if (masked)
+          all_weights(std::true_type{});
+        else
+          all_weights(std::false_type{});
         float a0, a1;
         f2_unpack(acc, a0, a1);
         l += a0 + a1;
@@ -892,8 +942,7 @@ int launch_d(const Plan& plan, const Args& a, cudaStream_t stream) {
   // A V stage in one page takes all its 64-dimension chunks in one box.
   p.v_4d = Lay::kChunks > 1 && p.box_rows_v == Lay::kVKeys ? 1 : 0;
   p.out_v8 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 ? 1 : 0;
-  p.scale_log2 = std::fabs(a.sm_scale) * 1.4426950408889634f;
-  p.sign = std::signbit(a.sm_scale) ? 0x80000000u : 0u;
+  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
   CUtensorMap tq, tk, tv;
   const uint64_t pool_rows = static_cast<uint64_t>(plan.num_pages) * plan.p;
   if (!make_tmap_3d(&tq, a.q, D, plan.hq, static_cast<uint64_t>(plan.total_q), G, p.per_tile) ||
