@@ -35,7 +35,8 @@
 #include <cuda.h>
 
 #include <algorithm>
-#include <type_traits>
+#include <cfloat>
+#include <cmath>
 
 #include "sm100_ptx.cuh"
 #include "tree.cuh"
@@ -243,7 +244,7 @@ __device__ __noinline__ bool make_safe(uint8_t* piece, int32_t key, int32_t lo, 
 // What make_safe took out of the part's tiles and this row sees, added to what was
 // stored of columns [c0, c1) (T: bf16 outputs or fp32 partials, the row's start).
 template <typename T>
-__device__ __noinline__ void add_unseen(const TreeParams& p, const Part& a, const uint64_t* mask_row, int32_t first,
+__device__ __noinline__ void add_unseen(const TreeParams& p, const Part a, const uint64_t* mask_row, int32_t first,
                                         int32_t d, int32_t c0, int32_t c1, T* row) {
   for (int32_t k0 = a.key0; k0 < a.key0 + a.n * kTreeKeys; k0 += kTreeKeys) {
     if (!a.masked(k0)) continue;
@@ -454,7 +455,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint64_t q_d0 = smem_desc(smem_addr(smem), 16, 1024);
     const uint64_t k_d0 = smem_desc(smem_addr(smem + Lay::kKOff), 16, 1024);
     const uint64_t v_d0 = smem_desc(smem_addr(smem + Lay::kVOff), Lay::kVKeys * 128, 1024);
-    uint32_t parts = 0, asked = 0, pv[2] = {0, 0};
+    uint32_t parts = 0, asked = 0, p_ph = 0;  // p_ph: a phase bit per S buffer
     int ks = 0, vs = 0;
     uint32_t kph = 0, vph = 0;
     bool alive = true;
@@ -509,8 +510,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         if (lane == 0) mbar_arrive(&B.v_ask);
       }
-      if (!wait(&B.p_full[b], pv[b] & 1)) return false;
-      ++pv[b];
+      if (!wait(&B.p_full[b], p_ph >> b & 1u)) return false;
+      p_ph ^= 1u << b;
       if (op == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
       if (masked && first) {
         if (!wait(&B.v_safe, asked & 1)) return false;
@@ -601,7 +602,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     const int G = p.group, tok = r / G, hd = r - tok * G;
     const float c = p.scale_log2, none = c < 0.f ? INFINITY : -INFINITY;
-    uint32_t used[2] = {0, 0};  // operations seen of each S buffer
+    uint32_t used = 0;  // operations seen of each S buffer, modulo 2: a bit each
     uint32_t parts = 0, merges = 0;
     bool alive = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, abort, kWaitNs); };
@@ -628,10 +629,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
           for (int i = 0; i < 4; ++i) bits[i] = valid ? tree_sees32(a.s, mask_row, first, key + 32 * i) : 0u;
         }
-        if (!(alive = wait(&B.s_full[b], used[b] & 1))) break;
+        if (!(alive = wait(&B.s_full[b], used >> b & 1u))) break;
         const int prev_b = last_b;
         last_b = b;
-        ++used[b];
+        used ^= 1u << b;
         tc_fence_after();
         if (!some) {  // no row of this warp is one: its P may be anything
           tc_fence_before();
@@ -641,30 +642,34 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t s_col = lane_addr + Lay::kSCol + b * kTreeKeys;
         // A quarter of the row's scores, read twice (for the extremum, then for the
         // weights; the last two quarters stay): 128 of them would not leave room.
-        // The largest score under a negative scale is the smallest product.
+        // The largest product under a negative scale is that of the smallest score.
+        // A masked score becomes the infinity whose product is -infinity.
         uint32_t sa[32], sb[32];
-        auto most = [&](const uint32_t (&x)[32], uint32_t seen) -> float {
-          if (!masked) return c < 0.f ? extremum<32, false>(x) : extremum<32, true>(x);
-          uint32_t y[32];
+        auto hide = [&](uint32_t (&x)[32], uint32_t seen) {
+          if (!masked) return;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = seen & 1u << i ? x[i] : __float_as_uint(none);
-          return c < 0.f ? extremum<32, false>(y) : extremum<32, true>(y);
+          for (int i = 0; i < 32; ++i) x[i] = seen & 1u << i ? x[i] : __float_as_uint(none);
+        };
+        auto most = [&](const uint32_t (&x)[32], const uint32_t (&y)[32]) -> float {
+          if (c < 0.f) return fminf(extremum<32, false>(x), extremum<32, false>(y));
+          return fmaxf(extremum<32, true>(x), extremum<32, true>(y));
         };
         tmem_ld32(s_col, sa);
         tmem_ld32(s_col + 32, sb);
         tmem_wait_ld();
         tmem_loaded(sa);
         tmem_loaded(sb);
-        float mx = most(sa, bits[0]), mx1 = most(sb, bits[1]);
-        mx = c < 0.f ? fminf(mx, mx1) : fmaxf(mx, mx1);
+        hide(sa, bits[0]);
+        hide(sb, bits[1]);
+        float mx = most(sa, sb);
         tmem_ld32(s_col + 64, sa);
         tmem_ld32(s_col + 96, sb);
         tmem_wait_ld();
         tmem_loaded(sa);
         tmem_loaded(sb);
-        mx1 = most(sa, bits[2]);
-        mx = c < 0.f ? fminf(mx, mx1) : fmaxf(mx, mx1);
-        mx1 = most(sb, bits[3]);
+        hide(sa, bits[2]);
+        hide(sb, bits[3]);
+        const float mx1 = most(sa, sb);
         mx = c < 0.f ? fminf(mx, mx1) : fmaxf(mx, mx1);
         mx = mx == none ? -INFINITY : mx * c;
         const float m_new = fmaxf(m_ref, mx);
@@ -672,7 +677,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const bool rescale = grow && m_ref != -INFINITY;
         if (__any_sync(0xffffffffu, rescale)) {
           // O holds earlier tiles: after the last of their products.
-          if (!(alive = wait(&B.o_done[prev_b], (used[prev_b] - (prev_b == b ? 2 : 1)) & 1))) break;
+          if (!(alive = wait(&B.o_done[prev_b], (used >> prev_b & 1u) ^ (prev_b == b ? 0u : 1u)))) break;
           tc_fence_after();
           const float f = rescale ? fast_exp2(m_ref - m_new) : 1.f;
           const uint32_t o_col = lane_addr + (kStreams == 2 ? w * D : 0);
@@ -697,7 +702,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         uint64_t acc = f2_pack(0.f, 0.f);
         // P of a quarter, into columns 64 + 16 i of the buffer: over scores that are in
         // registers by then.
-        auto weights = [&](auto with_mask, const uint32_t (&x)[32], int i, uint32_t seen) {
+        auto weights = [&](const uint32_t (&x)[32], int i) {
           uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -705,33 +710,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, nm2);
             float x0, x1;
             f2_unpack(x2, x0, x1);
-            float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-            // (-inf times a scale of zero is NaN: the mask is applied to the weights.)
-            if constexpr (with_mask) {
-              p0 = seen & 1u << 2 * k ? p0 : 0.f;
-              p1 = seen & 2u << 2 * k ? p1 : 0.f;
-            }
+            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
             acc = f2_add(acc, f2_pack(p0, p1));
             pk[k] = pack_bf16x2(p0, p1);
           }
           tmem_st16(s_col + 64 + 16 * i, pk);
         };
-        auto all_weights = [&](auto with_mask) {
-          weights(with_mask, sa, 2, bits[2]);
-          tmem_ld32(s_col, sa);
-          weights(with_mask, sb, 3, bits[3]);
-          tmem_wait_ld();
-          tmem_loaded(sa);
-          tmem_ld32(s_col + 32, sb);
-          weights(with_mask, sa, 0, bits[0]);
-          tmem_wait_ld();
-          tmem_loaded(sb);
-          weights(with_mask, sb, 1, bits[1]);
-        };
-        if (masked)
-          all_weights(std::true_type{});
-        else
-          all_weights(std::false_type{});
+        weights(sa, 2);
+        tmem_ld32(s_col, sa);
+        weights(sb, 3);
+        tmem_wait_ld();
+        tmem_loaded(sa);
+        tmem_ld32(s_col + 32, sb);
+        hide(sa, bits[0]);
+        weights(sa, 0);
+        tmem_wait_ld();
+        tmem_loaded(sb);
+        hide(sb, bits[1]);
+        weights(sb, 1);
         float a0, a1;
         f2_unpack(acc, a0, a1);
         l += a0 + a1;
@@ -741,7 +737,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       if (!alive) break;
       // The part's rows: this stream's, or half the columns of both streams' sum.
-      if (mine > 0 && !(alive = wait(&B.o_done[last_b], (used[last_b] - 1) & 1))) break;
+      if (mine > 0 && !(alive = wait(&B.o_done[last_b], (used >> last_b & 1u) ^ 1u))) break;
       tc_fence_after();
       const bool merge = kStreams == 2 && !two;
       float f0 = 1.f, f1 = 0.f, m = m_ref, sum = l;  // O = f0 O_0 + f1 O_1
@@ -942,7 +938,9 @@ int launch_d(const Plan& plan, const Args& a, cudaStream_t stream) {
   // A V stage in one page takes all its 64-dimension chunks in one box.
   p.v_4d = Lay::kChunks > 1 && p.box_rows_v == Lay::kVKeys ? 1 : 0;
   p.out_v8 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 ? 1 : 0;
-  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  // (Not zero: the infinity of a masked score times zero would be NaN.  Under the
+  // smallest number no product differs from zero.)
+  p.scale_log2 = std::fabs(a.sm_scale) < FLT_MIN ? FLT_MIN : a.sm_scale * 1.4426950408889634f;
   CUtensorMap tq, tk, tv;
   const uint64_t pool_rows = static_cast<uint64_t>(plan.num_pages) * plan.p;
   if (!make_tmap_3d(&tq, a.q, D, plan.hq, static_cast<uint64_t>(plan.total_q), G, p.per_tile) ||
