@@ -233,15 +233,16 @@ __device__ __forceinline__ void mma_ss_chunk(uint32_t d_tmem, uint64_t a, uint64
       "l"(a), "l"(b), "r"(idesc), "r"(acc0)
       : "memory");
 }
-__device__ __forceinline__ void mma_ss_2chunks(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+__device__ __forceinline__ void mma_ss_2chunks(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t acc0) {
   asm volatile(
-      "{\n .reg .pred e;\n .reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n"
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n .reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n"
       " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n add.s64 a4, %1, 1024;\n"
       " add.s64 a5, %1, 1026;\n add.s64 a6, %1, 1028;\n add.s64 a7, %1, 1030;\n"
       " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n add.s64 b4, %2, 1024;\n"
       " add.s64 b5, %2, 1026;\n add.s64 b6, %2, 1028;\n add.s64 b7, %2, 1030;\n"
       " elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n"
@@ -249,7 +250,7 @@ __device__ __forceinline__ void mma_ss_2chunks(uint32_t d_tmem, uint64_t a, uint
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, 1;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, 1;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, 1;\n}\n" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc)
+      "l"(a), "l"(b), "r"(idesc), "r"(acc0)
       : "memory");
 }
 // D (+)= A_i[tmem] * B_i over 128 keys, 16 a step (8 columns of A, 2048 bytes of B);
@@ -274,6 +275,22 @@ __device__ __forceinline__ void mma_ts_128keys(uint32_t d_tmem, uint32_t a, uint
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, 1;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, 1;\n}\n" ::"r"(d_tmem),
       "r"(a), "l"(b), "r"(idesc), "r"(acc0), "n"(kHalf)
+      : "memory");
+}
+
+// The same over two pieces of 32 keys, 16 KB apart.
+__device__ __forceinline__ void mma_ts_2x32keys(uint32_t d_tmem, uint32_t a, uint64_t b, uint32_t idesc,
+                                                uint32_t acc0) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n setp.ne.b32 p, %4, 0;\n"
+      " add.s64 b1, %2, 128;\n add.s64 b2, %2, 1024;\n add.s64 b3, %2, 1152;\n"
+      " add.s32 a1, %1, 8;\n add.s32 a2, %1, 16;\n add.s32 a3, %1, 24;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n}\n" ::"r"(d_tmem),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc0)
       : "memory");
 }
 

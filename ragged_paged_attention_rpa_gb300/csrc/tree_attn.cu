@@ -19,14 +19,14 @@
 //   end (by the maxima and sums that they swap through shared memory).
 // At head_dim 256 one O fills half of tensor memory: one stream, two S buffers.
 //
-// Warps: 0 copies Q and K, 1 copies V (TMA boxes through the page table, 16 KB
-// stages), 2 issues the MMAs, 3 makes V safe (below), 4 on are the softmax
-// warpgroups, a thread per row; each writes its rows at the part's end while the
+// Warps: 0 copies Q, K and V (TMA boxes through the page table, into one ring in the
+// order of their use), 2 issues the MMAs, 1 and 3 make V safe (below), 4 on are the
+// softmax warpgroups, a thread per row; each writes its rows at the part's end while the
 // copies run on into the ring.
 //
 // Masks are looked up where a tile holds nodes or a window's edge; 128 bits a row.
-// A product gives 0 * NaN to the rows that do not see a key, so in those tiles warp
-// 3 goes over V before the MMA reads it: rows of keys that no node sees become zero,
+// A product gives 0 * NaN to the rows that do not see a key, so in those tiles warps
+// 1 and 3 go over V before the MMA reads it: rows of keys that no node sees become zero,
 // and of the others each NaN or infinity, which the rows that see it then get back
 // from memory after they are written (add_unseen).
 //
@@ -37,6 +37,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "sm100_ptx.cuh"
 #include "tree.cuh"
@@ -91,14 +92,13 @@ struct Layout {
   static constexpr int kThreads = 128 + 128 * kStreams;
   static constexpr int kChunks = D / 64;         // 128-byte pieces of a row; 16 KB pieces of a tile, of K and of V
   static constexpr int kVKeys = 8192 / D;        // keys of such a piece of V
-  // Ring slots: a tile of 64 or 128 dimensions, a quarter of one of 256 (whose MMAs
-  // start before all of it has landed); their number for K and V.
-  static constexpr int kSubs = D == 128 ? 2 : 1, kSlots = kChunks / kSubs, kSlot = kSubs * kSub;
-  static constexpr int kKDepth = D == 64 ? 6 : D == 128 ? 2 : 5, kVDepth = D == 64 ? 6 : D == 128 ? 3 : 5;
+  // One ring for K and V, filled in the order in which the MMAs take them: a slot is a
+  // tile of K or of V, or half of one of 256 dimensions.
+  static constexpr int kSubs = D == 64 ? 1 : 2, kSlots = kChunks / kSubs, kSlot = kSubs * kSub;
+  static constexpr int kDepth = D == 64 ? 12 : 5;
   static constexpr int kQTile = kTreeRows * D * 2;
-  static constexpr int kKOff = kStreams * kQTile;
-  static constexpr int kVOff = kKOff + kKDepth * kSlot;
-  static constexpr int kBarOff = kVOff + kVDepth * kSlot;
+  static constexpr int kRingOff = kStreams * kQTile;
+  static constexpr int kBarOff = kRingOff + kDepth * kSlot;
   static constexpr int kXchOff = kBarOff + 512;  // [stream][row] (maximum, sum)
   static constexpr int kUsed = kXchOff + (kStreams == 2 ? 2 * kTreeRows * 8 : 0);
   static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;  // one CTA per SM
@@ -111,15 +111,16 @@ struct Layout {
 
 struct Barriers {
   uint64_t q_full, q_empty;
-  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
-  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t full[12], empty[12];
+  uint64_t s_full[2], p_full[2];
+  uint64_t o_done[2];       // one stream: a product of each S buffer; two: [0], the part's products
   uint64_t o_free;          // every row of the part's O has been read
   uint64_t xch;             // the streams' maxima and sums are posted
   uint64_t v_ask, v_safe;   // a masked tile's V has landed / may be read
   uint64_t fin;
   uint32_t tmem_base;
   int abort;
-  int32_t poison[2];        // 1 + the part of this parity in which warp 3 took something out
+  int32_t poison[2];        // 1 + the part of this parity in which something was taken out of V
 };
 static_assert(sizeof(Barriers) <= 512, "barrier block");
 
@@ -308,6 +309,19 @@ __device__ __forceinline__ void store32(void* dst, bool whole, const uint32_t (&
   }
 }
 
+// The ring's next slot and its phase.
+template <int kDepth>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == kDepth) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 template <int D, int N>
 __global__ void __launch_bounds__(Layout<D>::kThreads, 1)
 tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -315,7 +329,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                  const __grid_constant__ TreeWork<N> work) {
   using Lay = Layout<D>;
   constexpr int kChunks = Lay::kChunks, kStreams = Lay::kStreams, kSubs = Lay::kSubs, kSlots = Lay::kSlots;
-  constexpr int kKDepth = Lay::kKDepth, kVDepth = Lay::kVDepth;
+  constexpr int kDepth = Lay::kDepth;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_addr(smem) & 1023u) {
     if (threadIdx.x == 0) report_error(p.ws, RPA_DEVERR_LAUNCH, blockIdx.x);
@@ -329,22 +343,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (threadIdx.x == 0) {
     mbar_init(&B.q_full, 1);
     mbar_init(&B.q_empty, 1);
-    for (int i = 0; i < 6; ++i) {
-      mbar_init(&B.k_full[i], 1);
-      mbar_init(&B.k_empty[i], 1);
-      mbar_init(&B.v_full[i], 1);
-      mbar_init(&B.v_empty[i], 1);
+    for (int i = 0; i < kDepth; ++i) {
+      mbar_init(&B.full[i], 1);
+      mbar_init(&B.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.s_full[i], 1);
-      mbar_init(&B.p_full[i], 128);
+      mbar_init(&B.p_full[i], 4);
       mbar_init(&B.o_done[i], 1);
       B.poison[i] = 0;
     }
-    mbar_init(&B.o_free, 128 * kStreams);
-    mbar_init(&B.xch, 256);
+    mbar_init(&B.o_free, 4 * kStreams);
+    mbar_init(&B.xch, 8);
     mbar_init(&B.v_ask, 1);
-    mbar_init(&B.v_safe, 1);
+    mbar_init(&B.v_safe, 2);
     mbar_init(&B.fin, 1);
     B.abort = 0;
     fence_barrier_init();
@@ -361,31 +373,80 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = B.tmem_base;
   Walk<D, N> walk(work);
-  Part a;
-  if (warp <= 1) {
+  Part a{};
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, abort, kWaitNs); };
+  if (warp == 0) {
     // ------------------------------------------------------------ copies
-    const bool is_k = warp == 0;
-    uint64_t* full = is_k ? B.k_full : B.v_full;
-    uint64_t* empty = is_k ? B.k_empty : B.v_empty;
-    uint8_t* ring = smem + (is_k ? Lay::kKOff : Lay::kVOff);
-    const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
-    const int rows = is_k ? p.box_rows_k : p.box_rows_v;
-    const int nbox = (is_k ? kTreeKeys : Lay::kVKeys) / rows;  // boxes of 16 KB
-    const int depth = is_k ? kKDepth : kVDepth;
+    const int rows_k = p.box_rows_k, rows_v = p.box_rows_v;
+    const int nk = kTreeKeys / rows_k, nv = Lay::kVKeys / rows_v;  // boxes of 16 KB
     const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.per_tile) * 128u * kChunks;
-    int sl = 0;       // next slot
-    uint32_t ph = 0;  // and its phase
-    uint32_t C = 0, parts = 0, issued_q = 0;
+    Ring<kDepth> ring;
+    uint32_t filled = 0, parts = 0, issued_q = 0;
     bool alive = true;
+    // The next slot, empty, with its bytes announced.
+    auto take = [&]() -> bool {
+      if (lane == 0) alive = mbar_wait(&B.empty[ring.slot], ring.phase ^ 1, abort, kWaitNs);
+      alive = __shfl_sync(0xffffffffu, alive, 0);
+      if (!alive) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&B.full[ring.slot], Lay::kSlot);
+      ++filled;
+      __syncwarp();
+      return true;
+    };
+    // A tile's source rows, one box a lane: of K, and of each 16 KB of V.
+    struct Rows {
+      int32_t k, v[kChunks];
+    };
+    auto rows_of = [&](int j) -> Rows {
+      Rows r;
+      const int32_t k0 = a.key0 + j * kTreeKeys;
+      r.k = lane < nk ? box_row(p, a, k0 + lane * rows_k, rows_k) : 0;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        r.v[c] = lane < nv ? box_row(p, a, k0 + c * Lay::kVKeys + lane * rows_v, rows_v) : 0;
+      return r;
+    };
+    auto copy_k = [&](const Rows& r) -> bool {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (c % kSubs == 0 && !take()) return false;
+        if (lane < nk)
+          tma_load_3d(smem + Lay::kRingOff + ring.slot * Lay::kSlot + (c % kSubs) * kSub + lane * rows_k * 128, &tm_k,
+                      &B.full[ring.slot], c * 64, a.head, r.k);
+        if (c % kSubs == kSubs - 1) ring.step();
+      }
+      return true;
+    };
+    auto copy_v = [&](const Rows& r) -> bool {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (c % kSubs == 0 && !take()) return false;
+        uint8_t* dst = smem + Lay::kRingOff + ring.slot * Lay::kSlot + (c % kSubs) * kSub + lane * rows_v * 128;
+        if (lane < nv) {
+          if (p.v_4d) {
+            tma_load_4d(dst, &tm_v, &B.full[ring.slot], 0, a.head, r.v[c], 0);
+          } else {
+#pragma unroll
+            for (int x = 0; x < kChunks; ++x)
+              tma_load_3d(dst + x * Lay::kVKeys * 128, &tm_v, &B.full[ring.slot], x * 64, a.head, r.v[c]);
+          }
+        }
+        if (c % kSubs == kSubs - 1) ring.step();
+      }
+      return true;
+    };
     for (; alive && walk.next(work, p, a); ++parts) {
-      if (is_k && lane == 0) {
+      const bool two = a.n1 > 0;
+      // (Looked up before they are wanted.)
+      Rows now = rows_of(0), next = now;
+      if (lane == 0) {
         // (The device's lengths, once a request.)
         if (a.head == 0 && a.node0 == 0 && a.key0 + a.n * kTreeKeys >= a.s.len)
           tree_check_lengths(a.s, p.cu_q_lens, p.kv_lens, p.ws);
         alive = mbar_wait(&B.q_empty, (parts & 1) ^ 1, abort, kWaitNs);
         if (alive) {
-          mbar_arrive_expect_tx(&B.q_full, q_bytes * (a.n1 > 0 ? 2u : 1u));
-          for (int t = 0; t < (a.n1 > 0 ? 2 : 1); ++t)
+          mbar_arrive_expect_tx(&B.q_full, two ? 2 * q_bytes : q_bytes);
+          for (int t = 0; t < (two ? 2 : 1); ++t)
             for (int c = 0; c < kChunks; ++c)
               tma_load_3d(smem + t * Lay::kQTile + c * (kTreeRows * 128), &tm_q, &B.q_full, c * 64,
                           a.head * p.group, a.s.q0 + a.node0 + t * p.per_tile);
@@ -393,173 +454,199 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
       }
       alive = __shfl_sync(0xffffffffu, alive, 0);
-      // A tile's source rows are looked up a tile ahead (lane < nbox: one box a stage).
-      auto tile_rows = [&](int j, int32_t (&rw)[kChunks]) {
-        const int32_t k0 = a.key0 + j * kTreeKeys;
-        if (is_k) {
-          const int32_t r = lane < nbox ? box_row(p, a, k0 + lane * rows, rows) : 0;
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) rw[c] = r;
-        } else {
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            rw[c] = lane < nbox ? box_row(p, a, k0 + c * Lay::kVKeys + lane * rows, rows) : 0;
-        }
-      };
-      int32_t rcur[kChunks], rnext[kChunks];
-      tile_rows(0, rcur);
+      // K runs a tile ahead of V where a score tile runs ahead of the product of the
+      // tile before; with two row tiles it is the second one's that does.
+      if (alive) alive = copy_k(now);
       for (int j = 0; j < a.n && alive; ++j) {
-        if (j + 1 < a.n) tile_rows(j + 1, rnext);
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          if (c % kSubs == 0) {
-            if (lane == 0) alive = mbar_wait(&empty[sl], ph ^ 1, abort, kWaitNs);
-            alive = __shfl_sync(0xffffffffu, alive, 0);
-            if (!alive) break;
-            if (lane == 0) mbar_arrive_expect_tx(&full[sl], Lay::kSlot);
-            ++C;
-            __syncwarp();
-          }
-          if (lane < nbox) {
-            uint8_t* dst = ring + sl * Lay::kSlot + (c % kSubs) * kSub + lane * rows * 128;
-            if (is_k) {
-              tma_load_3d(dst, tm, &full[sl], c * 64, a.head, rcur[c]);
-            } else if (p.v_4d) {
-              tma_load_4d(dst, tm, &full[sl], 0, a.head, rcur[c], 0);
-            } else {
-              for (int x = 0; x < kChunks; ++x)
-                tma_load_3d(dst + x * Lay::kVKeys * 128, tm, &full[sl], x * 64, a.head, rcur[c]);
-            }
-          }
-          if (c % kSubs == kSubs - 1 && ++sl == depth) {
-            sl = 0;
-            ph ^= 1;
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) rcur[c] = rnext[c];
+        if (j + 1 < a.n) next = rows_of(j + 1);
+        if (!two && j + 1 < a.n && !copy_k(next)) break;
+        if (!copy_v(now)) break;
+        if (two && j + 1 < a.n && !copy_k(next)) break;
+        now = next;
       }
     }
     if (!alive && lane == 0) {
       // Every copy lands before its shared memory goes.
       report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
       int none = 0;
-      for (uint32_t t = C > static_cast<uint32_t>(depth) ? C - depth : 0; t < C; ++t)
-        mbar_wait(&full[t % depth], (t / depth) & 1, &none, kDrainNs);
+      for (uint32_t t = filled > kDepth ? filled - kDepth : 0; t < filled; ++t)
+        mbar_wait(&B.full[t % kDepth], (t / kDepth) & 1, &none, kDrainNs);
       if (issued_q > 0) mbar_wait(&B.q_full, (issued_q - 1) & 1, &none, kDrainNs);
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ MMAs
+    // Between two score tiles and two products this warp has 1024 cycles of the tensor
+    // cores (D = 128), and its instructions are fetched anew each time it goes on (the
+    // softmax warps' code takes the caches): so few of them, in straight lines, each S
+    // buffer with code of its own.
     constexpr uint32_t kIdS = idesc_bf16(kTreeKeys, 0), kIdPV = idesc_bf16(D, 1);
     // Operands differ from these in the start address alone (see prefill_tc.cu).
     const uint64_t q_d0 = smem_desc(smem_addr(smem), 16, 1024);
-    const uint64_t k_d0 = smem_desc(smem_addr(smem + Lay::kKOff), 16, 1024);
-    const uint64_t v_d0 = smem_desc(smem_addr(smem + Lay::kVOff), Lay::kVKeys * 128, 1024);
+    const uint64_t k_d0 = smem_desc(smem_addr(smem + Lay::kRingOff), 16, 1024);
+    const uint64_t v_d0 = smem_desc(smem_addr(smem + Lay::kRingOff), Lay::kVKeys * 128, 1024);
+    Ring<kDepth> ring;
     uint32_t parts = 0, asked = 0, p_ph = 0;  // p_ph: a phase bit per S buffer
-    int ks = 0, vs = 0;
-    uint32_t kph = 0, vph = 0;
     bool alive = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, abort, kWaitNs); };
-    auto step = [&](int& sl, uint32_t& ph, int depth) {
-      if (++sl == depth) {
-        sl = 0;
-        ph ^= 1;
-      }
-    };
-    // S of operation `op` (row tile `t` of Q) from the next K tile; `first`, `last`: of
-    // its uses, after which it is given back.
-    auto issue_s = [&](int op, int t, bool first, bool last) -> bool {
-      const uint32_t sc = tmem + Lay::kSCol + (op & 1) * kTreeKeys;
+    // S into buffer b from the K tile in `slot` (or the next slots) and row tile t.
+    auto mma_s = [&](auto bc, int t, int slot) {
+      constexpr int b = decltype(bc)::value;
+      const uint32_t sc = tmem + Lay::kSCol + b * kTreeKeys;
       const uint64_t qd = q_d0 + static_cast<uint64_t>(t * (Lay::kQTile >> 4));
-      if constexpr (kSlots == 1) {
-        if (first && !wait(&B.k_full[ks], kph)) return false;
-        tc_fence_after();
-        const uint64_t kd = k_d0 + static_cast<uint64_t>(ks * (Lay::kSlot >> 4));
-        if constexpr (kSubs == 2)
-          mma_ss_2chunks(sc, qd, kd, kIdS);
-        else
-          mma_ss_chunk(sc, qd, kd, kIdS, 0);
-        if (last) {
-          mma_commit(&B.k_empty[ks]);
-          step(ks, kph, kKDepth);
-        }
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < kSlots; ++c) {
-          if (!wait(&B.k_full[ks], kph)) return false;
-          tc_fence_after();
-          mma_ss_chunk(sc, qd + static_cast<uint64_t>(c * (kSub >> 4)),
-                       k_d0 + static_cast<uint64_t>(ks * (Lay::kSlot >> 4)), kIdS, c > 0 ? 1u : 0u);
-          mma_commit(&B.k_empty[ks]);
-          step(ks, kph, kKDepth);
-        }
-      }
-      mma_commit(&B.s_full[op & 1]);
-      return true;
+      const uint64_t kd = k_d0 + static_cast<uint64_t>(slot * (Lay::kSlot >> 4));
+      if constexpr (D == 64)
+        mma_ss_chunk(sc, qd, kd, kIdS, 0);
+      else
+        mma_ss_2chunks(sc, qd, kd, kIdS, 0);
     };
-    // O += P V of operation `op`; `fresh`: its stream's first in the part; `first`,
-    // `last`: the V tile's uses; `masked`: it has to be made safe before the first.
-    auto issue_pv = [&](int op, bool fresh, bool first, bool last, bool masked) -> bool {
-      const int b = op & 1;
-      if (masked && first) {
-        int sl = vs;
-        uint32_t ph = vph;
-        for (int c = 0; c < kSlots; ++c) {
-          if (!wait(&B.v_full[sl], ph)) return false;
-          step(sl, ph, kVDepth);
-        }
-        if (lane == 0) mbar_arrive(&B.v_ask);
-      }
-      if (!wait(&B.p_full[b], p_ph >> b & 1u)) return false;
+    // O += P V, P in buffer b, V in `slot`; `acc` 0: the stream's first in the part.
+    auto mma_pv = [&](auto bc, int slot, uint32_t acc) {
+      constexpr int b = decltype(bc)::value;
+      mma_ts_128keys<D == 64 ? 512 : kSub / 16>(tmem + b * D, tmem + Lay::kSCol + b * kTreeKeys + 64,
+                                                v_d0 + static_cast<uint64_t>(slot * (Lay::kSlot >> 4)), kIdPV, acc);
+    };
+    auto wait_p = [&](auto bc) -> bool {
+      constexpr int b = decltype(bc)::value;
+      const bool ok = wait(&B.p_full[b], p_ph >> b & 1u);
       p_ph ^= 1u << b;
-      if (op == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
-      if (masked && first) {
-        if (!wait(&B.v_safe, asked & 1)) return false;
-        ++asked;
-      }
-      const uint32_t p_col = tmem + Lay::kSCol + b * kTreeKeys + 64;
-      const uint32_t o_col = tmem + (kStreams == 2 ? b * D : 0);
-      if constexpr (kSlots == 1) {
-        if (first && !wait(&B.v_full[vs], vph)) return false;
-        tc_fence_after();
-        mma_ts_128keys<kSubs == 2 ? kSub / 16 : 512>(o_col, p_col, v_d0 + static_cast<uint64_t>(vs * (Lay::kSlot >> 4)),
-                                                     kIdPV, fresh ? 0u : 1u);
-        if (last) {
-          mma_commit(&B.v_empty[vs]);
-          step(vs, vph, kVDepth);
-        }
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < kSlots; ++c) {
-          if (!wait(&B.v_full[vs], vph)) return false;
-          tc_fence_after();
-          // Two MMAs of 16 keys (P: 8 columns, V: 2048 B apart).
-          static_assert(kSlots == 1 || Lay::kVKeys == 32, "");
-          const uint64_t vd = v_d0 + static_cast<uint64_t>(vs * (Lay::kSlot >> 4));
-          const uint32_t pc = p_col + c * 16;
-          mma_ts2_commit(o_col, pc, pc + 8, vd, vd + 128, kIdPV, !fresh || c > 0 ? 1u : 0u, &B.v_empty[vs]);
-          step(vs, vph, kVDepth);
-        }
-      }
-      mma_commit(&B.o_done[b]);
+      return ok;
+    };
+    // A masked tile's V: asked for once it has landed, used once it is safe.
+    auto ask = [&]() -> bool {
+      Ring<kDepth> r = ring;
+      for (int c = 0; c < kSlots; ++c, r.step())
+        if (!wait(&B.full[r.slot], r.phase)) return false;
+      if (lane == 0) mbar_arrive(&B.v_ask);
       return true;
     };
-    for (; alive && walk.next(work, p, a); ++parts) {
-      alive = wait(&B.q_full, parts & 1);
-      const bool two = a.n1 > 0;
-      const int ops = two ? 2 * a.n : a.n;
-      auto s_of = [&](int op) { return issue_s(op, two ? op & 1 : 0, !two || !(op & 1), !two || (op & 1)); };
-      if (alive) alive = s_of(0);
-      if (ops == 1) mma_commit(&B.q_empty);
-      for (int op = 0; op < ops && alive; ++op) {
-        if (op + 1 < ops) {
-          if (!(alive = s_of(op + 1))) break;
-          if (op + 2 == ops) mma_commit(&B.q_empty);
+    auto safe = [&]() -> bool { return wait(&B.v_safe, asked++ & 1); };
+    using B0 = std::integral_constant<int, 0>;
+    using B1 = std::integral_constant<int, 1>;
+    while (alive && walk.next(work, p, a)) {
+      if (!(alive = wait(&B.q_full, parts & 1))) break;
+      auto masked = [&](int j) { return a.masked(a.key0 + j * kTreeKeys); };
+      alive = [&]() -> bool {
+        if constexpr (kStreams == 2) {
+          if (a.n1 > 0) {
+            // Two row tiles: S(0, j), then S(1, j), O_0 += P(0, j) V(j), S(0, j + 1),
+            // O_1 += P(1, j) V(j).
+            if (!wait(&B.full[ring.slot], ring.phase)) return false;
+            tc_fence_after();
+            int ks = ring.slot;
+            ring.step();
+            mma_s(B0{}, 0, ks);
+            mma_commit(&B.s_full[0]);
+#pragma unroll 1
+            for (int j = 0;; ++j) {
+              const bool more = j + 1 < a.n;
+              mma_s(B1{}, 1, ks);
+              mma_commit(&B.s_full[1]);
+              mma_commit(&B.empty[ks]);
+              if (!more) mma_commit(&B.q_empty);
+              if (masked(j) && (!ask() || !safe())) return false;
+              if (!wait(&B.full[ring.slot], ring.phase)) return false;
+              if (!wait_p(B0{})) return false;
+              if (j == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
+              tc_fence_after();
+              const int vs = ring.slot;
+              ring.step();
+              mma_pv(B0{}, vs, j > 0);
+              if (more) {
+                if (!wait(&B.full[ring.slot], ring.phase)) return false;
+                tc_fence_after();
+                ks = ring.slot;
+                ring.step();
+                mma_s(B0{}, 0, ks);
+                mma_commit(&B.s_full[0]);
+              }
+              if (!wait_p(B1{})) return false;
+              tc_fence_after();
+              mma_pv(B1{}, vs, j > 0);
+              mma_commit(&B.empty[vs]);
+              if (!more) break;
+            }
+            mma_commit(&B.o_done[0]);
+            return true;
+          }
+          // One row tile, its key tiles by turns: S(j + 1), O_(j % 2) += P(j) V(j).
+          auto score = [&](auto bc) -> bool {
+            if (!wait(&B.full[ring.slot], ring.phase)) return false;
+            tc_fence_after();
+            mma_s(bc, 0, ring.slot);
+            mma_commit(&B.s_full[decltype(bc)::value]);
+            mma_commit(&B.empty[ring.slot]);
+            ring.step();
+            return true;
+          };
+          auto product = [&](auto bc, int j) -> bool {
+            if (masked(j) && (!ask() || !safe())) return false;
+            if (!wait(&B.full[ring.slot], ring.phase)) return false;
+            if (!wait_p(bc)) return false;
+            if (j == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
+            tc_fence_after();
+            mma_pv(bc, ring.slot, j > 1);
+            mma_commit(&B.empty[ring.slot]);
+            ring.step();
+            return true;
+          };
+          if (!score(B0{})) return false;
+          if (a.n == 1) mma_commit(&B.q_empty);
+#pragma unroll 1
+          for (int j = 0; j < a.n; j += 2) {
+            if (j + 1 < a.n && !score(B1{})) return false;
+            if (j + 2 == a.n) mma_commit(&B.q_empty);
+            if (!product(B0{}, j)) return false;
+            if (j + 1 >= a.n) break;
+            if (j + 2 < a.n && !score(B0{})) return false;
+            if (j + 3 == a.n) mma_commit(&B.q_empty);
+            if (!product(B1{}, j + 1)) return false;
+          }
+          mma_commit(&B.o_done[0]);
+          return true;
+        } else {
+          // One stream, tiles in halves: S(j + 1) into the other buffer, O += P(j) V(j).
+          auto score = [&](int b) -> bool {
+#pragma unroll
+            for (int h = 0; h < kSlots; ++h) {
+              if (!wait(&B.full[ring.slot], ring.phase)) return false;
+              tc_fence_after();
+              mma_ss_2chunks(tmem + Lay::kSCol + b * kTreeKeys, q_d0 + static_cast<uint64_t>(h * (2 * kSub >> 4)),
+                             k_d0 + static_cast<uint64_t>(ring.slot * (Lay::kSlot >> 4)), kIdS, h > 0 ? 1u : 0u);
+              mma_commit(&B.empty[ring.slot]);
+              ring.step();
+            }
+            mma_commit(&B.s_full[b]);
+            return true;
+          };
+          auto product = [&](int b, int j) -> bool {
+            if (masked(j) && (!ask() || !safe())) return false;
+            if (!wait(&B.p_full[b], p_ph >> b & 1u)) return false;
+            p_ph ^= 1u << b;
+            if (j == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
+#pragma unroll
+            for (int h = 0; h < kSlots; ++h) {
+              if (!wait(&B.full[ring.slot], ring.phase)) return false;
+              tc_fence_after();
+              mma_ts_2x32keys(tmem, tmem + Lay::kSCol + b * kTreeKeys + 64 + 32 * h,
+                              v_d0 + static_cast<uint64_t>(ring.slot * (Lay::kSlot >> 4)), kIdPV,
+                              j > 0 || h > 0 ? 1u : 0u);
+              mma_commit(&B.empty[ring.slot]);
+              ring.step();
+            }
+            mma_commit(&B.o_done[b]);
+            return true;
+          };
+          if (!score(0)) return false;
+          if (a.n == 1) mma_commit(&B.q_empty);
+#pragma unroll 1
+          for (int j = 0; j < a.n; ++j) {
+            if (j + 1 < a.n && !score((j + 1) & 1)) return false;
+            if (j + 2 == a.n) mma_commit(&B.q_empty);
+            if (!product(j & 1, j)) return false;
+          }
+          return true;
         }
-        const int tile = two ? op >> 1 : op;
-        alive = issue_pv(op, op < kStreams, !two || !(op & 1), !two || (op & 1),
-                         a.masked(a.key0 + tile * kTreeKeys));
-      }
+      }();
+      ++parts;
     }
     // Every MMA issued finishes before tensor memory is released.
     mma_commit(&B.fin);
@@ -567,32 +654,33 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     mbar_wait(&B.fin, 0, &none, kDrainNs);
     __syncwarp();
     if (!alive && lane == 0) report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
-  } else if (warp == 3) {
+  } else if (warp < 4) {
     // ------------------------------------------------------------ V made safe
+    // Warps 1 and 3, every second 16 KB each.
+    const int half = warp >> 1;
     uint32_t asked = 0, parts = 0;
-    int sl = 0;  // slot of the next tile's V
+    int base = 0;  // ring slot of the part's first tile
     bool alive = true;
     for (; alive && walk.next(work, p, a); ++parts) {
       for (int j = 0; j < a.n; ++j) {
         const int32_t k0 = a.key0 + j * kTreeKeys;
-        if (!a.masked(k0)) {
-          if ((sl += kSlots) >= kVDepth) sl -= kVDepth;
-          continue;
-        }
-        if (!(alive = warp_wait(&B.v_ask, asked & 1, abort, kWaitNs))) break;
+        if (!a.masked(k0)) continue;
+        if (!(alive = wait(&B.v_ask, asked & 1))) break;
         ++asked;
+        // The tile's place among the part's (see the copies).
+        const int tile = a.n1 > 0 || j == a.n - 1 ? 2 * j + 1 : 2 * j + 2;
         bool found = false;
-        for (int c = 0; c < kChunks; ++c) {
-          found |= make_safe<D>(smem + Lay::kVOff + sl * Lay::kSlot + (c % kSubs) * kSub, k0 + c * Lay::kVKeys, a.lo,
-                                a.s.len, lane);
-          if (c % kSubs == kSubs - 1 && ++sl == kVDepth) sl = 0;
-        }
+        for (int c = half; c < kChunks; c += 2)
+          found |= make_safe<D>(smem + Lay::kRingOff + (base + tile * kSlots + c / kSubs) % kDepth * Lay::kSlot +
+                                    (c % kSubs) * kSub,
+                                k0 + c * Lay::kVKeys, a.lo, a.s.len, lane);
         __syncwarp();
         if (lane == 0) {
           if (found) *reinterpret_cast<volatile int32_t*>(&B.poison[parts & 1]) = static_cast<int32_t>(parts) + 1;
           mbar_arrive(&B.v_safe);
         }
       }
+      base = static_cast<int>((base + 2u * a.n * kSlots) % kDepth);
     }
     if (!alive && lane == 0) report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
   } else {
@@ -605,7 +693,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     uint32_t used = 0;  // operations seen of each S buffer, modulo 2: a bit each
     uint32_t parts = 0, merges = 0;
     bool alive = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, abort, kWaitNs); };
+    // A warp's arrival, after what its lanes have done.
+    auto arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
     for (; alive && walk.next(work, p, a); ++parts) {
       const bool two = a.n1 > 0;
       const int tile_w = two ? w : 0;                     // row tile of this warp
@@ -630,13 +722,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           for (int i = 0; i < 4; ++i) bits[i] = valid ? tree_sees32(a.s, mask_row, first, key + 32 * i) : 0u;
         }
         if (!(alive = wait(&B.s_full[b], used >> b & 1u))) break;
-        const int prev_b = last_b;
         last_b = b;
         used ^= 1u << b;
         tc_fence_after();
         if (!some) {  // no row of this warp is one: its P may be anything
           tc_fence_before();
-          mbar_arrive(&B.p_full[b]);
+          arrive(&B.p_full[b]);
           continue;
         }
         const uint32_t s_col = lane_addr + Lay::kSCol + b * kTreeKeys;
@@ -676,8 +767,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const bool grow = m_new > m_ref + 8.f;  // also for the first visible key
         const bool rescale = grow && m_ref != -INFINITY;
         if (__any_sync(0xffffffffu, rescale)) {
-          // O holds earlier tiles: after the last of their products.
-          if (!(alive = wait(&B.o_done[prev_b], (used >> prev_b & 1u) ^ (prev_b == b ? 0u : 1u)))) break;
+          // O holds earlier tiles: after the last of their products (with two streams
+          // that was issued before this score tile, and has ended with it).
+          if (kStreams == 1 && !(alive = wait(&B.o_done[b ^ 1], (used >> (b ^ 1) & 1u) ^ 1u))) break;
           tc_fence_after();
           const float f = rescale ? fast_exp2(m_ref - m_new) : 1.f;
           const uint32_t o_col = lane_addr + (kStreams == 2 ? w * D : 0);
@@ -733,21 +825,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         l += a0 + a1;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&B.p_full[b]);
+        arrive(&B.p_full[b]);
       }
       if (!alive) break;
       // The part's rows: this stream's, or half the columns of both streams' sum.
-      if (mine > 0 && !(alive = wait(&B.o_done[last_b], (used >> last_b & 1u) ^ 1u))) break;
+      if constexpr (kStreams == 2)
+        alive = wait(&B.o_done[0], parts & 1);
+      else
+        alive = wait(&B.o_done[last_b], (used >> last_b & 1u) ^ 1u);
+      if (!alive) break;
       tc_fence_after();
       const bool merge = kStreams == 2 && !two;
       float f0 = 1.f, f1 = 0.f, m = m_ref, sum = l;  // O = f0 O_0 + f1 O_1
       if (merge) {
-        // (Products of this part have been waited for, so the last part's values have
-        // been read; a stream without one leaves them.)
+        // (This part's products have ended, so the last part's values have been read.)
         float2* x = reinterpret_cast<float2*>(smem + Lay::kXchOff);
         if (mine > 0) x[w * kTreeRows + r] = make_float2(m_ref, l);
         tc_fence_before();
-        mbar_arrive(&B.xch);
+        arrive(&B.xch);
         if (!(alive = wait(&B.xch, merges & 1))) break;
         ++merges;
         tc_fence_after();
@@ -812,7 +907,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         __syncwarp();
       }
       tc_fence_before();
-      mbar_arrive(&B.o_free);
+      arrive(&B.o_free);
     }
     if (!alive && lane == 0) report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
   }
@@ -933,7 +1028,7 @@ int launch_d(const Plan& plan, const Args& a, cudaStream_t stream) {
   p.num_pages = plan.num_pages;
   p.words = plan.tree_words;
   // Boxes never cross a page.
-  p.box_rows_k = std::min(plan.p, kTreeKeys);
+  p.box_rows_k = std::min(plan.p, 64);  // (the last tile's second half often lies behind the keys)
   p.box_rows_v = std::min(plan.p, Lay::kVKeys);
   // A V stage in one page takes all its 64-dimension chunks in one box.
   p.v_4d = Lay::kChunks > 1 && p.box_rows_v == Lay::kVKeys ? 1 : 0;
