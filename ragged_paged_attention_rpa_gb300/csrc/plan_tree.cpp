@@ -15,10 +15,11 @@ namespace {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// What a segment's queries, first tile and output cost, in key tiles.
-constexpr int32_t kSegCost = 2;
-// Fewest tiles (charges included) worth a CTA of its own.
-constexpr int32_t kLeastTiles = 3;
+// The line is counted in quarters of a key tile: what a segment's queries, first tile
+// and output cost, and the fewest worth a CTA of its own.
+constexpr int32_t kTile = 4;
+constexpr int32_t kSegCost = 6;
+constexpr int32_t kLeast = 4;
 
 rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
   const int32_t per = kTreeRows / (plan.hq / plan.hkv) * tree_row_tiles(plan.d);  // nodes of a segment
@@ -28,10 +29,10 @@ rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
   auto segments = [&](int32_t i) { return ceil_div(seq(i).nodes, per); };  // of a head
   std::vector<int64_t> v0(1, 0);  // the requests' starts on the line
   for (int32_t i = 0; i < n_seq; ++i)
-    v0.push_back(v0.back() + (tiles(i) + kSegCost) * segments(i) * plan.hkv);
+    v0.push_back(v0.back() + (static_cast<int64_t>(tiles(i)) * kTile + kSegCost) * segments(i) * plan.hkv);
   const int64_t total = v0.back();
   const int64_t most = std::min<int64_t>(plan.num_sms, kTreeMaxCtas);
-  const int64_t n = std::max<int64_t>(1, std::min(most, total / kLeastTiles));
+  const int64_t n = std::max<int64_t>(1, std::min(most, total / kLeast));
   // (A range's tiles travel in 31 bits.)
   if (ceil_div(total, n) > 0x3fffffff) return RPA_ERR_UNSUPPORTED;
   l.start_begin = static_cast<int32_t>(plan.tree_starts.size());
@@ -49,7 +50,7 @@ rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
     int64_t at = before[i];
     bool inside = false;
     if (i < n_seq) {
-      const int64_t cost = tiles(i) + kSegCost, off = (x - v0[i]) % cost;
+      const int64_t cost = static_cast<int64_t>(tiles(i)) * kTile + kSegCost, off = (x - v0[i]) % cost / kTile;
       int64_t sg = (x - v0[i]) / cost;
       at += sg * tiles(i) + std::min<int64_t>(off, tiles(i));
       inside = off > 0 && off < tiles(i);
@@ -83,7 +84,7 @@ rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
     plan.max_splits = std::max(plan.max_splits, plan.tree_cuts[l.cut_begin + k].nparts);
   plan.max_splits = std::max(plan.max_splits, 1);
   plan.kv_split = std::max(plan.kv_split, static_cast<int32_t>(std::min<int64_t>(
-                                              ceil_div(total, n) * kTreeKeys, 0x7fffffff)));
+                                              ceil_div(total, n * kTile) * kTreeKeys, 0x7fffffff)));
   plan.decode_ctas += n;
   plan.tree_slots = std::max(plan.tree_slots, static_cast<int32_t>(2 * n));
   return RPA_OK;

@@ -25,8 +25,8 @@
 // copies run on into the ring.
 //
 // Masks are looked up where a tile holds nodes or a window's edge; 128 bits a row.
-// A product gives 0 * NaN to the rows that do not see a key, so in those tiles warps
-// 1 and 3 go over V before the MMA reads it: rows of keys that no node sees become zero,
+// A product gives 0 * NaN to the rows that do not see a key, so in those tiles a warp
+// goes over V before the MMA reads it: rows of keys that no node sees become zero,
 // and of the others each NaN or infinity, which the rows that see it then get back
 // from memory after they are written (add_unseen).
 //
@@ -52,15 +52,18 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 
 // A wait (mbar_wait) of a converged warp, which agrees on the answer; what follows a phase that
-// is not complete yet stays out of the way of the caller's code.
+// is not complete yet stays out of the way of the caller's code.  kWho: callers that
+// differ in their registers have functions of their own.
+template <int kWho>
 __device__ __noinline__ bool warp_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort,
                                             uint64_t limit_ns) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns));
 }
+template <int kWho>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           uint64_t limit_ns) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return warp_wait_slow(bar, parity, abort, limit_ns);
+  return warp_wait_slow<kWho>(bar, parity, abort, limit_ns);
 }
 
 template <int N>
@@ -77,7 +80,7 @@ struct TreeParams {
   const int32_t* positions;
   const __nv_bfloat16* v_pages;
   __nv_bfloat16* out;
-  float* part_o;    // [slot][row][D]
+  float* part_o;    // [slot][D / 8][row][8]
   float* part_lse;  // [slot][row]
   unsigned char* ws;
   int32_t hq, hkv, group, per_tile;  // nodes a row tile
@@ -90,6 +93,10 @@ template <int D>
 struct Layout {
   static constexpr int kStreams = tree_row_tiles(D);
   static constexpr int kThreads = 128 + 128 * kStreams;
+  // Registers a thread with two streams (setmaxnreg), within the launch's 384 x 168; the
+  // 256 threads of one stream may have 255 each as they are.
+  static constexpr int kRegsCtl = 104, kRegsSoftmax = 200;
+  static_assert(kStreams == 1 || 128 * kRegsCtl + 256 * kRegsSoftmax <= 384 * 168, "registers");
   static constexpr int kChunks = D / 64;         // 128-byte pieces of a row; 16 KB pieces of a tile, of K and of V
   static constexpr int kVKeys = 8192 / D;        // keys of such a piece of V
   // One ring for K and V, filled in the order in which the MMAs take them: a slot is a
@@ -243,10 +250,11 @@ __device__ __noinline__ bool make_safe(uint8_t* piece, int32_t key, int32_t lo, 
 }
 
 // What make_safe took out of the part's tiles and this row sees, added to what was
-// stored of columns [c0, c1) (T: bf16 outputs or fp32 partials, the row's start).
+// stored of columns [c0, c1) (T: bf16 outputs or fp32 partials; every eight of a row's
+// columns lie `step` elements behind the eight before).
 template <typename T>
 __device__ __noinline__ void add_unseen(const TreeParams& p, const Part a, const uint64_t* mask_row, int32_t first,
-                                        int32_t d, int32_t c0, int32_t c1, T* row) {
+                                        int32_t d, int32_t c0, int32_t c1, T* row, int32_t step) {
   for (int32_t k0 = a.key0; k0 < a.key0 + a.n * kTreeKeys; k0 += kTreeKeys) {
     if (!a.masked(k0)) continue;
     for (int32_t k = k0; k < min(k0 + kTreeKeys, a.s.len); k += 32) {
@@ -258,7 +266,8 @@ __device__ __noinline__ void add_unseen(const TreeParams& p, const Part a, const
         const __nv_bfloat16* v = p.v_pages + (static_cast<int64_t>(from) * p.hkv + a.head) * d;
         for (int32_t c = c0; c < c1; ++c) {
           const float x = to_float(v[c]);
-          if (!(fabsf(x) < INFINITY)) row[c] = from_float<T>(to_float(row[c]) + x);
+          T* at = row + (c >> 3) * step + (c & 7);
+          if (!(fabsf(x) < INFINITY)) *at = from_float<T>(to_float(*at) + x);
         }
       }
     }
@@ -374,7 +383,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const uint32_t tmem = B.tmem_base;
   Walk<D, N> walk(work);
   Part a{};
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, abort, kWaitNs); };
+  if (warp < 4) {
+  if constexpr (kStreams == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Lay::kRegsCtl));
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait<0>(bar, parity, abort, kWaitNs); };
   if (warp == 0) {
     // ------------------------------------------------------------ copies
     const int rows_k = p.box_rows_k, rows_v = p.box_rows_v;
@@ -654,7 +665,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     mbar_wait(&B.fin, 0, &none, kDrainNs);
     __syncwarp();
     if (!alive && lane == 0) report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
-  } else if (warp < 4) {
+  } else {
     // ------------------------------------------------------------ V made safe
     // Warps 1 and 3, every second 16 KB each.
     const int half = warp >> 1;
@@ -683,7 +694,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       base = static_cast<int>((base + 2u * a.n * kSlots) % kDepth);
     }
     if (!alive && lane == 0) report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
+  }
   } else {
+    if constexpr (kStreams == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Lay::kRegsSoftmax));
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait<1>(bar, parity, abort, kWaitNs); };
     // ------------------------------------------------------------ softmax and output
     const int w = kStreams == 2 ? (warp - 4) >> 2 : 0;  // stream
     const int q4 = warp & 3, r = 32 * q4 + lane;        // lane quarter, row
@@ -860,49 +874,79 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const bool both = merge && ops > 1;  // (else the second O holds nothing of this part)
         const uint32_t o_col = lane_addr + (kStreams == 2 && !merge ? w * D : 0);
         __nv_bfloat16* out = p.out + (static_cast<int64_t>(node) * p.hq + a.head * G + hd) * D;
-        const int64_t row = (2ll * blockIdx.x + (parts > 0 ? 1 : 0)) * (kTreeRows * kStreams) + tile_w * kTreeRows + r;
-        float* part = p.part_o + row * D;
-#pragma unroll 1
-        for (int col = c0; col < c1; col += 16) {
-          uint32_t o[16];
-          tmem_ld16(o_col + col, o);
-          if (both) {
-            uint32_t o1[16];
-            tmem_ld16(o_col + D + col, o1);
-            tmem_wait_ld();
-            tmem_loaded(o);
-            tmem_loaded(o1);
+        // A partial's rows lie next to each other in pieces of eight columns: the warp's
+        // stores, and the combine's loads, are whole lines.
+        constexpr int kRows = kTreeRows * kStreams;
+        const int64_t slot = 2ll * blockIdx.x + (parts > 0 ? 1 : 0);
+        const int32_t row = tile_w * kTreeRows + r;
+        float* part = p.part_o + slot * (kRows * D) + row * 8;
+        // 32 columns of the row, as they come from tensor memory.
+        auto store = [&](const uint32_t (&o)[32], int col) {
+          if (!valid) return;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), f0, __uint_as_float(o1[i]) * f1));
-          } else {
-            tmem_wait_ld();
-            tmem_loaded(o);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t t[8];
+            if (a.whole) {
+              if (i & 1) continue;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
-          }
-          if (!valid) continue;
-          uint32_t t[8];
-          if (a.whole) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-            store32(out + col, p.out_v8, t);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
+              for (int x = 0; x < 8; ++x)
+                t[x] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * x]), __uint_as_float(o[8 * i + 2 * x + 1]));
+              store32(out + col + 8 * i, p.out_v8, t);
+            } else {
 #pragma unroll
               for (int x = 0; x < 8; ++x) t[x] = o[8 * i + x];
-              store32(part + col + 8 * i, true, t);
+              store32(part + (col / 8 + i) * (kRows * 8), true, t);
             }
+          }
+        };
+        if constexpr (kStreams == 2) {
+#pragma unroll 1
+          for (int col = c0; col < c1; col += 32) {
+            uint32_t o[32], o1[32];
+            tmem_ld32(o_col + col, o);
+            if (both) tmem_ld32(o_col + D + col, o1);
+            tmem_wait_ld();
+            tmem_loaded(o);
+            if (both) {
+              tmem_loaded(o1);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), f0, __uint_as_float(o1[i]) * f1));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+            }
+            store(o, col);
+          }
+        } else {
+          // The next columns load while these are stored.
+          uint32_t o[32], o1[32];
+          auto scale = [&](uint32_t (&x)[32]) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f0);
+          };
+          tmem_ld32(o_col, o);
+#pragma unroll 1
+          for (int col = 0; col < D; col += 64) {
+            tmem_wait_ld();
+            tmem_loaded(o);
+            tmem_ld32(o_col + col + 32, o1);
+            scale(o);
+            store(o, col);
+            tmem_wait_ld();
+            tmem_loaded(o1);
+            if (col + 64 < D) tmem_ld32(o_col + col + 64, o);
+            scale(o1);
+            store(o1, col + 32);
           }
         }
         if (valid && !a.whole && (!merge || w == 0))
-          p.part_lse[row] = sum == 0.f ? -INFINITY : m + __log2f(sum);
+          p.part_lse[slot * kRows + row] = sum == 0.f ? -INFINITY : m + __log2f(sum);
         if (valid && *reinterpret_cast<volatile int32_t*>(&B.poison[parts & 1]) == static_cast<int32_t>(parts) + 1) {
           if (a.whole)
-            add_unseen(p, a, mask_row, first, D, c0, c1, out);
+            add_unseen(p, a, mask_row, first, D, c0, c1, out, 8);
           else
-            add_unseen(p, a, mask_row, first, D, c0, c1, part);
+            add_unseen(p, a, mask_row, first, D, c0, c1, part, kRows * 8);
         }
         __syncwarp();
       }
@@ -922,54 +966,107 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
 template <int N>
 struct CutList {
+  int32_t n;
   TreeCut cut[kTreeMaxCtas];
   TreeSeqs<N> seqs;
 };
 
 // The parts of each cut segment joined: out = sum_k 2^(lse_k - M) O_k / sum_k
-// 2^(lse_k - M), M the largest lse_k.  A warp per row.
+// 2^(lse_k - M), M the largest lse_k.  A thread has 16 columns of a row, a warp those of
+// 32 rows.  Many parts are shared out to several warps, which add up in shared memory.
+constexpr int kCombineThreads = 256;
+__host__ __device__ constexpr int combine_warps(int nparts) { return nparts <= 4 ? 1 : nparts <= 16 ? 4 : 8; }
 template <int D, int N>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kCombineThreads, 4)
 tree_combine_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CutList<N> list) {
-  constexpr int E = D / 32, kRows = kTreeRows * tree_row_tiles(D);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kRows = kTreeRows * tree_row_tiles(D), kAtOnce = 2;
+  __shared__ float sums[8][17][32];
   const TreeCut& g = list.cut[blockIdx.x];
   const TreeSeq& s = list.seqs.s[g.i];
-  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int tile = row / kTreeRows, r = row % kTreeRows, tok = r / p.group, hd = r - tok * p.group;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int W = combine_warps(g.nparts), share = warp & (W - 1);
+  const int unit = (blockIdx.y * 8 + warp) / W, rows32 = unit / (D / 16), col = unit % (D / 16) * 16;
+  const int row = rows32 * 32 + lane, tile = row / kTreeRows, r = row % kTreeRows, tok = r / p.group;
   const int32_t node = (g.st * tree_row_tiles(D) + tile) * p.per_tile + tok;
-  if (tok >= p.per_tile || node >= s.nodes) return;
-  auto slot = [&](int k) -> int64_t { return (2ll * (g.cta + k) + (k == 0 ? g.first : 0)) * kRows + row; };
-  float M = -INFINITY;
-  for (int k = lane; k < g.nparts; k += 32) M = fmaxf(M, p.part_lse[slot(k)]);
+  const bool valid = row < kRows && tok < p.per_tile && node < s.nodes;
+  auto slot = [&](int k) -> int64_t { return (2ll * (g.cta + k) + (k == 0 ? g.first : 0)) * kRows; };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float acc[16], sum = 0.f, M = -INFINITY;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  float acc[E], sum = 0.f;
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  if (valid) {
+    // Two parts at a time, by a running maximum; the loads of both come first.
+    for (int k0 = share; k0 < g.nparts; k0 += kAtOnce * W) {
+      float4 v[kAtOnce][4];
+      float lse[kAtOnce];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int k0 = 0; k0 < g.nparts; k0 += 32) {
-    const int n = min(32, g.nparts - k0);
-    const float lse = lane < n ? p.part_lse[slot(k0 + lane)] : -INFINITY;
-    const float mine = lse == -INFINITY ? 0.f : lse == M ? 1.f : fast_exp2(lse - M);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float w = __shfl_sync(0xffffffffu, mine, k);
-      const float* src = p.part_o + slot(k0 + k) * D + lane * E;
-      sum += w;
+      for (int q = 0; q < kAtOnce; ++q) {
+        const int k = k0 + q * W;
+        lse[q] = -INFINITY;
+        if (k >= g.nparts) continue;
+        lse[q] = p.part_lse[slot(k) + row];
+        const float* src = p.part_o + slot(k) * D + col * kRows + row * 8;
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src + e);
-        acc[e] = fmaf(w, v.x, acc[e]);
-        acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
+        for (int i = 0; i < 4; ++i)
+          v[q][i] = *reinterpret_cast<const float4*>(src + (i >> 1) * (kRows * 8) + (i & 1) * 4);
+      }
+      float top = M;
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q) top = fmaxf(top, lse[q]);
+      if (top != M) {
+        const float f = M == -INFINITY ? 0.f : fast_exp2(M - top);
+        M = top;
+        sum *= f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] *= f;
+      }
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q) {
+        if (lse[q] == -INFINITY) continue;
+        const float w = lse[q] == M ? 1.f : fast_exp2(lse[q] - M);
+        sum += w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[4 * i] = fmaf(w, v[q][i].x, acc[4 * i]);
+          acc[4 * i + 1] = fmaf(w, v[q][i].y, acc[4 * i + 1]);
+          acc[4 * i + 2] = fmaf(w, v[q][i].z, acc[4 * i + 2]);
+          acc[4 * i + 3] = fmaf(w, v[q][i].w, acc[4 * i + 3]);
+        }
       }
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  __nv_bfloat16* dst =
-      p.out + (static_cast<int64_t>(s.q0 + node) * p.hq + g.head * p.group + hd) * D + lane * E;
+  if (W > 1) {
+    // The shares' maxima, then their sums under the largest.
+    sums[warp][16][lane] = M;
+    __syncthreads();
+    const int w0 = warp - share;
+    float top = -INFINITY;
+    for (int q = 0; q < W; ++q) top = fmaxf(top, sums[w0 + q][16][lane]);
+    const float f = M == top ? 1.f : M == -INFINITY ? 0.f : fast_exp2(M - top);
+    __syncthreads();
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    for (int i = 0; i < 16; ++i) sums[warp][i][lane] = acc[i] * f;
+    sums[warp][16][lane] = sum * f;
+    __syncthreads();
+    if (share != 0) return;
+    for (int q = 1; q < W; ++q) {
+      if (q == 1) {
+        sum = sums[w0][16][lane];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] = sums[w0][i][lane];
+      }
+      sum += sums[w0 + q][16][lane];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] += sums[w0 + q][i][lane];
+    }
+  }
+  if (!valid) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  store32(p.out + (static_cast<int64_t>(s.q0 + node) * p.hq + g.head * p.group + (r - tok * p.group)) * D + col,
+          p.out_v8, t);
 }
 
 template <int D, int N>
@@ -988,9 +1085,18 @@ int launch_one(const Plan& plan, const TreeLaunch& l, const CUtensorMap& tq, con
   CutList<N>& c = thread_staging<CutList<N>>();
   std::copy_n(plan.tree_cuts.begin() + l.cut_begin, l.n_cut, c.cut);
   std::copy_n(w.seqs.s, w.seqs.n, c.seqs.s);
+  // Warps of the segment that wants most: 32 rows and 16 columns each, times the shares
+  // of its parts.
+  int64_t warps = 0;
+  for (int i = 0; i < l.n_cut; ++i) {
+    const int32_t nodes = std::min(w.seqs.s[c.cut[i].i].nodes - c.cut[i].st * p.per_tile * Lay::kStreams,
+                                   p.per_tile * Lay::kStreams);
+    const int32_t rows = nodes > p.per_tile ? kTreeRows + (nodes - p.per_tile) * p.group : nodes * p.group;
+    warps = std::max<int64_t>(warps, static_cast<int64_t>((rows + 31) / 32) * (D / 16) * combine_warps(c.cut[i].nparts));
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(l.n_cut, kTreeRows * Lay::kStreams / 8);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(l.n_cut, static_cast<unsigned>((warps + 7) / 8));
+  cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
