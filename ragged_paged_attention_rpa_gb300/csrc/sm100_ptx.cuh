@@ -253,28 +253,19 @@ __device__ __forceinline__ void mma_ss_2chunks(uint32_t d_tmem, uint64_t a, uint
       "l"(a), "l"(b), "r"(idesc), "r"(acc0)
       : "memory");
 }
-// D (+)= A_i[tmem] * B_i over 128 keys, 16 a step (8 columns of A, 2048 bytes of B);
-// the last 64 keys' B begins kHalf descriptor units behind the first's.
-template <int kHalf>
-__device__ __forceinline__ void mma_ts_128keys(uint32_t d_tmem, uint32_t a, uint64_t b, uint32_t idesc,
-                                               uint32_t acc0) {
+// D (+)= A_i[tmem] * B_i over 64 keys, 16 a step (8 columns of A, 2048 bytes of B).
+__device__ __forceinline__ void mma_ts_64keys(uint32_t d_tmem, uint32_t a, uint64_t b, uint32_t idesc,
+                                              uint32_t acc0) {
   asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b64 b1, b2, b3, b4, b5, b6, b7;\n"
-      " .reg .b32 a1, a2, a3, a4, a5, a6, a7;\n setp.ne.b32 p, %4, 0;\n"
-      " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n add.s64 b4, %2, %5;\n"
-      " add.s64 b5, b4, 128;\n add.s64 b6, b4, 256;\n add.s64 b7, b4, 384;\n"
-      " add.s32 a1, %1, 8;\n add.s32 a2, %1, 16;\n add.s32 a3, %1, 24;\n add.s32 a4, %1, 32;\n"
-      " add.s32 a5, %1, 40;\n add.s32 a6, %1, 48;\n add.s32 a7, %1, 56;\n"
+      "{\n .reg .pred p, e;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n setp.ne.b32 p, %4, 0;\n"
+      " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n"
+      " add.s32 a1, %1, 8;\n add.s32 a2, %1, 16;\n add.s32 a3, %1, 24;\n"
       " elect.sync _|e, 0xffffffff;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, 1;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, 1;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, 1;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, 1;\n}\n" ::"r"(d_tmem),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc0), "n"(kHalf)
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n}\n" ::"r"(d_tmem),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc0)
       : "memory");
 }
 

@@ -119,7 +119,7 @@ struct Layout {
 struct Barriers {
   uint64_t q_full, q_empty;
   uint64_t full[12], empty[12];
-  uint64_t s_full[2], p_full[2];
+  uint64_t s_full[2], p_half[2], p_full[2];
   uint64_t o_done[2];       // one stream: a product of each S buffer; two: [0], the part's products
   uint64_t o_free;          // every row of the part's O has been read
   uint64_t xch;             // the streams' maxima and sums are posted
@@ -249,6 +249,13 @@ __device__ __noinline__ bool make_safe(uint8_t* piece, int32_t key, int32_t lo, 
   return __any_sync(0xffffffffu, found);
 }
 
+// The bits of 128 keys (tree_sees32), out of the way of the tiles that need none.
+__device__ __noinline__ uint4 tree_sees128(int32_t len, int32_t nodes, const uint64_t* row, int32_t lo, int32_t key) {
+  const TreeSeq s{0, 0, nodes, len, 0};
+  return make_uint4(tree_sees32(s, row, lo, key), tree_sees32(s, row, lo, key + 32), tree_sees32(s, row, lo, key + 64),
+                    tree_sees32(s, row, lo, key + 96));
+}
+
 // What make_safe took out of the part's tiles and this row sees, added to what was
 // stored of columns [c0, c1) (T: bf16 outputs or fp32 partials; every eight of a row's
 // columns lie `step` elements behind the eight before).
@@ -358,6 +365,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.s_full[i], 1);
+      mbar_init(&B.p_half[i], 4);
       mbar_init(&B.p_full[i], 4);
       mbar_init(&B.o_done[i], 1);
       B.poison[i] = 0;
@@ -509,17 +517,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       else
         mma_ss_2chunks(sc, qd, kd, kIdS, 0);
     };
-    // O += P V, P in buffer b, V in `slot`; `acc` 0: the stream's first in the part.
-    auto mma_pv = [&](auto bc, int slot, uint32_t acc) {
+    // O += P V, P in buffer b, V in `slot`, the first 64 keys as soon as their half of P is
+    // there; `acc` 0: the stream's first in the part.
+    auto mma_pv = [&](auto bc, int slot, uint32_t acc) -> bool {
       constexpr int b = decltype(bc)::value;
-      mma_ts_128keys<D == 64 ? 512 : kSub / 16>(tmem + b * D, tmem + Lay::kSCol + b * kTreeKeys + 64,
-                                                v_d0 + static_cast<uint64_t>(slot * (Lay::kSlot >> 4)), kIdPV, acc);
-    };
-    auto wait_p = [&](auto bc) -> bool {
-      constexpr int b = decltype(bc)::value;
-      const bool ok = wait(&B.p_full[b], p_ph >> b & 1u);
+      const uint32_t o = tmem + b * D, pc = tmem + Lay::kSCol + b * kTreeKeys;
+      const uint64_t vd = v_d0 + static_cast<uint64_t>(slot * (Lay::kSlot >> 4));
+      if (!wait(&B.p_half[b], p_ph >> b & 1u)) return false;
+      tc_fence_after();
+      mma_ts_64keys(o, pc, vd, kIdPV, acc);
+      if (!wait(&B.p_full[b], p_ph >> b & 1u)) return false;
       p_ph ^= 1u << b;
-      return ok;
+      tc_fence_after();
+      mma_ts_64keys(o, pc + 32, vd + (D == 64 ? 512 : kSub / 16), kIdPV, 1);
+      return true;
     };
     // A masked tile's V: asked for once it has landed, used once it is safe.
     auto ask = [&]() -> bool {
@@ -555,12 +566,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               if (!more) mma_commit(&B.q_empty);
               if (masked(j) && (!ask() || !safe())) return false;
               if (!wait(&B.full[ring.slot], ring.phase)) return false;
-              if (!wait_p(B0{})) return false;
               if (j == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
-              tc_fence_after();
               const int vs = ring.slot;
               ring.step();
-              mma_pv(B0{}, vs, j > 0);
+              if (!mma_pv(B0{}, vs, j > 0)) return false;
               if (more) {
                 if (!wait(&B.full[ring.slot], ring.phase)) return false;
                 tc_fence_after();
@@ -569,9 +578,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 mma_s(B0{}, 0, ks);
                 mma_commit(&B.s_full[0]);
               }
-              if (!wait_p(B1{})) return false;
-              tc_fence_after();
-              mma_pv(B1{}, vs, j > 0);
+              if (!mma_pv(B1{}, vs, j > 0)) return false;
               mma_commit(&B.empty[vs]);
               if (!more) break;
             }
@@ -591,10 +598,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           auto product = [&](auto bc, int j) -> bool {
             if (masked(j) && (!ask() || !safe())) return false;
             if (!wait(&B.full[ring.slot], ring.phase)) return false;
-            if (!wait_p(bc)) return false;
             if (j == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
-            tc_fence_after();
-            mma_pv(bc, ring.slot, j > 1);
+            if (!mma_pv(bc, ring.slot, j > 1)) return false;
             mma_commit(&B.empty[ring.slot]);
             ring.step();
             return true;
@@ -630,19 +635,19 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           };
           auto product = [&](int b, int j) -> bool {
             if (masked(j) && (!ask() || !safe())) return false;
-            if (!wait(&B.p_full[b], p_ph >> b & 1u)) return false;
-            p_ph ^= 1u << b;
             if (j == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
 #pragma unroll
             for (int h = 0; h < kSlots; ++h) {
               if (!wait(&B.full[ring.slot], ring.phase)) return false;
+              if (!wait(h == 0 ? &B.p_half[b] : &B.p_full[b], p_ph >> b & 1u)) return false;
               tc_fence_after();
-              mma_ts_2x32keys(tmem, tmem + Lay::kSCol + b * kTreeKeys + 64 + 32 * h,
+              mma_ts_2x32keys(tmem, tmem + Lay::kSCol + b * kTreeKeys + 32 * h,
                               v_d0 + static_cast<uint64_t>(ring.slot * (Lay::kSlot >> 4)), kIdPV,
                               j > 0 || h > 0 ? 1u : 0u);
               mma_commit(&B.empty[ring.slot]);
               ring.step();
             }
+            p_ph ^= 1u << b;
             mma_commit(&B.o_done[b]);
             return true;
           };
@@ -730,10 +735,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // (The mask's words come while the scores are awaited.)
         const int32_t key = a.key0 + (two ? op >> 1 : op) * kTreeKeys;
         const bool masked = a.masked(key);
-        uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+        uint4 bits = make_uint4(0u, 0u, 0u, 0u);
         if (masked) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) bits[i] = valid ? tree_sees32(a.s, mask_row, first, key + 32 * i) : 0u;
+          if (valid) bits = tree_sees128(a.s.len, a.s.nodes, mask_row, first, key);
+          __syncwarp();
         }
         if (!(alive = wait(&B.s_full[b], used >> b & 1u))) break;
         last_b = b;
@@ -741,41 +746,28 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tc_fence_after();
         if (!some) {  // no row of this warp is one: its P may be anything
           tc_fence_before();
+          arrive(&B.p_half[b]);
           arrive(&B.p_full[b]);
           continue;
         }
         const uint32_t s_col = lane_addr + Lay::kSCol + b * kTreeKeys;
-        // A quarter of the row's scores, read twice (for the extremum, then for the
-        // weights; the last two quarters stay): 128 of them would not leave room.
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(s_col + 32 * i, sr[i]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_loaded(sr[i]);
         // The largest product under a negative scale is that of the smallest score.
         // A masked score becomes the infinity whose product is -infinity.
-        uint32_t sa[32], sb[32];
-        auto hide = [&](uint32_t (&x)[32], uint32_t seen) {
-          if (!masked) return;
+        if (masked) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = seen & 1u << i ? x[i] : __float_as_uint(none);
-        };
-        auto most = [&](const uint32_t (&x)[32], const uint32_t (&y)[32]) -> float {
-          if (c < 0.f) return fminf(extremum<32, false>(x), extremum<32, false>(y));
-          return fmaxf(extremum<32, true>(x), extremum<32, true>(y));
-        };
-        tmem_ld32(s_col, sa);
-        tmem_ld32(s_col + 32, sb);
-        tmem_wait_ld();
-        tmem_loaded(sa);
-        tmem_loaded(sb);
-        hide(sa, bits[0]);
-        hide(sb, bits[1]);
-        float mx = most(sa, sb);
-        tmem_ld32(s_col + 64, sa);
-        tmem_ld32(s_col + 96, sb);
-        tmem_wait_ld();
-        tmem_loaded(sa);
-        tmem_loaded(sb);
-        hide(sa, bits[2]);
-        hide(sb, bits[3]);
-        const float mx1 = most(sa, sb);
-        mx = c < 0.f ? fminf(mx, mx1) : fmaxf(mx, mx1);
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t seen = i == 0 ? bits.x : i == 1 ? bits.y : i == 2 ? bits.z : bits.w;
+#pragma unroll
+            for (int x = 0; x < 32; ++x) sr[i][x] = seen & 1u << x ? sr[i][x] : __float_as_uint(none);
+          }
+        }
+        float mx = c < 0.f ? extremum<128, false>(&sr[0][0]) : extremum<128, true>(&sr[0][0]);
         mx = mx == none ? -INFINITY : mx * c;
         const float m_new = fmaxf(m_ref, mx);
         const bool grow = m_new > m_ref + 8.f;  // also for the first visible key
@@ -806,34 +798,28 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
         const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_use, -m_use);
         uint64_t acc = f2_pack(0.f, 0.f);
-        // P of a quarter, into columns 64 + 16 i of the buffer: over scores that are in
-        // registers by then.
-        auto weights = [&](const uint32_t (&x)[32], int i) {
+        // P over the first half of its scores, in two halves: the product starts on the
+        // first 64 keys while the others are exponentiated.
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const uint64_t x2 =
-                f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, nm2);
+                f2_fma(f2_pack(__uint_as_float(sr[i][2 * k]), __uint_as_float(sr[i][2 * k + 1])), c2, nm2);
             float x0, x1;
             f2_unpack(x2, x0, x1);
             const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
             acc = f2_add(acc, f2_pack(p0, p1));
             pk[k] = pack_bf16x2(p0, p1);
           }
-          tmem_st16(s_col + 64 + 16 * i, pk);
-        };
-        weights(sa, 2);
-        tmem_ld32(s_col, sa);
-        weights(sb, 3);
-        tmem_wait_ld();
-        tmem_loaded(sa);
-        tmem_ld32(s_col + 32, sb);
-        hide(sa, bits[0]);
-        weights(sa, 0);
-        tmem_wait_ld();
-        tmem_loaded(sb);
-        hide(sb, bits[1]);
-        weights(sb, 1);
+          tmem_st16(s_col + 16 * i, pk);
+          if (i == 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(&B.p_half[b]);
+          }
+        }
         float a0, a1;
         f2_unpack(acc, a0, a1);
         l += a0 + a1;
