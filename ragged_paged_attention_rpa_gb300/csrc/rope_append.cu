@@ -28,6 +28,10 @@ namespace rpa {
 namespace {
 
 constexpr int kWarps = 4;
+// CTAs an SM holds at least, which sets the registers: 8192 tokens of 64 rows of 256
+// take 83 us with 5 of them and 4 rows (2 of fp32) in flight a lane, 86 with 4 and 6, 90
+// with 6 and 3 or 2, 102 with 8 and 2.
+constexpr int kMinCtas = 5;
 
 struct AppendParams {
   const void* q;
@@ -48,21 +52,34 @@ struct AppendParams {
   bool pairs, whole;  // whole: fp32 rows are 32-byte aligned
 };
 
-// Eight elements of a row as floats, and back.
-__device__ __forceinline__ void load8(const __nv_bfloat16* src, bool, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(src);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight elements of a row as they lie in memory, as floats, and back.
+template <typename T>
+struct Octet;
+template <>
+struct Octet<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* src) { u = *reinterpret_cast<const uint4*>(src); }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
   }
-}
-__device__ __forceinline__ void load8(const float* src, bool, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+};
+template <>
+struct Octet<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* src) {
+    a = *reinterpret_cast<const float4*>(src);
+    b = reinterpret_cast<const float4*>(src)[1];
+  }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
 __device__ __forceinline__ void store8(__nv_bfloat16* dst, bool, const float (&x)[8], float, float) {
   *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
                                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
@@ -104,7 +121,7 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
 }
 
 template <int D, typename T, typename KV>
-__global__ void __launch_bounds__(32 * kWarps) append_rope_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * kWarps, kMinCtas) append_rope_kernel(const AppendParams p) {
   constexpr int kLanes = D / 16;          // of a row
   constexpr int kRows = 32 / kLanes;      // rows of a warp
   constexpr int kMine = 8 / kRows;        // sines and cosines a lane works out
@@ -121,6 +138,24 @@ __global__ void __launch_bounds__(32 * kWarps) append_rope_kernel(const AppendPa
     const int32_t t = static_cast<int32_t>(w / p.chunks);
     const int32_t r0 = static_cast<int32_t>(w - static_cast<int64_t>(t) * p.chunks) * p.rows;
     const int32_t r1 = min(heads, r0 + p.rows);
+    // The first rows are on their way while the sines are worked out.
+    Octet<T> raw[kBatch][2];
+    auto load = [&](int32_t rb) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int32_t r = rb + b * kRows;
+        if (r >= r1) continue;
+        const T* src = r < p.hq ? static_cast<const T*>(p.q) + t * p.qs + static_cast<int64_t>(r) * D
+                       : r < p.hq + p.hkv
+                           ? static_cast<const T*>(p.k) + t * p.ks + static_cast<int64_t>(r - p.hq) * D
+                           : static_cast<const T*>(p.v) + t * p.vs + static_cast<int64_t>(r - p.hq - p.hkv) * D;
+        raw[b][0].load(src + first);
+        raw[b][1].load(src + second);
+      }
+    };
+    load(r0 + sub);
+    int64_t slot = -1;
+    if (r1 > p.hq) slot = __ldg(p.slots + t);
     // Pair e of the lane (e < 4 in the first octet of neighbouring pairs) is pair
     // 8 u + e, or 4 u + e and R / 4 + 4 u + e - 4.
     float cs[8], sn[8];
@@ -146,55 +181,42 @@ __global__ void __launch_bounds__(32 * kWarps) append_rope_kernel(const AppendPa
         sn[e] = __shfl_sync(0xffffffffu, s[e % kMine], from);
       }
     }
-    int64_t slot = -1;
-    if (r1 > p.hq) {
-      slot = __ldg(p.slots + t);
-      if (slot >= p.pool_slots) {
-        if (lane == 0 && p.ws) report_error(p.ws, RPA_DEVERR_PAGE_ID, t);
-        slot = -1;
-      }
+    if (slot >= p.pool_slots) {
+      if (lane == 0 && p.ws) report_error(p.ws, RPA_DEVERR_PAGE_ID, t);
+      slot = -1;
     }
-    for (int32_t rb = r0 + sub; rb < r1; rb += kBatch * kRows) {
-      float x[kBatch][8], y[kBatch][8];
+    for (int32_t rb = r0 + sub; rb < r1;) {
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         const int32_t r = rb + b * kRows;
         if (r >= r1) continue;
-        const T* src = r < p.hq ? static_cast<const T*>(p.q) + t * p.qs + static_cast<int64_t>(r) * D
-                       : r < p.hq + p.hkv
-                           ? static_cast<const T*>(p.k) + t * p.ks + static_cast<int64_t>(r - p.hq) * D
-                           : static_cast<const T*>(p.v) + t * p.vs + static_cast<int64_t>(r - p.hq - p.hkv) * D;
-        load8(src + first, p.whole, x[b]);
-        load8(src + second, p.whole, y[b]);
-      }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int32_t r = rb + b * kRows;
-        if (r >= r1) continue;
+        float x[8], y[8];
+        raw[b][0].floats(x);
+        raw[b][1].floats(y);
         if (turns && r < p.hq + p.hkv) {
           if (!p.pairs) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float a = x[b][e], o = y[b][e];
-              x[b][e] = fmaf(a, cs[e], -o * sn[e]);
-              y[b][e] = fmaf(o, cs[e], a * sn[e]);
+              const float a = x[e], o = y[e];
+              x[e] = fmaf(a, cs[e], -o * sn[e]);
+              y[e] = fmaf(o, cs[e], a * sn[e]);
             }
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float a = x[b][2 * e], o = x[b][2 * e + 1];
-              x[b][2 * e] = fmaf(a, cs[e], -o * sn[e]);
-              x[b][2 * e + 1] = fmaf(o, cs[e], a * sn[e]);
-              const float a2 = y[b][2 * e], o2 = y[b][2 * e + 1];
-              y[b][2 * e] = fmaf(a2, cs[4 + e], -o2 * sn[4 + e]);
-              y[b][2 * e + 1] = fmaf(o2, cs[4 + e], a2 * sn[4 + e]);
+              const float a = x[2 * e], o = x[2 * e + 1];
+              x[2 * e] = fmaf(a, cs[e], -o * sn[e]);
+              x[2 * e + 1] = fmaf(o, cs[e], a * sn[e]);
+              const float a2 = y[2 * e], o2 = y[2 * e + 1];
+              y[2 * e] = fmaf(a2, cs[4 + e], -o2 * sn[4 + e]);
+              y[2 * e + 1] = fmaf(o2, cs[4 + e], a2 * sn[4 + e]);
             }
           }
         }
         if (r < p.hq) {
           T* dst = static_cast<T*>(p.q_out) + (static_cast<int64_t>(t) * p.hq + r) * D;
-          store8(dst + first, p.whole, x[b], 1.f, 1.f);
-          store8(dst + second, p.whole, y[b], 1.f, 1.f);
+          store8(dst + first, p.whole, x, 1.f, 1.f);
+          store8(dst + second, p.whole, y, 1.f, 1.f);
         } else if (slot >= 0) {
           const bool is_k = r < p.hq + p.hkv;
           const int32_t g = is_k ? r - p.hq : r - p.hq - p.hkv;
@@ -204,10 +226,12 @@ __global__ void __launch_bounds__(32 * kWarps) append_rope_kernel(const AppendPa
             s = __ldg((is_k ? p.k_scale : p.v_scale) + g);
             inv = 1.f / s;
           }
-          store8(dst + first, p.whole, x[b], s, inv);
-          store8(dst + second, p.whole, y[b], s, inv);
+          store8(dst + first, p.whole, x, s, inv);
+          store8(dst + second, p.whole, y, s, inv);
         }
       }
+      rb += kBatch * kRows;
+      load(rb);
     }
   }
 }

@@ -3,10 +3,13 @@
 //
 // build_tree: with depth(i) = 0 for a node that follows the context and
 // depth(parent) + 1 otherwise, positions = C + depth, and bit j of row i says
-// whether node j is i or an ancestor of it.  A request is one CTA: its parents go
-// to shared memory, a thread walks from its node to the root.  Parents come
-// before their children, so the walk meets the mask's words from the last to the
-// first and keeps one at a time.
+// whether node j is i or an ancestor of it.  A request is one CTA, whose first warp takes
+// the nodes 32 at a time in shared memory (all of it writes the rows out): parents come first, so an ancestor is among the 32 (found by
+// doubling: five rounds of shuffles) or its row is there already, and a row is that of
+// the first ancestor before the 32, with those among them set.  The path's nodes have
+// rising numbers, so a window's are a row's highest bits.  (A thread that walked from
+// its node to the root took 41 us for 64 requests of up to 256 nodes, chains among
+// them.)
 //
 // commit_tree: row k of the path takes the K and V of node path[k] >= k.  A thread
 // owns 16 bytes of the row and goes down the path, eight nodes read before eight
@@ -23,59 +26,101 @@ namespace rpa {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kMaxNodes = 64 * kTreeMaxWords;
+constexpr uint32_t kAll = 0xffffffffu;
 
 struct BuildTreeParams {
   const int32_t* parents;
   const int32_t* cu;
   const int32_t* kv;
   const int32_t* window;
-  unsigned long long* mask;
+  uint32_t* mask;
   int32_t* positions;
   unsigned char* ws;
-  int32_t total_q, words;
+  int32_t total_q, words;  // words of 32 bits
 };
 
+// Clears the lowest `n` set bits of w, and takes them off n.
+__device__ __forceinline__ uint32_t drop_lowest(uint32_t w, int32_t& n) {
+  const int32_t c = __popc(w);
+  if (n >= c) {
+    n -= c;
+    return 0;
+  }
+  for (; n > 0; --n) w &= w - 1;
+  return w;
+}
+
 __global__ void __launch_bounds__(kThreads) build_tree_kernel(const BuildTreeParams p) {
-  __shared__ int16_t parent[kMaxNodes];
-  const int32_t s = blockIdx.x;
+  extern __shared__ uint32_t smem[];
+  const int32_t s = blockIdx.x, lane = threadIdx.x & 31;
   const int32_t q0 = __ldg(p.cu + s), q1 = __ldg(p.cu + s + 1), len = __ldg(p.kv + s);
   const int32_t w = p.window ? __ldg(p.window + s) : 0;
   // (In 64 bits: lengths that cannot be used may be anything.)
   const int64_t n64 = static_cast<int64_t>(q1) - q0;
-  if (q0 < 0 || n64 < 0 || q1 > p.total_q || n64 > 64 * p.words || n64 > len) {
+  if (q0 < 0 || n64 < 0 || q1 > p.total_q || n64 > 32 * p.words || n64 > len) {
     if (threadIdx.x == 0 && p.ws) report_error(p.ws, RPA_DEVERR_LENGTHS, s);
     return;
   }
-  const int32_t n = static_cast<int32_t>(n64);
+  const int32_t n = static_cast<int32_t>(n64), W = p.words;
+  // Rows [node][W + 1] (the odd length keeps 32 rows' words in different banks), and
+  // parents, which become depths.
+  uint32_t* rows = smem;
+  int32_t* depths = reinterpret_cast<int32_t*>(smem + 32 * W * (W + 1));
   for (int32_t i = threadIdx.x; i < n; i += kThreads) {
-    int32_t j = __ldg(p.parents + q0 + i);
-    if (j < -1 || j >= i) {
+    int32_t up = __ldg(p.parents + q0 + i);
+    if (up < -1 || up >= i) {
       if (p.ws) report_error(p.ws, RPA_DEVERR_LENGTHS, s);
-      j = -1;
+      up = -1;
     }
-    parent[i] = static_cast<int16_t>(j);
+    depths[i] = up;
   }
   __syncthreads();
-  const int32_t most = w > 0 ? w : n;  // nodes of a path that its last one sees
-  for (int32_t i = threadIdx.x; i < n; i += kThreads) {
-    unsigned long long* row = p.mask + static_cast<int64_t>(q0 + i) * p.words;
-    for (int32_t k = p.words - 1; k > i >> 6; --k) row[k] = 0;
-    int32_t k = i >> 6, depth = 0;
-    unsigned long long bits = 0;
-    for (int32_t j = i;;) {
-      if (depth < most) bits |= 1ull << (j & 63);
-      j = parent[j];
-      if (j < 0) break;
-      ++depth;
-      for (; k > j >> 6; --k) {
-        row[k] = bits;
-        bits = 0;
+  if (threadIdx.x < 32) {
+    for (int32_t i0 = 0; i0 < n; i0 += 32) {
+      const int32_t i = i0 + lane;
+      // The node's parent, then its first ancestor before i0 as far as known.
+      int32_t up = i < n ? depths[i] : -1;
+      // Ancestors among the 32 (and the node): after k rounds those within 2^k steps.
+      uint32_t mine = 1u << lane;
+#pragma unroll
+      for (int k = 0; k < 5; ++k) {
+        const bool within = up >= i0;
+        if (!__any_sync(kAll, within)) break;
+        const int from = within ? up - i0 : lane;
+        const uint32_t theirs = __shfl_sync(kAll, mine, from);
+        const int32_t further = __shfl_sync(kAll, up, from);
+        if (within) {
+          mine |= theirs;
+          up = further;
+        }
       }
+      if (i < n) {
+        const int32_t own = i0 >> 5;
+        uint32_t* row = rows + i * (W + 1);
+#pragma unroll 4
+        for (int32_t k = 0; k < own; ++k) row[k] = k <= up >> 5 ? rows[up * (W + 1) + k] : 0u;
+        row[own] = mine;
+        depths[i] = __popc(mine) - 1 + (up >= 0 ? depths[up] + 1 : 0);
+      }
+      __syncwarp();
     }
-    row[k] = bits;
-    while (--k >= 0) row[k] = 0;
-    p.positions[q0 + i] = len - n + depth;
+  }
+  __syncthreads();
+  for (int32_t i = threadIdx.x; i < n; i += kThreads) p.positions[q0 + i] = len - n + depths[i];
+  uint32_t* out = p.mask + static_cast<int64_t>(q0) * W;
+  if (w <= 0) {
+    for (int32_t u = threadIdx.x; u < n * W; u += kThreads) {
+      const int32_t i = u / W, k = u - i * W;
+      out[u] = k <= i >> 5 ? rows[i * (W + 1) + k] : 0u;
+    }
+    return;
+  }
+  for (int32_t i = threadIdx.x; i < n; i += kThreads) {
+    int32_t drop = max(0, depths[i] + 1 - w);  // nodes of the path that lie too far back
+    for (int32_t k = 0; k < W; ++k) {
+      const uint32_t bits = k <= i >> 5 ? rows[i * (W + 1) + k] : 0u;
+      out[i * W + k] = drop > 0 ? drop_lowest(bits, drop) : bits;
+    }
   }
 }
 
@@ -148,10 +193,14 @@ __global__ void __launch_bounds__(kThreads) commit_tree_kernel(const CommitTreeP
 
 int launch_build_tree(const BuildTreeArgs& a, void* stream) {
   if (a.num_seqs == 0) return 0;
-  const BuildTreeParams p{a.parents, a.cu_q_lens, a.kv_lens, a.window,
-                          reinterpret_cast<unsigned long long*>(a.mask), a.positions, a.workspace,
-                          a.total_q, a.words};
-  build_tree_kernel<<<a.num_seqs, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  const int32_t W = 2 * a.words;
+  const BuildTreeParams p{a.parents, a.cu_q_lens, a.kv_lens, a.window, reinterpret_cast<uint32_t*>(a.mask),
+                          a.positions, a.workspace, a.total_q, W};
+  const int bytes = 32 * W * (W + 2) * static_cast<int>(sizeof(uint32_t));
+  const int most = 64 * kTreeMaxWords * (2 * kTreeMaxWords + 2) * static_cast<int>(sizeof(uint32_t));
+  if (bytes > 48 * 1024)
+    if (int e = ensure_dynamic_smem(reinterpret_cast<const void*>(build_tree_kernel), most)) return e;
+  build_tree_kernel<<<a.num_seqs, kThreads, bytes, static_cast<cudaStream_t>(stream)>>>(p);
   if (cudaError_t e = cudaGetLastError()) return static_cast<int>(e);
   trace_mark(RPA_KERNEL_BUILD_TREE, stream);
   return 0;

@@ -48,6 +48,12 @@ namespace {
 using namespace sm100;
 
 constexpr int kSub = 16384;  // a 64-dimension chunk of 128 keys of K, or 8192 / D keys of V
+// A row's weights are 2^(score - reference).  The reference is the maximum of the first
+// tile that the row sees; it goes up when a later tile's passes it by this much.  So the
+// weights need not wait for a tile's maximum: they are worked out under the reference
+// while the maximum is taken, and worked out again in the rare case.  They, their sums
+// and O stay far within 32-bit (and bf16's equal) range below 2^(kGrow + 40).
+constexpr float kGrow = 40.f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 
@@ -62,7 +68,7 @@ __device__ __noinline__ bool warp_wait_slow(uint64_t* bar, uint32_t parity, vola
 template <int kWho>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           uint64_t limit_ns) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity)), 1)) return true;
   return warp_wait_slow<kWho>(bar, parity, abort, limit_ns);
 }
 
@@ -123,7 +129,7 @@ struct Barriers {
   uint64_t o_done[2];       // one stream: a product of each S buffer; two: [0], the part's products
   uint64_t o_free;          // every row of the part's O has been read
   uint64_t xch;             // the streams' maxima and sums are posted
-  uint64_t v_ask, v_safe;   // a masked tile's V has landed / may be read
+  uint64_t v_ask[2], v_safe[2];  // by turns: a masked tile's V is on its way / may be read
   uint64_t fin;
   uint32_t tmem_base;
   int abort;
@@ -368,12 +374,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       mbar_init(&B.p_half[i], 4);
       mbar_init(&B.p_full[i], 4);
       mbar_init(&B.o_done[i], 1);
+      mbar_init(&B.v_ask[i], 1);
+      mbar_init(&B.v_safe[i], 2);
       B.poison[i] = 0;
     }
     mbar_init(&B.o_free, 4 * kStreams);
     mbar_init(&B.xch, 8);
-    mbar_init(&B.v_ask, 1);
-    mbar_init(&B.v_safe, 2);
     mbar_init(&B.fin, 1);
     B.abort = 0;
     fence_barrier_init();
@@ -504,7 +510,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint64_t k_d0 = smem_desc(smem_addr(smem + Lay::kRingOff), 16, 1024);
     const uint64_t v_d0 = smem_desc(smem_addr(smem + Lay::kRingOff), Lay::kVKeys * 128, 1024);
     Ring<kDepth> ring;
-    uint32_t parts = 0, asked = 0, p_ph = 0;  // p_ph: a phase bit per S buffer
+    uint32_t parts = 0, p_ph = 0;  // p_ph: a phase bit per S buffer
     bool alive = true;
     // S into buffer b from the K tile in `slot` (or the next slots) and row tile t.
     auto mma_s = [&](auto bc, int t, int slot) {
@@ -532,20 +538,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       mma_ts_64keys(o, pc + 32, vd + (D == 64 ? 512 : kSub / 16), kIdPV, 1);
       return true;
     };
-    // A masked tile's V: asked for once it has landed, used once it is safe.
-    auto ask = [&]() -> bool {
-      Ring<kDepth> r = ring;
-      for (int c = 0; c < kSlots; ++c, r.step())
-        if (!wait(&B.full[r.slot], r.phase)) return false;
-      if (lane == 0) mbar_arrive(&B.v_ask);
-      return true;
+    // A masked tile's V: announced where the ring's slots of it hold nothing older that
+    // has not landed (a tile ahead; for 256 dimensions, where half the ring is one tile, at
+    // its own score tile), used once it is safe.
+    uint32_t asked = 0, used_safe = 0;
+    auto ask = [&]() {
+      if (lane == 0) mbar_arrive(&B.v_ask[asked & 1]);
+      ++asked;
     };
-    auto safe = [&]() -> bool { return wait(&B.v_safe, asked++ & 1); };
+    auto safe = [&]() -> bool {
+      const uint32_t k = used_safe++;
+      return wait(&B.v_safe[k & 1], k >> 1 & 1);
+    };
     using B0 = std::integral_constant<int, 0>;
     using B1 = std::integral_constant<int, 1>;
     while (alive && walk.next(work, p, a)) {
       if (!(alive = wait(&B.q_full, parts & 1))) break;
-      auto masked = [&](int j) { return a.masked(a.key0 + j * kTreeKeys); };
+      auto masked = [&](int j) { return __builtin_expect(a.masked(a.key0 + j * kTreeKeys), 0); };
+      if (kStreams == 2 && masked(0)) ask();
       alive = [&]() -> bool {
         if constexpr (kStreams == 2) {
           if (a.n1 > 0) {
@@ -560,11 +570,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll 1
             for (int j = 0;; ++j) {
               const bool more = j + 1 < a.n;
+              if (more && masked(j + 1)) ask();
               mma_s(B1{}, 1, ks);
               mma_commit(&B.s_full[1]);
               mma_commit(&B.empty[ks]);
               if (!more) mma_commit(&B.q_empty);
-              if (masked(j) && (!ask() || !safe())) return false;
+              if (masked(j) && !safe()) return false;
               if (!wait(&B.full[ring.slot], ring.phase)) return false;
               if (j == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
               const int vs = ring.slot;
@@ -596,7 +607,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             return true;
           };
           auto product = [&](auto bc, int j) -> bool {
-            if (masked(j) && (!ask() || !safe())) return false;
+            if (j + 1 < a.n && masked(j + 1)) ask();
+            if (masked(j) && !safe()) return false;
             if (!wait(&B.full[ring.slot], ring.phase)) return false;
             if (j == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
             if (!mma_pv(bc, ring.slot, j > 1)) return false;
@@ -634,7 +646,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             return true;
           };
           auto product = [&](int b, int j) -> bool {
-            if (masked(j) && (!ask() || !safe())) return false;
+            if (masked(j) && !safe()) return false;
             if (j == 0 && !wait(&B.o_free, (parts & 1) ^ 1)) return false;
 #pragma unroll
             for (int h = 0; h < kSlots; ++h) {
@@ -655,6 +667,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           if (a.n == 1) mma_commit(&B.q_empty);
 #pragma unroll 1
           for (int j = 0; j < a.n; ++j) {
+            if (masked(j)) ask();
             if (j + 1 < a.n && !score((j + 1) & 1)) return false;
             if (j + 2 == a.n) mma_commit(&B.q_empty);
             if (!product(j & 1, j)) return false;
@@ -675,28 +688,31 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // Warps 1 and 3, every second 16 KB each.
     const int half = warp >> 1;
     uint32_t asked = 0, parts = 0;
-    int base = 0;  // ring slot of the part's first tile
+    uint32_t base = 0;  // slots filled before the part
     bool alive = true;
     for (; alive && walk.next(work, p, a); ++parts) {
       for (int j = 0; j < a.n; ++j) {
         const int32_t k0 = a.key0 + j * kTreeKeys;
         if (!a.masked(k0)) continue;
-        if (!(alive = wait(&B.v_ask, asked & 1))) break;
-        ++asked;
+        if (!(alive = wait(&B.v_ask[asked & 1], asked >> 1 & 1))) break;
         // The tile's place among the part's (see the copies).
-        const int tile = a.n1 > 0 || j == a.n - 1 ? 2 * j + 1 : 2 * j + 2;
+        const uint32_t at = base + (a.n1 > 0 || j == a.n - 1 ? 2 * j + 1 : 2 * j + 2) * kSlots;
         bool found = false;
-        for (int c = half; c < kChunks; c += 2)
-          found |= make_safe<D>(smem + Lay::kRingOff + (base + tile * kSlots + c / kSubs) % kDepth * Lay::kSlot +
-                                    (c % kSubs) * kSub,
+        for (int c = half; c < kChunks && alive; c += 2) {
+          const uint32_t n = at + c / kSubs;
+          if (!(alive = wait(&B.full[n % kDepth], n / kDepth & 1))) break;
+          found |= make_safe<D>(smem + Lay::kRingOff + n % kDepth * Lay::kSlot + (c % kSubs) * kSub,
                                 k0 + c * Lay::kVKeys, a.lo, a.s.len, lane);
+        }
+        if (!alive) break;
         __syncwarp();
         if (lane == 0) {
           if (found) *reinterpret_cast<volatile int32_t*>(&B.poison[parts & 1]) = static_cast<int32_t>(parts) + 1;
-          mbar_arrive(&B.v_safe);
+          mbar_arrive(&B.v_safe[asked & 1]);
         }
+        ++asked;
       }
-      base = static_cast<int>((base + 2u * a.n * kSlots) % kDepth);
+      base += 2u * a.n * kSlots;
     }
     if (!alive && lane == 0) report_error(p.ws, RPA_DEVERR_TIMEOUT, blockIdx.x);
   }
@@ -736,7 +752,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int32_t key = a.key0 + (two ? op >> 1 : op) * kTreeKeys;
         const bool masked = a.masked(key);
         uint4 bits = make_uint4(0u, 0u, 0u, 0u);
-        if (masked) {
+        if (__builtin_expect(masked, 0)) {
           if (valid) bits = tree_sees128(a.s.len, a.s.nodes, mask_row, first, key);
           __syncwarp();
         }
@@ -744,7 +760,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         last_b = b;
         used ^= 1u << b;
         tc_fence_after();
-        if (!some) {  // no row of this warp is one: its P may be anything
+        if (__builtin_expect(!some, 0)) {  // no row of this warp is one: its P may be anything
           tc_fence_before();
           arrive(&B.p_half[b]);
           arrive(&B.p_full[b]);
@@ -759,67 +775,85 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int i = 0; i < 4; ++i) tmem_loaded(sr[i]);
         // The largest product under a negative scale is that of the smallest score.
         // A masked score becomes the infinity whose product is -infinity.
-        if (masked) {
+        auto hide = [&](uint32_t (&x)[32], uint32_t seen) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t seen = i == 0 ? bits.x : i == 1 ? bits.y : i == 2 ? bits.z : bits.w;
-#pragma unroll
-            for (int x = 0; x < 32; ++x) sr[i][x] = seen & 1u << x ? sr[i][x] : __float_as_uint(none);
-          }
+          for (int i = 0; i < 32; ++i) x[i] = seen & 1u << i ? x[i] : __float_as_uint(none);
+        };
+        if (__builtin_expect(masked, 0)) {
+          hide(sr[0], bits.x);
+          hide(sr[1], bits.y);
+          hide(sr[2], bits.z);
+          hide(sr[3], bits.w);
         }
         float mx = c < 0.f ? extremum<128, false>(&sr[0][0]) : extremum<128, true>(&sr[0][0]);
         mx = mx == none ? -INFINITY : mx * c;
-        const float m_new = fmaxf(m_ref, mx);
-        const bool grow = m_new > m_ref + 8.f;  // also for the first visible key
-        const bool rescale = grow && m_ref != -INFINITY;
-        if (__any_sync(0xffffffffu, rescale)) {
-          // O holds earlier tiles: after the last of their products (with two streams
-          // that was issued before this score tile, and has ended with it).
-          if (kStreams == 1 && !(alive = wait(&B.o_done[b ^ 1], (used >> (b ^ 1) & 1u) ^ 1u))) break;
-          tc_fence_after();
-          const float f = rescale ? fast_exp2(m_ref - m_new) : 1.f;
-          const uint32_t o_col = lane_addr + (kStreams == 2 ? w * D : 0);
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t o[16];
-            tmem_ld16(o_col + c0, o);
-            tmem_wait_ld();
-            tmem_loaded(o);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-            tmem_st16(o_col + c0, o);
-          }
-          tmem_wait_st();
-        }
-        if (grow) {
-          if (l > 0.f) l *= fast_exp2(m_ref - m_new);
-          m_ref = m_new;
-        }
-        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_use, -m_use);
-        uint64_t acc = f2_pack(0.f, 0.f);
         // P over the first half of its scores, in two halves: the product starts on the
         // first 64 keys while the others are exponentiated.
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t pk[16];
+        uint32_t pk[2][16];
+        const uint64_t c2 = f2_pack(c, c);
+        float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        uint64_t acc = f2_pack(0.f, 0.f), nm2 = f2_pack(-m_use, -m_use);
+        auto weights = [&](const uint32_t (&x)[32], uint32_t (&w16)[16]) {
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const uint64_t x2 =
-                f2_fma(f2_pack(__uint_as_float(sr[i][2 * k]), __uint_as_float(sr[i][2 * k + 1])), c2, nm2);
+                f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, nm2);
             float x0, x1;
             f2_unpack(x2, x0, x1);
             const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
             acc = f2_add(acc, f2_pack(p0, p1));
-            pk[k] = pack_bf16x2(p0, p1);
+            w16[k] = pack_bf16x2(p0, p1);
           }
-          tmem_st16(s_col + 16 * i, pk);
-          if (i == 1) {
+        };
+        weights(sr[0], pk[0]);
+        weights(sr[1], pk[1]);
+        const bool grow = mx > m_ref + kGrow;  // also for the first visible key
+        if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
+          // The reference goes up to the tile's maximum, and these weights are worked out
+          // again (from scores read again); O, which holds earlier tiles, is scaled after
+          // the last of their products (with two streams that was issued before this score
+          // tile, and ended with it).
+          const float f = grow && m_ref != -INFINITY ? fast_exp2(m_ref - mx) : 1.f;
+          if (mine > 0) {
+            if (kStreams == 1 && !(alive = wait(&B.o_done[b ^ 1], (used >> (b ^ 1) & 1u) ^ 1u))) break;
+            tc_fence_after();
+            const uint32_t o_col = lane_addr + (kStreams == 2 ? w * D : 0);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_col + c0, o);
+              tmem_wait_ld();
+              tmem_loaded(o);
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tmem_st16(o_col + c0, o);
+            }
             tmem_wait_st();
-            tc_fence_before();
-            arrive(&B.p_half[b]);
+          }
+          l *= f;
+          if (grow) m_ref = mx;
+          m_use = m_ref == -INFINITY ? 0.f : m_ref;
+          nm2 = f2_pack(-m_use, -m_use);
+          acc = f2_pack(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t again[32];
+            tmem_ld32(s_col + 32 * i, again);
+            tmem_wait_ld();
+            tmem_loaded(again);
+            if (masked) hide(again, i == 0 ? bits.x : bits.y);
+            weights(again, pk[i]);
           }
         }
+        tmem_st16(s_col, pk[0]);
+        tmem_st16(s_col + 16, pk[1]);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(&B.p_half[b]);
+        weights(sr[2], pk[0]);
+        tmem_st16(s_col + 32, pk[0]);
+        weights(sr[3], pk[1]);
+        tmem_st16(s_col + 48, pk[1]);
         float a0, a1;
         f2_unpack(acc, a0, a1);
         l += a0 + a1;
