@@ -36,7 +36,6 @@
 
 #include <algorithm>
 #include <cfloat>
-#include <cmath>
 #include <type_traits>
 
 #include "sm100_ptx.cuh"
@@ -287,19 +286,13 @@ __device__ __noinline__ void add_unseen(const TreeParams& p, const Part a, const
   }
 }
 
-// The largest (or smallest) of N floats, as a tree of three-input operations.
-__device__ __forceinline__ float fmin3(float a, float b, float c) {
-  float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-template <int N, bool kMax>
-__device__ __forceinline__ float extremum(const uint32_t* v) {
+// The largest of N floats (their bits), as a tree of three-input maxima.
+template <int N>
+__device__ __forceinline__ float max_tree(const uint32_t* v) {
   if constexpr (N == 1) {
     return __uint_as_float(v[0]);
   } else if constexpr (N == 2) {
-    return kMax ? fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]))
-                : fminf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+    return fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
   } else {
     constexpr int M = (N + 2) / 3;
     uint32_t t[M];
@@ -307,15 +300,13 @@ __device__ __forceinline__ float extremum(const uint32_t* v) {
     for (int i = 0; i < M; ++i) {
       const float a = __uint_as_float(v[3 * i]);
       float m = a;
-      if (3 * i + 2 < N) {
-        const float b = __uint_as_float(v[3 * i + 1]), c = __uint_as_float(v[3 * i + 2]);
-        m = kMax ? fmax3(a, b, c) : fmin3(a, b, c);
-      } else if (3 * i + 1 < N) {
-        m = kMax ? fmaxf(a, __uint_as_float(v[3 * i + 1])) : fminf(a, __uint_as_float(v[3 * i + 1]));
-      }
+      if (3 * i + 2 < N)
+        m = fmax3(a, __uint_as_float(v[3 * i + 1]), __uint_as_float(v[3 * i + 2]));
+      else if (3 * i + 1 < N)
+        m = fmaxf(a, __uint_as_float(v[3 * i + 1]));
       t[i] = __float_as_uint(m);
     }
-    return extremum<M, kMax>(t);
+    return max_tree<M>(t);
   }
 }
 
@@ -724,7 +715,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int q4 = warp & 3, r = 32 * q4 + lane;        // lane quarter, row
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     const int G = p.group, tok = r / G, hd = r - tok * G;
-    const float c = p.scale_log2, none = c < 0.f ? INFINITY : -INFINITY;
+    const float c = p.scale_log2;
     uint32_t used = 0;  // operations seen of each S buffer, modulo 2: a bit each
     uint32_t parts = 0, merges = 0;
     bool alive = true;
@@ -767,32 +758,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           continue;
         }
         const uint32_t s_col = lane_addr + Lay::kSCol + b * kTreeKeys;
-        uint32_t sr[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(s_col + 32 * i, sr[i]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_loaded(sr[i]);
-        // The largest product under a negative scale is that of the smallest score.
-        // A masked score becomes the infinity whose product is -infinity.
-        auto hide = [&](uint32_t (&x)[32], uint32_t seen) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = seen & 1u << i ? x[i] : __float_as_uint(none);
-        };
-        if (__builtin_expect(masked, 0)) {
-          hide(sr[0], bits.x);
-          hide(sr[1], bits.y);
-          hide(sr[2], bits.z);
-          hide(sr[3], bits.w);
-        }
-        float mx = c < 0.f ? extremum<128, false>(&sr[0][0]) : extremum<128, true>(&sr[0][0]);
-        mx = mx == none ? -INFINITY : mx * c;
+        uint32_t sr[4][32], pk[2][16];
+        const uint64_t c2 = f2_pack(c, c);
+        uint64_t acc, nm2;
         // P over the first half of its scores, in two halves: the product starts on the
         // first 64 keys while the others are exponentiated.
-        uint32_t pk[2][16];
-        const uint64_t c2 = f2_pack(c, c);
-        float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        uint64_t acc = f2_pack(0.f, 0.f), nm2 = f2_pack(-m_use, -m_use);
         auto weights = [&](const uint32_t (&x)[32], uint32_t (&w16)[16]) {
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -805,14 +775,33 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             w16[k] = pack_bf16x2(p0, p1);
           }
         };
-        weights(sr[0], pk[0]);
-        weights(sr[1], pk[1]);
-        const bool grow = mx > m_ref + kGrow;  // also for the first visible key
-        if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
-          // The reference goes up to the tile's maximum, and these weights are worked out
-          // again (from scores read again); O, which holds earlier tiles, is scaled after
-          // the last of their products (with two streams that was issued before this score
-          // tile, and ended with it).
+#pragma unroll 1
+        for (;;) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s_col + 32 * i, sr[i]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_loaded(sr[i]);
+          if (__builtin_expect(masked, 0)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t seen = i == 0 ? bits.x : i == 1 ? bits.y : i == 2 ? bits.z : bits.w;
+#pragma unroll
+              for (int x = 0; x < 32; ++x) sr[i][x] = seen & 1u << x ? sr[i][x] : 0xff800000u;  // -inf
+            }
+          }
+          float mx = max_tree<128>(&sr[0][0]);
+          mx = mx == -INFINITY ? -INFINITY : mx * c;
+          const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+          acc = f2_pack(0.f, 0.f);
+          nm2 = f2_pack(-m_use, -m_use);
+          weights(sr[0], pk[0]);
+          weights(sr[1], pk[1]);
+          const bool grow = mx > m_ref + kGrow;  // also for the first visible key
+          if (__builtin_expect(!__any_sync(0xffffffffu, grow), 1)) break;
+          // The reference goes up to the tile's maximum, and the tile is gone over again; O,
+          // which holds earlier tiles, is scaled after the last of their products (with
+          // two streams that was issued before this score tile, and ended with it).
           const float f = grow && m_ref != -INFINITY ? fast_exp2(m_ref - mx) : 1.f;
           if (mine > 0) {
             if (kStreams == 1 && !(alive = wait(&B.o_done[b ^ 1], (used >> (b ^ 1) & 1u) ^ 1u))) break;
@@ -832,19 +821,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
           l *= f;
           if (grow) m_ref = mx;
-          m_use = m_ref == -INFINITY ? 0.f : m_ref;
-          nm2 = f2_pack(-m_use, -m_use);
-          acc = f2_pack(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t again[32];
-            tmem_ld32(s_col + 32 * i, again);
-            tmem_wait_ld();
-            tmem_loaded(again);
-            if (masked) hide(again, i == 0 ? bits.x : bits.y);
-            weights(again, pk[i]);
-          }
         }
+        if (!alive) break;
         tmem_st16(s_col, pk[0]);
         tmem_st16(s_col + 16, pk[1]);
         tmem_wait_st();
@@ -1161,7 +1139,7 @@ int launch_d(const Plan& plan, const Args& a, cudaStream_t stream) {
   p.out_v8 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 ? 1 : 0;
   // (Not zero: the infinity of a masked score times zero would be NaN.  Under the
   // smallest number no product differs from zero.)
-  p.scale_log2 = std::fabs(a.sm_scale) < FLT_MIN ? FLT_MIN : a.sm_scale * 1.4426950408889634f;
+  p.scale_log2 = std::max(a.sm_scale * 1.4426950408889634f, FLT_MIN);
   CUtensorMap tq, tk, tv;
   const uint64_t pool_rows = static_cast<uint64_t>(plan.num_pages) * plan.p;
   if (!make_tmap_3d(&tq, a.q, D, plan.hq, static_cast<uint64_t>(plan.total_q), G, p.per_tile) ||
@@ -1186,6 +1164,8 @@ bool tree_tc_supported(int32_t head_dim, int32_t page_size, int32_t group) {
 }
 
 int launch_tree_attn(const Plan& plan, const Args& a, void* stream) {
+  // (The maxima are taken before the scale.)
+  if (!(a.sm_scale >= 0.f)) return launch_tree_simt(plan, a, stream);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (plan.d) {
     case 64: return launch_d<64>(plan, a, s);
