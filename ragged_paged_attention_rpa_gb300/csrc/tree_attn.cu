@@ -124,7 +124,7 @@ struct Layout {
 struct Barriers {
   uint64_t q_full, q_empty;
   uint64_t full[12], empty[12];
-  uint64_t s_full[2], p_half[2], p_full[2];
+  uint64_t s_full[2], p_most[2], p_full[2];
   uint64_t o_done[2];       // one stream: a product of each S buffer; two: [0], the part's products
   uint64_t o_free;          // every row of the part's O has been read
   uint64_t xch;             // the streams' maxima and sums are posted
@@ -362,7 +362,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.s_full[i], 1);
-      mbar_init(&B.p_half[i], 4);
+      mbar_init(&B.p_most[i], 4);
       mbar_init(&B.p_full[i], 4);
       mbar_init(&B.o_done[i], 1);
       mbar_init(&B.v_ask[i], 1);
@@ -514,19 +514,21 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       else
         mma_ss_2chunks(sc, qd, kd, kIdS, 0);
     };
-    // O += P V, P in buffer b, V in `slot`, the first 64 keys as soon as their half of P is
+    // O += P V, P in buffer b, V in `slot`, the first 96 keys as soon as their part of P is
     // there; `acc` 0: the stream's first in the part.
     auto mma_pv = [&](auto bc, int slot, uint32_t acc) -> bool {
       constexpr int b = decltype(bc)::value;
       const uint32_t o = tmem + b * D, pc = tmem + Lay::kSCol + b * kTreeKeys;
       const uint64_t vd = v_d0 + static_cast<uint64_t>(slot * (Lay::kSlot >> 4));
-      if (!wait(&B.p_half[b], p_ph >> b & 1u)) return false;
+      if (!wait(&B.p_most[b], p_ph >> b & 1u)) return false;
       tc_fence_after();
+      constexpr uint64_t kHalf = D == 64 ? 512 : kSub / 16;  // 64 keys on
       mma_ts_64keys(o, pc, vd, kIdPV, acc);
+      mma_ts2(o, pc + 32, pc + 40, vd + kHalf, vd + kHalf + 128, kIdPV, 1);
       if (!wait(&B.p_full[b], p_ph >> b & 1u)) return false;
       p_ph ^= 1u << b;
       tc_fence_after();
-      mma_ts_64keys(o, pc + 32, vd + (D == 64 ? 512 : kSub / 16), kIdPV, 1);
+      mma_ts2(o, pc + 48, pc + 56, vd + kHalf + 256, vd + kHalf + 384, kIdPV, 1);
       return true;
     };
     // A masked tile's V: announced where the ring's slots of it hold nothing older that
@@ -642,7 +644,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
             for (int h = 0; h < kSlots; ++h) {
               if (!wait(&B.full[ring.slot], ring.phase)) return false;
-              if (!wait(h == 0 ? &B.p_half[b] : &B.p_full[b], p_ph >> b & 1u)) return false;
+              if (!wait(h == 0 ? &B.p_most[b] : &B.p_full[b], p_ph >> b & 1u)) return false;
               tc_fence_after();
               mma_ts_2x32keys(tmem, tmem + Lay::kSCol + b * kTreeKeys + 32 * h,
                               v_d0 + static_cast<uint64_t>(ring.slot * (Lay::kSlot >> 4)), kIdPV,
@@ -753,7 +755,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tc_fence_after();
         if (__builtin_expect(!some, 0)) {  // no row of this warp is one: its P may be anything
           tc_fence_before();
-          arrive(&B.p_half[b]);
+          arrive(&B.p_most[b]);
           arrive(&B.p_full[b]);
           continue;
         }
@@ -761,8 +763,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         uint32_t sr[4][32], pk[2][16];
         const uint64_t c2 = f2_pack(c, c);
         uint64_t acc, nm2;
-        // P over the first half of its scores, in two halves: the product starts on the
-        // first 64 keys while the others are exponentiated.
+        // P over the first half of its scores, three quarters of it first: the product
+        // starts on these while the others are exponentiated.
         auto weights = [&](const uint32_t (&x)[32], uint32_t (&w16)[16]) {
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -825,11 +827,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (!alive) break;
         tmem_st16(s_col, pk[0]);
         tmem_st16(s_col + 16, pk[1]);
-        tmem_wait_st();
-        tc_fence_before();
-        arrive(&B.p_half[b]);
         weights(sr[2], pk[0]);
         tmem_st16(s_col + 32, pk[0]);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(&B.p_most[b]);
         weights(sr[3], pk[1]);
         tmem_st16(s_col + 48, pk[1]);
         float a0, a1;
