@@ -385,6 +385,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // What came before on the stream has ended (this launch may be early: the barriers and
+  // tensor memory are set up while it ends).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = B.tmem_base;
   Walk<D, N> walk(work);
   Part a{};
@@ -989,6 +992,7 @@ tree_combine_kernel(const __grid_constant__ TreeParams p, const __grid_constant_
   const int row = rows32 * 32 + lane, tile = row / kTreeRows, r = row % kTreeRows, tok = r / p.group;
   const int32_t node = (g.st * tree_row_tiles(D) + tile) * p.per_tile + tok;
   const bool valid = row < kRows && tok < p.per_tile && node < s.nodes;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   auto slot = [&](int k) -> int64_t { return (2ll * (g.cta + k) + (k == 0 ? g.first : 0)) * kRows; };
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float acc[16], sum = 0.f, M = -INFINITY;
@@ -1078,8 +1082,17 @@ int launch_one(const Plan& plan, const TreeLaunch& l, const CUtensorMap& tq, con
   w.seqs.n = l.seq_end - l.seq_begin;
   std::copy(plan.tree_seqs.begin() + l.seq_begin, plan.tree_seqs.begin() + l.seq_end, w.seqs.s);
   std::copy_n(plan.tree_starts.begin() + l.start_begin, l.n_ctas, w.start);
-  tree_attn_kernel<D, N><<<l.n_ctas, Lay::kThreads, Lay::kBytes, stream>>>(tq, tk, tv, p, w);
-  if (cudaError_t e = cudaGetLastError()) return static_cast<int>(e);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3(l.n_ctas);
+  cfg.blockDim = dim3(Lay::kThreads);
+  cfg.dynamicSmemBytes = Lay::kBytes;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<D, N>, tq, tk, tv, p, w)) return static_cast<int>(e);
   trace_mark(RPA_KERNEL_TREE_ATTN, stream);
   if (l.n_cut == 0) return 0;
   CutList<N>& c = thread_staging<CutList<N>>();
@@ -1094,15 +1107,9 @@ int launch_one(const Plan& plan, const TreeLaunch& l, const CUtensorMap& tq, con
     const int32_t rows = nodes > p.per_tile ? kTreeRows + (nodes - p.per_tile) * p.group : nodes * p.group;
     warps = std::max<int64_t>(warps, static_cast<int64_t>((rows + 31) / 32) * (D / 16) * combine_warps(c.cut[i].nparts));
   }
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(l.n_cut, static_cast<unsigned>((warps + 7) / 8));
   cfg.blockDim = dim3(kCombineThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
   if (cudaError_t e = cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, N>, p, c)) return static_cast<int>(e);
   trace_mark(RPA_KERNEL_TREE_COMBINE, stream);
   return 0;
