@@ -669,7 +669,7 @@ rpa_status_t rpa_append_rope(const void* q, const void* k, const void* v, int64_
  *   key C + j, j < q_len, iff bit j % 64 of tree_mask[t][j / 64] is set.
  * Any mask will do (a node need not see itself, and may see a later one).  A row
  * that sees no key, or whose visible scores are all -infinity, is written as zeros.
- * `sm_scale` is any number.
+ * `sm_scale` is any number up to 2^120 in magnitude, else RPA_ERR_INVALID_ARG.
  *
  * The plan must have tree_words > 0; tree_mask [total_q, tree_words] 64-bit words,
  * 8-byte aligned.  positions [total_q] int32 are read where there is a window (with
@@ -678,7 +678,8 @@ rpa_status_t rpa_append_rope(const void* q, const void* k, const void* v, int64_
  * includes the nodes, whose rows are in their pages already.
  *
  * bf16 q, pages and out run on tensor cores (page_size at least 16 and num_q_heads
- * / num_kv_heads at most 128), fp32 and the rest on CUDA cores.  A NaN or an
+ * / num_kv_heads at most 128, sm_scale not below zero), fp32 and the rest on CUDA
+ * cores.  A NaN or an
  * infinity in K or V reaches the rows that see its key, and no other.  Device
  * lengths that differ from the plan's set RPA_DEVERR_LENGTHS; the call goes by the
  * plan's.  The other arguments, the error word, unused slots, threads and CUDA

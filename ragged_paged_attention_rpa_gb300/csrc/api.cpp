@@ -820,6 +820,8 @@ rpa_status_t rpa_forward_tree(const void* q, const void* k_pages, const void* v_
       head_dim != p.d || page_size != p.p || (window != nullptr) != p.has_window ||
       p.tree_words == 0)
     return RPA_ERR_PLAN_MISMATCH;
+  // (Finite, and so times log2 e.)
+  if (!(std::fabs(sm_scale) <= 0x1p120f)) return RPA_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256)) return RPA_ERR_INVALID_ARG;
   if (workspace_bytes < p.ws_bytes) return RPA_ERR_WORKSPACE_TOO_SMALL;
   if (p.total_q == 0) return RPA_OK;

@@ -1174,7 +1174,7 @@ bool tree_tc_supported(int32_t head_dim, int32_t page_size, int32_t group) {
 
 int launch_tree_attn(const Plan& plan, const Args& a, void* stream) {
   // (The maxima are taken before the scale.)
-  if (!(a.sm_scale >= 0.f)) return launch_tree_simt(plan, a, stream);
+  if (a.sm_scale < 0.f) return launch_tree_simt(plan, a, stream);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (plan.d) {
     case 64: return launch_d<64>(plan, a, s);

@@ -329,3 +329,78 @@ def test_random_batches(seed):
     first = t.run(num_sms=sms).clone()
     check(b, first)
     assert torch.equal(first.view(torch.int16), t.run(num_sms=sms).view(torch.int16))
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_infinite_keys(d, path):
+    """A score of -infinity weighs nothing, one of +infinity makes its rows NaN; a row that sees nothing else is zeros."""
+    b = ref.tree_batch([30, 90, 1], [140, 300, 0], 4, 2, d, 16, [0, 100, 0], seed=12)
+    for s, key, g, bad in [(0, 150, 0, float("inf")), (1, 300 - 60, 1, -float("inf")), (1, 388, 0, float("inf"))]:
+        page, i = ref.slot(b, s, key)
+        b.k_pages[page, i, g, 5] = bad
+    page, i = ref.slot(b, 2, 0)
+    b.k_pages[page, i, :, 7] = float("inf")
+    b.q[-1, :, 7] = -b.q[-1, :, 7].abs() - 1
+    want = ref.attention(b)
+    assert (want[0][-1] == 0).all() and torch.isnan(want[0]).any()
+    check(b, Tree(b).run(path=path), want)
+
+
+def test_two_graphs_share_a_workspace():
+    bs = [ref.tree_batch([8] * 10, list(range(50, 2050, 200)), 8, 1, 256, 128, None, seed=13),
+          ref.tree_batch([70, 5], [4000, 900], 8, 2, 128, 32, [0, 500], seed=14)]
+    ts = [Tree(b) for b in bs]
+    plans = [t.plan() for t in ts]
+    ws = max((binding.alloc_workspace(p) for p in plans), key=lambda w: w.nbytes)
+    graphs = []
+    for t, p in zip(ts, plans):
+        binding.rpa_forward_tree(*t.args(p, ws))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(3):
+                binding.rpa_forward_tree(*t.args(p, ws))
+        graphs.append(g)
+    for _ in range(4):
+        for t, g in zip(ts, graphs):
+            t.out.fill_(float("nan"))
+            g.replay()
+    torch.cuda.synchronize()
+    assert binding.rpa_get_device_error(ws) == 0
+    for b, t in zip(bs, ts):
+        check(b, t.out)
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_a_pool_beyond_32_bits(path):
+    """Pages past 2^32 elements: read, written by an append and moved by a commit."""
+    b = ref.tree_batch([20, 9], [700, 130], 8, 2, 128, 256, None, seed=15)
+    t = Tree(b)
+    pages = (1 << 32) // (256 * 2 * 128) + 10
+    shift = pages - b.pool
+    small = t.k_pages, t.v_pages
+    t.k_pages, t.v_pages = (torch.empty((pages, 256, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    b.pool = pages
+    t.table = torch.where(t.table >= 0, t.table + shift, -1).int()
+    for big, s in zip((t.k_pages, t.v_pages), small):
+        big[shift:] = s
+    # The nodes' rows once more, by the append: no rotation.
+    where = torch.tensor([(shift + p) * 256 + i for s in range(2) for p, i in
+                          (ref.slot(b, s, b.ctx[s] + n) for n in range(b.nodes[s]))], device="cuda")
+    assert int(where.min()) * 256 > 1 << 32
+    flat = [x.view(-1, 2, 128) for x in (t.k_pages, t.v_pages)]
+    rows = [f[where].clone() for f in flat]
+    for f in flat:
+        f[where] = float("nan")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    binding.rpa_append_rope(None, *rows, None, where, None, None, t.k_pages, t.v_pages, workspace=ws)
+    assert binding.rpa_get_device_error(ws) == 0
+    assert all(torch.equal(f[where], r) for f, r in zip(flat, rows))
+    check(b, t.run(path=path))
+    moved = torch.tensor([[2, 5, 19], [0, 8, -1]], dtype=torch.int32, device="cuda")
+    binding.rpa_commit_tree(t.k_pages, t.v_pages, where, t.cu, moved, ws)
+    assert binding.rpa_get_device_error(ws) == 0
+    for f, r in zip(flat, rows):
+        assert torch.equal(f[where[:3]], r[[2, 5, 19]]) and torch.equal(f[where[20:22]], r[[20, 28]])
+        assert torch.equal(f[where[3:20]], r[3:20])

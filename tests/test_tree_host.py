@@ -187,3 +187,10 @@ def test_schedules_cover_every_tile_once(tmp_path):
                     "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf"), 3e38, -2.0 ** 121])
+def test_scales_refused(scale):
+    L, p = binding.lib(), plan(nodes=(64, 64), ctx=(5000, 900))
+    args = [A] * 8 + [2, 8, 1, 128, 16, None, scale, A, None, p.handle, 1 << 21, p.workspace_bytes]
+    assert L.rpa_forward_tree(*args) == INVALID
