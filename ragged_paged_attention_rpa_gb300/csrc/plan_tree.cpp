@@ -2,10 +2,13 @@
 //
 // On tensor cores a request's nodes are row tiles of 128 / G nodes by G heads, and
 // a segment is (request, KV head, one or two row tiles) over the 128-key tiles its
-// nodes can see.  The segments' key tiles, each segment's followed by a charge for
-// its ends, form one line, which is cut into equal ranges, one per CTA.
+// nodes can see.  A request's segments run in passes of `width` segments side by side.
+// The passes' key tiles, each pass followed by a charge for its ends, form one line,
+// which is cut into equal ranges, one per group of `width` CTAs: the CTAs of a group
+// read the same keys of a head at the same time, so that all but one find them in L2.
 #include <algorithm>
 #include <cstdint>
+#include <numeric>
 #include <vector>
 
 #include "rpa_internal.h"
@@ -21,72 +24,121 @@ constexpr int32_t kTile = 4;
 constexpr int32_t kSegCost = 6;
 constexpr int32_t kLeast = 4;
 
+// What a key tile that no other CTA of the group reads at the same time costs on top.
+constexpr double kAlone = 0.27;
+constexpr int32_t kMaxWidth = 32;
+
 rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
   const int32_t per = kTreeRows / (plan.hq / plan.hkv) * tree_row_tiles(plan.d);  // nodes of a segment
   const int32_t n_seq = l.seq_end - l.seq_begin;
   auto seq = [&](int32_t i) -> const TreeSeq& { return plan.tree_seqs[l.seq_begin + i]; };
   auto tiles = [&](int32_t i) { return (seq(i).len - 1) / kTreeKeys + 1 - tree_first_tile(seq(i)); };
-  auto segments = [&](int32_t i) { return ceil_div(seq(i).nodes, per); };  // of a head
-  std::vector<int64_t> v0(1, 0);  // the requests' starts on the line
-  for (int32_t i = 0; i < n_seq; ++i)
-    v0.push_back(v0.back() + (static_cast<int64_t>(tiles(i)) * kTile + kSegCost) * segments(i) * plan.hkv);
-  const int64_t total = v0.back();
+  auto per_head = [&](int32_t i) -> int64_t { return seq(i).per_head; };
+  auto segments = [&](int32_t i) { return per_head(i) * plan.hkv; };
+  auto cost = [&](int32_t i) { return static_cast<int64_t>(tiles(i)) * kTile + kSegCost; };
+  int64_t work = 0, most_heads = 0;
+  for (int32_t i = 0; i < n_seq; ++i) {
+    plan.tree_seqs[l.seq_begin + i].per_head = static_cast<int32_t>(ceil_div(seq(i).nodes, per));
+    work += cost(i) * segments(i);
+    most_heads = std::max(most_heads, per_head(i));
+  }
   const int64_t most = std::min<int64_t>(plan.num_sms, kTreeMaxCtas);
-  const int64_t n = std::max<int64_t>(1, std::min(most, total / kLeast));
+  const int64_t ctas = std::max<int64_t>(1, std::min(most, work / kLeast));
+  // The width of least time: the longest lane's tiles, each a little more where its keys
+  // are read by it alone.
+  int64_t width = 1;
+  double least = 0;
+  for (int64_t w = 1; w <= std::min<int64_t>({kMaxWidth, ctas, most_heads > 1 ? kMaxWidth : 1}); ++w) {
+    int64_t line = 0, reads = 0, all = 0;
+    for (int32_t i = 0; i < n_seq; ++i) {
+      const int64_t passes = ceil_div(segments(i), w), s = per_head(i), step = s / std::gcd(s, w);
+      line += passes * cost(i);
+      // Heads that the passes read: one more for each pass that begins inside a head.
+      reads += (plan.hkv + passes - 1 - (passes - 1) / step) * tiles(i);
+      all += segments(i) * tiles(i);
+    }
+    const double t = static_cast<double>(line) / static_cast<double>(ctas / w) * (1 + kAlone * reads / all);
+    if (w > 1 && t >= least) continue;
+    least = t;
+    width = w;
+  }
+  const int64_t groups = ctas / width;
+  std::vector<int64_t> v0(1, 0);  // the requests' starts on the line
+  for (int32_t i = 0; i < n_seq; ++i) v0.push_back(v0.back() + cost(i) * ceil_div(segments(i), width));
+  const int64_t total = v0.back();
   // (A range's tiles travel in 31 bits.)
-  if (ceil_div(total, n) > 0x3fffffff) return RPA_ERR_UNSUPPORTED;
+  if (ceil_div(total, groups) > 0x3fffffff) return RPA_ERR_UNSUPPORTED;
   l.start_begin = static_cast<int32_t>(plan.tree_starts.size());
-  l.n_ctas = static_cast<int32_t>(n);
+  l.n_ctas = static_cast<int32_t>(groups * width);
   l.cut_begin = static_cast<int32_t>(plan.tree_cuts.size());
+  l.width = static_cast<int32_t>(width);
+  // A lane's segments of request i: lane, lane + width, ...
+  auto of_lane = [&](int32_t i, int64_t lane) { return segments(i) <= lane ? 0 : (segments(i) - lane - 1) / width + 1; };
+  std::vector<int64_t> before(width, 0);  // the lanes' tiles before request `i`
+  std::vector<int64_t> done(width, 0);    // ... before the current range
+  std::vector<int32_t> last(width, -1);   // the lanes' last cuts
   int32_t i = 0;
-  int64_t done = 0;  // tiles before the current range, charges left out
-  std::vector<int64_t> before(1, 0);
-  for (int32_t k = 0; k < n_seq; ++k) before.push_back(before.back() + tiles(k) * segments(k) * plan.hkv);
-  for (int64_t c = 0; c <= n; ++c) {
-    const int64_t x = total * c / n;
-    while (i < n_seq && v0[i + 1] <= x) ++i;
-    // The boundary as a tile: one inside a charge is the segment's end.
-    TreeStart st{i, 0, 0, 0, 0};
-    int64_t at = before[i];
-    bool inside = false;
+  for (int64_t g = 0; g <= groups; ++g) {
+    const int64_t x = total * g / groups;
+    for (; i < n_seq && v0[i + 1] <= x; ++i)
+      for (int64_t lane = 0; lane < width; ++lane) before[lane] += of_lane(i, lane) * tiles(i);
+    // The boundary as a pass and a tile: one inside a charge is the pass's end.
+    int64_t pass = 0, j = 0;
     if (i < n_seq) {
-      const int64_t cost = static_cast<int64_t>(tiles(i)) * kTile + kSegCost, off = (x - v0[i]) % cost / kTile;
-      int64_t sg = (x - v0[i]) / cost;
-      at += sg * tiles(i) + std::min<int64_t>(off, tiles(i));
-      inside = off > 0 && off < tiles(i);
-      if (off >= tiles(i)) ++sg;  // the next segment's first tile
-      const int64_t per_head = segments(i);
-      if (sg == per_head * plan.hkv) {
-        st.i = i + 1;
-      } else {
-        st.head = static_cast<int32_t>(sg / per_head);
-        st.st = static_cast<int32_t>(sg % per_head);
-        st.j = inside ? static_cast<int32_t>(off) : 0;
+      pass = (x - v0[i]) / cost(i);
+      j = (x - v0[i]) % cost(i) / kTile;
+      if (j >= tiles(i)) {
+        ++pass;
+        j = 0;
       }
     }
-    if (c > 0) plan.tree_starts.back().tiles = static_cast<int32_t>(at - done);
-    done = at;
-    if (c == n) break;
-    plan.tree_starts.push_back(st);
-    if (!inside) continue;
-    // The segment is cut here: between this CTA and the one before it.
-    TreeCut* last = l.n_cut > 0 ? &plan.tree_cuts.back() : nullptr;
-    if (last && last->i == st.i && last->head == st.head && last->st == st.st) {
-      ++last->nparts;
-    } else {
-      const TreeStart& prev = plan.tree_starts[plan.tree_starts.size() - 2];
-      const int32_t first = prev.i == st.i && prev.head == st.head && prev.st == st.st ? 0 : 1;
-      plan.tree_cuts.push_back({st.i, st.head, st.st, static_cast<int32_t>(c - 1), first, 2});
-      ++l.n_cut;
+    for (int64_t lane = 0; lane < width; ++lane) {
+      // The lane's first tile from there on.
+      TreeStart st{i, 0, 0, 0, 0, static_cast<int32_t>(lane)};
+      int64_t at = before[lane], seg = pass * width + lane;
+      bool inside = false;
+      if (i < n_seq && seg < segments(i)) {
+        at += pass * tiles(i) + j;
+        inside = j > 0;
+        st.j = static_cast<int32_t>(j);
+      } else {
+        if (i < n_seq) {
+          at += of_lane(i, lane) * tiles(i);
+          ++st.i;
+        }
+        while (st.i < n_seq && segments(st.i) <= lane) ++st.i;
+        seg = lane;
+      }
+      if (st.i < n_seq) {
+        st.head = static_cast<int32_t>(seg / per_head(st.i));
+        st.st = static_cast<int32_t>(seg % per_head(st.i));
+      }
+      TreeStart* prev = g > 0 ? &plan.tree_starts[l.start_begin + (g - 1) * width + lane] : nullptr;
+      if (prev) prev->tiles = static_cast<int32_t>(at - done[lane]);
+      done[lane] = at;
+      if (g == groups) continue;
+      plan.tree_starts.push_back(st);
+      if (!inside) continue;
+      // The segment is cut here: between this CTA and the lane's one before it.
+      prev = &plan.tree_starts[l.start_begin + (g - 1) * width + lane];
+      TreeCut* cut = last[lane] >= 0 ? &plan.tree_cuts[last[lane]] : nullptr;
+      if (cut && cut->i == st.i && cut->head == st.head && cut->st == st.st) {
+        ++cut->nparts;
+      } else {
+        const int32_t first = prev->i == st.i && prev->head == st.head && prev->st == st.st ? 0 : 1;
+        last[lane] = static_cast<int32_t>(plan.tree_cuts.size());
+        plan.tree_cuts.push_back({st.i, st.head, st.st, static_cast<int32_t>((g - 1) * width + lane), first, 2});
+        ++l.n_cut;
+      }
     }
   }
   for (int32_t k = 0; k < l.n_cut; ++k)
     plan.max_splits = std::max(plan.max_splits, plan.tree_cuts[l.cut_begin + k].nparts);
   plan.max_splits = std::max(plan.max_splits, 1);
   plan.kv_split = std::max(plan.kv_split, static_cast<int32_t>(std::min<int64_t>(
-                                              ceil_div(total, n * kTile) * kTreeKeys, 0x7fffffff)));
-  plan.decode_ctas += n;
-  plan.tree_slots = std::max(plan.tree_slots, static_cast<int32_t>(2 * n));
+                                              ceil_div(total, groups * kTile) * kTreeKeys, 0x7fffffff)));
+  plan.decode_ctas += l.n_ctas;
+  plan.tree_slots = std::max(plan.tree_slots, 2 * l.n_ctas);
   return RPA_OK;
 }
 
@@ -111,12 +163,12 @@ rpa_status_t build_tree_schedule(Plan& plan, const int32_t* cu, const int32_t* k
   for (int32_t s = 0; s < plan.num_seqs; ++s) {
     const int32_t n = cu[s + 1] - cu[s];
     if (n > 64 * opts.tree_words) return RPA_ERR_INVALID_ARG;
-    if (n > 0) plan.tree_seqs.push_back({s, cu[s], n, kv[s], win ? std::max(win[s], 0) : 0});
+    if (n > 0) plan.tree_seqs.push_back({s, cu[s], n, kv[s], win ? std::max(win[s], 0) : 0, 0});
   }
   const int32_t total = static_cast<int32_t>(plan.tree_seqs.size());
   plan.num_decode = total;
   for (int32_t i = 0; i < total; i += kTreeSeqsLarge) {
-    TreeLaunch l{i, std::min(total, i + kTreeSeqsLarge), 0, 0, 0, 0};
+    TreeLaunch l{i, std::min(total, i + kTreeSeqsLarge), 0, 0, 0, 0, 1};
     if (plan.path == RPA_PATH_TC)
       if (rpa_status_t st = cut_line(plan, l)) return st;
     plan.tree_launches.push_back(l);

@@ -115,21 +115,24 @@ constexpr int kKv4ExpandSeqs = 1024;
 // the page table, first node, nodes, keys (nodes included) and window.
 struct TreeSeq {
   int32_t seq, q0, nodes, len, window;
+  int32_t per_head;  // segments of a head (tensor cores)
 };
 // Row tiles of the tensor-core kernel: 128 rows are 128 / G nodes of G heads; a
 // segment is (request, KV head, row_tiles(D) such tiles), its keys in tiles of 128.
-// The segments' key tiles lie end to end and every CTA takes a contiguous range:
-// `tiles` of them from tile j of (request i, head, segment st) on.
+// A request's segments, in (head, row tiles) order, run in passes of `width` segments, a
+// lane each; the passes' key tiles lie end to end, and a group of `width` CTAs, one per
+// lane, takes a contiguous range of them: for a CTA `tiles` tiles of its lane from tile j
+// of (request i, head, segment st) on.
 struct TreeStart {
-  int32_t i, head, st, j, tiles;
+  int32_t i, head, st, j, tiles, lane;
 };
-// A segment cut across CTAs cta .. cta + nparts - 1: the first holds its partial in
-// slot 2 cta + first, each later CTA c in slot 2 c.
+// A segment cut across CTAs cta, cta + width, ..., nparts of them: the first holds its
+// partial in slot 2 cta + first, each later CTA c in slot 2 c.
 struct TreeCut {
   int32_t i, head, st, cta, first, nparts;
 };
 struct TreeLaunch {
-  int32_t seq_begin, seq_end, start_begin, n_ctas, cut_begin, n_cut;
+  int32_t seq_begin, seq_end, start_begin, n_ctas, cut_begin, n_cut, width;
 };
 constexpr int kTreeMaxWords = 16;
 constexpr int kTreeRows = 128;

@@ -4,9 +4,9 @@
 // nodes of its mask.  The 128 rows of an MMA are 128 / G nodes by the G query heads
 // of one KV head; a segment is (request, KV head, one such row tile, or two where
 // head_dim leaves tensor memory for two outputs), its keys come in tiles of 128.
-// plan_tree.cpp lays the segments' tiles end to end and cuts the line into equal
-// ranges, one per CTA, one CTA per SM: few rows over long contexts are bound by HBM,
-// and only all SMs together reach it.  A CTA's range is a list of parts of segments;
+// plan_tree.cpp lays the segments' tiles end to end (where a head has several segments,
+// these side by side) and cuts the line into equal ranges, one per CTA, one CTA per SM: few
+// rows over long contexts are bound by HBM, and only all SMs together reach it.  A CTA's range is a list of parts of segments;
 // a part that is not its whole segment leaves fp32 O / l and log2-sum-exps, which
 // tree_combine_kernel joins.
 //
@@ -90,7 +90,7 @@ struct TreeParams {
   unsigned char* ws;
   int32_t hq, hkv, group, per_tile;  // nodes a row tile
   int32_t page_size, page_shift, mpps, num_pages, words;
-  int32_t box_rows_k, box_rows_v, v_4d, out_v8;
+  int32_t box_rows_k, box_rows_v, v_4d, out_v8, width;  // width: lanes of a group of CTAs
   float scale_log2;  // sm_scale log2(e)
 };
 
@@ -179,14 +179,15 @@ struct Walk {
     j += a.n;
     if (j == nb) {
       j = 0;
-      if (a.node0 + per >= a.s.nodes) {
-        st = 0;
+      // The lane's next segment; a request begins with a new pass.
+      st += p.width;
+      while (left > 0 && st >= w.seqs.s[i].per_head) {
+        st -= w.seqs.s[i].per_head;
         if (++head == p.hkv) {
           head = 0;
+          st = w.start[blockIdx.x].lane;
           ++i;
         }
-      } else {
-        ++st;
       }
     }
     return true;
@@ -256,7 +257,7 @@ __device__ __noinline__ bool make_safe(uint8_t* piece, int32_t key, int32_t lo, 
 
 // The bits of 128 keys (tree_sees32), out of the way of the tiles that need none.
 __device__ __noinline__ uint4 tree_sees128(int32_t len, int32_t nodes, const uint64_t* row, int32_t lo, int32_t key) {
-  const TreeSeq s{0, 0, nodes, len, 0};
+  const TreeSeq s{0, 0, nodes, len, 0, 0};
   return make_uint4(tree_sees32(s, row, lo, key), tree_sees32(s, row, lo, key + 32), tree_sees32(s, row, lo, key + 64),
                     tree_sees32(s, row, lo, key + 96));
 }
@@ -993,7 +994,7 @@ tree_combine_kernel(const __grid_constant__ TreeParams p, const __grid_constant_
   const int32_t node = (g.st * tree_row_tiles(D) + tile) * p.per_tile + tok;
   const bool valid = row < kRows && tok < p.per_tile && node < s.nodes;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  auto slot = [&](int k) -> int64_t { return (2ll * (g.cta + k) + (k == 0 ? g.first : 0)) * kRows; };
+  auto slot = [&](int k) -> int64_t { return (2ll * (g.cta + k * p.width) + (k == 0 ? g.first : 0)) * kRows; };
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float acc[16], sum = 0.f, M = -INFINITY;
 #pragma unroll
@@ -1157,6 +1158,7 @@ int launch_d(const Plan& plan, const Args& a, cudaStream_t stream) {
                : make_tmap_3d(&tv, a.v_pages, D, plan.hkv, pool_rows, 1, p.box_rows_v)))
     return static_cast<int>(cudaErrorInvalidValue);
   for (const TreeLaunch& l : plan.tree_launches) {
+    p.width = l.width;
     const int e = l.seq_end - l.seq_begin <= kTreeSeqsSmall
                       ? launch_one<D, kTreeSeqsSmall>(plan, l, tq, tk, tv, p, stream)
                       : launch_one<D, kTreeSeqsLarge>(plan, l, tq, tk, tv, p, stream);

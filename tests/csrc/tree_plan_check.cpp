@@ -20,7 +20,7 @@ bool tree_tc_supported(int32_t, int32_t, int32_t) { return true; }
 int main() {
   std::mt19937 rng(7);
   auto pick = [&](int lo, int hi) { return std::uniform_int_distribution<int>(lo, hi)(rng); };
-  long cuts = 0, parts_seen = 0;
+  long cuts = 0, parts_seen = 0, widths = 0;
   for (int batch = 0; batch < 3000; ++batch) {
     rpa::Plan p;
     const int dims[] = {64, 128, 256};
@@ -48,18 +48,22 @@ int main() {
       CHECK(l.seq_begin == seqs && l.seq_end > l.seq_begin && l.seq_end - l.seq_begin <= rpa::kTreeSeqsLarge);
       seqs = l.seq_end;
       CHECK(l.n_ctas >= 1 && l.n_ctas <= p.num_sms && l.n_ctas <= rpa::kTreeMaxCtas);
-      int i = 0, head = 0, st = 0, j = 0;  // the next tile
+      CHECK(l.width >= 1 && l.n_ctas % l.width == 0);
+      widths += l.width > 1;
       std::map<std::tuple<int, int, int>, std::vector<std::pair<int, int>>> where;  // (cta, slot) of cut segments' parts
-      for (int c = 0; c < l.n_ctas; ++c) {
+      std::map<std::tuple<int, int, int>, int> seen;                                // tiles of each segment so far
+      for (int c = 0; c < l.n_ctas; ++c) {  // (a lane's CTAs come in the order of their keys)
         const rpa::TreeStart& s = p.tree_starts[l.start_begin + c];
         CHECK(s.tiles >= 0);
-        int left = s.tiles, ordinal = 0;
-        if (left > 0) CHECK(s.i == i && s.head == head && s.st == st && s.j == j);
+        int left = s.tiles, ordinal = 0, i = s.i, head = s.head, st = s.st, j = s.j;
         while (left > 0) {
-          CHECK(i < l.seq_end - l.seq_begin);
+          CHECK(i >= 0 && i < l.seq_end - l.seq_begin && head >= 0 && head < p.hkv && st >= 0);
           const rpa::TreeSeq& q = p.tree_seqs[l.seq_begin + i];
+          const int per_head = (q.nodes + per - 1) / per;
+          CHECK(st < per_head && (head * per_head + st) % l.width == c % l.width);
           const int nb = (q.len - 1) / 128 + 1 - rpa::tree_first_tile(q), n = std::min(left, nb - j);
-          CHECK(n >= 1);
+          CHECK(n >= 1 && (seen[{i, head, st}] == j));
+          seen[{i, head, st}] += n;
           if (n < nb) where[{i, head, st}].push_back({c, 2 * c + (ordinal > 0)});
           ++ordinal;
           ++parts_seen;
@@ -67,23 +71,35 @@ int main() {
           j += n;
           if (j == nb) {
             j = 0;
-            if ((st + 1) * per >= q.nodes) {
-              st = 0;
-              if (++head == p.hkv) head = 0, ++i;
-            } else {
-              ++st;
+            int at = head * per_head + st + l.width;  // the request's segment
+            if (at >= per_head * p.hkv) {
+              at = c % l.width;
+              do ++i;
+              while (i < l.seq_end - l.seq_begin &&
+                     (p.tree_seqs[l.seq_begin + i].nodes + per - 1) / per * p.hkv <= at);
+            }
+            if (i < l.seq_end - l.seq_begin) {
+              const int next = (p.tree_seqs[l.seq_begin + i].nodes + per - 1) / per;
+              head = at / next;
+              st = at % next;
             }
           }
         }
       }
-      CHECK(i == l.seq_end - l.seq_begin && head == 0 && st == 0 && j == 0);
+      for (int i = 0; i < l.seq_end - l.seq_begin; ++i) {
+        const rpa::TreeSeq& q = p.tree_seqs[l.seq_begin + i];
+        for (int head = 0; head < p.hkv; ++head)
+          for (int st = 0; st * per < q.nodes; ++st)
+            CHECK((seen[{i, head, st}] == (q.len - 1) / 128 + 1 - rpa::tree_first_tile(q)));
+      }
       CHECK(static_cast<int>(where.size()) == l.n_cut && l.n_cut <= rpa::kTreeMaxCtas);
       for (int k = 0; k < l.n_cut; ++k) {
         const rpa::TreeCut& c = p.tree_cuts[l.cut_begin + k];
         const auto& w = where.at({c.i, c.head, c.st});
         CHECK(static_cast<int>(w.size()) == c.nparts);
         for (int x = 0; x < c.nparts; ++x) {
-          CHECK(w[x].first == c.cta + x && w[x].second == 2 * (c.cta + x) + (x == 0 ? c.first : 0));
+          const int at = c.cta + x * l.width;
+          CHECK(w[x].first == at && w[x].second == 2 * at + (x == 0 ? c.first : 0));
           CHECK(w[x].second < p.tree_slots);
         }
         ++cuts;
@@ -93,6 +109,6 @@ int main() {
     const size_t rows = static_cast<size_t>(p.tree_slots) * 128 * rpa::tree_row_tiles(p.d);
     CHECK(p.tree_cuts.empty() || p.ws_bytes >= 256 + rows * (p.d + 1) * 4);
   }
-  std::printf("tree plans ok: %ld parts, %ld cut segments\n", parts_seen, cuts);
+  std::printf("tree plans ok: %ld parts, %ld cut segments, %ld launches of several lanes\n", parts_seen, cuts, widths);
   return 0;
 }
