@@ -42,7 +42,7 @@ rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
   auto cost = [&](int32_t i) { return static_cast<int64_t>(tiles(i)) * kTile + kSegCost; };
   int64_t work = 0, most_heads = 0;
   for (int32_t i = 0; i < n_seq; ++i) {
-    plan.tree_seqs[l.seq_begin + i].per_head = static_cast<int32_t>(ceil_div(seq(i).nodes, per));
+    plan.tree_seqs[l.seq_begin + i].per_head = static_cast<uint16_t>(ceil_div(seq(i).nodes, per));
     work += cost(i) * segments(i);
     most_heads = std::max(most_heads, per_head(i));
   }
@@ -98,7 +98,7 @@ rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
     }
     for (int64_t lane = 0; lane < width; ++lane) {
       // The lane's first tile from there on.
-      TreeStart st{i, 0, 0, 0, 0, static_cast<int32_t>(lane)};
+      TreeStart st{static_cast<uint16_t>(i), 0, 0, static_cast<uint16_t>(lane), 0, 0};
       int64_t at = before[lane], seg = pass * width + lane;
       bool inside = false;
       if (i < n_seq && seg < segments(i)) {
@@ -114,8 +114,8 @@ rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
         seg = lane;
       }
       if (st.i < n_seq) {
-        st.head = static_cast<int32_t>(seg / per_head(st.i));
-        st.st = static_cast<int32_t>(seg % per_head(st.i));
+        st.head = static_cast<uint16_t>(seg / per_head(st.i));
+        st.st = static_cast<uint16_t>(seg % per_head(st.i));
       }
       TreeStart* prev = g > 0 ? &plan.tree_starts[l.start_begin + (g - 1) * width + lane] : nullptr;
       if (prev) prev->tiles = static_cast<int32_t>(at - done[lane]);
@@ -129,15 +129,15 @@ rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
       if (cut && cut->i == st.i && cut->head == st.head && cut->st == st.st) {
         ++cut->nparts;
       } else {
-        const int32_t first = prev->i == st.i && prev->head == st.head && prev->st == st.st ? 0 : 1;
+        const uint16_t first = prev->i == st.i && prev->head == st.head && prev->st == st.st ? 0 : 1;
         last[lane] = static_cast<int32_t>(plan.tree_cuts.size());
-        plan.tree_cuts.push_back({st.i, st.head, st.st, static_cast<int32_t>((g - 1) * width + lane), first, 2});
+        plan.tree_cuts.push_back({st.i, st.head, st.st, static_cast<uint16_t>((g - 1) * width + lane), first, 2});
         ++l.n_cut;
       }
     }
   }
   for (int32_t k = 0; k < l.n_cut; ++k)
-    plan.max_splits = std::max(plan.max_splits, plan.tree_cuts[l.cut_begin + k].nparts);
+    plan.max_splits = std::max<int32_t>(plan.max_splits, plan.tree_cuts[l.cut_begin + k].nparts);
   plan.max_splits = std::max(plan.max_splits, 1);
   plan.kv_split = std::max(plan.kv_split, static_cast<int32_t>(std::min<int64_t>(
                                               ceil_div(total, groups * kTile) * kTreeKeys, 0x7fffffff)));
@@ -167,7 +167,8 @@ rpa_status_t build_tree_schedule(Plan& plan, const int32_t* cu, const int32_t* k
   for (int32_t s = 0; s < plan.num_seqs; ++s) {
     const int32_t n = cu[s + 1] - cu[s];
     if (n > 64 * opts.tree_words) return RPA_ERR_INVALID_ARG;
-    if (n > 0) plan.tree_seqs.push_back({s, cu[s], n, kv[s], win ? std::max(win[s], 0) : 0, 0});
+    if (n > 0)
+      plan.tree_seqs.push_back({s, cu[s], kv[s], win ? std::max(win[s], 0) : 0, static_cast<uint16_t>(n), 0});
   }
   const int32_t total = static_cast<int32_t>(plan.tree_seqs.size());
   plan.num_decode = total;

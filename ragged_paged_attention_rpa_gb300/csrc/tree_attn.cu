@@ -36,9 +36,9 @@
 // What bounds it.  Long contexts, HBM: 32 requests of 16 to 48 nodes after 4k to 32k keys
 // (32 heads of 128, 8 KV heads) read 2.17 GB in 365 us, 6.0 TB/s.  Many nodes, the tensor
 // cores and the softmax between their products: 8 requests of 256 nodes (64 heads of 128)
-// take 215 us, 1390 TFLOP/s; segments that need no cut run at 1790, and 10 us are the
+// take 213 us, 1405 TFLOP/s; segments that need no cut run at 1790, and 10 us are the
 // combine's.  128 requests of 8 nodes (8 heads of 256, one KV head) after 120 to 2040 keys:
-// 37.5 us for 137 MB: 30 here (HBM's share of 22, the start, ranges that end apart), the
+// 37.3 us for 137 MB: 30 here (HBM's share of 22, the start, ranges that end apart), the
 // rest the combine and its launch.
 //
 // Measured against this: no second MMA warp (one a stream: 326 us where 255 were, the two
@@ -270,7 +270,7 @@ __device__ __noinline__ bool make_safe(uint8_t* piece, int32_t key, int32_t lo, 
 
 // The bits of 128 keys (tree_sees32), out of the way of the tiles that need none.
 __device__ __noinline__ uint4 tree_sees128(int32_t len, int32_t nodes, const uint64_t* row, int32_t lo, int32_t key) {
-  const TreeSeq s{0, 0, nodes, len, 0, 0};
+  const TreeSeq s{0, 0, len, 0, static_cast<uint16_t>(nodes), 0};
   return make_uint4(tree_sees32(s, row, lo, key), tree_sees32(s, row, lo, key + 32), tree_sees32(s, row, lo, key + 64),
                     tree_sees32(s, row, lo, key + 96));
 }
@@ -990,22 +990,22 @@ struct CutList {
 
 // The parts of each cut segment joined: out = sum_k 2^(lse_k - M) O_k / sum_k
 // 2^(lse_k - M), M the largest lse_k.  A thread has 16 columns of a row, a warp those of
-// 32 rows.  Many parts are shared out to several warps, which add up in shared memory.
+// 32 rows.  Many parts are shared out to several warps, which add up in shared memory (6
+// parts of one request: 8.24 us in all, 8.57 by one warp).
 // 38 MB of partials (8 requests of 256 nodes) take 10 us, the few rows of 128 requests of 8
 // nodes 4.5, a launch and its reads.  Joined in the attention kernel by the last CTA of a
 // segment to end, these two took 253 us in place of 241 and 42.9 in place of 37.6: a CTA
 // has too few loads in flight.
 constexpr int kCombineThreads = 256;
 __host__ __device__ constexpr int combine_warps(int nparts) { return nparts <= 4 ? 1 : nparts <= 16 ? 4 : 8; }
-template <int D, int N>
+template <int D, int N, bool kShared>
 __global__ void __launch_bounds__(kCombineThreads, 4)
 tree_combine_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CutList<N> list) {
   constexpr int kRows = kTreeRows * tree_row_tiles(D), kAtOnce = 2;
-  __shared__ float sums[8][17][32];
   const TreeCut& g = list.cut[blockIdx.x];
   const TreeSeq& s = list.seqs.s[g.i];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int W = combine_warps(g.nparts), share = warp & (W - 1);
+  const int W = kShared ? combine_warps(g.nparts) : 1, share = warp & (W - 1);
   const int unit = (blockIdx.y * 8 + warp) / W, rows32 = unit / (D / 16), col = unit % (D / 16) * 16;
   const int row = rows32 * 32 + lane, tile = row / kTreeRows, r = row % kTreeRows, tok = r / p.group;
   const int32_t node = (g.st * tree_row_tiles(D) + tile) * p.per_tile + tok;
@@ -1057,7 +1057,8 @@ tree_combine_kernel(const __grid_constant__ TreeParams p, const __grid_constant_
       }
     }
   }
-  if (W > 1) {
+  if (kShared && W > 1) {
+    __shared__ float sums[kShared ? 8 : 1][17][32];
     // The shares' maxima, then their sums under the largest.
     sums[warp][16][lane] = M;
     __syncthreads();
@@ -1119,8 +1120,10 @@ int launch_one(const Plan& plan, const TreeLaunch& l, const CUtensorMap& tq, con
   // Warps of the segment that wants most: 32 rows and 16 columns each, times the shares
   // of its parts.
   int64_t warps = 0;
+  bool shared = false;
   for (int i = 0; i < l.n_cut; ++i) {
-    const int32_t nodes = std::min(w.seqs.s[c.cut[i].i].nodes - c.cut[i].st * p.per_tile * Lay::kStreams,
+    shared |= combine_warps(c.cut[i].nparts) > 1;
+    const int32_t nodes = std::min<int32_t>(w.seqs.s[c.cut[i].i].nodes - c.cut[i].st * p.per_tile * Lay::kStreams,
                                    p.per_tile * Lay::kStreams);
     const int32_t rows = nodes > p.per_tile ? kTreeRows + (nodes - p.per_tile) * p.group : nodes * p.group;
     warps = std::max<int64_t>(warps, static_cast<int64_t>((rows + 31) / 32) * (D / 16) * combine_warps(c.cut[i].nparts));
@@ -1128,7 +1131,9 @@ int launch_one(const Plan& plan, const TreeLaunch& l, const CUtensorMap& tq, con
   cfg.gridDim = dim3(l.n_cut, static_cast<unsigned>((warps + 7) / 8));
   cfg.blockDim = dim3(kCombineThreads);
   cfg.dynamicSmemBytes = 0;
-  if (cudaError_t e = cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, N>, p, c)) return static_cast<int>(e);
+  if (cudaError_t e = shared ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, N, true>, p, c)
+                             : cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, N, false>, p, c))
+    return static_cast<int>(e);
   trace_mark(RPA_KERNEL_TREE_COMBINE, stream);
   return 0;
 }
