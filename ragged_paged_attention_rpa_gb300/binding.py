@@ -738,8 +738,9 @@ def rpa_append_rope(q, k, v, positions, slot_map, inv_freq, q_out, k_pages, v_pa
         kss, vss = _addr(k_scale, "k_scale", torch.float32, dev), _addr(v_scale, "v_scale", torch.float32, dev)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale are for e4m3 pages")
-    rope = Rope(None, 0, 0)
-    if inv_freq is not None:
+    if inv_freq is None:
+        rope = Rope(None, 0, 0)
+    else:
         rope = Rope(_addr(inv_freq, "inv_freq", torch.float32, dev), 2 * inv_freq.numel(), int(interleaved))
     rc = lib().rpa_append_rope(
         qp, kp, vp, qs, ks, vs, None if positions is None else _addr(positions, "positions", torch.int32, dev),
@@ -748,6 +749,12 @@ def rpa_append_rope(q, k, v, positions, slot_map, inv_freq, q_out, k_pages, v_pa
         _optional_workspace(workspace, dev), st)
     if rc != RPA_OK:
         raise RpaError(rc, "rpa_append_rope")
+
+
+def _at_least(t, shape):
+    """Whether t has `shape`, or more rows of it."""
+    s = t.shape
+    return s == shape or (len(s) == len(shape) and s[0] >= shape[0] and s[1:] == shape[1:])
 
 
 def _tree_args(q, k_pages, v_pages, page_table, cu_q_lens, kv_lens, tree_mask, positions, window, sm_scale,
@@ -759,13 +766,10 @@ def _tree_args(q, k_pages, v_pages, page_table, cu_q_lens, kv_lens, tree_mask, p
     i32 = torch.int32
     dt = torch.bfloat16 if m["dtype"] == RPA_DTYPE_BF16 else torch.float32
     s, total, words = m["num_seqs"], m["total_q"], m["tree_words"]
-    pool = (m["page_size"], m["num_kv_heads"], m["head_dim"])
-    if (len(k_pages.shape) != 4 or k_pages.shape[1:] != pool or v_pages.shape != k_pages.shape
-            or k_pages.shape[0] < m["num_pages"]):
+    pool = (m["num_pages"], m["page_size"], m["num_kv_heads"], m["head_dim"])
+    if not _at_least(k_pages, pool) or v_pages.shape != k_pages.shape:
         raise ValueError("the pools' shape differs from the plan's")
-    rows = m["q_shape"][1:]
-    if (q.dim() != 3 or out.dim() != 3 or q.shape[1:] != rows or out.shape[1:] != rows
-            or q.shape[0] < total or out.shape[0] < total):
+    if not _at_least(q, m["q_shape"]) or not _at_least(out, m["q_shape"]):
         raise ValueError("q and out must be [>= %d, %d, %d]" % m["q_shape"])
     if (page_table.shape != m["table_shape"] or cu_q_lens.numel() != s + 1 or kv_lens.numel() != s
             or (window is not None and window.numel() != s)):
