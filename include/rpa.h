@@ -622,7 +622,7 @@ rpa_status_t rpa_build_tree(const int32_t* parents, const int32_t* cu_q_lens,
  * of every q and k row become x cos a - y sin a and y cos a + x sin a, where (x, y)
  * are (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when `interleaved` is nonzero;
  * dimensions from rotary_dim on, and v, stay as they are.  fp32 arithmetic; the
- * angle is reduced in fixed point, its error at most 2^-47 |a| + 2^-23.  Any int32
+ * angle is reduced in fixed point, its error at most 2^-47 |a| + 2^-28.  Any int32
  * is a position.
  */
 typedef struct rpa_rope {

@@ -7,8 +7,10 @@
 // inv_freq / 2 pi is taken modulo 1 too (a position is a whole number) as a 64-bit
 // fraction F; pos * F modulo 2^64 is then one wrapping product and exact.  F comes
 // from a product of two floats and two floats' worth of 1 / 2 pi, the rounding
-// error kept by an FMA: 48 bits of it are right.  The fraction's upper 32 bits,
-// signed, are half turns for sincospif.
+// error kept by an FMA: 48 bits of it are right.  Its upper two bits, rounded, are quarter
+// turns; of the rest, signed, 24 bits go through sincospif, and eight more by their
+// first derivatives (a page of e4m3 shows it: a sine off by 2^-22 rounds twice as many
+// values to the other neighbour as one off by 2^-24).
 //
 // A lane holds two octets of a row, so that both dimensions of every pair are its
 // own: octets u and u + R / 16 of the rotated part, or of the rest (R the rotated
@@ -123,6 +125,22 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
          static_cast<uint64_t>(__float2ll_rn(rest * 18446744073709551616.f));
 }
 
+// Sine and cosine of a / 2^64 turns.
+__device__ __forceinline__ void turned(uint64_t a, float& s, float& c) {
+  const uint32_t quarter = static_cast<uint32_t>((a + (uint64_t{1} << 61)) >> 62);
+  // The rest, |rest| <= 2^29, over 2^31 half turns.
+  const int32_t rest = static_cast<int32_t>(static_cast<uint32_t>(a >> 32) - (quarter << 30));
+  const float x = __int2float_rn(rest);
+  const float e = static_cast<float>(rest - __float2int_rn(x)) * 1.4629180792671596e-9f;  // pi / 2^31
+  float s0, c0;
+  sincospif(x * 4.656612873077393e-10f, &s0, &c0);
+  const float s1 = fmaf(c0, e, s0), c1 = fmaf(-s0, e, c0);
+  s = quarter & 1 ? c1 : s1;
+  c = quarter & 1 ? s1 : c1;
+  if (quarter & 2) s = -s;
+  if ((quarter + 1) & 2) c = -c;
+}
+
 template <int D, typename T, typename KV>
 __global__ void __launch_bounds__(32 * kWarps, kMinCtas) append_rope_kernel(const AppendParams p) {
   constexpr int kLanes = D / 16;          // of a row
@@ -172,9 +190,7 @@ __global__ void __launch_bounds__(32 * kWarps, kMinCtas) append_rope_kernel(cons
         s[i] = 0.f;
         if (turns) {
           const int32_t pair = !p.pairs ? 8 * u + e : (e < 4 ? 4 * u + e : R / 4 + 4 * u + e - 4);
-          const uint64_t a = pos * turn_fraction(__ldg(p.freq + pair));
-          // Half turns: the upper 32 bits, signed, over 2^31.
-          sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f, &s[i], &c[i]);
+          turned(pos * turn_fraction(__ldg(p.freq + pair)), s[i], c[i]);
         }
       }
 #pragma unroll
