@@ -404,3 +404,16 @@ def test_a_pool_beyond_32_bits(path):
     for f, r in zip(flat, rows):
         assert torch.equal(f[where[:3]], r[[2, 5, 19]]) and torch.equal(f[where[20:22]], r[[20, 28]])
         assert torch.equal(f[where[3:20]], r[3:20])
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_large_values(d, path):
+    """Values of 2^90 under scores that grow by dozens from one tile of keys to the next."""
+    b = ref.tree_batch([20, 3], [1500, 700], 4, 1, d, 32, None, seed=16, scale=0.5)
+    for s in range(2):
+        for key in range(b.kv[s]):
+            page, i = ref.slot(b, s, key)
+            b.k_pages[page, i] *= 0.25 + key / 500
+    b.v_pages *= 2.0 ** 90
+    check(b, Tree(b).run(path=path))
