@@ -3,14 +3,13 @@
 //
 // build_tree: with depth(i) = 0 for a node that follows the context and
 // depth(parent) + 1 otherwise, positions = C + depth, and bit j of row i says
-// whether node j is i or an ancestor of it.  A request is one CTA, whose first warp takes
-// the nodes 32 at a time in shared memory (all its warps write the rows out): parents
-// come first, so an ancestor is among the 32 (found by doubling: five rounds of shuffles)
-// or its row is there already, and a row is that of the first ancestor before the 32,
-// with those among them set.  The path's nodes have rising numbers, so a window's are a
-// row's highest bits.  64 requests of up to 256 nodes take 7.1 us, of which 4 are the
-// eight steps of 32 nodes; a thread that walked from its node to the root took 41 where
-// chains were among them.  128 requests of 8 nodes: 2.8 us.
+// whether node j is i or an ancestor of it.  A request is one CTA.  Parents come first, so
+// its warps take 32 nodes each and find the ancestors among these by doubling (five rounds
+// of shuffles), and the first ancestor before them; then the 32s' rows in turn: a row is
+// that ancestor's, with those among the 32 set.  The path's nodes have rising numbers, so
+// a window's are a row's highest bits.  64 requests of up to 256 nodes take 5.7 us (7.1 with
+// one warp that did both for 32 nodes after 32; 41 where a thread walked from its node to
+// the root and chains were among them), 128 requests of 8 nodes 2.8.
 //
 // commit_tree: row k of the path takes the K and V of node path[k] >= k.  A thread
 // owns 16 bytes of the row and goes down the path, eight nodes read before eight
@@ -65,50 +64,50 @@ __global__ void __launch_bounds__(kThreads) build_tree_kernel(const BuildTreePar
     return;
   }
   const int32_t n = static_cast<int32_t>(n64), W = p.words;
-  // Rows [node][W + 1] (the odd length keeps 32 rows' words in different banks), and
-  // parents, which become depths.
+  // Rows [node][W + 1] (the odd length keeps 32 rows' words in different banks), parents,
+  // which become each node's first ancestor before its 32, and depths.
   uint32_t* rows = smem;
-  int32_t* depths = reinterpret_cast<int32_t*>(smem + 32 * W * (W + 1));
-  for (int32_t i = threadIdx.x; i < n; i += kThreads) {
-    int32_t up = __ldg(p.parents + q0 + i);
+  int32_t* ups = reinterpret_cast<int32_t*>(smem + 32 * W * (W + 1));
+  int32_t* depths = ups + 32 * W;
+  for (int32_t i0 = threadIdx.x & ~31; i0 < n; i0 += kThreads) {
+    const int32_t i = i0 + lane;
+    int32_t up = i < n ? __ldg(p.parents + q0 + i) : -1;
     if (up < -1 || up >= i) {
       if (p.ws) report_error(p.ws, RPA_DEVERR_LENGTHS, s);
       up = -1;
     }
-    depths[i] = up;
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    for (int32_t i0 = 0; i0 < n; i0 += 32) {
-      const int32_t i = i0 + lane;
-      // The node's parent, then its first ancestor before i0 as far as known.
-      int32_t up = i < n ? depths[i] : -1;
-      // Ancestors among the 32 (and the node): after k rounds those within 2^k steps.
-      uint32_t mine = 1u << lane;
+    // Ancestors among the 32 (and the node): after k rounds those within 2^k steps.
+    uint32_t mine = 1u << lane;
 #pragma unroll
-      for (int k = 0; k < 5; ++k) {
-        const bool within = up >= i0;
-        if (!__any_sync(kAll, within)) break;
-        const int from = within ? up - i0 : lane;
-        const uint32_t theirs = __shfl_sync(kAll, mine, from);
-        const int32_t further = __shfl_sync(kAll, up, from);
-        if (within) {
-          mine |= theirs;
-          up = further;
-        }
+    for (int k = 0; k < 5; ++k) {
+      const bool within = up >= i0;
+      if (!__any_sync(kAll, within)) break;
+      const int from = within ? up - i0 : lane;
+      const uint32_t theirs = __shfl_sync(kAll, mine, from);
+      const int32_t further = __shfl_sync(kAll, up, from);
+      if (within) {
+        mine |= theirs;
+        up = further;
       }
-      if (i < n) {
-        const int32_t own = i0 >> 5;
-        uint32_t* row = rows + i * (W + 1);
-#pragma unroll 4
-        for (int32_t k = 0; k < own; ++k) row[k] = k <= up >> 5 ? rows[up * (W + 1) + k] : 0u;
-        row[own] = mine;
-        depths[i] = __popc(mine) - 1 + (up >= 0 ? depths[up] + 1 : 0);
-      }
-      __syncwarp();
+    }
+    if (i < n) {
+      rows[i * (W + 1) + (i0 >> 5)] = mine;
+      ups[i] = up;
+      depths[i] = __popc(mine) - 1;  // among the 32
     }
   }
   __syncthreads();
+  // The words before the 32's own, and the depths, from that ancestor.
+  for (int32_t i0 = 32; i0 < n; i0 += 32) {
+    const int32_t i = i0 + lane;
+    if (i < n) {
+      const int32_t up = ups[i];
+      for (int32_t k = threadIdx.x >> 5; k < i0 >> 5; k += kThreads / 32)
+        rows[i * (W + 1) + k] = k <= up >> 5 ? rows[up * (W + 1) + k] : 0u;
+      if (threadIdx.x < 32 && up >= 0) depths[i] += depths[up] + 1;
+    }
+    __syncthreads();
+  }
   for (int32_t i = threadIdx.x; i < n; i += kThreads) p.positions[q0 + i] = len - n + depths[i];
   uint32_t* out = p.mask + static_cast<int64_t>(q0) * W;
   if (w <= 0) {
@@ -199,8 +198,8 @@ int launch_build_tree(const BuildTreeArgs& a, void* stream) {
   const int32_t W = 2 * a.words;
   const BuildTreeParams p{a.parents, a.cu_q_lens, a.kv_lens, a.window, reinterpret_cast<uint32_t*>(a.mask),
                           a.positions, a.workspace, a.total_q, W};
-  const int bytes = 32 * W * (W + 2) * static_cast<int>(sizeof(uint32_t));
-  const int most = 64 * kTreeMaxWords * (2 * kTreeMaxWords + 2) * static_cast<int>(sizeof(uint32_t));
+  const int bytes = 32 * W * (W + 3) * static_cast<int>(sizeof(uint32_t));
+  const int most = 64 * kTreeMaxWords * (2 * kTreeMaxWords + 3) * static_cast<int>(sizeof(uint32_t));
   if (bytes > 48 * 1024)
     if (int e = ensure_dynamic_smem(reinterpret_cast<const void*>(build_tree_kernel), most)) return e;
   build_tree_kernel<<<a.num_seqs, kThreads, bytes, static_cast<cudaStream_t>(stream)>>>(p);
