@@ -40,12 +40,21 @@ rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
   auto per_head = [&](int32_t i) -> int64_t { return seq(i).per_head; };
   auto segments = [&](int32_t i) { return per_head(i) * plan.hkv; };
   auto cost = [&](int32_t i) { return static_cast<int64_t>(tiles(i)) * kTile + kSegCost; };
-  int64_t work = 0, most_heads = 0;
+  // Requests by their segments of a head: what a pass of each costs, and its tiles.
+  struct Kind {
+    int64_t cost = 0, tiles = 0;
+  };
+  std::vector<Kind> kinds(2);
+  int64_t work = 0;
   for (int32_t i = 0; i < n_seq; ++i) {
-    plan.tree_seqs[l.seq_begin + i].per_head = static_cast<uint16_t>(ceil_div(seq(i).nodes, per));
+    const int64_t s = ceil_div(seq(i).nodes, per);
+    plan.tree_seqs[l.seq_begin + i].per_head = static_cast<uint16_t>(s);
+    if (static_cast<int64_t>(kinds.size()) <= s) kinds.resize(s + 1);
+    kinds[s].cost += cost(i);
+    kinds[s].tiles += tiles(i);
     work += cost(i) * segments(i);
-    most_heads = std::max(most_heads, per_head(i));
   }
+  const int64_t most_heads = static_cast<int64_t>(kinds.size()) - 1;
   const int64_t most = std::min<int64_t>(plan.num_sms, kTreeMaxCtas);
   const int64_t ctas = std::max<int64_t>(1, std::min(most, work / kLeast));
   // The width of least time: the longest lane's tiles, each a little more where its keys
@@ -54,12 +63,13 @@ rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
   double least = 0;
   for (int64_t w = 1; w <= std::min<int64_t>({kMaxWidth, ctas, most_heads > 1 ? kMaxWidth : 1}); ++w) {
     int64_t line = 0, reads = 0, all = 0;
-    for (int32_t i = 0; i < n_seq; ++i) {
-      const int64_t passes = ceil_div(segments(i), w), s = per_head(i), step = s / std::gcd(s, w);
-      line += passes * cost(i);
+    for (int64_t s = 1; s <= most_heads; ++s) {
+      if (kinds[s].tiles == 0) continue;
+      const int64_t passes = ceil_div(s * plan.hkv, w), step = s / std::gcd(s, w);
+      line += passes * kinds[s].cost;
       // Heads that the passes read: one more for each pass that begins inside a head.
-      reads += (plan.hkv + passes - 1 - (passes - 1) / step) * tiles(i);
-      all += segments(i) * tiles(i);
+      reads += (plan.hkv + passes - 1 - (passes - 1) / step) * kinds[s].tiles;
+      all += s * plan.hkv * kinds[s].tiles;
     }
     const double t = static_cast<double>(line) / static_cast<double>(ctas / w) * (1 + kAlone * reads / all);
     if (w > 1 && t >= least) continue;
