@@ -183,13 +183,16 @@ typedef struct rpa_plan_options {
 typedef struct rpa_plan_info {
   int32_t path;             /* RPA_PATH_SIMT or RPA_PATH_TC                     */
   int32_t num_decode_seqs;  /* sequences with q_len == 1 (4-bit pages: those of
-                               few query rows, on the split-KV kernel)          */
+                               few query rows, on the split-KV kernel; trees:
+                               requests with nodes)                             */
   int32_t num_prefill_seqs; /* sequences with q_len > 1 (4-bit pages: the
                                others, on the tensor-core prefill)              */
   int32_t q_block;          /* prefill query block in tokens (query tokens of
                                one work item; on SM pairs, of both CTAs)     */
-  int32_t kv_split;         /* decode split length in tokens                    */
-  int32_t max_splits;       /* largest split count of any decode sequence       */
+  int32_t kv_split;         /* decode split length in tokens (trees: keys of the
+                               longest CTA range)                               */
+  int32_t max_splits;       /* largest split count of any decode sequence (trees:
+                               of any segment)                                  */
   int32_t num_prefill_items;/* (sequence, query block, kv head) work items      */
   int32_t prefill_ctas;     /* persistent prefill CTAs launched                 */
   int64_t workspace_bytes;  /* bytes rpa_forward needs                          */
