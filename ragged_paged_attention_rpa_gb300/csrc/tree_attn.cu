@@ -104,7 +104,7 @@ struct TreeParams {
   unsigned char* ws;
   int32_t hq, hkv, group, per_tile;  // nodes a row tile
   int32_t page_size, page_shift, mpps, num_pages, words;
-  int32_t box_rows_k, box_rows_v, v_4d, out_v8, width;  // width: lanes of a group of CTAs
+  int32_t box_nodes_q, box_rows_k, box_rows_v, v_4d, out_v8, width;  // width: lanes of a group of CTAs
   float scale_log2;  // sm_scale log2(e)
 };
 
@@ -413,7 +413,31 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // ------------------------------------------------------------ copies
     const int rows_k = p.box_rows_k, rows_v = p.box_rows_v;
     const int nk = kTreeKeys / rows_k, nv = Lay::kVKeys / rows_v;  // boxes of 16 KB
-    const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.per_tile) * 128u * kChunks;
+    // Q's boxes: 32 rows where these are whole nodes, and those without a node are zeros, for
+    // which the tensor cores take less power: run for seconds, 32 long contexts take 382 us
+    // at 1780 MHz, 401 at 1660 with rows of the nodes that follow; 128 requests of 8 nodes
+    // draw 897 W in place of 978.
+    const int q_nodes = p.box_nodes_q, q_rows = p.group * q_nodes;
+    int q_used[2] = {kTreeRows / q_rows, kTreeRows / q_rows};  // boxes that are not zeros
+    auto boxes_of = [&](int nodes) { return (nodes + q_nodes - 1) / q_nodes; };
+    // (Nothing waits for it: nobody reads what becomes of these rows.)
+    auto clear_q = [&](int t, int boxes) {
+      uint8_t* tile = smem + t * Lay::kQTile;
+      const int32_t from = boxes * q_rows * 8, units = (q_used[t] - boxes) * q_rows * 8;  // of 16 bytes
+      for (int32_t u = lane; u < units; u += 32)
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          reinterpret_cast<uint4*>(tile + c * (kTreeRows * 128))[from + u] = make_uint4(0u, 0u, 0u, 0u);
+      if (units > 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      q_used[t] = boxes;
+    };
+    auto copy_q = [&](int t, int boxes) {
+      for (int x = lane; x < boxes * kChunks; x += 32) {
+        const int c = x % kChunks, b = x / kChunks;
+        tma_load_3d(smem + t * Lay::kQTile + c * (kTreeRows * 128) + b * q_rows * 128, &tm_q, &B.q_full, c * 64,
+                    a.head * p.group, a.s.q0 + a.node0 + t * p.per_tile + b * q_nodes);
+      }
+    };
     Ring<kDepth> ring;
     uint32_t filled = 0, parts = 0, issued_q = 0;
     bool alive = true;
@@ -478,19 +502,21 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (a.head == 0 && a.node0 == 0 && a.key0 + a.n * kTreeKeys >= a.s.len)
           tree_check_lengths(a.s, p.cu_q_lens, p.kv_lens, p.ws);
         alive = mbar_wait(&B.q_empty, (parts & 1) ^ 1, abort, kWaitNs);
-        if (alive) {
-          mbar_arrive_expect_tx(&B.q_full, two ? 2 * q_bytes : q_bytes);
-          for (int t = 0; t < (two ? 2 : 1); ++t)
-            for (int c = 0; c < kChunks; ++c)
-              tma_load_3d(smem + t * Lay::kQTile + c * (kTreeRows * 128), &tm_q, &B.q_full, c * 64,
-                          a.head * p.group, a.s.q0 + a.node0 + t * p.per_tile);
-          ++issued_q;
-        }
       }
       alive = __shfl_sync(0xffffffffu, alive, 0);
+      const int b0 = boxes_of(a.n0), b1 = kStreams == 2 && two ? boxes_of(a.n1) : 0;
+      if (alive) {
+        if (lane == 0) mbar_arrive_expect_tx(&B.q_full, static_cast<uint32_t>((b0 + b1) * q_rows) * 128u * kChunks);
+        __syncwarp();
+        copy_q(0, b0);
+        if (kStreams == 2 && b1 > 0) copy_q(kStreams - 1, b1);
+        ++issued_q;
+      }
       // K runs a tile ahead of V where a score tile runs ahead of the product of the
       // tile before; with two row tiles it is the second one's that does.
       if (alive) alive = copy_k(now);
+      clear_q(0, b0);
+      if (kStreams == 2 && two) clear_q(kStreams - 1, b1);
       for (int j = 0; j < a.n && alive; ++j) {
         if (j + 1 < a.n) next = rows_of(j + 1);
         if (!two && j + 1 < a.n && !copy_k(next)) break;
@@ -1164,6 +1190,9 @@ int launch_d(const Plan& plan, const Args& a, cudaStream_t stream) {
   p.mpps = plan.mpps;
   p.num_pages = plan.num_pages;
   p.words = plan.tree_words;
+  // A quarter of a row tile a box of Q where a quarter's rows are whole nodes (else the tile:
+  // its last rows then hold what follows in q, and nobody reads what becomes of them).
+  p.box_nodes_q = p.per_tile * G == kTreeRows && p.per_tile % 4 == 0 ? p.per_tile / 4 : p.per_tile;
   // Boxes never cross a page (32 contexts of 4k to 32k keys: 496 us with pages of 16, 380 with
   // 32, 366 with 64 to 256).
   p.box_rows_k = std::min(plan.p, 64);  // (the last tile's second half often lies behind the keys)
@@ -1177,7 +1206,7 @@ int launch_d(const Plan& plan, const Args& a, cudaStream_t stream) {
   p.scale_log2 = std::max(a.sm_scale * 1.4426950408889634f, FLT_MIN);
   CUtensorMap tq, tk, tv;
   const uint64_t pool_rows = static_cast<uint64_t>(plan.num_pages) * plan.p;
-  if (!make_tmap_3d(&tq, a.q, D, plan.hq, static_cast<uint64_t>(plan.total_q), G, p.per_tile) ||
+  if (!make_tmap_3d(&tq, a.q, D, plan.hq, static_cast<uint64_t>(plan.total_q), G, p.box_nodes_q) ||
       !make_tmap_3d(&tk, a.k_pages, D, plan.hkv, pool_rows, 1, p.box_rows_k) ||
       !(p.v_4d ? make_tmap_4d_chunks(&tv, a.v_pages, D, plan.hkv, pool_rows, 1, p.box_rows_v, false)
                : make_tmap_3d(&tv, a.v_pages, D, plan.hkv, pool_rows, 1, p.box_rows_v)))
