@@ -26,6 +26,10 @@ constexpr int32_t kTile = 4;
 constexpr int32_t kSegCost = 6;
 constexpr int32_t kLeast = 4;
 
+// What the kernel that joins the parts of segments costs, and its launch: 5 us, about 4 tiles.
+// (17 requests of 65 to 195 nodes after up to 150 keys, 16 heads a KV head: 31.6 us cut, 23.8 in
+// whole passes; 83 of 2 to 8 nodes under a window of 371: 72 and 56.)
+constexpr int32_t kCombine = 16;
 // What a key tile that no other CTA reads at the same time costs on top: 64 heads over 40000
 // keys of 8 KV heads run at 1391 TFLOP/s with their row tiles one after the other, at 1634
 // side by side, where only one CTA in 8 reads HBM; 8 requests of 256 nodes take 239 and 215 us.
@@ -76,10 +80,46 @@ rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
     least = t;
     width = w;
   }
-  const int64_t groups = ctas / width;
+  int64_t groups = ctas / width;
+  auto passes = [&](int32_t i) { return ceil_div(segments(i), width); };
   std::vector<int64_t> v0(1, 0);  // the requests' starts on the line
-  for (int32_t i = 0; i < n_seq; ++i) v0.push_back(v0.back() + cost(i) * ceil_div(segments(i), width));
+  for (int32_t i = 0; i < n_seq; ++i) v0.push_back(v0.back() + cost(i) * passes(i));
   const int64_t total = v0.back();
+  // The ranges' ends on the line: equal ranges, or whole passes where the longest of such
+  // ranges is not much longer.
+  std::vector<int64_t> ends;
+  auto whole_passes = [&](int64_t most) {
+    ends.assign(1, 0);
+    for (int32_t i = 0; i < n_seq; ++i) {
+      const int64_t c = cost(i);
+      if (c > most) return false;
+      for (int64_t at = v0[i]; at < v0[i + 1];) {
+        const int64_t fit = (ends.back() + most - at) / c;  // passes that the range still takes
+        if (fit > 0)
+          at = std::min(v0[i + 1], at + fit * c);
+        else
+          ends.push_back(at);
+        if (static_cast<int64_t>(ends.size()) > groups) return false;
+      }
+    }
+    ends.push_back(total);
+    return true;
+  };
+  int64_t least_most = total / groups + kCombine;
+  if (groups > 1 && whole_passes(least_most)) {
+    for (int64_t low = total / groups; low < least_most;) {
+      const int64_t mid = (low + least_most) / 2;
+      if (whole_passes(mid))
+        least_most = mid;
+      else
+        low = mid + 1;
+    }
+    whole_passes(least_most);
+    groups = static_cast<int64_t>(ends.size()) - 1;
+  } else {
+    ends.clear();
+    for (int64_t g = 0; g <= groups; ++g) ends.push_back(total * g / groups);
+  }
   // (A range's tiles travel in 31 bits.)
   if (ceil_div(total, groups) > 0x3fffffff) return RPA_ERR_UNSUPPORTED;
   l.start_begin = static_cast<int32_t>(plan.tree_starts.size());
@@ -93,7 +133,7 @@ rpa_status_t cut_line(Plan& plan, TreeLaunch& l) {
   std::vector<int32_t> last(width, -1);   // the lanes' last cuts
   int32_t i = 0;
   for (int64_t g = 0; g <= groups; ++g) {
-    const int64_t x = total * g / groups;
+    const int64_t x = ends[g];
     for (; i < n_seq && v0[i + 1] <= x; ++i)
       for (int64_t lane = 0; lane < width; ++lane) before[lane] += of_lane(i, lane) * tiles(i);
     // The boundary as a pass and a tile: one inside a charge is the pass's end.
