@@ -4,8 +4,9 @@
 // a segment is (request, KV head, one or two row tiles) over the 128-key tiles its
 // nodes can see.  A request's segments run in passes of `width` segments side by side.
 // The passes' key tiles, each pass followed by a charge for its ends, form one line,
-// which is cut into equal ranges, one per group of `width` CTAs: the CTAs of a group
-// read the same keys of a head at the same time, so that all but one find them in L2.
+// which is cut into equal ranges, one per group of `width` CTAs (or between passes, where
+// that costs less than joining their parts): the CTAs of a group read the same keys of a
+// head at the same time, so that all but one find them in L2.
 #include <algorithm>
 #include <cstdint>
 #include <numeric>

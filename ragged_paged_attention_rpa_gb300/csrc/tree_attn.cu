@@ -5,10 +5,10 @@
 // of one KV head; a segment is (request, KV head, one such row tile, or two where
 // head_dim leaves tensor memory for two outputs), its keys come in tiles of 128.
 // plan_tree.cpp lays the segments' tiles end to end (where a head has several segments,
-// these side by side) and cuts the line into equal ranges, one per CTA, one CTA per SM: few
-// rows over long contexts are bound by HBM, and only all SMs together reach it.  A CTA's range is a list of parts of segments;
-// a part that is not its whole segment leaves fp32 O / l and log2-sum-exps, which
-// tree_combine_kernel joins.
+// these side by side) and cuts the line into equal ranges, one per CTA, one CTA per SM:
+// few rows over long contexts are bound by HBM, and only all SMs together reach it.  A
+// CTA's range is a list of parts of segments; a part that is not its whole segment leaves
+// fp32 O / l and log2-sum-exps, which tree_combine_kernel joins.
 //
 // Within a part the score tile S = Q K^T (SMEM x SMEM -> TMEM) runs one ahead of
 // O += P V (P from TMEM, written over half of its S; V MN-major from SMEM).  With two
