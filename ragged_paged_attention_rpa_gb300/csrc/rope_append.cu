@@ -115,14 +115,17 @@ __device__ __forceinline__ void store8(uint8_t* dst, bool, const float (&x)[8], 
   *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
 }
 
-// f / 2 pi modulo 1, in 2^-64.
+// f / 2 pi modulo 1, in 2^-64: of |f|, negated modulo 1 where f < 0 (one less a small fraction
+// would not fit 24 bits).
 __device__ __forceinline__ uint64_t turn_fraction(float f) {
   constexpr float kHi = 0.15915493667125702f, kLo = 6.4206382432985265e-09f;  // 1 / 2 pi
-  const float hi = f * kHi, lo = fmaf(f, kLo, fmaf(f, kHi, -hi));
-  const float part = hi - floorf(hi);  // exact, in [0, 1)
+  const float a = fabsf(f);
+  const float hi = a * kHi, lo = fmaf(a, kLo, fmaf(a, kHi, -hi));
+  const float part = hi - floorf(hi);  // exact, in [0, 1): hi >= 0
   const float rest = lo - rintf(lo);     // |lo| passes 1 only for |f| beyond 2^26
-  return __float2ull_rz(part * 18446744073709551616.f) +
-         static_cast<uint64_t>(__float2ll_rn(rest * 18446744073709551616.f));
+  const uint64_t turn = __float2ull_rz(part * 18446744073709551616.f) +
+                        static_cast<uint64_t>(__float2ll_rn(rest * 18446744073709551616.f));
+  return f < 0.f ? uint64_t{0} - turn : turn;
 }
 
 // Sine and cosine of a / 2^64 turns.

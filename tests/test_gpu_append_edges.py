@@ -1,0 +1,104 @@
+"""Rotation and cache write where their arithmetic could go wrong: angles of either sign.  The bounds are worked out
+pair by pair."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from ragged_paged_attention_rpa_gb300 import binding, build
+
+from . import tree_reference as ref
+from .test_gpu_tree_step import i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build.build()
+
+
+def turn(x, pos, freq, pairs, dt=torch.float32):
+    """Rows x [t, heads, d] turned as q, and as k through fresh pages of the same type."""
+    t, heads, d = x.shape
+    x = x.to(dt).cuda()
+    out = torch.empty_like(x)
+    pages = torch.zeros((t, 1, heads, d), dtype=dt, device="cuda")
+    freq = torch.as_tensor(np.asarray(freq, np.float32)).cuda()
+    binding.rpa_append_rope(x, x, x, i32(pos), torch.arange(t, device="cuda"), freq, out, pages, pages.clone(),
+                            interleaved=pairs)
+    assert torch.equal(out.view(torch.uint8), pages[:, 0].view(torch.uint8))
+    return out
+
+
+def pair_sums(x, n, pairs):
+    """|x| + |y| of each dimension's pair; zero where nothing turns."""
+    i = torch.arange(n)
+    first, second = (2 * i, 2 * i + 1) if pairs else (i, i + n)
+    both = torch.zeros_like(x)
+    both[..., first] = both[..., second] = x[..., first].abs() + x[..., second].abs()
+    return both, first, second
+
+
+def sine_error(pos, freq, first, second, d):
+    """[t, 1, d]: the angle's error (2^-47 of itself + 2^-28), a sine's two roundings (one unit and half a unit in the
+    last place, under 2^-23) and the products' (2^-24 of each, 2^-24 of their sum: under 2^-23 of |x| + |y|)."""
+    a = np.abs(np.asarray(pos, np.float64)[:, None] * np.asarray(freq, np.float64)[None])
+    e = torch.zeros((len(pos), 1, d), dtype=torch.float64)
+    e[..., first] = e[..., second] = torch.from_numpy(a * 2.0 ** -47 + 2.0 ** -28 + 2.0 ** -22)[:, None]
+    return e
+
+
+def near(got, x, pos, freq, pairs, half):
+    x = x.double()
+    both, first, second = pair_sums(x, len(freq), pairs)
+    want = ref.turned(x, pos, freq, pairs)
+    off = sine_error(pos, freq, first, second, x.shape[-1]) * both
+    bound = off + half * (want.abs() + off)
+    diff = (got.double().cpu() - want).abs()
+    assert (diff <= bound).all(), "%g of the bound" % float((diff / bound.clamp(min=1e-300)).max())
+
+
+POSITIONS = [0, 1, -1, 1001, 4095, 8191, 20001, 65537, 131071, 999999, -8191, -131071, 16777215, (1 << 31) - 1, -(1 << 31) + 1]
+
+
+def frequencies(kind, n, rng):
+    table = 10000.0 ** (-np.arange(n) / n)
+    if kind == "negative":
+        return -table
+    if kind == "mixed":
+        return table * np.where(np.arange(n) % 2, -1.0, 1.0)
+    if kind == "listed":
+        f = np.array([-1.0, -0.1, -1e-3, -1e-5, -1e-7, -2.0 ** -24, -2.0 ** -26, -0.3, -7.5, -100.0, -3.0, -6.2831855])
+        return np.resize(np.concatenate([f, -f]), n)
+    return rng.choice([-1.0, 1.0], n) * 2.0 ** rng.uniform(-40, 12, n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("kind", ["negative", "mixed", "listed", "random"])
+def test_frequencies_of_either_sign(kind, pairs, dtype):
+    rng = np.random.default_rng(5)
+    dt, half = (torch.bfloat16, 2.0 ** -8) if dtype == "bf16" else (torch.float32, 2.0 ** -24)
+    pos = np.array(POSITIONS + rng.integers(1000, 1000000, 50).tolist())
+    freq = np.float32(frequencies(kind, 64, rng))
+    x = torch.from_numpy(rng.standard_normal((len(pos), 3, 128))).to(dt)
+    near(turn(x, pos, freq, pairs, dt), x, pos, freq, pairs, half)
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("kind", ["negative", "mixed", "random"])
+def test_turned_there_and_back(kind, pairs):
+    """By f, then by -f.  The first turn's error of a pair is turned itself (2 of it at most), the second's goes with
+    |x| + |y| after the first (sqrt 2 of it before)."""
+    rng = np.random.default_rng(6)
+    pos = np.array(POSITIONS + rng.integers(1000, 1000000, 50).tolist())
+    freq = np.float32(frequencies(kind, 64, rng))
+    x = torch.from_numpy(rng.standard_normal((len(pos), 2, 128))).float()
+    back = turn(turn(x, pos, freq, pairs).cpu(), pos, -freq, pairs)
+    both, first, second = pair_sums(x.double(), 64, pairs)
+    bound = 3.5 * sine_error(pos, freq, first, second, 128) * both
+    diff = (back.double().cpu() - x.double()).abs()
+    assert (diff <= bound).all(), "%g of the bound" % float((diff / bound.clamp(min=1e-300)).max())
