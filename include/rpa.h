@@ -626,7 +626,8 @@ rpa_status_t rpa_build_tree(const int32_t* parents, const int32_t* cu_q_lens,
  * are (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when `interleaved` is nonzero;
  * dimensions from rotary_dim on, and v, stay as they are.  fp32 arithmetic; the
  * angle is reduced in fixed point, its error at most 2^-47 |a| + 2^-28.  Any int32
- * is a position, and a frequency may have either sign (-f turns back).
+ * is a position, and a frequency may have either sign (-f turns back); one that is
+ * NaN or infinite makes its pairs NaN.
  */
 typedef struct rpa_rope {
   const float* inv_freq; /* device, [rotary_dim / 2]; NULL with rotary_dim 0   */

@@ -193,7 +193,10 @@ __global__ void __launch_bounds__(32 * kWarps, kMinCtas) append_rope_kernel(cons
         s[i] = 0.f;
         if (turns) {
           const int32_t pair = !p.pairs ? 8 * u + e : (e < 4 ? 4 * u + e : R / 4 + 4 * u + e - 4);
-          turned(pos * turn_fraction(__ldg(p.freq + pair)), s[i], c[i]);
+          const float f = __ldg(p.freq + pair), nan = f - f;  // 0, or NaN where f is no number
+          turned(pos * turn_fraction(f), s[i], c[i]);
+          s[i] += nan;
+          c[i] += nan;
         }
       }
 #pragma unroll

@@ -1,5 +1,5 @@
-"""Rotation and cache write where their arithmetic could go wrong: angles of either sign.  The bounds are worked out
-pair by pair."""
+"""Rotation and cache write where their arithmetic could go wrong: angles of either sign, frequencies that are no
+numbers.  The bounds are worked out pair by pair."""
 
 from __future__ import annotations
 
@@ -102,3 +102,23 @@ def test_turned_there_and_back(kind, pairs):
     bound = 3.5 * sine_error(pos, freq, first, second, 128) * both
     diff = (back.double().cpu() - x.double()).abs()
     assert (diff <= bound).all(), "%g of the bound" % float((diff / bound.clamp(min=1e-300)).max())
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+def test_frequencies_that_are_no_numbers(pairs):
+    """Their pairs come out NaN at any position, the others as they should."""
+    rng = np.random.default_rng(7)
+    pos = np.array([0, 1, -3, 5000, (1 << 31) - 1, -(1 << 31)])
+    freq = np.float32(frequencies("mixed", 32, rng))
+    bad = {0: np.nan, 5: np.inf, 17: -np.inf, 31: -np.nan}
+    for i, f in bad.items():
+        freq[i] = f
+    x = torch.from_numpy(rng.standard_normal((len(pos), 2, 64))).float()
+    got = turn(x, pos, freq, pairs).cpu()
+    gone = torch.zeros(64, dtype=torch.bool)
+    for i in bad:
+        gone[[2 * i, 2 * i + 1] if pairs else [i, i + 32]] = True
+    assert torch.isnan(got[..., gone]).all()
+    fine = np.where(np.isfinite(freq), freq, 0)
+    want = x.double()
+    near(torch.where(gone, x, got).cuda(), want, pos, fine, pairs, 2.0 ** -24)
