@@ -95,7 +95,9 @@ __device__ __forceinline__ void store8(float* dst, bool whole, const float (&x)[
   for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[i]);
   kv4::store32(dst, whole, w);
 }
-// e4m3: x / s to the nearest, at most 448, NaN as NaN.
+// e4m3: x / s to the nearest, at most 448, NaN as NaN.  x r by one correction with the
+// exact remainder (as kv4::quotient), except where it passes the range of 32 bits, as an
+// infinite x does: the remainder of an infinity is NaN.
 __device__ __forceinline__ void store8(uint8_t* dst, bool, const float (&x)[8], float s, float r) {
   uint32_t w[2];
 #pragma unroll
@@ -103,9 +105,8 @@ __device__ __forceinline__ void store8(uint8_t* dst, bool, const float (&x)[8], 
     float y[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float v = x[4 * i + j], t = kv4::quotient(v, s, r);
-      // (The correction turns an infinity into NaN.)
-      y[j] = fabsf(v) < INFINITY ? t : v;
+      const float v = x[4 * i + j], q = v * r;
+      y[j] = fabsf(q) < INFINITY ? fmaf(fmaf(-q, s, v), r, q) : q;
     }
     asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n"
         " cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n mov.b32 %0, {a, b};\n}\n"
@@ -249,6 +250,16 @@ __global__ void __launch_bounds__(32 * kWarps, kMinCtas) append_rope_kernel(cons
           float s = 1.f, inv = 1.f;
           if constexpr (sizeof(KV) == 1) {
             s = __ldg((is_k ? p.k_scale : p.v_scale) + g);
+            // Row and scale 2^64 times as large where the reciprocal could be infinite, or
+            // the remainder too small for 32 bits.
+            if (s < 0x1p-64f) {
+              s *= 0x1p64f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                x[e] *= 0x1p64f;
+                y[e] *= 0x1p64f;
+              }
+            }
             inv = 1.f / s;
           }
           store8(dst + first, p.whole, x, s, inv);

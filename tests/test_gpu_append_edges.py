@@ -1,5 +1,5 @@
 """Rotation and cache write where their arithmetic could go wrong: angles of either sign, frequencies that are no
-numbers.  The bounds are worked out pair by pair."""
+numbers, quotients beyond 32 bits.  The bounds are worked out pair by pair."""
 
 from __future__ import annotations
 
@@ -10,7 +10,7 @@ import torch
 from ragged_paged_attention_rpa_gb300 import binding, build
 
 from . import tree_reference as ref
-from .test_gpu_tree_step import i32
+from .test_gpu_tree_step import e4m3, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +122,67 @@ def test_frequencies_that_are_no_numbers(pairs):
     fine = np.where(np.isfinite(freq), freq, 0)
     want = x.double()
     near(torch.where(gone, x, got).cuda(), want, pos, fine, pairs, 2.0 ** -24)
+
+
+def nearest_e4m3(y):
+    """The nearest e4m3 value (ties to even), 448 at most, NaN as NaN."""
+    y = np.asarray(y, np.float64)
+    a = np.minimum(np.abs(y), 1e6)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        e = np.maximum(np.frexp(a)[1] - 1, -6)
+        v = np.minimum(np.rint(a / 2.0 ** (e - 3.0)) * 2.0 ** (e - 3.0), 448.0)
+    return np.where(np.isnan(y), np.nan, np.copysign(v, y))
+
+
+def stored(v, scale, dt):
+    """Values of the e4m3 pages that rows v [t, heads, 64] leave (as v, and as k that is not turned)."""
+    t, heads, d = v.shape
+    v, scale = v.to(dt).cuda(), torch.as_tensor(np.asarray(scale, np.float32)).cuda()
+    kp, vp = (torch.zeros((t, 1, heads, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    binding.rpa_append_rope(None, v, v, None, torch.arange(t, device="cuda"), None, None, kp, vp, k_scale=scale, v_scale=scale)
+    assert torch.equal(kp, vp)
+    return e4m3(vp[:, 0]).numpy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_e4m3_quotients_beyond_32_bits(dtype):
+    """At most 448 where the quotient overflows; zeros stay zeros under scales whose reciprocal does; infinities, NaN."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    large = [1e37, -1e37, 3e38, -3e38, 1e30, 0.0, -0.0, float("inf"), -float("inf"), float("nan"), 2.0 ** -126, -2.0 ** -133]
+    ratios = [0.0, 1.0, -1.0, 3.0, 17.0, -19.0, 448.0, 500.0, -1e5, 2.0 ** -3, 1.5, 208.0]
+    scales = [0.01, 1e-30, 2.0 ** -64, 2.0 ** -65, 2.0 ** -126, 2.0 ** -127, 2.0 ** -128, 2.0 ** -130, 1.0, 1e30, 2.0 ** 126, 3e38]
+    x = torch.zeros((2, len(scales), 64), dtype=torch.float64)
+    x[0, :, :len(large)] = torch.tensor(large, dtype=torch.float64)
+    for h, s in enumerate(scales):
+        x[1, h, :len(ratios)] = torch.tensor(ratios, dtype=torch.float64) * s
+    x = x.clamp(-3.3e38, 3.3e38).where(~torch.isinf(x), x).to(dt)
+    s = np.float64(np.float32(scales))[None, :, None]
+    with np.errstate(over="ignore"):
+        y = x.double().numpy() / s
+    got = stored(x, scales, dt)
+    # (Ties are decided by the quotient's roundings, two of 2^-24.)
+    low, high = nearest_e4m3(y * (1 - 2.0 ** -22 * np.sign(y))), nearest_e4m3(y * (1 + 2.0 ** -22 * np.sign(y)))
+    nan = np.isnan(y)
+    assert np.array_equal(np.isnan(got), nan)
+    ok = nan | ((got >= low) & (got <= high))
+    assert ok.all(), [(x[tuple(i)].item(), scales[i[1]], got[tuple(i)]) for i in np.argwhere(~ok)[:5]]
+    # The listed ratios are exact, ties among them.
+    exact = nearest_e4m3(np.array(ratios))
+    for h in range(len(scales)):
+        kept = x[1, h, :len(ratios)].double().numpy() == np.array(ratios) * s[0, h, 0]
+        assert np.array_equal(got[1, h, :len(ratios)][kept], exact[kept]), scales[h]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_e4m3_quotients_of_any_size(dtype):
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    rng = np.random.default_rng(8)
+    scales = np.float32(2.0 ** rng.uniform(-140, 127, 40))
+    x = rng.choice([-1.0, 1.0], (30, 40, 64)) * scales[None, :, None].astype(np.float64) * 2.0 ** rng.uniform(-12, 11, (30, 40, 64))
+    x[::3] = rng.choice([-1.0, 1.0], x[::3].shape) * 2.0 ** rng.uniform(-140, 127.9, x[::3].shape)
+    x = torch.from_numpy(x.clip(-3.3e38, 3.3e38)).to(dt)
+    y = x.double().numpy() / scales.astype(np.float64)[None, :, None]
+    got = stored(x, scales, dt)
+    low, high = nearest_e4m3(y * (1 - 2.0 ** -22 * np.sign(y))), nearest_e4m3(y * (1 + 2.0 ** -22 * np.sign(y)))
+    ok = (got >= low) & (got <= high)
+    assert ok.all(), [(x[tuple(i)].item(), scales[i[1]], got[tuple(i)]) for i in np.argwhere(~ok)[:5]]
