@@ -50,7 +50,9 @@ tree_simt_kernel(const T* q, const T* k_pages, const T* v_pages, T* out, const T
     x[e] = to_float(q[(static_cast<int64_t>(t) * p.hq + h) * D + 32 * e + lane]);
     o[e] = 0.f;
   }
-  for (int32_t k0 = (first & ~31) + 32 * warp; k0 < s.len; k0 += 32 * kWarps) {
+  // From the window's first key or the first node, whichever is earlier: the window bounds the
+  // context alone.
+  for (int32_t k0 = (min(first, s.len - s.nodes) & ~31) + 32 * warp; k0 < s.len; k0 += 32 * kWarps) {
     for (uint32_t bits = tree_sees32(s, row, first, k0); bits; bits &= bits - 1) {
       const int32_t key = k0 + __ffs(bits) - 1;
       const int32_t page = __ldg(table + (key >> p.page_shift));

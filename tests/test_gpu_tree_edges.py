@@ -1,0 +1,32 @@
+"""Drafted trees at the edges of what their calls take: masks under windows.  The bound is that of
+test_gpu_tree.py."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from ragged_paged_attention_rpa_gb300 import build
+
+from . import tree_reference as ref
+from .test_gpu_tree import PATHS, Tree, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build.build()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_any_mask_under_a_window(d, path, dtype):
+    """The window bounds the context alone: a node sees the nodes of its mask however far back they lie."""
+    rng = np.random.default_rng(d)
+    nodes, ctx, windows = [130, 40, 70], [50, 0, 33], [2, 7, 1]
+    b = ref.tree_batch(nodes, ctx, 6, 2, d, 16, windows, seed=d, sees=[rng.random((t, t)) < 0.2 for t in nodes],
+                       dtype=dtype)
+    b.pos[:] = np.concatenate([c + np.arange(t) for c, t in zip(ctx, nodes)])
+    check(b, Tree(b).run(path=path))
