@@ -682,8 +682,8 @@ rpa_status_t rpa_append_rope(const void* q, const void* k, const void* v, int64_
  * includes the nodes, whose rows are in their pages already.
  *
  * bf16 q, pages and out run on tensor cores (page_size at least 16 and num_q_heads
- * / num_kv_heads at most 128, sm_scale not below zero), fp32 and the rest on CUDA
- * cores.  A NaN or an
+ * / num_kv_heads at most 128, sm_scale at least 2^-126), fp32 and the rest on CUDA
+ * cores, which take far longer.  A NaN or an
  * infinity in K or V reaches the rows that see its key, and no other.  Device
  * lengths that differ from the plan's set RPA_DEVERR_LENGTHS; the call goes by the
  * plan's.  The other arguments, the error word, unused slots, threads and CUDA

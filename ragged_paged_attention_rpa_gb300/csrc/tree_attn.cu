@@ -1201,9 +1201,7 @@ int launch_d(const Plan& plan, const Args& a, cudaStream_t stream) {
   // nodes: 38.1 us, 38.6 with a box a chunk).
   p.v_4d = Lay::kChunks > 1 && p.box_rows_v == Lay::kVKeys ? 1 : 0;
   p.out_v8 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 ? 1 : 0;
-  // (Not zero: the infinity of a masked score times zero would be NaN.  Under the
-  // smallest number no product differs from zero.)
-  p.scale_log2 = std::max(a.sm_scale * 1.4426950408889634f, FLT_MIN);
+  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
   CUtensorMap tq, tk, tv;
   const uint64_t pool_rows = static_cast<uint64_t>(plan.num_pages) * plan.p;
   if (!make_tmap_3d(&tq, a.q, D, plan.hq, static_cast<uint64_t>(plan.total_q), G, p.box_nodes_q) ||
@@ -1229,8 +1227,9 @@ bool tree_tc_supported(int32_t head_dim, int32_t page_size, int32_t group) {
 }
 
 int launch_tree_attn(const Plan& plan, const Args& a, void* stream) {
-  // (The maxima are taken before the scale.)
-  if (a.sm_scale < 0.f) return launch_tree_simt(plan, a, stream);
+  // (The maxima are taken before the scale, so it must not turn them round; and the infinity of
+  // a masked score times zero would be NaN.)
+  if (!(a.sm_scale * 1.4426950408889634f >= FLT_MIN)) return launch_tree_simt(plan, a, stream);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (plan.d) {
     case 64: return launch_d<64>(plan, a, s);

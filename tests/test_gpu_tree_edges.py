@@ -1,5 +1,5 @@
-"""Drafted trees at the edges of what their calls take: masks under windows.  The bound is that of
-test_gpu_tree.py."""
+"""Drafted trees at the edges of what their calls take: masks under windows, scales near zero.  The
+bound is that of test_gpu_tree.py."""
 
 from __future__ import annotations
 
@@ -29,4 +29,14 @@ def test_any_mask_under_a_window(d, path, dtype):
     b = ref.tree_batch(nodes, ctx, 6, 2, d, 16, windows, seed=d, sees=[rng.random((t, t)) < 0.2 for t in nodes],
                        dtype=dtype)
     b.pos[:] = np.concatenate([c + np.arange(t) for c, t in zip(ctx, nodes)])
+    check(b, Tree(b).run(path=path))
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-40, 2.0 ** -127, 2.0 ** -126, 2.0 ** -125])
+def test_scales_near_zero(scale, path):
+    """Scores of up to 2^125 that such a scale makes small, or nothing."""
+    b = ref.tree_batch([9, 5], [12, 0], 8, 2, 64, 16, [0, 40], seed=3, scale=scale)
+    b.q *= 2.0 ** 59
+    b.k_pages *= 2.0 ** 59
     check(b, Tree(b).run(path=path))
