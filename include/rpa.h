@@ -683,7 +683,9 @@ rpa_status_t rpa_append_rope(const void* q, const void* k, const void* v, int64_
  *
  * bf16 q, pages and out run on tensor cores (page_size at least 16 and num_q_heads
  * / num_kv_heads at most 128, sm_scale at least 2^-126), fp32 and the rest on CUDA
- * cores, which take far longer.  A NaN or an
+ * cores, which take far longer.  Scores and sums are 32-bit: a row's output is finite
+ * while its scaled scores are, and the keys it sees times the largest |V| among them
+ * stay below 2^128.  A NaN or an
  * infinity in K or V reaches the rows that see its key, and no other.  Device
  * lengths that differ from the plan's set RPA_DEVERR_LENGTHS; the call goes by the
  * plan's.  The other arguments, the error word, unused slots, threads and CUDA

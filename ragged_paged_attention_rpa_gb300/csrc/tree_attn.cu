@@ -60,13 +60,13 @@ namespace {
 using namespace sm100;
 
 constexpr int kSub = 16384;  // a 64-dimension chunk of 128 keys of K, or 8192 / D keys of V
-// A row's weights are 2^(score - reference).  The reference is the maximum of the first
-// tile that the row sees; it goes up when a later tile's passes it by this much.  So the
-// weights need not wait for a tile's maximum: they are worked out under the reference
-// while the maximum is taken, and worked out again in the rare case.  Weights stay below
-// 2^kGrow, and O in the range of 32 bits (bf16 has the same) for values of V up to 2^94 and
-// 2^17 keys; 8 and 40 took the same times.
-constexpr float kGrow = 16.f;
+// A row's weights are 2^(score - reference).  The reference is kAbove over the maximum of the
+// first tile that the row sees; when a later tile's maximum passes it, it goes up to kAbove over
+// that one.  So the weights need not wait for a tile's maximum: they are worked out under the
+// reference while the maximum is taken, and worked out again in the rare case.  Weights stay
+// at 1 or below, so O stays in the range of 32 bits (bf16 has the same) while the row's keys
+// times the largest value do, as on CUDA cores.  (8 and 16 take the same times.)
+constexpr float kAbove = 8.f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 
@@ -843,12 +843,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           nm2 = f2_pack(-m_use, -m_use);
           weights(sr[0], pk[0]);
           weights(sr[1], pk[1]);
-          const bool grow = mx > m_ref + kGrow;  // also for the first visible key
+          const bool grow = mx > m_ref;  // also for the first visible key
           if (__builtin_expect(!__any_sync(0xffffffffu, grow), 1)) break;
-          // The reference goes up to the tile's maximum, and the tile is gone over again; O,
+          // The reference goes up over the tile's maximum, and the tile is gone over again; O,
           // which holds earlier tiles, is scaled after the last of their products (with
           // two streams that was issued before this score tile, and ended with it).
-          const float f = grow && m_ref != -INFINITY ? fast_exp2(m_ref - mx) : 1.f;
+          const float up = mx + kAbove, f = grow && m_ref != -INFINITY ? fast_exp2(m_ref - up) : 1.f;
           if (mine > 0) {
             if (kStreams == 1 && !(alive = wait(&B.o_done[b ^ 1], (used >> (b ^ 1) & 1u) ^ 1u))) break;
             tc_fence_after();
@@ -866,7 +866,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tmem_wait_st();
           }
           l *= f;
-          if (grow) m_ref = mx;
+          if (grow) m_ref = up;
         }
         if (!alive) break;
         tmem_st16(s_col, pk[0]);

@@ -1,5 +1,5 @@
-"""Drafted trees at the edges of what their calls take: masks under windows, scales near zero.  The
-bound is that of test_gpu_tree.py."""
+"""Drafted trees at the edges of what their calls take: masks under windows, scales near zero, values
+near the ends of their range.  The bound is that of test_gpu_tree.py."""
 
 from __future__ import annotations
 
@@ -40,3 +40,37 @@ def test_scales_near_zero(scale, path):
     b.q *= 2.0 ** 59
     b.k_pages *= 2.0 ** 59
     check(b, Tree(b).run(path=path))
+
+
+def rising_scores(d, nodes, ctx, by, seed):
+    """Scores (base 2) that rise from 0 to `by` along the keys, and positive values of about 1."""
+    b = ref.tree_batch(nodes, ctx, 4, 1, d, 32, None, seed=seed, scale=0.5)
+    b.q[:], b.k_pages[:] = 0, 0
+    b.q[..., 0] = 2.8853900817779268   # 1 / (scale log2 e)
+    for s, n in enumerate(b.kv):
+        for key in range(n):
+            page, i = ref.slot(b, s, key)
+            b.k_pages[page, i, :, 0] = by * key / n
+    b.v_pages = (1 + b.v_pages.abs() / 8).to(b.v_pages.dtype)
+    return b
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("by", [0, 7, 15, 60])
+@pytest.mark.parametrize("sms", [1, 0])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_values_near_the_end_of_the_range(d, by, path, sms):
+    """2^116 of them times 1500 keys stay below 2^128, whatever the scores do."""
+    b = rising_scores(d, [20, 3], [1500, 700], by, 16)
+    b.v_pages *= 2.0 ** 116
+    check(b, Tree(b).run(path=path, num_sms=sms))
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("by", [0, 15, 60])
+@pytest.mark.parametrize("sms", [1, 0])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_small_values(d, by, path, sms):
+    b = rising_scores(d, [20, 3], [1500, 700], by, 17)
+    b.v_pages *= 2.0 ** -116
+    check(b, Tree(b).run(path=path, num_sms=sms))
