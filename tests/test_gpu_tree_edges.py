@@ -1,12 +1,14 @@
 """Drafted trees at the edges of what their calls take: masks under windows, scales near zero, values
-near the ends of their range.  The bound is that of test_gpu_tree.py."""
+near the ends of their range, paths of requests whose lengths cannot be used.  The attention's bound is that of
+test_gpu_tree.py."""
 
 from __future__ import annotations
 
 import numpy as np
 import pytest
+import torch
 
-from ragged_paged_attention_rpa_gb300 import build
+from ragged_paged_attention_rpa_gb300 import binding, build
 
 from . import tree_reference as ref
 from .test_gpu_tree import PATHS, Tree, check
@@ -74,3 +76,15 @@ def test_small_values(d, by, path, sms):
     b = rising_scores(d, [20, 3], [1500, 700], by, 17)
     b.v_pages *= 2.0 ** -116
     check(b, Tree(b).run(path=path, num_sms=sms))
+
+
+def test_empty_paths_of_unusable_lengths_are_reported():
+    pages = torch.arange(4 * 8 * 64, dtype=torch.float32).view(4, 8, 1, 64).cuda()
+    slots = torch.arange(12, device="cuda")
+    path = torch.tensor([[-1, -1], [-1, -1]], dtype=torch.int32, device="cuda")
+    for cu, code in [([0, 6, 12], 0), ([0, 0, 0], 0), ([0, -6, 12], binding.RPA_DEVERR_LENGTHS),
+                     ([0, 6, 13], binding.RPA_DEVERR_LENGTHS), ([0, 6, 5], binding.RPA_DEVERR_LENGTHS)]:
+        k, v, ws = pages.clone(), -pages, torch.zeros(256, dtype=torch.uint8, device="cuda")
+        binding.rpa_commit_tree(k, v, slots, torch.tensor(cu, dtype=torch.int32, device="cuda"), path, ws)
+        assert binding.rpa_get_device_error(ws) == code, cu
+        assert torch.equal(k, pages) and torch.equal(v, -pages)
