@@ -144,13 +144,13 @@ __global__ void __launch_bounds__(kThreads) commit_tree_kernel(const CommitTreeP
   __shared__ int64_t src[kMaxPath], dst[kMaxPath];
   __shared__ int32_t s_len, s_bad;
   const int32_t s = blockIdx.x;
-  const int32_t q0 = __ldg(p.cu + s), q1 = __ldg(p.cu + s + 1);
-  const bool usable = q0 >= 0 && q1 >= q0 && q1 <= p.total_q;
   if (threadIdx.x == 0) {
     s_len = p.max_path;
-    s_bad = usable ? 0 : RPA_DEVERR_LENGTHS;
+    s_bad = 0;
   }
   __syncthreads();
+  const int32_t q0 = __ldg(p.cu + s), q1 = __ldg(p.cu + s + 1);
+  const bool usable = q0 >= 0 && q1 >= q0 && q1 <= p.total_q;
   const int32_t* path = p.path + static_cast<int64_t>(s) * p.max_path;
   for (int32_t k = threadIdx.x; k < p.max_path; k += kThreads) {
     const int32_t j = __ldg(path + k), before = k > 0 ? __ldg(path + k - 1) : -1;
@@ -189,6 +189,8 @@ __global__ void __launch_bounds__(kThreads) commit_tree_kernel(const CommitTreeP
         if (k0 + i < n && src[k0 + i] != dst[k0 + i]) pool[dst[k0 + i] * p.row16 + at] = r[i];
     }
   }
+  // (An empty path has not looked at the lengths.  Asked ahead of the copies it costs 4% of a long path.)
+  if (n == 0 && !usable && threadIdx.x == 0 && blockIdx.y == 0 && p.ws) report_error(p.ws, RPA_DEVERR_LENGTHS, s);
 }
 
 }  // namespace
