@@ -175,7 +175,8 @@ typedef struct rpa_plan_options {
                                rpa_forward_tree, whose masks have that many
                                64-bit words a row (every q_len at most 64 times
                                as many); of the other options it takes path and
-                               num_sms, the rest must be 0, else
+                               num_sms, the rest must be 0, and every kv_len
+                               is at most 2^31 - 1024, else
                                RPA_ERR_UNSUPPORTED                              */
 } rpa_plan_options;
 

@@ -218,6 +218,7 @@ rpa_status_t build_tree_schedule(Plan& plan, const int32_t* cu, const int32_t* k
   for (int32_t s = 0; s < plan.num_seqs; ++s) {
     const int32_t n = cu[s + 1] - cu[s];
     if (n > 64 * opts.tree_words) return RPA_ERR_INVALID_ARG;
+    if (kv[s] > kTreeMaxLen) return RPA_ERR_UNSUPPORTED;
     if (n > 0)
       plan.tree_seqs.push_back({s, cu[s], kv[s], win ? std::max(win[s], 0) : 0, static_cast<uint16_t>(n), 0});
   }

@@ -138,6 +138,7 @@ struct TreeLaunch {
   int32_t seq_begin, seq_end, start_begin, n_ctas, cut_begin, n_cut, width;
 };
 constexpr int kTreeMaxWords = 16;
+constexpr int32_t kTreeMaxLen = 0x7fffffff - 1023;  // the kernels step past the last key in 32 bits
 constexpr int kTreeRows = 128;
 constexpr int kTreeKeys = 128;
 constexpr int kTreeSeqsSmall = 128;   // requests a launch carries in its parameters
