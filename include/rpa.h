@@ -644,7 +644,9 @@ typedef struct rpa_rope {
  * num_q_heads, head_dim] contiguous; it may be q.  With num_q_heads 0, q and q_out
  * are not used (NULL).  slot_map [total_q] int64: token t goes to slot slot_map[t]
  * of the pool (slot_map[t] / page_size is its page); of a token with a negative
- * entry only q is written.  The slots of a call are distinct.
+ * entry only q is written.  The slots of a call are distinct.  A row of k or v may
+ * be the slot that it goes to (the cache turned further); otherwise the rows, q_out
+ * and the pages lie apart.
  *
  * kv_dtype is `dtype`, or RPA_DTYPE_FP8_E4M3: k_pages, v_pages [num_pages,
  * page_size, num_kv_heads, head_dim] of it.  e4m3 pages hold row / k_scale[head]

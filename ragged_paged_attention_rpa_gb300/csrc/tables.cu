@@ -9,8 +9,8 @@
 // position in the page.  Releasing requests pushes their pages back in
 // (request, slot) order, and cutting requests short pushes the pages behind their
 // new lengths.  All or nothing: a step that the stack or the slot map cannot hold
-// changes nothing and sets the error word.  (A trim of 512 requests takes 4.6 us, of 2048
-// requests that drop up to 256 tokens 5.1.)
+// changes nothing and sets the error word.  (A trim of 512 requests takes 4.3 us, of 2048
+// requests that drop up to 256 tokens 4.6.)
 //
 // Integer work on a few kilobytes: what bounds it is latency, so every CTA
 // scans all the requests' lengths for itself (L2 reads, two block scans) and

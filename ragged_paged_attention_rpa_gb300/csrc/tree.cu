@@ -7,18 +7,18 @@
 // its warps take 32 nodes each and find the ancestors among these by doubling (five rounds
 // of shuffles), and the first ancestor before them; then the 32s' rows in turn: a row is
 // that ancestor's, with those among the 32 set.  The path's nodes have rising numbers, so
-// a window's are a row's highest bits.  64 requests of up to 256 nodes take 5.7 us (7.1 with
+// a window's are a row's highest bits.  64 requests of up to 256 nodes take 5.4 us (7.1 with
 // one warp that did both for 32 nodes after 32; 41 where a thread walked from its node to
-// the root and chains were among them), 128 requests of 8 nodes 2.8.
+// the root and chains were among them), 128 requests of 8 nodes 2.2.
 //
 // commit_tree: row k of the path takes the K and V of node path[k] >= k.  A thread
 // owns 16 bytes of the row and goes down the path, eight nodes read before eight
 // are written: a later node's source lies behind every place written so far, so
 // nothing is lost where source and destination rows overlap.  A row is read once and
 // written once; the path, its slots and the rows are three dependent reads.  128 paths of
-// up to 4 rows of 512 bytes: 2.9 us; 64 of up to 16 rows of 8 KB: 7.5 us (14.7 MB, 2.0 TB/s;
-// with the path's eights on threads of their own, all read before one writes, 7.1, and the
-// small one 3.0).
+// up to 4 rows of 512 bytes: 2.4 us; 64 of up to 16 rows of 8 KB: 7.2 us (14.7 MB, 2.0 TB/s;
+// with the path's eights on threads of their own, all read before one writes, 5% less, and
+// 3% more for the small one).
 #include <algorithm>
 
 #include "common.cuh"

@@ -34,11 +34,11 @@
 // Every wait is bounded; see prefill_tc.cu for what follows when one gives up.
 //
 // What bounds it.  Long contexts, HBM: 32 requests of 16 to 48 nodes after 4k to 32k keys
-// (32 heads of 128, 8 KV heads) read 2.17 GB in 365 us, 6.0 TB/s.  Many nodes, the tensor
+// (32 heads of 128, 8 KV heads) read 2.17 GB in 362 us, 6.0 TB/s.  Many nodes, the tensor
 // cores and the softmax between their products: 8 requests of 256 nodes (64 heads of 128)
 // take 213 us, 1405 TFLOP/s; segments that need no cut run at 1790, and 10 us are the
 // combine's.  128 requests of 8 nodes (8 heads of 256, one KV head) after 120 to 2040 keys:
-// 37.3 us for 137 MB: 30 here (HBM's share of 22, the start, ranges that end apart), the
+// 37.4 us for 137 MB: 30 here (HBM's share of 22, the start, ranges that end apart), the
 // rest the combine and its launch.
 //
 // Measured against this: no second MMA warp (one a stream: 326 us where 255 were, the two
@@ -1193,8 +1193,8 @@ int launch_d(const Plan& plan, const Args& a, cudaStream_t stream) {
   // A quarter of a row tile a box of Q where a quarter's rows are whole nodes (else the tile:
   // its last rows then hold what follows in q, and nobody reads what becomes of them).
   p.box_nodes_q = p.per_tile * G == kTreeRows && p.per_tile % 4 == 0 ? p.per_tile / 4 : p.per_tile;
-  // Boxes never cross a page (32 contexts of 4k to 32k keys: 496 us with pages of 16, 380 with
-  // 32, 366 with 64 to 256).
+  // Boxes never cross a page (32 contexts of 4k to 32k keys: 489 us with pages of 16, 375 with
+  // 32, 362 with 64).
   p.box_rows_k = std::min(plan.p, 64);  // (the last tile's second half often lies behind the keys)
   p.box_rows_v = std::min(plan.p, Lay::kVKeys);
   // A V stage in one page takes all its 64-dimension chunks in one box (128 requests of 8

@@ -186,3 +186,19 @@ def test_e4m3_quotients_of_any_size(dtype):
     low, high = nearest_e4m3(y * (1 - 2.0 ** -22 * np.sign(y))), nearest_e4m3(y * (1 + 2.0 ** -22 * np.sign(y)))
     ok = (got >= low) & (got <= high)
     assert ok.all(), [(x[tuple(i)].item(), scales[i[1]], got[tuple(i)]) for i in np.argwhere(~ok)[:5]]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 256])
+def test_rows_of_the_cache_turned_further_in_place(d, dtype):
+    """Rows that are the slots they go to: the same bits as from a copy."""
+    t, heads = 300, 3
+    pages = [torch.randn((t // 4, 4, heads, d), device="cuda").to(dtype) for _ in range(2)]
+    rows = [p.view(t, heads, d) for p in pages]
+    pos, slots = i32(np.arange(t) * 37 - 5000), torch.arange(t, device="cuda")
+    freq = torch.tensor(frequencies("mixed", d // 2, np.random.default_rng(9)), dtype=torch.float32, device="cuda")
+    want = [p.clone() for p in pages]
+    binding.rpa_append_rope(None, rows[0].clone(), rows[1].clone(), pos, slots, freq, None, *want)
+    binding.rpa_append_rope(None, *rows, pos, slots, freq, None, *pages)
+    for p, w in zip(pages, want):
+        assert torch.equal(p.view(torch.uint8), w.view(torch.uint8))
