@@ -21,7 +21,7 @@
 //
 // HBM-bound: every row is read once and written once.  8192 tokens of 32 + 2 x 16 rows of
 // 256, the pages e4m3: 470 MB in 79 us, 5.9 TB/s (0.87 of a plain copy; the lanes'
-// conversions keep the schedulers 47% busy); bf16 pages 83.5 us, 6.4 TB/s; fp32 rows and
+// conversions keep the schedulers 48% busy); bf16 pages 83.5 us, 6.4 TB/s; fp32 rows and
 // pages 164 us, 6.6 TB/s.  1024 tokens of 8 + 2 rows: 5.6 us, a launch
 // and two dependent reads (positions and rows, then the stores) for 10 MB.
 #include <algorithm>
